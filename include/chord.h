@@ -92,6 +92,9 @@ typedef enum chord_kernel {
        with its rows reordered so that each 16-row group holds gate rows
        8g..8g+7 and then their up rows I+8g..I+8g+7: a thread that holds rows r
        and r+8 of an MMA tile holds a gate value and its up value */
+#define CHORD_LAYOUT_MXFP4 4
+    /* microscaled 4-bit matrices (chord_mxfp4_quantize): tiles of 128 rows x 256
+       columns, 16384 bytes of codes and 1024 bytes of scales each */
 
 /* GEMM epilogue. */
 typedef enum chord_epilogue {
@@ -103,6 +106,12 @@ typedef enum chord_dtype {
     CHORD_DTYPE_BF16 = 0,
     CHORD_DTYPE_F32 = 1
 } chord_dtype;
+
+/* Expert weights of chord_moe_layer_few. */
+typedef enum chord_weights {
+    CHORD_WEIGHTS_INT4 = 0,    /* chord_pack_weights blobs */
+    CHORD_WEIGHTS_MXFP4 = 1    /* chord_mxfp4_quantize matrices */
+} chord_weights;
 
 typedef struct chord_opts {
     int32_t kernel;      /* chord_kernel (the packed blobs must have its layout) */
@@ -493,6 +502,114 @@ chord_status chord_moe_layer_cached(const void *x, const int32_t *topk_ids, cons
 
 /* Destroys every graph chord_moe_layer_cached holds; returns how many. */
 int chord_moe_layer_cache_clear(void);
+
+/* ------------------------------------------------- microscaled 4-bit (MXFP4) */
+
+/* MXFP4 matrices (OCP Microscaling Formats specification v1.0): E2M1 codes
+ * (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives) with one E8M0 scale 2^(b - 127)
+ * per 32 consecutive K elements of a row.  The tensor cores multiply these codes
+ * and scales as they are, so weights need no dequantisation in the prefill
+ * regime; the article's INT4 format has no such instruction.
+ *
+ * A packed matrix holds G groups (experts, or blocks of routed rows) of N x K
+ * values in CHORD_LAYOUT_MXFP4: a 256-byte header (magic "CHRD", version 1,
+ * layout 4, group size 32, G, N, K, then the 64-bit bytes of one group at word 8
+ * and the data offset 256 at word 10) followed by tiles of 128 rows x 256 columns
+ * (17408 bytes), the last ones padded with zeros.  K % 32 == 0, N is free.
+ *
+ * Bytes of such a matrix; 0 on bad arguments. */
+size_t chord_mxfp4_bytes(int64_t G, int64_t N, int K);
+
+/* Quantise src [G, N, K] (CHORD_DTYPE_BF16 or CHORD_DTYPE_F32, unit stride along
+ * K, row_stride and mat_stride elements between rows and groups, aligned to its
+ * element size only).  For 32 columns with largest magnitude a:
+ *   e = floor(log2(a)) - 2 clamped to [-127, 127] (a = 0: -127), b = e + 127,
+ *   code = the E2M1 number nearest to v * 2^-e, ties to the even code, magnitudes
+ *   above 5 to 6.
+ * A block holding an infinity or NaN gets the NaN scale (b = 255).  The result
+ * is unique, bit for bit.  packed_bytes must be chord_mxfp4_bytes(G, N, K). */
+chord_status chord_mxfp4_quantize(const void *src, int src_dtype, int64_t row_stride,
+                                  int64_t mat_stride, int64_t G, int64_t N, int K, void *packed,
+                                  size_t packed_bytes, void *stream);
+
+/* Bytes of the quantised routed rows of a call (one group of block_m rows per
+ * align block): chord_mxfp4_bytes(capacity / block_m, block_m, K). */
+size_t chord_mxfp4_rows_bytes(int64_t capacity, int block_m, int K);
+
+/* Quantise activation rows into the order of chord_moe_align's sorted_ids, the
+ * gather of the indexed contract done on the way: for every pair id p at position
+ * i of sorted_ids (p < num_pairs, p / a_row_divisor < a_rows), row i mod block_m
+ * of group i / block_m is the quantised row p / a_row_divisor of A [a_rows, K]
+ * (a_dtype, row_stride elements apart).  Positions without a pair hold no
+ * defined codes and no product reads them. */
+chord_status chord_mxfp4_quantize_rows(const void *A, int a_dtype, int64_t a_rows,
+                                       int64_t row_stride, int a_row_divisor, int K,
+                                       const int32_t *sorted_ids, const int32_t *num_tokens_padded,
+                                       int64_t capacity, int block_m, int64_t num_pairs, void *packed,
+                                       size_t packed_bytes, void *stream);
+
+/* The values of a packed matrix: out [G, N, K] dense, bf16 (every value whose
+ * exponent fits is exact) or FP32. */
+chord_status chord_mxfp4_dequantize(const void *packed, size_t packed_bytes, int64_t G, int64_t N,
+                                    int K, void *out, int out_dtype, void *stream);
+
+/* Block size for the grouped product: the rows an expert rarely exceeds
+ * (tok_e + 3 sqrt(tok_e) + 1, tok_e = T * topk / E_global) split into as few equal
+ * blocks of at most 224 rows as hold them, rounded up to 32. */
+int chord_mxfp4_select_block_m(int T, int topk, int E_local, int E_global);
+
+/* Grouped product, the indexed contract of chord_w4a16_moe_gemm with both
+ * operands quantised:
+ *   C[p, n] = sum_k a[p, k] * w[expert_ids[b], n, k]   (FP32 sum)
+ * for every block b < num_tokens_padded / block_m and every pair id p in
+ * sorted_ids[b * block_m .. + block_m); a[p, :] is that position's quantised row.
+ *   Aq      chord_mxfp4_quantize_rows of the same capacity, block_m and K
+ *   packed  chord_mxfp4_quantize of the weights [E, N, K]
+ *   C       [num_pairs, N], CHORD_DTYPE_BF16 or CHORD_DTYPE_F32; rows no block
+ *           names are not written
+ * block_m % 32 == 0 and at most 224; K % 32 == 0; N is free. */
+chord_status chord_mxfp4_moe_gemm(const void *Aq, size_t aq_bytes, const void *packed,
+                                  size_t packed_bytes, int E, int N, int K,
+                                  const int32_t *sorted_ids, const int32_t *expert_ids,
+                                  const int32_t *num_tokens_padded, int64_t capacity, int block_m,
+                                  int64_t num_pairs, void *C, int c_dtype, const chord_opts *opts,
+                                  void *stream);
+
+/* Dense product of two packed matrices: C [M, N] = a [M, K] * w [N, K]^T with
+ * Aq = chord_mxfp4_quantize of [1, M, K] and packed of [1, N, K]. */
+chord_status chord_mxfp4_gemm(const void *Aq, size_t aq_bytes, int64_t M, const void *packed,
+                              size_t packed_bytes, int N, int K, void *C, int c_dtype,
+                              const chord_opts *opts, void *stream);
+
+/* ------------------------------------------------------ layer, a few tokens */
+
+#define CHORD_FEW_MAX_TOKENS 32
+
+/* Scratch bytes of chord_moe_layer_few: 4 bytes per pair and column of I. */
+size_t chord_moe_few_workspace_bytes(int T, int topk, int E, int H, int I);
+
+/* One MoE expert layer for at most CHORD_FEW_MAX_TOKENS tokens in two launches
+ * (decode of one request or of a small batch, where chord_moe_layer's align,
+ * GEMMs, reductions and combine cost more than the weights' bytes):
+ *   out[t] = bf16( sum over k with topk_ids[t, k] in [0, E) of
+ *                  topk_w[t, k] * W2[e] ( SiLU(W13[e][:I] x_t) * (W13[e][I:] x_t) ) )
+ * with FP32 sums and nothing rounded in between (chord_moe_layer rounds the
+ * gate_up result and SiLU * up to bf16, so the two agree within those
+ * roundings).  Ids outside [0, E) are skipped, tokens with no local pair get +0.
+ *   weights     CHORD_WEIGHTS_INT4: blobs of chord_pack_weights, w13 (E, 2I, H) in
+ *               CHORD_LAYOUT_TCGEN05 or CHORD_LAYOUT_GATE_UP_INTERLEAVED (read from
+ *               its header), w2 (E, H, I) in CHORD_LAYOUT_TCGEN05; H % 128 == 0,
+ *               I % 64 == 0
+ *               CHORD_WEIGHTS_MXFP4: chord_mxfp4_quantize of w13 [E, 2I, H] (gate
+ *               rows, then up rows) and w2 [E, H, I]; H % 32 == 0, I % 32 == 0
+ *   x           device bf16 [T, H]; topk <= 32, E <= 1024
+ *   workspace   >= chord_moe_few_workspace_bytes(T, topk, E, H, I), 16-byte aligned
+ * The result does not depend on the order in which blocks run. */
+chord_status chord_moe_layer_few(const void *x, const int32_t *topk_ids, const float *topk_w, int T,
+                                 int topk, int E, int H, int I, int weights, const void *packed_w13,
+                                 size_t w13_bytes, const void *packed_w2, size_t w2_bytes,
+                                 void *workspace, size_t workspace_bytes, void *out,
+                                 const chord_opts *opts, void *stream);
 
 /* ------------------------------------------------------------------ errors */
 

@@ -23,6 +23,9 @@ __all__ = [
     "chord_layer_workspace_bytes", "chord_moe_layer", "chord_moe_layer_cached", "chord_moe_layer_cache_clear", "chord_get_device_error", "chord_selftest_wait_timeout",
     "chord_grouped_contiguous_workspace_bytes", "chord_grouped_contiguous_gemm",
     "chord_grouped_masked_workspace_bytes", "chord_grouped_masked_gemm",
+    "chord_mxfp4_bytes", "chord_mxfp4_rows_bytes", "chord_mxfp4_quantize", "chord_mxfp4_quantize_rows",
+    "chord_mxfp4_dequantize", "chord_mxfp4_select_block_m", "chord_mxfp4_moe_gemm", "chord_mxfp4_gemm",
+    "chord_moe_few_workspace_bytes", "chord_moe_layer_few", "WEIGHTS_INT4", "WEIGHTS_MXFP4", "FEW_MAX_TOKENS",
     "KERNEL_AUTO", "KERNEL_TCGEN05", "KERNEL_WARP_MMA", "LAYOUT_WARP_MMA", "LAYOUT_TCGEN05",
     "DTYPE_BF16", "DTYPE_F32",
 ]
@@ -31,6 +34,9 @@ KERNEL_AUTO, KERNEL_TCGEN05, KERNEL_WARP_MMA = 0, 1, 2
 LAYOUT_WARP_MMA, LAYOUT_TCGEN05, LAYOUT_GATE_UP_INTERLEAVED = 1, 2, 3
 EPILOGUE_NONE, EPILOGUE_SILU_MUL = 0, 1
 DTYPE_BF16, DTYPE_F32 = 0, 1
+LAYOUT_MXFP4 = 4
+WEIGHTS_INT4, WEIGHTS_MXFP4 = 0, 1
+FEW_MAX_TOKENS = 32
 STATUS = {0: "CHORD_OK", 1: "CHORD_ERR_INVALID_ARG", 2: "CHORD_ERR_UNSUPPORTED", 3: "CHORD_ERR_LAYOUT_MISMATCH",
           4: "CHORD_ERR_BUFFER_TOO_SMALL", 5: "CHORD_ERR_CUDA", 6: "CHORD_ERR_DEVICE_VALIDATION",
           7: "CHORD_ERR_TIMEOUT"}
@@ -88,6 +94,19 @@ _SIGS = {
     "chord_grouped_masked_workspace_bytes": (_sz, [_int, _int, _int]),
     "chord_grouped_masked_gemm": (_int, [_vp, _int, _int, _vp, _int, _vp, _sz, _int, _int, _vp, _vp, _sz, _OPTS,
                                          _vp]),
+    "chord_mxfp4_bytes": (_sz, [_i64, _i64, _int]),
+    "chord_mxfp4_rows_bytes": (_sz, [_i64, _int, _int]),
+    "chord_mxfp4_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _i64, _int, _vp, _sz, _vp]),
+    "chord_mxfp4_quantize_rows": (_int, [_vp, _int, _i64, _i64, _int, _int, _vp, _vp, _i64, _int, _i64, _vp, _sz,
+                                         _vp]),
+    "chord_mxfp4_dequantize": (_int, [_vp, _sz, _i64, _i64, _int, _vp, _int, _vp]),
+    "chord_mxfp4_select_block_m": (_int, [_int, _int, _int, _int]),
+    "chord_mxfp4_moe_gemm": (_int, [_vp, _sz, _vp, _sz, _int, _int, _int, _vp, _vp, _vp, _i64, _int, _i64, _vp, _int,
+                                    _OPTS, _vp]),
+    "chord_mxfp4_gemm": (_int, [_vp, _sz, _i64, _vp, _sz, _int, _int, _vp, _int, _OPTS, _vp]),
+    "chord_moe_few_workspace_bytes": (_sz, [_int, _int, _int, _int, _int]),
+    "chord_moe_layer_few": (_int, [_vp, _vp, _vp, _int, _int, _int, _int, _int, _int, _vp, _sz, _vp, _sz, _vp, _sz,
+                                   _vp, _OPTS, _vp]),
 }
 
 
@@ -297,6 +316,83 @@ def chord_grouped_masked_gemm(A, masked_m, expected_m: int, packed, N: int, K: i
     _check(load().chord_grouped_masked_gemm(_p(A), G, max_m, _p(masked_m), expected_m, _p(packed), _nbytes(packed),
                                             N, K, _p(C), _p(workspace), _nbytes(workspace), _o(opts), _s(stream)),
            "chord_grouped_masked_gemm")
+
+
+def _dtype(t, what: str) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float32:
+        return DTYPE_F32
+    raise ChordError(1, f"{what}: dtype {t.dtype}")
+
+
+def chord_mxfp4_bytes(G: int, N: int, K: int) -> int:
+    return load().chord_mxfp4_bytes(G, N, K)
+
+
+def chord_mxfp4_rows_bytes(capacity: int, block_m: int, K: int) -> int:
+    return load().chord_mxfp4_rows_bytes(capacity, block_m, K)
+
+
+def chord_mxfp4_quantize(src, packed, stream=None):
+    """src bf16 or float32 [G, N, K] (unit stride along K, any row and matrix stride), packed uint8 output."""
+    G, N, K = src.shape
+    if K > 1 and src.stride(2) != 1:
+        raise ChordError(1, "chord_mxfp4_quantize: src needs unit stride along K")
+    _check(load().chord_mxfp4_quantize(_p(src), _dtype(src, "chord_mxfp4_quantize"), src.stride(1), src.stride(0), G,
+                                       N, K, _p(packed), _nbytes(packed), _s(stream)), "chord_mxfp4_quantize")
+
+
+def chord_mxfp4_quantize_rows(A, a_row_divisor: int, sorted_ids, num_tokens_padded, block_m: int, num_pairs: int,
+                              packed, stream=None):
+    """A bf16 or float32 [a_rows, K] (any row stride), quantised into the order of sorted_ids."""
+    a_rows, K = A.shape
+    if K > 1 and A.stride(1) != 1:
+        raise ChordError(1, "chord_mxfp4_quantize_rows: A needs unit stride along K")
+    _check(load().chord_mxfp4_quantize_rows(_p(A), _dtype(A, "chord_mxfp4_quantize_rows"), a_rows, A.stride(0),
+                                            a_row_divisor, K, _p(sorted_ids), _p(num_tokens_padded),
+                                            sorted_ids.numel(), block_m, num_pairs, _p(packed), _nbytes(packed),
+                                            _s(stream)), "chord_mxfp4_quantize_rows")
+
+
+def chord_mxfp4_dequantize(packed, out, stream=None):
+    """out bf16 or float32 [G, N, K] dense: the values of the packed matrix."""
+    G, N, K = out.shape
+    _check(load().chord_mxfp4_dequantize(_p(packed), _nbytes(packed), G, N, K, _p(out),
+                                         _dtype(out, "chord_mxfp4_dequantize"), _s(stream)), "chord_mxfp4_dequantize")
+
+
+def chord_mxfp4_select_block_m(T: int, topk: int, E_local: int, E_global: int) -> int:
+    return load().chord_mxfp4_select_block_m(T, topk, E_local, E_global)
+
+
+def chord_mxfp4_moe_gemm(Aq, packed, E: int, N: int, K: int, sorted_ids, expert_ids, num_tokens_padded, block_m: int,
+                         num_pairs: int, C, opts=None, stream=None):
+    """C bf16 or float32 [num_pairs, N] (its dtype selects the output type)."""
+    _check(load().chord_mxfp4_moe_gemm(_p(Aq), _nbytes(Aq), _p(packed), _nbytes(packed), E, N, K, _p(sorted_ids),
+                                       _p(expert_ids), _p(num_tokens_padded), sorted_ids.numel(), block_m, num_pairs,
+                                       _p(C), _dtype(C, "chord_mxfp4_moe_gemm"), _o(opts), _s(stream)),
+           "chord_mxfp4_moe_gemm")
+
+
+def chord_mxfp4_gemm(Aq, M: int, packed, N: int, K: int, C, opts=None, stream=None):
+    """C bf16 or float32 [M, N] (its dtype selects the output type)."""
+    _check(load().chord_mxfp4_gemm(_p(Aq), _nbytes(Aq), M, _p(packed), _nbytes(packed), N, K, _p(C),
+                                   _dtype(C, "chord_mxfp4_gemm"), _o(opts), _s(stream)), "chord_mxfp4_gemm")
+
+
+def chord_moe_few_workspace_bytes(T: int, topk: int, E: int, H: int, I: int) -> int:
+    return load().chord_moe_few_workspace_bytes(T, topk, E, H, I)
+
+
+def chord_moe_layer_few(x, topk_ids, topk_w, E: int, I: int, packed_w13, packed_w2, workspace, out,
+                        weights: int = WEIGHTS_INT4, opts=None, stream=None):
+    T, H = x.shape
+    topk = topk_ids.shape[1]
+    _check(load().chord_moe_layer_few(_p(x), _p(topk_ids), _p(topk_w), T, topk, E, H, I, weights, _p(packed_w13),
+                                      _nbytes(packed_w13), _p(packed_w2), _nbytes(packed_w2), _p(workspace),
+                                      _nbytes(workspace), _p(out), _o(opts), _s(stream)), "chord_moe_layer_few")
 
 
 def chord_selftest_wait_timeout(stream=None):

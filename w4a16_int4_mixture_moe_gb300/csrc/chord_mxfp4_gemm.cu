@@ -9,6 +9,7 @@
 
 #include "chord_internal.h"
 #include "chord_mxfp4.cuh"
+#include "chord_tcgen05.cuh"
 
 namespace chord {
 namespace {
@@ -27,73 +28,343 @@ struct MxGemmArgs {
     int* err;
 };
 
-__device__ __forceinline__ float group_dot(uint4 x, uint4 w) {
-    const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {w.x, w.y, w.z, w.w};
-    float s = 0.0f;
+// One work item is (row block, 128 rows of N).  The weight rows are the MMA's M
+// side and the block's rows its N side, so a block of 11 rows costs an N = 16
+// instruction.  Roles:
+//   * a producer lane copies K stages of 256 columns into a shared-memory ring
+//     with cp.async.bulk: the weight tile (17408 contiguous bytes) and the codes
+//     of the block's rows with their scales;
+//   * an issuing lane copies the stage's scales to tensor memory, issues its four
+//     K = 64 instructions into one of two FP32 accumulators and commits the
+//     stage back to the producer;
+//   * eight warps read the finished accumulator and write C while the next item
+//     is computed into the other one.
+// Every wait is bounded; the grid is persistent (static round robin).
+constexpr int kEpiWarps = 8;
+constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
+constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kStgBytes = 2048;          // one epilogue warp's buffer: 16 rows x 32 columns x FP32
+constexpr uint32_t kTmemCols = 512;
+constexpr size_t kSmemBudget = 227 * 1024;
+
+struct MxPlan {
+    int tok;        // rows of a block (dense: a multiple of 64)
+    int stages;     // shared-memory ring
+    int sf_slots;   // tensor-memory scale ring
+    int stage_bytes;
+};
+
+struct Item {
+    int64_t b;      // row block
+    int nt;         // 128-row tile of N
+    int e;          // expert
+    int rows;       // rows of the block that hold pairs (a prefix), rounded up to 16; 0: nothing to do
+    int off;        // first row inside its 128-row tile (dense blocks of 64 or 192: 0 or 64)
+};
+
+// Facts of item i, computed identically by every warp from the same arrays.
+__device__ __forceinline__ Item item_at(const MxGemmArgs& g, const MxPlan& pl, int64_t i, int ntiles, int lane,
+                                        bool report) {
+    Item it;
+    it.b = divmod_idx(i, ntiles, it.nt);
+    it.e = 0;
+    it.off = 0;
+    if (!g.sorted_ids) {
+        const int64_t r0 = it.b * pl.tok;
+        const int64_t n = min((int64_t)pl.tok, g.a_rows - r0);
+        it.rows = (int)((n + 15) / 16 * 16);
+        it.off = (int)(r0 % kMxTileRows);
+        return it;
+    }
+    it.e = g.expert_ids[it.b];
+    int32_t ids[7];
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        s = fmaf(e2m1_f32((a[i >> 3] >> (4 * (i & 7))) & 15u), e2m1_f32((b[i >> 3] >> (4 * (i & 7))) & 15u), s);
-    return s;
+    for (int k = 0; k < 7; ++k) {
+        const int r = lane + 32 * k;
+        ids[k] = r < pl.tok ? g.sorted_ids[it.b * pl.tok + r] : (int32_t)g.num_pairs;
+    }
+    it.rows = 0;
+    if (it.e < 0 || it.e >= g.E) {
+        if (report && lane == 0) set_error(g.err, CHORD_DEV_BAD_EXPERT);
+        return it;
+    }
+    int last = 0;
+#pragma unroll
+    for (int k = 0; k < 7; ++k) {
+        const bool ok = ids[k] >= 0 && ids[k] < g.num_pairs;
+        if (report && !ok && ids[k] != g.num_pairs) set_error(g.err, CHORD_DEV_BAD_ROW);
+        if (ok) last = lane + 32 * k + 1;
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    it.rows = (last + 15) / 16 * 16;
+    return it;
 }
 
-// One thread per output element.
-__global__ void mx_gemm_kernel(MxGemmArgs g) {
-    if (!mx_header_ok(g.a, g.a_groups, g.a_rows, g.K) || !mx_header_ok(g.w, g.E, g.N, g.K)) {
-        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_error(g.err, CHORD_DEV_BAD_HEADER);
-        return;
-    }
-    const int n = blockIdx.x * blockDim.x + threadIdx.x;
-    int64_t rows = g.a_groups * g.a_rows;
-    if (g.ntp) {
-        const int64_t ntp = *g.ntp;
-        if (ntp < 0 || ntp > rows || ntp % g.a_rows) {
-            if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_error(g.err, CHORD_DEV_BAD_PADDED);
-            return;
+// Accumulator columns of one epilogue warp (its 32 lanes are rows of N; warp
+// group wg takes every other slice of 16 block rows) to C, 16 x 32 values at a time through
+// the warp's buffer so that C is written in 16-byte pieces.
+__device__ __forceinline__ void drain(const MxGemmArgs& g, const MxPlan& pl, const Item& it, uint32_t acc, int wg,
+                                      int quarter, int lane, uint8_t* stg) {
+    const int esz = g.out_f32 ? 4 : 2;
+    const int n0 = it.nt * kMxTileRows + quarter * 32;
+    const bool wide = (int64_t)g.N * esz % 16 == 0;
+    const int per = 16 / esz, pieces = 32 / per;
+    const uint32_t sbase = smem_u32(stg);
+    for (int j0 = wg * 16; j0 < it.rows; j0 += 32) {
+        int32_t mine = -1;   // C row of block row j0 + lane
+        if (lane < 16) {
+            const int64_t r = it.b * pl.tok + j0 + lane;
+            if (!g.sorted_ids) {
+                if (r < g.a_rows) mine = (int32_t)r;
+            } else if (j0 + lane < pl.tok) {
+                const int32_t id = g.sorted_ids[r];
+                if (id >= 0 && id < g.num_pairs) mine = id;
+            }
         }
-        rows = ntp;
+        uint32_t v[16];
+        tc5::ld16(acc + ((uint32_t)(quarter * 32) << 16) + j0, v);
+        tc5::wait_ld();
+        if (n0 >= g.N) continue;
+        if (!wide) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int32_t p = __shfl_sync(0xffffffffu, mine, u);
+                if (p < 0 || n0 + lane >= g.N) continue;
+                const int64_t o = (int64_t)p * g.N + n0 + lane;
+                if (g.out_f32)
+                    static_cast<float*>(g.C)[o] = __uint_as_float(v[u]);
+                else
+                    static_cast<__nv_bfloat16*>(g.C)[o] = __float2bfloat16_rn(__uint_as_float(v[u]));
+            }
+            continue;
+        }
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+            const uint32_t at = sbase + (uint32_t)((u * 32 + lane) * esz);
+            if (g.out_f32)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v[u]) : "memory");
+            else
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at),
+                             "h"(__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[u]))))
+                             : "memory");
+        }
+        __syncwarp();
+        for (int q = lane; q < 16 * pieces; q += 32) {
+            const int u = q / pieces, c = n0 + (q % pieces) * per;
+            const int32_t p = __shfl_sync(0xffffffffu, mine, u);
+            uint4 w;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "r"(sbase + (uint32_t)(q * 16))
+                         : "memory");
+            // N is a multiple of `per` here, so a piece lies wholly inside or outside
+            if (p >= 0 && c < g.N)
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.C) + ((int64_t)p * g.N + c) * esz) = w;
+        }
+        __syncwarp();
     }
-    if (n >= g.N) return;
-    const int64_t kb = mx_col_tiles(g.K), art = mx_row_tiles(g.a_rows), wrt = mx_row_tiles(g.N);
-    for (int64_t i = blockIdx.y; i < rows; i += gridDim.y) {
-        int64_t grp = 0, ar = i, p = i;
-        int e = 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g, const MxPlan pl) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* stg = smem + pl.stages * pl.stage_bytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(stg + kEpiWarps * kStgBytes);
+    uint64_t* empty = full + pl.stages;
+    uint64_t* acc_full = empty + pl.stages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] row count, [1] abort, [2] skip
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        bool ok = mx_header_ok(g.a, g.a_groups, g.a_rows, g.K) && mx_header_ok(g.w, g.E, g.N, g.K);
+        if (!ok) set_error(g.err, CHORD_DEV_BAD_HEADER);
+        int64_t blocks = (g.a_rows + pl.tok - 1) / pl.tok;
         if (g.sorted_ids) {
-            grp = i / g.a_rows;
-            ar = i % g.a_rows;
-            p = g.sorted_ids[i];
-            e = g.expert_ids[grp];
-            if (e < 0 || e >= g.E) {
-                if (n == 0) set_error(g.err, CHORD_DEV_BAD_EXPERT);
-                continue;
+            const int64_t ntp = *g.ntp;
+            if (ntp < 0 || ntp > g.a_groups * g.a_rows || ntp % pl.tok) {
+                if (ok) set_error(g.err, CHORD_DEV_BAD_PADDED);
+                ok = false;
             }
-            if (p < 0 || p >= g.num_pairs) {
-                if (p != g.num_pairs && n == 0) set_error(g.err, CHORD_DEV_BAD_ROW);
-                continue;
-            }
+            blocks = ok ? ntp / pl.tok : 0;
         }
-        const uint8_t* at = g.a + kHeaderBytes + (grp * art + ar / kMxTileRows) * kb * kMxTileBytes;
-        const uint8_t* wt = g.w + kHeaderBytes + ((int64_t)e * wrt + n / kMxTileRows) * kb * kMxTileBytes;
-        const uint32_t r = (uint32_t)(ar % kMxTileRows), q = (uint32_t)(n % kMxTileRows);
-        float sum = 0.0f;
-        for (int k = 0; k < g.K / kGroup; ++k) {
-            const uint8_t* a = at + (k >> 3) * (int64_t)kMxTileBytes;
-            const uint8_t* w = wt + (k >> 3) * (int64_t)kMxTileBytes;
-            const uint32_t j = k & 7;
-            const float d = group_dot(*reinterpret_cast<const uint4*>(a + mx_code_offset(r, j)),
-                                      *reinterpret_cast<const uint4*>(w + mx_code_offset(q, j)));
-            sum += d * mx_scale_f32(a[mx_scale_offset(r, j)]) * mx_scale_f32(w[mx_scale_offset(q, j)]);
+        flags[0] = (int)blocks;
+        flags[1] = 0;
+        flags[2] = ok ? 0 : 1;
+        for (int s = 0; s < pl.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
         }
-        if (g.out_f32)
-            static_cast<float*>(g.C)[p * g.N + n] = sum;
-        else
-            static_cast<__nv_bfloat16*>(g.C)[p * g.N + n] = __float2bfloat16_rn(sum);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], kEpiWarps);
+        }
+        fence_barrier_init();
     }
+    __syncthreads();
+    if (flags[2]) return;
+    if (warp == kProducerWarp) tc5::alloc(tmem_slot, kTmemCols);
+    tc5::fence_before();
+    __syncthreads();
+    tc5::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int ntiles = (g.N + kMxTileRows - 1) / kMxTileRows;
+    const int kstages = (g.K + kMxTileCols - 1) / kMxTileCols;
+    const int64_t n_items = (int64_t)flags[0] * ntiles;
+    const int64_t art = mx_row_tiles(g.a_rows);
+
+    if (warp == kProducerWarp) {
+        tc5::Ring r;
+        int64_t issued = 0;
+        bool ok = true;
+        for (int64_t i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+            const Item it = item_at(g, pl, i, ntiles, lane, false);
+            if (it.rows == 0) continue;
+            if (lane == 0) {
+                const uint8_t* wt = g.w + kHeaderBytes + ((int64_t)it.e * ntiles + it.nt) * kstages * kMxTileBytes;
+                // tiles of the block's rows: its own (grouped), or those of the matrix it starts in (dense)
+                const int64_t t0 = g.sorted_ids ? it.b * art : it.b * pl.tok / kMxTileRows;
+                const uint8_t* at = g.a + kHeaderBytes + t0 * kstages * kMxTileBytes;
+                const int64_t tstride = (int64_t)kstages * kMxTileBytes;
+                const int r0 = min(it.rows, kMxTileRows - it.off), r1 = it.rows - r0;
+                const uint32_t bytes = kMxTileBytes + (uint32_t)it.rows * 128u + (r1 > 0 ? 2048u : 1024u);
+                for (int ks = 0; ks < kstages; ++ks, ++issued, r.next(pl.stages)) {
+                    if (!tc5::wait(&empty[r.slot], r.phase ^ 1u, &flags[1], g.err)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* st = smem + r.slot * pl.stage_bytes;
+                    uint8_t* sb = st + kMxTileBytes;
+                    uint8_t* ss = sb + pl.tok * 128;
+                    const uint8_t* a0 = at + (int64_t)ks * kMxTileBytes;
+                    mbar_arrive_expect_tx(&full[r.slot], bytes);
+                    bulk_g2s(st, wt + (int64_t)ks * kMxTileBytes, kMxTileBytes, &full[r.slot]);
+                    bulk_g2s(sb, a0 + it.off * 128, (uint32_t)r0 * 128u, &full[r.slot]);
+                    bulk_g2s(ss, a0 + kMxCodeBytes, 1024u, &full[r.slot]);
+                    if (r1 > 0) {
+                        bulk_g2s(sb + r0 * 128, a0 + tstride, (uint32_t)r1 * 128u, &full[r.slot]);
+                        bulk_g2s(ss + 1024, a0 + tstride + kMxCodeBytes, 1024u, &full[r.slot]);
+                    }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+        // leave only after every copy issued here has landed
+        if (lane == 0) {
+            for (int k = 0; k < pl.stages && k < issued; ++k) {
+                r.slot = r.slot == 0 ? pl.stages - 1 : r.slot - 1;
+                if (r.slot == pl.stages - 1) r.phase ^= 1u;
+                if (!mbar_wait(&full[r.slot], r.phase)) set_error(g.err, CHORD_DEV_TIMEOUT);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        tc5::Ring r;
+        int64_t nitem = 0, g_stage = 0;
+        int sf_slot = 0;
+        uint64_t* last_bar = nullptr;
+        uint32_t last_parity = 0;
+        bool ok = true;
+        const uint32_t sf_base = tmem + 2u * (uint32_t)pl.tok;
+        for (int64_t i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+            const Item it = item_at(g, pl, i, ntiles, lane, false);
+            if (it.rows == 0) continue;
+            if (lane == 0) {
+                const int buf = (int)(nitem & 1);
+                if (!tc5::wait(&acc_empty[buf], (uint32_t)((nitem >> 1) & 1) ^ 1u, &flags[1], g.err)) ok = false;
+                tc5::fence_after();
+                const uint32_t acc = tmem + (uint32_t)(buf * pl.tok);
+                const uint32_t id0 = tc5::idesc_mxf4(it.rows, 0), id2 = tc5::idesc_mxf4(it.rows, 2);
+                const bool two = it.off + it.rows > kMxTileRows;
+                for (int ks = 0; ks < kstages && ok; ++ks, ++g_stage, r.next(pl.stages)) {
+                    // the scale slot was last read by the instructions of sf_slots stages ago
+                    if (g_stage >= pl.sf_slots && pl.sf_slots < pl.stages) {
+                        const int64_t old = g_stage - pl.sf_slots;
+                        if (!tc5::wait(&empty[old % pl.stages], (uint32_t)((old / pl.stages) & 1), &flags[1], g.err)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if (!tc5::wait(&full[r.slot], r.phase, &flags[1], g.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc5::fence_after();
+                    const uint32_t st = smem_u32(smem + r.slot * pl.stage_bytes);
+                    const uint32_t sb = st + kMxTileBytes, ss = sb + (uint32_t)pl.tok * 128u;
+                    const uint32_t sfa = sf_base + (uint32_t)sf_slot * 24u, sfb = sfa + 8u;
+                    const uint64_t dsa = tc5::desc_scales(st + kMxCodeBytes), dsb = tc5::desc_scales(ss);
+#pragma unroll
+                    for (uint32_t h = 0; h < 2; ++h) {
+                        tc5::cp_scales(sfa + 4u * h, dsa + h * (kMxScaleBlock >> 4));
+                        tc5::cp_scales(sfb + 8u * h, dsb + h * (kMxScaleBlock >> 4));
+                        if (two) tc5::cp_scales(sfb + 8u * h + 4u, dsb + (1024u >> 4) + h * (kMxScaleBlock >> 4));
+                    }
+                    const uint64_t da = tc5::desc_sw128(st), db = tc5::desc_sw128(sb);
+                    const int nk = min(4, (g.K - ks * kMxTileCols + 63) / 64);
+#pragma unroll
+                    for (uint32_t kk = 0; kk < 4; ++kk)
+                        if ((int)kk < nk)
+                            tc5::mma_mxf4(acc, da + 2u * kk, db + 2u * kk, kk & 1 ? id2 : id0, sfa + 4u * (kk >> 1),
+                                          sfb + 8u * (kk >> 1) + (uint32_t)(it.off >> 5), ks > 0 || kk > 0 ? 1u : 0u);
+                    tc5::commit(&empty[r.slot]);
+                    last_bar = &empty[r.slot];
+                    last_parity = r.phase;
+                    if (++sf_slot == pl.sf_slots) sf_slot = 0;
+                }
+                if (ok) tc5::commit(&acc_full[buf]);
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            ++nitem;
+        }
+        // the last instructions are done before the tensor memory is released
+        if (lane == 0 && last_bar) mbar_wait(last_bar, last_parity);
+        __syncwarp();
+    } else {
+        const int wg = warp >> 2, quarter = warp & 3;
+        int64_t nitem = 0;
+        for (int64_t i = blockIdx.x; i < n_items; i += gridDim.x) {
+            const Item it = item_at(g, pl, i, ntiles, lane, warp == 0);
+            if (it.rows == 0) continue;
+            const int buf = (int)(nitem & 1);
+            if (!tc5::wait(&acc_full[buf], (uint32_t)((nitem >> 1) & 1), &flags[1], g.err)) break;
+            tc5::fence_after();
+            drain(g, pl, it, tmem + (uint32_t)(buf * pl.tok), wg, quarter, lane, stg + warp * kStgBytes);
+            tc5::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            ++nitem;
+        }
+    }
+    tc5::fence_before();
+    __syncthreads();
+    tc5::fence_after();
+    if (warp == kProducerWarp) tc5::dealloc(tmem, kTmemCols);
 }
 
 cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
-    const int64_t rows = g.a_groups * g.a_rows;
-    const dim3 grid((unsigned)((g.N + 127) / 128), (unsigned)(rows < 65535 ? rows : 65535));
-    mx_gemm_kernel<<<grid, 128, 0, st>>>(g);
+    MxPlan pl;
+    // Dense blocks: 192 rows (two accumulators and the scales fill the tensor
+    // memory), fewer when the matrix is shorter.
+    pl.tok = g.sorted_ids ? (int)g.a_rows : (g.a_rows > 128 ? 192 : (g.a_rows > 64 ? 128 : 64));
+    const int tiles = (pl.tok + 64 + kMxTileRows - 1) / kMxTileRows;   // row tiles a block may touch
+    pl.stage_bytes = kMxTileBytes + pl.tok * 128 + 1024 * tiles;
+    const size_t fixed = 1024 + kEpiWarps * kStgBytes + 256;
+    pl.stages = (int)((kSmemBudget - fixed) / (pl.stage_bytes + 16));
+    if (pl.stages > 12) pl.stages = 12;
+    if (pl.stages < 2) return cudaErrorInvalidConfiguration;
+    pl.sf_slots = (int)((kTmemCols - 2 * pl.tok) / 24);
+    if (pl.sf_slots > pl.stages) pl.sf_slots = pl.stages;
+    // one CTA per SM: it takes the whole tensor memory (the ring is larger than half the shared memory)
+    const size_t smem = fixed + (size_t)pl.stages * (pl.stage_bytes + 16);
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(mx_gemm_kernel), kSmemBudget);
+    if (e != cudaSuccess) return e;
+    const int64_t ntiles = (g.N + kMxTileRows - 1) / kMxTileRows;
+    const int64_t blocks = g.sorted_ids ? g.a_groups : (g.a_rows + pl.tok - 1) / pl.tok;
+    const int64_t items = blocks * ntiles;
+    const int64_t sms = device_info().sm_count;
+    mx_gemm_kernel<<<(unsigned)(items < sms ? items : sms), kThreads, smem, st>>>(g, pl);
     return cudaGetLastError();
 }
 

@@ -10,6 +10,7 @@
 // FP32 (a power of two), so the only rounding is the code's.  A block that
 // holds an infinity or NaN gets the NaN scale: it stays visible downstream.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -19,15 +20,60 @@
 namespace chord {
 namespace {
 
-__device__ __forceinline__ float load_elem(const void* p, int64_t i, bool f32) {
-    return f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+// E2M1 codes of eight columns, column i in bits 4i (the hardware conversion:
+// round to nearest, ties to even, magnitudes above 5 to 6).
+__device__ __forceinline__ uint32_t e2m1_codes8(const float (&y)[8]) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+    return w;
 }
 
-// Nearest E2M1 code of y (finite): ties to even, |y| above 5 to 6.
-__device__ __forceinline__ uint32_t e2m1_code(float y) {
-    const float a = fabsf(y);
-    const uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
-    return c | (__float_as_uint(y) >> 31 << 3);
+// The values of eight codes as four half pairs (exact).
+__device__ __forceinline__ void e2m1_halves8(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+// Eight consecutive elements; VEC: 16-byte loads (the address is aligned).
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load8(const void* src, int64_t at, float (&v)[8]) {
+    if constexpr (F32) {
+        const float* p = static_cast<const float*>(src) + at;
+        if constexpr (VEC) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __ldg(p + i);
+        }
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(src) + at;
+        if constexpr (VEC) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float((uint32_t)__ldg(p + i) << 16);
+        }
+    }
 }
 
 // Where the rows of a packed matrix come from: row i of group g is row
@@ -43,10 +89,8 @@ struct RowSource {
     int divisor;
 };
 
-__global__ void mx_header_kernel(uint8_t* packed, int64_t G, int64_t N, int K) {
+__device__ __forceinline__ void mx_write_header(uint8_t* packed, int i, int64_t G, int64_t N, int K) {
     const unsigned long long stride = mx_group_bytes(N, K);
-    const int i = threadIdx.x;
-    if (i >= kHeaderBytes / 4) return;
     uint32_t v = 0;
     switch (i) {
         case 0: v = kMagic; break;
@@ -64,9 +108,16 @@ __global__ void mx_header_kernel(uint8_t* packed, int64_t G, int64_t N, int K) {
     reinterpret_cast<uint32_t*>(packed)[i] = v;
 }
 
-// One thread per (row, 32-column group) of the padded tiles.
-__global__ void mx_quantize_kernel(RowSource s, int64_t G, int64_t N, int K, uint8_t* __restrict__ packed, int* err) {
-    const int64_t rt = mx_row_tiles(N), kb = mx_col_tiles(K);
+// One warp takes rows r, r + 32, r + 64, r + 96 of a tile (four independent
+// loads; their scales are 16 contiguous bytes of each scale block), a lane eight
+// columns of each: a group of 32 columns is four lanes, its largest magnitude
+// two shuffles, and a row's codes one 128-byte store.
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int64_t G, int64_t N, int K,
+                                                          uint8_t* __restrict__ packed, int* err) {
+    if (blockIdx.x == 0 && threadIdx.x < kHeaderBytes / 4) mx_write_header(packed, threadIdx.x, G, N, K);
+    const int64_t rt = mx_row_tiles(N);
+    const int kb = (int)mx_col_tiles(K);
     int64_t groups = G;
     if (s.ntp) {
         const int64_t ntp = *s.ntp;
@@ -76,84 +127,141 @@ __global__ void mx_quantize_kernel(RowSource s, int64_t G, int64_t N, int K, uin
         }
         groups = ntp / N;
     }
-    const int64_t total = groups * rt * kb * (kMxTileRows * 8);
+    const int lane = threadIdx.x & 31;
+    const uint32_t j = lane >> 2;
+    const int64_t tasks = groups * rt * kb * 32;
     uint8_t* data = packed + kHeaderBytes;
-    for (int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; q < total; q += (int64_t)gridDim.x * blockDim.x) {
-        const uint32_t j = (uint32_t)(q & 7), r = (uint32_t)(q >> 3) & 127u;
-        const int64_t tile = q >> 10;
-        const int64_t kt = tile % kb, band = tile / kb;
-        const int64_t g = band / rt, row = (band % rt) * kMxTileRows + r;
-        const int64_t k0 = kt * kMxTileCols + j * 32;
-        int64_t base = -1;
-        if (row < N && k0 < K) {
-            if (!s.sorted_ids) {
-                base = g * s.mat_stride + row * s.row_stride + k0;
-            } else {
-                const int32_t id = s.sorted_ids[g * N + row];
-                if (id >= 0 && id < s.id_limit) base = (int64_t)(id / s.divisor) * s.row_stride + k0;
+    for (int64_t q = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; q < tasks;
+         q += ((int64_t)gridDim.x * blockDim.x) >> 5) {
+        const uint32_t r0 = (uint32_t)(q & 31);
+        int kt, bt;
+        const int64_t band = divmod_idx(q >> 5, kb, kt);
+        const int64_t g = divmod_idx(band, (int)rt, bt);
+        const int k0 = kt * kMxTileCols + lane * 8;
+        float v[4][8];
+        uint32_t live = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = (int64_t)bt * kMxTileRows + r0 + 32 * i;
+            int64_t at = -1;
+            if (row < N) {
+                if (!s.sorted_ids) {
+                    at = g * s.mat_stride + row * s.row_stride;
+                } else {
+                    const int32_t id = __ldg(s.sorted_ids + g * N + row);
+                    if (id >= 0 && id < s.id_limit) at = (int64_t)((uint32_t)id / (uint32_t)s.divisor) * s.row_stride;
+                }
             }
-        }
-        float v[32];
-        uint32_t top = 0;
+            if (at >= 0) live |= 1u << i;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            v[i] = base >= 0 ? load_elem(s.src, base + i, s.f32 != 0) : 0.0f;
-            top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+            for (int c = 0; c < 8; ++c) v[i][c] = 0.0f;
+            if (at >= 0 && k0 < K) load8<F32, VEC>(s.src, at + k0, v[i]);
         }
-        const uint32_t ex = top >> 23;   // biased exponent; 0 for zero and subnormals
-        uint32_t b = ex == 255u ? 255u : (ex > 2u ? ex - 2u : 0u);
-        if (base < 0) b = 127u;
-        const float up = __uint_as_float((254u - min(b, 253u)) << 23);   // 2^(127 - b)
-        uint32_t w[4] = {0, 0, 0, 0};
+        if (s.sorted_ids && !live) continue;
+        uint8_t* t = data + (q >> 5) * kMxTileBytes;
+        uint32_t sc[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) w[i >> 3] |= (b == 255u ? 0u : e2m1_code(v[i] * up)) << (4 * (i & 7));
-        uint8_t* t = data + tile * kMxTileBytes;
-        *reinterpret_cast<uint4*>(t + mx_code_offset(r, j)) = make_uint4(w[0], w[1], w[2], w[3]);
-        t[mx_scale_offset(r, j)] = (uint8_t)b;
+        for (int i = 0; i < 4; ++i) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) top = max(top, __float_as_uint(v[i][c]) & 0x7fffffffu);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t ex = top >> 23;   // biased exponent; 0 for zero and subnormals
+            uint32_t b = ex == 255u ? 255u : (ex > 2u ? ex - 2u : 0u);
+            const float up = __uint_as_float((254u - min(b, 253u)) << 23);   // 2^(127 - b)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[i][c] *= up;
+            const uint32_t codes = b == 255u ? 0u : e2m1_codes8(v[i]);
+            if (k0 >= K || !(live >> i & 1u)) b = 127u;   // padding: zeros with scale 1
+            const uint32_t r = r0 + 32 * i;
+            if (!s.sorted_ids || (live >> i & 1u))
+                *reinterpret_cast<uint32_t*>(t + mx_code_offset(r, j) + 4 * (lane & 3)) = codes;
+            uint32_t w = b << (8 * (j & 3));
+            w |= __shfl_xor_sync(0xffffffffu, w, 4);
+            w |= __shfl_xor_sync(0xffffffffu, w, 8);
+            sc[i] = w;
+        }
+        if ((lane & 15) == 0)
+            *reinterpret_cast<uint4*>(t + mx_scale_offset(r0, j)) = make_uint4(sc[0], sc[1], sc[2], sc[3]);
     }
 }
 
-__global__ void mx_dequantize_kernel(const uint8_t* __restrict__ packed, int64_t G, int64_t N, int K, int f32,
-                                     void* __restrict__ out, int* err) {
+// The same split; a lane writes the values of its eight columns of each row.
+template <bool F32>
+__global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ packed, int64_t G, int64_t N,
+                                                            int K, void* __restrict__ out, int* err) {
     if (!mx_header_ok(packed, G, N, K)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_error(err, CHORD_DEV_BAD_HEADER);
         return;
     }
-    const int64_t rt = mx_row_tiles(N), kb = mx_col_tiles(K);
-    const int kg = K / kGroup;
-    const int64_t total = G * N * kg;
+    const int64_t rt = mx_row_tiles(N);
+    const int kb = (int)mx_col_tiles(K);
+    const int lane = threadIdx.x & 31;
+    const uint32_t j = lane >> 2;
+    const int64_t tasks = G * rt * kb * 32;
     const uint8_t* data = packed + kHeaderBytes;
-    for (int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; q < total; q += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t grow = q / kg;
-        const int jg = (int)(q % kg);
-        const int64_t g = grow / N, row = grow % N;
-        const uint8_t* t = data + ((g * rt + row / kMxTileRows) * kb + jg / 8) * kMxTileBytes;
-        const uint32_t r = (uint32_t)(row % kMxTileRows), j = (uint32_t)(jg % 8);
-        const uint4 c = *reinterpret_cast<const uint4*>(t + mx_code_offset(r, j));
-        const float sc = mx_scale_f32(t[mx_scale_offset(r, j)]);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    for (int64_t q = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; q < tasks;
+         q += ((int64_t)gridDim.x * blockDim.x) >> 5) {
+        const uint32_t r0 = (uint32_t)(q & 31);
+        int kt, bt;
+        const int64_t band = divmod_idx(q >> 5, kb, kt);
+        const int64_t g = divmod_idx(band, (int)rt, bt);
+        const int k0 = kt * kMxTileCols + lane * 8;
+        const uint8_t* t = data + (q >> 5) * kMxTileBytes;
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float v = e2m1_f32((w[i >> 3] >> (4 * (i & 7))) & 15u) * sc;
-            const int64_t o = grow * K + jg * 32 + i;
-            if (f32)
-                static_cast<float*>(out)[o] = v;
-            else
-                static_cast<__nv_bfloat16*>(out)[o] = __float2bfloat16_rn(v);
+        for (int i = 0; i < 4; ++i)
+            w[i] = __ldg(reinterpret_cast<const uint32_t*>(t + mx_code_offset(r0 + 32 * i, j) + 4 * (lane & 3)));
+        const uint4 sc = __ldg(reinterpret_cast<const uint4*>(t + mx_scale_offset(r0, j & 4u)));
+        const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = (int64_t)bt * kMxTileRows + r0 + 32 * i;
+            if (row >= N || k0 >= K) continue;
+            const float f = mx_scale_f32((scw[i] >> (8 * (j & 3))) & 255u);
+            uint32_t h[4];
+            e2m1_halves8(w[i], h);
+            float v[8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h[c]));
+                v[2 * c] = p.x * f;
+                v[2 * c + 1] = p.y * f;
+            }
+            const int64_t o = (g * N + row) * K + k0;   // K % 32 == 0: 16-byte aligned
+            if constexpr (F32) {
+                float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+                d[0] = make_float4(v[0], v[1], v[2], v[3]);
+                d[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                uint4 d;
+                d.x = bf2_as_u32(__floats2bfloat162_rn(v[0], v[1]));
+                d.y = bf2_as_u32(__floats2bfloat162_rn(v[2], v[3]));
+                d.z = bf2_as_u32(__floats2bfloat162_rn(v[4], v[5]));
+                d.w = bf2_as_u32(__floats2bfloat162_rn(v[6], v[7]));
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) = d;
+            }
         }
     }
 }
 
-unsigned grid_for(int64_t items, int threads) {
-    const int64_t b = (items + threads - 1) / threads, cap = (int64_t)device_info().sm_count * 16;
+// CTAs of 8 warps for `tasks` warp tasks: at most 8 per SM (the kernels stride).
+unsigned grid_for(int64_t tasks) {
+    const int64_t b = (tasks + 7) / 8, cap = (int64_t)device_info().sm_count * 8;
     return (unsigned)(b < 1 ? 1 : (b > cap ? cap : b));
 }
 
 cudaError_t launch_quantize(const RowSource& s, int64_t G, int64_t N, int K, uint8_t* packed, int* err,
                             cudaStream_t st) {
-    mx_header_kernel<<<1, 64, 0, st>>>(packed, G, N, K);
-    const int64_t items = G * mx_row_tiles(N) * mx_col_tiles(K) * kMxTileRows * 8;
-    if (items > 0) mx_quantize_kernel<<<grid_for(items, 256), 256, 0, st>>>(s, G, N, K, packed, err);
+    const int esz = s.f32 ? 4 : 2;
+    // 16-byte loads where every row starts on a 16-byte boundary
+    const bool vec = (reinterpret_cast<uintptr_t>(s.src) | (s.sorted_ids || N > 1 ? (uintptr_t)(s.row_stride * esz) : 0) |
+                      (G > 1 ? (uintptr_t)(s.mat_stride * esz) : 0)) % 16 == 0;
+    const unsigned grid = grid_for(G * mx_row_tiles(N) * mx_col_tiles(K) * 32);
+    auto kern = s.f32 ? (vec ? mx_quantize_kernel<true, true> : mx_quantize_kernel<true, false>)
+                      : (vec ? mx_quantize_kernel<false, true> : mx_quantize_kernel<false, false>);
+    kern<<<grid, 256, 0, st>>>(s, G, N, K, packed, err);
     return cudaGetLastError();
 }
 
@@ -228,10 +336,11 @@ chord_status chord_mxfp4_dequantize(const void* packed, size_t packed_bytes, int
     if (!packed || !aligned16(packed) || (G * N > 0 && (!out || !aligned16(out)))) return CHORD_ERR_INVALID_ARG;
     const DeviceInfo& di = device_info();
     if (!di.err) return CHORD_ERR_CUDA;
-    const int64_t items = G * N * (K / kGroup);
-    if (items == 0) return CHORD_OK;
-    mx_dequantize_kernel<<<grid_for(items, 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint8_t*>(packed), G, N, K, out_dtype == CHORD_DTYPE_F32, out, di.err);
+    const int64_t tasks = G * mx_row_tiles(N) * mx_col_tiles(K) * 32;
+    if (tasks == 0) return CHORD_OK;
+    auto kern = out_dtype == CHORD_DTYPE_F32 ? mx_dequantize_kernel<true> : mx_dequantize_kernel<false>;
+    kern<<<grid_for(tasks), 256, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<const uint8_t*>(packed), G, N, K,
+                                                                        out, di.err);
     return cudaGetLastError() == cudaSuccess ? CHORD_OK : CHORD_ERR_CUDA;
 }
 

@@ -261,8 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
         __syncwarp();
     } else if (warp == kMmaWarp) {
         tc5::Ring r;
-        int64_t nitem = 0, g_stage = 0;
-        int sf_slot = 0;
+        uint32_t nitem = 0, g_stage = 0, sf_slot = 0;
         uint64_t* last_bar = nullptr;
         uint32_t last_parity = 0;
         bool ok = true;
@@ -270,56 +269,56 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
         for (int64_t i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
             const Item it = item_at(g, pl, i, ntiles, lane, false);
             if (it.rows == 0) continue;
-            if (lane == 0) {
-                const int buf = (int)(nitem & 1);
-                if (!tc5::wait(&acc_empty[buf], (uint32_t)((nitem >> 1) & 1) ^ 1u, &flags[1], g.err)) ok = false;
-                tc5::fence_after();
-                const uint32_t acc = tmem + (uint32_t)(buf * pl.tok);
-                const uint32_t id0 = tc5::idesc_mxf4(it.rows, 0), id2 = tc5::idesc_mxf4(it.rows, 2);
-                const bool two = it.off + it.rows > kMxTileRows;
-                for (int ks = 0; ks < kstages && ok; ++ks, ++g_stage, r.next(pl.stages)) {
-                    // the scale slot was last read by the instructions of sf_slots stages ago
-                    if (g_stage >= pl.sf_slots && pl.sf_slots < pl.stages) {
-                        const int64_t old = g_stage - pl.sf_slots;
-                        if (!tc5::wait(&empty[old % pl.stages], (uint32_t)((old / pl.stages) & 1), &flags[1], g.err)) {
-                            ok = false;
-                            break;
-                        }
-                    }
-                    if (!tc5::wait(&full[r.slot], r.phase, &flags[1], g.err)) {
+            const uint32_t buf = nitem & 1u;
+            if (!tc5::wait(&acc_empty[buf], ((nitem >> 1) & 1u) ^ 1u, &flags[1], g.err)) break;
+            tc5::fence_after();
+            const uint32_t acc = tmem + buf * (uint32_t)pl.tok;
+            const uint32_t id0 = tc5::idesc_mxf4(it.rows, 0), id2 = tc5::idesc_mxf4(it.rows, 2);
+            const bool two = it.off + it.rows > kMxTileRows;
+            for (int ks = 0; ks < kstages; ++ks, ++g_stage, r.next(pl.stages)) {
+                // the scale slot was last read by the instructions of sf_slots stages ago
+                if (g_stage >= (uint32_t)pl.sf_slots && pl.sf_slots < pl.stages) {
+                    const uint32_t old = g_stage - (uint32_t)pl.sf_slots;
+                    if (!tc5::wait(&empty[old % pl.stages], (old / pl.stages) & 1u, &flags[1], g.err)) {
                         ok = false;
                         break;
                     }
-                    tc5::fence_after();
-                    const uint32_t st = smem_u32(smem + r.slot * pl.stage_bytes);
-                    const uint32_t sb = st + kMxTileBytes, ss = sb + (uint32_t)pl.tok * 128u;
-                    const uint32_t sfa = sf_base + (uint32_t)sf_slot * 24u, sfb = sfa + 8u;
-                    const uint64_t dsa = tc5::desc_scales(st + kMxCodeBytes), dsb = tc5::desc_scales(ss);
+                }
+                if (!tc5::wait(&full[r.slot], r.phase, &flags[1], g.err)) {
+                    ok = false;
+                    break;
+                }
+                tc5::fence_after();
+                const uint32_t st = smem_u32(smem) + (uint32_t)(r.slot * pl.stage_bytes);
+                const uint32_t sb = st + kMxTileBytes, ss = sb + (uint32_t)pl.tok * 128u;
+                const uint32_t sfa = sf_base + sf_slot * 24u, sfb = sfa + 8u;
+                const uint64_t dsa = tc5::desc_scales(st + kMxCodeBytes), dsb = tc5::desc_scales(ss);
+                const uint64_t da = tc5::desc_sw128(st), db = tc5::desc_sw128(sb);
+                const int nk = min(4, (g.K - ks * kMxTileCols + 63) / 64);
+                if (tc5::elect()) {
 #pragma unroll
                     for (uint32_t h = 0; h < 2; ++h) {
                         tc5::cp_scales(sfa + 4u * h, dsa + h * (kMxScaleBlock >> 4));
                         tc5::cp_scales(sfb + 8u * h, dsb + h * (kMxScaleBlock >> 4));
                         if (two) tc5::cp_scales(sfb + 8u * h + 4u, dsb + (1024u >> 4) + h * (kMxScaleBlock >> 4));
                     }
-                    const uint64_t da = tc5::desc_sw128(st), db = tc5::desc_sw128(sb);
-                    const int nk = min(4, (g.K - ks * kMxTileCols + 63) / 64);
 #pragma unroll
                     for (uint32_t kk = 0; kk < 4; ++kk)
                         if ((int)kk < nk)
                             tc5::mma_mxf4(acc, da + 2u * kk, db + 2u * kk, kk & 1 ? id2 : id0, sfa + 4u * (kk >> 1),
                                           sfb + 8u * (kk >> 1) + (uint32_t)(it.off >> 5), ks > 0 || kk > 0 ? 1u : 0u);
                     tc5::commit(&empty[r.slot]);
-                    last_bar = &empty[r.slot];
-                    last_parity = r.phase;
-                    if (++sf_slot == pl.sf_slots) sf_slot = 0;
+                    if (ks == kstages - 1) tc5::commit(&acc_full[buf]);
                 }
-                if (ok) tc5::commit(&acc_full[buf]);
+                __syncwarp();
+                last_bar = &empty[r.slot];
+                last_parity = r.phase;
+                if (++sf_slot == (uint32_t)pl.sf_slots) sf_slot = 0;
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             ++nitem;
         }
         // the last instructions are done before the tensor memory is released
-        if (lane == 0 && last_bar) mbar_wait(last_bar, last_parity);
+        if (last_bar) mbar_wait(last_bar, last_parity);
         __syncwarp();
     } else {
         const int wg = warp >> 2, quarter = warp & 3;

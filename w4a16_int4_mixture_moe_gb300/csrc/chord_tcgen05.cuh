@@ -28,6 +28,19 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
                  : "memory");
 }
 
+// One lane of the (converged) warp.  The issuing warp runs its loop with all
+// lanes, so that addresses and descriptors stay warp-uniform, and this lane
+// alone issues the tensor-core instructions.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // D[128 x N] (+)= (A x scales)[128 x 64] * (B x scales)[N x 64]^T, E2M1 codes in
 // shared memory, one E8M0 scale per 32 columns in tensor memory.
 __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,

@@ -47,33 +47,71 @@ __device__ __forceinline__ void e2m1_halves8(uint32_t w, uint32_t (&h)[4]) {
         : "r"(w));
 }
 
-// Eight consecutive elements; VEC: 16-byte loads (the address is aligned).
+// Eight consecutive elements as loaded: bf16 pairs or FP32.  VEC: 16-byte loads
+// (the address is aligned).
+template <bool F32>
+struct Raw {
+    uint32_t w[F32 ? 8 : 4];
+};
+
 template <bool F32, bool VEC>
-__device__ __forceinline__ void load8(const void* src, int64_t at, float (&v)[8]) {
-    if constexpr (F32) {
-        const float* p = static_cast<const float*>(src) + at;
-        if constexpr (VEC) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
+__device__ __forceinline__ void load8(const void* src, int64_t at, Raw<F32>& v) {
+    if constexpr (VEC) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(src) + at * (F32 ? 4 : 2));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __ldg(p + i);
+        for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+            const uint4 a = __ldg(p + i);
+            v.w[4 * i] = a.x, v.w[4 * i + 1] = a.y, v.w[4 * i + 2] = a.z, v.w[4 * i + 3] = a.w;
         }
+    } else if constexpr (F32) {
+        const uint32_t* p = static_cast<const uint32_t*>(src) + at;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v.w[i] = __ldg(p + i);
     } else {
         const uint16_t* p = static_cast<const uint16_t*>(src) + at;
-        if constexpr (VEC) {
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        } else {
+        for (int i = 0; i < 4; ++i) v.w[i] = (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
+    }
+}
+
+// Codes of a lane's eight columns and the biased scale of their group (the
+// lane's quad).  The largest magnitude is found on the bit patterns, whose order
+// is the values' order with infinities and NaN on top.
+template <bool F32>
+__device__ __forceinline__ uint32_t quantize8(const Raw<F32>& v, uint32_t& b) {
+    uint32_t ex;
+    float y[8];
+    if constexpr (F32) {
+        uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float((uint32_t)__ldg(p + i) << 16);
+        for (int i = 0; i < 8; ++i) top = max(top, v.w[i] & 0x7fffffffu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        ex = top >> 23;   // biased exponent; 0 for zero and subnormals
+    } else {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, v.w[i] & 0x7fff7fffu);
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        ex = max(top >> 16, top & 0xffffu) >> 7;
+    }
+    b = ex == 255u ? 255u : (ex > 2u ? ex - 2u : 0u);
+    const uint32_t up = 254u - min(b, 253u);   // exponent field of 2^(127 - b)
+    if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(v.w[i]) * __uint_as_float(up << 23);
+    } else {
+        // exact: a power of two; what falls below bf16's range has code 0
+        const __nv_bfloat162 f = u32_as_bf2(up << 7 | up << 23);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t p = bf2_as_u32(__hmul2(u32_as_bf2(v.w[i]), f));
+            y[2 * i] = __uint_as_float(p << 16);
+            y[2 * i + 1] = __uint_as_float(p & 0xffff0000u);
         }
     }
+    return b == 255u ? 0u : e2m1_codes8(y);
 }
 
 // Where the rows of a packed matrix come from: row i of group g is row
@@ -108,16 +146,18 @@ __device__ __forceinline__ void mx_write_header(uint8_t* packed, int i, int64_t 
     reinterpret_cast<uint32_t*>(packed)[i] = v;
 }
 
-// One warp takes rows r, r + 32, r + 64, r + 96 of a tile (four independent
-// loads; their scales are 16 contiguous bytes of each scale block), a lane eight
-// columns of each: a group of 32 columns is four lanes, its largest magnitude
-// two shuffles, and a row's codes one 128-byte store.
+// One warp takes rows r, r + 32, r + 64, r + 96 of a band of tiles (four
+// independent loads; their scales are 16 contiguous bytes of each scale block)
+// over a run of `run` tiles along K, the next tile's loads in flight while one is
+// converted.  A lane holds eight columns of each row: a group of 32 columns is
+// four lanes, its largest magnitude two shuffles, a row's codes one 128-byte store.
 template <bool F32, bool VEC>
-__global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int64_t G, int64_t N, int K,
+__global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int64_t G, int64_t N, int K, int run,
                                                           uint8_t* __restrict__ packed, int* err) {
     if (blockIdx.x == 0 && threadIdx.x < kHeaderBytes / 4) mx_write_header(packed, threadIdx.x, G, N, K);
     const int64_t rt = mx_row_tiles(N);
     const int kb = (int)mx_col_tiles(K);
+    const int runs = (kb + run - 1) / run;
     int64_t groups = G;
     if (s.ntp) {
         const int64_t ntp = *s.ntp;
@@ -129,121 +169,147 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int
     }
     const int lane = threadIdx.x & 31;
     const uint32_t j = lane >> 2;
-    const int64_t tasks = groups * rt * kb * 32;
+    const int64_t tasks = groups * rt * runs * 32;
     uint8_t* data = packed + kHeaderBytes;
     for (int64_t q = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; q < tasks;
          q += ((int64_t)gridDim.x * blockDim.x) >> 5) {
         const uint32_t r0 = (uint32_t)(q & 31);
-        int kt, bt;
-        const int64_t band = divmod_idx(q >> 5, kb, kt);
+        int part, bt;
+        const int64_t band = divmod_idx(q >> 5, runs, part);
         const int64_t g = divmod_idx(band, (int)rt, bt);
-        const int k0 = kt * kMxTileCols + lane * 8;
-        float v[4][8];
+        const int kt0 = part * run, kt1 = min(kt0 + run, kb);
+        int64_t at[4];   // first element of the row, -1: none
         uint32_t live = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t row = (int64_t)bt * kMxTileRows + r0 + 32 * i;
-            int64_t at = -1;
+            at[i] = -1;
             if (row < N) {
                 if (!s.sorted_ids) {
-                    at = g * s.mat_stride + row * s.row_stride;
+                    at[i] = g * s.mat_stride + row * s.row_stride;
                 } else {
                     const int32_t id = __ldg(s.sorted_ids + g * N + row);
-                    if (id >= 0 && id < s.id_limit) at = (int64_t)((uint32_t)id / (uint32_t)s.divisor) * s.row_stride;
+                    if (id >= 0 && id < s.id_limit) at[i] = (int64_t)((uint32_t)id / (uint32_t)s.divisor) * s.row_stride;
                 }
             }
-            if (at >= 0) live |= 1u << i;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) v[i][c] = 0.0f;
-            if (at >= 0 && k0 < K) load8<F32, VEC>(s.src, at + k0, v[i]);
+            if (at[i] >= 0) live |= 1u << i;
         }
         if (s.sorted_ids && !live) continue;
-        uint8_t* t = data + (q >> 5) * kMxTileBytes;
-        uint32_t sc[4];
+        Raw<F32> cur[4] = {}, nxt[4];
+        auto fetch = [&](Raw<F32>(&v)[4], int kt) {
+            const int k0 = kt * kMxTileCols + lane * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t top = 0;
+            for (int i = 0; i < 4; ++i) {
+                v[i] = Raw<F32>{};
+                if (at[i] >= 0 && k0 < K) load8<F32, VEC>(s.src, at[i] + k0, v[i]);
+            }
+        };
+        fetch(cur, kt0);
+        uint8_t* t = data + (band * kb + kt0) * kMxTileBytes;
+        for (int kt = kt0; kt < kt1; ++kt, t += kMxTileBytes) {
+            if (kt + 1 < kt1) fetch(nxt, kt + 1);
+            const bool in_k = kt * kMxTileCols + lane * 8 < K;
+            uint32_t sc[4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) top = max(top, __float_as_uint(v[i][c]) & 0x7fffffffu);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const uint32_t ex = top >> 23;   // biased exponent; 0 for zero and subnormals
-            uint32_t b = ex == 255u ? 255u : (ex > 2u ? ex - 2u : 0u);
-            const float up = __uint_as_float((254u - min(b, 253u)) << 23);   // 2^(127 - b)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) v[i][c] *= up;
-            const uint32_t codes = b == 255u ? 0u : e2m1_codes8(v[i]);
-            if (k0 >= K || !(live >> i & 1u)) b = 127u;   // padding: zeros with scale 1
-            const uint32_t r = r0 + 32 * i;
-            if (!s.sorted_ids || (live >> i & 1u))
-                *reinterpret_cast<uint32_t*>(t + mx_code_offset(r, j) + 4 * (lane & 3)) = codes;
-            uint32_t w = b << (8 * (j & 3));
-            w |= __shfl_xor_sync(0xffffffffu, w, 4);
-            w |= __shfl_xor_sync(0xffffffffu, w, 8);
-            sc[i] = w;
+            for (int i = 0; i < 4; ++i) {
+                uint32_t b;
+                const uint32_t codes = quantize8<F32>(cur[i], b);
+                const bool row_in = (live >> i & 1u) != 0;
+                if (!in_k || !row_in) b = 127u;   // padding: zeros with scale 1
+                if (!s.sorted_ids || row_in)
+                    *reinterpret_cast<uint32_t*>(t + mx_code_offset(r0 + 32 * i, j) + 4 * (lane & 3)) = codes;
+                uint32_t w = b << (8 * (j & 3));
+                w |= __shfl_xor_sync(0xffffffffu, w, 4);
+                w |= __shfl_xor_sync(0xffffffffu, w, 8);
+                sc[i] = w;
+                cur[i] = nxt[i];
+            }
+            if ((lane & 15) == 0)
+                *reinterpret_cast<uint4*>(t + mx_scale_offset(r0, j)) = make_uint4(sc[0], sc[1], sc[2], sc[3]);
         }
-        if ((lane & 15) == 0)
-            *reinterpret_cast<uint4*>(t + mx_scale_offset(r0, j)) = make_uint4(sc[0], sc[1], sc[2], sc[3]);
     }
 }
 
 // The same split; a lane writes the values of its eight columns of each row.
 template <bool F32>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ packed, int64_t G, int64_t N,
-                                                            int K, void* __restrict__ out, int* err) {
+                                                            int K, int run, void* __restrict__ out, int* err) {
     if (!mx_header_ok(packed, G, N, K)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_error(err, CHORD_DEV_BAD_HEADER);
         return;
     }
     const int64_t rt = mx_row_tiles(N);
     const int kb = (int)mx_col_tiles(K);
+    const int runs = (kb + run - 1) / run;
     const int lane = threadIdx.x & 31;
     const uint32_t j = lane >> 2;
-    const int64_t tasks = G * rt * kb * 32;
+    const int64_t tasks = G * rt * runs * 32;
     const uint8_t* data = packed + kHeaderBytes;
     for (int64_t q = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; q < tasks;
          q += ((int64_t)gridDim.x * blockDim.x) >> 5) {
         const uint32_t r0 = (uint32_t)(q & 31);
-        int kt, bt;
-        const int64_t band = divmod_idx(q >> 5, kb, kt);
+        int part, bt;
+        const int64_t band = divmod_idx(q >> 5, runs, part);
         const int64_t g = divmod_idx(band, (int)rt, bt);
-        const int k0 = kt * kMxTileCols + lane * 8;
-        const uint8_t* t = data + (q >> 5) * kMxTileBytes;
-        uint32_t w[4];
+        const int kt0 = part * run, kt1 = min(kt0 + run, kb);
+        const uint8_t* t = data + (band * kb + kt0) * kMxTileBytes;
+        uint32_t w[4], wn[4] = {};
+        uint4 sc, scn = {};
+        auto fetch = [&](uint32_t(&c)[4], uint4& s4, const uint8_t* tile) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = __ldg(reinterpret_cast<const uint32_t*>(t + mx_code_offset(r0 + 32 * i, j) + 4 * (lane & 3)));
-        const uint4 sc = __ldg(reinterpret_cast<const uint4*>(t + mx_scale_offset(r0, j & 4u)));
-        const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
+            for (int i = 0; i < 4; ++i)
+                c[i] = __ldg(reinterpret_cast<const uint32_t*>(tile + mx_code_offset(r0 + 32 * i, j) + 4 * (lane & 3)));
+            s4 = __ldg(reinterpret_cast<const uint4*>(tile + mx_scale_offset(r0, j & 4u)));
+        };
+        fetch(w, sc, t);
+        const int64_t row0 = (int64_t)bt * kMxTileRows + r0;
+        int64_t o = (g * N + row0) * K + kt0 * kMxTileCols + lane * 8;   // K % 32 == 0: 16-byte aligned
+        for (int kt = kt0; kt < kt1; ++kt, t += kMxTileBytes, o += kMxTileCols) {
+            if (kt + 1 < kt1) fetch(wn, scn, t + kMxTileBytes);
+            const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
+            if (kt * kMxTileCols + lane * 8 < K) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = (int64_t)bt * kMxTileRows + r0 + 32 * i;
-            if (row >= N || k0 >= K) continue;
-            const float f = mx_scale_f32((scw[i] >> (8 * (j & 3))) & 255u);
-            uint32_t h[4];
-            e2m1_halves8(w[i], h);
-            float v[8];
+                for (int i = 0; i < 4; ++i) {
+                    if (row0 + 32 * i >= N) continue;
+                    const float f = mx_scale_f32((scw[i] >> (8 * (j & 3))) & 255u);
+                    uint32_t h[4];
+                    e2m1_halves8(w[i], h);
+                    float v[8];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h[c]));
-                v[2 * c] = p.x * f;
-                v[2 * c + 1] = p.y * f;
+                    for (int c = 0; c < 4; ++c) {
+                        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h[c]));
+                        v[2 * c] = p.x * f;
+                        v[2 * c + 1] = p.y * f;
+                    }
+                    const int64_t oi = o + (int64_t)(32 * i) * K;
+                    if constexpr (F32) {
+                        float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + oi);
+                        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    } else {
+                        uint4 d;
+                        d.x = bf2_as_u32(__floats2bfloat162_rn(v[0], v[1]));
+                        d.y = bf2_as_u32(__floats2bfloat162_rn(v[2], v[3]));
+                        d.z = bf2_as_u32(__floats2bfloat162_rn(v[4], v[5]));
+                        d.w = bf2_as_u32(__floats2bfloat162_rn(v[6], v[7]));
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + oi) = d;
+                    }
+                }
             }
-            const int64_t o = (g * N + row) * K + k0;   // K % 32 == 0: 16-byte aligned
-            if constexpr (F32) {
-                float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
-                d[0] = make_float4(v[0], v[1], v[2], v[3]);
-                d[1] = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-                uint4 d;
-                d.x = bf2_as_u32(__floats2bfloat162_rn(v[0], v[1]));
-                d.y = bf2_as_u32(__floats2bfloat162_rn(v[2], v[3]));
-                d.z = bf2_as_u32(__floats2bfloat162_rn(v[4], v[5]));
-                d.w = bf2_as_u32(__floats2bfloat162_rn(v[6], v[7]));
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) = d;
-            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = wn[i];
+            sc = scn;
         }
     }
+}
+
+// Tiles along K per warp task: up to 4 (loads of the next tile overlap the
+// conversion), fewer while that leaves fewer tasks than the GPU holds warps.
+int run_for(int64_t bands, int kb) {
+    const int64_t warps = (int64_t)device_info().sm_count * 32;
+    int run = 4;
+    while (run > 1 && bands * 32 * ((kb + run - 1) / run) < warps) run >>= 1;
+    return run;
 }
 
 // CTAs of 8 warps for `tasks` warp tasks: at most 8 per SM (the kernels stride).
@@ -258,10 +324,13 @@ cudaError_t launch_quantize(const RowSource& s, int64_t G, int64_t N, int K, uin
     // 16-byte loads where every row starts on a 16-byte boundary
     const bool vec = (reinterpret_cast<uintptr_t>(s.src) | (s.sorted_ids || N > 1 ? (uintptr_t)(s.row_stride * esz) : 0) |
                       (G > 1 ? (uintptr_t)(s.mat_stride * esz) : 0)) % 16 == 0;
-    const unsigned grid = grid_for(G * mx_row_tiles(N) * mx_col_tiles(K) * 32);
+    const int kb = (int)mx_col_tiles(K);
+    const int64_t bands = G * mx_row_tiles(N);
+    const int run = run_for(bands, kb);
+    const unsigned grid = grid_for(bands * ((kb + run - 1) / run) * 32);
     auto kern = s.f32 ? (vec ? mx_quantize_kernel<true, true> : mx_quantize_kernel<true, false>)
                       : (vec ? mx_quantize_kernel<false, true> : mx_quantize_kernel<false, false>);
-    kern<<<grid, 256, 0, st>>>(s, G, N, K, packed, err);
+    kern<<<grid, 256, 0, st>>>(s, G, N, K, run, packed, err);
     return cudaGetLastError();
 }
 
@@ -336,11 +405,13 @@ chord_status chord_mxfp4_dequantize(const void* packed, size_t packed_bytes, int
     if (!packed || !aligned16(packed) || (G * N > 0 && (!out || !aligned16(out)))) return CHORD_ERR_INVALID_ARG;
     const DeviceInfo& di = device_info();
     if (!di.err) return CHORD_ERR_CUDA;
-    const int64_t tasks = G * mx_row_tiles(N) * mx_col_tiles(K) * 32;
-    if (tasks == 0) return CHORD_OK;
+    const int kb = (int)mx_col_tiles(K);
+    const int64_t bands = G * mx_row_tiles(N);
+    if (bands == 0) return CHORD_OK;
+    const int run = run_for(bands, kb);
     auto kern = out_dtype == CHORD_DTYPE_F32 ? mx_dequantize_kernel<true> : mx_dequantize_kernel<false>;
-    kern<<<grid_for(tasks), 256, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<const uint8_t*>(packed), G, N, K,
-                                                                        out, di.err);
+    kern<<<grid_for(bands * ((kb + run - 1) / run) * 32), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        static_cast<const uint8_t*>(packed), G, N, K, run, out, di.err);
     return cudaGetLastError() == cudaSuccess ? CHORD_OK : CHORD_ERR_CUDA;
 }
 

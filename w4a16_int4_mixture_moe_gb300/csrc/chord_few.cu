@@ -4,6 +4,24 @@
 //   out[t]    = bf16( sum over the token's local experts of W2[e] h[t, e] )
 // in two launches: gate_up with the activation and the routing weight, then
 // the down projection with the sum over the experts.
+//
+// The weights' bytes bound the layer, so both kernels stream every used
+// expert's weights once, each lane into its own shared-memory slots (16-byte
+// cp.async, a ring of kDepth units per warp, no barrier in the loop), and multiply on
+// the warp-level tensor cores: a unit is 16 weight rows x 128 columns, the MMA's
+// A side, and column n of the B side is token n of the call, zero where the token
+// does not use the expert.  Lane (g, c) of a warp holds rows g and g + 8 and the
+// 32-column group c of the unit: one 16-byte load and one scale per row.  The
+// MMA's k order inside a unit is whatever puts a lane's own 32 columns into its
+// slots, the same for A and B.
+//   gate_up: an item is 8 gate rows and their 8 up rows of one expert, the K
+//     range split over the warps of a group and joined in shared memory in warp
+//     order; a lane then holds a gate sum and its up sum, and h is written as
+//     two bf16 numbers (value and remainder, 16 significant bits together).
+//   down: a CTA owns rows of the output for all experts; its warps split the
+//     (expert, K unit) pairs and join their sums in warp order, so neither atomics
+//     nor a combine pass are needed.  The kernel is launched early (programmatic
+//     dependent launch) and fills its rings while gate_up still runs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -14,124 +32,697 @@
 namespace chord {
 namespace {
 
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnitBytes = 1280;     // 32 lanes x (2 x 16 bytes of codes + 2 x 4 bytes of scales)
+constexpr int kUpDepth = 6;          // units in flight per warp, gate_up
+constexpr int kDownDepth = 3;        // (units x row tiles) in flight per warp, down
+
 struct FewArgs {
     const uint16_t* x;
     const int32_t* ids;
     const float* wts;
     int T, topk, E, H, I;
-    int mx;              // weights: 0 INT4 blobs, 1 MXFP4
     const uint8_t* w13;
     const uint8_t* w2;
-    float* h;            // [T * topk, I]
+    uint16_t* h;         // [2][T * topk, I]: bf16 values, then bf16 remainders; one row per (expert, token) in use
     uint16_t* out;
     int* err;
     int validate;        // report ids outside [-1, E)
+    int used_cap;        // min(E, T * topk)
+    int warps_item;      // gate_up: warps that share an item's K range
+    int units_warp;      // gate_up: K units of one warp, at most
+    int x_cap;           // gate_up: tokens of an expert whose activations fit the warp's shared memory
 };
 
-__device__ __forceinline__ float bf(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+// ---- which experts are used, by which tokens --------------------------------
+struct Route {
+    int used;
+    const uint16_t* expert;    // ascending
+    const uint32_t* tokens;    // bit t: token t uses it
+    const uint16_t* first;     // its first row of h
+};
 
-// 32 consecutive columns (group j) of row `row` of expert e.
-__device__ __forceinline__ void weights32(const uint8_t* blob, int mx, int e, int row, int N, int K, int j, float* v) {
-    if (mx) {
-        const uint8_t* t = blob + kHeaderBytes +
-                           (((int64_t)e * mx_row_tiles(N) + row / 128) * mx_col_tiles(K) + j / 8) * kMxTileBytes;
-        const uint4 c = *reinterpret_cast<const uint4*>(t + mx_code_offset(row % 128, j % 8));
-        const float s = mx_scale_f32(t[mx_scale_offset(row % 128, j % 8)]);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        for (int i = 0; i < 32; ++i) v[i] = e2m1_f32((w[i >> 3] >> (4 * (i & 7))) & 15u) * s;
-        return;
-    }
-    const uint8_t* t = blob + kHeaderBytes +
-                       (uint64_t)e * ((uint64_t)N * (uint64_t)K * 9ull / 16ull) + ((int64_t)(row / 128) * (K / 64) + j / 2) * 4608;
-    const int r = row % 128, hf = j & 1;
-    const uint4 c = *reinterpret_cast<const uint4*>(t + hf * 2048 + r * 16);
-    const uint32_t s = *reinterpret_cast<const uint16_t*>(t + 4096 + r * 4 + 2 * hf);
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t d[16];
-    for (int i = 0; i < 4; ++i) dequant_row8(w[i], s | (s << 16), d + 4 * i);
-    for (int i = 0; i < 16; ++i) {
-        v[2 * i] = __uint_as_float(d[i] << 16);
-        v[2 * i + 1] = __uint_as_float(d[i] & 0xffff0000u);
-    }
+__host__ __device__ __forceinline__ size_t route_bytes(int E, int P, int used_cap) {
+    return (size_t)E * 4 + (size_t)P * 8 + (size_t)used_cap * 8 + 64 + 16;
 }
 
-// Gate and up rows of column c in the packed w13; false: not a w13 of this shape.
-__device__ __forceinline__ bool gate_up_rows(const FewArgs& a, int c, int& rg, int& ru) {
-    rg = c;
-    ru = a.I + c;
-    if (a.mx) return mx_header_ok(a.w13, a.E, 2 * a.I, a.H);
-    if (header_ok_layout(a.w13, a.E, 2 * a.I, a.H, CHORD_LAYOUT_TCGEN05)) return true;
-    rg = 16 * (c / 8) + c % 8;
-    ru = rg + 8;
-    return header_ok_layout(a.w13, a.E, 2 * a.I, a.H, CHORD_LAYOUT_GATE_UP_INTERLEAVED);
+// Builds the route in shared memory (all threads) and leaves the ids and
+// weights there too.
+__device__ Route build_route(const FewArgs& a, uint8_t* sm, int32_t*& s_ids, float*& s_w, bool report) {
+    const int P = a.T * a.topk, tid = threadIdx.x;
+    uint32_t* mask = reinterpret_cast<uint32_t*>(sm);
+    s_ids = reinterpret_cast<int32_t*>(mask + a.E);
+    s_w = reinterpret_cast<float*>(s_ids + P);
+    uint32_t* tokens = reinterpret_cast<uint32_t*>(s_w + P);
+    uint16_t* expert = reinterpret_cast<uint16_t*>(tokens + a.used_cap);
+    uint16_t* first = expert + a.used_cap;
+    uint32_t* sums = reinterpret_cast<uint32_t*>((reinterpret_cast<uintptr_t>(first + a.used_cap) + 15) & ~(uintptr_t)15);
+    for (int e = tid; e < a.E; e += kThreads) mask[e] = 0;
+    __syncthreads();
+    for (int p = tid; p < P; p += kThreads) {
+        const int32_t e = a.ids[p];
+        s_ids[p] = e;
+        s_w[p] = a.wts[p];
+        if (e >= 0 && e < a.E)
+            atomicOr(&mask[e], 1u << (p / a.topk));
+        else if (report && e != -1)
+            set_error(a.err, CHORD_DEV_BAD_EXPERT);
+    }
+    __syncthreads();
+    // exclusive scan over the experts of (used, rows of h), four experts a thread
+    // (E <= 1024), packed as used << 16 | rows (both at most 1024)
+    uint32_t m[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int e = tid * 4 + i;
+        m[i] = e < a.E ? mask[e] : 0u;
+        mine += m[i] ? (1u << 16) + __popc(m[i]) : 0u;
+    }
+    uint32_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if ((tid & 31) >= o) inc += v;
+    }
+    if ((tid & 31) == 31) sums[tid >> 5] = inc;
+    __syncthreads();
+    uint32_t at = inc - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < (tid >> 5)) at += sums[w];
+        total += sums[w];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (!m[i]) continue;
+        const uint32_t u = at >> 16;
+        expert[u] = (uint16_t)(tid * 4 + i);
+        tokens[u] = m[i];
+        first[u] = (uint16_t)at;
+        at += (1u << 16) + __popc(m[i]);
+    }
+    __syncthreads();
+    return Route{(int)(total >> 16), expert, tokens, first};
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+// ---- weights: addresses and dequantisation ------------------------------------
+// Where a lane's codes and scale word of one weight row are: codes(u) and
+// scale(u) of K unit u.
+template <bool MX>
+struct RowPtr {
+    const uint8_t* code;
+    const uint8_t* scale;
+    uint32_t flip;   // MXFP4: the swizzled 16-byte slot alternates between the tile's halves
+
+    __device__ __forceinline__ void set(const uint8_t* blob, int64_t row_tiles, int e, int row, int K, int c) {
+        const int r = row & 127;
+        if constexpr (MX) {
+            const uint8_t* t = blob + kHeaderBytes + ((int64_t)e * row_tiles + (row >> 7)) * mx_col_tiles(K) * kMxTileBytes;
+            code = t + r * 128 + ((c ^ (r & 7)) << 4);
+            flip = ((r & 4) ? -64 : 64);
+            scale = t + mx_scale_offset(r, 0);
+        } else {
+            const uint8_t* t = blob + kHeaderBytes + ((int64_t)e * row_tiles + (row >> 7)) * (int64_t)(K / 64) * 4608 + (c >> 1) * 4608;
+            code = t + (c & 1) * 2048 + r * 16;
+            scale = t + 4096 + r * 4;
+            flip = 0;
+        }
+    }
+    __device__ __forceinline__ const uint8_t* codes(int u) const {
+        if constexpr (MX)
+            return code + (int64_t)(u >> 1) * kMxTileBytes + (u & 1 ? (int32_t)flip : 0);
+        else
+            return code + (int64_t)u * 9216;
+    }
+    __device__ __forceinline__ const uint8_t* scales(int u) const {
+        if constexpr (MX)
+            return scale + (int64_t)(u >> 1) * kMxTileBytes + (u & 1) * kMxScaleBlock;
+        else
+            return scale + (int64_t)u * 9216;
+    }
+};
+
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4u : 0u) : "memory");
+}
+
+// A unit of 16 rows (row pointers of g and g + 8) to this lane's slots.
+template <bool MX>
+__device__ __forceinline__ void fetch_unit(uint32_t slot, int lane, const RowPtr<MX>& p0, const RowPtr<MX>& p1, int u,
+                                           bool valid) {
+    cp_async16_zfill(slot + lane * 16, valid ? p0.codes(u) : p0.code, valid);
+    cp_async16_zfill(slot + 512 + lane * 16, valid ? p1.codes(u) : p1.code, valid);
+    cp_async4_zfill(slot + 1024 + lane * 4, valid ? p0.scales(u) : p0.scale, valid);
+    cp_async4_zfill(slot + 1152 + lane * 4, valid ? p1.scales(u) : p1.scale, valid);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
 
-// One warp per (pair, column of I).
-__global__ void few_gate_up_kernel(FewArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t q = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (q >= (int64_t)a.T * a.topk * a.I) return;
-    const int p = (int)(q / a.I), c = (int)(q % a.I);
-    const int e = a.ids[p];
-    if (a.validate && lane == 0 && c == 0 && (e < -1 || e >= a.E)) set_error(a.err, CHORD_DEV_BAD_EXPERT);
-    if (e < 0 || e >= a.E) return;
-    int rg, ru;
-    if (!gate_up_rows(a, c, rg, ru)) {
-        set_error(a.err, CHORD_DEV_BAD_HEADER);
-        return;
+// The scale of a lane's group, ready for the dequantisation in use.
+//   INT4, every scale in the one-FMA range: (s * 2^129, -8 s); else (s, s).
+//   MXFP4: a code's three magnitude bits at bits 6..8 of a half-word are the bf16
+//   number value * 2^-126 (subnormal 0.5 included), so one multiply by
+//   2^(b - 1) gives the weight exactly; it fits bf16 for b <= 128, and larger scales
+//   (wide) take two multiplies, 2^126 and 2^(b - 127).
+struct Scale {
+    uint32_t m, n;
+};
+
+template <bool MX, bool FAST>
+__device__ __forceinline__ Scale make_scale(uint32_t word, int c) {
+    Scale s;
+    if constexpr (MX) {
+        const uint32_t b = (word >> (8 * c)) & 255u;
+        const uint32_t m = b <= 128u ? (b + 126u) << 7 : (b == 255u ? 0x7FC0u : (b << 7));
+        s.m = m | m << 16;
+        s.n = b > 128u ? 1u : 0u;
+    } else {
+        const uint32_t sp = prmt(word, c & 1 ? 0x3232u : 0x1010u);
+        s.m = sp;
+        s.n = 0;
+        if constexpr (FAST) fma_scale_pair(sp, s.m, s.n);
     }
-    const uint16_t* x = a.x + (int64_t)(p / a.topk) * a.H;
-    float g = 0.0f, u = 0.0f;
-    for (int j = lane; j < a.H / kGroup; j += 32) {
-        float vg[32], vu[32];
-        weights32(a.w13, a.mx, e, rg, 2 * a.I, a.H, j, vg);
-        weights32(a.w13, a.mx, e, ru, 2 * a.I, a.H, j, vu);
-        for (int i = 0; i < 32; ++i) {
-            const float xv = bf(x[j * 32 + i]);
-            g = fmaf(xv, vg[i], g);
-            u = fmaf(xv, vu[i], u);
-        }
-    }
-    g = warp_sum(g);
-    u = warp_sum(u);
-    if (lane == 0) a.h[(int64_t)p * a.I + c] = a.wts[p] * silu_times(g, u);
+    return s;
 }
 
-// One warp per (token, column of H).
-__global__ void few_down_kernel(FewArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t q = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (q >= (int64_t)a.T * a.H) return;
-    const int t = (int)(q / a.H), n = (int)(q % a.H);
-    const bool ok = a.mx ? mx_header_ok(a.w2, a.E, a.H, a.I) : header_ok_layout(a.w2, a.E, a.H, a.I, CHORD_LAYOUT_TCGEN05);
-    if (!ok) {
-        set_error(a.err, CHORD_DEV_BAD_HEADER);
-        return;
-    }
-    float s = 0.0f;
-    for (int k = 0; k < a.topk; ++k) {
-        const int p = t * a.topk + k, e = a.ids[p];
-        if (e < 0 || e >= a.E) continue;
-        for (int j = lane; j < a.I / kGroup; j += 32) {
-            float v[32];
-            weights32(a.w2, a.mx, e, n, a.H, a.I, j, v);
-            for (int i = 0; i < 32; ++i) s = fmaf(a.h[(int64_t)p * a.I + j * 32 + i], v[i], s);
+// Eight codes to four bf16 pairs; wide: MXFP4 scales above 2 are present.
+template <bool MX, bool FAST>
+__device__ __forceinline__ void dequant8(uint32_t w, const Scale& s, bool wide, uint32_t (&o)[4]) {
+    if constexpr (MX) {
+        uint32_t v[4];
+        v[0] = ((w << 6) & 0x01C001C0u) | ((w << 12) & 0x80008000u);   // columns 0, 4
+        v[1] = ((w << 2) & 0x01C001C0u) | ((w << 8) & 0x80008000u);    // 1, 5
+        v[2] = ((w >> 2) & 0x01C001C0u) | ((w << 4) & 0x80008000u);    // 2, 6
+        v[3] = ((w >> 6) & 0x01C001C0u) | (w & 0x80008000u);           // 3, 7
+        if (wide) {
+            const __nv_bfloat162 big = u32_as_bf2(0x7E807E80u);        // 2^126
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (s.n) v[i] = bf2_as_u32(__hmul2(u32_as_bf2(v[i]), big));
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = bf2_as_u32(__hmul2(u32_as_bf2(v[i]), u32_as_bf2(s.m)));
+    } else if constexpr (FAST) {
+        dequant_row8_fma(w, s.m, s.n, o);
+    } else {
+        dequant_row8(w, s.m, o);
     }
-    s = warp_sum(s);
-    if (lane == 0) a.out[(int64_t)t * a.H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
 }
 
-cudaError_t launch_few(const FewArgs& a, cudaStream_t st) {
-    const int64_t w1 = (int64_t)a.T * a.topk * a.I, w2 = (int64_t)a.T * a.H;
-    few_gate_up_kernel<<<(unsigned)((w1 + 7) / 8), 256, 0, st>>>(a);
-    few_down_kernel<<<(unsigned)((w2 + 7) / 8), 256, 0, st>>>(a);
+// Activations in the order in which dequant8 leaves the columns: INT4 natural,
+// MXFP4 (0, 4), (1, 5), (2, 6), (3, 7).
+template <bool MX>
+__device__ __forceinline__ uint4 b_order(uint4 v) {
+    if constexpr (!MX) return v;
+    uint4 r;
+    asm("prmt.b32 %0, %1, %2, 0x5410;" : "=r"(r.x) : "r"(v.x), "r"(v.z));
+    asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(r.y) : "r"(v.x), "r"(v.z));
+    asm("prmt.b32 %0, %1, %2, 0x5410;" : "=r"(r.z) : "r"(v.y), "r"(v.w));
+    asm("prmt.b32 %0, %1, %2, 0x7632;" : "=r"(r.w) : "r"(v.y), "r"(v.w));
+    return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void group_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Headers of both blobs; inter: w13 in the gate/up-interleaved layout; fast:
+// the one-FMA dequantisation fits the blob asked for.
+template <bool MX>
+__device__ __forceinline__ int check_headers(const FewArgs& a, bool down) {
+    bool inter = false, ok;
+    if constexpr (MX) {
+        ok = mx_header_ok(a.w13, a.E, 2 * a.I, a.H) && mx_header_ok(a.w2, a.E, a.H, a.I);
+    } else {
+        inter = header_ok_layout(a.w13, a.E, 2 * a.I, a.H, CHORD_LAYOUT_GATE_UP_INTERLEAVED);
+        ok = (inter || header_ok_layout(a.w13, a.E, 2 * a.I, a.H, CHORD_LAYOUT_TCGEN05)) &&
+             header_ok_layout(a.w2, a.E, a.H, a.I, CHORD_LAYOUT_TCGEN05);
+    }
+    const bool fast = !MX && ok && header_scales_in_fma_range(down ? a.w2 : a.w13);
+    return (ok ? 1 : 0) | (inter ? 2 : 0) | (fast ? 4 : 0);
+}
+
+// ---- gate_up ----------------------------------------------------------------
+struct UpSmem {
+    uint32_t ring;      // this warp's slots
+    uint32_t x;         // this warp's activations
+    float4* red;        // [2][kWarps][NT][32]
+};
+
+template <bool MX, int NT, bool FAST>
+__device__ __forceinline__ void gate_up_loop(const FewArgs& a, const Route& rt, const int32_t* s_ids, const float* s_w,
+                                             const UpSmem& sm, bool inter) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int W = a.warps_item, ngrp = kWarps / W, grp = warp / W, rank = warp % W;
+    const int U = (a.H + 127) / 128, kgroups = a.H / 32;
+    const int ua = rank * U / W, ub = (rank + 1) * U / W, nu = ub - ua;
+    const int per_e = a.I / 8;
+    const int n_items = rt.used * per_e;
+    const int i0 = (int)((int64_t)blockIdx.x * n_items / gridDim.x), i1 = (int)((int64_t)(blockIdx.x + 1) * n_items / gridDim.x);
+    const int first = i0 + grp;
+    const int mine = first < i1 ? (i1 - first + ngrp - 1) / ngrp : 0;
+    const int steps = mine * nu;
+    const int64_t row_tiles = MX ? mx_row_tiles(2 * a.I) : (2 * a.I) / 128;
+
+    // producer: the next unit to fetch
+    RowPtr<MX> p0, p1;
+    int p_item = first, p_u = ub, p_slot = 0;
+    auto set_rows = [&](int item) {
+        const int ue = item / per_e, col = (item - ue * per_e) * 8 + g;
+        const int e = rt.expert[ue];
+        const int r0 = inter ? 16 * (col >> 3) + (col & 7) : col;
+        p0.set(a.w13, row_tiles, e, r0, a.H, c);
+        p1.set(a.w13, row_tiles, e, inter ? r0 + 8 : a.I + col, a.H, c);
+    };
+    int fetched = 0;
+    auto fetch = [&]() {
+        if (fetched < steps) {
+            if (p_u == ub) {
+                if (fetched) p_item += ngrp;
+                p_u = ua;
+                set_rows(p_item);
+            }
+            fetch_unit<MX>(sm.ring + p_slot * kUnitBytes, lane, p0, p1, p_u, p_u * 4 + c < kgroups);
+            ++p_u;
+            ++fetched;
+            if (++p_slot == kUpDepth) p_slot = 0;
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kUpDepth - 1; ++i) fetch();
+
+    const uint32_t x_stride = (uint32_t)a.units_warp * 256u + 64u;   // one token's activations of this warp's K range
+    int cur = -1, slot = 0;
+    uint32_t tokens = 0;
+    int where[NT];   // token 8 nt + g: byte offset in this warp's activations, -1 not routed here, -2 read from global
+    for (int n = 0; n < mine; ++n) {
+        const int item = first + n * ngrp, ue = item / per_e;
+        if (ue != cur) {
+            cur = ue;
+            tokens = rt.tokens[ue];
+            __syncwarp();
+            int at = 0;
+            for (uint32_t m = tokens; m && at < a.x_cap; m &= m - 1, ++at) {
+                const int t = __ffs(m) - 1;
+                for (int q = lane; q < nu * 16; q += 32) {
+                    // piece q: 8 columns; kept as (unit, piece of the group, group) so that a
+                    // quad's four loads of one piece are contiguous
+                    const int k = (ua * 16 + q) * 8;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (k < a.H) v = b_order<MX>(__ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H + k)));
+                    const uint32_t d = sm.x + (uint32_t)at * x_stride + (uint32_t)((q >> 4) * 256 + (q & 3) * 64 + ((q >> 2) & 3) * 16);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(d), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                                 : "memory");
+                }
+            }
+            __syncwarp();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int t = 8 * nt + g;
+                const int r = __popc(tokens & ((1u << t) - 1u));
+                where[nt] = !(tokens >> t & 1u) ? -1 : (r < a.x_cap ? (int)(r * x_stride) + c * 16 : -2);
+            }
+        }
+        float acc[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[nt][i >> 2][i & 3] = 0.0f;
+        for (int u = ua; u < ub; ++u) {
+            cp_async_wait<kUpDepth - 2>();
+            const uint32_t st = sm.ring + slot * kUnitBytes;
+            const uint4 q0 = lds128(st + lane * 16), q1 = lds128(st + 512 + lane * 16);
+            const Scale s0 = make_scale<MX, FAST>(lds32(st + 1024 + lane * 4), c);
+            const Scale s1 = make_scale<MX, FAST>(lds32(st + 1152 + lane * 4), c);
+            if (++slot == kUpDepth) slot = 0;
+            const bool wide = MX && __any_sync(0xffffffffu, (s0.n | s1.n) != 0);
+            const uint32_t w0[4] = {q0.x, q0.y, q0.z, q0.w}, w1[4] = {q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t x0[4], x1[4];
+                dequant8<MX, FAST>(w0[j], s0, wide, x0);
+                dequant8<MX, FAST>(w1[j], s1, wide, x1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (NT > 1 && !(tokens >> (8 * nt) & 0xffu)) continue;
+                    uint4 b = make_uint4(0, 0, 0, 0);
+                    if (where[nt] >= 0) {
+                        b = lds128(sm.x + (uint32_t)where[nt] + (uint32_t)((u - ua) * 256 + j * 64));
+                    } else if (where[nt] == -2 && u * 4 + c < kgroups) {
+                        b = b_order<MX>(__ldg(reinterpret_cast<const uint4*>(
+                            a.x + (int64_t)(8 * nt + g) * a.H + u * 128 + c * 32 + j * 8)));
+                    }
+                    mma16816(acc[nt][0], x0[0], x1[0], x0[1], x1[1], b.x, b.y);
+                    mma16816(acc[nt][1], x0[2], x1[2], x0[3], x1[3], b.z, b.w);
+                }
+            }
+            fetch();
+        }
+        // join the K ranges of the group's warps, in warp order; the buffer alternates so that
+        // one barrier per item is enough
+        float4* red = sm.red + (size_t)(n & 1) * kWarps * NT * 32;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            red[(warp * NT + nt) * 32 + lane] = make_float4(acc[nt][0][0] + acc[nt][1][0], acc[nt][0][1] + acc[nt][1][1],
+                                                            acc[nt][0][2] + acc[nt][1][2], acc[nt][0][3] + acc[nt][1][3]);
+        if (W > 1)
+            group_sync(1 + grp, W * 32);
+        else
+            __syncwarp();
+        if (rank != n % W) continue;
+        const int e = rt.expert[ue], col = (item - ue * per_e) * 8 + g;
+        const int pos = MX ? (col & ~7) | ((col & 3) << 1) | ((col >> 2) & 1) : col;
+        for (int nt = 0; nt < NT; ++nt) {
+            if (!(tokens >> (8 * nt) & 0xffu)) continue;
+            float4 s = make_float4(0, 0, 0, 0);
+            for (int w = 0; w < W; ++w) {
+                const float4 v = red[((grp * W + w) * NT + nt) * 32 + lane];
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int t = 8 * nt + 2 * c + i;
+                if (!(tokens >> t & 1u)) continue;
+                float wt = 0.0f;
+                for (int k = 0; k < a.topk; ++k)
+                    if (s_ids[t * a.topk + k] == e) wt += s_w[t * a.topk + k];
+                const float h = wt * silu_times(i ? s.y : s.x, i ? s.w : s.z);
+                // bf16 value and remainder; no remainder for infinities and NaN
+                const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+                const float rest = h - __bfloat162float(hi);
+                const int64_t at = (int64_t)(rt.first[ue] + __popc(tokens & ((1u << t) - 1u))) * a.I + pos;
+                a.h[at] = __bfloat16_as_ushort(hi);
+                a.h[at + (int64_t)a.T * a.topk * a.I] =
+                    __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(rest) ? rest : 0.0f));
+            }
+        }
+    }
+    cp_async_wait<0>();
+}
+
+template <bool MX, int NT>
+__global__ void __launch_bounds__(kThreads) few_gate_up_kernel(const FewArgs a) {
+    pdl_trigger();
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int flags;
+    if (threadIdx.x == 0) {
+        flags = check_headers<MX>(a, false);
+        if (!(flags & 1) && blockIdx.x == 0) set_error(a.err, CHORD_DEV_BAD_HEADER);
+    }
+    const int warp = threadIdx.x >> 5;
+    UpSmem sm;
+    sm.ring = smem_u32(smem) + warp * kUpDepth * kUnitBytes;
+    uint8_t* red = smem + kWarps * kUpDepth * kUnitBytes;
+    sm.red = reinterpret_cast<float4*>(red);
+    uint8_t* xs = red + 2 * kWarps * NT * 32 * sizeof(float4);
+    const uint32_t x_warp = (uint32_t)a.x_cap * ((uint32_t)a.units_warp * 256u + 64u);
+    sm.x = smem_u32(xs) + warp * x_warp;
+    int32_t* s_ids;
+    float* s_w;
+    const Route rt = build_route(a, xs + kWarps * x_warp, s_ids, s_w, a.validate && blockIdx.x == 0);
+    if (!(flags & 1)) return;
+    if (MX || (flags & 4))
+        gate_up_loop<MX, NT, true>(a, rt, s_ids, s_w, sm, (flags & 2) != 0);
+    else
+        gate_up_loop<MX, NT, false>(a, rt, s_ids, s_w, sm, (flags & 2) != 0);
+}
+
+// ---- down -------------------------------------------------------------------
+template <bool MX, int NT, int RT, bool FAST>
+__device__ __forceinline__ void down_loop(const FewArgs& a, const Route& rt, uint32_t ring, int tile0, int rank, int ranks,
+                                          float (&acc)[RT][NT][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int KU = (a.I + 127) / 128, kgroups = a.I / 32, tiles = a.H / 16;
+    const int total = rt.used * KU;
+    const int64_t row_tiles = MX ? mx_row_tiles(a.H) : a.H / 128;
+    int pv = rank, p_slot = 0;
+    auto fetch = [&]() {
+        if (pv < total) {
+            const int ue = pv / KU, ku = pv - ue * KU;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                if (RT > 1 && tile0 + i >= tiles) continue;
+                RowPtr<MX> p0, p1;
+                p0.set(a.w2, row_tiles, rt.expert[ue], (tile0 + i) * 16 + g, a.I, c);
+                p1.set(a.w2, row_tiles, rt.expert[ue], (tile0 + i) * 16 + 8 + g, a.I, c);
+                fetch_unit<MX>(ring + (p_slot * RT + i) * kUnitBytes, lane, p0, p1, ku, ku * 4 + c < kgroups);
+            }
+            pv += ranks;
+            if (++p_slot == kDownDepth) p_slot = 0;
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kDownDepth - 1; ++i) fetch();
+    pdl_wait();   // h of the gate_up kernel is complete from here on
+    const int64_t lo_plane = (int64_t)a.T * a.topk * a.I;
+    int slot = 0;
+    for (int v = rank; v < total; v += ranks) {
+        const int ue = v / KU, ku = v - ue * KU;
+        const uint32_t tokens = rt.tokens[ue];
+        const uint16_t* hp[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int t = 8 * nt + g;
+            const bool on = (tokens >> t & 1u) && ku * 4 + c < kgroups;
+            hp[nt] = on ? a.h + (int64_t)(rt.first[ue] + __popc(tokens & ((1u << t) - 1u))) * a.I + ku * 128 + c * 32 : nullptr;
+        }
+        cp_async_wait<kDownDepth - 2>();
+        const uint32_t st = ring + slot * RT * kUnitBytes;
+        if (++slot == kDownDepth) slot = 0;
+        uint4 q[RT][2];
+        Scale s[RT][2];
+        bool wide = false;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            q[i][0] = lds128(st + i * kUnitBytes + lane * 16);
+            q[i][1] = lds128(st + i * kUnitBytes + 512 + lane * 16);
+            s[i][0] = make_scale<MX, FAST>(lds32(st + i * kUnitBytes + 1024 + lane * 4), c);
+            s[i][1] = make_scale<MX, FAST>(lds32(st + i * kUnitBytes + 1152 + lane * 4), c);
+            if constexpr (MX) wide |= (RT == 1 || tile0 + i < tiles) && (s[i][0].n | s[i][1].n) != 0;
+        }
+        if constexpr (MX) wide = __any_sync(0xffffffffu, wide);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4 bh[NT], bl[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                bh[nt] = bl[nt] = make_uint4(0, 0, 0, 0);
+                if (hp[nt]) {
+                    bh[nt] = *reinterpret_cast<const uint4*>(hp[nt] + j * 8);
+                    bl[nt] = *reinterpret_cast<const uint4*>(hp[nt] + lo_plane + j * 8);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                if (RT > 1 && tile0 + i >= tiles) continue;
+                uint32_t x0[4], x1[4];
+                const uint32_t wa = j == 0 ? q[i][0].x : j == 1 ? q[i][0].y : j == 2 ? q[i][0].z : q[i][0].w;
+                const uint32_t wb = j == 0 ? q[i][1].x : j == 1 ? q[i][1].y : j == 2 ? q[i][1].z : q[i][1].w;
+                dequant8<MX, FAST>(wa, s[i][0], wide, x0);
+                dequant8<MX, FAST>(wb, s[i][1], wide, x1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (NT > 1 && !(tokens >> (8 * nt) & 0xffu)) continue;
+                    mma16816(acc[i][nt], x0[0], x1[0], x0[1], x1[1], bh[nt].x, bh[nt].y);
+                    mma16816(acc[i][nt], x0[2], x1[2], x0[3], x1[3], bh[nt].z, bh[nt].w);
+                    mma16816(acc[i][nt], x0[0], x1[0], x0[1], x1[1], bl[nt].x, bl[nt].y);
+                    mma16816(acc[i][nt], x0[2], x1[2], x0[3], x1[3], bl[nt].z, bl[nt].w);
+                }
+            }
+        }
+        fetch();
+    }
+    cp_async_wait<0>();
+}
+
+__device__ __forceinline__ void few_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t cta) {
+    uint32_t ra;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(cta));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(ra)
+                 : "memory");
+    return v;
+}
+
+// gridDim.x = row groups x cluster size; the CTAs of a cluster split the
+// (expert, K unit) pairs of one row group and CTA 0 joins their sums in order.
+template <bool MX, int NT, int RT>
+__global__ void __launch_bounds__(kThreads) few_down_kernel(const FewArgs a, int cluster) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int flags;
+    if (threadIdx.x == 0) flags = check_headers<MX>(a, true);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = cluster > 1 ? (int)(blockIdx.x % cluster) : 0;
+    const int tile0 = (int)(blockIdx.x / cluster) * RT, tiles = a.H / 16;
+    constexpr int kRing = kDownDepth * RT * kUnitBytes;
+    int32_t* s_ids;
+    float* s_w;
+    const Route rt = build_route(a, smem + kWarps * kRing, s_ids, s_w, false);
+    if (!(flags & 1)) return;   // the same in every CTA; the gate_up kernel reported it
+    float acc[RT][NT][4];
+#pragma unroll
+    for (int i = 0; i < RT * NT * 4; ++i) acc[i / (NT * 4)][i / 4 % NT][i % 4] = 0.0f;
+    const uint32_t ring = smem_u32(smem) + warp * kRing;
+    if (MX || (flags & 4))
+        down_loop<MX, NT, RT, true>(a, rt, ring, tile0, cta * kWarps + warp, cluster * kWarps, acc);
+    else
+        down_loop<MX, NT, RT, false>(a, rt, ring, tile0, cta * kWarps + warp, cluster * kWarps, acc);
+    // join the warps' sums in warp order (the rings' space is free now)
+    __syncthreads();
+    float4* red = reinterpret_cast<float4*>(smem);
+    constexpr int kPer = RT * NT * 32;
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            red[warp * kPer + (i * NT + nt) * 32 + lane] =
+                make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+    __syncthreads();
+    if (cluster > 1) {
+        for (int q = threadIdx.x; q < kPer; q += kThreads) {
+            float4 s = red[q];
+            for (int w = 1; w < kWarps; ++w) {
+                const float4 v = red[w * kPer + q];
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
+            red[q] = s;   // only this thread reads slot q of any warp
+        }
+        few_cluster_sync();
+    }
+    if (cta == 0) {
+        for (int q = threadIdx.x; q < kPer; q += kThreads) {
+            float4 s = red[q];
+            if (cluster > 1) {
+                for (int r = 1; r < cluster; ++r) {
+                    const float4 v = ld_cluster(smem_u32(red + q), r);
+                    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+                }
+            } else {
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 v = red[w * kPer + q];
+                    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+                }
+            }
+            const int l = q & 31, nt = (q >> 5) % NT, tile = tile0 + (q >> 5) / NT;
+            if (tile >= tiles) continue;
+            const int row = tile * 16 + (l >> 2), t = 8 * nt + 2 * (l & 3);
+            // + 0.0f: a sum of nothing, or of zeros of either sign, is +0
+            if (t < a.T) {
+                a.out[(int64_t)t * a.H + row] = __bfloat16_as_ushort(__float2bfloat16_rn(s.x + 0.0f));
+                a.out[(int64_t)t * a.H + row + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(s.z + 0.0f));
+            }
+            if (t + 1 < a.T) {
+                a.out[(int64_t)(t + 1) * a.H + row] = __bfloat16_as_ushort(__float2bfloat16_rn(s.y + 0.0f));
+                a.out[(int64_t)(t + 1) * a.H + row + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(s.w + 0.0f));
+            }
+        }
+    }
+    if (cluster > 1) few_cluster_sync();   // CTA 0 has read the others' sums
+}
+
+constexpr size_t kSmemMax = 226 * 1024;   // dynamic; the kernels hold a few static bytes too
+
+template <bool MX, int NT>
+cudaError_t launch_up(FewArgs a, cudaStream_t st) {
+    auto kern = few_gate_up_kernel<MX, NT>;
+    const int U = (a.H + 127) / 128;
+    a.warps_item = U >= 8 ? 8 : (U >= 4 ? 4 : (U >= 2 ? 2 : 1));
+    a.units_warp = (U + a.warps_item - 1) / a.warps_item;
+    const size_t fixed = (size_t)kWarps * kUpDepth * kUnitBytes + 2 * kWarps * NT * 512 + route_bytes(a.E, a.T * a.topk, a.used_cap);
+    // two CTAs per SM; the activations of as many tokens as then fit
+    const size_t tok = (size_t)kWarps * (a.units_warp * 256 + 64);
+    const size_t half = 113 * 1024;
+    int cap = (int)((fixed < half ? half - fixed : 0) / tok);
+    a.x_cap = cap < a.T ? cap : a.T;
+    const size_t smem = fixed + tok * a.x_cap;
+    int per_sm = 1;
+    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, kSmemMax, &per_sm);
+    if (e != cudaSuccess) return e;
+    if (per_sm > 2) per_sm = 2;
+    const int64_t items = (int64_t)a.used_cap * (a.I / 8), groups = kWarps / a.warps_item;
+    const int64_t want = (items + groups - 1) / groups, cap_ctas = (int64_t)device_info().sm_count * per_sm;
+    kern<<<(unsigned)(want < cap_ctas ? want : cap_ctas), kThreads, smem, st>>>(a);
     return cudaGetLastError();
+}
+
+template <bool MX, int NT, int RT>
+cudaError_t launch_down(const FewArgs& a, int cluster, cudaStream_t st) {
+    auto kern = few_down_kernel<MX, NT, RT>;
+    size_t ring = (size_t)kWarps * kDownDepth * RT * kUnitBytes;
+    const size_t sums = (size_t)kWarps * RT * NT * 512;
+    const size_t smem = (ring > sums ? ring : sums) + route_bytes(a.E, a.T * a.topk, a.used_cap);
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmemMax);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.H / 16 + RT - 1) / RT * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl_enabled()) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kern, a, cluster);
+}
+
+template <bool MX, int NT>
+cudaError_t launch_few_nt(const FewArgs& a, cudaStream_t st) {
+    cudaError_t e = launch_up<MX, NT>(a, st);
+    if (e != cudaSuccess) return e;
+    // Row tiles per CTA: enough that one wave of CTAs covers H.  Few tiles: clusters
+    // that split the (expert, K unit) pairs, while every warp still gets one.
+    const int tiles = a.H / 16, sms = device_info().sm_count;
+    const int rt = tiles > 2 * sms ? 3 : (tiles > sms ? 2 : 1);
+    int cluster = 1;
+    const int64_t pairs = (int64_t)a.used_cap * ((a.I + 127) / 128);
+    while (cluster < 8 && rt == 1 && tiles * cluster * 2 <= sms && cluster * 2 * kWarps <= pairs) cluster *= 2;
+    return rt == 3 ? launch_down<MX, NT, 3>(a, cluster, st)
+                   : (rt == 2 ? launch_down<MX, NT, 2>(a, cluster, st) : launch_down<MX, NT, 1>(a, cluster, st));
+}
+
+cudaError_t launch_few(const FewArgs& a, bool mx, cudaStream_t st) {
+    if (a.T <= 8) return mx ? launch_few_nt<true, 1>(a, st) : launch_few_nt<false, 1>(a, st);
+    if (a.T <= 16) return mx ? launch_few_nt<true, 2>(a, st) : launch_few_nt<false, 2>(a, st);
+    return mx ? launch_few_nt<true, 4>(a, st) : launch_few_nt<false, 4>(a, st);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -167,12 +758,24 @@ chord_status chord_moe_layer_few(const void* x, const int32_t* topk_ids, const f
         return CHORD_ERR_INVALID_ARG;
     const DeviceInfo& di = device_info();
     if (!di.err) return CHORD_ERR_CUDA;
-    FewArgs a{static_cast<const uint16_t*>(x), topk_ids, topk_w, T, topk, E, H, I, mx ? 1 : 0,
-              static_cast<const uint8_t*>(packed_w13), static_cast<const uint8_t*>(packed_w2),
-              static_cast<float*>(workspace), static_cast<uint16_t*>(out), di.err,
-              opts && opts->validate ? 1 : 0};
+    FewArgs a{};
+    a.x = static_cast<const uint16_t*>(x);
+    a.ids = topk_ids;
+    a.wts = topk_w;
+    a.T = T;
+    a.topk = topk;
+    a.E = E;
+    a.H = H;
+    a.I = I;
+    a.w13 = static_cast<const uint8_t*>(packed_w13);
+    a.w2 = static_cast<const uint8_t*>(packed_w2);
+    a.h = static_cast<uint16_t*>(workspace);
+    a.out = static_cast<uint16_t*>(out);
+    a.err = di.err;
+    a.validate = opts && opts->validate ? 1 : 0;
+    a.used_cap = T * topk < E ? T * topk : E;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (launch_few(a, st) != cudaSuccess) return CHORD_ERR_CUDA;
+    if (launch_few(a, mx, st) != cudaSuccess) return CHORD_ERR_CUDA;
     if (!opts || !opts->validate) return CHORD_OK;
     int32_t code = 0;
     const chord_status s = chord_get_device_error(st, &code);

@@ -5,41 +5,38 @@
 // in two launches: gate_up with the activation and the routing weight, then
 // the down projection with the sum over the experts.
 //
-// The weights' bytes bound the layer, so both kernels stream every used
-// expert's weights once, each lane into its own shared-memory slots (16-byte
-// cp.async, a ring of units per warp, no barrier in the loop), and multiply on the
-// warp-level tensor cores: a tile is 16 weight rows x 128 columns, the MMA's A
-// side, with tokens on the B side.  Lane (g, c) of a warp holds rows g and g + 8 and
-// the 32-column group c of the tile: one 16-byte load and one scale per row.  The
-// MMA's k order inside a tile is whatever puts a lane's own 32 columns into its
-// slots, the same for A and B.
-//   gate_up: an item is 16 gate rows and their 16 up rows of one expert (two
-//     tiles of 8 + 8), B column j its j-th token, the K range split over the warps of
-//     a group and joined in shared memory in warp order; a lane then holds a gate
-//     sum and its up sum, and h is written as two bf16 numbers (value and
-//     remainder, 16 significant bits together).
-//   down: a CTA owns rows of the output for all experts, B column t token t of the
-//     call (zero where it does not use the expert); its warps split the (expert, K
-//     unit) pairs and join their sums in warp order, so neither atomics nor a
-//     combine pass are needed.  The kernel is launched early (programmatic
-//     dependent launch) and fills its rings while gate_up still runs.
+// The used experts' weight bytes bound the layer, next to them the instructions that
+// turn codes into bf16.  Both kernels are the same stream: a producer lane copies K
+// stages of 128 weight rows (and the tokens' activations for those columns) into
+// a ring with cp.async.bulk; four consumer warps take 32 rows each, dequantise in registers
+// and multiply on the warp-level tensor cores with up to eight tokens on the B side.  A
+// 16 x 128 tile is a warp's A operand: lane (g, c) holds rows g and g + 8 and the
+// 32-column group c, one 16-byte load and one scale per row; the MMA's k order
+// inside a tile is whatever puts a lane's own 32 columns into its slots, the same for A
+// and B.  An expert with more than eight tokens is taken in several passes.
+//   gate_up: an item is 64 gate rows and their 64 up rows of one expert, so a lane
+//     ends with a gate sum and its up sum; h is written as two bf16 numbers (value
+//     and remainder, 16 significant bits together).  Few items: a cluster of CTAs
+//     splits K and joins the sums through distributed shared memory in rank order.
+//   down: a cluster of CTAs owns 128 output rows for all experts, splits the
+//     (expert, K stage) list, and joins the FP32 sums in rank order, so neither
+//     atomics nor a combine pass are needed.  It is launched early (programmatic
+//     dependent launch) and its weights are on the way while gate_up still runs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "chord_internal.h"
 #include "chord_mxfp4.cuh"
+#include "chord_tcgen05.cuh"
 
 namespace chord {
 namespace {
 
-constexpr int kUpWarps = 8;
-constexpr int kUpThreads = kUpWarps * 32;
-constexpr int kTileBytes = 1280;     // a tile's slots: 32 lanes x (2 x 16 bytes of codes + 2 x 4 bytes of scales)
-constexpr int kUpDepth = 3;          // units (two tiles) in flight per warp, gate_up
-constexpr int kDownDepth = 2;        // units (RT tiles) in flight per warp, down
-constexpr size_t kSmemMax = 226 * 1024;    // dynamic; the kernels hold a few static bytes too
-constexpr size_t kSmemHalf = 112 * 1024;   // two CTAs per SM
+constexpr int kConsumers = 4;                      // warps, 32 weight rows each
+constexpr int kThreads = (kConsumers + 1) * 32;    // and the producer warp
+constexpr int kPassTokens = 8;                     // tokens of one pass over an expert (MMA N)
+constexpr size_t kSmemMax = 226 * 1024;            // dynamic; the kernels hold a few static bytes too
 
 struct FewArgs {
     const uint16_t* x;
@@ -48,41 +45,39 @@ struct FewArgs {
     int T, topk, E, H, I;
     const uint8_t* w13;
     const uint8_t* w2;
-    uint16_t* h;         // [2][T * topk, I]: bf16 values, then bf16 remainders; one row per (expert, token) in use
+    uint16_t* h;         // [2][T * topk, Ip]: bf16 values, then bf16 remainders; a row per (expert, token) in use
+    int Ip;              // I rounded up to whole stages
     uint16_t* out;
     int* err;
     int validate;        // report ids outside [-1, E)
-    int used_cap;        // min(E, T * topk)
-    int warps_item;      // gate_up: warps that share an item's K range
-    int units_warp;      // gate_up: K units of one warp, at most
-    int x_cap;           // gate_up: tokens of an expert whose activations fit in shared memory
+    int slot_cap;        // most passes a call can need
+    int cluster;         // CTAs that share an item (gate_up) or an output tile (down)
+    int depth;           // stages of the ring
 };
 
-// ---- which experts are used, by which tokens --------------------------------
+// ---- passes: which experts are used, by which tokens -----------------------
 struct Route {
-    int used;
-    const uint16_t* expert;    // ascending
-    const uint32_t* tokens;    // bit t: token t uses it
-    const uint16_t* first;     // its first row of h
+    int slots;                 // passes: (expert, up to eight of its tokens), experts ascending
+    const uint16_t* expert;
+    const uint32_t* tokens;    // bit t: token t
+    const uint16_t* first;     // row of h of the pass's first token
 };
 
-__host__ __device__ __forceinline__ size_t route_bytes(int E, int P, int used_cap) {
-    return (size_t)E * 4 + (size_t)P * 8 + (size_t)used_cap * 8 + 128 + 16;
+__host__ __device__ __forceinline__ size_t route_bytes(int E, int P, int slot_cap) {
+    return ((size_t)E * 4 + (size_t)P * 8 + (size_t)slot_cap * 8 + 64 + 127) / 128 * 128;
 }
 
-// Builds the route in shared memory (all threads) and leaves the ids and
+// Builds the passes in shared memory (all threads) and leaves the ids and
 // weights there too.
-template <int WARPS>
 __device__ Route build_route(const FewArgs& a, uint8_t* sm, int32_t*& s_ids, float*& s_w, bool report) {
     const int P = a.T * a.topk, tid = threadIdx.x;
     uint32_t* mask = reinterpret_cast<uint32_t*>(sm);
     s_ids = reinterpret_cast<int32_t*>(mask + a.E);
     s_w = reinterpret_cast<float*>(s_ids + P);
     uint32_t* tokens = reinterpret_cast<uint32_t*>(s_w + P);
-    uint16_t* expert = reinterpret_cast<uint16_t*>(tokens + a.used_cap);
-    uint16_t* first = expert + a.used_cap;
-    uint32_t* sums = reinterpret_cast<uint32_t*>((reinterpret_cast<uintptr_t>(first + a.used_cap) + 15) & ~(uintptr_t)15);
-    constexpr int kThreads = WARPS * 32, kPer = 1024 / kThreads;   // experts per thread in the scan (E <= 1024)
+    uint32_t* sums = tokens + a.slot_cap;
+    uint16_t* expert = reinterpret_cast<uint16_t*>(sums + 16);
+    uint16_t* first = expert + a.slot_cap;
     for (int e = tid; e < a.E; e += kThreads) mask[e] = 0;
     __syncthreads();
     for (int p = tid; p < P; p += kThreads) {
@@ -95,14 +90,14 @@ __device__ Route build_route(const FewArgs& a, uint8_t* sm, int32_t*& s_ids, flo
             set_error(a.err, CHORD_DEV_BAD_EXPERT);
     }
     __syncthreads();
-    // exclusive scan over the experts of (used, rows of h), packed as
-    // used << 16 | rows (both at most 1024)
-    uint32_t m[kPer], mine = 0;
+    // exclusive scan over the experts of (passes, rows of h), packed as
+    // passes << 16 | rows (both at most 1024)
+    constexpr int kPer = (1024 + kThreads - 1) / kThreads;
+    uint32_t mine = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i;
-        m[i] = e < a.E ? mask[e] : 0u;
-        mine += m[i] ? (1u << 16) + __popc(m[i]) : 0u;
+        const int e = tid * kPer + i, n = e < a.E ? __popc(mask[e]) : 0;
+        mine += (uint32_t)((n + kPassTokens - 1) / kPassTokens) << 16 | (uint32_t)n;
     }
     uint32_t inc = mine;
 #pragma unroll
@@ -114,82 +109,63 @@ __device__ Route build_route(const FewArgs& a, uint8_t* sm, int32_t*& s_ids, flo
     __syncthreads();
     uint32_t at = inc - mine, total = 0;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < (tid >> 5)) at += sums[w];
         total += sums[w];
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        if (!m[i]) continue;
-        const uint32_t u = at >> 16;
-        expert[u] = (uint16_t)(tid * kPer + i);
-        tokens[u] = m[i];
-        first[u] = (uint16_t)at;
-        at += (1u << 16) + __popc(m[i]);
+        const int e = tid * kPer + i;
+        uint32_t m = e < a.E ? mask[e] : 0u;
+        while (m) {
+            uint32_t part = 0;
+            for (int k = 0; k < kPassTokens && m; ++k) {
+                part |= m & (0u - m);
+                m &= m - 1;
+            }
+            const uint32_t u = at >> 16;
+            expert[u] = (uint16_t)e;
+            tokens[u] = part;
+            first[u] = (uint16_t)at;
+            at += (1u << 16) + __popc(part);
+        }
     }
     __syncthreads();
     return Route{(int)(total >> 16), expert, tokens, first};
 }
 
-// ---- weights: addresses and dequantisation ------------------------------------
-// Offsets from an expert's first byte of a lane's codes (group c of K unit 0)
-// and scale word of weight row `row`; the next row of the same 8-row phase (row + 8) is
-// kRow8 and kScale8 further on, K unit u at unit_offset(u).
+// Position of the n-th set bit of m (n below their number; mostly 0 or 1 here).
+__device__ __forceinline__ int nth_bit(uint32_t m, int n) {
+    for (; n > 0; --n) m &= m - 1;
+    return __ffs(m) - 1;
+}
+
+// ---- stages -----------------------------------------------------------------
+// INT4: 128 columns.  The blob's four (64-column chunk, 32-column half) blocks of
+//   codes go 32 bytes further apart than they are long, so that the four lanes of a
+//   quad read different banks; then the scale words, row r of chunk h at 512 h + 4 r.
+// MXFP4: 256 columns, 128-byte swizzled rows as in the blob, then the scale blocks.
+// After the weights: the activations, one row per token of the pass.
 template <bool MX>
-struct Lay {
-    static constexpr uint32_t kRow8 = MX ? 1024 : 128, kScale8 = MX ? 128 : 32;
-    static __device__ __forceinline__ uint64_t expert_bytes(int N, int K) {
-        return MX ? mx_group_bytes(N, K) : (uint64_t)N * (uint64_t)K * 9ull / 16ull;
-    }
-    static __device__ __forceinline__ uint32_t code(int row, int K, int c) {
-        const uint32_t r = row & 127;
-        if constexpr (MX)
-            return (uint32_t)(row >> 7) * (uint32_t)mx_col_tiles(K) * kMxTileBytes + r * 128 + ((c ^ (r & 7)) << 4);
-        else
-            return (uint32_t)(row >> 7) * (uint32_t)(K / 64) * 4608u + (c >> 1) * 4608 + (c & 1) * 2048 + r * 16;
-    }
-    static __device__ __forceinline__ uint32_t scale(int row, int K, int c) {
-        const uint32_t r = row & 127;
-        if constexpr (MX)
-            return (uint32_t)(row >> 7) * (uint32_t)mx_col_tiles(K) * kMxTileBytes + mx_scale_offset(r, 0);
-        else
-            return (uint32_t)(row >> 7) * (uint32_t)(K / 64) * 4608u + (c >> 1) * 4608 + 4096 + r * 4;
-    }
-    // MXFP4: two units share a 256-column tile; the swizzled code slot of the second
-    // one is 64 bytes up or down (g: the lane's row mod 8)
-    static __device__ __forceinline__ int64_t code_unit(int u, int g) {
-        if constexpr (MX) return (int64_t)(u >> 1) * kMxTileBytes + (u & 1 ? (g & 4 ? -64 : 64) : 0);
-        return (int64_t)u * 9216;
-    }
-    static __device__ __forceinline__ int64_t scale_unit(int u) {
-        if constexpr (MX) return (int64_t)(u >> 1) * kMxTileBytes + (u & 1) * kMxScaleBlock;
-        return (int64_t)u * 9216;
-    }
+struct Stage {
+    static constexpr int kCols = MX ? 256 : 128;
+    static constexpr int kUnits = kCols / 128;
+    static constexpr int kBlock = 2048 + 32;                  // INT4
+    static constexpr int kScale = MX ? 16384 : 4 * kBlock;    // offset of the scales
+    static constexpr int kUpWeights = kScale + (MX ? 4096 : 1024);
+    static constexpr int kDownWeights = kScale + 1024;
+    static constexpr int kUpRow = kCols * 2 + 16;             // activations of a token, gate_up
+    static constexpr int kDownRow = kCols * 4 + 64;           // value and remainder, down
+    static constexpr int kUpBytes = kUpWeights + kPassTokens * kUpRow;
+    static constexpr int kDownBytes = kDownWeights + kPassTokens * kDownRow;
+    static_assert(kUpBytes % 128 == 0 && kDownBytes % 128 == 0, "stages stay 128-byte aligned");
 };
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
-// A tile's rows g and g + 8 to this lane's slots: codes at 0 and 512, the two
-// scale words together at 1024.  Columns past K (off): zeros.
-__device__ __forceinline__ void fetch_tile(uint32_t slot, int lane, const uint8_t* c0, const uint8_t* c1, const uint8_t* s0,
-                                           const uint8_t* s1, bool on) {
-    const uint32_t d = slot + lane * 16, ds = slot + 1024 + lane * 8;
-    if (on) {
-        cp_async16(d, c0);
-        cp_async16(d + 512, c1);
-        cp_async4(ds, s0);
-        cp_async4(ds + 4, s1);
-    } else {
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        sts128(d, z);
-        sts128(d + 512, z);
-        asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(ds), "r"(0) : "memory");
-    }
+// MXFP4 rows are 128 bytes apart and swizzled by row mod 8: with MMA row g taken
+// from row (g & 1) * 4 + g / 2 the eight lanes of a load phase hit different banks.
+template <bool MX>
+__device__ __forceinline__ int phys_row(int g) {
+    return MX ? ((g & 1) << 2) | (g >> 1) : g;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -197,9 +173,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
@@ -209,7 +185,7 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 
 //   MXFP4: a code's three magnitude bits at bits 6..8 of a half-word are the bf16
 //   number value * 2^-126 (subnormal 0.5 included), so one multiply by
 //   2^(b - 1) gives the weight exactly; it fits bf16 for b <= 128, and larger scales
-//   (wide) take two multiplies, 2^126 and 2^(b - 127).
+//   (n set) take two multiplies, 2^126 and 2^(b - 127).
 struct Scale {
     uint32_t m, n;
 };
@@ -268,20 +244,27 @@ __device__ __forceinline__ uint4 b_order(uint4 v) {
     return r;
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+// Where column `col` of an h row is kept: by 128-column unit, then (8-column piece
+// of the group, group), so that a quad's loads of one piece are contiguous, in b_order.
+template <bool MX>
+__device__ __forceinline__ int h_pos(int col) {
+    const int e = MX ? ((col & 3) << 1) | ((col >> 2) & 1) : col & 7;
+    return (col & ~127) | ((col >> 3) & 3) << 5 | ((col >> 5) & 3) << 3 | e;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&r0)[4], const uint32_t (&r1)[4], const uint4& b) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(r0[0]), "r"(r1[0]), "r"(r0[1]), "r"(r1[1]), "r"(b.x), "r"(b.y));
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(r0[2]), "r"(r1[2]), "r"(r0[3]), "r"(r1[3]), "r"(b.z), "r"(b.w));
 }
 
-__device__ __forceinline__ void group_sync(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// Headers of both blobs; inter: w13 in the gate/up-interleaved layout; fast:
-// the one-FMA dequantisation fits the blob asked for.
+// Headers of both blobs: bit 0 they fit the call, bit 1 w13 in the gate/up-interleaved
+// layout, bit 2 the one-FMA dequantisation fits the blob asked for.
 template <bool MX>
 __device__ __forceinline__ int check_headers(const FewArgs& a, bool down) {
     bool inter = false, ok;
@@ -296,342 +279,13 @@ __device__ __forceinline__ int check_headers(const FewArgs& a, bool down) {
     return (ok ? 1 : 0) | (inter ? 2 : 0) | (fast ? 4 : 0);
 }
 
-// Position of the n-th set bit of m (n below their number; mostly 0 or 1 here).
-__device__ __forceinline__ int nth_bit(uint32_t m, int n) {
-    for (; n > 0; --n) m &= m - 1;
-    return __ffs(m) - 1;
-}
-
-// ---- gate_up ----------------------------------------------------------------
-struct UpSmem {
-    uint32_t ring;      // this warp's slots
-    uint32_t x;         // this warp's activations
-    uint32_t zero;      // 256 bytes of zeros: what lanes without a token read
-    float4* red;        // [2][kUpWarps][2][32]
-};
-
-// One item's K range of one warp.  SPILL: the expert has more tokens than x_cap,
-// the others' activations are read from global memory.
-template <bool MX, int NT, bool FAST, bool SPILL, typename Fetch>
-__device__ __forceinline__ void up_units(const FewArgs& a, const UpSmem& sm, int ua, int ub, int nts, int& slot,
-                                         const uint32_t (&xa)[NT], const uint32_t (&step)[NT], const int (&far)[NT],
-                                         float (&acc)[2][NT][4], Fetch&& fetch) {
-    const int lane = threadIdx.x & 31, c = lane & 3;
-    for (int u = ua; u < ub; ++u) {
-        cp_async_wait<kUpDepth - 2>();
-        const uint32_t st = sm.ring + slot * 2 * kTileBytes + lane * 16;
-        if (++slot == kUpDepth) slot = 0;
-        uint4 q[2][2];
-        Scale s[2][2];
-        bool wide = false;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            q[i][0] = lds128(st + i * kTileBytes);
-            q[i][1] = lds128(st + i * kTileBytes + 512);
-            const uint2 w = lds64(st + i * kTileBytes + 1024 - lane * 8);
-            s[i][0] = make_scale<MX, FAST>(w.x, c);
-            s[i][1] = make_scale<MX, FAST>(w.y, c);
-            if constexpr (MX) wide |= (s[i][0].n | s[i][1].n) != 0;
-        }
-        if constexpr (MX) wide = __any_sync(0xffffffffu, wide);
-        fetch();   // into the slots that the unit before this one left
-        const uint32_t at = (uint32_t)(u - ua) * 256u;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t x[2][2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                dequant8<MX, FAST>(word(q[i][0], j), s[i][0], wide, x[i][0]);
-                dequant8<MX, FAST>(word(q[i][1], j), s[i][1], wide, x[i][1]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (NT > 1 && nt >= nts) continue;
-                uint4 b = lds128(xa[nt] + (at & step[nt]) + j * 64);
-                if constexpr (SPILL) {
-                    if (far[nt] >= 0 && (u * 4 + c) * 32 < a.H)
-                        b = b_order<MX>(__ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)far[nt] * a.H + u * 128 + c * 32 + j * 8)));
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mma16816(acc[i][nt], x[i][0][0], x[i][1][0], x[i][0][1], x[i][1][1], b.x, b.y);
-                    mma16816(acc[i][nt], x[i][0][2], x[i][1][2], x[i][0][3], x[i][1][3], b.z, b.w);
-                }
-            }
-        }
-    }
-}
-
-template <bool MX, int NT, bool FAST>
-__device__ __forceinline__ void gate_up_loop(const FewArgs& a, const Route& rt, const int32_t* s_ids, const float* s_w,
-                                             const UpSmem& sm, bool inter) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int W = a.warps_item, ngrp = kUpWarps / W, grp = warp / W, rank = warp % W;
-    const int U = (a.H + 127) / 128, kgroups = a.H / 32;
-    const int ua = rank * U / W, ub = (rank + 1) * U / W, nu = ub - ua;
-    const int per_e = a.I / 16;
-    const int n_items = rt.used * per_e;
-    const int i0 = (int)((int64_t)blockIdx.x * n_items / gridDim.x), i1 = (int)((int64_t)(blockIdx.x + 1) * n_items / gridDim.x);
-    const int first = i0 + grp;
-    const int mine = first < i1 ? (i1 - first + ngrp - 1) / ngrp : 0;
-    const int steps = mine * nu;
-    const uint64_t expert_bytes = Lay<MX>::expert_bytes(2 * a.I, a.H);
-    // interleaved: rows of tile i at 16 i of the item's 32 (8 gate, 8 up); else gate and up rows 8 i apart
-    const uint32_t d_code = (inter ? 2 : 1) * Lay<MX>::kRow8, d_scale = (inter ? 2 : 1) * Lay<MX>::kScale8;
-
-    // producer: the next unit to fetch
-    const uint8_t *gc = nullptr, *gs = nullptr, *uc = nullptr, *us = nullptr;
-    int p_item = first, p_u = ub, p_slot = 0, fetched = 0;
-    auto fetch = [&]() {
-        if (fetched < steps) {
-            if (p_u == ub) {
-                if (fetched) p_item += ngrp;
-                p_u = ua;
-                const int ue = p_item / per_e, it = p_item - ue * per_e;
-                const uint8_t* base = a.w13 + kHeaderBytes + (uint64_t)rt.expert[ue] * expert_bytes;
-                const int gr = inter ? 32 * it + g : 16 * it + g, ur = inter ? gr + 8 : a.I + gr;
-                gc = base + Lay<MX>::code(gr, a.H, c);
-                gs = base + Lay<MX>::scale(gr, a.H, c);
-                uc = base + Lay<MX>::code(ur, a.H, c);
-                us = base + Lay<MX>::scale(ur, a.H, c);
-            }
-            const int64_t co = Lay<MX>::code_unit(p_u, g), so = Lay<MX>::scale_unit(p_u);
-            const bool on = p_u * 4 + c < kgroups;
-            const uint32_t slot = sm.ring + p_slot * 2 * kTileBytes;
-            fetch_tile(slot, lane, gc + co, uc + co, gs + so, us + so, on);
-            fetch_tile(slot + kTileBytes, lane, gc + co + d_code, uc + co + d_code, gs + so + d_scale, us + so + d_scale, on);
-            ++p_u;
-            ++fetched;
-            if (++p_slot == kUpDepth) p_slot = 0;
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kUpDepth - 1; ++i) fetch();
-
-    const uint32_t x_stride = (uint32_t)a.units_warp * 256u + 64u;   // one token's activations of this warp's K range
-    int cur = -1, slot = 0, join = 0, ntok = 0;
-    uint32_t tokens = 0;
-    // B column 8 nt + g: address and step (all ones, or 0 for the zeros) of its
-    // activations in shared memory; far: the token whose activations are in global memory
-    uint32_t xa[NT], step[NT];
-    int far[NT];
-    for (int n = 0; n < mine; ++n) {
-        const int item = first + n * ngrp, ue = item / per_e;
-        if (ue != cur) {
-            cur = ue;
-            tokens = rt.tokens[ue];
-            ntok = __popc(tokens);
-            __syncwarp();
-            int at = 0;
-            for (uint32_t m = tokens; m && at < a.x_cap; m &= m - 1, ++at) {
-                const int t = __ffs(m) - 1;
-                for (int q = lane; q < nu * 16; q += 32) {
-                    // piece q: 8 columns; kept as (unit, piece of the group, group) so that a
-                    // quad's four loads of one piece are contiguous
-                    const int k = (ua * 16 + q) * 8;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (k < a.H) v = b_order<MX>(__ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.H + k)));
-                    sts128(sm.x + (uint32_t)at * x_stride + (uint32_t)((q >> 4) * 256 + (q & 3) * 64 + ((q >> 2) & 3) * 16), v);
-                }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int col = 8 * nt + g;
-                const bool near = col < ntok && col < a.x_cap;
-                xa[nt] = (near ? sm.x + (uint32_t)col * x_stride : sm.zero) + c * 16;
-                step[nt] = near ? 0xffffffffu : 0u;
-                far[nt] = -1;
-                if (col < ntok && !near) far[nt] = nth_bit(tokens, col);
-            }
-        }
-        float acc[2][NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i >> 2][nt][i & 3] = 0.0f;
-        const int nts = (ntok + 7) / 8;
-        if (ntok > a.x_cap)
-            up_units<MX, NT, FAST, true>(a, sm, ua, ub, nts, slot, xa, step, far, acc, fetch);
-        else
-            up_units<MX, NT, FAST, false>(a, sm, ua, ub, nts, slot, xa, step, far, acc, fetch);
-        // join the K ranges of the group's warps in warp order, eight tokens at a time (the
-        // buffers alternate, so one barrier each is enough; the warps take turns joining)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (nt >= nts) continue;
-            float4* red = sm.red + (size_t)(join & 1) * kUpWarps * 64;
-            red[warp * 64 + lane] = make_float4(acc[0][nt][0], acc[0][nt][1], acc[0][nt][2], acc[0][nt][3]);
-            red[warp * 64 + 32 + lane] = make_float4(acc[1][nt][0], acc[1][nt][1], acc[1][nt][2], acc[1][nt][3]);
-            if (W > 1)
-                group_sync(1 + grp, W * 32);
-            else
-                __syncwarp();
-            if (rank == join++ % W) {
-                const int e = rt.expert[ue];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float4 s = red[grp * W * 64 + i * 32 + lane];
-                    for (int w = 1; w < W; ++w) {
-                        const float4 v = red[(grp * W + w) * 64 + i * 32 + lane];
-                        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-                    }
-                    const int col = (item - ue * per_e) * 16 + i * 8 + g;
-                    const int pos = MX ? (col & ~7) | ((col & 3) << 1) | ((col >> 2) & 1) : col;
-#pragma unroll
-                    for (int h2 = 0; h2 < 2; ++h2) {
-                        const int jt = 8 * nt + 2 * c + h2;
-                        if (jt >= ntok) continue;
-                        const int t = nth_bit(tokens, jt);
-                        float wt = 0.0f;
-                        for (int k = 0; k < a.topk; ++k)
-                            if (s_ids[t * a.topk + k] == e) wt += s_w[t * a.topk + k];
-                        const float h = wt * silu_times(h2 ? s.y : s.x, h2 ? s.w : s.z);
-                        // bf16 value and remainder; no remainder for infinities and NaN
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-                        const float rest = h - __bfloat162float(hi);
-                        const int64_t to = (int64_t)(rt.first[ue] + jt) * a.I + pos;
-                        a.h[to] = __bfloat16_as_ushort(hi);
-                        a.h[to + (int64_t)a.T * a.topk * a.I] =
-                            __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(rest) ? rest : 0.0f));
-                    }
-                }
-            }
-        }
-    }
-    cp_async_wait<0>();
-}
-
-template <bool MX, int NT>
-__global__ void __launch_bounds__(kUpThreads, 2) few_gate_up_kernel(const FewArgs a) {
-    pdl_trigger();
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int flags;
-    __shared__ __align__(16) uint8_t zeros[256];
-    if (threadIdx.x < 64) reinterpret_cast<uint32_t*>(zeros)[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) {
-        flags = check_headers<MX>(a, false);
-        if (!(flags & 1) && blockIdx.x == 0) set_error(a.err, CHORD_DEV_BAD_HEADER);
-    }
-    const int warp = threadIdx.x >> 5;
-    UpSmem sm;
-    sm.ring = smem_u32(smem) + warp * kUpDepth * 2 * kTileBytes;
-    uint8_t* red = smem + kUpWarps * kUpDepth * 2 * kTileBytes;
-    sm.red = reinterpret_cast<float4*>(red);
-    uint8_t* xs = red + 2 * kUpWarps * 64 * sizeof(float4);
-    const uint32_t x_warp = (uint32_t)a.x_cap * ((uint32_t)a.units_warp * 256u + 64u);
-    sm.x = smem_u32(xs) + warp * x_warp;
-    sm.zero = smem_u32(zeros);
-    int32_t* s_ids;
-    float* s_w;
-    const Route rt = build_route<kUpWarps>(a, xs + kUpWarps * x_warp, s_ids, s_w, a.validate && blockIdx.x == 0);
-    if (!(flags & 1)) return;
-    if (MX || (flags & 4))
-        gate_up_loop<MX, NT, true>(a, rt, s_ids, s_w, sm, (flags & 2) != 0);
-    else
-        gate_up_loop<MX, NT, false>(a, rt, s_ids, s_w, sm, (flags & 2) != 0);
-}
-
-// ---- down -------------------------------------------------------------------
-// Warps per CTA: 16, or 8 where the sums of more than 16 tokens need the registers.
-template <int NT>
-constexpr int kDownWarps = NT > 2 ? 8 : 16;
-
-template <bool MX, int NT, int RT, bool FAST>
-__device__ __forceinline__ void down_loop(const FewArgs& a, const Route& rt, uint32_t ring, int tile0, int rank, int ranks,
-                                          float (&acc)[RT][NT][4]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int KU = (a.I + 127) / 128, kgroups = a.I / 32, tiles = a.H / 16;
-    const int total = rt.used * KU;
-    const uint64_t expert_bytes = Lay<MX>::expert_bytes(a.H, a.I);
-    uint32_t co[RT], so[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        const int row = min(tile0 + i, tiles - 1) * 16 + g;   // a tile past H repeats the last one and is not written
-        co[i] = Lay<MX>::code(row, a.I, c);
-        so[i] = Lay<MX>::scale(row, a.I, c);
-    }
-    int pv = rank, p_slot = 0;
-    auto fetch = [&]() {
-        if (pv < total) {
-            const int ue = pv / KU, ku = pv - ue * KU;
-            const uint8_t* base = a.w2 + kHeaderBytes + (uint64_t)rt.expert[ue] * expert_bytes;
-            const uint8_t *cb = base + Lay<MX>::code_unit(ku, g), *sb = base + Lay<MX>::scale_unit(ku);
-            const bool on = ku * 4 + c < kgroups;
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-                fetch_tile(ring + (p_slot * RT + i) * kTileBytes, lane, cb + co[i], cb + co[i] + Lay<MX>::kRow8, sb + so[i],
-                           sb + so[i] + Lay<MX>::kScale8, on);
-            pv += ranks;
-            if (++p_slot == kDownDepth) p_slot = 0;
-        }
-        cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kDownDepth - 1; ++i) fetch();
-    pdl_wait();   // h of the gate_up kernel is complete from here on
-    const int64_t lo_plane = (int64_t)a.T * a.topk * a.I;
-    int slot = 0;
-    for (int v = rank; v < total; v += ranks) {
-        const int ue = v / KU, ku = v - ue * KU;
-        const uint32_t tokens = rt.tokens[ue];
-        const uint16_t* hp[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int t = 8 * nt + g;
-            const bool on = (tokens >> t & 1u) && ku * 4 + c < kgroups;
-            hp[nt] = on ? a.h + (int64_t)(rt.first[ue] + __popc(tokens & ((1u << t) - 1u))) * a.I + ku * 128 + c * 32 : nullptr;
-        }
-        fetch();
-        cp_async_wait<kDownDepth - 1>();
-        const uint32_t st = ring + slot * RT * kTileBytes + lane * 16;
-        if (++slot == kDownDepth) slot = 0;
-        uint4 q[RT][2];
-        Scale s[RT][2];
-        bool wide = false;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            q[i][0] = lds128(st + i * kTileBytes);
-            q[i][1] = lds128(st + i * kTileBytes + 512);
-            const uint2 w = lds64(st + i * kTileBytes + 1024 - lane * 8);
-            s[i][0] = make_scale<MX, FAST>(w.x, c);
-            s[i][1] = make_scale<MX, FAST>(w.y, c);
-            if constexpr (MX) wide |= (s[i][0].n | s[i][1].n) != 0;
-        }
-        if constexpr (MX) wide = __any_sync(0xffffffffu, wide);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint4 bh[NT], bl[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                bh[nt] = bl[nt] = make_uint4(0, 0, 0, 0);
-                if (hp[nt]) {
-                    bh[nt] = *reinterpret_cast<const uint4*>(hp[nt] + j * 8);
-                    bl[nt] = *reinterpret_cast<const uint4*>(hp[nt] + lo_plane + j * 8);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                uint32_t x0[4], x1[4];
-                dequant8<MX, FAST>(word(q[i][0], j), s[i][0], wide, x0);
-                dequant8<MX, FAST>(word(q[i][1], j), s[i][1], wide, x1);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (NT > 1 && !(tokens >> (8 * nt) & 0xffu)) continue;
-                    mma16816(acc[i][nt], x0[0], x1[0], x0[1], x1[1], bh[nt].x, bh[nt].y);
-                    mma16816(acc[i][nt], x0[2], x1[2], x0[3], x1[3], bh[nt].z, bh[nt].w);
-                    mma16816(acc[i][nt], x0[0], x1[0], x0[1], x1[1], bl[nt].x, bl[nt].y);
-                    mma16816(acc[i][nt], x0[2], x1[2], x0[3], x1[3], bl[nt].z, bl[nt].w);
-                }
-            }
-        }
-    }
-    cp_async_wait<0>();
-}
-
-__device__ __forceinline__ void few_cluster_sync() {
+__device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
 __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t cta) {
     uint32_t ra;
@@ -643,151 +297,495 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t cta) {
                  : "memory");
     return v;
 }
+// Sum over the cluster's CTAs, in rank order, of the float4 at `p` of each.
+__device__ __forceinline__ float4 cluster_sum(const float4* p, int n) {
+    float4 s = make_float4(0, 0, 0, 0);
+    for (int r = 0; r < n; ++r) {
+        const float4 v = ld_cluster(smem_u32(p), (uint32_t)r);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    return s;
+}
 
-// gridDim.x = row groups x cluster size; the CTAs of a cluster split the
-// (expert, K unit) pairs of one row group and CTA 0 joins their sums in order.
-template <bool MX, int NT, int RT>
-__global__ void __launch_bounds__(kDownWarps<NT> * 32, 1) few_down_kernel(const FewArgs a, int cluster) {
-    constexpr int kWarps = kDownWarps<NT>, kThreads = kWarps * 32;
+// The ring and what both kernels keep beside it.
+struct Ring {
+    uint64_t *full, *empty;
+    volatile int* abort_flag;
+    uint32_t base;      // stage 0
+    uint32_t zero;      // 256 bytes of zeros: what lanes without a token read
+    uint8_t* ptr;
+};
+
+struct Shared {
+    uint64_t full[16], empty[16];
+    int flags, abort_flag;
+    __align__(16) uint32_t zeros[64];
+};
+
+template <bool MX>
+__device__ __forceinline__ Ring init_shared(const FewArgs& a, Shared& sh, uint8_t* smem, bool down) {
+    if (threadIdx.x < 64) sh.zeros[threadIdx.x] = 0u;
+    if (threadIdx.x == 0) {
+        sh.flags = check_headers<MX>(a, down);
+        sh.abort_flag = 0;
+        for (int s = 0; s < a.depth; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], kConsumers);
+        }
+        fence_barrier_init();
+    }
+    return Ring{sh.full, sh.empty, &sh.abort_flag, smem_u32(smem), smem_u32(sh.zeros), smem};
+}
+
+// A lane's weight addresses inside a stage: tile i's first row at off + i * d_tile, its
+// second row d_row further on (the same for the scale words).
+struct LaneRows {
+    uint32_t off, d_row, d_tile;
+    uint32_t soff, sd_row, sd_tile;
+};
+
+// One 128-column unit of a stage: 32 rows of this warp times the tokens of NT
+// column tiles (active: bit per tile).  b(nt, j): piece j of the tokens' value
+// (and, REST, remainder) columns.
+template <bool MX, bool FAST, int NT, bool REST, typename LoadB>
+__device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32_t code_xor, uint32_t scale_add, bool on, int c,
+                                         uint32_t active, float (&acc)[2][NT][4], LoadB&& b) {
+    uint4 q[2][2];
+    Scale s[2][2];
+    bool wide = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            q[i][h] = lds128(st + ((lr.off + i * lr.d_tile + h * lr.d_row) ^ code_xor));
+            uint32_t w = lds32(st + lr.soff + i * lr.sd_tile + h * lr.sd_row + scale_add);
+            if (!MX && !on) w = 0;   // columns past K: codes left in the stage, times 0
+            s[i][h] = make_scale<MX, FAST>(w, c);
+            if constexpr (MX) wide |= s[i][h].n != 0;
+        }
+    if constexpr (MX) wide = __any_sync(0xffffffffu, wide);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t x[2][2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) dequant8<MX, FAST>(word(q[i][h], j), s[i][h], wide, x[i][h]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (NT > 1 && !(active >> nt & 1u)) continue;
+            const uint4 v = b(nt, j, false);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) mma16816(acc[i][nt], x[i][0], x[i][1], v);
+            if constexpr (REST) {
+                const uint4 r = b(nt, j, true);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) mma16816(acc[i][nt], x[i][0], x[i][1], r);
+            }
+        }
+    }
+}
+
+// After the last stage: every copy that was issued has landed.
+__device__ __forceinline__ void drain_ring(const FewArgs& a, const Ring& rg, tc5::Ring r, int issued) {
+    for (int k = 0; k < a.depth && k < issued; ++k) {
+        if (r.slot == 0) {
+            r.slot = a.depth - 1;
+            r.phase ^= 1u;
+        } else {
+            --r.slot;
+        }
+        if (!mbar_wait(&rg.full[r.slot], r.phase)) set_error(a.err, CHORD_DEV_TIMEOUT);
+    }
+}
+
+// ---- gate_up ----------------------------------------------------------------
+// h of one lane's gate and up sums (column col; tokens 2c and 2c + 1 of the pass).
+template <bool MX>
+__device__ __forceinline__ void store_h(const FewArgs& a, const Route& rt, int slot, const int32_t* s_ids, const float* s_w,
+                                        int col, int c, float4 s) {
+    if (col >= a.I) return;
+    const uint32_t tokens = rt.tokens[slot];
+    const int n = __popc(tokens), e = rt.expert[slot];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int j = 2 * c + i;
+        if (j >= n) continue;
+        const int t = nth_bit(tokens, j);
+        float wt = 0.0f;
+        for (int k = 0; k < a.topk; ++k)
+            if (s_ids[t * a.topk + k] == e) wt += s_w[t * a.topk + k];
+        const float h = wt * silu_times(i ? s.y : s.x, i ? s.w : s.z);
+        // bf16 value and remainder; no remainder for infinities and NaN
+        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+        const float rest = h - __bfloat162float(hi);
+        uint16_t* to = a.h + (int64_t)(rt.first[slot] + j) * a.Ip + h_pos<MX>(col);
+        to[0] = __bfloat16_as_ushort(hi);
+        to[(int64_t)a.T * a.topk * a.Ip] = __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(rest) ? rest : 0.0f));
+    }
+}
+
+template <bool MX>
+__device__ __forceinline__ void up_producer(const FewArgs& a, const Route& rt, const Ring& rg, bool inter, int items, int mt,
+                                            int rank, int ks0, int ks1) {
+    using S = Stage<MX>;
+    const int lane = threadIdx.x & 31;
+    tc5::Ring r;
+    int issued = 0;
+    bool ok = true;
+    for (int item = blockIdx.x / a.cluster; item < items; item += gridDim.x / a.cluster) {
+        if (lane == 0 && ok) {
+            const int slot = item / mt, m = item - slot * mt, e = rt.expert[slot];
+            const uint32_t tokens = rt.tokens[slot];
+            const int n = __popc(tokens);
+            for (int ks = ks0; ks < ks1; ++ks, ++issued, r.next(a.depth)) {
+                ok = tc5::wait(&rg.empty[r.slot], r.phase ^ 1u, rg.abort_flag, a.err);
+                if (!ok) break;
+                uint64_t* bar = &rg.full[r.slot];
+                uint8_t* st = rg.ptr + r.slot * S::kUpBytes;
+                const uint32_t xbytes = (uint32_t)min(S::kCols, a.H - ks * S::kCols) * 2u;
+                mbar_arrive_expect_tx(bar, (MX ? 16384u + 4096u : 9216u) + (uint32_t)n * xbytes);
+                if constexpr (MX) {
+                    // 32 rows at a time: gate, gate, up, up (a group of 32 never crosses a tile)
+                    const uint8_t* base = a.w13 + kHeaderBytes + (uint64_t)e * mx_group_bytes(2 * a.I, a.H);
+#pragma unroll
+                    for (int gi = 0; gi < 4; ++gi) {
+                        const int row = (gi >> 1) * a.I + m * 64 + (gi & 1) * 32;
+                        const uint8_t* t = base + ((int64_t)(row >> 7) * mx_col_tiles(a.H) + ks) * kMxTileBytes;
+                        bulk_g2s(st + gi * 4096, t + (row & 127) * 128, 4096, bar);
+                        bulk_g2s(st + S::kScale + gi * 1024, t + kMxCodeBytes, 1024, bar);
+                    }
+                } else {
+                    const uint8_t* base = a.w13 + kHeaderBytes + (uint64_t)e * ((uint64_t)(2 * a.I) * a.H * 9ull / 16ull);
+                    const int64_t band = (int64_t)(a.H / 64) * 4608;
+                    if (inter) {
+                        const uint8_t* t = base + m * band + (int64_t)ks * 9216;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            bulk_g2s(st + q * S::kBlock, t + (q >> 1) * 4608 + (q & 1) * 2048, 2048, bar);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) bulk_g2s(st + S::kScale + q * 512, t + q * 4608 + 4096, 512, bar);
+                    } else {
+#pragma unroll
+                        for (int gu = 0; gu < 2; ++gu) {
+                            const int row = gu * a.I + m * 64;   // I % 64 == 0: 64 rows of one tile
+                            const uint8_t* t = base + (row >> 7) * band + (int64_t)ks * 9216;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                bulk_g2s(st + q * S::kBlock + gu * 1024,
+                                         t + (q >> 1) * 4608 + (q & 1) * 2048 + (row & 127) * 16, 1024, bar);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+                                bulk_g2s(st + S::kScale + q * 512 + gu * 256, t + q * 4608 + 4096 + (row & 127) * 4, 256, bar);
+                        }
+                    }
+                }
+                uint8_t* xs = st + S::kUpWeights;
+                for (uint32_t mk = tokens; mk; mk &= mk - 1, xs += S::kUpRow)
+                    bulk_g2s(xs, a.x + (int64_t)(__ffs(mk) - 1) * a.H + ks * S::kCols, xbytes, bar);
+            }
+        }
+        __syncwarp();
+        if (a.cluster > 1) cluster_sync_all();
+    }
+    if (lane == 0) drain_ring(a, rg, r, issued);
+    __syncwarp();
+}
+
+template <bool MX, bool FAST>
+__device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, const Ring& rg, float4* part, bool inter,
+                                            const int32_t* s_ids, const float* s_w, int items, int mt, int rank, int ks0, int ks1) {
+    using S = Stage<MX>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, p = phys_row<MX>(g);
+    LaneRows lr;
+    if constexpr (MX) {
+        const uint32_t row = 16 * warp + p;    // of the 64 gate rows
+        lr = LaneRows{row * 128 + ((c ^ (row & 7)) << 4), 8192, 1024, 0, 2048, 128};
+    } else {
+        const uint32_t row = inter ? 32 * warp + g : 16 * warp + g;
+        lr = LaneRows{(uint32_t)c * S::kBlock + row * 16, inter ? 128u : 1024u, inter ? 256u : 128u,
+                      (uint32_t)S::kScale + (c >> 1) * 512 + row * 4, inter ? 32u : 256u, inter ? 64u : 32u};
+    }
+    tc5::Ring r;
+    bool ok = true;
+    int nitem = 0;
+    for (int item = blockIdx.x / a.cluster; item < items; item += gridDim.x / a.cluster, ++nitem) {
+        const int slot = item / mt, m = item - slot * mt, n = __popc(rt.tokens[slot]);
+        uint32_t quad[2] = {0, 0};
+        if constexpr (MX) {
+            // scale words of row R of the 64: block R / 32, word (absolute row / 32) mod 4
+            lr.soff = S::kScale + (warp >> 1) * 1024 + ((16 * warp + p) & 31) * 16;
+            quad[0] = (((uint32_t)(m * 64) >> 5) + (warp >> 1)) & 3;
+            quad[1] = (((uint32_t)(a.I + m * 64) >> 5) + (warp >> 1)) & 3;
+            lr.soff += quad[0] * 4;
+            lr.sd_row = 2048 + quad[1] * 4 - quad[0] * 4;
+        }
+        float acc[2][1][4] = {};
+        for (int ks = ks0; ks < ks1; ++ks, r.next(a.depth)) {
+            if (ok) ok = tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err);
+            if (!ok) break;
+            const uint32_t st = rg.base + r.slot * S::kUpBytes;
+            const uint32_t xs = st + S::kUpWeights + g * S::kUpRow + c * 64;
+#pragma unroll
+            for (int u = 0; u < S::kUnits; ++u) {
+                const bool on = ks * S::kCols + u * 128 + c * 32 < a.H;
+                const uint32_t xb = g < n && on ? xs + u * 256 : rg.zero;
+                unit_mma<MX, FAST, 1, false>(st, lr, u * 64, u * kMxScaleBlock, on, c, 1u, acc,
+                                             [&](int, int j, bool) { return b_order<MX>(lds128(xb + j * 16)); });
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&rg.empty[r.slot]);
+        }
+        const int col0 = m * 64 + 16 * warp + p;
+        if (a.cluster == 1) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (ok) store_h<MX>(a, rt, slot, s_ids, s_w, col0 + 8 * i, c, make_float4(acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]));
+            continue;
+        }
+        // join the cluster's K ranges: CTA `rank` takes tiles rank, rank + cluster, ... of the
+        // eight (warp, i); the buffers alternate, so one barrier an item is enough
+        float4* buf = part + (nitem & 1) * 256;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            buf[(warp * 2 + i) * 32 + lane] = make_float4(acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]);
+        __syncwarp();
+        cluster_sync_all();
+        const int tile = rank + a.cluster * warp;
+        if (ok && tile < 8)
+            store_h<MX>(a, rt, slot, s_ids, s_w, m * 64 + 8 * tile + p, c, cluster_sum(buf + tile * 32 + lane, a.cluster));
+    }
+}
+
+template <bool MX>
+__global__ void __launch_bounds__(kThreads, MX ? 3 : 4) few_gate_up_kernel(const FewArgs a) {
+    using S = Stage<MX>;
+    pdl_trigger();
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int flags;
-    if (threadIdx.x == 0) flags = check_headers<MX>(a, true);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cta = cluster > 1 ? (int)(blockIdx.x % cluster) : 0;
-    const int tile0 = (int)(blockIdx.x / cluster) * RT, tiles = a.H / 16;
-    constexpr int kRing = kDownDepth * RT * kTileBytes;
+    __shared__ Shared sh;
+    const Ring rg = init_shared<MX>(a, sh, smem, false);
+    float4* part = reinterpret_cast<float4*>(smem + a.depth * S::kUpBytes);
     int32_t* s_ids;
     float* s_w;
-    const Route rt = build_route<kWarps>(a, smem + kWarps * kRing, s_ids, s_w, false);
-    if (!(flags & 1)) return;   // the same in every CTA; the gate_up kernel reported it
-    float acc[RT][NT][4];
-#pragma unroll
-    for (int i = 0; i < RT * NT * 4; ++i) acc[i / (NT * 4)][i / 4 % NT][i % 4] = 0.0f;
-    const uint32_t ring = smem_u32(smem) + warp * kRing;
-    if (MX || (flags & 4))
-        down_loop<MX, NT, RT, true>(a, rt, ring, tile0, cta * kWarps + warp, cluster * kWarps, acc);
+    const Route rt = build_route(a, reinterpret_cast<uint8_t*>(part + (a.cluster > 1 ? 512 : 0)), s_ids, s_w,
+                                 a.validate && blockIdx.x == 0);
+    if (!(sh.flags & 1)) {   // the same in every CTA
+        if (blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, CHORD_DEV_BAD_HEADER);
+        return;
+    }
+    const int stages = (a.H + S::kCols - 1) / S::kCols, mt = (a.I + 63) / 64, items = rt.slots * mt;
+    const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
+    const int ks0 = rank * stages / a.cluster, ks1 = (rank + 1) * stages / a.cluster;
+    const bool inter = (sh.flags & 2) != 0;
+    if (threadIdx.x >= kConsumers * 32)
+        up_producer<MX>(a, rt, rg, inter, items, mt, rank, ks0, ks1);
+    else if (MX || (sh.flags & 4))
+        up_consumer<MX, true>(a, rt, rg, part, inter, s_ids, s_w, items, mt, rank, ks0, ks1);
     else
-        down_loop<MX, NT, RT, false>(a, rt, ring, tile0, cta * kWarps + warp, cluster * kWarps, acc);
-    // join the warps' sums in warp order (the rings' space is free now)
-    __syncthreads();
-    float4* red = reinterpret_cast<float4*>(smem);
-    constexpr int kPer = RT * NT * 32;
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            red[warp * kPer + (i * NT + nt) * 32 + lane] =
-                make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
-    __syncthreads();
-    if (cluster > 1) {
-        for (int q = threadIdx.x; q < kPer; q += kThreads) {
-            float4 s = red[q];
-            for (int w = 1; w < kWarps; ++w) {
-                const float4 v = red[w * kPer + q];
-                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-            }
-            red[q] = s;   // only this thread reads slot q of any warp
-        }
-        few_cluster_sync();
+        up_consumer<MX, false>(a, rt, rg, part, inter, s_ids, s_w, items, mt, rank, ks0, ks1);
+    if (a.cluster > 1) {
+        __syncwarp();
+        cluster_sync_all();   // the others have read this CTA's sums
     }
-    if (cta == 0) {
-        for (int q = threadIdx.x; q < kPer; q += kThreads) {
-            float4 s = red[q];
-            if (cluster > 1) {
-                for (int r = 1; r < cluster; ++r) {
-                    const float4 v = ld_cluster(smem_u32(red + q), r);
-                    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-                }
-            } else {
-                for (int w = 1; w < kWarps; ++w) {
-                    const float4 v = red[w * kPer + q];
-                    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-                }
-            }
-            const int l = q & 31, nt = (q >> 5) % NT, tile = tile0 + (q >> 5) / NT;
-            if (tile >= tiles) continue;
-            const int row = tile * 16 + (l >> 2), t = 8 * nt + 2 * (l & 3);
-            // + 0.0f: a sum of nothing, or of zeros of either sign, is +0
-            if (t < a.T) {
-                a.out[(int64_t)t * a.H + row] = __bfloat16_as_ushort(__float2bfloat16_rn(s.x + 0.0f));
-                a.out[(int64_t)t * a.H + row + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(s.z + 0.0f));
-            }
-            if (t + 1 < a.T) {
-                a.out[(int64_t)(t + 1) * a.H + row] = __bfloat16_as_ushort(__float2bfloat16_rn(s.y + 0.0f));
-                a.out[(int64_t)(t + 1) * a.H + row + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(s.w + 0.0f));
-            }
-        }
-    }
-    if (cluster > 1) few_cluster_sync();   // CTA 0 has read the others' sums
 }
 
+// ---- down -------------------------------------------------------------------
+template <bool MX>
+__device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt, const Ring& rg, int tile, int rank, int kst,
+                                              int total) {
+    using S = Stage<MX>;
+    if ((threadIdx.x & 31) != 0) return;
+    const int64_t plane = (int64_t)a.T * a.topk * a.Ip;
+    auto weights = [&](int v, int slot) {
+        const int sl = v / kst, ks = v - sl * kst, n = __popc(rt.tokens[sl]);
+        uint64_t* bar = &rg.full[slot];
+        uint8_t* st = rg.ptr + slot * S::kDownBytes;
+        const uint32_t hb = (uint32_t)n * S::kCols * 4u;
+        if constexpr (MX) {
+            mbar_arrive_expect_tx(bar, kMxTileBytes + hb);
+            bulk_g2s(st, a.w2 + kHeaderBytes + (uint64_t)rt.expert[sl] * mx_group_bytes(a.H, a.I) +
+                             ((int64_t)tile * mx_col_tiles(a.I) + ks) * kMxTileBytes,
+                     kMxTileBytes, bar);
+        } else {
+            const int chunks = a.I / 64 - 2 * ks >= 2 ? 2 : 1;
+            mbar_arrive_expect_tx(bar, (uint32_t)chunks * 4608u + hb);
+            const uint8_t* t = a.w2 + kHeaderBytes + (uint64_t)rt.expert[sl] * ((uint64_t)a.H * a.I * 9ull / 16ull) +
+                               (int64_t)tile * (a.I / 64) * 4608 + (int64_t)ks * 9216;
+            for (int q = 0; q < chunks; ++q) {
+                bulk_g2s(st + 2 * q * S::kBlock, t + q * 4608, 2048, bar);
+                bulk_g2s(st + (2 * q + 1) * S::kBlock, t + q * 4608 + 2048, 2048, bar);
+                bulk_g2s(st + S::kScale + q * 512, t + q * 4608 + 4096, 512, bar);
+            }
+        }
+    };
+    auto activations = [&](int v, int slot) {
+        const int sl = v / kst, ks = v - sl * kst, n = __popc(rt.tokens[sl]);
+        uint8_t* hs = rg.ptr + slot * S::kDownBytes + S::kDownWeights;
+        const uint16_t* src = a.h + (int64_t)rt.first[sl] * a.Ip + ks * S::kCols;
+        for (int k = 0; k < n; ++k, hs += S::kDownRow, src += a.Ip) {
+            bulk_g2s(hs, src, S::kCols * 2, &rg.full[slot]);
+            bulk_g2s(hs + S::kCols * 2, src + plane, S::kCols * 2, &rg.full[slot]);
+        }
+    };
+    // the first stages' weights do not depend on the gate_up kernel
+    int pre = 0;
+    for (int v = rank; v < total && pre < a.depth; v += a.cluster, ++pre) weights(v, pre);
+    pdl_wait();   // h of the gate_up kernel is complete from here on
+    tc5::Ring r;
+    int issued = 0;
+    for (int v = rank; v < total; v += a.cluster, ++issued, r.next(a.depth)) {
+        if (issued >= pre) {
+            if (!tc5::wait(&rg.empty[r.slot], r.phase ^ 1u, rg.abort_flag, a.err)) break;
+            weights(v, r.slot);
+        }
+        activations(v, r.slot);
+    }
+    drain_ring(a, rg, r, issued);
+}
+
+template <bool MX, int NT, bool FAST>
+__device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt, const Ring& rg, int rank, int kst, int total,
+                                              float (&acc)[2][NT][4]) {
+    using S = Stage<MX>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const uint32_t row = 32 * warp + phys_row<MX>(g);
+    const LaneRows lr = MX ? LaneRows{row * 128 + ((c ^ (row & 7)) << 4), 1024, 2048,
+                                      (uint32_t)S::kScale + (row & 31) * 16 + (row >> 5) * 4, 128, 256}
+                           : LaneRows{(uint32_t)c * S::kBlock + row * 16, 128, 256,
+                                      (uint32_t)S::kScale + (c >> 1) * 512 + row * 4, 32, 64};
+    tc5::Ring r;
+    for (int v = rank; v < total; v += a.cluster, r.next(a.depth)) {
+        const int sl = v / kst, ks = v - sl * kst;
+        const uint32_t tokens = rt.tokens[sl];
+        uint32_t active = 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) active |= (tokens >> (8 * nt) & 0xffu) ? 1u << nt : 0u;
+        if (!tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err)) break;
+        const uint32_t st = rg.base + r.slot * S::kDownBytes;
+        uint32_t hrow[NT];   // 0: the token is not in this pass
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int t = 8 * nt + g;
+            hrow[nt] = tokens >> t & 1u ? st + S::kDownWeights + __popc(tokens & ((1u << t) - 1u)) * S::kDownRow + c * 16 : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < S::kUnits; ++u) {
+            const bool on = ks * S::kCols + u * 128 + c * 32 < a.I;
+            unit_mma<MX, FAST, NT, true>(st, lr, u * 64, u * kMxScaleBlock, on, c, active, acc, [&](int nt, int j, bool rest) {
+                return lds128(hrow[nt] && on ? hrow[nt] + u * 256 + (rest ? S::kCols * 2 : 0) + j * 64 : rg.zero);
+            });
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rg.empty[r.slot]);
+    }
+}
+
+// gridDim.x = output tiles of 128 rows x cluster size.
 template <bool MX, int NT>
-cudaError_t launch_up(FewArgs a, cudaStream_t st) {
-    auto kern = few_gate_up_kernel<MX, NT>;
-    const int U = (a.H + 127) / 128;
-    a.warps_item = U >= 8 ? 8 : (U >= 4 ? 4 : (U >= 2 ? 2 : 1));
-    a.units_warp = (U + a.warps_item - 1) / a.warps_item;
-    // two CTAs per SM; the activations of as many of an expert's tokens as then fit
-    const size_t fixed = (size_t)kUpWarps * kUpDepth * 2 * kTileBytes + 2 * kUpWarps * 64 * sizeof(float4) +
-                         route_bytes(a.E, a.T * a.topk, a.used_cap);
-    const size_t tok = (size_t)kUpWarps * (a.units_warp * 256 + 64);
-    const int cap = (int)((kSmemHalf - fixed) / tok);
-    a.x_cap = cap < a.T ? cap : a.T;
-    const size_t smem = fixed + tok * a.x_cap;
-    int per_sm = 1;
-    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kUpThreads, smem, kSmemMax, &per_sm);
-    if (e != cudaSuccess) return e;
-    if (per_sm > 2) per_sm = 2;
-    const int64_t items = (int64_t)a.used_cap * (a.I / 16), groups = kUpWarps / a.warps_item;
-    const int64_t want = (items + groups - 1) / groups, cap_ctas = (int64_t)device_info().sm_count * per_sm;
-    kern<<<(unsigned)(want < cap_ctas ? want : cap_ctas), kUpThreads, smem, st>>>(a);
-    return cudaGetLastError();
+__global__ void __launch_bounds__(kThreads, MX || NT > 2 ? 3 : 4) few_down_kernel(const FewArgs a) {
+    using S = Stage<MX>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Shared sh;
+    const Ring rg = init_shared<MX>(a, sh, smem, true);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float4* part = reinterpret_cast<float4*>(smem + a.depth * S::kDownBytes);   // [4 warps][2][NT][32]
+    int32_t* s_ids;
+    float* s_w;
+    const Route rt = build_route(a, reinterpret_cast<uint8_t*>(part + kConsumers * 2 * NT * 32), s_ids, s_w, false);
+    if (!(sh.flags & 1)) return;   // the same in every CTA; the gate_up kernel reported it
+    const int rank = a.cluster > 1 ? (int)cluster_rank() : 0, tile = blockIdx.x / a.cluster;
+    const int kst = (a.I + S::kCols - 1) / S::kCols, total = rt.slots * kst;
+    float acc[2][NT][4];
+#pragma unroll
+    for (int i = 0; i < 2 * NT * 4; ++i) acc[i / (NT * 4)][i / 4 % NT][i % 4] = 0.0f;
+    if (warp == kConsumers)
+        down_producer<MX>(a, rt, rg, tile, rank, kst, total);
+    else if (MX || (sh.flags & 4))
+        down_consumer<MX, NT, true>(a, rt, rg, rank, kst, total, acc);
+    else
+        down_consumer<MX, NT, false>(a, rt, rg, rank, kst, total, acc);
+    __syncwarp();
+    if (warp < kConsumers) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                part[((warp * 2 + i) * NT + nt) * 32 + lane] =
+                    make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+    }
+    if (a.cluster > 1)
+        cluster_sync_all();
+    else
+        __syncthreads();
+    // CTA `rank` joins and writes tiles rank, rank + cluster, ... of the (warp, i, nt)
+    for (int q = rank + a.cluster * warp; q < kConsumers * 2 * NT && warp < kConsumers; q += a.cluster * kConsumers) {
+        const float4 s = a.cluster > 1 ? cluster_sum(part + q * 32 + lane, a.cluster) : part[q * 32 + lane];
+        const int nt = q % NT, row = tile * 128 + (q / NT) * 16 + phys_row<MX>(lane >> 2), t = 8 * nt + 2 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int tk = t + (k & 1), n = row + (k >> 1) * 8;
+            const float v = k == 0 ? s.x : k == 1 ? s.y : k == 2 ? s.z : s.w;
+            // + 0.0f: a sum of nothing, or of zeros of either sign, is +0
+            if (tk < a.T && n < a.H)
+                a.out[(int64_t)tk * a.H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v + 0.0f));
+        }
+    }
+    if (a.cluster > 1) {
+        __syncwarp();
+        cluster_sync_all();   // the others have read this CTA's sums
+    }
 }
 
-template <bool MX, int NT, int RT>
-cudaError_t launch_down(const FewArgs& a, int cluster, cudaStream_t st) {
-    auto kern = few_down_kernel<MX, NT, RT>;
-    constexpr int kWarps = kDownWarps<NT>;
-    constexpr size_t ring = (size_t)kWarps * kDownDepth * RT * kTileBytes, sums = (size_t)kWarps * RT * NT * 512;
-    const size_t smem = (ring > sums ? ring : sums) + route_bytes(a.E, a.T * a.topk, a.used_cap);
+template <typename Kern>
+cudaError_t launch_clustered(Kern kern, FewArgs a, unsigned groups, size_t smem, bool pdl, cudaStream_t st) {
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmemMax);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.H / 16 + RT - 1) / RT * cluster));
-    cfg.blockDim = dim3(kWarps * 32);
+    cfg.gridDim = dim3(groups * (unsigned)a.cluster);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (cluster > 1) {
+    if (a.cluster > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n].val.clusterDim.x = (unsigned)cluster;
+        attr[n].val.clusterDim.x = (unsigned)a.cluster;
         attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
         ++n;
     }
-    if (pdl_enabled()) {
+    if (pdl) {
         attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[n].val.programmaticStreamSerializationAllowed = 1;
         ++n;
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kern, a, cluster);
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <bool MX, int NT>
-cudaError_t launch_few_nt(const FewArgs& a, cudaStream_t st) {
-    cudaError_t e = launch_up<MX, NT>(a, st);
+cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
+    using S = Stage<MX>;
+    const int sms = device_info().sm_count, per_sm = MX ? 3 : 4;
+    const size_t route = route_bytes(a.E, a.T * a.topk, a.slot_cap);
+    // gate_up: a cluster shares an item's K range while the items then still fit the
+    // GPU at once (few items leave SMs idle and one CTA streams a long K alone)
+    const int64_t items = (int64_t)a.slot_cap * ((a.I + 63) / 64);
+    const int stages = (a.H + S::kCols - 1) / S::kCols;
+    a.cluster = 8;
+    while (a.cluster > 1 && (items * a.cluster > (int64_t)sms * per_sm || a.cluster > stages)) a.cluster >>= 1;
+    a.depth = MX ? 3 : 4;
+    size_t smem = (size_t)a.depth * S::kUpBytes + (a.cluster > 1 ? 8192 : 0) + route;
+    const int64_t resident = (int64_t)sms * per_sm / a.cluster;
+    cudaError_t e = launch_clustered(few_gate_up_kernel<MX>, a, (unsigned)(items < resident ? items : resident), smem, false, st);
     if (e != cudaSuccess) return e;
-    // Row tiles per CTA: enough that one wave of CTAs covers H.  Few tiles: clusters
-    // that split the (expert, K unit) pairs, while every warp still gets one.
-    const int tiles = a.H / 16, sms = device_info().sm_count;
-    const int rt = tiles > 2 * sms ? 3 : (tiles > sms ? 2 : 1);
-    int cluster = 1;
-    const int64_t pairs = (int64_t)a.used_cap * ((a.I + 127) / 128);
-    while (cluster < 8 && rt == 1 && tiles * cluster * 2 <= sms && cluster * 2 * kDownWarps<NT> <= pairs) cluster *= 2;
-    return rt == 3 ? launch_down<MX, NT, 3>(a, cluster, st)
-                   : (rt == 2 ? launch_down<MX, NT, 2>(a, cluster, st) : launch_down<MX, NT, 1>(a, cluster, st));
+    // down: a cluster of 8 shares an output tile's (pass, K stage) list, fewer while
+    // every CTA would not get one
+    const int64_t list = (int64_t)a.slot_cap * ((a.I + S::kCols - 1) / S::kCols);
+    a.cluster = 8;
+    while (a.cluster > 1 && a.cluster > list) a.cluster >>= 1;
+    smem = (size_t)a.depth * S::kDownBytes + (size_t)kConsumers * 2 * NT * 512 + route;
+    return launch_clustered(few_down_kernel<MX, NT>, a, (unsigned)((a.H + 127) / 128), smem, pdl_enabled(), st);
 }
 
 cudaError_t launch_few(const FewArgs& a, bool mx, cudaStream_t st) {
@@ -807,7 +805,7 @@ extern "C" {
 
 size_t chord_moe_few_workspace_bytes(int T, int topk, int E, int H, int I) {
     if (T < 0 || topk <= 0 || E <= 0 || H <= 0 || I <= 0) return 0;
-    return ((size_t)T * (size_t)topk * (size_t)I * 4 + 255) / 256 * 256;
+    return (size_t)T * (size_t)topk * (((size_t)I + 255) / 256 * 256) * 4;
 }
 
 chord_status chord_moe_layer_few(const void* x, const int32_t* topk_ids, const float* topk_w, int T, int topk, int E,
@@ -845,7 +843,10 @@ chord_status chord_moe_layer_few(const void* x, const int32_t* topk_ids, const f
     a.out = static_cast<uint16_t*>(out);
     a.err = di.err;
     a.validate = opts && opts->validate ? 1 : 0;
-    a.used_cap = T * topk < E ? T * topk : E;
+    a.Ip = (I + 255) / 256 * 256;
+    // every used expert's tokens in passes of eight
+    const int P = T * topk, many = E + P / kPassTokens;
+    a.slot_cap = P < many ? P : many;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (launch_few(a, mx, st) != cudaSuccess) return CHORD_ERR_CUDA;
     if (!opts || !opts->validate) return CHORD_OK;

@@ -586,7 +586,7 @@ chord_status chord_mxfp4_gemm(const void *Aq, size_t aq_bytes, int64_t M, const 
 #define CHORD_FEW_MAX_TOKENS 32
 
 /* Scratch bytes of chord_moe_layer_few: 4 bytes per pair and column of I (I
- * rounded up to 256). */
+ * rounded up to 256), and the down projection's partial sums. */
 size_t chord_moe_few_workspace_bytes(int T, int topk, int E, int H, int I);
 
 /* One MoE expert layer for at most CHORD_FEW_MAX_TOKENS tokens in two launches

@@ -18,10 +18,11 @@
 //     ends with a gate sum and its up sum; h is written as two bf16 numbers (value
 //     and remainder, 16 significant bits together).  Few items: a cluster of CTAs
 //     splits K and joins the sums through distributed shared memory in rank order.
-//   down: a cluster of CTAs owns 128 output rows for all experts, splits the
-//     (expert, K stage) list, and joins the FP32 sums in rank order, so neither
-//     atomics nor a combine pass are needed.  It is launched early (programmatic
-//     dependent launch) and its weights are on the way while gate_up still runs.
+//   down: several CTAs share 128 output rows for all experts: each takes a slice of
+//     the (expert, K stage) list, and the last one to finish adds the FP32 sums in
+//     slice order, so there is no combine pass and no order that changes a result.  The
+//     kernel is launched early (programmatic dependent launch) and its weights are on
+//     the way while gate_up still runs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -51,7 +52,9 @@ struct FewArgs {
     int* err;
     int validate;        // report ids outside [-1, E)
     int slot_cap;        // most passes a call can need
-    int cluster;         // CTAs that share an item (gate_up) or an output tile (down)
+    int cluster;         // CTAs that share an item (gate_up, a cluster) or an output tile (down, list slices)
+    float4* part;        // down: the slices' sums
+    int* joined;         // down: CTAs of each output tile that have left theirs
     int depth;           // stages of the ring
 };
 
@@ -64,74 +67,132 @@ struct Route {
 };
 
 __host__ __device__ __forceinline__ size_t route_bytes(int E, int P, int slot_cap) {
-    return ((size_t)E * 4 + (size_t)P * 8 + (size_t)slot_cap * 8 + 64 + 127) / 128 * 128;
+    return ((size_t)E * 4 + 128 + (size_t)P * 8 + (size_t)slot_cap * 8 + 127) / 128 * 128;
 }
 
-// Builds the passes in shared memory (all threads) and leaves the ids and
-// weights there too.
-__device__ Route build_route(const FewArgs& a, uint8_t* sm, int32_t*& s_ids, float*& s_w, bool report) {
+// What both kernels keep beside their ring of stages.
+struct Shared {
+    uint64_t full[16], empty[16];
+    int flags;        // check_headers
+    int abort_flag;
+    int slots;
+    int last;         // down: this CTA joins its tile
+    __align__(16) uint32_t zeros[64];   // what lanes without a token read
+};
+
+// Headers of both blobs, a word per lane of one warp: bit 0 they fit the call, bit 1 w13 is in
+// the gate/up-interleaved layout, bit 2 the one-FMA dequantisation fits w13, bit 3
+// it fits w2.
+template <bool MX>
+__device__ __forceinline__ int check_headers(const FewArgs& a) {
+    const int lane = threadIdx.x & 31, i = lane & 15;
+    const bool second = lane >= 16;
+    const int N = second ? a.H : 2 * a.I, K = second ? a.I : a.H;
+    const uint32_t v = i < 12 ? __ldg(reinterpret_cast<const uint32_t*>(second ? a.w2 : a.w13) + i) : 0u;
+    const uint64_t stride = MX ? (uint64_t)mx_group_bytes(N, K) : (uint64_t)N * (uint64_t)K * 9ull / 16ull;
+    uint32_t want = 0;
+    switch (i) {
+        case 0: want = kMagic; break;
+        case 1: want = 1u; break;
+        case 2: want = MX ? CHORD_LAYOUT_MXFP4 : CHORD_LAYOUT_TCGEN05; break;
+        case 3: want = kGroup; break;
+        case 4: want = (uint32_t)a.E; break;
+        case 5: want = (uint32_t)N; break;
+        case 6: want = (uint32_t)K; break;
+        case 7: want = v; break;
+        case 8: want = (uint32_t)stride; break;
+        case 9: want = (uint32_t)(stride >> 32); break;
+        case 10: want = (uint32_t)kHeaderBytes; break;
+        default: break;
+    }
+    const bool inter = !MX && lane == 2 && v == (uint32_t)CHORD_LAYOUT_GATE_UP_INTERLEAVED;
+    const bool ok = __all_sync(0xffffffffu, v == want || inter);
+    const uint32_t ones = __ballot_sync(0xffffffffu, v == 1u);
+    return (ok ? 1 : 0) | (__any_sync(0xffffffffu, inter) ? 2 : 0) | (ones >> kHdrScaleRangeWord & 1u ? 4 : 0) |
+           (ones >> (16 + kHdrScaleRangeWord) & 1u ? 8 : 0);
+}
+
+// Barriers, header check and the passes, built in shared memory by all threads;
+// the ids and weights are left there too.  Every global load is issued first.
+template <bool MX>
+__device__ Route prologue(const FewArgs& a, Shared& sh, uint8_t* sm, int32_t*& s_ids, float*& s_w, bool report) {
     const int P = a.T * a.topk, tid = threadIdx.x;
     uint32_t* mask = reinterpret_cast<uint32_t*>(sm);
-    s_ids = reinterpret_cast<int32_t*>(mask + a.E);
+    uint32_t* used = mask + a.E;             // bit e % 32 of word e / 32
+    s_ids = reinterpret_cast<int32_t*>(used + 32);
     s_w = reinterpret_cast<float*>(s_ids + P);
     uint32_t* tokens = reinterpret_cast<uint32_t*>(s_w + P);
-    uint32_t* sums = tokens + a.slot_cap;
-    uint16_t* expert = reinterpret_cast<uint16_t*>(sums + 16);
+    uint16_t* expert = reinterpret_cast<uint16_t*>(tokens + a.slot_cap);
     uint16_t* first = expert + a.slot_cap;
-    for (int e = tid; e < a.E; e += kThreads) mask[e] = 0;
+    const int32_t id0 = tid < P ? __ldg(a.ids + tid) : 0;
+    const float w0 = tid < P ? __ldg(a.wts + tid) : 0.0f;
+    if (tid >= kConsumers * 32) {
+        const int f = check_headers<MX>(a);
+        if (tid == kConsumers * 32) sh.flags = f;
+    }
+    for (int e = tid; e < a.E + 32; e += kThreads) mask[e] = 0;
+    if (tid < 64) sh.zeros[tid] = 0u;
+    if (tid == 0) {
+        sh.abort_flag = 0;
+        for (int s = 0; s < a.depth; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], kConsumers);
+        }
+        fence_barrier_init();
+    }
     __syncthreads();
     for (int p = tid; p < P; p += kThreads) {
-        const int32_t e = a.ids[p];
+        const int32_t e = p == tid ? id0 : a.ids[p];
         s_ids[p] = e;
-        s_w[p] = a.wts[p];
-        if (e >= 0 && e < a.E)
+        s_w[p] = p == tid ? w0 : a.wts[p];
+        if (e >= 0 && e < a.E) {
             atomicOr(&mask[e], 1u << (p / a.topk));
-        else if (report && e != -1)
+            atomicOr(&used[e >> 5], 1u << (e & 31));
+        } else if (report && e != -1) {
             set_error(a.err, CHORD_DEV_BAD_EXPERT);
-    }
-    __syncthreads();
-    // exclusive scan over the experts of (passes, rows of h), packed as
-    // passes << 16 | rows (both at most 1024)
-    constexpr int kPer = (1024 + kThreads - 1) / kThreads;
-    uint32_t mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i, n = e < a.E ? __popc(mask[e]) : 0;
-        mine += (uint32_t)((n + kPassTokens - 1) / kPassTokens) << 16 | (uint32_t)n;
-    }
-    uint32_t inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if ((tid & 31) >= o) inc += v;
-    }
-    if ((tid & 31) == 31) sums[tid >> 5] = inc;
-    __syncthreads();
-    uint32_t at = inc - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < (tid >> 5)) at += sums[w];
-        total += sums[w];
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = tid * kPer + i;
-        uint32_t m = e < a.E ? mask[e] : 0u;
-        while (m) {
-            uint32_t part = 0;
-            for (int k = 0; k < kPassTokens && m; ++k) {
-                part |= m & (0u - m);
-                m &= m - 1;
-            }
-            const uint32_t u = at >> 16;
-            expert[u] = (uint16_t)e;
-            tokens[u] = part;
-            first[u] = (uint16_t)at;
-            at += (1u << 16) + __popc(part);
         }
     }
     __syncthreads();
-    return Route{(int)(total >> 16), expert, tokens, first};
+    // Warp 0, lane l: the used experts among 32 l .. 32 l + 31.  An exclusive scan of
+    // (passes << 16 | rows of h), then the passes.
+    if (tid < 32) {
+        const uint32_t u = used[tid];
+        uint32_t mine = 0;
+        for (uint32_t m = u; m; m &= m - 1) {
+            const int n = __popc(mask[tid * 32 + __ffs(m) - 1]);
+            mine += (uint32_t)((n + kPassTokens - 1) / kPassTokens) << 16 | (uint32_t)n;
+        }
+        uint32_t at = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, at, o);
+            if (tid >= o) at += v;
+        }
+        if (tid == 31) sh.slots = (int)(at >> 16);
+        at -= mine;
+        for (uint32_t m = u; m; m &= m - 1) {
+            const int e = tid * 32 + __ffs(m) - 1;
+            uint32_t left = mask[e];
+            while (left) {
+                uint32_t part = left;
+                if (__popc(left) > kPassTokens) {
+                    part = 0;
+                    for (int k = 0; k < kPassTokens; ++k) {
+                        part |= left & (0u - left);
+                        left &= left - 1;
+                    }
+                } else {
+                    left = 0;
+                }
+                expert[at >> 16] = (uint16_t)e;
+                tokens[at >> 16] = part;
+                first[at >> 16] = (uint16_t)at;
+                at += (1u << 16) + __popc(part);
+            }
+        }
+    }
+    __syncthreads();
+    return Route{sh.slots, expert, tokens, first};
 }
 
 // Position of the n-th set bit of m (n below their number; mostly 0 or 1 here).
@@ -263,22 +324,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&r0)[4],
         : "r"(r0[2]), "r"(r1[2]), "r"(r0[3]), "r"(r1[3]), "r"(b.z), "r"(b.w));
 }
 
-// Headers of both blobs: bit 0 they fit the call, bit 1 w13 in the gate/up-interleaved
-// layout, bit 2 the one-FMA dequantisation fits the blob asked for.
-template <bool MX>
-__device__ __forceinline__ int check_headers(const FewArgs& a, bool down) {
-    bool inter = false, ok;
-    if constexpr (MX) {
-        ok = mx_header_ok(a.w13, a.E, 2 * a.I, a.H) && mx_header_ok(a.w2, a.E, a.H, a.I);
-    } else {
-        inter = header_ok_layout(a.w13, a.E, 2 * a.I, a.H, CHORD_LAYOUT_GATE_UP_INTERLEAVED);
-        ok = (inter || header_ok_layout(a.w13, a.E, 2 * a.I, a.H, CHORD_LAYOUT_TCGEN05)) &&
-             header_ok_layout(a.w2, a.E, a.H, a.I, CHORD_LAYOUT_TCGEN05);
-    }
-    const bool fast = !MX && ok && header_scales_in_fma_range(down ? a.w2 : a.w13);
-    return (ok ? 1 : 0) | (inter ? 2 : 0) | (fast ? 4 : 0);
-}
-
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -307,35 +352,12 @@ __device__ __forceinline__ float4 cluster_sum(const float4* p, int n) {
     return s;
 }
 
-// The ring and what both kernels keep beside it.
 struct Ring {
     uint64_t *full, *empty;
     volatile int* abort_flag;
-    uint32_t base;      // stage 0
-    uint32_t zero;      // 256 bytes of zeros: what lanes without a token read
+    uint32_t base, zero;      // stage 0, the zeros
     uint8_t* ptr;
 };
-
-struct Shared {
-    uint64_t full[16], empty[16];
-    int flags, abort_flag;
-    __align__(16) uint32_t zeros[64];
-};
-
-template <bool MX>
-__device__ __forceinline__ Ring init_shared(const FewArgs& a, Shared& sh, uint8_t* smem, bool down) {
-    if (threadIdx.x < 64) sh.zeros[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) {
-        sh.flags = check_headers<MX>(a, down);
-        sh.abort_flag = 0;
-        for (int s = 0; s < a.depth; ++s) {
-            mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], kConsumers);
-        }
-        fence_barrier_init();
-    }
-    return Ring{sh.full, sh.empty, &sh.abort_flag, smem_u32(smem), smem_u32(sh.zeros), smem};
-}
 
 // A lane's weight addresses inside a stage: tile i's first row at off + i * d_tile, its
 // second row d_row further on (the same for the scale words).
@@ -563,12 +585,14 @@ __global__ void __launch_bounds__(kThreads, MX ? 3 : 4) few_gate_up_kernel(const
     pdl_trigger();
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
-    const Ring rg = init_shared<MX>(a, sh, smem, false);
+    const Ring rg{sh.full, sh.empty, &sh.abort_flag, smem_u32(smem), smem_u32(sh.zeros), smem};
     float4* part = reinterpret_cast<float4*>(smem + a.depth * S::kUpBytes);
     int32_t* s_ids;
     float* s_w;
-    const Route rt = build_route(a, reinterpret_cast<uint8_t*>(part + (a.cluster > 1 ? 512 : 0)), s_ids, s_w,
-                                 a.validate && blockIdx.x == 0);
+    const Route rt = prologue<MX>(a, sh, reinterpret_cast<uint8_t*>(part + (a.cluster > 1 ? 512 : 0)), s_ids, s_w,
+                                  a.validate && blockIdx.x == 0);
+    if (blockIdx.x == 0)   // for the down kernel
+        for (int i = threadIdx.x; i < (a.H + 127) / 128; i += kThreads) a.joined[i] = 0;
     if (!(sh.flags & 1)) {   // the same in every CTA
         if (blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, CHORD_DEV_BAD_HEADER);
         return;
@@ -680,64 +704,88 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
     }
 }
 
-// gridDim.x = output tiles of 128 rows x cluster size.
+// gridDim.x = output tiles of 128 rows x a.cluster list slices (slice fastest).  Each
+// CTA leaves its FP32 sums in the workspace and the tile's last one adds the
+// slices, always in slice order, so the result does not depend on which is last.
 template <bool MX, int NT>
 __global__ void __launch_bounds__(kThreads, MX || NT > 2 ? 3 : 4) few_down_kernel(const FewArgs a) {
     using S = Stage<MX>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
-    const Ring rg = init_shared<MX>(a, sh, smem, true);
+    const Ring rg{sh.full, sh.empty, &sh.abort_flag, smem_u32(smem), smem_u32(sh.zeros), smem};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float4* part = reinterpret_cast<float4*>(smem + a.depth * S::kDownBytes);   // [4 warps][2][NT][32]
     int32_t* s_ids;
     float* s_w;
-    const Route rt = build_route(a, reinterpret_cast<uint8_t*>(part + kConsumers * 2 * NT * 32), s_ids, s_w, false);
+    const Route rt = prologue<MX>(a, sh, smem + a.depth * S::kDownBytes, s_ids, s_w, false);
     if (!(sh.flags & 1)) return;   // the same in every CTA; the gate_up kernel reported it
-    const int rank = a.cluster > 1 ? (int)cluster_rank() : 0, tile = blockIdx.x / a.cluster;
+    const int rank = blockIdx.x % a.cluster, tile = blockIdx.x / a.cluster;
     const int kst = (a.I + S::kCols - 1) / S::kCols, total = rt.slots * kst;
     float acc[2][NT][4];
 #pragma unroll
     for (int i = 0; i < 2 * NT * 4; ++i) acc[i / (NT * 4)][i / 4 % NT][i % 4] = 0.0f;
     if (warp == kConsumers)
         down_producer<MX>(a, rt, rg, tile, rank, kst, total);
-    else if (MX || (sh.flags & 4))
+    else if (MX || (sh.flags & 8))
         down_consumer<MX, NT, true>(a, rt, rg, rank, kst, total, acc);
     else
         down_consumer<MX, NT, false>(a, rt, rg, rank, kst, total, acc);
     __syncwarp();
-    if (warp < kConsumers) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                part[((warp * 2 + i) * NT + nt) * 32 + lane] =
-                    make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
-    }
-    if (a.cluster > 1)
-        cluster_sync_all();
-    else
-        __syncthreads();
-    // CTA `rank` joins and writes tiles rank, rank + cluster, ... of the (warp, i, nt)
-    for (int q = rank + a.cluster * warp; q < kConsumers * 2 * NT && warp < kConsumers; q += a.cluster * kConsumers) {
-        const float4 s = a.cluster > 1 ? cluster_sum(part + q * 32 + lane, a.cluster) : part[q * 32 + lane];
-        const int nt = q % NT, row = tile * 128 + (q / NT) * 16 + phys_row<MX>(lane >> 2), t = 8 * nt + 2 * (lane & 3);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int tk = t + (k & 1), n = row + (k >> 1) * 8;
-            const float v = k == 0 ? s.x : k == 1 ? s.y : k == 2 ? s.z : s.w;
-            // + 0.0f: a sum of nothing, or of zeros of either sign, is +0
-            if (tk < a.T && n < a.H)
-                a.out[(int64_t)tk * a.H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v + 0.0f));
-        }
-    }
+    constexpr int kPer = kConsumers * 2 * NT * 32;   // float4 of a CTA: [warp][i][nt][lane]
+    float4* mine = a.part + (int64_t)blockIdx.x * kPer;
     if (a.cluster > 1) {
-        __syncwarp();
-        cluster_sync_all();   // the others have read this CTA's sums
+        pdl_wait();   // (threads that read nothing of the gate_up kernel) its zeroed counters and the workspace
+        if (warp < kConsumers) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mine[((warp * 2 + i) * NT + nt) * 32 + lane] =
+                        make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+        }
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) sh.last = atomicAdd(a.joined + tile, 1) == a.cluster - 1;
+        __syncthreads();
+        if (!sh.last) return;
+        __threadfence();
     }
+    if (warp == kConsumers) return;
+    const float4* from = a.part + (int64_t)tile * a.cluster * kPer;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float4 s = make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+            if (a.cluster > 1) {
+                s = make_float4(0, 0, 0, 0);
+                for (int r = 0; r < a.cluster; ++r) {
+                    const float4 v = __ldcg(from + (int64_t)r * kPer + ((warp * 2 + i) * NT + nt) * 32 + lane);
+                    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+                }
+            }
+            const int row = tile * 128 + (warp * 2 + i) * 16 + phys_row<MX>(lane >> 2), t = 8 * nt + 2 * (lane & 3);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int tk = t + (k & 1), n = row + (k >> 1) * 8;
+                const float v = k == 0 ? s.x : k == 1 ? s.y : k == 2 ? s.z : s.w;
+                // + 0.0f: a sum of nothing, or of zeros of either sign, is +0
+                if (tk < a.T && n < a.H)
+                    a.out[(int64_t)tk * a.H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v + 0.0f));
+            }
+        }
+}
+
+// List slices per output tile of the down kernel: three CTAs per SM of a GB300 (152
+// SMs; host arithmetic, the workspace depends on it), at most 16, one for every list entry.
+int down_slices(int H, int64_t list) {
+    const int tiles = (H + 127) / 128;
+    int n = 152 * 3 / tiles;
+    n = n > 16 ? 16 : (n < 1 ? 1 : n);
+    return list < n ? (int)(list < 1 ? 1 : list) : n;
 }
 
 template <typename Kern>
-cudaError_t launch_clustered(Kern kern, FewArgs a, unsigned groups, size_t smem, bool pdl, cudaStream_t st) {
+cudaError_t launch(Kern kern, const FewArgs& a, unsigned groups, size_t smem, bool cluster, bool pdl, cudaStream_t st) {
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmemMax);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -747,7 +795,7 @@ cudaError_t launch_clustered(Kern kern, FewArgs a, unsigned groups, size_t smem,
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (a.cluster > 1) {
+    if (cluster && a.cluster > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
         attr[n].val.clusterDim.x = (unsigned)a.cluster;
         attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
@@ -777,21 +825,34 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     a.depth = MX ? 3 : 4;
     size_t smem = (size_t)a.depth * S::kUpBytes + (a.cluster > 1 ? 8192 : 0) + route;
     const int64_t resident = (int64_t)sms * per_sm / a.cluster;
-    cudaError_t e = launch_clustered(few_gate_up_kernel<MX>, a, (unsigned)(items < resident ? items : resident), smem, false, st);
+    cudaError_t e = launch(few_gate_up_kernel<MX>, a, (unsigned)(items < resident ? items : resident), smem, true, false, st);
     if (e != cudaSuccess) return e;
-    // down: a cluster of 8 shares an output tile's (pass, K stage) list, fewer while
-    // every CTA would not get one
+    // down: the (pass, K stage) list of an output tile in slices, as many as fill the GPU
+    // once at three CTAs per SM
     const int64_t list = (int64_t)a.slot_cap * ((a.I + S::kCols - 1) / S::kCols);
-    a.cluster = 8;
-    while (a.cluster > 1 && a.cluster > list) a.cluster >>= 1;
-    smem = (size_t)a.depth * S::kDownBytes + (size_t)kConsumers * 2 * NT * 512 + route;
-    return launch_clustered(few_down_kernel<MX, NT>, a, (unsigned)((a.H + 127) / 128), smem, pdl_enabled(), st);
+    const int tiles = (a.H + 127) / 128;
+    a.cluster = down_slices(a.H, list);
+    smem = (size_t)a.depth * S::kDownBytes + route;
+    return launch(few_down_kernel<MX, NT>, a, (unsigned)tiles, smem, false, pdl_enabled(), st);
 }
 
 cudaError_t launch_few(const FewArgs& a, bool mx, cudaStream_t st) {
     if (a.T <= 8) return mx ? launch_few_nt<true, 1>(a, st) : launch_few_nt<false, 1>(a, st);
     if (a.T <= 16) return mx ? launch_few_nt<true, 2>(a, st) : launch_few_nt<false, 2>(a, st);
     return mx ? launch_few_nt<true, 4>(a, st) : launch_few_nt<false, 4>(a, st);
+}
+
+// Workspace: h (value and remainder), the down kernel's slices and its counters.
+struct FewWs {
+    size_t part, joined, total;
+};
+FewWs few_ws(int T, int topk, int H, int I) {
+    FewWs w;
+    w.part = (size_t)T * (size_t)topk * (((size_t)I + 255) / 256 * 256) * 4;
+    const size_t tiles = ((size_t)H + 127) / 128, nt = T <= 8 ? 1 : (T <= 16 ? 2 : 4);
+    w.joined = w.part + tiles * (size_t)down_slices(H, INT32_MAX) * kConsumers * 2 * nt * 512;
+    w.total = w.joined + (tiles * 4 + 255) / 256 * 256;
+    return w;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -805,7 +866,7 @@ extern "C" {
 
 size_t chord_moe_few_workspace_bytes(int T, int topk, int E, int H, int I) {
     if (T < 0 || topk <= 0 || E <= 0 || H <= 0 || I <= 0) return 0;
-    return (size_t)T * (size_t)topk * (((size_t)I + 255) / 256 * 256) * 4;
+    return few_ws(T, topk, H, I).total;
 }
 
 chord_status chord_moe_layer_few(const void* x, const int32_t* topk_ids, const float* topk_w, int T, int topk, int E,
@@ -844,6 +905,9 @@ chord_status chord_moe_layer_few(const void* x, const int32_t* topk_ids, const f
     a.err = di.err;
     a.validate = opts && opts->validate ? 1 : 0;
     a.Ip = (I + 255) / 256 * 256;
+    const FewWs ws = few_ws(T, topk, H, I);
+    a.part = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + ws.part);
+    a.joined = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + ws.joined);
     // every used expert's tokens in passes of eight
     const int P = T * topk, many = E + P / kPassTokens;
     a.slot_cap = P < many ? P : many;

@@ -56,6 +56,7 @@ struct FewArgs {
     float4* part;        // down: the slices' sums
     int* joined;         // down: CTAs of each output tile that have left theirs
     int depth;           // stages of the ring
+    int stage_bytes;
 };
 
 // ---- passes: which experts are used, by which tokens -----------------------
@@ -135,7 +136,7 @@ __device__ Route prologue(const FewArgs& a, Shared& sh, uint8_t* sm, int32_t*& s
     if (tid == 0) {
         sh.abort_flag = 0;
         for (int s = 0; s < a.depth; ++s) {
-            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.full[s], 1 + 32);   // the bulk copies' bytes, and every producer lane's own copies
             mbar_init(&sh.empty[s], kConsumers);
         }
         fence_barrier_init();
@@ -217,9 +218,9 @@ struct Stage {
     static constexpr int kDownWeights = kScale + 1024;
     static constexpr int kUpRow = kCols * 2 + 16;             // activations of a token, gate_up
     static constexpr int kDownRow = kCols * 4 + 64;           // value and remainder, down
-    static constexpr int kUpBytes = kUpWeights + kPassTokens * kUpRow;
-    static constexpr int kDownBytes = kDownWeights + kPassTokens * kDownRow;
-    static_assert(kUpBytes % 128 == 0 && kDownBytes % 128 == 0, "stages stay 128-byte aligned");
+    // a stage with room for the activations of `tokens`, 128-byte aligned
+    static __host__ __device__ int up_bytes(int tokens) { return (kUpWeights + tokens * kUpRow + 127) / 128 * 128; }
+    static __host__ __device__ int down_bytes(int tokens) { return (kDownWeights + tokens * kDownRow + 127) / 128 * 128; }
 };
 
 // MXFP4 rows are 128 bytes apart and swizzled by row mod 8: with MMA row g taken
@@ -447,28 +448,31 @@ __device__ __forceinline__ void store_h(const FewArgs& a, const Route& rt, int s
     }
 }
 
+// The weights' code blocks go through cp.async.bulk, issued by lane 0; what comes in
+// short pieces (scale words, activation rows) through 16-byte cp.async of all
+// lanes: bulk copies of a few hundred bytes hold up the ones behind them.
 template <bool MX>
 __device__ __forceinline__ void up_producer(const FewArgs& a, const Route& rt, const Ring& rg, bool inter, int items, int mt,
-                                            int rank, int ks0, int ks1) {
+                                            int ks0, int ks1) {
     using S = Stage<MX>;
     const int lane = threadIdx.x & 31;
+    constexpr int kPieces = S::kCols / 8;   // 16-byte pieces of an activation row
     tc5::Ring r;
     int issued = 0;
     bool ok = true;
     for (int item = blockIdx.x / a.cluster; item < items; item += gridDim.x / a.cluster) {
-        if (lane == 0 && ok) {
-            const int slot = item / mt, m = item - slot * mt, e = rt.expert[slot];
-            const uint32_t tokens = rt.tokens[slot];
-            const int n = __popc(tokens);
-            for (int ks = ks0; ks < ks1; ++ks, ++issued, r.next(a.depth)) {
-                ok = tc5::wait(&rg.empty[r.slot], r.phase ^ 1u, rg.abort_flag, a.err);
-                if (!ok) break;
-                uint64_t* bar = &rg.full[r.slot];
-                uint8_t* st = rg.ptr + r.slot * S::kUpBytes;
-                const uint32_t xbytes = (uint32_t)min(S::kCols, a.H - ks * S::kCols) * 2u;
-                mbar_arrive_expect_tx(bar, (MX ? 16384u + 4096u : 9216u) + (uint32_t)n * xbytes);
-                if constexpr (MX) {
-                    // 32 rows at a time: gate, gate, up, up (a group of 32 never crosses a tile)
+        const int slot = item / mt, m = item - slot * mt, e = rt.expert[slot];
+        const uint32_t tokens = rt.tokens[slot];
+        const int n = __popc(tokens);
+        for (int ks = ks0; ks < ks1 && ok; ++ks) {
+            ok = tc5::wait(&rg.empty[r.slot], r.phase ^ 1u, rg.abort_flag, a.err);
+            if (!ok) break;
+            uint64_t* bar = &rg.full[r.slot];
+            uint8_t* st = rg.ptr + r.slot * a.stage_bytes;
+            if constexpr (MX) {
+                // 32 rows at a time: gate, gate, up, up (a group of 32 never crosses a tile)
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, 16384u + 4096u);
                     const uint8_t* base = a.w13 + kHeaderBytes + (uint64_t)e * mx_group_bytes(2 * a.I, a.H);
 #pragma unroll
                     for (int gi = 0; gi < 4; ++gi) {
@@ -477,40 +481,52 @@ __device__ __forceinline__ void up_producer(const FewArgs& a, const Route& rt, c
                         bulk_g2s(st + gi * 4096, t + (row & 127) * 128, 4096, bar);
                         bulk_g2s(st + S::kScale + gi * 1024, t + kMxCodeBytes, 1024, bar);
                     }
-                } else {
-                    const uint8_t* base = a.w13 + kHeaderBytes + (uint64_t)e * ((uint64_t)(2 * a.I) * a.H * 9ull / 16ull);
-                    const int64_t band = (int64_t)(a.H / 64) * 4608;
+                }
+            } else {
+                const uint8_t* base = a.w13 + kHeaderBytes + (uint64_t)e * ((uint64_t)(2 * a.I) * a.H * 9ull / 16ull) +
+                                      (int64_t)ks * 9216;
+                const int64_t band = (int64_t)(a.H / 64) * 4608;
+                // rows of this lane's scale pieces and of the code blocks: all of a tile's, or 64 gate and 64 up
+                const int up = lane >> 4;
+                const int row = inter ? m * 128 : (up ? a.I : 0) + m * 64;   // I % 64 == 0: 64 rows of one tile
+                const uint8_t* ts = base + (row >> 7) * band + 4096 + (inter ? lane * 16 : (row & 127) * 4 + (lane & 15) * 16);
+                const uint32_t ds = smem_u32(st + S::kScale) + lane * 16;
+                cp_async16(ds, ts);
+                cp_async16(ds + 512, ts + 4608);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, 8192u);
                     if (inter) {
-                        const uint8_t* t = base + m * band + (int64_t)ks * 9216;
+                        const uint8_t* t = base + m * band;
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             bulk_g2s(st + q * S::kBlock, t + (q >> 1) * 4608 + (q & 1) * 2048, 2048, bar);
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) bulk_g2s(st + S::kScale + q * 512, t + q * 4608 + 4096, 512, bar);
                     } else {
 #pragma unroll
                         for (int gu = 0; gu < 2; ++gu) {
-                            const int row = gu * a.I + m * 64;   // I % 64 == 0: 64 rows of one tile
-                            const uint8_t* t = base + (row >> 7) * band + (int64_t)ks * 9216;
+                            const int rw = gu * a.I + m * 64;
+                            const uint8_t* t = base + (rw >> 7) * band + (rw & 127) * 16;
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                bulk_g2s(st + q * S::kBlock + gu * 1024,
-                                         t + (q >> 1) * 4608 + (q & 1) * 2048 + (row & 127) * 16, 1024, bar);
-#pragma unroll
-                            for (int q = 0; q < 2; ++q)
-                                bulk_g2s(st + S::kScale + q * 512 + gu * 256, t + q * 4608 + 4096 + (row & 127) * 4, 256, bar);
+                                bulk_g2s(st + q * S::kBlock + gu * 1024, t + (q >> 1) * 4608 + (q & 1) * 2048, 1024, bar);
                         }
                     }
                 }
-                uint8_t* xs = st + S::kUpWeights;
-                for (uint32_t mk = tokens; mk; mk &= mk - 1, xs += S::kUpRow)
-                    bulk_g2s(xs, a.x + (int64_t)(__ffs(mk) - 1) * a.H + ks * S::kCols, xbytes, bar);
             }
+            __syncwarp();
+            const uint32_t xs = smem_u32(st + S::kUpWeights);
+            for (int q = lane; q < n * kPieces; q += 32) {
+                const int j = q / kPieces, pc = q % kPieces, k = ks * S::kCols + pc * 8;
+                if (k < a.H) cp_async16(xs + j * S::kUpRow + pc * 16, a.x + (int64_t)nth_bit(tokens, j) * a.H + k);
+            }
+            cp_async_arrive_noinc(bar);
+            ++issued;
+            r.next(a.depth);
         }
         __syncwarp();
         if (a.cluster > 1) cluster_sync_all();
     }
-    if (lane == 0) drain_ring(a, rg, r, issued);
+    cp_async_wait<0>();
+    drain_ring(a, rg, r, issued);
     __syncwarp();
 }
 
@@ -546,7 +562,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
         for (int ks = ks0; ks < ks1; ++ks, r.next(a.depth)) {
             if (ok) ok = tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err);
             if (!ok) break;
-            const uint32_t st = rg.base + r.slot * S::kUpBytes;
+            const uint32_t st = rg.base + r.slot * a.stage_bytes;
             const uint32_t xs = st + S::kUpWeights + g * S::kUpRow + c * 64;
 #pragma unroll
             for (int u = 0; u < S::kUnits; ++u) {
@@ -580,13 +596,13 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
 }
 
 template <bool MX>
-__global__ void __launch_bounds__(kThreads, MX ? 3 : 4) few_gate_up_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) few_gate_up_kernel(const FewArgs a) {
     using S = Stage<MX>;
     pdl_trigger();
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
     const Ring rg{sh.full, sh.empty, &sh.abort_flag, smem_u32(smem), smem_u32(sh.zeros), smem};
-    float4* part = reinterpret_cast<float4*>(smem + a.depth * S::kUpBytes);
+    float4* part = reinterpret_cast<float4*>(smem + a.depth * a.stage_bytes);
     int32_t* s_ids;
     float* s_w;
     const Route rt = prologue<MX>(a, sh, reinterpret_cast<uint8_t*>(part + (a.cluster > 1 ? 512 : 0)), s_ids, s_w,
@@ -602,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, MX ? 3 : 4) few_gate_up_kernel(const
     const int ks0 = rank * stages / a.cluster, ks1 = (rank + 1) * stages / a.cluster;
     const bool inter = (sh.flags & 2) != 0;
     if (threadIdx.x >= kConsumers * 32)
-        up_producer<MX>(a, rt, rg, inter, items, mt, rank, ks0, ks1);
+        up_producer<MX>(a, rt, rg, inter, items, mt, ks0, ks1);
     else if (MX || (sh.flags & 4))
         up_consumer<MX, true>(a, rt, rg, part, inter, s_ids, s_w, items, mt, rank, ks0, ks1);
     else
@@ -618,38 +634,45 @@ template <bool MX>
 __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt, const Ring& rg, int tile, int rank, int kst,
                                               int total) {
     using S = Stage<MX>;
-    if ((threadIdx.x & 31) != 0) return;
+    const int lane = threadIdx.x & 31;
     const int64_t plane = (int64_t)a.T * a.topk * a.Ip;
     auto weights = [&](int v, int slot) {
-        const int sl = v / kst, ks = v - sl * kst, n = __popc(rt.tokens[sl]);
+        const int sl = v / kst, ks = v - sl * kst;
         uint64_t* bar = &rg.full[slot];
-        uint8_t* st = rg.ptr + slot * S::kDownBytes;
-        const uint32_t hb = (uint32_t)n * S::kCols * 4u;
+        uint8_t* st = rg.ptr + slot * a.stage_bytes;
         if constexpr (MX) {
-            mbar_arrive_expect_tx(bar, kMxTileBytes + hb);
-            bulk_g2s(st, a.w2 + kHeaderBytes + (uint64_t)rt.expert[sl] * mx_group_bytes(a.H, a.I) +
-                             ((int64_t)tile * mx_col_tiles(a.I) + ks) * kMxTileBytes,
-                     kMxTileBytes, bar);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, kMxTileBytes);
+                bulk_g2s(st, a.w2 + kHeaderBytes + (uint64_t)rt.expert[sl] * mx_group_bytes(a.H, a.I) +
+                                 ((int64_t)tile * mx_col_tiles(a.I) + ks) * kMxTileBytes,
+                         kMxTileBytes, bar);
+            }
         } else {
             const int chunks = a.I / 64 - 2 * ks >= 2 ? 2 : 1;
-            mbar_arrive_expect_tx(bar, (uint32_t)chunks * 4608u + hb);
             const uint8_t* t = a.w2 + kHeaderBytes + (uint64_t)rt.expert[sl] * ((uint64_t)a.H * a.I * 9ull / 16ull) +
                                (int64_t)tile * (a.I / 64) * 4608 + (int64_t)ks * 9216;
-            for (int q = 0; q < chunks; ++q) {
-                bulk_g2s(st + 2 * q * S::kBlock, t + q * 4608, 2048, bar);
-                bulk_g2s(st + (2 * q + 1) * S::kBlock, t + q * 4608 + 2048, 2048, bar);
-                bulk_g2s(st + S::kScale + q * 512, t + q * 4608 + 4096, 512, bar);
+            const uint32_t ds = smem_u32(st + S::kScale) + lane * 16;
+            cp_async16(ds, t + 4096 + lane * 16);
+            if (chunks == 2) cp_async16(ds + 512, t + 4608 + 4096 + lane * 16);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, (uint32_t)chunks * 4096u);
+                for (int q = 0; q < 2 * chunks; ++q)
+                    bulk_g2s(st + q * S::kBlock, t + (q >> 1) * 4608 + (q & 1) * 2048, 2048, bar);
             }
         }
+        __syncwarp();
     };
     auto activations = [&](int v, int slot) {
+        constexpr int kPieces = S::kCols / 8;   // of the value row, then as many of the remainder row
         const int sl = v / kst, ks = v - sl * kst, n = __popc(rt.tokens[sl]);
-        uint8_t* hs = rg.ptr + slot * S::kDownBytes + S::kDownWeights;
+        const uint32_t hs = smem_u32(rg.ptr + slot * a.stage_bytes + S::kDownWeights);
         const uint16_t* src = a.h + (int64_t)rt.first[sl] * a.Ip + ks * S::kCols;
-        for (int k = 0; k < n; ++k, hs += S::kDownRow, src += a.Ip) {
-            bulk_g2s(hs, src, S::kCols * 2, &rg.full[slot]);
-            bulk_g2s(hs + S::kCols * 2, src + plane, S::kCols * 2, &rg.full[slot]);
+        for (int q = lane; q < n * 2 * kPieces; q += 32) {
+            const int j = q / (2 * kPieces), pc = q % (2 * kPieces);
+            cp_async16(hs + j * S::kDownRow + pc * 16,
+                       src + (int64_t)j * a.Ip + (pc < kPieces ? pc * 8 : plane + (pc - kPieces) * 8));
         }
+        cp_async_arrive_noinc(&rg.full[slot]);
     };
     // the first stages' weights do not depend on the gate_up kernel
     int pre = 0;
@@ -664,6 +687,7 @@ __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt,
         }
         activations(v, r.slot);
     }
+    cp_async_wait<0>();
     drain_ring(a, rg, r, issued);
 }
 
@@ -685,7 +709,7 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) active |= (tokens >> (8 * nt) & 0xffu) ? 1u << nt : 0u;
         if (!tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err)) break;
-        const uint32_t st = rg.base + r.slot * S::kDownBytes;
+        const uint32_t st = rg.base + r.slot * a.stage_bytes;
         uint32_t hrow[NT];   // 0: the token is not in this pass
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -708,7 +732,7 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
 // CTA leaves its FP32 sums in the workspace and the tile's last one adds the
 // slices, always in slice order, so the result does not depend on which is last.
 template <bool MX, int NT>
-__global__ void __launch_bounds__(kThreads, MX || NT > 2 ? 3 : 4) few_down_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) few_down_kernel(const FewArgs a) {
     using S = Stage<MX>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
@@ -716,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, MX || NT > 2 ? 3 : 4) few_down_kerne
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t* s_ids;
     float* s_w;
-    const Route rt = prologue<MX>(a, sh, smem + a.depth * S::kDownBytes, s_ids, s_w, false);
+    const Route rt = prologue<MX>(a, sh, smem + a.depth * a.stage_bytes, s_ids, s_w, false);
     if (!(sh.flags & 1)) return;   // the same in every CTA; the gate_up kernel reported it
     const int rank = blockIdx.x % a.cluster, tile = blockIdx.x / a.cluster;
     const int kst = (a.I + S::kCols - 1) / S::kCols, total = rt.slots * kst;
@@ -814,7 +838,7 @@ cudaError_t launch(Kern kern, const FewArgs& a, unsigned groups, size_t smem, bo
 template <bool MX, int NT>
 cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     using S = Stage<MX>;
-    const int sms = device_info().sm_count, per_sm = MX ? 3 : 4;
+    const int sms = device_info().sm_count, per_sm = 3;
     const size_t route = route_bytes(a.E, a.T * a.topk, a.slot_cap);
     // gate_up: a cluster shares an item's K range while the items then still fit the
     // GPU at once (few items leave SMs idle and one CTA streams a long K alone)
@@ -822,8 +846,13 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     const int stages = (a.H + S::kCols - 1) / S::kCols;
     a.cluster = 8;
     while (a.cluster > 1 && (items * a.cluster > (int64_t)sms * per_sm || a.cluster > stages)) a.cluster >>= 1;
-    a.depth = MX ? 3 : 4;
-    size_t smem = (size_t)a.depth * S::kUpBytes + (a.cluster > 1 ? 8192 : 0) + route;
+    // three CTAs per SM, as many stages as then fit
+    const size_t third = 74 * 1024, beside = route + (a.cluster > 1 ? 8192 : 0);
+    const int tokens = a.T < kPassTokens ? a.T : kPassTokens;
+    a.stage_bytes = S::up_bytes(tokens);
+    a.depth = (int)((third - beside) / a.stage_bytes);
+    a.depth = a.depth > 16 ? 16 : (a.depth < 2 ? 2 : a.depth);
+    size_t smem = (size_t)a.depth * a.stage_bytes + beside;
     const int64_t resident = (int64_t)sms * per_sm / a.cluster;
     cudaError_t e = launch(few_gate_up_kernel<MX>, a, (unsigned)(items < resident ? items : resident), smem, true, false, st);
     if (e != cudaSuccess) return e;
@@ -832,7 +861,10 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     const int64_t list = (int64_t)a.slot_cap * ((a.I + S::kCols - 1) / S::kCols);
     const int tiles = (a.H + 127) / 128;
     a.cluster = down_slices(a.H, list);
-    smem = (size_t)a.depth * S::kDownBytes + route;
+    a.stage_bytes = S::down_bytes(tokens);
+    a.depth = (int)((third - route) / a.stage_bytes);
+    a.depth = a.depth > 16 ? 16 : (a.depth < 2 ? 2 : a.depth);
+    smem = (size_t)a.depth * a.stage_bytes + route;
     return launch(few_down_kernel<MX, NT>, a, (unsigned)tiles, smem, false, pdl_enabled(), st);
 }
 

@@ -37,7 +37,8 @@ namespace {
 constexpr int kConsumers = 4;                      // warps, 32 weight rows each
 constexpr int kThreads = (kConsumers + 1) * 32;    // and the producer warp
 constexpr int kPassTokens = 8;                     // tokens of one pass over an expert (MMA N)
-constexpr size_t kSmemMax = 226 * 1024;            // dynamic; the kernels hold a few static bytes too
+constexpr int kZeroBytes = 1024;                   // covers a token's row of a stage
+constexpr size_t kSmemMax = 96 * 1024;             // dynamic; a ring never takes more than a third of an SM
 
 struct FewArgs {
     const uint16_t* x;
@@ -68,7 +69,7 @@ struct Route {
 };
 
 __host__ __device__ __forceinline__ size_t route_bytes(int E, int P, int slot_cap) {
-    return ((size_t)E * 4 + 128 + (size_t)P * 8 + (size_t)slot_cap * 8 + 127) / 128 * 128;
+    return ((size_t)E * 4 + (size_t)P * 8 + (size_t)slot_cap * 8 + 127) / 128 * 128;
 }
 
 // What both kernels keep beside their ring of stages.
@@ -78,7 +79,8 @@ struct Shared {
     int abort_flag;
     int slots;
     int last;         // down: this CTA joins its tile
-    __align__(16) uint32_t zeros[64];   // what lanes without a token read
+    uint32_t sums[kThreads / 32];
+    __align__(16) uint32_t zeros[kZeroBytes / 4];   // what lanes without a token read
 };
 
 // Headers of both blobs, a word per lane of one warp: bit 0 they fit the call, bit 1 w13 is in
@@ -119,8 +121,7 @@ template <bool MX>
 __device__ Route prologue(const FewArgs& a, Shared& sh, uint8_t* sm, int32_t*& s_ids, float*& s_w, bool report) {
     const int P = a.T * a.topk, tid = threadIdx.x;
     uint32_t* mask = reinterpret_cast<uint32_t*>(sm);
-    uint32_t* used = mask + a.E;             // bit e % 32 of word e / 32
-    s_ids = reinterpret_cast<int32_t*>(used + 32);
+    s_ids = reinterpret_cast<int32_t*>(mask + a.E);
     s_w = reinterpret_cast<float*>(s_ids + P);
     uint32_t* tokens = reinterpret_cast<uint32_t*>(s_w + P);
     uint16_t* expert = reinterpret_cast<uint16_t*>(tokens + a.slot_cap);
@@ -131,8 +132,8 @@ __device__ Route prologue(const FewArgs& a, Shared& sh, uint8_t* sm, int32_t*& s
         const int f = check_headers<MX>(a);
         if (tid == kConsumers * 32) sh.flags = f;
     }
-    for (int e = tid; e < a.E + 32; e += kThreads) mask[e] = 0;
-    if (tid < 64) sh.zeros[tid] = 0u;
+    for (int e = tid; e < a.E; e += kThreads) mask[e] = 0;
+    for (int i = tid; i < kZeroBytes / 4; i += kThreads) sh.zeros[i] = 0u;
     if (tid == 0) {
         sh.abort_flag = 0;
         for (int s = 0; s < a.depth; ++s) {
@@ -148,48 +149,50 @@ __device__ Route prologue(const FewArgs& a, Shared& sh, uint8_t* sm, int32_t*& s
         s_w[p] = p == tid ? w0 : a.wts[p];
         if (e >= 0 && e < a.E) {
             atomicOr(&mask[e], 1u << (p / a.topk));
-            atomicOr(&used[e >> 5], 1u << (e & 31));
         } else if (report && e != -1) {
             set_error(a.err, CHORD_DEV_BAD_EXPERT);
         }
     }
     __syncthreads();
-    // Warp 0, lane l: the used experts among 32 l .. 32 l + 31.  An exclusive scan of
-    // (passes << 16 | rows of h), then the passes.
-    if (tid < 32) {
-        const uint32_t u = used[tid];
-        uint32_t mine = 0;
-        for (uint32_t m = u; m; m &= m - 1) {
-            const int n = __popc(mask[tid * 32 + __ffs(m) - 1]);
-            mine += (uint32_t)((n + kPassTokens - 1) / kPassTokens) << 16 | (uint32_t)n;
-        }
-        uint32_t at = mine;
+    // Each thread takes `per` consecutive experts: an exclusive scan of (passes << 16 |
+    // rows of h) over the threads, then the passes.
+    const int per = (a.E + kThreads - 1) / kThreads, e0 = tid * per, e1 = min(e0 + per, a.E);
+    uint32_t mine = 0;
+    for (int e = e0; e < e1; ++e) {
+        const int n = __popc(mask[e]);
+        mine += (uint32_t)((n + kPassTokens - 1) / kPassTokens) << 16 | (uint32_t)n;
+    }
+    uint32_t at = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, at, o);
-            if (tid >= o) at += v;
-        }
-        if (tid == 31) sh.slots = (int)(at >> 16);
-        at -= mine;
-        for (uint32_t m = u; m; m &= m - 1) {
-            const int e = tid * 32 + __ffs(m) - 1;
-            uint32_t left = mask[e];
-            while (left) {
-                uint32_t part = left;
-                if (__popc(left) > kPassTokens) {
-                    part = 0;
-                    for (int k = 0; k < kPassTokens; ++k) {
-                        part |= left & (0u - left);
-                        left &= left - 1;
-                    }
-                } else {
-                    left = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, at, o);
+        if ((tid & 31) >= o) at += v;
+    }
+    if ((tid & 31) == 31) sh.sums[tid >> 5] = at;
+    at -= mine;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < (tid >> 5)) at += sh.sums[w];
+    }
+    if (tid == kThreads - 1) sh.slots = (int)((at + mine) >> 16);
+    for (int e = e0; e < e1; ++e) {
+        uint32_t left = mask[e];
+        while (left) {
+            uint32_t part = left;
+            if (__popc(left) > kPassTokens) {
+                part = 0;
+                for (int k = 0; k < kPassTokens; ++k) {
+                    part |= left & (0u - left);
+                    left &= left - 1;
                 }
-                expert[at >> 16] = (uint16_t)e;
-                tokens[at >> 16] = part;
-                first[at >> 16] = (uint16_t)at;
-                at += (1u << 16) + __popc(part);
+            } else {
+                left = 0;
             }
+            expert[at >> 16] = (uint16_t)e;
+            tokens[at >> 16] = part;
+            first[at >> 16] = (uint16_t)at;
+            at += (1u << 16) + __popc(part);
         }
     }
     __syncthreads();
@@ -345,11 +348,11 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t cta) {
 }
 // Sum over the cluster's CTAs, in rank order, of the float4 at `p` of each.
 __device__ __forceinline__ float4 cluster_sum(const float4* p, int n) {
-    float4 s = make_float4(0, 0, 0, 0);
-    for (int r = 0; r < n; ++r) {
-        const float4 v = ld_cluster(smem_u32(p), (uint32_t)r);
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-    }
+    float4 v[8], s = make_float4(0, 0, 0, 0);   // at most 8 CTAs; every load before the first sum
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[r] = r < n ? ld_cluster(smem_u32(p), (uint32_t)r) : make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
     return s;
 }
 
@@ -463,7 +466,6 @@ __device__ __forceinline__ void up_producer(const FewArgs& a, const Route& rt, c
     for (int item = blockIdx.x / a.cluster; item < items; item += gridDim.x / a.cluster) {
         const int slot = item / mt, m = item - slot * mt, e = rt.expert[slot];
         const uint32_t tokens = rt.tokens[slot];
-        const int n = __popc(tokens);
         for (int ks = ks0; ks < ks1 && ok; ++ks) {
             ok = tc5::wait(&rg.empty[r.slot], r.phase ^ 1u, rg.abort_flag, a.err);
             if (!ok) break;
@@ -513,11 +515,11 @@ __device__ __forceinline__ void up_producer(const FewArgs& a, const Route& rt, c
                 }
             }
             __syncwarp();
-            const uint32_t xs = smem_u32(st + S::kUpWeights);
-            for (int q = lane; q < n * kPieces; q += 32) {
-                const int j = q / kPieces, pc = q % kPieces, k = ks * S::kCols + pc * 8;
-                if (k < a.H) cp_async16(xs + j * S::kUpRow + pc * 16, a.x + (int64_t)nth_bit(tokens, j) * a.H + k);
-            }
+            uint32_t xs = smem_u32(st + S::kUpWeights) + lane * 16;
+            const int k = ks * S::kCols + lane * 8;
+            if (lane < kPieces && k < a.H)
+                for (uint32_t mk = tokens; mk; mk &= mk - 1, xs += S::kUpRow)
+                    cp_async16(xs, a.x + (int64_t)(__ffs(mk) - 1) * a.H + k);
             cp_async_arrive_noinc(bar);
             ++issued;
             r.next(a.depth);
@@ -596,7 +598,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
 }
 
 template <bool MX>
-__global__ void __launch_bounds__(kThreads, 3) few_gate_up_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads, MX ? 4 : 5) few_gate_up_kernel(const FewArgs a) {
     using S = Stage<MX>;
     pdl_trigger();
     extern __shared__ __align__(128) uint8_t smem[];
@@ -665,12 +667,13 @@ __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt,
     auto activations = [&](int v, int slot) {
         constexpr int kPieces = S::kCols / 8;   // of the value row, then as many of the remainder row
         const int sl = v / kst, ks = v - sl * kst, n = __popc(rt.tokens[sl]);
-        const uint32_t hs = smem_u32(rg.ptr + slot * a.stage_bytes + S::kDownWeights);
-        const uint16_t* src = a.h + (int64_t)rt.first[sl] * a.Ip + ks * S::kCols;
-        for (int q = lane; q < n * 2 * kPieces; q += 32) {
-            const int j = q / (2 * kPieces), pc = q % (2 * kPieces);
-            cp_async16(hs + j * S::kDownRow + pc * 16,
-                       src + (int64_t)j * a.Ip + (pc < kPieces ? pc * 8 : plane + (pc - kPieces) * 8));
+        uint32_t hs = smem_u32(rg.ptr + slot * a.stage_bytes + S::kDownWeights) + lane * 16;
+        const uint16_t* src = a.h + (int64_t)rt.first[sl] * a.Ip + ks * S::kCols + lane * 8;
+        const int64_t second = MX ? plane : plane - kPieces * 8;   // INT4: lanes 16 .. 31 take the remainder row
+        if (!MX && lane >= kPieces) src += second;
+        for (int j = 0; j < n; ++j, hs += S::kDownRow, src += a.Ip) {
+            cp_async16(hs, src);
+            if constexpr (MX) cp_async16(hs + kPieces * 16, src + second);
         }
         cp_async_arrive_noinc(&rg.full[slot]);
     };
@@ -719,8 +722,11 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
 #pragma unroll
         for (int u = 0; u < S::kUnits; ++u) {
             const bool on = ks * S::kCols + u * 128 + c * 32 < a.I;
+            uint32_t hb[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) hb[nt] = hrow[nt] && on ? hrow[nt] + u * 256 : rg.zero;
             unit_mma<MX, FAST, NT, true>(st, lr, u * 64, u * kMxScaleBlock, on, c, active, acc, [&](int nt, int j, bool rest) {
-                return lds128(hrow[nt] && on ? hrow[nt] + u * 256 + (rest ? S::kCols * 2 : 0) + j * 64 : rg.zero);
+                return lds128(hb[nt] + (rest ? S::kCols * 2 : 0) + j * 64);
             });
         }
         __syncwarp();
@@ -732,7 +738,7 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
 // CTA leaves its FP32 sums in the workspace and the tile's last one adds the
 // slices, always in slice order, so the result does not depend on which is last.
 template <bool MX, int NT>
-__global__ void __launch_bounds__(kThreads, 3) few_down_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 5 : 3) few_down_kernel(const FewArgs a) {
     using S = Stage<MX>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
@@ -782,9 +788,15 @@ __global__ void __launch_bounds__(kThreads, 3) few_down_kernel(const FewArgs a) 
             float4 s = make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
             if (a.cluster > 1) {
                 s = make_float4(0, 0, 0, 0);
-                for (int r = 0; r < a.cluster; ++r) {
-                    const float4 v = __ldcg(from + (int64_t)r * kPer + ((warp * 2 + i) * NT + nt) * 32 + lane);
-                    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+                for (int r0 = 0; r0 < a.cluster; r0 += 8) {   // eight loads before their sums
+                    float4 v[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        v[r] = r0 + r < a.cluster
+                                   ? __ldcg(from + (int64_t)(r0 + r) * kPer + ((warp * 2 + i) * NT + nt) * 32 + lane)
+                                   : make_float4(0, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
                 }
             }
             const int row = tile * 128 + (warp * 2 + i) * 16 + phys_row<MX>(lane >> 2), t = 8 * nt + 2 * (lane & 3);
@@ -806,6 +818,14 @@ int down_slices(int H, int64_t list) {
     int n = 152 * 3 / tiles;
     n = n > 16 ? 16 : (n < 1 ? 1 : n);
     return list < n ? (int)(list < 1 ? 1 : list) : n;
+}
+
+// Stages of a ring: what fits, but no more than a CTA will use (a small ring lets the
+// down kernel's CTAs in beside the gate_up kernel's).
+int ring_depth(size_t room, int stage_bytes, int64_t used) {
+    int64_t d = (int64_t)(room / (size_t)stage_bytes);
+    if (d > used) d = used;
+    return d > 16 ? 16 : (d < 2 ? 2 : (int)d);
 }
 
 template <typename Kern>
@@ -846,14 +866,13 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     const int stages = (a.H + S::kCols - 1) / S::kCols;
     a.cluster = 8;
     while (a.cluster > 1 && (items * a.cluster > (int64_t)sms * per_sm || a.cluster > stages)) a.cluster >>= 1;
+    const int64_t resident = (int64_t)sms * per_sm / a.cluster;
     // three CTAs per SM, as many stages as then fit
     const size_t third = 74 * 1024, beside = route + (a.cluster > 1 ? 8192 : 0);
     const int tokens = a.T < kPassTokens ? a.T : kPassTokens;
     a.stage_bytes = S::up_bytes(tokens);
-    a.depth = (int)((third - beside) / a.stage_bytes);
-    a.depth = a.depth > 16 ? 16 : (a.depth < 2 ? 2 : a.depth);
+    a.depth = ring_depth(third - beside, a.stage_bytes, items > resident ? 16 : (stages + a.cluster - 1) / a.cluster);
     size_t smem = (size_t)a.depth * a.stage_bytes + beside;
-    const int64_t resident = (int64_t)sms * per_sm / a.cluster;
     cudaError_t e = launch(few_gate_up_kernel<MX>, a, (unsigned)(items < resident ? items : resident), smem, true, false, st);
     if (e != cudaSuccess) return e;
     // down: the (pass, K stage) list of an output tile in slices, as many as fill the GPU
@@ -862,8 +881,7 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     const int tiles = (a.H + 127) / 128;
     a.cluster = down_slices(a.H, list);
     a.stage_bytes = S::down_bytes(tokens);
-    a.depth = (int)((third - route) / a.stage_bytes);
-    a.depth = a.depth > 16 ? 16 : (a.depth < 2 ? 2 : a.depth);
+    a.depth = ring_depth(third - route, a.stage_bytes, (int)((list + a.cluster - 1) / a.cluster));
     smem = (size_t)a.depth * a.stage_bytes + route;
     return launch(few_down_kernel<MX, NT>, a, (unsigned)tiles, smem, false, pdl_enabled(), st);
 }

@@ -19,12 +19,13 @@
 //     and remainder, 16 significant bits together).  Few items: a cluster of CTAs
 //     splits K and joins the sums through distributed shared memory in rank order.
 //   down: several CTAs share 128 output rows for all experts: each takes a slice of
-//     the (expert, K stage) list, and the last one to finish adds the FP32 sums in
+//     the (pass, K stage) list, and the last one to finish adds the FP32 sums in
 //     slice order, so there is no combine pass and no order that changes a result.  The
 //     kernel is launched early (programmatic dependent launch) and its weights are on
 //     the way while gate_up still runs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "chord_internal.h"
@@ -370,12 +371,12 @@ struct LaneRows {
     uint32_t soff, sd_row, sd_tile;
 };
 
-// One 128-column unit of a stage: 32 rows of this warp times the tokens of NT
-// column tiles (active: bit per tile).  b(nt, j): piece j of the tokens' value
-// (and, REST, remainder) columns.
-template <bool MX, bool FAST, int NT, bool REST, typename LoadB>
+// One 128-column unit of a stage: 32 rows of this warp times eight columns.  b(j): this
+// lane's piece j of its column's activations; REST: a second operand for the same
+// columns (b(4 + j)).
+template <bool MX, bool FAST, bool REST, typename LoadB>
 __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32_t code_xor, uint32_t scale_add, bool on, int c,
-                                         uint32_t active, float (&acc)[2][NT][4], LoadB&& b) {
+                                         float (&acc)[2][4], LoadB&& b) {
     uint4 q[2][2];
     Scale s[2][2];
     bool wide = false;
@@ -392,22 +393,16 @@ __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32
     if constexpr (MX) wide = __any_sync(0xffffffffu, wide);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        uint32_t x[2][2][4];
+        const uint4 v = b(j);
+        uint4 r;
+        if constexpr (REST) r = b(4 + j);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) dequant8<MX, FAST>(word(q[i][h], j), s[i][h], wide, x[i][h]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && !(active >> nt & 1u)) continue;
-            const uint4 v = b(nt, j, false);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) mma16816(acc[i][nt], x[i][0], x[i][1], v);
-            if constexpr (REST) {
-                const uint4 r = b(nt, j, true);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) mma16816(acc[i][nt], x[i][0], x[i][1], r);
-            }
+        for (int i = 0; i < 2; ++i) {
+            uint32_t x0[4], x1[4];
+            dequant8<MX, FAST>(word(q[i][0], j), s[i][0], wide, x0);
+            dequant8<MX, FAST>(word(q[i][1], j), s[i][1], wide, x1);
+            mma16816(acc[i], x0, x1, v);
+            if constexpr (REST) mma16816(acc[i], x0, x1, r);
         }
     }
 }
@@ -560,7 +555,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
             lr.soff += quad[0] * 4;
             lr.sd_row = 2048 + quad[1] * 4 - quad[0] * 4;
         }
-        float acc[2][1][4] = {};
+        float acc[2][4] = {};
         for (int ks = ks0; ks < ks1; ++ks, r.next(a.depth)) {
             if (ok) ok = tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err);
             if (!ok) break;
@@ -570,8 +565,8 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
             for (int u = 0; u < S::kUnits; ++u) {
                 const bool on = ks * S::kCols + u * 128 + c * 32 < a.H;
                 const uint32_t xb = g < n && on ? xs + u * 256 : rg.zero;
-                unit_mma<MX, FAST, 1, false>(st, lr, u * 64, u * kMxScaleBlock, on, c, 1u, acc,
-                                             [&](int, int j, bool) { return b_order<MX>(lds128(xb + j * 16)); });
+                unit_mma<MX, FAST, false>(st, lr, u * 64, u * kMxScaleBlock, on, c, acc,
+                                          [&](int j) { return b_order<MX>(lds128(xb + j * 16)); });
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&rg.empty[r.slot]);
@@ -580,7 +575,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
         if (a.cluster == 1) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (ok) store_h<MX>(a, rt, slot, s_ids, s_w, col0 + 8 * i, c, make_float4(acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]));
+                if (ok) store_h<MX>(a, rt, slot, s_ids, s_w, col0 + 8 * i, c, make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]));
             continue;
         }
         // join the cluster's K ranges: CTA `rank` takes tiles rank, rank + cluster, ... of the
@@ -588,7 +583,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
         float4* buf = part + (nitem & 1) * 256;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            buf[(warp * 2 + i) * 32 + lane] = make_float4(acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]);
+            buf[(warp * 2 + i) * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
         __syncwarp();
         cluster_sync_all();
         const int tile = rank + a.cluster * warp;
@@ -598,7 +593,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
 }
 
 template <bool MX>
-__global__ void __launch_bounds__(kThreads, MX ? 4 : 5) few_gate_up_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) few_gate_up_kernel(const FewArgs a) {
     using S = Stage<MX>;
     pdl_trigger();
     extern __shared__ __align__(128) uint8_t smem[];
@@ -632,27 +627,35 @@ __global__ void __launch_bounds__(kThreads, MX ? 4 : 5) few_gate_up_kernel(const
 }
 
 // ---- down -------------------------------------------------------------------
+// Entries [v0, v1) of the list, entry v = (pass v / kst, K stage v % kst).
 template <bool MX>
-__device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt, const Ring& rg, int tile, int rank, int kst,
-                                              int total) {
+__device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt, const Ring& rg, int tile, int v0, int v1, int kst) {
     using S = Stage<MX>;
+    constexpr int kPieces = S::kCols / 8;   // 16-byte pieces of a value row; as many of the remainder row
     const int lane = threadIdx.x & 31;
-    const int64_t plane = (int64_t)a.T * a.topk * a.Ip;
-    auto weights = [&](int v, int slot) {
-        const int sl = v / kst, ks = v - sl * kst;
+    struct At {
+        int sl, ks;
+        __device__ void next(int kst) {
+            if (++ks == kst) {
+                ks = 0;
+                ++sl;
+            }
+        }
+    };
+    auto weights = [&](const At& at, int slot) {
         uint64_t* bar = &rg.full[slot];
         uint8_t* st = rg.ptr + slot * a.stage_bytes;
         if constexpr (MX) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar, kMxTileBytes);
-                bulk_g2s(st, a.w2 + kHeaderBytes + (uint64_t)rt.expert[sl] * mx_group_bytes(a.H, a.I) +
-                                 ((int64_t)tile * mx_col_tiles(a.I) + ks) * kMxTileBytes,
+                bulk_g2s(st, a.w2 + kHeaderBytes + (uint64_t)rt.expert[at.sl] * mx_group_bytes(a.H, a.I) +
+                                 ((int64_t)tile * mx_col_tiles(a.I) + at.ks) * kMxTileBytes,
                          kMxTileBytes, bar);
             }
         } else {
-            const int chunks = a.I / 64 - 2 * ks >= 2 ? 2 : 1;
-            const uint8_t* t = a.w2 + kHeaderBytes + (uint64_t)rt.expert[sl] * ((uint64_t)a.H * a.I * 9ull / 16ull) +
-                               (int64_t)tile * (a.I / 64) * 4608 + (int64_t)ks * 9216;
+            const int chunks = a.I / 64 - 2 * at.ks >= 2 ? 2 : 1;
+            const uint8_t* t = a.w2 + kHeaderBytes + (uint64_t)rt.expert[at.sl] * ((uint64_t)a.H * a.I * 9ull / 16ull) +
+                               (int64_t)tile * (a.I / 64) * 4608 + (int64_t)at.ks * 9216;
             const uint32_t ds = smem_u32(st + S::kScale) + lane * 16;
             cp_async16(ds, t + 4096 + lane * 16);
             if (chunks == 2) cp_async16(ds + 512, t + 4608 + 4096 + lane * 16);
@@ -664,12 +667,12 @@ __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt,
         }
         __syncwarp();
     };
-    auto activations = [&](int v, int slot) {
-        constexpr int kPieces = S::kCols / 8;   // of the value row, then as many of the remainder row
-        const int sl = v / kst, ks = v - sl * kst, n = __popc(rt.tokens[sl]);
+    const int64_t plane = (int64_t)a.T * a.topk * a.Ip;
+    const int64_t second = MX ? plane : plane - kPieces * 8;   // INT4: lanes 16 .. 31 take the remainder row
+    auto activations = [&](const At& at, int slot) {
+        const int n = __popc(rt.tokens[at.sl]);
         uint32_t hs = smem_u32(rg.ptr + slot * a.stage_bytes + S::kDownWeights) + lane * 16;
-        const uint16_t* src = a.h + (int64_t)rt.first[sl] * a.Ip + ks * S::kCols + lane * 8;
-        const int64_t second = MX ? plane : plane - kPieces * 8;   // INT4: lanes 16 .. 31 take the remainder row
+        const uint16_t* src = a.h + (int64_t)rt.first[at.sl] * a.Ip + at.ks * S::kCols + lane * 8;
         if (!MX && lane >= kPieces) src += second;
         for (int j = 0; j < n; ++j, hs += S::kDownRow, src += a.Ip) {
             cp_async16(hs, src);
@@ -678,25 +681,62 @@ __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt,
         cp_async_arrive_noinc(&rg.full[slot]);
     };
     // the first stages' weights do not depend on the gate_up kernel
+    const int n = v1 - v0;
+    At w{v0 / kst, v0 % kst}, act = w;
     int pre = 0;
-    for (int v = rank; v < total && pre < a.depth; v += a.cluster, ++pre) weights(v, pre);
+    for (; pre < n && pre < a.depth; ++pre, w.next(kst)) weights(w, pre);
     pdl_wait();   // h of the gate_up kernel is complete from here on
     tc5::Ring r;
     int issued = 0;
-    for (int v = rank; v < total; v += a.cluster, ++issued, r.next(a.depth)) {
+    for (; issued < n; ++issued, r.next(a.depth), act.next(kst)) {
         if (issued >= pre) {
             if (!tc5::wait(&rg.empty[r.slot], r.phase ^ 1u, rg.abort_flag, a.err)) break;
-            weights(v, r.slot);
+            weights(act, r.slot);
         }
-        activations(v, r.slot);
+        activations(act, r.slot);
     }
     cp_async_wait<0>();
     drain_ring(a, rg, r, issued);
 }
 
+// A pass's sums (column j: its j-th token) into the sums by token (lane (g, c), tile nt:
+// tokens 8 nt + 2c and + 1).  half: columns 4 .. 7 hold the remainders' products.
+template <int NT>
+__device__ __forceinline__ void add_pass(float (&sum)[2][NT][4], float (&p)[2][4], uint32_t tokens, bool half, int c) {
+    if (half) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] += __shfl_xor_sync(0xffffffffu, p[i >> 2][i & 3], 2);
+    }
+    for (int jj = 0; tokens; ++jj) {   // columns 2 jj and 2 jj + 1
+        const int ta = __ffs(tokens) - 1;
+        tokens &= tokens - 1;
+        const int tb = __ffs(tokens) - 1;   // -1: no such column
+        tokens &= tokens - 1;
+        float v[2][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i >> 2][i & 3] = __shfl_sync(0xffffffffu, p[i >> 2][i & 3], jj, 4);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (NT > 1 && (ta >> 3) != nt && (tb >> 3) != nt) continue;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int t = 8 * nt + 2 * c + k;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {   // (tile, row half)
+                    if (t == ta) sum[i >> 1][nt][(i & 1) * 2 + k] += v[i >> 1][(i & 1) * 2];
+                    if (t == tb) sum[i >> 1][nt][(i & 1) * 2 + k] += v[i >> 1][(i & 1) * 2 + 1];
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = 0.0f;
+}
+
 template <bool MX, int NT, bool FAST>
-__device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt, const Ring& rg, int rank, int kst, int total,
-                                              float (&acc)[2][NT][4]) {
+__device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt, const Ring& rg, int v0, int v1, int kst,
+                                              float (&sum)[2][NT][4]) {
     using S = Stage<MX>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const uint32_t row = 32 * warp + phys_row<MX>(g);
@@ -705,32 +745,36 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
                            : LaneRows{(uint32_t)c * S::kBlock + row * 16, 128, 256,
                                       (uint32_t)S::kScale + (c >> 1) * 512 + row * 4, 32, 64};
     tc5::Ring r;
-    for (int v = rank; v < total; v += a.cluster, r.next(a.depth)) {
-        const int sl = v / kst, ks = v - sl * kst;
+    int sl = v0 / kst, ks = v0 - sl * kst;
+    float pass[2][4] = {};
+    for (int left = v1 - v0; left > 0; ++sl, ks = 0) {
         const uint32_t tokens = rt.tokens[sl];
-        uint32_t active = 0;
+        const int n = __popc(tokens);
+        // up to four tokens: their values in columns 0 .. 3, their remainders in 4 .. 7, one
+        // instruction for both; more: two instructions
+        const bool half = n <= 4;
+        const int j = half ? g & 3 : g;
+        const uint32_t h0 = j < n ? S::kDownWeights + (uint32_t)j * S::kDownRow + c * 16 + (half && g >= 4 ? S::kCols * 2 : 0) : 0u;
+        const int end = min(kst, ks + left);
+        left -= end - ks;
+        for (; ks < end; ++ks, r.next(a.depth)) {
+            if (!tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err)) return;
+            const uint32_t st = rg.base + r.slot * a.stage_bytes;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) active |= (tokens >> (8 * nt) & 0xffu) ? 1u << nt : 0u;
-        if (!tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err)) break;
-        const uint32_t st = rg.base + r.slot * a.stage_bytes;
-        uint32_t hrow[NT];   // 0: the token is not in this pass
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int t = 8 * nt + g;
-            hrow[nt] = tokens >> t & 1u ? st + S::kDownWeights + __popc(tokens & ((1u << t) - 1u)) * S::kDownRow + c * 16 : 0u;
+            for (int u = 0; u < S::kUnits; ++u) {
+                const bool on = ks * S::kCols + u * 128 + c * 32 < a.I;
+                const uint32_t hb = h0 && on ? st + h0 + u * 256 : rg.zero;
+                if (half)
+                    unit_mma<MX, FAST, false>(st, lr, u * 64, u * kMxScaleBlock, on, c, pass,
+                                              [&](int j) { return lds128(hb + j * 64); });
+                else
+                    unit_mma<MX, FAST, true>(st, lr, u * 64, u * kMxScaleBlock, on, c, pass,
+                                             [&](int j) { return lds128(hb + (j & 3) * 64 + (j >> 2) * S::kCols * 2); });
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&rg.empty[r.slot]);
         }
-#pragma unroll
-        for (int u = 0; u < S::kUnits; ++u) {
-            const bool on = ks * S::kCols + u * 128 + c * 32 < a.I;
-            uint32_t hb[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) hb[nt] = hrow[nt] && on ? hrow[nt] + u * 256 : rg.zero;
-            unit_mma<MX, FAST, NT, true>(st, lr, u * 64, u * kMxScaleBlock, on, c, active, acc, [&](int nt, int j, bool rest) {
-                return lds128(hb[nt] + (rest ? S::kCols * 2 : 0) + j * 64);
-            });
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&rg.empty[r.slot]);
+        add_pass<NT>(sum, pass, tokens, half, c);
     }
 }
 
@@ -738,7 +782,7 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
 // CTA leaves its FP32 sums in the workspace and the tile's last one adds the
 // slices, always in slice order, so the result does not depend on which is last.
 template <bool MX, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 5 : 3) few_down_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) few_down_kernel(const FewArgs a) {
     using S = Stage<MX>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
@@ -750,15 +794,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 5 : 3) few_down_kernel(con
     if (!(sh.flags & 1)) return;   // the same in every CTA; the gate_up kernel reported it
     const int rank = blockIdx.x % a.cluster, tile = blockIdx.x / a.cluster;
     const int kst = (a.I + S::kCols - 1) / S::kCols, total = rt.slots * kst;
+    const int v0 = (int)((int64_t)rank * total / a.cluster), v1 = (int)((int64_t)(rank + 1) * total / a.cluster);
     float acc[2][NT][4];
 #pragma unroll
     for (int i = 0; i < 2 * NT * 4; ++i) acc[i / (NT * 4)][i / 4 % NT][i % 4] = 0.0f;
     if (warp == kConsumers)
-        down_producer<MX>(a, rt, rg, tile, rank, kst, total);
+        down_producer<MX>(a, rt, rg, tile, v0, v1, kst);
     else if (MX || (sh.flags & 8))
-        down_consumer<MX, NT, true>(a, rt, rg, rank, kst, total, acc);
+        down_consumer<MX, NT, true>(a, rt, rg, v0, v1, kst, acc);
     else
-        down_consumer<MX, NT, false>(a, rt, rg, rank, kst, total, acc);
+        down_consumer<MX, NT, false>(a, rt, rg, v0, v1, kst, acc);
     __syncwarp();
     constexpr int kPer = kConsumers * 2 * NT * 32;   // float4 of a CTA: [warp][i][nt][lane]
     float4* mine = a.part + (int64_t)blockIdx.x * kPer;
@@ -858,20 +903,24 @@ cudaError_t launch(Kern kern, const FewArgs& a, unsigned groups, size_t smem, bo
 template <bool MX, int NT>
 cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     using S = Stage<MX>;
-    const int sms = device_info().sm_count, per_sm = 3;
+    const int sms = device_info().sm_count;
     const size_t route = route_bytes(a.E, a.T * a.topk, a.slot_cap);
     // gate_up: a cluster shares an item's K range while the items then still fit the
     // GPU at once (few items leave SMs idle and one CTA streams a long K alone)
     const int64_t items = (int64_t)a.slot_cap * ((a.I + 63) / 64);
+    // Three CTAs per SM while the items of an even routing then run in one wave (they
+    // spread evenly: 16 tokens TP8, 436 items, gate_up done after 52 us against 64
+    // with four per SM), else four (32 tokens EP8, 768 items: 67 us against 82).
+    const double even = a.E * (1.0 - pow(1.0 - 1.0 / a.E, (double)a.T * a.topk));
+    const int per_sm = even * ((a.I + 63) / 64) <= 3.0 * sms ? 3 : 4;
     const int stages = (a.H + S::kCols - 1) / S::kCols;
     a.cluster = 8;
     while (a.cluster > 1 && (items * a.cluster > (int64_t)sms * per_sm || a.cluster > stages)) a.cluster >>= 1;
     const int64_t resident = (int64_t)sms * per_sm / a.cluster;
-    // three CTAs per SM, as many stages as then fit
-    const size_t third = 74 * 1024, beside = route + (a.cluster > 1 ? 8192 : 0);
+    const size_t third = 72 * 1024, up_room = per_sm == 3 ? third : 53 * 1024, beside = route + (a.cluster > 1 ? 8192 : 0);
     const int tokens = a.T < kPassTokens ? a.T : kPassTokens;
     a.stage_bytes = S::up_bytes(tokens);
-    a.depth = ring_depth(third - beside, a.stage_bytes, items > resident ? 16 : (stages + a.cluster - 1) / a.cluster);
+    a.depth = ring_depth(up_room - beside, a.stage_bytes, items > resident ? 16 : (stages + a.cluster - 1) / a.cluster);
     size_t smem = (size_t)a.depth * a.stage_bytes + beside;
     cudaError_t e = launch(few_gate_up_kernel<MX>, a, (unsigned)(items < resident ? items : resident), smem, true, false, st);
     if (e != cudaSuccess) return e;

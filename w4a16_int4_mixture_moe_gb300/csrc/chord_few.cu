@@ -318,15 +318,20 @@ __device__ __forceinline__ int h_pos(int col) {
     return (col & ~127) | ((col >> 3) & 3) << 5 | ((col >> 5) & 3) << 3 | e;
 }
 
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&r0)[4], const uint32_t (&r1)[4], const uint4& b) {
+// d: two sums, one per k16 half, so that consecutive instructions do not wait on one another.
+__device__ __forceinline__ void mma16816(float (&d)[2][4], const uint32_t (&r0)[4], const uint32_t (&r1)[4], const uint4& b) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "+f"(d[0][0]), "+f"(d[0][1]), "+f"(d[0][2]), "+f"(d[0][3])
         : "r"(r0[0]), "r"(r1[0]), "r"(r0[1]), "r"(r1[1]), "r"(b.x), "r"(b.y));
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "+f"(d[1][0]), "+f"(d[1][1]), "+f"(d[1][2]), "+f"(d[1][3])
         : "r"(r0[2]), "r"(r1[2]), "r"(r0[3]), "r"(r1[3]), "r"(b.z), "r"(b.w));
+}
+
+__device__ __forceinline__ float4 both(const float (&d)[2][4]) {
+    return make_float4(d[0][0] + d[1][0], d[0][1] + d[1][1], d[0][2] + d[1][2], d[0][3] + d[1][3]);
 }
 
 __device__ __forceinline__ void cluster_sync_all() {
@@ -376,7 +381,7 @@ struct LaneRows {
 // columns (b(4 + j)).
 template <bool MX, bool FAST, bool REST, typename LoadB>
 __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32_t code_xor, uint32_t scale_add, bool on, int c,
-                                         float (&acc)[2][4], LoadB&& b) {
+                                         float (&acc)[2][2][4], LoadB&& b) {
     uint4 q[2][2];
     Scale s[2][2];
     bool wide = false;
@@ -555,7 +560,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
             lr.soff += quad[0] * 4;
             lr.sd_row = 2048 + quad[1] * 4 - quad[0] * 4;
         }
-        float acc[2][4] = {};
+        float acc[2][2][4] = {};
         for (int ks = ks0; ks < ks1; ++ks, r.next(a.depth)) {
             if (ok) ok = tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err);
             if (!ok) break;
@@ -575,7 +580,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
         if (a.cluster == 1) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (ok) store_h<MX>(a, rt, slot, s_ids, s_w, col0 + 8 * i, c, make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]));
+                if (ok) store_h<MX>(a, rt, slot, s_ids, s_w, col0 + 8 * i, c, both(acc[i]));
             continue;
         }
         // join the cluster's K ranges: CTA `rank` takes tiles rank, rank + cluster, ... of the
@@ -583,7 +588,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
         float4* buf = part + (nitem & 1) * 256;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            buf[(warp * 2 + i) * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+            buf[(warp * 2 + i) * 32 + lane] = both(acc[i]);
         __syncwarp();
         cluster_sync_all();
         const int tile = rank + a.cluster * warp;
@@ -702,7 +707,13 @@ __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt,
 // A pass's sums (column j: its j-th token) into the sums by token (lane (g, c), tile nt:
 // tokens 8 nt + 2c and + 1).  half: columns 4 .. 7 hold the remainders' products.
 template <int NT>
-__device__ __forceinline__ void add_pass(float (&sum)[2][NT][4], float (&p)[2][4], uint32_t tokens, bool half, int c) {
+__device__ __forceinline__ void add_pass(float (&sum)[2][NT][4], float (&chains)[2][2][4], uint32_t tokens, bool half, int c) {
+    float p[2][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        p[i >> 2][i & 3] = chains[i >> 2][0][i & 3] + chains[i >> 2][1][i & 3];
+        chains[i >> 2][0][i & 3] = chains[i >> 2][1][i & 3] = 0.0f;
+    }
     if (half) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] += __shfl_xor_sync(0xffffffffu, p[i >> 2][i & 3], 2);
@@ -730,8 +741,6 @@ __device__ __forceinline__ void add_pass(float (&sum)[2][NT][4], float (&p)[2][4
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = 0.0f;
 }
 
 template <bool MX, int NT, bool FAST>
@@ -746,7 +755,7 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
                                       (uint32_t)S::kScale + (c >> 1) * 512 + row * 4, 32, 64};
     tc5::Ring r;
     int sl = v0 / kst, ks = v0 - sl * kst;
-    float pass[2][4] = {};
+    float pass[2][2][4] = {};
     for (int left = v1 - v0; left > 0; ++sl, ks = 0) {
         const uint32_t tokens = rt.tokens[sl];
         const int n = __popc(tokens);
@@ -817,41 +826,56 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) few_down_kernel(con
                     mine[((warp * 2 + i) * NT + nt) * 32 + lane] =
                         make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
         }
-        __threadfence();
         __syncthreads();
-        if (threadIdx.x == 0) sh.last = atomicAdd(a.joined + tile, 1) == a.cluster - 1;
+        if (threadIdx.x == 0) {
+            __threadfence();   // the CTA's sums (ordered before it by the barrier) before the count
+            sh.last = atomicAdd(a.joined + tile, 1) == a.cluster - 1;
+            __threadfence();
+        }
         __syncthreads();
         if (!sh.last) return;
-        __threadfence();
     }
     if (warp == kConsumers) return;
-    const float4* from = a.part + (int64_t)tile * a.cluster * kPer;
+    if (a.cluster > 1) {
+        // slices in order, eight at a time, the loads of all column tiles of a row tile before
+        // their sums
+        const float4* from = a.part + (int64_t)tile * a.cluster * kPer + warp * 2 * NT * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float4 s[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[nt] = make_float4(0, 0, 0, 0);
+            for (int r0 = 0; r0 < a.cluster; r0 += 8) {
+                float4 v[NT][8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        v[nt][r] = r0 + r < a.cluster && 8 * nt < a.T
+                                       ? __ldcg(from + (int64_t)(r0 + r) * kPer + (i * NT + nt) * 32)
+                                       : make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        s[nt].x += v[nt][r].x, s[nt].y += v[nt][r].y, s[nt].z += v[nt][r].z, s[nt].w += v[nt][r].w;
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                acc[i][nt][0] = s[nt].x, acc[i][nt][1] = s[nt].y, acc[i][nt][2] = s[nt].z, acc[i][nt][3] = s[nt].w;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float4 s = make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
-            if (a.cluster > 1) {
-                s = make_float4(0, 0, 0, 0);
-                for (int r0 = 0; r0 < a.cluster; r0 += 8) {   // eight loads before their sums
-                    float4 v[8];
-#pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        v[r] = r0 + r < a.cluster
-                                   ? __ldcg(from + (int64_t)(r0 + r) * kPer + ((warp * 2 + i) * NT + nt) * 32 + lane)
-                                   : make_float4(0, 0, 0, 0);
-#pragma unroll
-                    for (int r = 0; r < 8; ++r) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
-                }
-            }
             const int row = tile * 128 + (warp * 2 + i) * 16 + phys_row<MX>(lane >> 2), t = 8 * nt + 2 * (lane & 3);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int tk = t + (k & 1), n = row + (k >> 1) * 8;
-                const float v = k == 0 ? s.x : k == 1 ? s.y : k == 2 ? s.z : s.w;
                 // + 0.0f: a sum of nothing, or of zeros of either sign, is +0
                 if (tk < a.T && n < a.H)
-                    a.out[(int64_t)tk * a.H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v + 0.0f));
+                    a.out[(int64_t)tk * a.H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i][nt][k] + 0.0f));
             }
         }
 }
@@ -905,17 +929,16 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     using S = Stage<MX>;
     const int sms = device_info().sm_count;
     const size_t route = route_bytes(a.E, a.T * a.topk, a.slot_cap);
-    // gate_up: a cluster shares an item's K range while the items then still fit the
-    // GPU at once (few items leave SMs idle and one CTA streams a long K alone)
-    const int64_t items = (int64_t)a.slot_cap * ((a.I + 63) / 64);
-    // Three CTAs per SM while the items of an even routing then run in one wave (they
-    // spread evenly: 16 tokens TP8, 436 items, gate_up done after 52 us against 64
-    // with four per SM), else four (32 tokens EP8, 768 items: 67 us against 82).
-    const double even = a.E * (1.0 - pow(1.0 - 1.0 / a.E, (double)a.T * a.topk));
-    const int per_sm = even * ((a.I + 63) / 64) <= 3.0 * sms ? 3 : 4;
-    const int stages = (a.H + S::kCols - 1) / S::kCols;
+    // gate_up: three CTAs per SM while the items of an even routing then run in one wave
+    // (they spread evenly: 16 tokens TP8, 436 items, done after 52 us against 64 with
+    // four per SM), else four (32 tokens EP8, 768 items: 67 us against 82).  Where they
+    // would leave half of the GPU idle, a cluster shares each item's K range.
+    const int mt = (a.I + 63) / 64, stages = (a.H + S::kCols - 1) / S::kCols;
+    const int64_t items = (int64_t)a.slot_cap * mt;
+    const double even = a.E * (1.0 - pow(1.0 - 1.0 / a.E, (double)a.T * a.topk)) * mt;
     a.cluster = 8;
-    while (a.cluster > 1 && (items * a.cluster > (int64_t)sms * per_sm || a.cluster > stages)) a.cluster >>= 1;
+    while (a.cluster > 1 && (even * a.cluster > 4.0 * sms || a.cluster > stages)) a.cluster >>= 1;
+    const int per_sm = a.cluster == 1 && even <= 3.0 * sms ? 3 : 4;
     const int64_t resident = (int64_t)sms * per_sm / a.cluster;
     const size_t third = 72 * 1024, up_room = per_sm == 3 ? third : 53 * 1024, beside = route + (a.cluster > 1 ? 8192 : 0);
     const int tokens = a.T < kPassTokens ? a.T : kPassTokens;

@@ -212,17 +212,20 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int
             uint32_t sc[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t b;
-                const uint32_t codes = quantize8<F32>(cur[i], b);
+                // padding: zeros with scale 1 (the same rows for the whole warp)
                 const bool row_in = (live >> i & 1u) != 0;
-                if (!in_k || !row_in) b = 127u;   // padding: zeros with scale 1
+                uint32_t codes = 0, w = 0x7F7F7F7Fu;
+                if (row_in) {
+                    uint32_t b;
+                    codes = quantize8<F32>(cur[i], b);
+                    w = (in_k ? b : 127u) << (8 * (j & 3));
+                    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+                    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+                    cur[i] = nxt[i];
+                }
                 if (!s.sorted_ids || row_in)
                     *reinterpret_cast<uint32_t*>(t + mx_code_offset(r0 + 32 * i, j) + 4 * (lane & 3)) = codes;
-                uint32_t w = b << (8 * (j & 3));
-                w |= __shfl_xor_sync(0xffffffffu, w, 4);
-                w |= __shfl_xor_sync(0xffffffffu, w, 8);
                 sc[i] = w;
-                cur[i] = nxt[i];
             }
             if ((lane & 15) == 0)
                 *reinterpret_cast<uint4*>(t + mx_scale_offset(r0, j)) = make_uint4(sc[0], sc[1], sc[2], sc[3]);

@@ -34,15 +34,17 @@ struct MxGemmArgs {
 //   * a producer lane copies K stages of 256 columns into a shared-memory ring
 //     with cp.async.bulk: the weight tile (17408 contiguous bytes) and the codes
 //     of the block's rows with their scales;
-//   * an issuing lane copies the stage's scales to tensor memory, issues its four
-//     K = 64 instructions into one of two FP32 accumulators and commits the
-//     stage back to the producer;
+//   * a scale warp's lane copies the stage's scales to tensor memory;
+//   * an issuing lane issues the stage's four K = 64 instructions into one of two FP32
+//     accumulators and commits the stage back to the producer (with the scale
+//     copies in the same lane a stage took about 900 cycles, paced by that lane);
 //   * eight warps read the finished accumulator and write C while the next item
 //     is computed into the other one.
 // Every wait is bounded; the grid is persistent (static round robin).
 constexpr int kEpiWarps = 8;
-constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
-constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kScaleWarp = kEpiWarps + 2;
+constexpr int kThreads = (kEpiWarps + 3) * 32;
+constexpr int kMaxStages = 12;
 constexpr int kStgBytes = 2048;          // one epilogue warp's buffer: 16 rows x 32 columns x FP32
 constexpr uint32_t kTmemCols = 512;
 constexpr size_t kSmemBudget = 227 * 1024;
@@ -171,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     uint8_t* stg = smem + pl.stages * pl.stage_bytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(stg + kEpiWarps * kStgBytes);
     uint64_t* empty = full + pl.stages;
-    uint64_t* acc_full = empty + pl.stages;
+    uint64_t* sf_full = empty + pl.stages;
+    uint64_t* acc_full = sf_full + pl.sf_slots;
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] row count, [1] abort, [2] skip
@@ -196,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
+        for (int s = 0; s < pl.sf_slots; ++s) mbar_init(&sf_full[s], 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&acc_full[s], 1);
             mbar_init(&acc_empty[s], kEpiWarps);
@@ -259,9 +263,43 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             }
         }
         __syncwarp();
+    } else if (warp == kScaleWarp) {
+        tc5::Ring r, sf;
+        uint32_t g_stage = 0;
+        bool ok = true;
+        const uint32_t sf_base = tmem + 2u * (uint32_t)pl.tok;
+        for (int64_t i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
+            const Item it = item_at(g, pl, i, ntiles, lane, false);
+            if (it.rows == 0) continue;
+            const bool two = it.off + it.rows > kMxTileRows;
+            for (int ks = 0; ks < kstages; ++ks, ++g_stage, r.next(pl.stages), sf.next(pl.sf_slots)) {
+                // the slot was last read by the instructions of sf_slots stages ago
+                if (g_stage >= (uint32_t)pl.sf_slots) {
+                    const uint32_t old = g_stage - (uint32_t)pl.sf_slots;
+                    ok = tc5::wait(&empty[old % pl.stages], (old / pl.stages) & 1u, &flags[1], g.err);
+                }
+                ok = ok && tc5::wait(&full[r.slot], r.phase, &flags[1], g.err);
+                if (!ok) break;
+                tc5::fence_after();
+                const uint32_t st = smem_u32(smem) + (uint32_t)(r.slot * pl.stage_bytes);
+                const uint32_t sfa = sf_base + (uint32_t)sf.slot * 24u, sfb = sfa + 8u;
+                const uint64_t dsa = tc5::desc_scales(st + kMxCodeBytes);
+                const uint64_t dsb = tc5::desc_scales(st + kMxTileBytes + (uint32_t)pl.tok * 128u);
+                if (tc5::elect()) {
+#pragma unroll
+                    for (uint32_t h = 0; h < 2; ++h) {
+                        tc5::cp_scales(sfa + 4u * h, dsa + h * (kMxScaleBlock >> 4));
+                        tc5::cp_scales(sfb + 8u * h, dsb + h * (kMxScaleBlock >> 4));
+                        if (two) tc5::cp_scales(sfb + 8u * h + 4u, dsb + (1024u >> 4) + h * (kMxScaleBlock >> 4));
+                    }
+                    tc5::commit(&sf_full[sf.slot]);
+                }
+                __syncwarp();
+            }
+        }
     } else if (warp == kMmaWarp) {
-        tc5::Ring r;
-        uint32_t nitem = 0, g_stage = 0, sf_slot = 0;
+        tc5::Ring r, sf;
+        uint32_t nitem = 0;
         uint64_t* last_bar = nullptr;
         uint32_t last_parity = 0;
         bool ok = true;
@@ -274,46 +312,29 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             tc5::fence_after();
             const uint32_t acc = tmem + buf * (uint32_t)pl.tok;
             const uint32_t id0 = tc5::idesc_mxf4(it.rows, 0), id2 = tc5::idesc_mxf4(it.rows, 2);
-            const bool two = it.off + it.rows > kMxTileRows;
-            for (int ks = 0; ks < kstages; ++ks, ++g_stage, r.next(pl.stages)) {
-                // the scale slot was last read by the instructions of sf_slots stages ago
-                if (g_stage >= (uint32_t)pl.sf_slots && pl.sf_slots < pl.stages) {
-                    const uint32_t old = g_stage - (uint32_t)pl.sf_slots;
-                    if (!tc5::wait(&empty[old % pl.stages], (old / pl.stages) & 1u, &flags[1], g.err)) {
-                        ok = false;
-                        break;
-                    }
-                }
-                if (!tc5::wait(&full[r.slot], r.phase, &flags[1], g.err)) {
+            for (int ks = 0; ks < kstages; ++ks, r.next(pl.stages), sf.next(pl.sf_slots)) {
+                if (!tc5::wait(&full[r.slot], r.phase, &flags[1], g.err) ||
+                    !tc5::wait(&sf_full[sf.slot], sf.phase, &flags[1], g.err)) {
                     ok = false;
                     break;
                 }
                 tc5::fence_after();
                 const uint32_t st = smem_u32(smem) + (uint32_t)(r.slot * pl.stage_bytes);
-                const uint32_t sb = st + kMxTileBytes, ss = sb + (uint32_t)pl.tok * 128u;
-                const uint32_t sfa = sf_base + sf_slot * 24u, sfb = sfa + 8u;
-                const uint64_t dsa = tc5::desc_scales(st + kMxCodeBytes), dsb = tc5::desc_scales(ss);
-                const uint64_t da = tc5::desc_sw128(st), db = tc5::desc_sw128(sb);
+                const uint32_t sfa = sf_base + (uint32_t)sf.slot * 24u, sfb = sfa + 8u + (uint32_t)(it.off >> 5);
+                const uint64_t da = tc5::desc_sw128(st), db = tc5::desc_sw128(st + kMxTileBytes);
                 const int nk = min(4, (g.K - ks * kMxTileCols + 63) / 64);
                 if (tc5::elect()) {
-#pragma unroll
-                    for (uint32_t h = 0; h < 2; ++h) {
-                        tc5::cp_scales(sfa + 4u * h, dsa + h * (kMxScaleBlock >> 4));
-                        tc5::cp_scales(sfb + 8u * h, dsb + h * (kMxScaleBlock >> 4));
-                        if (two) tc5::cp_scales(sfb + 8u * h + 4u, dsb + (1024u >> 4) + h * (kMxScaleBlock >> 4));
-                    }
 #pragma unroll
                     for (uint32_t kk = 0; kk < 4; ++kk)
                         if ((int)kk < nk)
                             tc5::mma_mxf4(acc, da + 2u * kk, db + 2u * kk, kk & 1 ? id2 : id0, sfa + 4u * (kk >> 1),
-                                          sfb + 8u * (kk >> 1) + (uint32_t)(it.off >> 5), ks > 0 || kk > 0 ? 1u : 0u);
+                                          sfb + 8u * (kk >> 1), ks > 0 || kk > 0 ? 1u : 0u);
                     tc5::commit(&empty[r.slot]);
                     if (ks == kstages - 1) tc5::commit(&acc_full[buf]);
                 }
                 __syncwarp();
                 last_bar = &empty[r.slot];
                 last_parity = r.phase;
-                if (++sf_slot == (uint32_t)pl.sf_slots) sf_slot = 0;
             }
             ++nitem;
         }
@@ -349,9 +370,9 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
     pl.tok = g.sorted_ids ? (int)g.a_rows : (g.a_rows > 128 ? 192 : (g.a_rows > 64 ? 128 : 64));
     const int tiles = (pl.tok + 64 + kMxTileRows - 1) / kMxTileRows;   // row tiles a block may touch
     pl.stage_bytes = kMxTileBytes + pl.tok * 128 + 1024 * tiles;
-    const size_t fixed = 1024 + kEpiWarps * kStgBytes + 256;
+    const size_t fixed = 1024 + kEpiWarps * kStgBytes + 128 + 8 * kMaxStages;
     pl.stages = (int)((kSmemBudget - fixed) / (pl.stage_bytes + 16));
-    if (pl.stages > 12) pl.stages = 12;
+    if (pl.stages > kMaxStages) pl.stages = kMaxStages;
     if (pl.stages < 2) return cudaErrorInvalidConfiguration;
     pl.sf_slots = (int)((kTmemCols - 2 * pl.tok) / 24);
     if (pl.sf_slots > pl.stages) pl.sf_slots = pl.stages;

@@ -154,6 +154,7 @@ __device__ __forceinline__ void mx_write_header(uint8_t* packed, int i, int64_t 
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int64_t G, int64_t N, int K, int run,
                                                           uint8_t* __restrict__ packed, int* err) {
+    pdl_trigger();   // a product that follows sets itself up meanwhile
     if (blockIdx.x == 0 && threadIdx.x < kHeaderBytes / 4) mx_write_header(packed, threadIdx.x, G, N, K);
     const int64_t rt = mx_row_tiles(N);
     const int kb = (int)mx_col_tiles(K);

@@ -55,6 +55,22 @@ __device__ __forceinline__ bool mx_header_ok(const uint8_t* blob, int64_t G, int
            h64[1] == (unsigned long long)kHeaderBytes;
 }
 
+// Header check by one warp, a word per lane (one memory latency).
+__device__ __forceinline__ bool mx_header_ok_warp(const uint8_t* blob, int64_t G, int64_t N, int K) {
+    const int i = threadIdx.x & 31;
+    const unsigned long long bytes = mx_group_bytes(N, K);
+    const uint32_t v = i < 12 ? reinterpret_cast<const uint32_t*>(blob)[i] : 0u;
+    const uint32_t want[4] = {kMagic, 1u, (uint32_t)CHORD_LAYOUT_MXFP4, (uint32_t)kGroup};
+    uint32_t w = i < 4 ? want[i & 3] : 0u;
+    if (i == 4) w = (uint32_t)G;
+    if (i == 5) w = (uint32_t)N;
+    if (i == 6) w = (uint32_t)K;
+    if (i == 8) w = (uint32_t)bytes;
+    if (i == 9) w = (uint32_t)(bytes >> 32);
+    if (i == 10) w = (uint32_t)kHeaderBytes;
+    return __all_sync(0xffffffffu, v == w);
+}
+
 // Scale 2^(b - 127) as FP32; b = 255 is NaN, b = 0 the subnormal 2^-127.
 __device__ __forceinline__ float mx_scale_f32(uint32_t b) {
     return __uint_as_float(b == 255u ? 0x7FC00000u : (b == 0u ? 0x00400000u : b << 23));

@@ -34,17 +34,24 @@ struct MxGemmArgs {
 //   * a producer lane copies K stages of 256 columns into a shared-memory ring
 //     with cp.async.bulk: the weight tile (17408 contiguous bytes) and the codes
 //     of the block's rows with their scales;
-//   * a scale warp's lane copies the stage's scales to tensor memory;
-//   * an issuing lane issues the stage's four K = 64 instructions into one of two FP32
-//     accumulators and commits the stage back to the producer (with the scale
-//     copies in the same lane a stage took about 900 cycles, paced by that lane);
+//   * an issuing warp copies the stage's scales to tensor memory, issues its four
+//     K = 64 instructions into one of two FP32 accumulators and commits the stage
+//     back to the producer.  This warp paces the kernel (a stage's instructions
+//     take 400 to 500 cycles, and its loop took as long again), so it takes two stages a
+//     turn and learns what an item is from the producer, beside the stage;
 //   * eight warps read the finished accumulator and write C while the next item
 //     is computed into the other one.
 // Every wait is bounded; the grid is persistent (static round robin).
+// Blocks of many rows run in clusters of two CTAs on neighbouring tiles of N: each
+// copies its own weights and half of the block's rows, the rows going to both CTAs
+// (multicast), since at fp4 rates the rows re-read from L2 for every 128 rows of N
+// are what an SM waits for.  A stage is then free once both CTAs have used it.
 constexpr int kEpiWarps = 8;
-constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kScaleWarp = kEpiWarps + 2;
-constexpr int kThreads = (kEpiWarps + 3) * 32;
+constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
+constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr uint32_t kStop = 0xffffffffu;   // stage info: no more items
 constexpr int kMaxStages = 12;
+constexpr int kPairRows = 96;            // blocks from here on run in pairs of CTAs
 constexpr int kStgBytes = 2048;          // one epilogue warp's buffer: 16 rows x 32 columns x FP32
 constexpr uint32_t kTmemCols = 512;
 constexpr size_t kSmemBudget = 227 * 1024;
@@ -54,6 +61,7 @@ struct MxPlan {
     int stages;     // shared-memory ring
     int sf_slots;   // tensor-memory scale ring
     int stage_bytes;
+    int pair;       // clusters of two CTAs
 };
 
 struct Item {
@@ -62,13 +70,46 @@ struct Item {
     int e;          // expert
     int rows;       // rows of the block that hold pairs (a prefix), rounded up to 16; 0: nothing to do
     int off;        // first row inside its 128-row tile (dense blocks of 64 or 192: 0 or 64)
+    bool write;     // false: a pair's repeat of an odd last tile
 };
 
+// The routing of one item's block as loaded: issued an item ahead, so that no role
+// waits for it between two items.
+struct Routing {
+    int32_t e, ids[7];   // lane l: rows l, l + 32, ... of the block
+};
+
+struct Walk {
+    int64_t n_items, step;
+    int nper, ntiles;
+    uint32_t rank;
+};
+
+__device__ __forceinline__ Routing load_routing(const MxGemmArgs& g, const MxPlan& pl, const Walk& w, int64_t i, int lane) {
+    Routing r{};
+    if (!g.sorted_ids || i >= w.n_items) return r;
+    int q;
+    const int64_t b = divmod_idx(i, w.nper, q);
+    r.e = g.expert_ids[b];
+#pragma unroll
+    for (int k = 0; k < 7; ++k) {
+        const int row = lane + 32 * k;
+        r.ids[k] = row < pl.tok ? g.sorted_ids[b * pl.tok + row] : (int32_t)g.num_pairs;
+    }
+    return r;
+}
+
 // Facts of item i, computed identically by every warp from the same arrays.
-__device__ __forceinline__ Item item_at(const MxGemmArgs& g, const MxPlan& pl, int64_t i, int ntiles, int lane,
-                                        bool report) {
+__device__ __forceinline__ Item item_at(const MxGemmArgs& g, const MxPlan& pl, const Walk& w, int64_t i, const Routing& rt,
+                                        int lane, bool report) {
     Item it;
-    it.b = divmod_idx(i, ntiles, it.nt);
+    it.b = divmod_idx(i, w.nper, it.nt);
+    it.write = true;
+    if (pl.pair) {
+        it.nt = 2 * it.nt + (int)w.rank;
+        it.write = it.nt < w.ntiles;
+        if (!it.write) --it.nt;
+    }
     it.e = 0;
     it.off = 0;
     if (!g.sorted_ids) {
@@ -78,13 +119,7 @@ __device__ __forceinline__ Item item_at(const MxGemmArgs& g, const MxPlan& pl, i
         it.off = (int)(r0 % kMxTileRows);
         return it;
     }
-    it.e = g.expert_ids[it.b];
-    int32_t ids[7];
-#pragma unroll
-    for (int k = 0; k < 7; ++k) {
-        const int r = lane + 32 * k;
-        ids[k] = r < pl.tok ? g.sorted_ids[it.b * pl.tok + r] : (int32_t)g.num_pairs;
-    }
+    it.e = rt.e;
     it.rows = 0;
     if (it.e < 0 || it.e >= g.E) {
         if (report && lane == 0) set_error(g.err, CHORD_DEV_BAD_EXPERT);
@@ -93,8 +128,8 @@ __device__ __forceinline__ Item item_at(const MxGemmArgs& g, const MxPlan& pl, i
     int last = 0;
 #pragma unroll
     for (int k = 0; k < 7; ++k) {
-        const bool ok = ids[k] >= 0 && ids[k] < g.num_pairs;
-        if (report && !ok && ids[k] != g.num_pairs) set_error(g.err, CHORD_DEV_BAD_ROW);
+        const bool ok = rt.ids[k] >= 0 && rt.ids[k] < g.num_pairs;
+        if (report && !ok && rt.ids[k] != g.num_pairs) set_error(g.err, CHORD_DEV_BAD_ROW);
         if (ok) last = lane + 32 * k + 1;
     }
     last = __reduce_max_sync(0xffffffffu, last);
@@ -173,57 +208,70 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     uint8_t* stg = smem + pl.stages * pl.stage_bytes;
     uint64_t* full = reinterpret_cast<uint64_t*>(stg + kEpiWarps * kStgBytes);
     uint64_t* empty = full + pl.stages;
-    uint64_t* sf_full = empty + pl.stages;
-    uint64_t* acc_full = sf_full + pl.sf_slots;
+    uint64_t* acc_full = empty + pl.stages;
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
-    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] row count, [1] abort, [2] skip
+    volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] row blocks, [1] abort, [2] skip
+    // what each stage's item is, written by the producer before the stage is full:
+    // rows | offset << 16, or kStop
+    volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(tmem_slot + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        bool ok = mx_header_ok(g.a, g.a_groups, g.a_rows, g.K) && mx_header_ok(g.w, g.E, g.N, g.K);
-        if (!ok) set_error(g.err, CHORD_DEV_BAD_HEADER);
-        int64_t blocks = (g.a_rows + pl.tok - 1) / pl.tok;
-        if (g.sorted_ids) {
-            const int64_t ntp = *g.ntp;
-            if (ntp < 0 || ntp > g.a_groups * g.a_rows || ntp % pl.tok) {
-                if (ok) set_error(g.err, CHORD_DEV_BAD_PADDED);
-                ok = false;
-            }
-            blocks = ok ? ntp / pl.tok : 0;
-        }
-        flags[0] = (int)blocks;
-        flags[1] = 0;
-        flags[2] = ok ? 0 : 1;
-        for (int s = 0; s < pl.stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        for (int s = 0; s < pl.sf_slots; ++s) mbar_init(&sf_full[s], 1);
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&acc_full[s], 1);
-            mbar_init(&acc_empty[s], kEpiWarps);
-        }
-        fence_barrier_init();
-    }
-    __syncthreads();
-    if (flags[2]) return;
+    const uint32_t rank = pl.pair ? tc5::cluster_rank() : 0u;
     if (warp == kProducerWarp) tc5::alloc(tmem_slot, kTmemCols);
+    pdl_wait();   // before the first access to global memory
+    if (warp == 0) {
+        const bool oka = mx_header_ok_warp(g.a, g.a_groups, g.a_rows, g.K), okw = mx_header_ok_warp(g.w, g.E, g.N, g.K);
+        if (lane == 0) {
+            bool ok = oka && okw;
+            if (!ok) set_error(g.err, CHORD_DEV_BAD_HEADER);
+            int64_t blocks = (g.a_rows + pl.tok - 1) / pl.tok;
+            if (g.sorted_ids) {
+                const int64_t ntp = *g.ntp;
+                if (ntp < 0 || ntp > g.a_groups * g.a_rows || ntp % pl.tok) {
+                    if (ok) set_error(g.err, CHORD_DEV_BAD_PADDED);
+                    ok = false;
+                }
+                blocks = ok ? ntp / pl.tok : 0;
+            }
+            flags[0] = (int)blocks;
+            flags[1] = 0;
+            flags[2] = ok ? 0 : 1;
+            for (int s = 0; s < pl.stages; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], pl.pair ? 2 : 1);   // the CTAs that read the stage's rows
+            }
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(&acc_full[s], 1);
+                mbar_init(&acc_empty[s], kEpiWarps);
+            }
+            fence_barrier_init();
+        }
+    }
     tc5::fence_before();
     __syncthreads();
     tc5::fence_after();
+    // a pair's barriers are initialised before the other CTA's copies and commits reach them
+    if (pl.pair) tc5::cluster_sync();
     const uint32_t tmem = *tmem_slot;
     const int ntiles = (g.N + kMxTileRows - 1) / kMxTileRows;
     const int kstages = (g.K + kMxTileCols - 1) / kMxTileCols;
-    const int64_t n_items = (int64_t)flags[0] * ntiles;
+    // a pair's item is (row block, two tiles of N); an odd last tile leaves the second CTA a
+    // repeat of the first's that it does not write
+    const int nper = pl.pair ? (ntiles + 1) / 2 : ntiles;
+    const int64_t n_items = flags[2] ? 0 : (int64_t)flags[0] * nper;
+    const int64_t first = pl.pair ? blockIdx.x >> 1 : blockIdx.x;
+    const Walk wk{n_items, pl.pair ? gridDim.x >> 1 : gridDim.x, nper, ntiles, rank};
+    Routing nxt = load_routing(g, pl, wk, first, lane);
     const int64_t art = mx_row_tiles(g.a_rows);
 
     if (warp == kProducerWarp) {
         tc5::Ring r;
         int64_t issued = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-            const Item it = item_at(g, pl, i, ntiles, lane, false);
+        for (int64_t i = first; i < n_items && ok; i += wk.step) {
+            const Item it = item_at(g, pl, wk, i, nxt, lane, false);
+            nxt = load_routing(g, pl, wk, i + wk.step, lane);
             if (it.rows == 0) continue;
             if (lane == 0) {
                 const uint8_t* wt = g.w + kHeaderBytes + ((int64_t)it.e * ntiles + it.nt) * kstages * kMxTileBytes;
@@ -242,17 +290,39 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
                     uint8_t* sb = st + kMxTileBytes;
                     uint8_t* ss = sb + pl.tok * 128;
                     const uint8_t* a0 = at + (int64_t)ks * kMxTileBytes;
-                    mbar_arrive_expect_tx(&full[r.slot], bytes);
-                    bulk_g2s(st, wt + (int64_t)ks * kMxTileBytes, kMxTileBytes, &full[r.slot]);
-                    bulk_g2s(sb, a0 + it.off * 128, (uint32_t)r0 * 128u, &full[r.slot]);
-                    bulk_g2s(ss, a0 + kMxCodeBytes, 1024u, &full[r.slot]);
-                    if (r1 > 0) {
-                        bulk_g2s(sb + r0 * 128, a0 + tstride, (uint32_t)r1 * 128u, &full[r.slot]);
-                        bulk_g2s(ss + 1024, a0 + tstride + kMxCodeBytes, 1024u, &full[r.slot]);
+                    uint64_t* bar = &full[r.slot];
+                    info[r.slot] = (uint32_t)it.rows | (uint32_t)it.off << 16;
+                    mbar_arrive_expect_tx(bar, bytes);
+                    bulk_g2s(st, wt + (int64_t)ks * kMxTileBytes, kMxTileBytes, bar);
+                    if (!pl.pair) {
+                        bulk_g2s(sb, a0 + it.off * 128, (uint32_t)r0 * 128u, bar);
+                        bulk_g2s(ss, a0 + kMxCodeBytes, 1024u, bar);
+                        if (r1 > 0) {
+                            bulk_g2s(sb + r0 * 128, a0 + tstride, (uint32_t)r1 * 128u, bar);
+                            bulk_g2s(ss + 1024, a0 + tstride + kMxCodeBytes, 1024u, bar);
+                        }
+                    } else {
+                        // rows [h0, h1) and scale block `rank` of every tile touched, to both CTAs
+                        const int h0 = (int)rank * (it.rows / 2), h1 = h0 + it.rows / 2;
+                        const uint32_t so = kMxCodeBytes + rank * kMxScaleBlock;
+                        if (h0 < r0)
+                            tc5::bulk_g2s_pair(sb + h0 * 128, a0 + (it.off + h0) * 128, (uint32_t)(min(h1, r0) - h0) * 128u, bar);
+                        if (h1 > r0) {
+                            const int s0 = max(h0, r0);
+                            tc5::bulk_g2s_pair(sb + s0 * 128, a0 + tstride + (s0 - r0) * 128, (uint32_t)(h1 - s0) * 128u, bar);
+                        }
+                        tc5::bulk_g2s_pair(ss + rank * kMxScaleBlock, a0 + so, kMxScaleBlock, bar);
+                        if (r1 > 0) tc5::bulk_g2s_pair(ss + 1024 + rank * kMxScaleBlock, a0 + tstride + so, kMxScaleBlock, bar);
                     }
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+        if (lane == 0 && ok && tc5::wait(&empty[r.slot], r.phase ^ 1u, &flags[1], g.err)) {
+            info[r.slot] = kStop;
+            mbar_arrive(&full[r.slot]);
+            ++issued;
+            r.next(pl.stages);
         }
         // leave only after every copy issued here has landed
         if (lane == 0) {
@@ -263,94 +333,106 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             }
         }
         __syncwarp();
-    } else if (warp == kScaleWarp) {
-        tc5::Ring r, sf;
-        uint32_t g_stage = 0;
-        bool ok = true;
-        const uint32_t sf_base = tmem + 2u * (uint32_t)pl.tok;
-        for (int64_t i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-            const Item it = item_at(g, pl, i, ntiles, lane, false);
-            if (it.rows == 0) continue;
-            const bool two = it.off + it.rows > kMxTileRows;
-            for (int ks = 0; ks < kstages; ++ks, ++g_stage, r.next(pl.stages), sf.next(pl.sf_slots)) {
-                // the slot was last read by the instructions of sf_slots stages ago
-                if (g_stage >= (uint32_t)pl.sf_slots) {
-                    const uint32_t old = g_stage - (uint32_t)pl.sf_slots;
-                    ok = tc5::wait(&empty[old % pl.stages], (old / pl.stages) & 1u, &flags[1], g.err);
-                }
-                ok = ok && tc5::wait(&full[r.slot], r.phase, &flags[1], g.err);
-                if (!ok) break;
-                tc5::fence_after();
-                const uint32_t st = smem_u32(smem) + (uint32_t)(r.slot * pl.stage_bytes);
-                const uint32_t sfa = sf_base + (uint32_t)sf.slot * 24u, sfb = sfa + 8u;
-                const uint64_t dsa = tc5::desc_scales(st + kMxCodeBytes);
-                const uint64_t dsb = tc5::desc_scales(st + kMxTileBytes + (uint32_t)pl.tok * 128u);
-                if (tc5::elect()) {
-#pragma unroll
-                    for (uint32_t h = 0; h < 2; ++h) {
-                        tc5::cp_scales(sfa + 4u * h, dsa + h * (kMxScaleBlock >> 4));
-                        tc5::cp_scales(sfb + 8u * h, dsb + h * (kMxScaleBlock >> 4));
-                        if (two) tc5::cp_scales(sfb + 8u * h + 4u, dsb + (1024u >> 4) + h * (kMxScaleBlock >> 4));
-                    }
-                    tc5::commit(&sf_full[sf.slot]);
-                }
-                __syncwarp();
-            }
-        }
     } else if (warp == kMmaWarp) {
-        tc5::Ring r, sf;
-        uint32_t nitem = 0;
-        uint64_t* last_bar = nullptr;
-        uint32_t last_parity = 0;
+        // Slot, its address and parity; barriers as shared-memory addresses.
+        struct Pos {
+            uint32_t slot, st, parity;
+        };
+        const uint32_t base = smem_u32(smem), full_a = smem_u32(full), empty_a = smem_u32(empty);
+        const uint32_t stages = (uint32_t)pl.stages, stage_bytes = (uint32_t)pl.stage_bytes, tok128 = (uint32_t)pl.tok * 128u;
+        auto next = [&](Pos p) {
+            return p.slot + 1 == stages ? Pos{0, base, p.parity ^ 1u} : Pos{p.slot + 1, p.st + stage_bytes, p.parity};
+        };
+        const uint32_t sf_base = tmem + 2u * (uint32_t)pl.tok, sf_end = sf_base + (uint32_t)pl.sf_slots * 24u;
+        const bool sf_short = pl.sf_slots < pl.stages;
+        Pos p{0, base, 0};
+        uint32_t nitem = 0, g_stage = 0, sfa = sf_base;
+        uint32_t last_bar = 0, last_parity = 0;
         bool ok = true;
-        const uint32_t sf_base = tmem + 2u * (uint32_t)pl.tok;
-        for (int64_t i = blockIdx.x; i < n_items && ok; i += gridDim.x) {
-            const Item it = item_at(g, pl, i, ntiles, lane, false);
-            if (it.rows == 0) continue;
-            const uint32_t buf = nitem & 1u;
-            if (!tc5::wait(&acc_empty[buf], ((nitem >> 1) & 1u) ^ 1u, &flags[1], g.err)) break;
+        while (ok) {
+            if (!tc5::wait(full_a + p.slot * 8, p.parity, &flags[1], g.err)) break;
+            const uint32_t inf = __shfl_sync(0xffffffffu, info[p.slot], 0);
+            if (inf == kStop) break;
+            const uint32_t rows = inf & 0xffffu, off = inf >> 16, buf = nitem & 1u;
+            if (!tc5::wait(smem_u32(&acc_empty[buf]), ((nitem >> 1) & 1u) ^ 1u, &flags[1], g.err)) break;
             tc5::fence_after();
             const uint32_t acc = tmem + buf * (uint32_t)pl.tok;
-            const uint32_t id0 = tc5::idesc_mxf4(it.rows, 0), id2 = tc5::idesc_mxf4(it.rows, 2);
-            for (int ks = 0; ks < kstages; ++ks, r.next(pl.stages), sf.next(pl.sf_slots)) {
-                if (!tc5::wait(&full[r.slot], r.phase, &flags[1], g.err) ||
-                    !tc5::wait(&sf_full[sf.slot], sf.phase, &flags[1], g.err)) {
-                    ok = false;
-                    break;
-                }
-                tc5::fence_after();
-                const uint32_t st = smem_u32(smem) + (uint32_t)(r.slot * pl.stage_bytes);
-                const uint32_t sfa = sf_base + (uint32_t)sf.slot * 24u, sfb = sfa + 8u + (uint32_t)(it.off >> 5);
-                const uint64_t da = tc5::desc_sw128(st), db = tc5::desc_sw128(st + kMxTileBytes);
+            const uint32_t id0 = tc5::idesc_mxf4((int)rows, 0), id2 = tc5::idesc_mxf4((int)rows, 2);
+            const bool two = off + rows > (uint32_t)kMxTileRows;
+            // One stage: scales of its two 128-column halves to the slot's columns, then its
+            // instructions.  (A slot is reused only after the instructions that read it.)
+            auto stage = [&](const Pos& q, uint32_t sf, int ks) {
+                const uint64_t dsa = tc5::desc_scales(q.st + kMxCodeBytes);
+                const uint64_t dsb = tc5::desc_scales(q.st + kMxTileBytes + tok128);
+                const uint64_t da = tc5::desc_sw128(q.st), db = tc5::desc_sw128(q.st + kMxTileBytes);
                 const int nk = min(4, (g.K - ks * kMxTileCols + 63) / 64);
-                if (tc5::elect()) {
 #pragma unroll
-                    for (uint32_t kk = 0; kk < 4; ++kk)
-                        if ((int)kk < nk)
-                            tc5::mma_mxf4(acc, da + 2u * kk, db + 2u * kk, kk & 1 ? id2 : id0, sfa + 4u * (kk >> 1),
-                                          sfb + 8u * (kk >> 1), ks > 0 || kk > 0 ? 1u : 0u);
-                    tc5::commit(&empty[r.slot]);
-                    if (ks == kstages - 1) tc5::commit(&acc_full[buf]);
+                for (uint32_t h = 0; h < 2; ++h) {
+                    tc5::cp_scales(sf + 4u * h, dsa + h * (kMxScaleBlock >> 4));
+                    tc5::cp_scales(sf + 8u + 8u * h, dsb + h * (kMxScaleBlock >> 4));
+                    if (two) tc5::cp_scales(sf + 12u + 8u * h, dsb + (1024u >> 4) + h * (kMxScaleBlock >> 4));
+                }
+#pragma unroll
+                for (uint32_t kk = 0; kk < 4; ++kk)
+                    if ((int)kk < nk)
+                        tc5::mma_mxf4(acc, da + 2u * kk, db + 2u * kk, kk & 1 ? id2 : id0, sf + 4u * (kk >> 1),
+                                      sf + 8u + 8u * (kk >> 1) + (off >> 5), ks > 0 || kk > 0 ? 1u : 0u);
+                if (pl.pair)
+                    tc5::commit_pair(empty_a + q.slot * 8);
+                else
+                    tc5::commit(empty_a + q.slot * 8);
+                if (ks == kstages - 1) tc5::commit(smem_u32(&acc_full[buf]));
+            };
+            // instructions of the stage that used this stage's scale slot are done
+            auto sf_free = [&](uint32_t st) {
+                if (!sf_short || st < (uint32_t)pl.sf_slots) return true;
+                const uint32_t old = st - (uint32_t)pl.sf_slots;
+                return tc5::wait(empty_a + (old % stages) * 8, (old / stages) & 1u, &flags[1], g.err);
+            };
+            for (int ks = 0; ks < kstages; ks += 2) {
+                const bool second = ks + 1 < kstages;
+                const Pos q = next(p);
+                const uint32_t sfb = sfa + 24u == sf_end ? sf_base : sfa + 24u;
+                ok = (ks == 0 || tc5::wait(full_a + p.slot * 8, p.parity, &flags[1], g.err)) && sf_free(g_stage);
+                if (!sf_short) ok = ok && (!second || tc5::wait(full_a + q.slot * 8, q.parity, &flags[1], g.err));
+                if (!ok) break;
+                if (!sf_short) {
+                    if (tc5::elect()) {
+                        stage(p, sfa, ks);
+                        if (second) stage(q, sfb, ks + 1);
+                    }
+                } else {
+                    if (tc5::elect()) stage(p, sfa, ks);
+                    __syncwarp();
+                    if (second) {
+                        ok = tc5::wait(full_a + q.slot * 8, q.parity, &flags[1], g.err) && sf_free(g_stage + 1);
+                        if (!ok) break;
+                        if (tc5::elect()) stage(q, sfb, ks + 1);
+                    }
                 }
                 __syncwarp();
-                last_bar = &empty[r.slot];
-                last_parity = r.phase;
+                last_bar = empty_a + (second ? q.slot : p.slot) * 8;
+                last_parity = second ? q.parity : p.parity;
+                g_stage += second ? 2u : 1u;
+                sfa = second ? (sfb + 24u == sf_end ? sf_base : sfb + 24u) : sfb;
+                p = second ? next(q) : q;
             }
             ++nitem;
         }
         // the last instructions are done before the tensor memory is released
-        if (last_bar) mbar_wait(last_bar, last_parity);
+        if (last_bar) tc5::wait(last_bar, last_parity, &flags[1], g.err);
         __syncwarp();
     } else {
         const int wg = warp >> 2, quarter = warp & 3;
         int64_t nitem = 0;
-        for (int64_t i = blockIdx.x; i < n_items; i += gridDim.x) {
-            const Item it = item_at(g, pl, i, ntiles, lane, warp == 0);
+        for (int64_t i = first; i < n_items; i += wk.step) {
+            const Item it = item_at(g, pl, wk, i, nxt, lane, warp == 0);
+            nxt = load_routing(g, pl, wk, i + wk.step, lane);
             if (it.rows == 0) continue;
             const int buf = (int)(nitem & 1);
-            if (!tc5::wait(&acc_full[buf], (uint32_t)((nitem >> 1) & 1), &flags[1], g.err)) break;
+            if (!tc5::wait<true>(&acc_full[buf], (uint32_t)((nitem >> 1) & 1), &flags[1], g.err)) break;
             tc5::fence_after();
-            drain(g, pl, it, tmem + (uint32_t)(buf * pl.tok), wg, quarter, lane, stg + warp * kStgBytes);
+            if (it.write) drain(g, pl, it, tmem + (uint32_t)(buf * pl.tok), wg, quarter, lane, stg + warp * kStgBytes);
             tc5::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[buf]);
@@ -359,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     }
     tc5::fence_before();
     __syncthreads();
+    if (pl.pair) tc5::cluster_sync();   // the other CTA's copies and commits into this one are done
     tc5::fence_after();
     if (warp == kProducerWarp) tc5::dealloc(tmem, kTmemCols);
 }
@@ -370,7 +453,7 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
     pl.tok = g.sorted_ids ? (int)g.a_rows : (g.a_rows > 128 ? 192 : (g.a_rows > 64 ? 128 : 64));
     const int tiles = (pl.tok + 64 + kMxTileRows - 1) / kMxTileRows;   // row tiles a block may touch
     pl.stage_bytes = kMxTileBytes + pl.tok * 128 + 1024 * tiles;
-    const size_t fixed = 1024 + kEpiWarps * kStgBytes + 128 + 8 * kMaxStages;
+    const size_t fixed = 1024 + kEpiWarps * kStgBytes + 128 + 4 * kMaxStages;
     pl.stages = (int)((kSmemBudget - fixed) / (pl.stage_bytes + 16));
     if (pl.stages > kMaxStages) pl.stages = kMaxStages;
     if (pl.stages < 2) return cudaErrorInvalidConfiguration;
@@ -382,10 +465,30 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int64_t ntiles = (g.N + kMxTileRows - 1) / kMxTileRows;
     const int64_t blocks = g.sorted_ids ? g.a_groups : (g.a_rows + pl.tok - 1) / pl.tok;
-    const int64_t items = blocks * ntiles;
     const int64_t sms = device_info().sm_count;
-    mx_gemm_kernel<<<(unsigned)(items < sms ? items : sms), kThreads, smem, st>>>(g, pl);
-    return cudaGetLastError();
+    pl.pair = pl.tok >= kPairRows && ntiles > 1;
+    const int64_t items = pl.pair ? blocks * ((ntiles + 1) / 2) : blocks * ntiles, ctas = pl.pair ? sms / 2 : sms;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((items < ctas ? items : ctas) * (pl.pair ? 2 : 1)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pl.pair) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = 2;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl_enabled()) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, mx_gemm_kernel, g, pl);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -23,9 +23,8 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Arrive on `bar` once every tcgen05 operation this thread issued has completed.
-__device__ __forceinline__ void commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // One lane of the (converged) warp.  The issuing warp runs its loop with all
@@ -39,6 +38,33 @@ __device__ __forceinline__ bool elect() {
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(p));
     return p != 0;
+}
+
+// The same, on this barrier of both CTAs of a cluster of two.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// cp.async.bulk into both CTAs of a cluster of two: the same shared-memory offset,
+// bytes counted on the same barrier of each.
+__device__ __forceinline__ void bulk_g2s_pair(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1], %2, [%3], "
+        "%4;" ::"r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of every CTA of the cluster.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // D[128 x N] (+)= (A x scales)[128 x 64] * (B x scales)[N x 64]^T, E2M1 codes in
@@ -89,13 +115,29 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int n, uint32_t sf) {
            (sf << 29);
 }
 
-// Wait for a phase of `bar`, bounded in time; gives up at once when another
-// role has set the abort flag.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
-    if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Wait for a phase of the barrier at shared-memory address `bar`, bounded in
+// time; gives up at once when another role has set the abort flag.  RELAX: poll
+// every couple of hundred nanoseconds only (long waits off the critical path, whose
+// polling would take issue slots from the other roles).
+template <bool RELAX = false>
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    if (try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if constexpr (RELAX) __nanosleep(200);
+        if (try_wait(bar, parity)) return true;
         if ((it & 63u) == 0) {
             if (*abort_flag) return false;
             if (clock64() - t0 > kWaitLimitCycles) {
@@ -105,6 +147,10 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
             }
         }
     }
+}
+template <bool RELAX = false>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    return wait<RELAX>(smem_u32(bar), parity, abort_flag, err);
 }
 
 // Slot and parity of a ring of n stages.

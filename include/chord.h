@@ -554,8 +554,8 @@ chord_status chord_mxfp4_dequantize(const void *packed, size_t packed_bytes, int
                                     int K, void *out, int out_dtype, void *stream);
 
 /* Block size for the grouped product: the rows an expert rarely exceeds
- * (tok_e + 3 sqrt(tok_e) + 1, tok_e = T * topk / E_global) split into as few equal
- * blocks of at most 224 rows as hold them, rounded up to 32. */
+ * (tok_e + 3 sqrt(tok_e) + 1, tok_e = T * topk / E_global) in as few equal blocks
+ * of at most 208 rows as hold tok_e + 2 sqrt(tok_e) + 1 of them, rounded up to 16. */
 int chord_mxfp4_select_block_m(int T, int topk, int E_local, int E_global);
 
 /* Grouped product, the indexed contract of chord_w4a16_moe_gemm with both
@@ -567,7 +567,7 @@ int chord_mxfp4_select_block_m(int T, int topk, int E_local, int E_global);
  *   packed  chord_mxfp4_quantize of the weights [E, N, K]
  *   C       [num_pairs, N], CHORD_DTYPE_BF16 or CHORD_DTYPE_F32; rows no block
  *           names are not written
- * block_m % 32 == 0 and at most 224; K % 32 == 0; N is free. */
+ * block_m % 16 == 0 and at most 208; K % 32 == 0; N is free. */
 chord_status chord_mxfp4_moe_gemm(const void *Aq, size_t aq_bytes, const void *packed,
                                   size_t packed_bytes, int E, int N, int K,
                                   const int32_t *sorted_ids, const int32_t *expert_ids,

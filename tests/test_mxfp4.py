@@ -107,10 +107,10 @@ def test_sizes():
 def test_select_block_m():
     for T, topk, E in [(1, 1, 8), (1, 8, 384), (64, 8, 48), (1024, 8, 48), (4096, 8, 48), (100000, 8, 8), (0, 8, 8)]:
         bm = chord.chord_mxfp4_select_block_m(T, topk, E, E)
-        assert bm % 32 == 0 and 32 <= bm <= 224
+        assert bm % 16 == 0 and 16 <= bm <= 208
         tok = T * topk / E
-        if tok + 3 * tok ** .5 + 1 <= 224:
-            assert bm >= tok + 3 * tok ** .5 + 1
+        if tok + 2 * tok ** .5 + 1 <= 208:
+            assert bm >= min(tok + 3 * tok ** .5 + 1, 208)
 
 
 def test_refusals():
@@ -141,7 +141,7 @@ def test_refusals():
     g = lib.chord_mxfp4_moe_gemm
     wb = n(2, 100, 64)
     ok = [p, nb, p, wb, 2, 100, 64, p, p, p, 64, 32, 8, p, 0, None, None]
-    for at, v, st in [(11, 48, 2), (11, 256, 2), (6, 48, 2), (1, nb + 16, 3), (3, wb - 16, 3), (14, 3, 1), (4, 0, 1),
+    for at, v, st in [(11, 40, 2), (11, 224, 2), (6, 48, 2), (1, nb + 16, 3), (3, wb - 16, 3), (14, 3, 1), (4, 0, 1),
                       (13, vp((1 << 20) + 4), 1), (0, None, 1), (7, None, 1), (9, None, 1), (10, 63, 1)]:
         a = list(ok)
         a[at] = v
@@ -349,7 +349,7 @@ def align(ids, E, bm):
 @pytest.mark.parametrize("T,E,topk,N,K,bm,div", [
     (1, 4, 1, 128, 256, 32, 1), (3, 8, 2, 200, 96, 32, 2), (40, 3, 2, 129, 288, 64, 1), (50, 2, 1, 256, 512, 96, 1),
     (200, 2, 2, 130, 320, 128, 2), (150, 1, 1, 140, 64, 160, 1), (300, 4, 2, 260, 1056, 192, 2),
-    (250, 1, 1, 128, 256, 224, 1), (500, 3, 2, 384, 800, 224, 2)])
+    (250, 1, 1, 128, 256, 208, 1), (500, 3, 2, 384, 800, 208, 2), (30, 3, 2, 150, 544, 16, 2)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_grouped_product(T, E, topk, N, K, bm, div, dtype):
     need_gpu()

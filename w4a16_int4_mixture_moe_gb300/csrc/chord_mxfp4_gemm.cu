@@ -30,37 +30,42 @@ struct MxGemmArgs {
 
 // One work item is (row block, 128 rows of N).  The weight rows are the MMA's M
 // side and the block's rows its N side, so a block of 11 rows costs an N = 16
-// instruction.  Roles:
-//   * a producer lane copies K stages of 256 columns into a shared-memory ring
-//     with cp.async.bulk: the weight tile (17408 contiguous bytes) and the codes
-//     of the block's rows with their scales;
-//   * an issuing warp copies the stage's scales to tensor memory, issues its four
-//     K = 64 instructions into one of two FP32 accumulators and commits the stage
-//     back to the producer.  This warp paces the kernel (a stage's instructions
-//     take 400 to 500 cycles, and its loop took as long again), so it takes two stages a
-//     turn and learns what an item is from the producer, beside the stage;
+// instruction.  Roles, each a warp that keeps its addresses warp-uniform and lets one
+// elected lane issue (a lane on its own issued at half the rate):
+//   * two producers copy K stages of 256 columns into shared-memory rings with
+//     cp.async.bulk: one the weight tiles (17408 contiguous bytes), one the codes
+//     of the block's rows with their scales.  The rows come from L2, the weights from
+//     HBM, so the weights' ring is the deeper one;
+//   * a scale warp copies the stages' scales to tensor memory;
+//   * an issuing warp issues the stages' four K = 64 instructions into one of two FP32
+//     accumulators and commits the stages back to the producers.  It paces the
+//     kernel, so it takes two stages a turn and learns what an item is from the
+//     producer, beside the stage;
 //   * eight warps read the finished accumulator and write C while the next item
 //     is computed into the other one.
 // Every wait is bounded; the grid is persistent (static round robin).
 // Blocks of many rows run in clusters of two CTAs on neighbouring tiles of N: each
 // copies its own weights and half of the block's rows, the rows going to both CTAs
-// (multicast), since at fp4 rates the rows re-read from L2 for every 128 rows of N
-// are what an SM waits for.  A stage is then free once both CTAs have used it.
+// (multicast).  A stage is then free once both CTAs have used it.
 constexpr int kEpiWarps = 8;
-constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
-constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kWeightWarp = kEpiWarps, kRowWarp = kEpiWarps + 1, kScaleWarp = kEpiWarps + 2, kMmaWarp = kEpiWarps + 3;
+constexpr int kThreads = (kEpiWarps + 4) * 32;
 constexpr uint32_t kStop = 0xffffffffu;   // stage info: no more items
 constexpr int kMaxStages = 12;
+constexpr int kDone = 16;                // barriers of finished stages, above any ring's depth
 constexpr int kPairRows = 96;            // blocks from here on run in pairs of CTAs
 constexpr int kStgBytes = 2048;          // one epilogue warp's buffer: 16 rows x 32 columns x FP32
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kScaleCols = 24;      // tensor-memory columns of a stage's scales: 2 x (4 + 8)
+constexpr int kTurns = 16;               // scale barriers, one per turn in flight (a turn is one or two stages)
 constexpr size_t kSmemBudget = 227 * 1024;
+constexpr int kMxMaxBlockM = 208;        // two accumulators and four stages' scales fill the tensor memory
 
 struct MxPlan {
     int tok;        // rows of a block (dense: a multiple of 64)
-    int stages;     // shared-memory ring
-    int sf_slots;   // tensor-memory scale ring
-    int stage_bytes;
+    int w_stages;   // ring of weight tiles
+    int r_stages;   // ring of rows; as many scale slots in tensor memory
+    int r_bytes;    // one stage of rows: codes, then 1 KB of scales per 128 rows
     int pair;       // clusters of two CTAs
 };
 
@@ -137,78 +142,93 @@ __device__ __forceinline__ Item item_at(const MxGemmArgs& g, const MxPlan& pl, c
     return it;
 }
 
-// Accumulator columns of one epilogue warp (its 32 lanes are rows of N; warp
-// group wg takes every other slice of 16 block rows) to C, 16 x 32 values at a time through
-// the warp's buffer so that C is written in 16-byte pieces.
-__device__ __forceinline__ void drain(const MxGemmArgs& g, const MxPlan& pl, const Item& it, uint32_t acc, int wg,
-                                      int quarter, int lane, uint8_t* stg) {
-    const int esz = g.out_f32 ? 4 : 2;
+// Accumulator columns of one epilogue warp (its 32 lanes are rows of N; warp group wg
+// takes every other slice of 32 block rows) to C, through the warp's buffer so that C is
+// written in 16-byte pieces: 32 (bf16) or twice 16 (FP32) block rows of 32 columns.  Lane l
+// of rt.ids[k] holds the pair of block row 32 k + l, so nothing is loaded here.
+template <bool F32>
+__device__ __forceinline__ void drain(const MxGemmArgs& g, const MxPlan& pl, const Item& it, const Routing& rt, uint32_t acc,
+                                      int wg, int quarter, int lane, uint8_t* stg) {
+    constexpr int kEsz = F32 ? 4 : 2, kPer = 16 / kEsz, kPieces = 32 / kPer;   // pieces of a block row's 32 columns
+    constexpr int kHalf = F32 ? 16 : 32;                                       // block rows per pass
     const int n0 = it.nt * kMxTileRows + quarter * 32;
-    const bool wide = (int64_t)g.N * esz % 16 == 0;
-    const int per = 16 / esz, pieces = 32 / per;
+    if (n0 >= g.N) return;
+    const bool wide = (int64_t)g.N * kEsz % 16 == 0;
     const uint32_t sbase = smem_u32(stg);
-    for (int j0 = wg * 16; j0 < it.rows; j0 += 32) {
-        int32_t mine = -1;   // C row of block row j0 + lane
-        if (lane < 16) {
-            const int64_t r = it.b * pl.tok + j0 + lane;
-            if (!g.sorted_ids) {
-                if (r < g.a_rows) mine = (int32_t)r;
-            } else if (j0 + lane < pl.tok) {
-                const int32_t id = g.sorted_ids[r];
-                if (id >= 0 && id < g.num_pairs) mine = id;
-            }
+#pragma unroll
+    for (int k = 0; k < 7; ++k) {
+        if ((k & 1) != wg || 32 * k >= it.rows) continue;
+        int32_t mine;   // C row of block row 32 k + lane, -1: none
+        if (g.sorted_ids) {
+            mine = rt.ids[k] >= 0 && rt.ids[k] < g.num_pairs ? rt.ids[k] : -1;
+        } else {
+            const int64_t r = it.b * pl.tok + 32 * k + lane;
+            mine = 32 * k + lane < pl.tok && r < g.a_rows ? (int32_t)r : -1;
         }
-        uint32_t v[16];
-        tc5::ld16(acc + ((uint32_t)(quarter * 32) << 16) + j0, v);
+        uint32_t v[2][16];
+        const uint32_t at = acc + ((uint32_t)(quarter * 32) << 16) + 32 * k;
+        tc5::ld16(at, v[0]);
+        if (32 * k + 16 < it.rows) tc5::ld16(at + 16, v[1]);
         tc5::wait_ld();
-        if (n0 >= g.N) continue;
         if (!wide) {
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
+            for (int u = 0; u < 32; ++u) {
                 const int32_t p = __shfl_sync(0xffffffffu, mine, u);
-                if (p < 0 || n0 + lane >= g.N) continue;
+                if (p < 0 || 32 * k + u >= it.rows || n0 + lane >= g.N) continue;
                 const int64_t o = (int64_t)p * g.N + n0 + lane;
-                if (g.out_f32)
-                    static_cast<float*>(g.C)[o] = __uint_as_float(v[u]);
+                if (F32)
+                    static_cast<float*>(g.C)[o] = __uint_as_float(v[u >> 4][u & 15]);
                 else
-                    static_cast<__nv_bfloat16*>(g.C)[o] = __float2bfloat16_rn(__uint_as_float(v[u]));
+                    static_cast<__nv_bfloat16*>(g.C)[o] = __float2bfloat16_rn(__uint_as_float(v[u >> 4][u & 15]));
             }
             continue;
         }
 #pragma unroll
-        for (int u = 0; u < 16; ++u) {
-            const uint32_t at = sbase + (uint32_t)((u * 32 + lane) * esz);
-            if (g.out_f32)
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(v[u]) : "memory");
-            else
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(at),
-                             "h"(__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[u]))))
+        for (int h = 0; h < 32 / kHalf; ++h) {
+            if (32 * k + h * kHalf >= it.rows) continue;
+#pragma unroll
+            for (int u = 0; u < kHalf; ++u) {
+                const uint32_t x = v[(h * kHalf + u) >> 4][u & 15];
+                const uint32_t to = sbase + (uint32_t)((u * 32 + lane) * kEsz);
+                if (F32)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(x) : "memory");
+                else
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(to),
+                                 "h"(__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(x))))
+                                 : "memory");
+            }
+            __syncwarp();
+            uint4 w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[q].x), "=r"(w[q].y), "=r"(w[q].z), "=r"(w[q].w)
+                             : "r"(sbase + (uint32_t)((q * 32 + lane) * 16))
                              : "memory");
+            const int c = n0 + (lane % kPieces) * kPer;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int u = h * kHalf + (q * 32 + lane) / kPieces;
+                const int32_t p = __shfl_sync(0xffffffffu, mine, u);
+                // N is a multiple of kPer here, so a piece lies wholly inside or outside
+                if (p >= 0 && 32 * k + u < it.rows && c < g.N)
+                    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.C) + ((int64_t)p * g.N + c) * kEsz) = w[q];
+            }
+            __syncwarp();
         }
-        __syncwarp();
-        for (int q = lane; q < 16 * pieces; q += 32) {
-            const int u = q / pieces, c = n0 + (q % pieces) * per;
-            const int32_t p = __shfl_sync(0xffffffffu, mine, u);
-            uint4 w;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                         : "r"(sbase + (uint32_t)(q * 16))
-                         : "memory");
-            // N is a multiple of `per` here, so a piece lies wholly inside or outside
-            if (p >= 0 && c < g.N)
-                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(g.C) + ((int64_t)p * g.N + c) * esz) = w;
-        }
-        __syncwarp();
     }
 }
 
 __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g, const MxPlan pl) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* stg = smem + pl.stages * pl.stage_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(stg + kEpiWarps * kStgBytes);
-    uint64_t* empty = full + pl.stages;
-    uint64_t* acc_full = empty + pl.stages;
+    uint8_t* ring_r = smem + pl.w_stages * kMxTileBytes;
+    uint8_t* stg = ring_r + pl.r_stages * pl.r_bytes;
+    uint64_t* full_w = reinterpret_cast<uint64_t*>(stg + kEpiWarps * kStgBytes);
+    uint64_t* full_r = full_w + kMaxStages;
+    uint64_t* done = full_r + kMaxStages;      // stage g's instructions: barrier g mod kDone
+    uint64_t* turn_full = done + kDone;
+    uint64_t* acc_full = turn_full + kTurns;
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] row blocks, [1] abort, [2] skip
@@ -218,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = pl.pair ? tc5::cluster_rank() : 0u;
-    if (warp == kProducerWarp) tc5::alloc(tmem_slot, kTmemCols);
+    if (warp == kMmaWarp) tc5::alloc(tmem_slot, kTmemCols);
     pdl_wait();   // before the first access to global memory
     if (warp == 0) {
         const bool oka = mx_header_ok_warp(g.a, g.a_groups, g.a_rows, g.K), okw = mx_header_ok_warp(g.w, g.E, g.N, g.K);
@@ -237,10 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             flags[0] = (int)blocks;
             flags[1] = 0;
             flags[2] = ok ? 0 : 1;
-            for (int s = 0; s < pl.stages; ++s) {
-                mbar_init(&full[s], 1);
-                mbar_init(&empty[s], pl.pair ? 2 : 1);   // the CTAs that read the stage's rows
+            for (int s = 0; s < kMaxStages; ++s) {
+                mbar_init(&full_w[s], 1);
+                mbar_init(&full_r[s], 1);
             }
+            for (int s = 0; s < kDone; ++s) mbar_init(&done[s], pl.pair ? 2 : 1);   // the CTAs that read a stage's rows
+            for (int s = 0; s < kTurns; ++s) mbar_init(&turn_full[s], 1);
             for (int s = 0; s < 2; ++s) {
                 mbar_init(&acc_full[s], 1);
                 mbar_init(&acc_empty[s], kEpiWarps);
@@ -265,174 +287,217 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     Routing nxt = load_routing(g, pl, wk, first, lane);
     const int64_t art = mx_row_tiles(g.a_rows);
 
-    if (warp == kProducerWarp) {
-        tc5::Ring r;
-        int64_t issued = 0;
-        bool ok = true;
+    // Position in a ring: stage number, slot, its address and the parity of its current
+    // fill; barriers as shared-memory addresses.
+    struct Pos {
+        uint32_t g, slot, st, parity;
+    };
+    const uint32_t base_w = smem_u32(smem), base_r = smem_u32(ring_r), tok128 = (uint32_t)pl.tok * 128u;
+    const uint32_t full_w_a = smem_u32(full_w), full_r_a = smem_u32(full_r), done_a = smem_u32(done), turn_a = smem_u32(turn_full);
+    const uint32_t w_stages = (uint32_t)pl.w_stages, r_stages = (uint32_t)pl.r_stages, r_bytes = (uint32_t)pl.r_bytes;
+    auto next_w = [&](const Pos& p) {
+        return p.slot + 1 == w_stages ? Pos{p.g + 1, 0, base_w, p.parity ^ 1u}
+                                      : Pos{p.g + 1, p.slot + 1, p.st + kMxTileBytes, p.parity};
+    };
+    auto next_r = [&](const Pos& p) {
+        return p.slot + 1 == r_stages ? Pos{p.g + 1, 0, base_r, p.parity ^ 1u}
+                                      : Pos{p.g + 1, p.slot + 1, p.st + r_bytes, p.parity};
+    };
+    auto wait_full = [&](uint32_t bars, const Pos& p) { return tc5::wait(bars + p.slot * 8, p.parity, &flags[1], g.err); };
+    // the slot of stage p.g is free: the instructions of the stage a ring before are done
+    auto wait_free = [&](const Pos& p, uint32_t depth) {
+        if (p.g < depth) return true;
+        const uint32_t old = p.g - depth;
+        return tc5::wait(done_a + (old % kDone) * 8, (old / kDone) & 1u, &flags[1], g.err);
+    };
+    bool ok = true;
+
+    if (warp == kWeightWarp) {
+        Pos p{0, 0, base_w, 0};
         for (int64_t i = first; i < n_items && ok; i += wk.step) {
             const Item it = item_at(g, pl, wk, i, nxt, lane, false);
             nxt = load_routing(g, pl, wk, i + wk.step, lane);
             if (it.rows == 0) continue;
-            if (lane == 0) {
-                const uint8_t* wt = g.w + kHeaderBytes + ((int64_t)it.e * ntiles + it.nt) * kstages * kMxTileBytes;
-                // tiles of the block's rows: its own (grouped), or those of the matrix it starts in (dense)
-                const int64_t t0 = g.sorted_ids ? it.b * art : it.b * pl.tok / kMxTileRows;
-                const uint8_t* at = g.a + kHeaderBytes + t0 * kstages * kMxTileBytes;
-                const int64_t tstride = (int64_t)kstages * kMxTileBytes;
-                const int r0 = min(it.rows, kMxTileRows - it.off), r1 = it.rows - r0;
-                const uint32_t bytes = kMxTileBytes + (uint32_t)it.rows * 128u + (r1 > 0 ? 2048u : 1024u);
-                for (int ks = 0; ks < kstages; ++ks, ++issued, r.next(pl.stages)) {
-                    if (!tc5::wait(&empty[r.slot], r.phase ^ 1u, &flags[1], g.err)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* st = smem + r.slot * pl.stage_bytes;
-                    uint8_t* sb = st + kMxTileBytes;
-                    uint8_t* ss = sb + pl.tok * 128;
-                    const uint8_t* a0 = at + (int64_t)ks * kMxTileBytes;
-                    uint64_t* bar = &full[r.slot];
-                    info[r.slot] = (uint32_t)it.rows | (uint32_t)it.off << 16;
-                    mbar_arrive_expect_tx(bar, bytes);
-                    bulk_g2s(st, wt + (int64_t)ks * kMxTileBytes, kMxTileBytes, bar);
-                    if (!pl.pair) {
-                        bulk_g2s(sb, a0 + it.off * 128, (uint32_t)r0 * 128u, bar);
-                        bulk_g2s(ss, a0 + kMxCodeBytes, 1024u, bar);
-                        if (r1 > 0) {
-                            bulk_g2s(sb + r0 * 128, a0 + tstride, (uint32_t)r1 * 128u, bar);
-                            bulk_g2s(ss + 1024, a0 + tstride + kMxCodeBytes, 1024u, bar);
-                        }
-                    } else {
-                        // rows [h0, h1) and scale block `rank` of every tile touched, to both CTAs
-                        const int h0 = (int)rank * (it.rows / 2), h1 = h0 + it.rows / 2;
-                        const uint32_t so = kMxCodeBytes + rank * kMxScaleBlock;
-                        if (h0 < r0)
-                            tc5::bulk_g2s_pair(sb + h0 * 128, a0 + (it.off + h0) * 128, (uint32_t)(min(h1, r0) - h0) * 128u, bar);
-                        if (h1 > r0) {
-                            const int s0 = max(h0, r0);
-                            tc5::bulk_g2s_pair(sb + s0 * 128, a0 + tstride + (s0 - r0) * 128, (uint32_t)(h1 - s0) * 128u, bar);
-                        }
-                        tc5::bulk_g2s_pair(ss + rank * kMxScaleBlock, a0 + so, kMxScaleBlock, bar);
-                        if (r1 > 0) tc5::bulk_g2s_pair(ss + 1024 + rank * kMxScaleBlock, a0 + tstride + so, kMxScaleBlock, bar);
-                    }
+            const uint8_t* src = g.w + kHeaderBytes + ((int64_t)it.e * ntiles + it.nt) * kstages * kMxTileBytes;
+            for (int ks = 0; ks < kstages; ++ks, src += kMxTileBytes) {
+                ok = wait_free(p, w_stages);
+                if (!ok) break;
+                if (tc5::elect()) {
+                    const uint32_t bar = full_w_a + p.slot * 8;
+                    tc5::arrive_expect_tx(bar, kMxTileBytes);
+                    tc5::bulk_g2s(p.st, src, kMxTileBytes, bar);
                 }
+                __syncwarp();
+                p = next_w(p);
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        }
-        if (lane == 0 && ok && tc5::wait(&empty[r.slot], r.phase ^ 1u, &flags[1], g.err)) {
-            info[r.slot] = kStop;
-            mbar_arrive(&full[r.slot]);
-            ++issued;
-            r.next(pl.stages);
         }
         // leave only after every copy issued here has landed
-        if (lane == 0) {
-            for (int k = 0; k < pl.stages && k < issued; ++k) {
-                r.slot = r.slot == 0 ? pl.stages - 1 : r.slot - 1;
-                if (r.slot == pl.stages - 1) r.phase ^= 1u;
-                if (!mbar_wait(&full[r.slot], r.phase)) set_error(g.err, CHORD_DEV_TIMEOUT);
-            }
+        for (uint32_t k = 0; k < w_stages && p.g > 0; ++k) {
+            p = p.slot == 0 ? Pos{p.g - 1, w_stages - 1, 0, p.parity ^ 1u} : Pos{p.g - 1, p.slot - 1, 0, p.parity};
+            if (!wait_full(full_w_a, p)) break;
         }
-        __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // Slot, its address and parity; barriers as shared-memory addresses.
-        struct Pos {
-            uint32_t slot, st, parity;
-        };
-        const uint32_t base = smem_u32(smem), full_a = smem_u32(full), empty_a = smem_u32(empty);
-        const uint32_t stages = (uint32_t)pl.stages, stage_bytes = (uint32_t)pl.stage_bytes, tok128 = (uint32_t)pl.tok * 128u;
-        auto next = [&](Pos p) {
-            return p.slot + 1 == stages ? Pos{0, base, p.parity ^ 1u} : Pos{p.slot + 1, p.st + stage_bytes, p.parity};
-        };
-        const uint32_t sf_base = tmem + 2u * (uint32_t)pl.tok, sf_end = sf_base + (uint32_t)pl.sf_slots * 24u;
-        const bool sf_short = pl.sf_slots < pl.stages;
-        Pos p{0, base, 0};
-        uint32_t nitem = 0, g_stage = 0, sfa = sf_base;
-        uint32_t last_bar = 0, last_parity = 0;
-        bool ok = true;
-        while (ok) {
-            if (!tc5::wait(full_a + p.slot * 8, p.parity, &flags[1], g.err)) break;
-            const uint32_t inf = __shfl_sync(0xffffffffu, info[p.slot], 0);
-            if (inf == kStop) break;
-            const uint32_t rows = inf & 0xffffu, off = inf >> 16, buf = nitem & 1u;
-            if (!tc5::wait(smem_u32(&acc_empty[buf]), ((nitem >> 1) & 1u) ^ 1u, &flags[1], g.err)) break;
-            tc5::fence_after();
-            const uint32_t acc = tmem + buf * (uint32_t)pl.tok;
-            const uint32_t id0 = tc5::idesc_mxf4((int)rows, 0), id2 = tc5::idesc_mxf4((int)rows, 2);
-            const bool two = off + rows > (uint32_t)kMxTileRows;
-            // One stage: scales of its two 128-column halves to the slot's columns, then its
-            // instructions.  (A slot is reused only after the instructions that read it.)
-            auto stage = [&](const Pos& q, uint32_t sf, int ks) {
-                const uint64_t dsa = tc5::desc_scales(q.st + kMxCodeBytes);
-                const uint64_t dsb = tc5::desc_scales(q.st + kMxTileBytes + tok128);
-                const uint64_t da = tc5::desc_sw128(q.st), db = tc5::desc_sw128(q.st + kMxTileBytes);
-                const int nk = min(4, (g.K - ks * kMxTileCols + 63) / 64);
-#pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {
-                    tc5::cp_scales(sf + 4u * h, dsa + h * (kMxScaleBlock >> 4));
-                    tc5::cp_scales(sf + 8u + 8u * h, dsb + h * (kMxScaleBlock >> 4));
-                    if (two) tc5::cp_scales(sf + 12u + 8u * h, dsb + (1024u >> 4) + h * (kMxScaleBlock >> 4));
-                }
-#pragma unroll
-                for (uint32_t kk = 0; kk < 4; ++kk)
-                    if ((int)kk < nk)
-                        tc5::mma_mxf4(acc, da + 2u * kk, db + 2u * kk, kk & 1 ? id2 : id0, sf + 4u * (kk >> 1),
-                                      sf + 8u + 8u * (kk >> 1) + (off >> 5), ks > 0 || kk > 0 ? 1u : 0u);
-                if (pl.pair)
-                    tc5::commit_pair(empty_a + q.slot * 8);
-                else
-                    tc5::commit(empty_a + q.slot * 8);
-                if (ks == kstages - 1) tc5::commit(smem_u32(&acc_full[buf]));
-            };
-            // instructions of the stage that used this stage's scale slot are done
-            auto sf_free = [&](uint32_t st) {
-                if (!sf_short || st < (uint32_t)pl.sf_slots) return true;
-                const uint32_t old = st - (uint32_t)pl.sf_slots;
-                return tc5::wait(empty_a + (old % stages) * 8, (old / stages) & 1u, &flags[1], g.err);
-            };
-            for (int ks = 0; ks < kstages; ks += 2) {
-                const bool second = ks + 1 < kstages;
-                const Pos q = next(p);
-                const uint32_t sfb = sfa + 24u == sf_end ? sf_base : sfa + 24u;
-                ok = (ks == 0 || tc5::wait(full_a + p.slot * 8, p.parity, &flags[1], g.err)) && sf_free(g_stage);
-                if (!sf_short) ok = ok && (!second || tc5::wait(full_a + q.slot * 8, q.parity, &flags[1], g.err));
+    } else if (warp == kRowWarp) {
+        Pos p{0, 0, base_r, 0};
+        for (int64_t i = first; i < n_items && ok; i += wk.step) {
+            const Item it = item_at(g, pl, wk, i, nxt, lane, false);
+            nxt = load_routing(g, pl, wk, i + wk.step, lane);
+            if (it.rows == 0) continue;
+            // tiles of the block's rows: its own (grouped), or those of the matrix it starts in (dense)
+            const int64_t t0 = g.sorted_ids ? it.b * art : it.b * pl.tok / kMxTileRows;
+            const int64_t tstride = (int64_t)kstages * kMxTileBytes;
+            const uint8_t* src = g.a + kHeaderBytes + t0 * tstride;
+            const int rows = it.rows, r0 = min(rows, kMxTileRows - it.off), r1 = rows - r0;
+            const uint32_t bytes = (uint32_t)rows * 128u + (r1 > 0 ? 2048u : 1024u);
+            // a pair's CTA copies rows [h0, h1) and scale block `rank` of every tile touched
+            const int h0 = pl.pair ? (int)rank * (rows / 2) : 0, h1 = pl.pair ? h0 + rows / 2 : rows;
+            const int a0 = min(h0, r0), a1 = min(h1, r0), b0 = max(h0, r0), b1 = max(h1, r0);   // in the first, second tile
+            const uint32_t inf = (uint32_t)rows | (uint32_t)it.off << 16;
+            for (int ks = 0; ks < kstages; ++ks, src += kMxTileBytes) {
+                ok = wait_free(p, r_stages);
                 if (!ok) break;
-                if (!sf_short) {
-                    if (tc5::elect()) {
-                        stage(p, sfa, ks);
-                        if (second) stage(q, sfb, ks + 1);
-                    }
-                } else {
-                    if (tc5::elect()) stage(p, sfa, ks);
-                    __syncwarp();
-                    if (second) {
-                        ok = tc5::wait(full_a + q.slot * 8, q.parity, &flags[1], g.err) && sf_free(g_stage + 1);
-                        if (!ok) break;
-                        if (tc5::elect()) stage(q, sfb, ks + 1);
+                if (tc5::elect()) {
+                    const uint32_t bar = full_r_a + p.slot * 8, ss = p.st + tok128;
+                    info[p.slot] = inf;
+                    tc5::arrive_expect_tx(bar, bytes);
+                    if (!pl.pair) {
+                        tc5::bulk_g2s(p.st, src + it.off * 128, (uint32_t)r0 * 128u, bar);
+                        tc5::bulk_g2s(ss, src + kMxCodeBytes, 1024u, bar);
+                        if (r1 > 0) {
+                            tc5::bulk_g2s(p.st + r0 * 128, src + tstride, (uint32_t)r1 * 128u, bar);
+                            tc5::bulk_g2s(ss + 1024, src + tstride + kMxCodeBytes, 1024u, bar);
+                        }
+                    } else {
+                        const uint32_t so = kMxCodeBytes + rank * kMxScaleBlock;
+                        if (a1 > a0)
+                            tc5::bulk_g2s_pair(p.st + a0 * 128, src + (it.off + a0) * 128, (uint32_t)(a1 - a0) * 128u, bar);
+                        if (b1 > b0)
+                            tc5::bulk_g2s_pair(p.st + b0 * 128, src + tstride + (b0 - r0) * 128, (uint32_t)(b1 - b0) * 128u, bar);
+                        tc5::bulk_g2s_pair(ss + rank * kMxScaleBlock, src + so, kMxScaleBlock, bar);
+                        if (r1 > 0) tc5::bulk_g2s_pair(ss + 1024 + rank * kMxScaleBlock, src + tstride + so, kMxScaleBlock, bar);
                     }
                 }
                 __syncwarp();
-                last_bar = empty_a + (second ? q.slot : p.slot) * 8;
-                last_parity = second ? q.parity : p.parity;
-                g_stage += second ? 2u : 1u;
-                sfa = second ? (sfb + 24u == sf_end ? sf_base : sfb + 24u) : sfb;
-                p = second ? next(q) : q;
+                p = next_r(p);
+            }
+        }
+        if (ok && wait_free(p, r_stages)) {
+            if (tc5::elect()) {
+                info[p.slot] = kStop;
+                tc5::arrive(full_r_a + p.slot * 8);
+            }
+            __syncwarp();
+            p = next_r(p);
+        }
+        for (uint32_t k = 0; k < r_stages && p.g > 0; ++k) {
+            p = p.slot == 0 ? Pos{p.g - 1, r_stages - 1, 0, p.parity ^ 1u} : Pos{p.g - 1, p.slot - 1, 0, p.parity};
+            if (!wait_full(full_r_a, p)) break;
+        }
+    } else if (warp == kScaleWarp) {
+        // Scales of a stage's two 128-column halves to the columns of its rows' slot: 4 columns
+        // per 128 rows (and four groups), weights first.  They are free when the slot is.
+        const uint32_t sf_base = tmem + 2u * (uint32_t)pl.tok;
+        Pos w{0, 0, base_w, 0}, r{0, 0, base_r, 0};
+        uint32_t turn = 0;
+        while (ok) {
+            ok = wait_full(full_r_a, r);
+            if (!ok) break;
+            const uint32_t inf = __shfl_sync(0xffffffffu, info[r.slot], 0);
+            if (inf == kStop) break;
+            const bool two = (inf >> 16) + (inf & 0xffffu) > (uint32_t)kMxTileRows;
+            for (int ks = 0; ks < kstages; ks += 2, ++turn) {
+                const Pos w2 = next_w(w), r2 = next_r(r);
+                const bool second = ks + 1 < kstages;
+                ok = wait_full(full_r_a, r) && wait_full(full_w_a, w) &&
+                     (!second || (wait_full(full_r_a, r2) && wait_full(full_w_a, w2)));
+                if (!ok) break;
+                if (tc5::elect()) {
+                    auto copy = [&](const Pos& wp, const Pos& rp) {
+                        const uint32_t sf = sf_base + rp.slot * kScaleCols;
+                        const uint64_t dsa = tc5::desc_scales(wp.st + kMxCodeBytes), dsb = tc5::desc_scales(rp.st + tok128);
+#pragma unroll
+                        for (uint32_t h = 0; h < 2; ++h) {
+                            tc5::cp_scales(sf + 4u * h, dsa + h * (kMxScaleBlock >> 4));
+                            tc5::cp_scales(sf + 8u + 8u * h, dsb + h * (kMxScaleBlock >> 4));
+                            if (two) tc5::cp_scales(sf + 12u + 8u * h, dsb + (1024u >> 4) + h * (kMxScaleBlock >> 4));
+                        }
+                    };
+                    copy(w, r);
+                    if (second) copy(w2, r2);
+                    tc5::commit(turn_a + (turn % kTurns) * 8);
+                }
+                __syncwarp();
+                w = second ? next_w(w2) : w2;
+                r = second ? next_r(r2) : r2;
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        const uint32_t sf_base = tmem + 2u * (uint32_t)pl.tok;
+        Pos w{0, 0, base_w, 0}, r{0, 0, base_r, 0};
+        uint32_t nitem = 0, turn = 0;
+        while (ok) {
+            ok = wait_full(full_r_a, r);
+            if (!ok) break;
+            const uint32_t inf = __shfl_sync(0xffffffffu, info[r.slot], 0);
+            if (inf == kStop) break;
+            const uint32_t rows = inf & 0xffffu, off = inf >> 21, buf = nitem & 1u;   // off: in 32 rows
+            ok = tc5::wait(smem_u32(&acc_empty[buf]), ((nitem >> 1) & 1u) ^ 1u, &flags[1], g.err);
+            if (!ok) break;
+            const uint32_t acc = tmem + buf * (uint32_t)pl.tok;
+            const uint32_t id0 = tc5::idesc_mxf4((int)rows, 0), id2 = tc5::idesc_mxf4((int)rows, 2);
+            for (int ks = 0; ks < kstages; ks += 2, ++turn) {
+                const Pos w2 = next_w(w), r2 = next_r(r);
+                const bool second = ks + 1 < kstages;
+                // the scale warp has waited for both stages' copies before it committed this turn
+                ok = tc5::wait(turn_a + (turn % kTurns) * 8, (turn / kTurns) & 1u, &flags[1], g.err);
+                if (!ok) break;
+                tc5::fence_after();
+                if (tc5::elect()) {
+                    auto mma = [&](const Pos& wp, const Pos& rp, int k) {
+                        const uint32_t sf = sf_base + rp.slot * kScaleCols;
+                        const uint64_t da = tc5::desc_sw128(wp.st), db = tc5::desc_sw128(rp.st);
+                        const int nk = min(4, (g.K - k * kMxTileCols + 63) / 64);
+#pragma unroll
+                        for (uint32_t kk = 0; kk < 4; ++kk)
+                            if ((int)kk < nk)
+                                tc5::mma_mxf4(acc, da + 2u * kk, db + 2u * kk, kk & 1 ? id2 : id0, sf + 4u * (kk >> 1),
+                                              sf + 8u + 8u * (kk >> 1) + off, k > 0 || kk > 0 ? 1u : 0u);
+                        const uint32_t bar = done_a + (wp.g % kDone) * 8;
+                        if (pl.pair)
+                            tc5::commit_pair(bar);
+                        else
+                            tc5::commit(bar);
+                    };
+                    mma(w, r, ks);
+                    if (second) mma(w2, r2, ks + 1);
+                    if (ks + 2 >= kstages) tc5::commit(smem_u32(&acc_full[buf]));
+                }
+                __syncwarp();
+                w = second ? next_w(w2) : w2;
+                r = second ? next_r(r2) : r2;
             }
             ++nitem;
         }
         // the last instructions are done before the tensor memory is released
-        if (last_bar) tc5::wait(last_bar, last_parity, &flags[1], g.err);
+        if (w.g > 0) tc5::wait(done_a + ((w.g - 1) % kDone) * 8, ((w.g - 1) / kDone) & 1u, &flags[1], g.err);
         __syncwarp();
     } else {
         const int wg = warp >> 2, quarter = warp & 3;
         int64_t nitem = 0;
         for (int64_t i = first; i < n_items; i += wk.step) {
-            const Item it = item_at(g, pl, wk, i, nxt, lane, warp == 0);
+            const Routing cur = nxt;
+            const Item it = item_at(g, pl, wk, i, cur, lane, warp == 0);
             nxt = load_routing(g, pl, wk, i + wk.step, lane);
             if (it.rows == 0) continue;
             const int buf = (int)(nitem & 1);
             if (!tc5::wait<true>(&acc_full[buf], (uint32_t)((nitem >> 1) & 1), &flags[1], g.err)) break;
             tc5::fence_after();
-            if (it.write) drain(g, pl, it, tmem + (uint32_t)(buf * pl.tok), wg, quarter, lane, stg + warp * kStgBytes);
+            if (it.write) {
+                const uint32_t acc = tmem + (uint32_t)(buf * pl.tok);
+                if (g.out_f32)
+                    drain<true>(g, pl, it, cur, acc, wg, quarter, lane, stg + warp * kStgBytes);
+                else
+                    drain<false>(g, pl, it, cur, acc, wg, quarter, lane, stg + warp * kStgBytes);
+            }
             tc5::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[buf]);
@@ -443,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     __syncthreads();
     if (pl.pair) tc5::cluster_sync();   // the other CTA's copies and commits into this one are done
     tc5::fence_after();
-    if (warp == kProducerWarp) tc5::dealloc(tmem, kTmemCols);
+    if (warp == kMmaWarp) tc5::dealloc(tmem, kTmemCols);
 }
 
 cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
@@ -451,16 +516,21 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
     // Dense blocks: 192 rows (two accumulators and the scales fill the tensor
     // memory), fewer when the matrix is shorter.
     pl.tok = g.sorted_ids ? (int)g.a_rows : (g.a_rows > 128 ? 192 : (g.a_rows > 64 ? 128 : 64));
-    const int tiles = (pl.tok + 64 + kMxTileRows - 1) / kMxTileRows;   // row tiles a block may touch
-    pl.stage_bytes = kMxTileBytes + pl.tok * 128 + 1024 * tiles;
-    const size_t fixed = 1024 + kEpiWarps * kStgBytes + 128 + 4 * kMaxStages;
-    pl.stages = (int)((kSmemBudget - fixed) / (pl.stage_bytes + 16));
-    if (pl.stages > kMaxStages) pl.stages = kMaxStages;
-    if (pl.stages < 2) return cudaErrorInvalidConfiguration;
-    pl.sf_slots = (int)((kTmemCols - 2 * pl.tok) / 24);
-    if (pl.sf_slots > pl.stages) pl.sf_slots = pl.stages;
-    // one CTA per SM: it takes the whole tensor memory (the ring is larger than half the shared memory)
-    const size_t smem = fixed + (size_t)pl.stages * (pl.stage_bytes + 16);
+    // 128-row tiles a block may touch (dense blocks of 192 start at row 0 or 64 of one)
+    const int tiles = (pl.tok + kMxTileRows - 1) / kMxTileRows;
+    pl.r_bytes = pl.tok * 128 + 1024 * tiles;
+    const size_t fixed = 1024 + kEpiWarps * kStgBytes + (2 * kMaxStages + kDone + kTurns + 4) * 8 + 64 + 4 * kMaxStages;
+    const size_t room = kSmemBudget - fixed;
+    // Large blocks: four stages of rows (two turns), the rest for weights; small ones: as many of each.
+    pl.r_stages = 4;
+    if (pl.tok < kPairRows) pl.r_stages = (int)(room / (kMxTileBytes + pl.r_bytes));
+    const int slots = (int)((kTmemCols - 2 * pl.tok) / kScaleCols);
+    pl.r_stages = pl.r_stages > slots ? slots : (pl.r_stages > kMaxStages ? kMaxStages : pl.r_stages);
+    pl.w_stages = (int)((room - (size_t)pl.r_stages * pl.r_bytes) / kMxTileBytes);
+    if (pl.w_stages > kMaxStages) pl.w_stages = kMaxStages;
+    if (pl.r_stages < 2 || pl.w_stages < 2) return cudaErrorInvalidConfiguration;
+    // one CTA per SM: it takes the whole tensor memory, and more than half of the shared memory
+    const size_t smem = fixed + (size_t)pl.w_stages * kMxTileBytes + (size_t)pl.r_stages * pl.r_bytes;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(mx_gemm_kernel), kSmemBudget);
     if (e != cudaSuccess) return e;
     const int64_t ntiles = (g.N + kMxTileRows - 1) / kMxTileRows;
@@ -493,8 +563,6 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int kMxMaxBlockM = 224;
-
 // After a call in validate mode: wait for it and turn the error word into a status.
 chord_status mx_finish(const chord_opts* o, cudaStream_t st) {
     if (cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;
@@ -519,8 +587,9 @@ int chord_mxfp4_select_block_m(int T, int topk, int E_local, int E_global) {
     // rows that an expert rarely exceeds (mean + 3 sd of a Poisson count), in
     // as few equal blocks as the kernel's largest allows
     const double need = tok_e + 3.0 * sqrt(tok_e) + 1.0;
-    const double blocks = ceil(need / kMxMaxBlockM);
-    const int bm = (int)ceil(need / blocks / 32.0) * 32;
+    // a second block streams the expert's weights again: the few experts above mean + 2 sd may take one
+    const double blocks = ceil((tok_e + 2.0 * sqrt(tok_e) + 1.0) / kMxMaxBlockM);
+    const int bm = (int)ceil(need / blocks / 16.0) * 16;
     return bm > kMxMaxBlockM ? kMxMaxBlockM : bm;
 }
 
@@ -529,7 +598,7 @@ chord_status chord_mxfp4_moe_gemm(const void* Aq, size_t aq_bytes, const void* p
                                   const int32_t* num_tokens_padded, int64_t capacity, int block_m, int64_t num_pairs,
                                   void* C, int c_dtype, const chord_opts* opts, void* stream) {
     if (E <= 0 || N <= 0 || K <= 0 || block_m <= 0 || capacity < 0 || num_pairs < 0) return CHORD_ERR_INVALID_ARG;
-    if (K % kGroup || block_m % 32 || block_m > kMxMaxBlockM || num_pairs >= INT32_MAX || capacity >= INT32_MAX)
+    if (K % kGroup || block_m % 16 || block_m > kMxMaxBlockM || num_pairs >= INT32_MAX || capacity >= INT32_MAX)
         return CHORD_ERR_UNSUPPORTED;
     if (capacity % block_m || (c_dtype != CHORD_DTYPE_BF16 && c_dtype != CHORD_DTYPE_F32)) return CHORD_ERR_INVALID_ARG;
     if (packed_bytes != chord_mxfp4_bytes(E, N, K) || aq_bytes != chord_mxfp4_rows_bytes(capacity, block_m, K))

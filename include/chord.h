@@ -532,8 +532,10 @@ chord_status chord_mxfp4_quantize(const void *src, int src_dtype, int64_t row_st
                                   int64_t mat_stride, int64_t G, int64_t N, int K, void *packed,
                                   size_t packed_bytes, void *stream);
 
-/* Bytes of the quantised routed rows of a call (one group of block_m rows per
- * align block): chord_mxfp4_bytes(capacity / block_m, block_m, K). */
+/* Bytes of the quantised routed rows of a call: chord_mxfp4_bytes(capacity / block_m,
+ * block_m, K) (one group of block_m rows per align block) and, after them, four per
+ * position (rounded up to 256) in which chord_mxfp4_quantize_rows keeps where each
+ * pair's row goes. */
 size_t chord_mxfp4_rows_bytes(int64_t capacity, int block_m, int K);
 
 /* Quantise activation rows into the order of chord_moe_align's sorted_ids, the

@@ -100,7 +100,7 @@ def test_sizes():
     assert chord.chord_mxfp4_bytes(0, 5, 32) == chord.chord_mxfp4_bytes(2, 0, 32) == 256
     for bad in [(1, 1, 0), (1, 1, 33), (-1, 1, 32), (1, -1, 32)]:
         assert chord.chord_mxfp4_bytes(*bad) == 0
-    assert chord.chord_mxfp4_rows_bytes(96, 32, 64) == chord.chord_mxfp4_bytes(3, 32, 64)
+    assert chord.chord_mxfp4_rows_bytes(96, 32, 64) == chord.chord_mxfp4_bytes(3, 32, 64) + 512
     assert chord.chord_mxfp4_rows_bytes(95, 32, 64) == 0
 
 
@@ -378,6 +378,35 @@ def test_grouped_product(T, E, topk, N, K, bm, div, dtype):
         av = xv[rows // div]
         ref = av @ wv.T
         check(C[torch.from_numpy(rows).to(DEV)], ref, bound(av, wv, K), f"expert {ex}")
+
+
+@gpu
+@pytest.mark.parametrize("topk", [3, 17, 40])
+def test_quantised_rows_of_shared_tokens(topk):
+    """Rows shared by many pairs, some without a position; and routing arrays
+    that name a few pairs of many.  Every routed position holds its row."""
+    need_gpu()
+    T, E, K, bm = 9, 50, 352, 16
+    g = torch.Generator().manual_seed(topk)
+    x = torch.randn(T, K, generator=g)
+    c, b = ref_quantise(x.double().numpy())
+    ids = torch.rand(T, E, generator=g).argsort(dim=1)[:, :topk].to(torch.int32)
+    ids[torch.rand(T, topk, generator=g) < 0.3] = -1
+    s, e, n = align(ids.to(DEV), E, bm)
+    few = torch.full((32,), T * topk, dtype=torch.int32, device=DEV)       # 32 positions, up to 360 pairs
+    few[:5] = torch.tensor([0, topk, 2 * topk + 1, 4 * topk, T * topk - 1], dtype=torch.int32)
+    few[16] = 3 * topk + 2
+    for order, cnt in ((s, n), (few, torch.tensor([32], dtype=torch.int32, device=DEV))):
+        xq = torch.full((chord.chord_mxfp4_rows_bytes(order.numel(), bm, K),), 0x11, dtype=torch.uint8, device=DEV)
+        chord.chord_mxfp4_quantize_rows(x.to(DEV), topk, order, cnt, bm, T * topk, xq)
+        assert chord.chord_get_device_error() == 0
+        G = order.numel() // bm
+        gc, gb = unpack(xq[:chord.chord_mxfp4_bytes(G, bm, K)], G, bm, K)
+        pos = order[:int(cnt)].cpu().numpy()
+        at = np.nonzero(pos < T * topk)[0]
+        assert at.size
+        np.testing.assert_array_equal(gc.reshape(-1, K)[at], c[pos[at] // topk])
+        np.testing.assert_array_equal(gb.reshape(-1, K // 32)[at], b[pos[at] // topk])
 
 
 @gpu

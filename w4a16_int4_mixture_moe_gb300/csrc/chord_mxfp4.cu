@@ -234,6 +234,109 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int
     }
 }
 
+// Where each pair's row goes, for rows that several pairs share: index[p] = the position of
+// pair p in sorted_ids.  Entries of pairs without a position are not written; a reader
+// checks sorted_ids[index[p]] == p.
+__global__ void __launch_bounds__(256) mx_index_kernel(const RowSource s, int64_t G, int64_t N, int K,
+                                                       uint8_t* __restrict__ packed, int32_t* __restrict__ index, int* err) {
+    pdl_trigger();
+    if (blockIdx.x == 0 && threadIdx.x < kHeaderBytes / 4) mx_write_header(packed, threadIdx.x, G, N, K);
+    const int64_t ntp = *s.ntp;
+    if (ntp < 0 || ntp > G * N || ntp % N) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) set_error(err, CHORD_DEV_BAD_PADDED);
+        return;
+    }
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < ntp; i += (int64_t)gridDim.x * blockDim.x) {
+        const int32_t id = __ldg(s.sorted_ids + i);
+        if (id >= 0 && id < s.id_limit) index[id] = (int32_t)i;
+    }
+}
+
+// Activation rows shared by `divisor` pairs (a token's experts): a row is loaded and
+// quantised once and stored at each of its pairs' positions.  One warp, kRows rows,
+// `run` tiles along K; lane k keeps where pair k of a row goes.  (A warp per position
+// quantised every row `divisor` times: 1024 rows of 7168 for eight experts each took 45 us.)
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(256) mx_quantize_shared_kernel(const RowSource s, int64_t a_rows, int64_t G, int64_t N, int K,
+                                                                 int run, uint8_t* __restrict__ packed,
+                                                                 const int32_t* __restrict__ index) {
+    pdl_trigger();
+    pdl_wait();   // the index
+    constexpr int kRows = 2;
+    const int64_t ntp = *s.ntp;
+    if (ntp < 0 || ntp > G * N || ntp % N) return;   // reported by the index kernel
+    const int kb = (int)mx_col_tiles(K), rt = (int)mx_row_tiles(N), runs = (kb + run - 1) / run;
+    const int lane = threadIdx.x & 31;
+    const uint32_t j = lane >> 2;
+    const int64_t groups = (a_rows + kRows - 1) / kRows, tasks = groups * runs;
+    uint8_t* data = packed + kHeaderBytes;
+    for (int64_t q = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; q < tasks;
+         q += ((int64_t)gridDim.x * blockDim.x) >> 5) {
+        int part;
+        const int64_t row0 = divmod_idx(q, runs, part) * kRows;
+        const int kt0 = part * run, kt1 = min(kt0 + run, kb);
+        Raw<F32> cur[kRows] = {}, nxt[kRows];
+        auto fetch = [&](Raw<F32>(&v)[kRows], int kt) {
+            const int k0 = kt * kMxTileCols + lane * 8;
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                v[i] = Raw<F32>{};
+                if (row0 + i < a_rows && k0 < K) load8<F32, VEC>(s.src, (row0 + i) * s.row_stride + k0, v[i]);
+            }
+        };
+        // pairs 32 at a time (a row is read again for each such group; 32 experts a token is
+        // far above common use)
+        for (int first = 0; first < s.divisor; first += 32) {
+            uint64_t to[kRows];   // the pair's row in its block's first tile, row mod 8 in the low bits
+            uint32_t on[kRows];   // pairs of this group that have a position
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int64_t p = (row0 + i) * s.divisor + first + lane;
+                int64_t pos = -1;
+                if (row0 + i < a_rows && first + lane < s.divisor && p < s.id_limit) {
+                    pos = index[p];
+                    if (pos < 0 || pos >= ntp || __ldg(s.sorted_ids + pos) != (int32_t)p) pos = -1;
+                }
+                on[i] = __ballot_sync(0xffffffffu, pos >= 0);
+                int r = 0;
+                const int64_t blk = pos >= 0 ? divmod_idx(pos, (int)N, r) : 0;
+                to[i] = (uint64_t)((blk * rt + (r >> 7)) * kb) * kMxTileBytes << 7 | (uint32_t)(r & 127);
+            }
+            fetch(cur, kt0);
+            for (int kt = kt0; kt < kt1; ++kt) {
+                if (kt + 1 < kt1) fetch(nxt, kt + 1);
+                const bool in_k = kt * kMxTileCols + lane * 8 < K;
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    if (!on[i]) continue;
+                    uint32_t b;
+                    const uint32_t codes = quantize8<F32>(cur[i], b);
+                    uint32_t w = (in_k ? b : 127u) << (8 * (j & 3));
+                    w |= __shfl_xor_sync(0xffffffffu, w, 4);
+                    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+                    uint8_t* tile = data + (int64_t)kt * kMxTileBytes;
+                    for (uint32_t m = on[i]; m; m &= m - 1) {
+                        const uint64_t d = __shfl_sync(0xffffffffu, to[i], __ffs(m) - 1);
+                        const uint32_t r = (uint32_t)d & 127u;
+                        *reinterpret_cast<uint32_t*>(tile + (d >> 7) + mx_code_offset(r, j) + 4 * (lane & 3)) = codes;
+                    }
+                    // scale words: lane 2 k + h stores half h of pair k, sixteen pairs at a time
+                    const uint32_t wh = __shfl_sync(0xffffffffu, w, (lane & 1) * 16);
+#pragma unroll
+                    for (int k0 = 0; k0 < 32; k0 += 16) {
+                        const uint64_t d = __shfl_sync(0xffffffffu, to[i], k0 + (lane >> 1));
+                        if (on[i] >> (k0 + (lane >> 1)) & 1u)
+                            *reinterpret_cast<uint32_t*>(tile + (d >> 7) + mx_scale_offset((uint32_t)d & 127u, 4 * (lane & 1))) = wh;
+                        if (first + 16 >= s.divisor) break;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) cur[i] = nxt[i];
+            }
+        }
+    }
+}
+
 // The same split; a lane writes the values of its eight columns of each row.
 template <bool F32>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ packed, int64_t G, int64_t N,
@@ -338,6 +441,23 @@ cudaError_t launch_quantize(const RowSource& s, int64_t G, int64_t N, int K, uin
     return cudaGetLastError();
 }
 
+// Routed rows: shared ones through the index (it has an entry per position, so room for every
+// pair id unless the caller routes a few pairs of many), others position by position.
+cudaError_t launch_quantize_rows(const RowSource& s, int64_t a_rows, int64_t G, int64_t N, int K, uint8_t* packed,
+                                 int32_t* index, int* err, cudaStream_t st) {
+    if (s.divisor == 1 || a_rows == 0 || s.id_limit > G * N) return launch_quantize(s, G, N, K, packed, err, st);
+    const int esz = s.f32 ? 4 : 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(s.src) | (a_rows > 1 ? (uintptr_t)(s.row_stride * esz) : 0)) % 16 == 0;
+    const int kb = (int)mx_col_tiles(K);
+    const int run = run_for((a_rows + 63) / 64, kb);
+    const int64_t ids = (G * N + 255) / 256, cap = (int64_t)device_info().sm_count * 8;
+    mx_index_kernel<<<(unsigned)(ids < 1 ? 1 : (ids > cap ? cap : ids)), 256, 0, st>>>(s, G, N, K, packed, index, err);
+    auto kern = s.f32 ? (vec ? mx_quantize_shared_kernel<true, true> : mx_quantize_shared_kernel<true, false>)
+                      : (vec ? mx_quantize_shared_kernel<false, true> : mx_quantize_shared_kernel<false, false>);
+    return launch_pdl(pdl_enabled(), kern, dim3(grid_for((a_rows + 1) / 2 * ((kb + run - 1) / run))), dim3(256), 0, st, s, a_rows,
+                      G, N, K, run, packed, (const int32_t*)index);
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool known_dtype(int d) { return d == CHORD_DTYPE_BF16 || d == CHORD_DTYPE_F32; }
@@ -356,7 +476,8 @@ size_t chord_mxfp4_bytes(int64_t G, int64_t N, int K) {
 
 size_t chord_mxfp4_rows_bytes(int64_t capacity, int block_m, int K) {
     if (capacity < 0 || block_m <= 0 || capacity % block_m) return 0;
-    return chord_mxfp4_bytes(capacity / block_m, block_m, K);
+    const size_t n = chord_mxfp4_bytes(capacity / block_m, block_m, K);
+    return n ? n + ((size_t)capacity * 4 + 255) / 256 * 256 : 0;   // and each pair's position
 }
 
 chord_status chord_mxfp4_quantize(const void* src, int src_dtype, int64_t row_stride, int64_t mat_stride, int64_t G,
@@ -395,8 +516,10 @@ chord_status chord_mxfp4_quantize_rows(const void* A, int a_dtype, int64_t a_row
     const int64_t limit = a_rows * (int64_t)a_row_divisor;
     RowSource s{A,         a_dtype == CHORD_DTYPE_F32, row_stride, 0, sorted_ids, num_tokens_padded,
                 limit < num_pairs ? limit : num_pairs, a_row_divisor};
-    return launch_quantize(s, capacity / block_m, block_m, K, static_cast<uint8_t*>(packed), di.err,
-                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+    uint8_t* out = static_cast<uint8_t*>(packed);
+    int32_t* index = reinterpret_cast<int32_t*>(out + chord_mxfp4_bytes(capacity / block_m, block_m, K));
+    return launch_quantize_rows(s, a_rows, capacity / block_m, block_m, K, out, index, di.err,
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? CHORD_OK
                : CHORD_ERR_CUDA;
 }

@@ -74,36 +74,38 @@ __device__ __forceinline__ void load8(const void* src, int64_t at, Raw<F32>& v) 
     }
 }
 
-// Codes of a lane's eight columns and the biased scale of their group (the
-// lane's quad).  The largest magnitude is found on the bit patterns, whose order
-// is the values' order with infinities and NaN on top.
+// Codes of a lane's eight columns and the biased scale b of their group (the lane's quad).
+// The largest magnitude is found on the bit patterns, whose order is the values' order with
+// infinities and NaN on top.  A block with one of those: b = 255, and whatever codes come out.
 template <bool F32>
 __device__ __forceinline__ uint32_t quantize8(const Raw<F32>& v, uint32_t& b) {
-    uint32_t ex;
+    uint32_t ex;   // biased exponent of the largest magnitude; 0 for zero and subnormals
     float y[8];
     if constexpr (F32) {
-        uint32_t top = 0;
+        uint32_t top = v.w[0] & 0x7fffffffu;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, v.w[i] & 0x7fffffffu);
+        for (int i = 1; i < 8; ++i) top = max(top, v.w[i] & 0x7fffffffu);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        ex = top >> 23;   // biased exponent; 0 for zero and subnormals
+        ex = top >> 23;
     } else {
-        uint32_t top = 0;
+        uint32_t top = v.w[0] & 0x7fff7fffu;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, v.w[i] & 0x7fff7fffu);
+        for (int i = 1; i < 4; ++i) top = __vmaxu2(top, v.w[i] & 0x7fff7fffu);
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
         ex = max(top >> 16, top & 0xffffu) >> 7;
     }
-    b = ex == 255u ? 255u : (ex > 2u ? ex - 2u : 0u);
-    const uint32_t up = 254u - min(b, 253u);   // exponent field of 2^(127 - b)
+    const uint32_t e = max(ex, 2u) - 2u;
+    const uint32_t up = 254u - e;   // exponent field of 2^(127 - e)
+    b = ex == 255u ? 255u : e;
     if constexpr (F32) {
+        const float f = __uint_as_float(up << 23);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(v.w[i]) * __uint_as_float(up << 23);
+        for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(v.w[i]) * f;
     } else {
         // exact: a power of two; what falls below bf16's range has code 0
-        const __nv_bfloat162 f = u32_as_bf2(up << 7 | up << 23);
+        const __nv_bfloat162 f = u32_as_bf2(up * 0x00800080u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t p = bf2_as_u32(__hmul2(u32_as_bf2(v.w[i]), f));
@@ -111,7 +113,7 @@ __device__ __forceinline__ uint32_t quantize8(const Raw<F32>& v, uint32_t& b) {
             y[2 * i + 1] = __uint_as_float(p & 0xffff0000u);
         }
     }
-    return b == 255u ? 0u : e2m1_codes8(y);
+    return e2m1_codes8(y);
 }
 
 // Where the rows of a packed matrix come from: row i of group g is row
@@ -151,7 +153,8 @@ __device__ __forceinline__ void mx_write_header(uint8_t* packed, int i, int64_t 
 // over a run of `run` tiles along K, the next tile's loads in flight while one is
 // converted.  A lane holds eight columns of each row: a group of 32 columns is
 // four lanes, its largest magnitude two shuffles, a row's codes one 128-byte store.
-template <bool F32, bool VEC>
+// ROUTED: the rows of a routing array's positions (those without a pair are skipped).
+template <bool F32, bool VEC, bool ROUTED>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int64_t G, int64_t N, int K, int run,
                                                           uint8_t* __restrict__ packed, int* err) {
     pdl_trigger();   // a product that follows sets itself up meanwhile
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int
     const int kb = (int)mx_col_tiles(K);
     const int runs = (kb + run - 1) / run;
     int64_t groups = G;
-    if (s.ntp) {
+    if (ROUTED) {
         const int64_t ntp = *s.ntp;
         if (ntp < 0 || ntp > G * N || ntp % N) {
             if (blockIdx.x == 0 && threadIdx.x == 0) set_error(err, CHORD_DEV_BAD_PADDED);
@@ -179,57 +182,62 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int
         const int64_t band = divmod_idx(q >> 5, runs, part);
         const int64_t g = divmod_idx(band, (int)rt, bt);
         const int kt0 = part * run, kt1 = min(kt0 + run, kb);
-        int64_t at[4];   // first element of the row, -1: none
+        int64_t at[4];   // first element of the row
         uint32_t live = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t row = (int64_t)bt * kMxTileRows + r0 + 32 * i;
-            at[i] = -1;
+            at[i] = 0;
             if (row < N) {
-                if (!s.sorted_ids) {
+                if (!ROUTED) {
                     at[i] = g * s.mat_stride + row * s.row_stride;
+                    live |= 1u << i;
                 } else {
                     const int32_t id = __ldg(s.sorted_ids + g * N + row);
-                    if (id >= 0 && id < s.id_limit) at[i] = (int64_t)((uint32_t)id / (uint32_t)s.divisor) * s.row_stride;
+                    if (id >= 0 && id < s.id_limit) {
+                        at[i] = (int64_t)((uint32_t)id / (uint32_t)s.divisor) * s.row_stride;
+                        live |= 1u << i;
+                    }
                 }
             }
-            if (at[i] >= 0) live |= 1u << i;
         }
-        if (s.sorted_ids && !live) continue;
-        Raw<F32> cur[4] = {}, nxt[4];
+        if (ROUTED && !live) continue;
+        Raw<F32> cur[4] = {}, nxt[4] = {};
         auto fetch = [&](Raw<F32>(&v)[4], int kt) {
             const int k0 = kt * kMxTileCols + lane * 8;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = Raw<F32>{};
-                if (at[i] >= 0 && k0 < K) load8<F32, VEC>(s.src, at[i] + k0, v[i]);
-            }
+            for (int i = 0; i < 4; ++i)   // a row's last columns past K stay zero: in the last tile only
+                if (live >> i & 1u) {
+                    if (k0 < K)
+                        load8<F32, VEC>(s.src, at[i] + k0, v[i]);
+                    else
+                        v[i] = Raw<F32>{};
+                }
         };
         fetch(cur, kt0);
         uint8_t* t = data + (band * kb + kt0) * kMxTileBytes;
         for (int kt = kt0; kt < kt1; ++kt, t += kMxTileBytes) {
             if (kt + 1 < kt1) fetch(nxt, kt + 1);
             const bool in_k = kt * kMxTileCols + lane * 8 < K;
-            uint32_t sc[4];
+            uint32_t col = 0x7F7F7F7Fu;   // this group's scales of the four rows; padding: 1
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                // padding: zeros with scale 1 (the same rows for the whole warp)
-                const bool row_in = (live >> i & 1u) != 0;
-                uint32_t codes = 0, w = 0x7F7F7F7Fu;
-                if (row_in) {
+                if (!ROUTED || (live >> i & 1u)) {
                     uint32_t b;
-                    codes = quantize8<F32>(cur[i], b);
-                    w = (in_k ? b : 127u) << (8 * (j & 3));
-                    w |= __shfl_xor_sync(0xffffffffu, w, 4);
-                    w |= __shfl_xor_sync(0xffffffffu, w, 8);
+                    const uint32_t codes = quantize8<F32>(cur[i], b);
+                    if (in_k && (live >> i & 1u)) col = (col & ~(255u << (8 * i))) | b << (8 * i);
+                    *reinterpret_cast<uint32_t*>(t + mx_code_offset(r0 + 32 * i, j) + 4 * (lane & 3)) = codes;
                     cur[i] = nxt[i];
                 }
-                if (!s.sorted_ids || row_in)
-                    *reinterpret_cast<uint32_t*>(t + mx_code_offset(r0 + 32 * i, j) + 4 * (lane & 3)) = codes;
-                sc[i] = w;
             }
-            if ((lane & 15) == 0)
-                *reinterpret_cast<uint4*>(t + mx_scale_offset(r0, j)) = make_uint4(sc[0], sc[1], sc[2], sc[3]);
+            // transpose the 4 groups x 4 rows of each half-warp: lane i of its first quad gets row
+            // i's word
+            const uint32_t pick = 0x0040u | (lane & 3) * 0x0011u;   // byte i of either operand
+            const int half = lane & 16;
+            const uint32_t c0 = __shfl_sync(0xffffffffu, col, half), c1 = __shfl_sync(0xffffffffu, col, half + 4);
+            const uint32_t c2 = __shfl_sync(0xffffffffu, col, half + 8), c3 = __shfl_sync(0xffffffffu, col, half + 12);
+            const uint32_t w = __byte_perm(__byte_perm(c0, c1, pick), __byte_perm(c2, c3, pick), 0x5410u);
+            if ((lane & 12) == 0) *reinterpret_cast<uint32_t*>(t + mx_scale_offset(r0 + 32 * (lane & 3), j)) = w;
         }
     }
 }
@@ -435,8 +443,10 @@ cudaError_t launch_quantize(const RowSource& s, int64_t G, int64_t N, int K, uin
     const int64_t bands = G * mx_row_tiles(N);
     const int run = run_for(bands, kb);
     const unsigned grid = grid_for(bands * ((kb + run - 1) / run) * 32);
-    auto kern = s.f32 ? (vec ? mx_quantize_kernel<true, true> : mx_quantize_kernel<true, false>)
-                      : (vec ? mx_quantize_kernel<false, true> : mx_quantize_kernel<false, false>);
+    auto kern = s.sorted_ids ? (s.f32 ? (vec ? mx_quantize_kernel<true, true, true> : mx_quantize_kernel<true, false, true>)
+                                      : (vec ? mx_quantize_kernel<false, true, true> : mx_quantize_kernel<false, false, true>))
+                             : (s.f32 ? (vec ? mx_quantize_kernel<true, true, false> : mx_quantize_kernel<true, false, false>)
+                                      : (vec ? mx_quantize_kernel<false, true, false> : mx_quantize_kernel<false, false, false>));
     kern<<<grid, 256, 0, st>>>(s, G, N, K, run, packed, err);
     return cudaGetLastError();
 }

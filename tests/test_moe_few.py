@@ -29,15 +29,15 @@ def need_gpu():
     chord.chord_get_device_error()
 
 
-def make_weights(fmt, E, N, K, g, wide=False):
-    """(values float64 [E, N, K], pack(layout) -> device blob)"""
+def make_weights(fmt, E, N, K, g, wide=False, scales=None):
+    """(values float64 [E, N, K], pack(layout) -> device blob); scales: INT4 scales to use"""
     codes = torch.randint(0, 16, (E, N, K), generator=g, dtype=torch.uint8)
     if fmt == "int4":
         s = (torch.randn((E, N, K // 32), generator=g).abs() * 0.02 + 1e-3)
         if wide:     # scales outside the one-FMA dequantisation's range
             s[:, ::3] *= 64.0
             s[:, 1::5] = -s[:, 1::5]
-        s = s.to(torch.bfloat16)
+        s = (s if scales is None else scales).to(torch.bfloat16)
         v = ((codes.double() - 8) * s.double().repeat_interleave(32, -1)).float().to(torch.bfloat16).double()
 
         def pack(layout=chord.LAYOUT_TCGEN05):
@@ -166,6 +166,25 @@ def test_wide_scales(fmt):
     ids, w = routing(T, E, topk, g)
     x = (torch.randn(T, H, generator=g) * 0.05).to(torch.bfloat16)
     check(run(x, ids, w, E, I, p13(), p2(), fmt), *reference(x, ids, w, v13, v2))
+
+
+@gpu
+@pytest.mark.parametrize("lo,hi", [(-126, -116), (-119, -117), (-8, -2)])
+def test_int4_scales_at_the_ends_of_the_normal_range(lo, hi):
+    """Scales from the smallest normal number on, and up to 1/2, one per group
+    at random: every weight is exact, so the bound is the usual one."""
+    need_gpu()
+    g = torch.Generator().manual_seed(-lo)
+    T, E, topk, H, I = 5, 3, 2, 384, 192
+    def scales(N, K):
+        return torch.exp2(torch.randint(lo, hi + 1, (E, N, K // 32), generator=g).double()) * (
+            1 + torch.randint(0, 128, (E, N, K // 32), generator=g).double() / 128)
+    v13, p13 = make_weights("int4", E, 2 * I, H, g, scales=scales(2 * I, H).clamp(max=0.498))
+    v2, p2 = make_weights("int4", E, H, I, g, scales=scales(H, I).clamp(max=0.498))
+    ids, w = routing(T, E, topk, g)
+    x = (torch.randn(T, H, generator=g) * 2.0 ** -(hi + 5)).to(torch.bfloat16)
+    for layout in (2, 3):
+        check(run(x, ids, w, E, I, p13(layout), p2(), "int4"), *reference(x, ids, w, v13, v2))
 
 
 @gpu

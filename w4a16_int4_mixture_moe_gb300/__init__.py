@@ -143,6 +143,9 @@ def _p(t):
 def _s(stream):
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():
+            # the handle of torch.cuda.current_stream() without its Python object (3.4 us of a 9 us call)
+            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(getattr(stream, "cuda_stream", stream) or 0)
 
@@ -318,13 +321,17 @@ def chord_grouped_masked_gemm(A, masked_m, expected_m: int, packed, N: int, K: i
            "chord_grouped_masked_gemm")
 
 
+_dtypes = {}
+
+
 def _dtype(t, what: str) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return DTYPE_BF16
-    if t.dtype == torch.float32:
-        return DTYPE_F32
-    raise ChordError(1, f"{what}: dtype {t.dtype}")
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32})
+    code = _dtypes.get(t.dtype)
+    if code is None:
+        raise ChordError(1, f"{what}: dtype {t.dtype}")
+    return code
 
 
 def chord_mxfp4_bytes(G: int, N: int, K: int) -> int:

@@ -28,6 +28,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "chord_internal.h"
 #include "chord_mxfp4.cuh"
 #include "chord_tcgen05.cuh"
@@ -247,13 +249,18 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
 __device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 
 // The scale of a lane's group, ready for the dequantisation in use.
-//   INT4, every scale in the one-FMA range: (s * 2^129, -8 s); else (s, s).
+//   INT4, every scale in the one-FMA range (dequant_row8_fma): (s * 2^129, -8 s, -s / 2).
+//     A nibble at bits 4..7 of a half-word is q * 2^-129 and becomes (q - 8) s; one at bits
+//     0..3 is q * 2^-133 and becomes (q - 8) s / 16 with the same multiplier, so two of a
+//     word's four pairs need no shift; their products are summed apart and join times 16
+//     (mma16816).  A sixteenth of a weight is exact unless it is subnormal, so units with a
+//     scale below 2^-118 (`odd`) shift instead and take -8 s.  Else: (s, s).
 //   MXFP4: a code's three magnitude bits at bits 6..8 of a half-word are the bf16
 //   number value * 2^-126 (subnormal 0.5 included), so one multiply by
 //   2^(b - 1) gives the weight exactly; it fits bf16 for b <= 128, and larger scales
-//   (n set) take two multiplies, 2^126 and 2^(b - 127).
+//   (n set, `odd` units) take two multiplies, 2^126 and 2^(b - 127).
 struct Scale {
-    uint32_t m, n;
+    uint32_t m, n, o;
 };
 
 template <bool MX, bool FAST>
@@ -267,22 +274,26 @@ __device__ __forceinline__ Scale make_scale(uint32_t word, int c) {
     } else {
         const uint32_t sp = prmt(word, c & 1 ? 0x3232u : 0x1010u);
         s.m = sp;
-        s.n = 0;
-        if constexpr (FAST) fma_scale_pair(sp, s.m, s.n);
+        s.n = s.o = 0;
+        if constexpr (FAST) {
+            fma_scale_pair(sp, s.m, s.n);
+            s.o = bf2_as_u32(__hmul2(u32_as_bf2(sp), u32_as_bf2(0xBF00BF00u)));   // times -1/2
+        }
     }
     return s;
 }
 
-// Eight codes to four bf16 pairs; wide: MXFP4 scales above 2 are present.
-template <bool MX, bool FAST>
-__device__ __forceinline__ void dequant8(uint32_t w, const Scale& s, bool wide, uint32_t (&o)[4]) {
+// Eight codes to four bf16 pairs.  ODD: the unit has a scale that the short form does not
+// cover (see Scale).  Pairs 0 and 2 of a FAST, not ODD word are sixteenths.
+template <bool MX, bool FAST, bool ODD>
+__device__ __forceinline__ void dequant8(uint32_t w, const Scale& s, uint32_t (&o)[4]) {
     if constexpr (MX) {
         uint32_t v[4];
         v[0] = ((w << 6) & 0x01C001C0u) | ((w << 12) & 0x80008000u);   // columns 0, 4
         v[1] = ((w << 2) & 0x01C001C0u) | ((w << 8) & 0x80008000u);    // 1, 5
         v[2] = ((w >> 2) & 0x01C001C0u) | ((w << 4) & 0x80008000u);    // 2, 6
         v[3] = ((w >> 6) & 0x01C001C0u) | (w & 0x80008000u);           // 3, 7
-        if (wide) {
+        if constexpr (ODD) {
             const __nv_bfloat162 big = u32_as_bf2(0x7E807E80u);        // 2^126
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -290,8 +301,15 @@ __device__ __forceinline__ void dequant8(uint32_t w, const Scale& s, bool wide, 
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = bf2_as_u32(__hmul2(u32_as_bf2(v[i]), u32_as_bf2(s.m)));
-    } else if constexpr (FAST) {
+    } else if constexpr (FAST && ODD) {
         dequant_row8_fma(w, s.m, s.n, o);
+    } else if constexpr (FAST) {
+        const uint32_t t = w >> 8;
+        const __nv_bfloat162 m = u32_as_bf2(s.m), n = u32_as_bf2(s.n), h = u32_as_bf2(s.o);
+        o[0] = bf2_as_u32(__hfma2(u32_as_bf2(w & 0x000F000Fu), m, h));   // columns +0, +1, a sixteenth
+        o[1] = bf2_as_u32(__hfma2(u32_as_bf2(w & 0x00F000F0u), m, n));   // +2, +3
+        o[2] = bf2_as_u32(__hfma2(u32_as_bf2(t & 0x000F000Fu), m, h));   // +4, +5, a sixteenth
+        o[3] = bf2_as_u32(__hfma2(u32_as_bf2(t & 0x00F000F0u), m, n));   // +6, +7
     } else {
         dequant_row8(w, s.m, o);
     }
@@ -318,20 +336,27 @@ __device__ __forceinline__ int h_pos(int col) {
     return (col & ~127) | ((col >> 3) & 3) << 5 | ((col >> 5) & 3) << 3 | e;
 }
 
-// d: two sums, one per k16 half, so that consecutive instructions do not wait on one another.
+// 16 rows x 32 columns (eight of each lane) times eight tokens.  d: two sums, so that
+// consecutive instructions do not wait on one another: d[0] of pairs 0 and 2, which may be
+// sixteenths (whole: they are not, and go to d[1]), d[1] of pairs 1 and 3.
+template <bool WHOLE>
 __device__ __forceinline__ void mma16816(float (&d)[2][4], const uint32_t (&r0)[4], const uint32_t (&r1)[4], const uint4& b) {
+    float(&e)[4] = d[WHOLE ? 1 : 0];
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0][0]), "+f"(d[0][1]), "+f"(d[0][2]), "+f"(d[0][3])
-        : "r"(r0[0]), "r"(r1[0]), "r"(r0[1]), "r"(r1[1]), "r"(b.x), "r"(b.y));
+        : "+f"(e[0]), "+f"(e[1]), "+f"(e[2]), "+f"(e[3])
+        : "r"(r0[0]), "r"(r1[0]), "r"(r0[2]), "r"(r1[2]), "r"(b.x), "r"(b.z));
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[1][0]), "+f"(d[1][1]), "+f"(d[1][2]), "+f"(d[1][3])
-        : "r"(r0[2]), "r"(r1[2]), "r"(r0[3]), "r"(r1[3]), "r"(b.z), "r"(b.w));
+        : "r"(r0[1]), "r"(r1[1]), "r"(r0[3]), "r"(r1[3]), "r"(b.y), "r"(b.w));
 }
 
+// The two sums joined.
+template <bool SIXTEENTH>
 __device__ __forceinline__ float4 both(const float (&d)[2][4]) {
-    return make_float4(d[0][0] + d[1][0], d[0][1] + d[1][1], d[0][2] + d[1][2], d[0][3] + d[1][3]);
+    constexpr float f = SIXTEENTH ? 16.0f : 1.0f;
+    return make_float4(fmaf(d[0][0], f, d[1][0]), fmaf(d[0][1], f, d[1][1]), fmaf(d[0][2], f, d[1][2]), fmaf(d[0][3], f, d[1][3]));
 }
 
 __device__ __forceinline__ void cluster_sync_all() {
@@ -384,7 +409,8 @@ __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32
                                          float (&acc)[2][2][4], LoadB&& b) {
     uint4 q[2][2];
     Scale s[2][2];
-    bool wide = false;
+    uint32_t least = 0xffffffffu;   // INT4: least scale - 1 (a scale of 0 stands for no column)
+    bool odd = false;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -393,23 +419,32 @@ __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32
             uint32_t w = lds32(st + lr.soff + i * lr.sd_tile + h * lr.sd_row + scale_add);
             if (!MX && !on) w = 0;   // columns past K: codes left in the stage, times 0
             s[i][h] = make_scale<MX, FAST>(w, c);
-            if constexpr (MX) wide |= s[i][h].n != 0;
+            if constexpr (MX)
+                odd |= s[i][h].n != 0;
+            else if constexpr (FAST)
+                least = min(least, prmt(w, c & 1 ? 0x3232u : 0x1010u) - 1u);
         }
-    if constexpr (MX) wide = __any_sync(0xffffffffu, wide);
+    if constexpr (!MX && FAST) odd = least < 0x04800480u - 1u;   // below 2^-118
+    auto columns = [&](auto is_odd) {
+        constexpr bool kOdd = decltype(is_odd)::value;
+        constexpr bool kWhole = !MX && FAST && kOdd;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint4 v = b(j);
-        uint4 r;
-        if constexpr (REST) r = b(4 + j);
+        for (int j = 0; j < 4; ++j) {
+            const uint4 v = b(j), r = REST ? b(4 + j) : v;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t x0[4], x1[4];
-            dequant8<MX, FAST>(word(q[i][0], j), s[i][0], wide, x0);
-            dequant8<MX, FAST>(word(q[i][1], j), s[i][1], wide, x1);
-            mma16816(acc[i], x0, x1, v);
-            if constexpr (REST) mma16816(acc[i], x0, x1, r);
+            for (int i = 0; i < 2; ++i) {
+                uint32_t x0[4], x1[4];
+                dequant8<MX, FAST, kOdd>(word(q[i][0], j), s[i][0], x0);
+                dequant8<MX, FAST, kOdd>(word(q[i][1], j), s[i][1], x1);
+                mma16816<kWhole>(acc[i], x0, x1, v);
+                if constexpr (REST) mma16816<kWhole>(acc[i], x0, x1, r);
+            }
         }
-    }
+    };
+    if ((MX || FAST) && __any_sync(0xffffffffu, odd))
+        columns(std::true_type{});
+    else
+        columns(std::false_type{});
 }
 
 // After the last stage: every copy that was issued has landed.
@@ -451,76 +486,69 @@ __device__ __forceinline__ void store_h(const FewArgs& a, const Route& rt, int s
     }
 }
 
-// The weights' code blocks go through cp.async.bulk, issued by lane 0; what comes in
+// The weights' code blocks go through cp.async.bulk, a block per lane; what comes in
 // short pieces (scale words, activation rows) through 16-byte cp.async of all
-// lanes: bulk copies of a few hundred bytes hold up the ones behind them.
+// lanes: bulk copies of a few hundred bytes hold up the ones behind them.  The warp
+// shares its scheduler with consumers, so a stage costs it few instructions: every
+// address is a running pointer.
 template <bool MX>
 __device__ __forceinline__ void up_producer(const FewArgs& a, const Route& rt, const Ring& rg, bool inter, int items, int mt,
                                             int ks0, int ks1) {
     using S = Stage<MX>;
     const int lane = threadIdx.x & 31;
     constexpr int kPieces = S::kCols / 8;   // 16-byte pieces of an activation row
+    constexpr int kStep = MX ? kMxTileBytes : 9216;
+    // lane l copies block l of a stage: `bytes` to `to`, from `from` of the item
+    const int blocks = MX || !inter ? 8 : 4;
+    uint32_t bytes, to;
+    if constexpr (MX) {   // codes, then scale blocks, of 32 rows each: gate, gate, up, up
+        bytes = lane < 4 ? 4096u : 1024u;
+        to = lane < 4 ? lane * 4096u : S::kScale + (lane - 4) * 1024u;
+    } else {              // (chunk, half) blocks of 128 rows, or of 64 gate and 64 up rows
+        bytes = inter ? 2048u : 1024u;
+        to = inter ? lane * S::kBlock : (lane >> 1) * S::kBlock + (lane & 1) * 1024u;
+    }
+    const uint32_t total = MX ? 16384u + 4096u : 8192u;
     tc5::Ring r;
     int issued = 0;
     bool ok = true;
     for (int item = blockIdx.x / a.cluster; item < items; item += gridDim.x / a.cluster) {
         const int slot = item / mt, m = item - slot * mt, e = rt.expert[slot];
         const uint32_t tokens = rt.tokens[slot];
+        const uint8_t *from, *scales = nullptr;
+        if constexpr (MX) {
+            const uint8_t* base = a.w13 + kHeaderBytes + (uint64_t)e * mx_group_bytes(2 * a.I, a.H);
+            const int gi = lane & 3, row = (gi >> 1) * a.I + m * 64 + (gi & 1) * 32;   // 32 rows never cross a tile
+            from = base + ((int64_t)(row >> 7) * mx_col_tiles(a.H) + ks0) * kStep + (lane < 4 ? (row & 127) * 128 : kMxCodeBytes);
+        } else {
+            const uint8_t* base = a.w13 + kHeaderBytes + (uint64_t)e * ((uint64_t)(2 * a.I) * a.H * 9ull / 16ull) + (int64_t)ks0 * kStep;
+            const int64_t band = (int64_t)(a.H / 64) * 4608;
+            const int q = inter ? lane : lane >> 1, row = inter ? m * 128 : (lane & 1) * a.I + m * 64;   // I % 64 == 0
+            from = base + (row >> 7) * band + ((q >> 1) & 1) * 4608 + (q & 1) * 2048 + (row & 127) * 16;
+            const int srow = inter ? m * 128 : (lane >> 4) * a.I + m * 64;
+            scales = base + (srow >> 7) * band + 4096 + (inter ? lane * 16 : (srow & 127) * 4 + (lane & 15) * 16);
+        }
+        const uint16_t* x = a.x + ks0 * S::kCols + lane * 8;
+        int left = a.H - ks0 * S::kCols - lane * 8;   // columns from this lane's piece on
         for (int ks = ks0; ks < ks1 && ok; ++ks) {
             ok = tc5::wait(&rg.empty[r.slot], r.phase ^ 1u, rg.abort_flag, a.err);
             if (!ok) break;
-            uint64_t* bar = &rg.full[r.slot];
-            uint8_t* st = rg.ptr + r.slot * a.stage_bytes;
-            if constexpr (MX) {
-                // 32 rows at a time: gate, gate, up, up (a group of 32 never crosses a tile)
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, 16384u + 4096u);
-                    const uint8_t* base = a.w13 + kHeaderBytes + (uint64_t)e * mx_group_bytes(2 * a.I, a.H);
-#pragma unroll
-                    for (int gi = 0; gi < 4; ++gi) {
-                        const int row = (gi >> 1) * a.I + m * 64 + (gi & 1) * 32;
-                        const uint8_t* t = base + ((int64_t)(row >> 7) * mx_col_tiles(a.H) + ks) * kMxTileBytes;
-                        bulk_g2s(st + gi * 4096, t + (row & 127) * 128, 4096, bar);
-                        bulk_g2s(st + S::kScale + gi * 1024, t + kMxCodeBytes, 1024, bar);
-                    }
-                }
-            } else {
-                const uint8_t* base = a.w13 + kHeaderBytes + (uint64_t)e * ((uint64_t)(2 * a.I) * a.H * 9ull / 16ull) +
-                                      (int64_t)ks * 9216;
-                const int64_t band = (int64_t)(a.H / 64) * 4608;
-                // rows of this lane's scale pieces and of the code blocks: all of a tile's, or 64 gate and 64 up
-                const int up = lane >> 4;
-                const int row = inter ? m * 128 : (up ? a.I : 0) + m * 64;   // I % 64 == 0: 64 rows of one tile
-                const uint8_t* ts = base + (row >> 7) * band + 4096 + (inter ? lane * 16 : (row & 127) * 4 + (lane & 15) * 16);
-                const uint32_t ds = smem_u32(st + S::kScale) + lane * 16;
-                cp_async16(ds, ts);
-                cp_async16(ds + 512, ts + 4608);
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, 8192u);
-                    if (inter) {
-                        const uint8_t* t = base + m * band;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            bulk_g2s(st + q * S::kBlock, t + (q >> 1) * 4608 + (q & 1) * 2048, 2048, bar);
-                    } else {
-#pragma unroll
-                        for (int gu = 0; gu < 2; ++gu) {
-                            const int rw = gu * a.I + m * 64;
-                            const uint8_t* t = base + (rw >> 7) * band + (rw & 127) * 16;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                bulk_g2s(st + q * S::kBlock + gu * 1024, t + (q >> 1) * 4608 + (q & 1) * 2048, 1024, bar);
-                        }
-                    }
-                }
+            const uint32_t bar = smem_u32(&rg.full[r.slot]), st = rg.base + r.slot * a.stage_bytes;
+            if (lane == 0) tc5::arrive_expect_tx(bar, total);
+            if (lane < blocks) tc5::bulk_g2s(st + to, from, bytes, bar);
+            if constexpr (!MX) {
+                cp_async16(st + S::kScale + lane * 16, scales);
+                cp_async16(st + S::kScale + 512 + lane * 16, scales + 4608);
+                scales += kStep;
             }
-            __syncwarp();
-            uint32_t xs = smem_u32(st + S::kUpWeights) + lane * 16;
-            const int k = ks * S::kCols + lane * 8;
-            if (lane < kPieces && k < a.H)
-                for (uint32_t mk = tokens; mk; mk &= mk - 1, xs += S::kUpRow)
-                    cp_async16(xs, a.x + (int64_t)(__ffs(mk) - 1) * a.H + k);
-            cp_async_arrive_noinc(bar);
+            if (lane < kPieces && left > 0) {
+                uint32_t xs = st + S::kUpWeights + lane * 16;
+                for (uint32_t mk = tokens; mk; mk &= mk - 1, xs += S::kUpRow) cp_async16(xs, x + (int64_t)(__ffs(mk) - 1) * a.H);
+            }
+            cp_async_arrive_noinc(&rg.full[r.slot]);
+            from += kStep;
+            x += S::kCols;
+            left -= S::kCols;
             ++issued;
             r.next(a.depth);
         }
@@ -580,7 +608,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
         if (a.cluster == 1) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (ok) store_h<MX>(a, rt, slot, s_ids, s_w, col0 + 8 * i, c, both(acc[i]));
+                if (ok) store_h<MX>(a, rt, slot, s_ids, s_w, col0 + 8 * i, c, both<!MX && FAST>(acc[i]));
             continue;
         }
         // join the cluster's K ranges: CTA `rank` takes tiles rank, rank + cluster, ... of the
@@ -588,7 +616,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
         float4* buf = part + (nitem & 1) * 256;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            buf[(warp * 2 + i) * 32 + lane] = both(acc[i]);
+            buf[(warp * 2 + i) * 32 + lane] = both<!MX && FAST>(acc[i]);
         __syncwarp();
         cluster_sync_all();
         const int tile = rank + a.cluster * warp;
@@ -647,30 +675,25 @@ __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt,
             }
         }
     };
+    const uint64_t expert_bytes = MX ? mx_group_bytes(a.H, a.I) : (uint64_t)a.H * a.I * 9ull / 16ull;
+    const uint8_t* tile_base = a.w2 + kHeaderBytes + (MX ? (int64_t)tile * mx_col_tiles(a.I) * kMxTileBytes
+                                                        : (int64_t)tile * (a.I / 64) * 4608);
     auto weights = [&](const At& at, int slot) {
-        uint64_t* bar = &rg.full[slot];
-        uint8_t* st = rg.ptr + slot * a.stage_bytes;
+        const uint32_t bar = smem_u32(&rg.full[slot]), st = rg.base + slot * a.stage_bytes;
+        const uint8_t* t = tile_base + (uint64_t)rt.expert[at.sl] * expert_bytes;
         if constexpr (MX) {
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar, kMxTileBytes);
-                bulk_g2s(st, a.w2 + kHeaderBytes + (uint64_t)rt.expert[at.sl] * mx_group_bytes(a.H, a.I) +
-                                 ((int64_t)tile * mx_col_tiles(a.I) + at.ks) * kMxTileBytes,
-                         kMxTileBytes, bar);
+                tc5::arrive_expect_tx(bar, kMxTileBytes);
+                tc5::bulk_g2s(st, t + (int64_t)at.ks * kMxTileBytes, kMxTileBytes, bar);
             }
         } else {
             const int chunks = a.I / 64 - 2 * at.ks >= 2 ? 2 : 1;
-            const uint8_t* t = a.w2 + kHeaderBytes + (uint64_t)rt.expert[at.sl] * ((uint64_t)a.H * a.I * 9ull / 16ull) +
-                               (int64_t)tile * (a.I / 64) * 4608 + (int64_t)at.ks * 9216;
-            const uint32_t ds = smem_u32(st + S::kScale) + lane * 16;
-            cp_async16(ds, t + 4096 + lane * 16);
-            if (chunks == 2) cp_async16(ds + 512, t + 4608 + 4096 + lane * 16);
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, (uint32_t)chunks * 4096u);
-                for (int q = 0; q < 2 * chunks; ++q)
-                    bulk_g2s(st + q * S::kBlock, t + (q >> 1) * 4608 + (q & 1) * 2048, 2048, bar);
-            }
+            t += (int64_t)at.ks * 9216;
+            if (lane == 0) tc5::arrive_expect_tx(bar, (uint32_t)chunks * 4096u);
+            if (lane < 2 * chunks) tc5::bulk_g2s(st + lane * S::kBlock, t + (lane >> 1) * 4608 + (lane & 1) * 2048, 2048, bar);
+            cp_async16(st + S::kScale + lane * 16, t + 4096 + lane * 16);
+            if (chunks == 2) cp_async16(st + S::kScale + 512 + lane * 16, t + 4608 + 4096 + lane * 16);
         }
-        __syncwarp();
     };
     const int64_t plane = (int64_t)a.T * a.topk * a.Ip;
     const int64_t second = MX ? plane : plane - kPieces * 8;   // INT4: lanes 16 .. 31 take the remainder row
@@ -706,12 +729,12 @@ __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt,
 
 // A pass's sums (column j: its j-th token) into the sums by token (lane (g, c), tile nt:
 // tokens 8 nt + 2c and + 1).  half: columns 4 .. 7 hold the remainders' products.
-template <int NT>
+template <int NT, bool SIXTEENTH>
 __device__ __forceinline__ void add_pass(float (&sum)[2][NT][4], float (&chains)[2][2][4], uint32_t tokens, bool half, int c) {
     float p[2][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        p[i >> 2][i & 3] = chains[i >> 2][0][i & 3] + chains[i >> 2][1][i & 3];
+        p[i >> 2][i & 3] = fmaf(chains[i >> 2][0][i & 3], SIXTEENTH ? 16.0f : 1.0f, chains[i >> 2][1][i & 3]);
         chains[i >> 2][0][i & 3] = chains[i >> 2][1][i & 3] = 0.0f;
     }
     if (half) {
@@ -783,7 +806,7 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
             __syncwarp();
             if (lane == 0) mbar_arrive(&rg.empty[r.slot]);
         }
-        add_pass<NT>(sum, pass, tokens, half, c);
+        add_pass<NT, !MX && FAST>(sum, pass, tokens, half, c);
     }
 }
 

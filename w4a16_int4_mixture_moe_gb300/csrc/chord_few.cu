@@ -1020,8 +1020,8 @@ chord_status chord_moe_layer_few(const void* x, const int32_t* topk_ids, const f
                                  void* out, const chord_opts* opts, void* stream) {
     if (T < 0 || topk <= 0 || E <= 0 || H <= 0 || I <= 0) return CHORD_ERR_INVALID_ARG;
     if (weights != CHORD_WEIGHTS_INT4 && weights != CHORD_WEIGHTS_MXFP4) return CHORD_ERR_INVALID_ARG;
-    if (T > CHORD_FEW_MAX_TOKENS || topk > 32 || E > 1024 || (int64_t)H * I > (1LL << 31))
-        return CHORD_ERR_UNSUPPORTED;   // an expert's bytes are addressed with 32 bits
+    if (T > CHORD_FEW_MAX_TOKENS || topk > 32 || E > 1024 || H > (1 << 20) || I > (1 << 20))
+        return CHORD_ERR_UNSUPPORTED;
     const bool mx = weights == CHORD_WEIGHTS_MXFP4;
     if (mx ? (H % 32 || I % 32) : (H % 128 || I % 64)) return CHORD_ERR_UNSUPPORTED;
     const size_t n13 = mx ? chord_mxfp4_bytes(E, 2 * I, H) : chord_packed_weight_bytes(E, 2 * I, H, CHORD_LAYOUT_TCGEN05);

@@ -57,7 +57,8 @@ struct FewArgs {
     int validate;        // report ids outside [-1, E)
     int slot_cap;        // most passes a call can need
     int cluster;         // CTAs that share an item (gate_up, a cluster) or an output tile (down, list slices)
-    float4* part;        // down: the slices' sums
+    int clustered;       // down: the slices are a cluster
+    float4* part;        // down, not clustered: the slices' sums
     int* joined;         // down: CTAs of each output tile that have left theirs
     int depth;           // stages of the ring
     int stage_bytes;
@@ -367,24 +368,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr, uint32_t cta) {
+// To the same shared-memory address of CTA `cta` of the cluster.
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t cta, float4 v) {
     uint32_t ra;
-    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(cta));
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(ra)
-                 : "memory");
-    return v;
-}
-// Sum over the cluster's CTAs, in rank order, of the float4 at `p` of each.
-__device__ __forceinline__ float4 cluster_sum(const float4* p, int n) {
-    float4 v[8], s = make_float4(0, 0, 0, 0);   // at most 8 CTAs; every load before the first sum
-#pragma unroll
-    for (int r = 0; r < 8; ++r) v[r] = r < n ? ld_cluster(smem_u32(p), (uint32_t)r) : make_float4(0, 0, 0, 0);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
-    return s;
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(ra), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
 struct Ring {
@@ -611,17 +599,28 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
                 if (ok) store_h<MX>(a, rt, slot, s_ids, s_w, col0 + 8 * i, c, both<!MX && FAST>(acc[i]));
             continue;
         }
-        // join the cluster's K ranges: CTA `rank` takes tiles rank, rank + cluster, ... of the
-        // eight (warp, i); the buffers alternate, so one barrier an item is enough
+        // join the cluster's K ranges: tile q = 2 warp + i belongs to CTA q mod cluster, which
+        // is sent every CTA's sums ([tile of its own][rank][lane]) and adds them in rank order.
+        // Buffers alternate, so one barrier an item is enough, and after the last nobody
+        // touches another CTA's memory.
+        const uint32_t own = 8u / (uint32_t)a.cluster;   // tiles of a CTA
         float4* buf = part + (nitem & 1) * 256;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            buf[(warp * 2 + i) * 32 + lane] = both<!MX && FAST>(acc[i]);
+        for (uint32_t i = 0; i < 2; ++i) {
+            const uint32_t q = (uint32_t)warp * 2 + i;
+            st_cluster(smem_u32(buf + ((q / a.cluster) * a.cluster + rank) * 32 + lane), q % a.cluster, both<!MX && FAST>(acc[i]));
+        }
         __syncwarp();
         cluster_sync_all();
-        const int tile = rank + a.cluster * warp;
-        if (ok && tile < 8)
-            store_h<MX>(a, rt, slot, s_ids, s_w, m * 64 + 8 * tile + p, c, cluster_sum(buf + tile * 32 + lane, a.cluster));
+        if (ok && (uint32_t)warp < own) {
+            const float4* mine = buf + warp * a.cluster * 32 + lane;
+            float4 s = mine[0];
+            for (int r = 1; r < a.cluster; ++r) {
+                const float4 v = mine[r * 32];
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
+            store_h<MX>(a, rt, slot, s_ids, s_w, m * 64 + 8 * (warp * a.cluster + rank) + p, c, s);
+        }
     }
 }
 
@@ -643,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 4) few_gate_up_kernel(const FewArgs 
         if (blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, CHORD_DEV_BAD_HEADER);
         return;
     }
+    if (a.cluster > 1) cluster_sync_all();   // every CTA runs before another one's sums arrive
     const int stages = (a.H + S::kCols - 1) / S::kCols, mt = (a.I + 63) / 64, items = rt.slots * mt;
     const int rank = a.cluster > 1 ? (int)cluster_rank() : 0;
     const int ks0 = rank * stages / a.cluster, ks1 = (rank + 1) * stages / a.cluster;
@@ -653,10 +653,6 @@ __global__ void __launch_bounds__(kThreads, 4) few_gate_up_kernel(const FewArgs 
         up_consumer<MX, true>(a, rt, rg, part, inter, s_ids, s_w, items, mt, rank, ks0, ks1);
     else
         up_consumer<MX, false>(a, rt, rg, part, inter, s_ids, s_w, items, mt, rank, ks0, ks1);
-    if (a.cluster > 1) {
-        __syncwarp();
-        cluster_sync_all();   // the others have read this CTA's sums
-    }
 }
 
 // ---- down -------------------------------------------------------------------
@@ -810,9 +806,12 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
     }
 }
 
-// gridDim.x = output tiles of 128 rows x a.cluster list slices (slice fastest).  Each
-// CTA leaves its FP32 sums in the workspace and the tile's last one adds the
-// slices, always in slice order, so the result does not depend on which is last.
+// gridDim.x = output tiles of 128 rows x a.cluster list slices (slice fastest).  Short
+// lists: the slices are a cluster and exchange their FP32 sums through distributed shared
+// memory.  Long ones, whose rings leave room for three CTAs per SM (51 clusters of eight, and
+// 56 tiles of 7168 rows would take a second wave): each CTA leaves its sums in the workspace
+// and the tile's last one adds them.  Always in slice order, so the result does not depend
+// on which CTA is last.
 template <bool MX, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) few_down_kernel(const FewArgs a) {
     using S = Stage<MX>;
@@ -822,8 +821,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) few_down_kernel(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t* s_ids;
     float* s_w;
-    const Route rt = prologue<MX>(a, sh, smem + a.depth * a.stage_bytes, s_ids, s_w, false);
+    const Route rt = prologue<MX>(a, sh, smem + a.depth * a.stage_bytes + (a.clustered ? kConsumers * 2 * NT * 512 : 0), s_ids,
+                                  s_w, false);
     if (!(sh.flags & 1)) return;   // the same in every CTA; the gate_up kernel reported it
+    if (a.clustered) cluster_sync_all();   // every CTA runs before another one's sums arrive
     const int rank = blockIdx.x % a.cluster, tile = blockIdx.x / a.cluster;
     const int kst = (a.I + S::kCols - 1) / S::kCols, total = rt.slots * kst;
     const int v0 = (int)((int64_t)rank * total / a.cluster), v1 = (int)((int64_t)(rank + 1) * total / a.cluster);
@@ -837,70 +838,94 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) few_down_kernel(con
     else
         down_consumer<MX, NT, false>(a, rt, rg, v0, v1, kst, acc);
     __syncwarp();
-    constexpr int kPer = kConsumers * 2 * NT * 32;   // float4 of a CTA: [warp][i][nt][lane]
-    float4* mine = a.part + (int64_t)blockIdx.x * kPer;
-    if (a.cluster > 1) {
-        pdl_wait();   // (threads that read nothing of the gate_up kernel) its zeroed counters and the workspace
+    constexpr int kTiles = kConsumers * 2 * NT;      // (16 rows, 8 tokens) tiles of a CTA, q = (2 warp + i) NT + nt
+    constexpr int kPer = kTiles * 32;                // float4 of a CTA: [tile][lane]
+    auto write = [&](int q, float4 s) {
+        const int row = tile * 128 + (q / NT) * 16 + phys_row<MX>(lane >> 2), t = 8 * (q % NT) + 2 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int tk = t + (k & 1), n = row + (k >> 1) * 8;
+            const float v = k == 0 ? s.x : k == 1 ? s.y : k == 2 ? s.z : s.w;
+            // + 0.0f: a sum of nothing, or of zeros of either sign, is +0
+            if (tk < a.T && n < a.H) a.out[(int64_t)tk * a.H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v + 0.0f));
+        }
+    };
+    auto sum_of = [&](int i, int nt) { return make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]); };
+    if (a.cluster == 1) {
+        if (warp == kConsumers) return;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) write((2 * warp + i) * NT + nt, sum_of(i, nt));
+        return;
+    }
+    if (a.clustered) {
+        // short lists: tile q belongs to CTA q mod cluster, which is sent every slice's sums
+        float4* buf = reinterpret_cast<float4*>(smem + a.depth * a.stage_bytes);   // [tile of its own][slice][lane]
         if (warp < kConsumers) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int q = (2 * warp + i) * NT + nt;
+                    st_cluster(smem_u32(buf + ((q / a.cluster) * a.cluster + rank) * 32 + lane), (uint32_t)(q % a.cluster), sum_of(i, nt));
+                }
+        }
+        __syncwarp();
+        cluster_sync_all();
+        if (warp == kConsumers) return;
+        for (int j = warp; j * a.cluster + rank < kTiles; j += kConsumers) {
+            const float4* from = buf + j * a.cluster * 32 + lane;
+            float4 s = from[0];
+            for (int r = 1; r < a.cluster; ++r) {
+                const float4 v = from[r * 32];
+                s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+            }
+            write(j * a.cluster + rank, s);
+        }
+        return;
+    }
+    pdl_wait();   // (threads that read nothing of the gate_up kernel) its zeroed counters
+    float4* mine = a.part + (int64_t)blockIdx.x * kPer;
+    if (warp < kConsumers) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mine[((2 * warp + i) * NT + nt) * 32 + lane] = sum_of(i, nt);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();   // the CTA's sums (ordered before it by the barrier) before the count
+        sh.last = atomicAdd(a.joined + tile, 1) == a.cluster - 1;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!sh.last || warp == kConsumers) return;
+    // slices in order, eight at a time, the loads of all column tiles of a row tile before
+    // their sums
+    const float4* from = a.part + (int64_t)tile * a.cluster * kPer + warp * 2 * NT * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float4 s[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt] = make_float4(0, 0, 0, 0);
+        for (int r0 = 0; r0 < a.cluster; r0 += 8) {
+            float4 v[NT][8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    mine[((warp * 2 + i) * NT + nt) * 32 + lane] =
-                        make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+                    v[nt][r] = r0 + r < a.cluster && 8 * nt < a.T ? __ldcg(from + (int64_t)(r0 + r) * kPer + (i * NT + nt) * 32)
+                                                                  : make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    s[nt].x += v[nt][r].x, s[nt].y += v[nt][r].y, s[nt].z += v[nt][r].z, s[nt].w += v[nt][r].w;
         }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            __threadfence();   // the CTA's sums (ordered before it by the barrier) before the count
-            sh.last = atomicAdd(a.joined + tile, 1) == a.cluster - 1;
-            __threadfence();
-        }
-        __syncthreads();
-        if (!sh.last) return;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) write((2 * warp + i) * NT + nt, s[nt]);
     }
-    if (warp == kConsumers) return;
-    if (a.cluster > 1) {
-        // slices in order, eight at a time, the loads of all column tiles of a row tile before
-        // their sums
-        const float4* from = a.part + (int64_t)tile * a.cluster * kPer + warp * 2 * NT * 32 + lane;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float4 s[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[nt] = make_float4(0, 0, 0, 0);
-            for (int r0 = 0; r0 < a.cluster; r0 += 8) {
-                float4 v[NT][8];
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        v[nt][r] = r0 + r < a.cluster && 8 * nt < a.T
-                                       ? __ldcg(from + (int64_t)(r0 + r) * kPer + (i * NT + nt) * 32)
-                                       : make_float4(0, 0, 0, 0);
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        s[nt].x += v[nt][r].x, s[nt].y += v[nt][r].y, s[nt].z += v[nt][r].z, s[nt].w += v[nt][r].w;
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                acc[i][nt][0] = s[nt].x, acc[i][nt][1] = s[nt].y, acc[i][nt][2] = s[nt].z, acc[i][nt][3] = s[nt].w;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int row = tile * 128 + (warp * 2 + i) * 16 + phys_row<MX>(lane >> 2), t = 8 * nt + 2 * (lane & 3);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int tk = t + (k & 1), n = row + (k >> 1) * 8;
-                // + 0.0f: a sum of nothing, or of zeros of either sign, is +0
-                if (tk < a.T && n < a.H)
-                    a.out[(int64_t)tk * a.H + n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i][nt][k] + 0.0f));
-            }
-        }
 }
 
 // List slices per output tile of the down kernel: three CTAs per SM of a GB300 (152
@@ -976,9 +1001,11 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     const int tiles = (a.H + 127) / 128;
     a.cluster = down_slices(a.H, list);
     a.stage_bytes = S::down_bytes(tokens);
-    a.depth = ring_depth(third - route, a.stage_bytes, (int)((list + a.cluster - 1) / a.cluster));
+    a.depth = ring_depth(third - route, a.stage_bytes, (list + a.cluster - 1) / a.cluster);
     smem = (size_t)a.depth * a.stage_bytes + route;
-    return launch(few_down_kernel<MX, NT>, a, (unsigned)tiles, smem, false, pdl_enabled(), st);
+    a.clustered = NT == 1 && a.cluster == 8 && smem + kConsumers * 2 * NT * 512 <= 53 * 1024;   // four CTAs per SM
+    if (a.clustered) smem += kConsumers * 2 * NT * 512;
+    return launch(few_down_kernel<MX, NT>, a, (unsigned)tiles, smem, a.clustered != 0, pdl_enabled(), st);
 }
 
 cudaError_t launch_few(const FewArgs& a, bool mx, cudaStream_t st) {

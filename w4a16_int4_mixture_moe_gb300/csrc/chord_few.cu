@@ -290,10 +290,14 @@ template <bool MX, bool FAST, bool ODD>
 __device__ __forceinline__ void dequant8(uint32_t w, const Scale& s, uint32_t (&o)[4]) {
     if constexpr (MX) {
         uint32_t v[4];
-        v[0] = ((w << 6) & 0x01C001C0u) | ((w << 12) & 0x80008000u);   // columns 0, 4
-        v[1] = ((w << 2) & 0x01C001C0u) | ((w << 8) & 0x80008000u);    // 1, 5
-        v[2] = ((w >> 2) & 0x01C001C0u) | ((w << 4) & 0x80008000u);    // 2, 6
-        v[3] = ((w >> 6) & 0x01C001C0u) | (w & 0x80008000u);           // 3, 7
+        // a code n at bits 0..3 of a half-word times 2^6 + 2^12 has its magnitude at bits 6..8
+        // and its sign at bit 15 (the other copies are masked away); at bits 4..7, times a
+        // sixteenth of that: two logical operations and a multiplication, on different pipes
+        const uint32_t t = w >> 8;
+        v[0] = ((w & 0x000F000Fu) * 4160u) & 0x81C081C0u;   // columns 0, 4
+        v[1] = ((w & 0x00F000F0u) * 260u) & 0x81C081C0u;    // 1, 5
+        v[2] = ((t & 0x000F000Fu) * 4160u) & 0x81C081C0u;   // 2, 6
+        v[3] = ((t & 0x00F000F0u) * 260u) & 0x81C081C0u;    // 3, 7
         if constexpr (ODD) {
             const __nv_bfloat162 big = u32_as_bf2(0x7E807E80u);        // 2^126
 #pragma unroll
@@ -416,7 +420,7 @@ __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32
     auto columns = [&](auto is_odd) {
         constexpr bool kOdd = decltype(is_odd)::value;
         constexpr bool kWhole = !MX && FAST && kOdd;
-#pragma unroll
+#pragma unroll(MX && kOdd ? 1 : 4)   // rare: kept short, the instruction cache is
         for (int j = 0; j < 4; ++j) {
             const uint4 v = b(j), r = REST ? b(4 + j) : v;
 #pragma unroll

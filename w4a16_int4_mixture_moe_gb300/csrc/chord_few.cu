@@ -259,7 +259,7 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int j) { return j == 0 
 //   MXFP4: a code's three magnitude bits at bits 6..8 of a half-word are the bf16
 //   number value * 2^-126 (subnormal 0.5 included), so one multiply by
 //   2^(b - 1) gives the weight exactly; it fits bf16 for b <= 128, and larger scales
-//   (n set, `odd` units) take two multiplies, 2^126 and 2^(b - 127).
+//   (`odd` units) take two multiplies, 2^126 and 2^(b - 127).  n: b itself.
 struct Scale {
     uint32_t m, n, o;
 };
@@ -269,9 +269,8 @@ __device__ __forceinline__ Scale make_scale(uint32_t word, int c) {
     Scale s;
     if constexpr (MX) {
         const uint32_t b = (word >> (8 * c)) & 255u;
-        const uint32_t m = b <= 128u ? (b + 126u) << 7 : (b == 255u ? 0x7FC0u : (b << 7));
-        s.m = m | m << 16;
-        s.n = b > 128u ? 1u : 0u;
+        s.m = b * 0x00800080u + 0x3F003F00u;   // twice 2^(b - 1), for b up to 128
+        s.n = b;
     } else {
         const uint32_t sp = prmt(word, c & 1 ? 0x3232u : 0x1010u);
         s.m = sp;
@@ -302,7 +301,7 @@ __device__ __forceinline__ void dequant8(uint32_t w, const Scale& s, uint32_t (&
             const __nv_bfloat162 big = u32_as_bf2(0x7E807E80u);        // 2^126
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (s.n) v[i] = bf2_as_u32(__hmul2(u32_as_bf2(v[i]), big));
+                if (s.n > 128u) v[i] = bf2_as_u32(__hmul2(u32_as_bf2(v[i]), big));
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = bf2_as_u32(__hmul2(u32_as_bf2(v[i]), u32_as_bf2(s.m)));
@@ -401,25 +400,33 @@ __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32
                                          float (&acc)[2][2][4], LoadB&& b) {
     uint4 q[2][2];
     Scale s[2][2];
+    const uint32_t codes = st + (lr.off ^ code_xor);   // (MXFP4: d_tile and d_row are multiples of 1024)
     uint32_t least = 0xffffffffu;   // INT4: least scale - 1 (a scale of 0 stands for no column)
-    bool odd = false;
+    uint32_t most = 0;              // MXFP4: largest scale
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            q[i][h] = lds128(st + ((lr.off + i * lr.d_tile + h * lr.d_row) ^ code_xor));
+            q[i][h] = lds128(codes + i * lr.d_tile + h * lr.d_row);
             uint32_t w = lds32(st + lr.soff + i * lr.sd_tile + h * lr.sd_row + scale_add);
             if (!MX && !on) w = 0;   // columns past K: codes left in the stage, times 0
             s[i][h] = make_scale<MX, FAST>(w, c);
             if constexpr (MX)
-                odd |= s[i][h].n != 0;
+                most = max(most, s[i][h].n);
             else if constexpr (FAST)
                 least = min(least, prmt(w, c & 1 ? 0x3232u : 0x1010u) - 1u);
         }
-    if constexpr (!MX && FAST) odd = least < 0x04800480u - 1u;   // below 2^-118
+    const bool odd = MX ? most > 128u : FAST && least < 0x04800480u - 1u;   // INT4: below 2^-118
     auto columns = [&](auto is_odd) {
         constexpr bool kOdd = decltype(is_odd)::value;
         constexpr bool kWhole = !MX && FAST && kOdd;
+        if constexpr (MX && kOdd) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                Scale& v = s[k >> 1][k & 1];
+                if (v.n > 128u) v.m = v.n == 255u ? 0x7FC07FC0u : v.n * 0x00800080u;
+            }
+        }
 #pragma unroll(MX && kOdd ? 1 : 4)   // rare: kept short, the instruction cache is
         for (int j = 0; j < 4; ++j) {
             const uint4 v = b(j), r = REST ? b(4 + j) : v;

@@ -33,20 +33,28 @@ struct MxGemmArgs {
 // instruction.  Roles, each a warp that keeps its addresses warp-uniform and lets one
 // elected lane issue (a lane on its own issued at half the rate):
 //   * two producers copy K stages of 256 columns into shared-memory rings with
-//     cp.async.bulk: one the weight tiles (17408 contiguous bytes), one the codes
-//     of the block's rows with their scales.  The rows come from L2, the weights from
-//     HBM, so the weights' ring is the deeper one;
+//     cp.async.bulk: one the weight tiles (17408 contiguous bytes, from HBM), one the codes
+//     of the block's rows with their scales (from L2);
 //   * a scale warp copies the stages' scales to tensor memory;
 //   * an issuing warp issues the stages' four K = 64 instructions into one of two FP32
 //     accumulators and commits the stages back to the producers.  It paces the
 //     kernel, so it takes two stages a turn and learns what an item is from the
-//     producer, beside the stage;
+//     producer, beside the stage (one stage a turn: dense 4096 x 4096 x 7168 84 us with its
+//     quantisation, two: 76);
 //   * eight warps read the finished accumulator and write C while the next item
 //     is computed into the other one.
 // Every wait is bounded; the grid is persistent (static round robin).
-// Blocks of many rows run in clusters of two CTAs on neighbouring tiles of N: each
-// copies its own weights and half of the block's rows, the rows going to both CTAs
-// (multicast).  A stage is then free once both CTAs have used it.
+// Blocks of 96 rows or more run in pairs of CTAs on neighbouring tiles of N, whose
+// instructions are one of 256 weight rows: each CTA copies its own weights and half of the
+// block's rows, which the tensor cores of both read, so a stage is 31 KB a CTA instead of
+// 44 and the rings are half as deep again (of measured 208-row blocks, 48 experts: 4096 x 7168
+// 152 us against 174 with single CTAs, 7168 x 2048 104 against 113; dense 4096 x 4096 x
+// 7168 59 against 76).  The first CTA issues for both; the second one's scale warp tells it when a
+// turn's copies have landed there.  Small blocks leave the rows' share small, and the pair's
+// extra hop costs more than it saves (64 rows: 135 us single, 141 paired; 112 rows: equal).
+// What bounds it: the weights' bytes (4096 x 7168 for 8192 rows: 749 MB, and 67 MB of C, in
+// 152 us = 5.4 TB/s; reading these weights alone takes 130 us), and in the dense product, whose tiles come from L2, those copies again: 650 MB in 59 us, 51 us with no
+// matrix instruction issued; the instructions alone take 40.
 constexpr int kEpiWarps = 8;
 constexpr int kWeightWarp = kEpiWarps, kRowWarp = kEpiWarps + 1, kScaleWarp = kEpiWarps + 2, kMmaWarp = kEpiWarps + 3;
 constexpr int kThreads = (kEpiWarps + 4) * 32;
@@ -64,9 +72,9 @@ constexpr int kMxMaxBlockM = 208;        // two accumulators and four stages' sc
 struct MxPlan {
     int tok;        // rows of a block (dense: a multiple of 64)
     int w_stages;   // ring of weight tiles
-    int r_stages;   // ring of rows; as many scale slots in tensor memory
-    int r_bytes;    // one stage of rows: codes, then 1 KB of scales per 128 rows
-    int pair;       // clusters of two CTAs
+    int r_stages;   // ring of rows
+    int r_bytes;    // one stage of rows: codes (a pair's CTA: of half of them), then 1 KB of scales per 128 rows
+    int slots;      // stages whose scales tensor memory holds
 };
 
 struct Item {
@@ -105,12 +113,13 @@ __device__ __forceinline__ Routing load_routing(const MxGemmArgs& g, const MxPla
 }
 
 // Facts of item i, computed identically by every warp from the same arrays.
+template <bool PAIR>
 __device__ __forceinline__ Item item_at(const MxGemmArgs& g, const MxPlan& pl, const Walk& w, int64_t i, const Routing& rt,
                                         int lane, bool report) {
     Item it;
     it.b = divmod_idx(i, w.nper, it.nt);
     it.write = true;
-    if (pl.pair) {
+    if (PAIR) {
         it.nt = 2 * it.nt + (int)w.rank;
         it.write = it.nt < w.ntiles;
         if (!it.write) --it.nt;
@@ -219,6 +228,7 @@ __device__ __forceinline__ void drain(const MxGemmArgs& g, const MxPlan& pl, con
     }
 }
 
+template <bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g, const MxPlan pl) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -228,7 +238,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     uint64_t* full_r = full_w + kMaxStages;
     uint64_t* done = full_r + kMaxStages;      // stage g's instructions: barrier g mod kDone
     uint64_t* turn_full = done + kDone;
-    uint64_t* acc_full = turn_full + kTurns;
+    uint64_t* peer_full = turn_full + kTurns;  // first CTA of a pair: the second one's copies of a turn have landed
+    uint64_t* acc_full = peer_full + kTurns;
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] row blocks, [1] abort, [2] skip
@@ -237,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     volatile uint32_t* info = reinterpret_cast<volatile uint32_t*>(tmem_slot + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = pl.pair ? tc5::cluster_rank() : 0u;
-    if (warp == kMmaWarp) tc5::alloc(tmem_slot, kTmemCols);
+    const uint32_t rank = PAIR ? tc5::cluster_rank() : 0u;
+    if (warp == kMmaWarp) tc5::alloc<PAIR>(tmem_slot, kTmemCols);
     pdl_wait();   // before the first access to global memory
     if (warp == 0) {
         const bool oka = mx_header_ok_warp(g.a, g.a_groups, g.a_rows, g.K), okw = mx_header_ok_warp(g.w, g.E, g.N, g.K);
@@ -261,11 +272,14 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
                 mbar_init(&full_w[s], 1);
                 mbar_init(&full_r[s], 1);
             }
-            for (int s = 0; s < kDone; ++s) mbar_init(&done[s], pl.pair ? 2 : 1);   // the CTAs that read a stage's rows
-            for (int s = 0; s < kTurns; ++s) mbar_init(&turn_full[s], 1);
+            for (int s = 0; s < kDone; ++s) mbar_init(&done[s], 1);
+            for (int s = 0; s < kTurns; ++s) {
+                mbar_init(&turn_full[s], 1);
+                mbar_init(&peer_full[s], 1);
+            }
             for (int s = 0; s < 2; ++s) {
                 mbar_init(&acc_full[s], 1);
-                mbar_init(&acc_empty[s], kEpiWarps);
+                mbar_init(&acc_empty[s], PAIR ? 2 * kEpiWarps : kEpiWarps);
             }
             fence_barrier_init();
         }
@@ -273,17 +287,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     tc5::fence_before();
     __syncthreads();
     tc5::fence_after();
-    // a pair's barriers are initialised before the other CTA's copies and commits reach them
-    if (pl.pair) tc5::cluster_sync();
+    // a pair's barriers are initialised before the other CTA's arrivals and commits reach them
+    if (PAIR) tc5::cluster_sync();
     const uint32_t tmem = *tmem_slot;
     const int ntiles = (g.N + kMxTileRows - 1) / kMxTileRows;
     const int kstages = (g.K + kMxTileCols - 1) / kMxTileCols;
     // a pair's item is (row block, two tiles of N); an odd last tile leaves the second CTA a
     // repeat of the first's that it does not write
-    const int nper = pl.pair ? (ntiles + 1) / 2 : ntiles;
+    const int nper = PAIR ? (ntiles + 1) / 2 : ntiles;
     const int64_t n_items = flags[2] ? 0 : (int64_t)flags[0] * nper;
-    const int64_t first = pl.pair ? blockIdx.x >> 1 : blockIdx.x;
-    const Walk wk{n_items, pl.pair ? gridDim.x >> 1 : gridDim.x, nper, ntiles, rank};
+    const int64_t first = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+    const Walk wk{n_items, PAIR ? gridDim.x >> 1 : gridDim.x, nper, ntiles, rank};
     Routing nxt = load_routing(g, pl, wk, first, lane);
     const int64_t art = mx_row_tiles(g.a_rows);
 
@@ -292,8 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     struct Pos {
         uint32_t g, slot, st, parity;
     };
-    const uint32_t base_w = smem_u32(smem), base_r = smem_u32(ring_r), tok128 = (uint32_t)pl.tok * 128u;
+    const uint32_t base_w = smem_u32(smem), base_r = smem_u32(ring_r), r_codes = (uint32_t)pl.tok * (PAIR ? 64u : 128u);
     const uint32_t full_w_a = smem_u32(full_w), full_r_a = smem_u32(full_r), done_a = smem_u32(done), turn_a = smem_u32(turn_full);
+    const uint32_t peer_a = smem_u32(peer_full), slots = (uint32_t)pl.slots;
     const uint32_t w_stages = (uint32_t)pl.w_stages, r_stages = (uint32_t)pl.r_stages, r_bytes = (uint32_t)pl.r_bytes;
     auto next_w = [&](const Pos& p) {
         return p.slot + 1 == w_stages ? Pos{p.g + 1, 0, base_w, p.parity ^ 1u}
@@ -315,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     if (warp == kWeightWarp) {
         Pos p{0, 0, base_w, 0};
         for (int64_t i = first; i < n_items && ok; i += wk.step) {
-            const Item it = item_at(g, pl, wk, i, nxt, lane, false);
+            const Item it = item_at<PAIR>(g, pl, wk, i, nxt, lane, false);
             nxt = load_routing(g, pl, wk, i + wk.step, lane);
             if (it.rows == 0) continue;
             const uint8_t* src = g.w + kHeaderBytes + ((int64_t)it.e * ntiles + it.nt) * kstages * kMxTileBytes;
@@ -339,42 +354,31 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     } else if (warp == kRowWarp) {
         Pos p{0, 0, base_r, 0};
         for (int64_t i = first; i < n_items && ok; i += wk.step) {
-            const Item it = item_at(g, pl, wk, i, nxt, lane, false);
+            const Item it = item_at<PAIR>(g, pl, wk, i, nxt, lane, false);
             nxt = load_routing(g, pl, wk, i + wk.step, lane);
             if (it.rows == 0) continue;
             // tiles of the block's rows: its own (grouped), or those of the matrix it starts in (dense)
             const int64_t t0 = g.sorted_ids ? it.b * art : it.b * pl.tok / kMxTileRows;
             const int64_t tstride = (int64_t)kstages * kMxTileBytes;
             const uint8_t* src = g.a + kHeaderBytes + t0 * tstride;
-            const int rows = it.rows, r0 = min(rows, kMxTileRows - it.off), r1 = rows - r0;
-            const uint32_t bytes = (uint32_t)rows * 128u + (r1 > 0 ? 2048u : 1024u);
-            // a pair's CTA copies rows [h0, h1) and scale block `rank` of every tile touched
-            const int h0 = pl.pair ? (int)rank * (rows / 2) : 0, h1 = pl.pair ? h0 + rows / 2 : rows;
+            const int rows = it.rows, r0 = min(rows, kMxTileRows - it.off);   // r0 of them in the first tile
+            // a pair's CTA copies rows [h0, h1), and the scales of all
+            const int h0 = PAIR ? (int)rank * (rows / 2) : 0, h1 = PAIR ? h0 + rows / 2 : rows;
             const int a0 = min(h0, r0), a1 = min(h1, r0), b0 = max(h0, r0), b1 = max(h1, r0);   // in the first, second tile
+            const uint32_t bytes = (uint32_t)(h1 - h0) * 128u + (rows > r0 ? 2048u : 1024u);
             const uint32_t inf = (uint32_t)rows | (uint32_t)it.off << 16;
             for (int ks = 0; ks < kstages; ++ks, src += kMxTileBytes) {
                 ok = wait_free(p, r_stages);
                 if (!ok) break;
                 if (tc5::elect()) {
-                    const uint32_t bar = full_r_a + p.slot * 8, ss = p.st + tok128;
+                    const uint32_t bar = full_r_a + p.slot * 8, ss = p.st + r_codes;
                     info[p.slot] = inf;
                     tc5::arrive_expect_tx(bar, bytes);
-                    if (!pl.pair) {
-                        tc5::bulk_g2s(p.st, src + it.off * 128, (uint32_t)r0 * 128u, bar);
-                        tc5::bulk_g2s(ss, src + kMxCodeBytes, 1024u, bar);
-                        if (r1 > 0) {
-                            tc5::bulk_g2s(p.st + r0 * 128, src + tstride, (uint32_t)r1 * 128u, bar);
-                            tc5::bulk_g2s(ss + 1024, src + tstride + kMxCodeBytes, 1024u, bar);
-                        }
-                    } else {
-                        const uint32_t so = kMxCodeBytes + rank * kMxScaleBlock;
-                        if (a1 > a0)
-                            tc5::bulk_g2s_pair(p.st + a0 * 128, src + (it.off + a0) * 128, (uint32_t)(a1 - a0) * 128u, bar);
-                        if (b1 > b0)
-                            tc5::bulk_g2s_pair(p.st + b0 * 128, src + tstride + (b0 - r0) * 128, (uint32_t)(b1 - b0) * 128u, bar);
-                        tc5::bulk_g2s_pair(ss + rank * kMxScaleBlock, src + so, kMxScaleBlock, bar);
-                        if (r1 > 0) tc5::bulk_g2s_pair(ss + 1024 + rank * kMxScaleBlock, src + tstride + so, kMxScaleBlock, bar);
-                    }
+                    if (a1 > a0) tc5::bulk_g2s(p.st, src + (it.off + a0) * 128, (uint32_t)(a1 - a0) * 128u, bar);
+                    if (b1 > b0)
+                        tc5::bulk_g2s(p.st + (a1 - a0) * 128, src + tstride + (b0 - r0) * 128, (uint32_t)(b1 - b0) * 128u, bar);
+                    tc5::bulk_g2s(ss, src + kMxCodeBytes, 1024u, bar);
+                    if (rows > r0) tc5::bulk_g2s(ss + 1024, src + tstride + kMxCodeBytes, 1024u, bar);
                 }
                 __syncwarp();
                 p = next_r(p);
@@ -410,26 +414,42 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
                 ok = wait_full(full_r_a, r) && wait_full(full_w_a, w) &&
                      (!second || (wait_full(full_r_a, r2) && wait_full(full_w_a, w2)));
                 if (!ok) break;
+                if (PAIR && rank) {   // the first CTA issues for both
+                    if (tc5::elect()) tc5::arrive_at(peer_a + (turn % kTurns) * 8, 0);
+                    __syncwarp();
+                    w = second ? next_w(w2) : w2;
+                    r = second ? next_r(r2) : r2;
+                    continue;
+                }
+                ok = wait_free(second ? r2 : r, slots) &&
+                     (!PAIR || tc5::wait(peer_a + (turn % kTurns) * 8, (turn / kTurns) & 1u, &flags[1], g.err));
+                if (!ok) break;
                 if (tc5::elect()) {
                     auto copy = [&](const Pos& wp, const Pos& rp) {
-                        const uint32_t sf = sf_base + rp.slot * kScaleCols;
-                        const uint64_t dsa = tc5::desc_scales(wp.st + kMxCodeBytes), dsb = tc5::desc_scales(rp.st + tok128);
+                        const uint32_t sf = sf_base + rp.g % slots * kScaleCols;
+                        const uint64_t dsa = tc5::desc_scales(wp.st + kMxCodeBytes), dsb = tc5::desc_scales(rp.st + r_codes);
 #pragma unroll
                         for (uint32_t h = 0; h < 2; ++h) {
-                            tc5::cp_scales(sf + 4u * h, dsa + h * (kMxScaleBlock >> 4));
-                            tc5::cp_scales(sf + 8u + 8u * h, dsb + h * (kMxScaleBlock >> 4));
-                            if (two) tc5::cp_scales(sf + 12u + 8u * h, dsb + (1024u >> 4) + h * (kMxScaleBlock >> 4));
+                            tc5::cp_scales<PAIR>(sf + 4u * h, dsa + h * (kMxScaleBlock >> 4));
+                            tc5::cp_scales<PAIR>(sf + 8u + 8u * h, dsb + h * (kMxScaleBlock >> 4));
+                            if (two) tc5::cp_scales<PAIR>(sf + 12u + 8u * h, dsb + (1024u >> 4) + h * (kMxScaleBlock >> 4));
                         }
                     };
                     copy(w, r);
                     if (second) copy(w2, r2);
-                    tc5::commit(turn_a + (turn % kTurns) * 8);
+                    tc5::commit<PAIR, false>(turn_a + (turn % kTurns) * 8);
                 }
                 __syncwarp();
                 w = second ? next_w(w2) : w2;
                 r = second ? next_r(r2) : r2;
             }
         }
+        // the last instructions are done: before tensor memory is released, and before a pair's
+        // second CTA leaves, whose barriers their commits arrive on
+        if (w.g > 0) tc5::wait(done_a + ((w.g - 1) % kDone) * 8, ((w.g - 1) / kDone) & 1u, &flags[1], g.err);
+        __syncwarp();
+    } else if (warp == kMmaWarp && rank) {
+        // the first CTA of the pair issues
     } else if (warp == kMmaWarp) {
         const uint32_t sf_base = tmem + 2u * (uint32_t)pl.tok;
         Pos w{0, 0, base_w, 0}, r{0, 0, base_r, 0};
@@ -443,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             ok = tc5::wait(smem_u32(&acc_empty[buf]), ((nitem >> 1) & 1u) ^ 1u, &flags[1], g.err);
             if (!ok) break;
             const uint32_t acc = tmem + buf * (uint32_t)pl.tok;
-            const uint32_t id0 = tc5::idesc_mxf4((int)rows, 0), id2 = tc5::idesc_mxf4((int)rows, 2);
+            const uint32_t id0 = tc5::idesc_mxf4<PAIR>((int)rows, 0), id2 = tc5::idesc_mxf4<PAIR>((int)rows, 2);
             for (int ks = 0; ks < kstages; ks += 2, ++turn) {
                 const Pos w2 = next_w(w), r2 = next_r(r);
                 const bool second = ks + 1 < kstages;
@@ -453,23 +473,19 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
                 tc5::fence_after();
                 if (tc5::elect()) {
                     auto mma = [&](const Pos& wp, const Pos& rp, int k) {
-                        const uint32_t sf = sf_base + rp.slot * kScaleCols;
+                        const uint32_t sf = sf_base + rp.g % slots * kScaleCols;
                         const uint64_t da = tc5::desc_sw128(wp.st), db = tc5::desc_sw128(rp.st);
                         const int nk = min(4, (g.K - k * kMxTileCols + 63) / 64);
 #pragma unroll
                         for (uint32_t kk = 0; kk < 4; ++kk)
                             if ((int)kk < nk)
-                                tc5::mma_mxf4(acc, da + 2u * kk, db + 2u * kk, kk & 1 ? id2 : id0, sf + 4u * (kk >> 1),
+                                tc5::mma_mxf4<PAIR>(acc, da + 2u * kk, db + 2u * kk, kk & 1 ? id2 : id0, sf + 4u * (kk >> 1),
                                               sf + 8u + 8u * (kk >> 1) + off, k > 0 || kk > 0 ? 1u : 0u);
-                        const uint32_t bar = done_a + (wp.g % kDone) * 8;
-                        if (pl.pair)
-                            tc5::commit_pair(bar);
-                        else
-                            tc5::commit(bar);
+                        tc5::commit<PAIR, true>(done_a + (wp.g % kDone) * 8);
                     };
                     mma(w, r, ks);
                     if (second) mma(w2, r2, ks + 1);
-                    if (ks + 2 >= kstages) tc5::commit(smem_u32(&acc_full[buf]));
+                    if (ks + 2 >= kstages) tc5::commit<PAIR, true>(smem_u32(&acc_full[buf]));
                 }
                 __syncwarp();
                 w = second ? next_w(w2) : w2;
@@ -477,15 +493,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             }
             ++nitem;
         }
-        // the last instructions are done before the tensor memory is released
-        if (w.g > 0) tc5::wait(done_a + ((w.g - 1) % kDone) * 8, ((w.g - 1) / kDone) & 1u, &flags[1], g.err);
-        __syncwarp();
     } else {
         const int wg = warp >> 2, quarter = warp & 3;
         int64_t nitem = 0;
         for (int64_t i = first; i < n_items; i += wk.step) {
             const Routing cur = nxt;
-            const Item it = item_at(g, pl, wk, i, cur, lane, warp == 0);
+            const Item it = item_at<PAIR>(g, pl, wk, i, cur, lane, warp == 0);
             nxt = load_routing(g, pl, wk, i + wk.step, lane);
             if (it.rows == 0) continue;
             const int buf = (int)(nitem & 1);
@@ -500,15 +513,20 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             }
             tc5::fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            if (lane == 0) {
+                if (PAIR)
+                    tc5::arrive_at(smem_u32(&acc_empty[buf]), 0);
+                else
+                    mbar_arrive(&acc_empty[buf]);
+            }
             ++nitem;
         }
     }
     tc5::fence_before();
     __syncthreads();
-    if (pl.pair) tc5::cluster_sync();   // the other CTA's copies and commits into this one are done
+    if (PAIR) tc5::cluster_sync();   // the pair's instructions, and arrivals on the other CTA's barriers, are done
     tc5::fence_after();
-    if (warp == kMmaWarp) tc5::dealloc(tmem, kTmemCols);
+    if (warp == kMmaWarp) tc5::dealloc<PAIR>(tmem, kTmemCols);
 }
 
 cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
@@ -518,34 +536,34 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
     pl.tok = g.sorted_ids ? (int)g.a_rows : (g.a_rows > 128 ? 192 : (g.a_rows > 64 ? 128 : 64));
     // 128-row tiles a block may touch (dense blocks of 192 start at row 0 or 64 of one)
     const int tiles = (pl.tok + kMxTileRows - 1) / kMxTileRows;
-    pl.r_bytes = pl.tok * 128 + 1024 * tiles;
-    const size_t fixed = 1024 + kEpiWarps * kStgBytes + (2 * kMaxStages + kDone + kTurns + 4) * 8 + 64 + 4 * kMaxStages;
+    const int64_t ntiles = (g.N + kMxTileRows - 1) / kMxTileRows;
+    const bool pair = pl.tok >= kPairRows && ntiles > 1;
+    pl.r_bytes = pl.tok * (pair ? 64 : 128) + 1024 * tiles;
+    const size_t fixed = 1024 + kEpiWarps * kStgBytes + (2 * kMaxStages + kDone + 2 * kTurns + 4) * 8 + 64 + 4 * kMaxStages;
     const size_t room = kSmemBudget - fixed;
-    // Large blocks: four stages of rows (two turns), the rest for weights; small ones: as many of each.
-    pl.r_stages = 4;
-    if (pl.tok < kPairRows) pl.r_stages = (int)(room / (kMxTileBytes + pl.r_bytes));
-    const int slots = (int)((kTmemCols - 2 * pl.tok) / kScaleCols);
-    pl.r_stages = pl.r_stages > slots ? slots : (pl.r_stages > kMaxStages ? kMaxStages : pl.r_stages);
+    pl.slots = (int)((kTmemCols - 2 * pl.tok) / kScaleCols);
+    if (pl.slots > kMaxStages) pl.slots = kMaxStages;
+    pl.r_stages = (int)(room / (kMxTileBytes + pl.r_bytes));
+    if (pl.r_stages > kMaxStages) pl.r_stages = kMaxStages;
     pl.w_stages = (int)((room - (size_t)pl.r_stages * pl.r_bytes) / kMxTileBytes);
     if (pl.w_stages > kMaxStages) pl.w_stages = kMaxStages;
-    if (pl.r_stages < 2 || pl.w_stages < 2) return cudaErrorInvalidConfiguration;
+    if (pl.r_stages < 2 || pl.w_stages < 2 || pl.slots < 2) return cudaErrorInvalidConfiguration;
     // one CTA per SM: it takes the whole tensor memory, and more than half of the shared memory
     const size_t smem = fixed + (size_t)pl.w_stages * kMxTileBytes + (size_t)pl.r_stages * pl.r_bytes;
-    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(mx_gemm_kernel), kSmemBudget);
+    void (*kern)(MxGemmArgs, MxPlan) = pair ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmemBudget);
     if (e != cudaSuccess) return e;
-    const int64_t ntiles = (g.N + kMxTileRows - 1) / kMxTileRows;
     const int64_t blocks = g.sorted_ids ? g.a_groups : (g.a_rows + pl.tok - 1) / pl.tok;
     const int64_t sms = device_info().sm_count;
-    pl.pair = pl.tok >= kPairRows && ntiles > 1;
-    const int64_t items = pl.pair ? blocks * ((ntiles + 1) / 2) : blocks * ntiles, ctas = pl.pair ? sms / 2 : sms;
+    const int64_t items = pair ? blocks * ((ntiles + 1) / 2) : blocks * ntiles, ctas = pair ? sms / 2 : sms;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((items < ctas ? items : ctas) * (pl.pair ? 2 : 1)));
+    cfg.gridDim = dim3((unsigned)((items < ctas ? items : ctas) * (pair ? 2 : 1)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (pl.pair) {
+    if (pair) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
         attr[n].val.clusterDim.x = 2;
         attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
@@ -558,7 +576,7 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, mx_gemm_kernel, g, pl);
+    return cudaLaunchKernelEx(&cfg, kern, g, pl);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

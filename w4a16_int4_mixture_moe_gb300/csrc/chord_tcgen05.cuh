@@ -9,22 +9,45 @@
 namespace chord {
 namespace tc5 {
 
+// PAIR: the instructions of a cluster of two CTAs (cta_group::2).  Tensor memory is allocated
+// and freed by a warp of each; one thread of the first CTA issues the copies and matrix
+// instructions for both.
+template <bool PAIR>
 __device__ __forceinline__ void alloc(uint32_t* slot, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
 }
+template <bool PAIR>
 __device__ __forceinline__ void dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// Arrive on `bar` once every tcgen05 operation this thread issued has completed.
+// Arrive on `bar` (ALL: of both CTAs of a pair) once every tcgen05 operation this thread
+// issued has completed.
+template <bool PAIR, bool ALL>
 __device__ __forceinline__ void commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (!PAIR)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    else if constexpr (!ALL)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
 }
 
 // One lane of the (converged) warp.  The issuing warp runs its loop with all
@@ -40,24 +63,7 @@ __device__ __forceinline__ bool elect() {
     return p != 0;
 }
 
-// The same, on this barrier of both CTAs of a cluster of two.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-}
-
-// cp.async.bulk into both CTAs of a cluster of two: the same shared-memory offset,
-// bytes counted on the same barrier of each.
-__device__ __forceinline__ void bulk_g2s_pair(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1], %2, [%3], "
-        "%4;" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar), "h"((uint16_t)3)
-        : "memory");
-}
-// Into this CTA, and the arrivals that go with it, on shared-memory addresses.
+// cp.async.bulk into this CTA, and the arrivals that go with it, on shared-memory addresses.
 __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
@@ -68,6 +74,14 @@ __device__ __forceinline__ void arrive_expect_tx(uint32_t bar, uint32_t bytes) {
 }
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// On the barrier at the same address of CTA `cta` of the cluster.  Tells it of asynchronous
+// copies and tensor-memory loads that this thread has seen complete; nothing of its own
+// stores (with release.cluster, which waits for those, a turn of the product took twice as long).
+__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t cta) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(bar), "r"(cta));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -80,21 +94,37 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // D[128 x N] (+)= (A x scales)[128 x 64] * (B x scales)[N x 64]^T, E2M1 codes in
-// shared memory, one E8M0 scale per 32 columns in tensor memory.
+// shared memory, one E8M0 scale per 32 columns in tensor memory.  PAIR: D, A and A's scales
+// are 256 rows, the first CTA's 128 and the second's; B's first half of rows is in the
+// first CTA's shared memory, the other in the second's, and all its scales in both's
+// tensor memory.
+template <bool PAIR>
 __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
                                          uint32_t sfb, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
 }
 
 // 512 bytes of shared memory (32 rows of 16 bytes) to four tensor-memory
-// columns, the 32 lanes repeated in all four lane quarters.
+// columns, the 32 lanes repeated in all four lane quarters.  PAIR: each CTA's to its own.
+template <bool PAIR>
 __device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&v)[16]) {
@@ -119,11 +149,12 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
            (uint64_t)1u << 46;
 }
 
-// Instruction descriptor: E2M1 x E2M1, E8M0 scales, FP32 accumulator, M = 128;
+// Instruction descriptor: E2M1 x E2M1, E8M0 scales, FP32 accumulator, M = 128 (a pair: 256);
 // sf: which two of the four scales of a tensor-memory word the instruction
 // takes (0 or 2), for both operands.
+template <bool PAIR>
 __device__ __forceinline__ uint32_t idesc_mxf4(int n, uint32_t sf) {
-    return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24) |
+    return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (PAIR ? 2u << 27 : 1u << 27) |
            (sf << 29);
 }
 

@@ -53,8 +53,9 @@ struct MxGemmArgs {
 // turn's copies have landed there.  Small blocks leave the rows' share small, and the pair's
 // extra hop costs more than it saves (64 rows: 135 us single, 141 paired; 112 rows: equal).
 // What bounds it: the weights' bytes (4096 x 7168 for 8192 rows: 749 MB, and 67 MB of C, in
-// 152 us = 5.4 TB/s; reading these weights alone takes 130 us), and in the dense product, whose tiles come from L2, those copies again: 650 MB in 59 us, 51 us with no
-// matrix instruction issued; the instructions alone take 40.
+// 152 us = 5.4 TB/s; reading these weights alone takes 130 us), and in the dense product,
+// whose tiles come from L2, those copies again: 650 MB in 59 us, 51 us with no matrix
+// instruction issued; the instructions alone take 40.
 constexpr int kEpiWarps = 8;
 constexpr int kWeightWarp = kEpiWarps, kRowWarp = kEpiWarps + 1, kScaleWarp = kEpiWarps + 2, kMmaWarp = kEpiWarps + 3;
 constexpr int kThreads = (kEpiWarps + 4) * 32;

@@ -635,6 +635,10 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
     }
 }
 
+// One token on 8 experts of 2 x 256 x 7168 is latency: 3 us to the first weights' copies, 2 to
+// their arrival, then 16.5 MB.  More tokens: the weights' stream, with instruction issue
+// close behind (8 tokens, 57 experts: 117 MB at 5.0 TB/s; 16 tokens INT4 issue 2.3 of 4
+// instructions a cycle; MXFP4 codes take 17 operations for eight against 9).
 template <bool MX>
 __global__ void __launch_bounds__(kThreads, 4) few_gate_up_kernel(const FewArgs a) {
     using S = Stage<MX>;
@@ -823,6 +827,12 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
 // 56 tiles of 7168 rows would take a second wave): each CTA leaves its sums in the workspace
 // and the tile's last one adds them.  Always in slice order, so the result does not depend
 // on which CTA is last.
+// Bound as gate_up is: 8 tokens, 57 experts of 7168 x 256: 58 MB in 12 us once its first
+// weights are there; before that 5 us pass between gate_up's last stage and this kernel's
+// first (its end, this one's routing, a ring's fill), half of it hidden where this kernel's
+// CTAs fit beside gate_up's.  (Both halves in one cooperative launch, the ring filled
+// ahead of a grid barrier, measured the same: 8 tokens 58.6 us against 58.5, 16 tokens 93
+// against 89.)
 template <bool MX, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) few_down_kernel(const FewArgs a) {
     using S = Stage<MX>;

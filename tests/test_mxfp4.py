@@ -313,6 +313,26 @@ def test_dense_product_exact_regime(M, N, K):
 
 
 @gpu
+@pytest.mark.parametrize("M,N,K", [(840, 4900, 4640), (64, 20500, 2080)])
+def test_dense_product_many_items(M, N, K):
+    """More blocks of C than resident CTAs or pairs of CTAs, and more K stages than
+    any ring holds, in the exact regime (sums below 36 * K < 2^24)."""
+    need_gpu()
+    g = torch.Generator(device=DEV).manual_seed(M)
+    vals = torch.tensor([0., 1, -1, 2, -2, 3, -3, 4, 6, -6, .5, 1.5], device=DEV)
+    a, w = (vals[torch.randint(0, 12, (1, n, K), generator=g, device=DEV)] for n in (M, N))
+    a[:, :, ::32] = 4.0
+    w[:, :, 31::32] = -4.0
+    C = torch.empty((M, N), device=DEV)
+    aq, wq = quantise(a), quantise(w)
+    for _ in range(2):
+        C.fill_(float("nan"))
+        chord.chord_mxfp4_gemm(aq, M, wq, N, K, C)
+        assert torch.equal(C.double(), a[0].double() @ w[0].double().T)
+    assert chord.chord_get_device_error() == 0
+
+
+@gpu
 def test_dense_product_extreme_scales():
     """Scales far from 1 on both sides: powers of two that cancel, and NaN
     scales that stay in their row and column."""

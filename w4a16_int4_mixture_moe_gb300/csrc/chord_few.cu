@@ -821,6 +821,12 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
     }
 }
 
+// What the slices of a cluster send one another, beside the ring: a CTA's share of the
+// (16 rows, 8 tokens) tiles, from every slice.
+__host__ __device__ __forceinline__ size_t down_part_bytes(int nt, int cluster) {
+    return (size_t)((kConsumers * 2 * nt + cluster - 1) / cluster) * cluster * 512;
+}
+
 // gridDim.x = output tiles of 128 rows x a.cluster list slices (slice fastest).  Short
 // lists: the slices are a cluster and exchange their FP32 sums through distributed shared
 // memory.  Long ones, whose rings leave room for three CTAs per SM (51 clusters of eight, and
@@ -842,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) few_down_kernel(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t* s_ids;
     float* s_w;
-    const Route rt = prologue<MX>(a, sh, smem + a.depth * a.stage_bytes + (a.clustered ? kConsumers * 2 * NT * 512 : 0), s_ids,
+    const Route rt = prologue<MX>(a, sh, smem + a.depth * a.stage_bytes + (a.clustered ? down_part_bytes(NT, a.cluster) : 0), s_ids,
                                   s_w, false);
     if (!(sh.flags & 1)) return;   // the same in every CTA; the gate_up kernel reported it
     if (a.clustered) cluster_sync_all();   // every CTA runs before another one's sums arrive
@@ -1001,12 +1007,15 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     // gate_up: three CTAs per SM while the items of an even routing then run in one wave
     // (they spread evenly: 16 tokens TP8, 436 items, done after 52 us against 64 with
     // four per SM), else four (32 tokens EP8, 768 items: 67 us against 82).  Where they
-    // would leave half of the GPU idle, a cluster shares each item's K range.
+    // would leave half of the GPU idle, a cluster shares each item's K range, three stages or
+    // more a CTA (4 tokens, 16 experts of 2 x 1024 x 1024, eight stages: in twos 21.6 us, in
+    // fours 24.7).
     const int mt = (a.I + 63) / 64, stages = (a.H + S::kCols - 1) / S::kCols;
     const int64_t items = (int64_t)a.slot_cap * mt;
-    const double even = a.E * (1.0 - pow(1.0 - 1.0 / a.E, (double)a.T * a.topk)) * mt;
+    const double pairs = (double)a.T * a.topk, hit = a.E * (1.0 - pow(1.0 - 1.0 / a.E, pairs));   // experts with a token
+    const double passes = hit * fmax(1.0, pairs / hit / kPassTokens + 0.5), even = passes * mt;
     a.cluster = 8;
-    while (a.cluster > 1 && (even * a.cluster > 4.0 * sms || a.cluster > stages)) a.cluster >>= 1;
+    while (a.cluster > 1 && (even * a.cluster > 4.0 * sms || a.cluster * 3 > stages)) a.cluster >>= 1;
     const int per_sm = a.cluster == 1 && even <= 3.0 * sms ? 3 : 4;
     const int64_t resident = (int64_t)sms * per_sm / a.cluster;
     const size_t third = 72 * 1024, up_room = per_sm == 3 ? third : 53 * 1024, beside = route + (a.cluster > 1 ? 8192 : 0);
@@ -1020,12 +1029,19 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     // once at three CTAs per SM
     const int64_t list = (int64_t)a.slot_cap * ((a.I + S::kCols - 1) / S::kCols);
     const int tiles = (a.H + 127) / 128;
-    a.cluster = down_slices(a.H, list);
+    const int slices = down_slices(a.H, list);
     a.stage_bytes = S::down_bytes(tokens);
+    // in clusters of up to eight where the ring then leaves room for four CTAs per SM (16
+    // tokens of a layer of 8 experts, 256 x 128: 17.5 us, joined by the last CTA 19.6)
+    a.cluster = slices < 8 ? slices : 8;
     a.depth = ring_depth(third - route, a.stage_bytes, (list + a.cluster - 1) / a.cluster);
-    smem = (size_t)a.depth * a.stage_bytes + route;
-    a.clustered = NT == 1 && a.cluster == 8 && smem + kConsumers * 2 * NT * 512 <= 53 * 1024;   // four CTAs per SM
-    if (a.clustered) smem += kConsumers * 2 * NT * 512;
+    smem = (size_t)a.depth * a.stage_bytes + route + down_part_bytes(NT, a.cluster);
+    a.clustered = a.cluster > 1 && smem <= 53 * 1024;
+    if (!a.clustered) {
+        a.cluster = slices;
+        a.depth = ring_depth(third - route, a.stage_bytes, (list + a.cluster - 1) / a.cluster);
+        smem = (size_t)a.depth * a.stage_bytes + route;
+    }
     return launch(few_down_kernel<MX, NT>, a, (unsigned)tiles, smem, a.clustered != 0, pdl_enabled(), st);
 }
 

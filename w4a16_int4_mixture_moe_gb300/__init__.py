@@ -118,6 +118,8 @@ def build(force: bool = False) -> str:
 def load():
     """Load libchord.so (built in-tree); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -137,17 +139,23 @@ def _check(st: int, what: str):
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+_torch = None
 
 
 def _s(stream):
     if stream is None:
-        import torch
-        if torch.cuda.is_initialized():
+        global _torch
+        if _torch is None:
+            import torch
+            _torch = torch
+        if _torch.cuda.is_initialized():
             # the handle of torch.cuda.current_stream() without its Python object (3.4 us of a 9 us call)
-            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(getattr(stream, "cuda_stream", stream) or 0)
+            return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
+        stream = _torch.cuda.current_stream()
+    return getattr(stream, "cuda_stream", stream) or 0
 
 
 def _o(opts):
@@ -155,7 +163,7 @@ def _o(opts):
 
 
 def _nbytes(t):
-    return t.numel() * t.element_size()
+    return t.nbytes
 
 
 # --- entry points (same names as the C ABI) ---------------------------------
@@ -345,10 +353,11 @@ def chord_mxfp4_rows_bytes(capacity: int, block_m: int, K: int) -> int:
 def chord_mxfp4_quantize(src, packed, stream=None):
     """src bf16 or float32 [G, N, K] (unit stride along K, any row and matrix stride), packed uint8 output."""
     G, N, K = src.shape
-    if K > 1 and src.stride(2) != 1:
+    mat_stride, row_stride, step = src.stride()
+    if K > 1 and step != 1:
         raise ChordError(1, "chord_mxfp4_quantize: src needs unit stride along K")
-    _check(load().chord_mxfp4_quantize(_p(src), _dtype(src, "chord_mxfp4_quantize"), src.stride(1), src.stride(0), G,
-                                       N, K, _p(packed), _nbytes(packed), _s(stream)), "chord_mxfp4_quantize")
+    _check(load().chord_mxfp4_quantize(_p(src), _dtype(src, "chord_mxfp4_quantize"), row_stride, mat_stride, G, N, K,
+                                       _p(packed), _nbytes(packed), _s(stream)), "chord_mxfp4_quantize")
 
 
 def chord_mxfp4_quantize_rows(A, a_row_divisor: int, sorted_ids, num_tokens_padded, block_m: int, num_pairs: int,

@@ -57,8 +57,7 @@ struct FewArgs {
     int validate;        // report ids outside [-1, E)
     int slot_cap;        // most passes a call can need
     int cluster;         // CTAs that share an item (gate_up, a cluster) or an output tile (down, list slices)
-    int clustered;       // down: the slices are a cluster
-    float4* part;        // down, not clustered: the slices' sums
+    float4* part;        // down, slices that are not a cluster: their sums
     int* joined;         // down: CTAs of each output tile that have left theirs
     int depth;           // stages of the ring
     int stage_bytes;
@@ -839,8 +838,10 @@ __host__ __device__ __forceinline__ size_t down_part_bytes(int nt, int cluster) 
 // CTAs fit beside gate_up's.  (Both halves in one cooperative launch, the ring filled
 // ahead of a grid barrier, measured the same: 8 tokens 58.6 us against 58.5, 16 tokens 93
 // against 89.)
-template <bool MX, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) few_down_kernel(const FewArgs a) {
+// CLUSTERED: four CTAs per SM.  Else three, so up to 128 registers a thread: with 96 the eight
+// tokens of MXFP4 TP8 took 59.9 us instead of 54.1.
+template <bool MX, int NT, bool CLUSTERED>
+__global__ void __launch_bounds__(kThreads, CLUSTERED ? 4 : 3) few_down_kernel(const FewArgs a) {
     using S = Stage<MX>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared sh;
@@ -848,10 +849,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) few_down_kernel(con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int32_t* s_ids;
     float* s_w;
-    const Route rt = prologue<MX>(a, sh, smem + a.depth * a.stage_bytes + (a.clustered ? down_part_bytes(NT, a.cluster) : 0), s_ids,
+    const Route rt = prologue<MX>(a, sh, smem + a.depth * a.stage_bytes + (CLUSTERED ? down_part_bytes(NT, a.cluster) : 0), s_ids,
                                   s_w, false);
     if (!(sh.flags & 1)) return;   // the same in every CTA; the gate_up kernel reported it
-    if (a.clustered) cluster_sync_all();   // every CTA runs before another one's sums arrive
+    if (CLUSTERED) cluster_sync_all();   // every CTA runs before another one's sums arrive
     const int rank = blockIdx.x % a.cluster, tile = blockIdx.x / a.cluster;
     const int kst = (a.I + S::kCols - 1) / S::kCols, total = rt.slots * kst;
     const int v0 = (int)((int64_t)rank * total / a.cluster), v1 = (int)((int64_t)(rank + 1) * total / a.cluster);
@@ -886,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 3) few_down_kernel(con
             for (int nt = 0; nt < NT; ++nt) write((2 * warp + i) * NT + nt, sum_of(i, nt));
         return;
     }
-    if (a.clustered) {
+    if constexpr (CLUSTERED) {
         // short lists: tile q belongs to CTA q mod cluster, which is sent every slice's sums
         float4* buf = reinterpret_cast<float4*>(smem + a.depth * a.stage_bytes);   // [tile of its own][slice][lane]
         if (warp < kConsumers) {
@@ -1036,13 +1037,15 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     a.cluster = slices < 8 ? slices : 8;
     a.depth = ring_depth(third - route, a.stage_bytes, (list + a.cluster - 1) / a.cluster);
     smem = (size_t)a.depth * a.stage_bytes + route + down_part_bytes(NT, a.cluster);
-    a.clustered = a.cluster > 1 && smem <= 53 * 1024;
-    if (!a.clustered) {
+    const bool clustered = a.cluster > 1 && smem <= 53 * 1024;
+    if (!clustered) {
         a.cluster = slices;
         a.depth = ring_depth(third - route, a.stage_bytes, (list + a.cluster - 1) / a.cluster);
         smem = (size_t)a.depth * a.stage_bytes + route;
     }
-    return launch(few_down_kernel<MX, NT>, a, (unsigned)tiles, smem, a.clustered != 0, pdl_enabled(), st);
+    const unsigned groups = (unsigned)tiles;
+    return clustered ? launch(few_down_kernel<MX, NT, true>, a, groups, smem, true, pdl_enabled(), st)
+                     : launch(few_down_kernel<MX, NT, false>, a, groups, smem, false, pdl_enabled(), st);
 }
 
 cudaError_t launch_few(const FewArgs& a, bool mx, cudaStream_t st) {

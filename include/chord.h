@@ -610,7 +610,7 @@ size_t chord_moe_few_workspace_bytes(int T, int topk, int E, int H, int I);
  *               calls that overlap on the GPU need one each
  * The result does not depend on the order in which blocks run.  An expert with
  * more than eight tokens is read once for every eight, so for few experts with
- * many tokens each (32 tokens over 8 experts of 4096 x 1024: 69 us against 54)
+ * many tokens each (32 tokens over 8 experts of 4096 x 1024: 67 us against 54)
  * chord_moe_layer is the faster call. */
 chord_status chord_moe_layer_few(const void *x, const int32_t *topk_ids, const float *topk_w, int T,
                                  int topk, int E, int H, int I, int weights, const void *packed_w13,

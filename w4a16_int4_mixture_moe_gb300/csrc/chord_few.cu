@@ -1006,8 +1006,8 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     const int sms = device_info().sm_count;
     const size_t route = route_bytes(a.E, a.T * a.topk, a.slot_cap);
     // gate_up: three CTAs per SM while the items of an even routing then run in one wave
-    // (they spread evenly: 16 tokens TP8, 436 items, done after 52 us against 64 with
-    // four per SM), else four (32 tokens EP8, 768 items: 67 us against 82).  Where they
+    // (they spread evenly: the layer for 16 tokens TP8, 436 items, 84 us against 92 with four per
+    // SM), else four (32 tokens EP8, 768 items: 99 us against 111).  Where they
     // would leave half of the GPU idle, a cluster shares each item's K range, three stages or
     // more a CTA (4 tokens, 16 experts of 2 x 1024 x 1024, eight stages: in twos 21.6 us, in
     // fours 24.7).

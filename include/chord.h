@@ -517,7 +517,7 @@ int chord_moe_layer_cache_clear(void);
  * and the data offset 256 at word 10) followed by tiles of 128 rows x 256 columns
  * (17408 bytes), the last ones padded with zeros.  K % 32 == 0, N is free.
  *
- * Bytes of such a matrix; 0 on bad arguments. */
+ * Bytes of such a matrix; 0 on bad arguments, and for a size past 2^62 bytes. */
 size_t chord_mxfp4_bytes(int64_t G, int64_t N, int K);
 
 /* Quantise src [G, N, K] (CHORD_DTYPE_BF16 or CHORD_DTYPE_F32, unit stride along

@@ -104,6 +104,24 @@ def test_sizes():
     assert chord.chord_mxfp4_rows_bytes(95, 32, 64) == 0
 
 
+def test_sizes_past_64_bits_are_refused():
+    """A byte count that does not fit is no size (2^30 groups of 2^31 x 2^31 once
+    gave 256), and every call that checks against it refuses the shape."""
+    big = 2 ** 31 - 32
+    assert chord.chord_mxfp4_bytes(2 ** 30, 2 ** 31 - 1, big) == 0
+    assert chord.chord_mxfp4_bytes(2 ** 31 - 1, 2 ** 31 - 1, big) == 0
+    assert chord.chord_mxfp4_rows_bytes(2 ** 31 - 2, 2, big) == 0
+    assert chord.chord_mxfp4_bytes(1, 2 ** 31 - 1, big) == 256 + 2 ** 24 * 2 ** 23 * 17408      # 2^61: the largest group
+    p = ctypes.c_void_p(1 << 20)
+    lib = chord.load()
+    assert lib.chord_mxfp4_quantize(p, 0, big, 0, 2 ** 30, 2 ** 31 - 1, big, p, 256, None) == 2
+    assert lib.chord_mxfp4_dequantize(p, 256, 2 ** 30, 2 ** 31 - 1, big, p, 0, None) == 2
+    for wrong in (0, 256):
+        assert lib.chord_mxfp4_quantize_rows(p, 0, 4, big, 1, big, p, p, 2 ** 31 - 2, 2, 4, p, wrong, None) == 3
+        assert lib.chord_mxfp4_moe_gemm(p, chord.chord_mxfp4_rows_bytes(64, 32, big), p, wrong, 2 ** 30, big, big, p, p, p,
+                                        64, 32, 8, p, 0, None, None) == 3
+
+
 def test_select_block_m():
     for T, topk, E in [(1, 1, 8), (1, 8, 384), (64, 8, 48), (1024, 8, 48), (4096, 8, 48), (100000, 8, 8), (0, 8, 8)]:
         bm = chord.chord_mxfp4_select_block_m(T, topk, E, E)

@@ -493,7 +493,10 @@ extern "C" {
 
 size_t chord_mxfp4_bytes(int64_t G, int64_t N, int K) {
     if (G < 0 || N < 0 || K <= 0 || K % kGroup || G > INT32_MAX || N > INT32_MAX) return 0;
-    return (size_t)kHeaderBytes + (size_t)G * (size_t)mx_group_bytes(N, K);
+    const unsigned long long group = mx_group_bytes(N, K);   // below 2^62
+    // what 64 bits of byte offset cannot hold is no size: a wrapped one would pass for a small buffer
+    if (group && (unsigned long long)G > ((1ull << 62) - kHeaderBytes) / group) return 0;
+    return (size_t)kHeaderBytes + (size_t)G * (size_t)group;
 }
 
 size_t chord_mxfp4_rows_bytes(int64_t capacity, int block_m, int K) {
@@ -528,7 +531,8 @@ chord_status chord_mxfp4_quantize_rows(const void* A, int a_dtype, int64_t a_row
         return CHORD_ERR_INVALID_ARG;
     if (K % kGroup || num_pairs >= INT32_MAX || capacity >= INT32_MAX) return CHORD_ERR_UNSUPPORTED;
     if (capacity % block_m) return CHORD_ERR_INVALID_ARG;
-    if (packed_bytes != chord_mxfp4_rows_bytes(capacity, block_m, K)) return CHORD_ERR_LAYOUT_MISMATCH;
+    const size_t need = chord_mxfp4_rows_bytes(capacity, block_m, K);
+    if (need == 0 || packed_bytes != need) return CHORD_ERR_LAYOUT_MISMATCH;
     if (a_rows > 1 && row_stride < K) return CHORD_ERR_INVALID_ARG;
     if (!packed || !aligned16(packed) || !num_tokens_padded || (capacity > 0 && !sorted_ids))
         return CHORD_ERR_INVALID_ARG;

@@ -620,8 +620,8 @@ chord_status chord_mxfp4_moe_gemm(const void* Aq, size_t aq_bytes, const void* p
     if (K % kGroup || block_m % 16 || block_m > kMxMaxBlockM || num_pairs >= INT32_MAX || capacity >= INT32_MAX)
         return CHORD_ERR_UNSUPPORTED;
     if (capacity % block_m || (c_dtype != CHORD_DTYPE_BF16 && c_dtype != CHORD_DTYPE_F32)) return CHORD_ERR_INVALID_ARG;
-    if (packed_bytes != chord_mxfp4_bytes(E, N, K) || aq_bytes != chord_mxfp4_rows_bytes(capacity, block_m, K))
-        return CHORD_ERR_LAYOUT_MISMATCH;
+    const size_t need_w = chord_mxfp4_bytes(E, N, K), need_a = chord_mxfp4_rows_bytes(capacity, block_m, K);
+    if (need_w == 0 || packed_bytes != need_w || need_a == 0 || aq_bytes != need_a) return CHORD_ERR_LAYOUT_MISMATCH;
     if (!packed || !aligned16(packed) || !Aq || !aligned16(Aq) || !num_tokens_padded ||
         (capacity > 0 && (!sorted_ids || !expert_ids)) || (num_pairs > 0 && (!C || !aligned16(C))))
         return CHORD_ERR_INVALID_ARG;

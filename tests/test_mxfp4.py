@@ -351,6 +351,62 @@ def test_dense_product_many_items(M, N, K):
 
 
 @gpu
+@pytest.mark.parametrize("M,N,K", [(96, 200, 256), (97, 640, 2304), (208, 1100, 7200), (1000, 3000, 1312), (2500, 388, 4640)])
+def test_pairs_of_ctas_repeat_bit_for_bit(M, N, K):
+    """Blocks that run in pairs of CTAs (dense blocks of 128 or 192 rows, an odd or even
+    number of 128-row tiles of N, odd and even numbers of K stages up to more than any
+    ring holds): exact in every one of many calls, other work between them."""
+    need_gpu()
+    g = torch.Generator(device=DEV).manual_seed(M + N + K)
+    vals = torch.tensor([0., 1, -1, 2, -2, 3, -3, 4, 6, -6, .5, 1.5], device=DEV)
+    a, w = (vals[torch.randint(0, 12, (1, n, K), generator=g, device=DEV)] for n in (M, N))
+    a[:, :, ::32] = 4.0
+    w[:, :, 31::32] = -4.0
+    aq, wq = quantise(a), quantise(w)
+    want = (a[0].double() @ w[0].double().T).float()
+    C = torch.empty((M, N), device=DEV)
+    noise = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+    for i in range(30):
+        C.fill_(float("nan"))
+        if i % 3 == 0:
+            noise.fill_(i)                       # the operands leave part of L2
+        chord.chord_mxfp4_gemm(aq, M, wq, N, K, C)
+        assert torch.equal(C, want), i
+    assert chord.chord_get_device_error() == 0
+
+
+@gpu
+@pytest.mark.parametrize("bm", [96, 112, 160, 208])
+@pytest.mark.parametrize("N,K", [(384, 544), (640, 2080), (1000, 4096)])
+def test_grouped_pairs_of_ctas(bm, N, K):
+    """Grouped blocks that run in pairs: full, ragged and nearly empty blocks of one
+    call, exact regime."""
+    need_gpu()
+    g = torch.Generator().manual_seed(bm + N + K)
+    vals = torch.tensor([0., 1, -1, 2, -2, 3, -3, 4, 6, -6, .5, 1.5])
+    E, counts = 9, [bm, 1, 0, 2 * bm + 17, bm - 8, 16, bm + 1, 129, 64]
+    flat = torch.tensor([e for e, c in enumerate(counts) for _ in range(c)], dtype=torch.int32)
+    flat = flat[torch.randperm(flat.numel(), generator=g)]
+    T = flat.numel()
+    x, w = vals[torch.randint(0, 12, (T, K), generator=g)], vals[torch.randint(0, 12, (E, N, K), generator=g)]
+    x[:, ::32] = 4.0
+    w[:, :, 31::32] = -4.0
+    s, e, n = align(flat.view(T, 1).to(DEV), E, bm)
+    xq = torch.full((chord.chord_mxfp4_rows_bytes(s.numel(), bm, K),), 0xFF, dtype=torch.uint8, device=DEV)
+    wq = quantise(w.to(DEV))
+    xd, wd, fd = x.to(DEV).double(), w.to(DEV).double(), flat.to(DEV)
+    want = torch.empty((T, N), dtype=torch.float64, device=DEV)
+    for ex in range(E):
+        want[fd == ex] = xd[fd == ex] @ wd[ex].T
+    for _ in range(5):
+        chord.chord_mxfp4_quantize_rows(x.to(DEV), 1, s, n, bm, T, xq)
+        C = torch.full((T, N), float("nan"), device=DEV)
+        chord.chord_mxfp4_moe_gemm(xq, wq, E, N, K, s, e, n, bm, T, C)
+        assert torch.equal(C.double(), want)
+    assert chord.chord_get_device_error() == 0
+
+
+@gpu
 def test_dense_product_extreme_scales():
     """Scales far from 1 on both sides: powers of two that cancel, and NaN
     scales that stay in their row and column."""

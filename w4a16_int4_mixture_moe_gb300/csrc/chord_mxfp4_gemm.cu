@@ -2,6 +2,7 @@
 //   C[p, n] = sum_k a[row(p), k] * w[e, n, k]     (FP32 sums),
 // dense (one weight matrix, row p of C is row p of a) or grouped by expert
 // through the routing arrays of chord_moe_align.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -49,9 +50,13 @@ struct MxGemmArgs {
 // block's rows, which the tensor cores of both read, so a stage is 31 KB a CTA instead of
 // 44 and the rings are half as deep again (of measured 208-row blocks, 48 experts: 4096 x 7168
 // 152 us against 174 with single CTAs, 7168 x 2048 104 against 113; dense 4096 x 4096 x
-// 7168 59 against 76).  The first CTA issues for both; the second one's scale warp tells it when a
-// turn's copies have landed there.  Small blocks leave the rows' share small, and the pair's
-// extra hop costs more than it saves (64 rows: 135 us single, 141 paired; 112 rows: equal).
+// 7168 59 against 76).  The first CTA issues for both.  What the second one has copied reaches it
+// through the copies themselves: they are counted on the first CTA's barrier, which only
+// copies through a tensor map can (cta_group::2), so a stage is full there when both CTAs' bytes
+// have landed.  (A barrier of the second CTA's own and an arrival on the first's would have to
+// release at cluster scope: 229 us for 152, 141 for 104, 78 for 59.)  A block's rows go in boxes of 32 and
+// then 8 rows (8 alone: 166, 107 and 80 us).  Small blocks leave the rows' share small (64 rows: 135 us single, 137 paired;
+// 112 and 128 rows: equal).
 // What bounds it: the weights' bytes (4096 x 7168 for 8192 rows: 749 MB, and 67 MB of C, in
 // 152 us = 5.4 TB/s; reading these weights alone takes 130 us), and in the dense product,
 // whose tiles come from L2, those copies again: 650 MB in 59 us, 51 us with no matrix
@@ -63,6 +68,8 @@ constexpr uint32_t kStop = 0xffffffffu;   // stage info: no more items
 constexpr int kMaxStages = 12;
 constexpr int kDone = 16;                // barriers of finished stages, above any ring's depth
 constexpr int kPairRows = 96;            // blocks from here on run in pairs of CTAs
+constexpr int kTileLines = kMxTileBytes / 128;   // 128-byte rows of a tile
+constexpr int kBoxRows = 32, kScaleRows = 8;   // a pair's copies of rows: half of a block is a multiple of 8, a tile's scales are 8
 constexpr int kStgBytes = 2048;          // one epilogue warp's buffer: 16 rows x 32 columns x FP32
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCols = 24;      // tensor-memory columns of a stage's scales: 2 x (4 + 8)
@@ -76,6 +83,12 @@ struct MxPlan {
     int r_stages;   // ring of rows
     int r_bytes;    // one stage of rows: codes (a pair's CTA: of half of them), then 1 KB of scales per 128 rows
     int slots;      // stages whose scales tensor memory holds
+};
+
+// Pairs of CTAs: both matrices as rows of 128 bytes (136 a tile: its code rows, then 8 of scales).
+struct MxMaps {
+    CUtensorMap w;      // boxes of a tile
+    CUtensorMap a, a8;  // boxes of 32 and of 8 rows
 };
 
 struct Item {
@@ -230,7 +243,7 @@ __device__ __forceinline__ void drain(const MxGemmArgs& g, const MxPlan& pl, con
 }
 
 template <bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g, const MxPlan pl) {
+__global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g, const MxPlan pl, const __grid_constant__ MxMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* ring_r = smem + pl.w_stages * kMxTileBytes;
@@ -239,8 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     uint64_t* full_r = full_w + kMaxStages;
     uint64_t* done = full_r + kMaxStages;      // stage g's instructions: barrier g mod kDone
     uint64_t* turn_full = done + kDone;
-    uint64_t* peer_full = turn_full + kTurns;  // first CTA of a pair: the second one's copies of a turn have landed
-    uint64_t* acc_full = peer_full + kTurns;
+    uint64_t* acc_full = turn_full + kTurns;
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [0] row blocks, [1] abort, [2] skip
@@ -274,10 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
                 mbar_init(&full_r[s], 1);
             }
             for (int s = 0; s < kDone; ++s) mbar_init(&done[s], 1);
-            for (int s = 0; s < kTurns; ++s) {
-                mbar_init(&turn_full[s], 1);
-                mbar_init(&peer_full[s], 1);
-            }
+            for (int s = 0; s < kTurns; ++s) mbar_init(&turn_full[s], 1);
             for (int s = 0; s < 2; ++s) {
                 mbar_init(&acc_full[s], 1);
                 mbar_init(&acc_empty[s], PAIR ? 2 * kEpiWarps : kEpiWarps);
@@ -309,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     };
     const uint32_t base_w = smem_u32(smem), base_r = smem_u32(ring_r), r_codes = (uint32_t)pl.tok * (PAIR ? 64u : 128u);
     const uint32_t full_w_a = smem_u32(full_w), full_r_a = smem_u32(full_r), done_a = smem_u32(done), turn_a = smem_u32(turn_full);
-    const uint32_t peer_a = smem_u32(peer_full), slots = (uint32_t)pl.slots;
+    const uint32_t slots = (uint32_t)pl.slots;
     const uint32_t w_stages = (uint32_t)pl.w_stages, r_stages = (uint32_t)pl.r_stages, r_bytes = (uint32_t)pl.r_bytes;
     auto next_w = [&](const Pos& p) {
         return p.slot + 1 == w_stages ? Pos{p.g + 1, 0, base_w, p.parity ^ 1u}
@@ -319,13 +328,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
         return p.slot + 1 == r_stages ? Pos{p.g + 1, 0, base_r, p.parity ^ 1u}
                                       : Pos{p.g + 1, p.slot + 1, p.st + r_bytes, p.parity};
     };
-    auto wait_full = [&](uint32_t bars, const Pos& p) { return tc5::wait(bars + p.slot * 8, p.parity, &flags[1], g.err); };
-    // the slot of stage p.g is free: the instructions of the stage a ring before are done
-    auto wait_free = [&](const Pos& p, uint32_t depth) {
-        if (p.g < depth) return true;
-        const uint32_t old = p.g - depth;
-        return tc5::wait(done_a + (old % kDone) * 8, (old / kDone) & 1u, &flags[1], g.err);
+    auto wait_full = [&](uint32_t bars, const Pos& p) {
+        return tc5::wait<false, PAIR>(bars + p.slot * 8, p.parity, &flags[1], g.err);
     };
+    // the instructions of a stage are done
+    auto wait_done = [&](uint32_t stage) {
+        return tc5::wait<false, PAIR>(done_a + (stage % kDone) * 8, (stage / kDone) & 1u, &flags[1], g.err);
+    };
+    // the slot of stage p.g is free: the instructions of the stage a ring before are done
+    auto wait_free = [&](const Pos& p, uint32_t depth) { return p.g < depth || wait_done(p.g - depth); };
+    // a stage's copies are counted on one barrier: a pair's, both CTAs' bytes, on the first CTA's
+    auto counted_on = [&](uint32_t bar) { return PAIR ? tc5::at_cta(bar, 0) : bar; };
     bool ok = true;
 
     if (warp == kWeightWarp) {
@@ -334,21 +347,26 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             const Item it = item_at<PAIR>(g, pl, wk, i, nxt, lane, false);
             nxt = load_routing(g, pl, wk, i + wk.step, lane);
             if (it.rows == 0) continue;
-            const uint8_t* src = g.w + kHeaderBytes + ((int64_t)it.e * ntiles + it.nt) * kstages * kMxTileBytes;
+            const int64_t tile = ((int64_t)it.e * ntiles + it.nt) * kstages;
+            const uint8_t* src = g.w + kHeaderBytes + tile * kMxTileBytes;
             for (int ks = 0; ks < kstages; ++ks, src += kMxTileBytes) {
                 ok = wait_free(p, w_stages);
                 if (!ok) break;
                 if (tc5::elect()) {
                     const uint32_t bar = full_w_a + p.slot * 8;
-                    tc5::arrive_expect_tx(bar, kMxTileBytes);
-                    tc5::bulk_g2s(p.st, src, kMxTileBytes, bar);
+                    if (!rank) tc5::arrive_expect_tx(bar, PAIR ? 2u * kMxTileBytes : kMxTileBytes);
+                    if constexpr (PAIR)
+                        tc5::box_g2s_pair(p.st, &maps.w, (int)(tile + ks) * kTileLines, counted_on(bar));
+                    else
+                        tc5::bulk_g2s(p.st, src, kMxTileBytes, bar);
                 }
                 __syncwarp();
                 p = next_w(p);
             }
         }
         // leave only after every copy issued here has landed
-        for (uint32_t k = 0; k < w_stages && p.g > 0; ++k) {
+        if (PAIR && p.g > 0) wait_done(p.g - 1);
+        for (uint32_t k = 0; k < w_stages && p.g > 0 && !PAIR; ++k) {
             p = p.slot == 0 ? Pos{p.g - 1, w_stages - 1, 0, p.parity ^ 1u} : Pos{p.g - 1, p.slot - 1, 0, p.parity};
             if (!wait_full(full_w_a, p)) break;
         }
@@ -366,26 +384,44 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             // a pair's CTA copies rows [h0, h1), and the scales of all
             const int h0 = PAIR ? (int)rank * (rows / 2) : 0, h1 = PAIR ? h0 + rows / 2 : rows;
             const int a0 = min(h0, r0), a1 = min(h1, r0), b0 = max(h0, r0), b1 = max(h1, r0);   // in the first, second tile
-            const uint32_t bytes = (uint32_t)(h1 - h0) * 128u + (rows > r0 ? 2048u : 1024u);
+            const uint32_t scales = rows > r0 ? 2048u : 1024u;
+            const uint32_t bytes = (uint32_t)rows * 128u + (PAIR ? 2u * scales : scales);
             const uint32_t inf = (uint32_t)rows | (uint32_t)it.off << 16;
             for (int ks = 0; ks < kstages; ++ks, src += kMxTileBytes) {
                 ok = wait_free(p, r_stages);
                 if (!ok) break;
                 if (tc5::elect()) {
                     const uint32_t bar = full_r_a + p.slot * 8, ss = p.st + r_codes;
-                    info[p.slot] = inf;
-                    tc5::arrive_expect_tx(bar, bytes);
-                    if (a1 > a0) tc5::bulk_g2s(p.st, src + (it.off + a0) * 128, (uint32_t)(a1 - a0) * 128u, bar);
-                    if (b1 > b0)
-                        tc5::bulk_g2s(p.st + (a1 - a0) * 128, src + tstride + (b0 - r0) * 128, (uint32_t)(b1 - b0) * 128u, bar);
-                    tc5::bulk_g2s(ss, src + kMxCodeBytes, 1024u, bar);
-                    if (rows > r0) tc5::bulk_g2s(ss + 1024, src + tstride + kMxCodeBytes, 1024u, bar);
+                    if (!rank) {
+                        info[p.slot] = inf;
+                        tc5::arrive_expect_tx(bar, bytes);
+                    }
+                    if constexpr (PAIR) {
+                        const uint32_t to = counted_on(bar);
+                        const int line = (int)(t0 * kstages + ks) * kTileLines, line2 = line + kstages * kTileLines;
+                        uint32_t st = p.st;
+                        auto copy = [&](int at, int n) {
+                            for (; n >= kBoxRows; n -= kBoxRows, at += kBoxRows, st += kBoxRows * 128)
+                                tc5::box_g2s_pair(st, &maps.a, at, to);
+                            for (; n > 0; n -= kScaleRows, at += kScaleRows, st += kScaleRows * 128)
+                                tc5::box_g2s_pair(st, &maps.a8, at, to);
+                        };
+                        copy(line + it.off + a0, a1 - a0);
+                        copy(line2 + b0 - r0, b1 - b0);
+                        tc5::box_g2s_pair(ss, &maps.a8, line + kMxTileRows, to);
+                        if (rows > r0) tc5::box_g2s_pair(ss + 1024, &maps.a8, line2 + kMxTileRows, to);
+                    } else {
+                        tc5::bulk_g2s(p.st, src + it.off * 128, (uint32_t)a1 * 128u, bar);
+                        if (b1 > b0) tc5::bulk_g2s(p.st + a1 * 128, src + tstride, (uint32_t)(b1 - b0) * 128u, bar);
+                        tc5::bulk_g2s(ss, src + kMxCodeBytes, 1024u, bar);
+                        if (rows > r0) tc5::bulk_g2s(ss + 1024, src + tstride + kMxCodeBytes, 1024u, bar);
+                    }
                 }
                 __syncwarp();
                 p = next_r(p);
             }
         }
-        if (ok && wait_free(p, r_stages)) {
+        if (!rank && ok && wait_free(p, r_stages)) {
             if (tc5::elect()) {
                 info[p.slot] = kStop;
                 tc5::arrive(full_r_a + p.slot * 8);
@@ -393,10 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             __syncwarp();
             p = next_r(p);
         }
-        for (uint32_t k = 0; k < r_stages && p.g > 0; ++k) {
+        if (PAIR && rank && p.g > 0) wait_done(p.g - 1);
+        for (uint32_t k = 0; k < r_stages && p.g > 0 && !rank; ++k) {
             p = p.slot == 0 ? Pos{p.g - 1, r_stages - 1, 0, p.parity ^ 1u} : Pos{p.g - 1, p.slot - 1, 0, p.parity};
             if (!wait_full(full_r_a, p)) break;
         }
+    } else if (rank && (warp == kScaleWarp || warp == kMmaWarp)) {
+        // the first CTA of the pair issues
     } else if (warp == kScaleWarp) {
         // Scales of a stage's two 128-column halves to the columns of its rows' slot: 4 columns
         // per 128 rows (and four groups), weights first.  They are free when the slot is.
@@ -415,15 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
                 ok = wait_full(full_r_a, r) && wait_full(full_w_a, w) &&
                      (!second || (wait_full(full_r_a, r2) && wait_full(full_w_a, w2)));
                 if (!ok) break;
-                if (PAIR && rank) {   // the first CTA issues for both
-                    if (tc5::elect()) tc5::arrive_at(peer_a + (turn % kTurns) * 8, 0);
-                    __syncwarp();
-                    w = second ? next_w(w2) : w2;
-                    r = second ? next_r(r2) : r2;
-                    continue;
-                }
-                ok = wait_free(second ? r2 : r, slots) &&
-                     (!PAIR || tc5::wait(peer_a + (turn % kTurns) * 8, (turn / kTurns) & 1u, &flags[1], g.err));
+                ok = wait_free(second ? r2 : r, slots);
                 if (!ok) break;
                 if (tc5::elect()) {
                     auto copy = [&](const Pos& wp, const Pos& rp) {
@@ -445,12 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
                 r = second ? next_r(r2) : r2;
             }
         }
-        // the last instructions are done: before tensor memory is released, and before a pair's
-        // second CTA leaves, whose barriers their commits arrive on
-        if (w.g > 0) tc5::wait(done_a + ((w.g - 1) % kDone) * 8, ((w.g - 1) / kDone) & 1u, &flags[1], g.err);
+        // the last instructions are done: before tensor memory is released
+        if (w.g > 0) wait_done(w.g - 1);
         __syncwarp();
-    } else if (warp == kMmaWarp && rank) {
-        // the first CTA of the pair issues
     } else if (warp == kMmaWarp) {
         const uint32_t sf_base = tmem + 2u * (uint32_t)pl.tok;
         Pos w{0, 0, base_w, 0}, r{0, 0, base_r, 0};
@@ -461,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             const uint32_t inf = __shfl_sync(0xffffffffu, info[r.slot], 0);
             if (inf == kStop) break;
             const uint32_t rows = inf & 0xffffu, off = inf >> 21, buf = nitem & 1u;   // off: in 32 rows
-            ok = tc5::wait(smem_u32(&acc_empty[buf]), ((nitem >> 1) & 1u) ^ 1u, &flags[1], g.err);
+            ok = tc5::wait<false, PAIR>(smem_u32(&acc_empty[buf]), ((nitem >> 1) & 1u) ^ 1u, &flags[1], g.err);
             if (!ok) break;
             const uint32_t acc = tmem + buf * (uint32_t)pl.tok;
             const uint32_t id0 = tc5::idesc_mxf4<PAIR>((int)rows, 0), id2 = tc5::idesc_mxf4<PAIR>((int)rows, 2);
@@ -503,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             nxt = load_routing(g, pl, wk, i + wk.step, lane);
             if (it.rows == 0) continue;
             const int buf = (int)(nitem & 1);
-            if (!tc5::wait<true>(&acc_full[buf], (uint32_t)((nitem >> 1) & 1), &flags[1], g.err)) break;
+            if (!tc5::wait<true, PAIR>(&acc_full[buf], (uint32_t)((nitem >> 1) & 1), &flags[1], g.err)) break;
             tc5::fence_after();
             if (it.write) {
                 const uint32_t acc = tmem + (uint32_t)(buf * pl.tok);
@@ -516,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
             __syncwarp();
             if (lane == 0) {
                 if (PAIR)
-                    tc5::arrive_at(smem_u32(&acc_empty[buf]), 0);
+                    tc5::arrive_relaxed_at(smem_u32(&acc_empty[buf]), 0);
                 else
                     mbar_arrive(&acc_empty[buf]);
             }
@@ -530,6 +558,22 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     if (warp == kMmaWarp) tc5::dealloc<PAIR>(tmem, kTmemCols);
 }
 
+// The tiles of a packed matrix as rows of 128 bytes, copied `box` at a time.
+bool tile_map(CUtensorMap* map, const uint8_t* packed, int64_t tiles, int box) {
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) == cudaSuccess;
+        return reinterpret_cast<Encode>(ok && r == cudaDriverEntryPointSuccess ? f : nullptr);
+    }();
+    const cuuint64_t dims[2] = {128, (cuuint64_t)(tiles * kTileLines)}, strides[1] = {128};
+    const cuuint32_t boxes[2] = {128, (cuuint32_t)box}, ones[2] = {1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(packed) + kHeaderBytes, dims, strides,
+                            boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
     MxPlan pl;
     // Dense blocks: 192 rows (two accumulators and the scales fill the tensor
@@ -538,9 +582,11 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
     // 128-row tiles a block may touch (dense blocks of 192 start at row 0 or 64 of one)
     const int tiles = (pl.tok + kMxTileRows - 1) / kMxTileRows;
     const int64_t ntiles = (g.N + kMxTileRows - 1) / kMxTileRows;
-    const bool pair = pl.tok >= kPairRows && ntiles > 1;
+    // tiles of either matrix; their 128-byte rows are a pair's 32-bit tensor-map coordinates
+    const int64_t w_tiles = (int64_t)g.E * ntiles * mx_col_tiles(g.K), a_tiles = g.a_groups * mx_row_tiles(g.a_rows) * mx_col_tiles(g.K);
+    const bool pair = pl.tok >= kPairRows && ntiles > 1 && (w_tiles > a_tiles ? w_tiles : a_tiles) <= INT32_MAX / kTileLines;
     pl.r_bytes = pl.tok * (pair ? 64 : 128) + 1024 * tiles;
-    const size_t fixed = 1024 + kEpiWarps * kStgBytes + (2 * kMaxStages + kDone + 2 * kTurns + 4) * 8 + 64 + 4 * kMaxStages;
+    const size_t fixed = 1024 + kEpiWarps * kStgBytes + (2 * kMaxStages + kDone + kTurns + 4) * 8 + 64 + 4 * kMaxStages;
     const size_t room = kSmemBudget - fixed;
     pl.slots = (int)((kTmemCols - 2 * pl.tok) / kScaleCols);
     if (pl.slots > kMaxStages) pl.slots = kMaxStages;
@@ -551,7 +597,11 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
     if (pl.r_stages < 2 || pl.w_stages < 2 || pl.slots < 2) return cudaErrorInvalidConfiguration;
     // one CTA per SM: it takes the whole tensor memory, and more than half of the shared memory
     const size_t smem = fixed + (size_t)pl.w_stages * kMxTileBytes + (size_t)pl.r_stages * pl.r_bytes;
-    void (*kern)(MxGemmArgs, MxPlan) = pair ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
+    MxMaps maps{};
+    if (pair && !(tile_map(&maps.w, g.w, w_tiles, kTileLines) && tile_map(&maps.a, g.a, a_tiles, kBoxRows) &&
+                  tile_map(&maps.a8, g.a, a_tiles, kScaleRows)))
+        return cudaErrorInvalidValue;
+    void (*kern)(MxGemmArgs, MxPlan, MxMaps) = pair ? mx_gemm_kernel<true> : mx_gemm_kernel<false>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmemBudget);
     if (e != cudaSuccess) return e;
     const int64_t blocks = g.sorted_ids ? g.a_groups : (g.a_rows + pl.tok - 1) / pl.tok;
@@ -577,7 +627,7 @@ cudaError_t launch_mx_gemm(const MxGemmArgs& g, cudaStream_t st) {
     }
     cfg.attrs = attr;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, kern, g, pl);
+    return cudaLaunchKernelEx(&cfg, kern, g, pl, maps);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -75,13 +75,25 @@ __device__ __forceinline__ void arrive_expect_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// On the barrier at the same address of CTA `cta` of the cluster.  Tells it of asynchronous
-// copies and tensor-memory loads that this thread has seen complete; nothing of its own
-// stores (with release.cluster, which waits for those, a turn of the product took twice as long).
-__device__ __forceinline__ void arrive_at(uint32_t bar, uint32_t cta) {
+// The address in CTA `cta` of the cluster of what is at `addr` in this one.
+__device__ __forceinline__ uint32_t at_cta(uint32_t addr, uint32_t cta) {
     uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(bar), "r"(cta));
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(cta));
+    return remote;
+}
+// On the barrier at the same address of CTA `cta`: the tensor-memory loads that this thread has
+// waited for, and fenced with fence_before(), are done.  Relaxed: it hands over nothing in memory.
+__device__ __forceinline__ void arrive_relaxed_at(uint32_t bar, uint32_t cta) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_cta(bar, cta)) : "memory");
+}
+// A box of a 2-D tensor map from row `row` into this CTA, its bytes counted on the barrier at the
+// cluster address `bar`: this CTA's or, as these copies may in a pair, the other one's.
+__device__ __forceinline__ void box_g2s_pair(uint32_t dst, const void* map, int row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(row), "r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -158,15 +170,27 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int n, uint32_t sf) {
            (sf << 29);
 }
 
+// CLUSTER: acquire at cluster scope, for phases that the other CTA of a pair, its copies or its
+// commits take part in.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 
@@ -174,13 +198,13 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
 // time; gives up at once when another role has set the abort flag.  RELAX: poll
 // every couple of hundred nanoseconds only (long waits off the critical path, whose
 // polling would take issue slots from the other roles).
-template <bool RELAX = false>
+template <bool RELAX = false, bool CLUSTER = false>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
-    if (try_wait(bar, parity)) return true;
+    if (try_wait<CLUSTER>(bar, parity)) return true;
     const long long t0 = clock64();
     for (uint32_t it = 1;; ++it) {
         if constexpr (RELAX) __nanosleep(200);
-        if (try_wait(bar, parity)) return true;
+        if (try_wait<CLUSTER>(bar, parity)) return true;
         if ((it & 63u) == 0) {
             if (*abort_flag) return false;
             if (clock64() - t0 > kWaitLimitCycles) {
@@ -191,9 +215,9 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
         }
     }
 }
-template <bool RELAX = false>
+template <bool RELAX = false, bool CLUSTER = false>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
-    return wait<RELAX>(smem_u32(bar), parity, abort_flag, err);
+    return wait<RELAX, CLUSTER>(smem_u32(bar), parity, abort_flag, err);
 }
 
 // Slot and parity of a ring of n stages.

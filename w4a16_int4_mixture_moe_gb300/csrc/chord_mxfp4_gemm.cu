@@ -74,6 +74,7 @@ constexpr int kStgBytes = 2048;          // one epilogue warp's buffer: 16 rows 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCols = 24;      // tensor-memory columns of a stage's scales: 2 x (4 + 8)
 constexpr int kTurns = 16;               // scale barriers, one per turn in flight (a turn is one or two stages)
+constexpr long long kLandCycles = 4000000;   // about 2 ms
 constexpr size_t kSmemBudget = 227 * 1024;
 constexpr int kMxMaxBlockM = 208;        // two accumulators and four stages' scales fill the tensor memory
 
@@ -553,6 +554,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const MxGemmArgs g
     }
     tc5::fence_before();
     __syncthreads();
+    // A role that gave up has made the others' last waits return at once: what is still in flight
+    // (copies into this CTA's shared memory, instructions on its tensor memory) gets its time here,
+    // some hundred times what it takes, before either is handed to the next CTA.
+    if (flags[1])
+        for (const long long t0 = clock64(); clock64() - t0 < kLandCycles;) __nanosleep(1000);
     if (PAIR) tc5::cluster_sync();   // the pair's instructions, and arrivals on the other CTA's barriers, are done
     tc5::fence_after();
     if (warp == kMmaWarp) tc5::dealloc<PAIR>(tmem, kTmemCols);

@@ -307,6 +307,31 @@ def test_wrong_blob_is_reported_and_nothing_written():
     assert torch.isnan(out).all()
 
 
+@gpu
+def test_refused_blob_leaves_the_stream_order_intact():
+    """Work behind a call whose blob is refused comes after both of its kernels:
+    the workspace keeps what is written there next, and the next call on it is right."""
+    need_gpu()
+    g = torch.Generator().manual_seed(6)
+    T, E, topk, H, I = 16, 4, 2, 4096, 128
+    v13, p13 = make_weights("int4", E, 2 * I, H, g)
+    v2, p2 = make_weights("int4", E, H, I, g)
+    ids, w = routing(T, E, topk, g)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16)
+    b13, b2, bad = p13(), p2(), p2(3)
+    xd, idd, wd = x.to(DEV), ids.to(DEV), w.to(DEV)
+    ws = torch.empty(chord.chord_moe_few_workspace_bytes(T, topk, E, H, I), dtype=torch.uint8, device=DEV)
+    out = torch.empty((T, H), dtype=torch.bfloat16, device=DEV)
+    for _ in range(20):
+        chord.chord_moe_layer_few(xd, idd, wd, E, I, b13, bad, ws, out)
+        ws.fill_(0xAB)
+        assert (ws == 0xAB).all()
+        chord.chord_moe_layer_few(xd, idd, wd, E, I, b13, bad, ws, out)
+        chord.chord_moe_layer_few(xd, idd, wd, E, I, b13, b2, ws, out)
+    assert chord.chord_get_device_error() == 3
+    check(out, *reference(x, ids, w, v13, v2))
+
+
 def test_refusals():
     lib = chord.load()
     vp = ctypes.c_void_p

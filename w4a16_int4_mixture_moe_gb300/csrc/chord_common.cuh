@@ -41,10 +41,15 @@ constexpr long long kWaitLimitCycles = 4000000000LL;
 // kernel may be scheduled while the previous kernel of the stream still runs
 // (once every block of that kernel has started), and waits in
 // griddepcontrol.wait until the previous kernel has finished and its memory
-// is visible.  Every kernel launched this way calls pdl_wait() before its
-// first access to global memory, so the order of reads and writes is the
-// stream order; what overlaps is the launch and block scheduling.  Without
-// the attribute both instructions return at once.
+// is visible.  Every kernel launched this way calls pdl_wait() on every path
+// before it ends, before it writes global memory, and before it reads what may be
+// younger than its primary's start, so the order of reads and writes is the
+// stream order.  Where the primary may itself have been launched this way, that is
+// before the first access to global memory.  Two kernels read earlier, each behind a
+// primary that its own call launches WITHOUT the attribute (everything older than that one
+// is complete when it starts): few_down_kernel (ids, weights, blobs; its primary is
+// few_gate_up_kernel) and mx_quantize_shared_kernel (rows, counts, sorted_ids; its
+// primary is mx_index_kernel).  Without the attribute both instructions return at once.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

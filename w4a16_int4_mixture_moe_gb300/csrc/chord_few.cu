@@ -851,7 +851,10 @@ __global__ void __launch_bounds__(kThreads, CLUSTERED ? 4 : 3) few_down_kernel(c
     float* s_w;
     const Route rt = prologue<MX>(a, sh, smem + a.depth * a.stage_bytes + (CLUSTERED ? down_part_bytes(NT, a.cluster) : 0), s_ids,
                                   s_w, false);
-    if (!(sh.flags & 1)) return;   // the same in every CTA; the gate_up kernel reported it
+    if (!(sh.flags & 1)) {   // the same in every CTA; the gate_up kernel reported it
+        pdl_wait();          // what follows in the stream comes after both kernels, also here
+        return;
+    }
     if (CLUSTERED) cluster_sync_all();   // every CTA runs before another one's sums arrive
     const int rank = blockIdx.x % a.cluster, tile = blockIdx.x / a.cluster;
     const int kst = (a.I + S::kCols - 1) / S::kCols, total = rt.slots * kst;
@@ -881,6 +884,7 @@ __global__ void __launch_bounds__(kThreads, CLUSTERED ? 4 : 3) few_down_kernel(c
     auto sum_of = [&](int i, int nt) { return make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]); };
     if (a.cluster == 1) {
         if (warp == kConsumers) return;
+        pdl_wait();   // (an empty list has waited for nothing yet)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -1024,6 +1028,7 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     a.stage_bytes = S::up_bytes(tokens);
     a.depth = ring_depth(up_room - beside, a.stage_bytes, items > resident ? 16 : (stages + a.cluster - 1) / a.cluster);
     size_t smem = (size_t)a.depth * a.stage_bytes + beside;
+    // a plain launch: the down kernel reads ids, weights and blobs before its wait (see pdl_wait)
     cudaError_t e = launch(few_gate_up_kernel<MX>, a, (unsigned)(items < resident ? items : resident), smem, true, false, st);
     if (e != cudaSuccess) return e;
     // down: the (pass, K stage) list of an output tile in slices, as many as fill the GPU

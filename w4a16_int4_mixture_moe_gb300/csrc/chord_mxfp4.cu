@@ -473,6 +473,7 @@ cudaError_t launch_quantize_rows(const RowSource& s, int64_t a_rows, int64_t G, 
     const int kb = (int)mx_col_tiles(K);
     const int run = run_for((a_rows + 63) / 64, kb);
     const int64_t ids = (G * N + 255) / 256, cap = (int64_t)device_info().sm_count * 8;
+    // a plain launch: the next kernel reads rows and counts before its wait (see pdl_wait)
     mx_index_kernel<<<(unsigned)(ids < 1 ? 1 : (ids > cap ? cap : ids)), 256, 0, st>>>(s, G, N, K, packed, index, err);
     auto kern = s.f32 ? (vec ? mx_quantize_shared_kernel<true, true> : mx_quantize_shared_kernel<true, false>)
                       : (vec ? mx_quantize_shared_kernel<false, true> : mx_quantize_shared_kernel<false, false>);

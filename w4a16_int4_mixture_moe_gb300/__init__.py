@@ -9,6 +9,7 @@ If the library has not been built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -332,14 +333,51 @@ def chord_grouped_masked_gemm(A, masked_m, expected_m: int, packed, N: int, K: i
 _dtypes = {}
 
 
-def _dtype(t, what: str) -> int:
+def _types():
+    """Type codes of the tensors the library reads; filled on first use, as torch is imported lazily."""
     if not _dtypes:
         import torch
-        _dtypes.update({torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32})
-    code = _dtypes.get(t.dtype)
+        _dtypes.update({torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32,
+                        "bf16": torch.bfloat16, "f32": torch.float32, "int32": torch.int32})
+    return _dtypes
+
+
+def _dtype(t, what: str) -> int:
+    code = (_dtypes or _types()).get(t.dtype)
     if code is None:
         raise ChordError(1, f"{what}: dtype {t.dtype}")
     return code
+
+
+# The library sees an address and sizes: a tensor of another type, shape or layout, or of
+# host memory, would be misread without a word, so it is refused here.  Each returns the address.
+
+def _refuse(what, name, t, expected):
+    where = "" if t.is_cuda else ", not in device memory"
+    raise ChordError(1, f"{what}: {name} must be {expected}, is {t.dtype} {tuple(t.shape)} with strides {t.stride()}{where}")
+
+
+def _dense(what, name, t, dtype, *shape):
+    """A dense tensor of this type (None: any that has a type code) and shape, or of more rows or
+    other leading dimensions that hold as many."""
+    if (t.dtype is dtype or dtype is None) and t.is_contiguous() and t.is_cuda:
+        if t.shape == shape or (t.dim() and t.shape[-1] == shape[-1] and t.numel() >= math.prod(shape)):
+            return t.data_ptr()
+    _refuse(what, name, t, f"dense {dtype or 'bf16 or float32'} {shape} in device memory")
+
+
+def _ints(what, name, t, at_least=1):
+    """A dense int32 array."""
+    if t.dtype is _dtypes["int32"] and t.numel() >= at_least and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
+    _refuse(what, name, t, f"a dense int32 array of {at_least} or more in device memory")
+
+
+def _blob(what, name, t):
+    """Packed bytes or scratch."""
+    if t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
+    _refuse(what, name, t, "dense bytes in device memory")
 
 
 def chord_mxfp4_bytes(G: int, N: int, K: int) -> int:
@@ -352,31 +390,35 @@ def chord_mxfp4_rows_bytes(capacity: int, block_m: int, K: int) -> int:
 
 def chord_mxfp4_quantize(src, packed, stream=None):
     """src bf16 or float32 [G, N, K] (unit stride along K, any row and matrix stride), packed uint8 output."""
-    G, N, K = src.shape
-    mat_stride, row_stride, step = src.stride()
-    if K > 1 and step != 1:
-        raise ChordError(1, "chord_mxfp4_quantize: src needs unit stride along K")
-    _check(load().chord_mxfp4_quantize(_p(src), _dtype(src, "chord_mxfp4_quantize"), row_stride, mat_stride, G, N, K,
-                                       _p(packed), _nbytes(packed), _s(stream)), "chord_mxfp4_quantize")
+    what = "chord_mxfp4_quantize"
+    shape, strides = src.shape, src.stride()
+    if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1) or not src.is_cuda:
+        _refuse(what, "src", src, "3-dimensional with unit stride along K in device memory")
+    _check(load().chord_mxfp4_quantize(src.data_ptr(), _dtype(src, what), strides[1], strides[0], *shape,
+                                       _blob(what, "packed", packed), packed.nbytes, _s(stream)), what)
 
 
 def chord_mxfp4_quantize_rows(A, a_row_divisor: int, sorted_ids, num_tokens_padded, block_m: int, num_pairs: int,
                               packed, stream=None):
     """A bf16 or float32 [a_rows, K] (any row stride), quantised into the order of sorted_ids."""
-    a_rows, K = A.shape
-    if K > 1 and A.stride(1) != 1:
-        raise ChordError(1, "chord_mxfp4_quantize_rows: A needs unit stride along K")
-    _check(load().chord_mxfp4_quantize_rows(_p(A), _dtype(A, "chord_mxfp4_quantize_rows"), a_rows, A.stride(0),
-                                            a_row_divisor, K, _p(sorted_ids), _p(num_tokens_padded),
-                                            sorted_ids.numel(), block_m, num_pairs, _p(packed), _nbytes(packed),
-                                            _s(stream)), "chord_mxfp4_quantize_rows")
+    what = "chord_mxfp4_quantize_rows"
+    shape, strides = A.shape, A.stride()
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1) or not A.is_cuda:
+        _refuse(what, "A", A, "2-dimensional with unit stride along K in device memory")
+    _check(load().chord_mxfp4_quantize_rows(A.data_ptr(), _dtype(A, what), shape[0], strides[0], a_row_divisor, shape[1],
+                                            _ints(what, "sorted_ids", sorted_ids, 0),
+                                            _ints(what, "num_tokens_padded", num_tokens_padded), sorted_ids.numel(),
+                                            block_m, num_pairs, _blob(what, "packed", packed), packed.nbytes, _s(stream)),
+           what)
 
 
 def chord_mxfp4_dequantize(packed, out, stream=None):
     """out bf16 or float32 [G, N, K] dense: the values of the packed matrix."""
+    what = "chord_mxfp4_dequantize"
     G, N, K = out.shape
-    _check(load().chord_mxfp4_dequantize(_p(packed), _nbytes(packed), G, N, K, _p(out),
-                                         _dtype(out, "chord_mxfp4_dequantize"), _s(stream)), "chord_mxfp4_dequantize")
+    code, op = _dtype(out, what), _dense(what, "out", out, None, G, N, K)
+    _check(load().chord_mxfp4_dequantize(_blob(what, "packed", packed), packed.nbytes, G, N, K, op, code, _s(stream)),
+           what)
 
 
 def chord_mxfp4_select_block_m(T: int, topk: int, E_local: int, E_global: int) -> int:
@@ -385,17 +427,23 @@ def chord_mxfp4_select_block_m(T: int, topk: int, E_local: int, E_global: int) -
 
 def chord_mxfp4_moe_gemm(Aq, packed, E: int, N: int, K: int, sorted_ids, expert_ids, num_tokens_padded, block_m: int,
                          num_pairs: int, C, opts=None, stream=None):
-    """C bf16 or float32 [num_pairs, N] (its dtype selects the output type)."""
-    _check(load().chord_mxfp4_moe_gemm(_p(Aq), _nbytes(Aq), _p(packed), _nbytes(packed), E, N, K, _p(sorted_ids),
-                                       _p(expert_ids), _p(num_tokens_padded), sorted_ids.numel(), block_m, num_pairs,
-                                       _p(C), _dtype(C, "chord_mxfp4_moe_gemm"), _o(opts), _s(stream)),
-           "chord_mxfp4_moe_gemm")
+    """C bf16 or float32 [num_pairs, N] dense (its dtype selects the output type)."""
+    what = "chord_mxfp4_moe_gemm"
+    code, cp = _dtype(C, what), _dense(what, "C", C, None, num_pairs, N)
+    capacity = sorted_ids.numel()
+    _check(load().chord_mxfp4_moe_gemm(_blob(what, "Aq", Aq), Aq.nbytes, _blob(what, "packed", packed), packed.nbytes,
+                                       E, N, K, _ints(what, "sorted_ids", sorted_ids, 0),
+                                       _ints(what, "expert_ids", expert_ids, capacity // block_m if block_m > 0 else 0),
+                                       _ints(what, "num_tokens_padded", num_tokens_padded), capacity, block_m, num_pairs,
+                                       cp, code, _o(opts), _s(stream)), what)
 
 
 def chord_mxfp4_gemm(Aq, M: int, packed, N: int, K: int, C, opts=None, stream=None):
-    """C bf16 or float32 [M, N] (its dtype selects the output type)."""
-    _check(load().chord_mxfp4_gemm(_p(Aq), _nbytes(Aq), M, _p(packed), _nbytes(packed), N, K, _p(C),
-                                   _dtype(C, "chord_mxfp4_gemm"), _o(opts), _s(stream)), "chord_mxfp4_gemm")
+    """C bf16 or float32 [M, N] dense (its dtype selects the output type)."""
+    what = "chord_mxfp4_gemm"
+    code, cp = _dtype(C, what), _dense(what, "C", C, None, M, N)
+    _check(load().chord_mxfp4_gemm(_blob(what, "Aq", Aq), Aq.nbytes, M, _blob(what, "packed", packed), packed.nbytes,
+                                   N, K, cp, code, _o(opts), _s(stream)), what)
 
 
 def chord_moe_few_workspace_bytes(T: int, topk: int, E: int, H: int, I: int) -> int:
@@ -404,11 +452,18 @@ def chord_moe_few_workspace_bytes(T: int, topk: int, E: int, H: int, I: int) -> 
 
 def chord_moe_layer_few(x, topk_ids, topk_w, E: int, I: int, packed_w13, packed_w2, workspace, out,
                         weights: int = WEIGHTS_INT4, opts=None, stream=None):
+    """x bf16 [T, H], topk_ids int32 and topk_w float32 [T, topk], out bf16 [T, H], all dense."""
+    what = "chord_moe_layer_few"
+    types = _dtypes or _types()
     T, H = x.shape
     topk = topk_ids.shape[1]
-    _check(load().chord_moe_layer_few(_p(x), _p(topk_ids), _p(topk_w), T, topk, E, H, I, weights, _p(packed_w13),
-                                      _nbytes(packed_w13), _p(packed_w2), _nbytes(packed_w2), _p(workspace),
-                                      _nbytes(workspace), _p(out), _o(opts), _s(stream)), "chord_moe_layer_few")
+    _check(load().chord_moe_layer_few(_dense(what, "x", x, types["bf16"], T, H),
+                                      _dense(what, "topk_ids", topk_ids, types["int32"], T, topk),
+                                      _dense(what, "topk_w", topk_w, types["f32"], T, topk), T, topk, E, H, I, weights,
+                                      _blob(what, "packed_w13", packed_w13), packed_w13.nbytes,
+                                      _blob(what, "packed_w2", packed_w2), packed_w2.nbytes,
+                                      _blob(what, "workspace", workspace), workspace.nbytes,
+                                      _dense(what, "out", out, types["bf16"], T, H), _o(opts), _s(stream)), what)
 
 
 def chord_selftest_wait_timeout(stream=None):

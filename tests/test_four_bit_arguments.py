@@ -29,6 +29,25 @@ def refused(call, args, at, bad, name):
     assert ei.value.status == 1 and f": {name} must be" in str(ei.value)
 
 
+class FakeStream:
+    cuda_stream = 77
+
+
+def test_current_stream_without_torch_internals(monkeypatch):
+    """The stream handle comes from torch's public call where its internal ones are
+    missing, take other arguments or disagree; a given stream is used as it is."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: FakeStream)
+    for raw, device in ((None, None), (lambda: 5, lambda: 0), (lambda d: 5, lambda: 0), (lambda d: 77, lambda: 0)):
+        monkeypatch.setattr(chord, "_current_stream", None)
+        for name, f in (("_cuda_getCurrentRawStream", raw), ("_cuda_getDevice", device)):
+            if f is None:
+                monkeypatch.delattr(torch._C, name, raising=False)
+            else:
+                monkeypatch.setattr(torch._C, name, f, raising=False)
+        assert chord._s(None) == 77 and chord._s(None) == 77
+    assert chord._s(FakeStream) == 77 and chord._s(0) == 0 and chord._s(9) == 9
+
+
 def every_other(t):
     """The same shape, two elements apart."""
     return t.repeat_interleave(2, dim=-1)[..., ::2]

@@ -143,19 +143,31 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-_torch = None
+_current_stream = None
+
+
+def _stream_getter():
+    """How the handle of the current stream is read.  torch.cuda.current_stream() makes a Python object on
+    the way (3.4 us of a 9 us call); its two halves are internal functions of torch, used where they
+    are and agree with it."""
+    import torch
+    public = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    expected = public()          # initialises CUDA, or raises
+    if raw is None or device is None:
+        return public
+    try:
+        return (lambda: raw(device())) if raw(device()) == expected else public
+    except (TypeError, RuntimeError):
+        return public
 
 
 def _s(stream):
     if stream is None:
-        global _torch
-        if _torch is None:
-            import torch
-            _torch = torch
-        if _torch.cuda.is_initialized():
-            # the handle of torch.cuda.current_stream() without its Python object (3.4 us of a 9 us call)
-            return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
-        stream = _torch.cuda.current_stream()
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _stream_getter()
+        return _current_stream()
     return getattr(stream, "cuda_stream", stream) or 0
 
 

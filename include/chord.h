@@ -542,8 +542,11 @@ size_t chord_mxfp4_rows_bytes(int64_t capacity, int block_m, int K);
  * gather of the indexed contract done on the way: for every pair id p at position
  * i of sorted_ids (p < num_pairs, p / a_row_divisor < a_rows), row i mod block_m
  * of group i / block_m is the quantised row p / a_row_divisor of A [a_rows, K]
- * (a_dtype, row_stride elements apart).  Positions without a pair hold no
- * defined codes and no product reads them. */
+ * (a_dtype, row_stride elements apart).  sorted_ids names a pair at most once, as
+ * chord_moe_align leaves it.  Positions of the sentinel num_pairs hold no
+ * defined codes and no product reads them.  An id that is neither the sentinel nor
+ * has a row sets CHORD_DEV_BAD_ROW and its position holds no defined codes: a product
+ * would take it for a pair. */
 chord_status chord_mxfp4_quantize_rows(const void *A, int a_dtype, int64_t a_rows,
                                        int64_t row_stride, int a_row_divisor, int K,
                                        const int32_t *sorted_ids, const int32_t *num_tokens_padded,

@@ -528,6 +528,37 @@ def test_grouped_product_reports_bad_routing():
 
 
 @gpu
+@pytest.mark.parametrize("div", [1, 2])
+@pytest.mark.parametrize("bad", [None, -3, 900])
+def test_rows_that_ids_do_not_have_are_reported(div, bad):
+    """A pair whose row lies past A (fewer rows than pairs / divisor), and ids that are no
+    pair: CHORD_DEV_BAD_ROW, as the INT4 product reports them; the other rows are right."""
+    need_gpu()
+    T, K, bm, E = 8, 96, 16, 2
+    ids = torch.tensor([[t % E, (t + 1) % E][:div] for t in range(T)], dtype=torch.int32, device=DEV)
+    P = T * div
+    s, e, n = align(ids, E, bm)
+    x = torch.randn(T, K, device=DEV)
+    have = T
+    if bad is None:
+        have = T - 3
+    else:
+        s[0] = bad
+    xq = torch.zeros(chord.chord_mxfp4_rows_bytes(s.numel(), bm, K), dtype=torch.uint8, device=DEV)
+    chord.chord_mxfp4_quantize_rows(x[:have], div, s, n, bm, P, xq)
+    assert chord.chord_get_device_error() == 2
+    G = s.numel() // bm
+    gc, gb = unpack(xq[:chord.chord_mxfp4_bytes(G, bm, K)], G, bm, K)
+    c, b = ref_quantise(x.double().cpu().numpy())
+    pos = s[:int(n)].cpu().numpy()
+    at = np.nonzero((pos >= 0) & (pos < have * div))[0]
+    np.testing.assert_array_equal(gc.reshape(-1, K)[at], c[pos[at] // div])
+    np.testing.assert_array_equal(gb.reshape(-1, K // 32)[at], b[pos[at] // div])
+    chord.chord_mxfp4_quantize_rows(x, div, align(ids, E, bm)[0], n, bm, P, xq)
+    assert chord.chord_get_device_error() == 0
+
+
+@gpu
 def test_product_on_its_own_stream_and_in_a_graph():
     need_gpu()
     a, w = torch.randn(1, 70, 512, device=DEV), torch.randn(1, 300, 512, device=DEV)

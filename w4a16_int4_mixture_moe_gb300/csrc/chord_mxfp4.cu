@@ -125,7 +125,8 @@ struct RowSource {
     int64_t row_stride, mat_stride;
     const int32_t* sorted_ids;   // null: plain matrices
     const int32_t* ntp;
-    int64_t id_limit;
+    int64_t id_limit;            // ids below this have a row
+    int32_t sentinel;            // the id of positions without a pair
     int divisor;
 };
 
@@ -200,6 +201,8 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const RowSource s, int
                     if (id >= 0 && id < s.id_limit) {
                         at[i] = (int64_t)((uint32_t)id / (uint32_t)s.divisor) * s.row_stride;
                         live |= 1u << i;
+                    } else if (id != s.sentinel && part == 0 && lane == 0) {
+                        set_error(err, CHORD_DEV_BAD_ROW);
                     }
                 }
             }
@@ -259,7 +262,10 @@ __global__ void __launch_bounds__(256) mx_index_kernel(const RowSource s, int64_
     }
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < ntp; i += (int64_t)gridDim.x * blockDim.x) {
         const int32_t id = __ldg(s.sorted_ids + i);
-        if (id >= 0 && id < s.id_limit) index[id] = (int32_t)i;
+        if (id >= 0 && id < s.id_limit)
+            index[id] = (int32_t)i;
+        else if (id != s.sentinel)
+            set_error(err, CHORD_DEV_BAD_ROW);
     }
 }
 
@@ -516,7 +522,7 @@ chord_status chord_mxfp4_quantize(const void* src, int src_dtype, int64_t row_st
     if (G * N > 0 && (!src || !aligned_to(src, src_dtype == CHORD_DTYPE_F32 ? 4 : 2))) return CHORD_ERR_INVALID_ARG;
     const DeviceInfo& di = device_info();
     if (!di.err) return CHORD_ERR_CUDA;
-    RowSource s{src, src_dtype == CHORD_DTYPE_F32, row_stride, mat_stride, nullptr, nullptr, 0, 1};
+    RowSource s{src, src_dtype == CHORD_DTYPE_F32, row_stride, mat_stride, nullptr, nullptr, 0, 0, 1};
     return launch_quantize(s, G, N, K, static_cast<uint8_t*>(packed), di.err, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? CHORD_OK
@@ -542,7 +548,7 @@ chord_status chord_mxfp4_quantize_rows(const void* A, int a_dtype, int64_t a_row
     if (!di.err) return CHORD_ERR_CUDA;
     const int64_t limit = a_rows * (int64_t)a_row_divisor;
     RowSource s{A,         a_dtype == CHORD_DTYPE_F32, row_stride, 0, sorted_ids, num_tokens_padded,
-                limit < num_pairs ? limit : num_pairs, a_row_divisor};
+                limit < num_pairs ? limit : num_pairs, (int32_t)num_pairs, a_row_divisor};
     uint8_t* out = static_cast<uint8_t*>(packed);
     int32_t* index = reinterpret_cast<int32_t*>(out + chord_mxfp4_bytes(capacity / block_m, block_m, K));
     return launch_quantize_rows(s, a_rows, capacity / block_m, block_m, K, out, index, di.err,

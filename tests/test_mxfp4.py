@@ -232,6 +232,79 @@ def test_quantise_bit_exact(G, N, K, dtype, pad):
 
 
 @gpu
+@pytest.mark.parametrize("G,N,K", [(1, 1, 32), (2, 33, 256), (3, 129, 288), (1, 200, 544), (2, 128, 1056)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_padding_of_the_last_tiles(G, N, K, dtype):
+    """Every byte that belongs to no row or no group: zero codes and the scale 1, which the
+    products and the layer rely on (a NaN scale there would make NaN of zero codes)."""
+    need_gpu()
+    rng = np.random.default_rng(N + K)
+    packed = quantise(nasty(rng, G, N, K, dtype).to(DEV))
+    raw = packed.cpu().numpy()[256:].reshape(G, -(-N // 128), -(-K // 256), 17408)
+    for r in range(raw.shape[1] * 128):
+        for j in range(raw.shape[2] * 8):
+            if r < N and 32 * j < K:
+                continue
+            t, q, jj = raw[:, r // 128, j // 8], r % 128, j % 8
+            o = q * 128 + 16 * (jj ^ (q % 8))
+            assert (t[:, o:o + 16] == 0).all()
+            assert (t[:, 16384 + 512 * (jj // 4) + 16 * (q % 32) + 4 * (q // 32) + jj % 4] == 127).all()
+
+
+@gpu
+@pytest.mark.parametrize("div", [1, 2])
+def test_padding_columns_of_routed_rows(div):
+    """The same for the columns past K of rows quantised in routed order."""
+    need_gpu()
+    T, K, bm, E = 20, 288, 16, 3
+    g = torch.Generator().manual_seed(div)
+    ids = torch.rand(T, E, generator=g).argsort(dim=1)[:, :div].to(torch.int32).contiguous()
+    s, _, n = align(ids.to(DEV), E, bm)
+    xq = torch.full((chord.chord_mxfp4_rows_bytes(s.numel(), bm, K),), 0xFF, dtype=torch.uint8, device=DEV)
+    chord.chord_mxfp4_quantize_rows(torch.randn(T, K, generator=g).to(DEV), div, s, n, bm, T * div, xq)
+    G = s.numel() // bm
+    raw = xq.cpu().numpy()[256:chord.chord_mxfp4_bytes(G, bm, K)].reshape(G, 2, 17408)
+    pos = s[:int(n)].cpu().numpy()
+    for i in np.nonzero(pos < T * div)[0]:
+        t, q = raw[i // bm, 1], i % bm
+        for jj in range(1, 8):
+            o = q * 128 + 16 * (jj ^ (q % 8))
+            assert (t[o:o + 16] == 0).all()
+            assert t[16384 + 512 * (jj // 4) + 16 * (q % 32) + 4 * (q // 32) + jj % 4] == 127
+
+
+@gpu
+def test_matrices_past_32_bits():
+    """More than 2^31 values in a matrix and in its dequantised form, more than 2^31 results of
+    a product: the last rows are as right as the first."""
+    need_gpu()
+    one = torch.randn(1, 4100, 7200, device=DEV, dtype=torch.bfloat16)
+    G = 75
+    assert G * one.numel() > 2 ** 31
+    packed = quantise(one.expand(G, 4100, 7200))
+    alone = quantise(one)[256:]
+    assert torch.equal(packed[256:].view(G, -1), alone.expand(G, -1))
+    out = torch.empty((G, 4100, 7200), dtype=torch.bfloat16, device=DEV)
+    chord.chord_mxfp4_dequantize(packed, out)
+    want = values_of(quantise(one), 1, 4100, 7200, torch.bfloat16)[0]
+    for i in (0, 36, 73, G - 1):
+        assert torch.equal(out[i], want)
+    del out, packed
+    M, N, K = 70000, 32000, 64
+    assert M * N > 2 ** 31
+    g = torch.Generator(device=DEV).manual_seed(3)
+    vals = torch.tensor([0., 1, -1, 2, -2, 3, -3, 4, 6, -6, .5, 1.5], device=DEV)
+    a, w = (vals[torch.randint(0, 12, (1, n, K), generator=g, device=DEV)] for n in (M, N))
+    a[:, :, ::32] = 4.0
+    w[:, :, 31::32] = -4.0
+    C = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+    chord.chord_mxfp4_gemm(quantise(a), M, quantise(w), N, K, C)
+    for lo in (0, 34000, 67100, M - 500):
+        assert torch.equal(C[lo:lo + 500], (a[0, lo:lo + 500].double() @ w[0].double().T).to(torch.bfloat16))
+    assert chord.chord_get_device_error() == 0
+
+
+@gpu
 def test_quantise_strided_groups_and_broadcast():
     need_gpu()
     big = torch.randn(4, 6, 40, 64, device=DEV)

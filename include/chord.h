@@ -590,7 +590,7 @@ chord_status chord_mxfp4_gemm(const void *Aq, size_t aq_bytes, int64_t M, const 
 
 #define CHORD_FEW_MAX_TOKENS 32
 
-/* Scratch bytes of chord_moe_layer_few: 4 bytes per pair and column of I (I
+/* Scratch bytes of chord_moe_layer_few: 6 bytes per pair and column of I (I
  * rounded up to 256), and the down projection's partial sums. */
 size_t chord_moe_few_workspace_bytes(int T, int topk, int E, int H, int I);
 
@@ -599,9 +599,9 @@ size_t chord_moe_few_workspace_bytes(int T, int topk, int E, int H, int I);
  * GEMMs, reductions and combine cost more than the weights' bytes):
  *   out[t] = bf16( sum over k with topk_ids[t, k] in [0, E) of
  *                  topk_w[t, k] * W2[e] ( SiLU(W13[e][:I] x_t) * (W13[e][I:] x_t) ) )
- * with FP32 sums; the weighted SiLU * up is kept to 16 significant bits in
- * between (chord_moe_layer rounds the gate_up result and SiLU * up to bf16, so
- * the two agree within those roundings).  Ids outside [0, E) are skipped, tokens with no local pair get +0.
+ * with FP32 sums, the weighted SiLU * up kept in FP32 between the two (chord_moe_layer
+ * rounds the gate_up result and SiLU * up to bf16, so the two agree within those
+ * roundings).  Ids outside [0, E) are skipped, tokens with no local pair get +0.
  *   weights     CHORD_WEIGHTS_INT4: blobs of chord_pack_weights, w13 (E, 2I, H) in
  *               CHORD_LAYOUT_TCGEN05 or CHORD_LAYOUT_GATE_UP_INTERLEAVED (read from
  *               its header), w2 (E, H, I) in CHORD_LAYOUT_TCGEN05; H % 128 == 0,

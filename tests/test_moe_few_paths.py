@@ -208,3 +208,62 @@ def test_infinity_in_an_activation_stays_in_its_token(T, value, fmt):
     assert torch.isnan(got[2]).all()                  # weights of 0 and both signs in that column
     keep = [t for t in range(T) if t != 2]
     assert torch.equal(got[keep].view(torch.int16), clean[keep].view(torch.int16))
+
+
+U0, U1 = 16760391 + 64, 16760391      # 24 bits each; 32 U rounded to two bf16 parts is off by 1024 either way
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["int4", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9, 32])
+def test_activation_is_kept_in_fp32(T, fmt):
+    """h_0 = 32 U0 and h_1 = 32 U1 (g = 32, whose SiLU is 32 to within 2^-22, and up sums that are
+    integers of 24 bits), and output rows that are s (h_0 - h_1): the sum cancels all but the
+    last bits.  Every partial sum is a multiple of 32 s below 2^29 s, so exact; an FP32 product
+    rounds each h to 2^-24 of 2^29, and the common error of SiLU scales the result."""
+    need_gpu()
+    H, I, base, digits, s = (128, 64, 8, 8, 0.25) if fmt == "int4" else (128, 64, 4, 12, 1.0)
+    v13, v2 = torch.zeros(1, 2 * I, H, dtype=torch.float64), torch.zeros(1, H, I, dtype=torch.float64)
+    x = torch.zeros(T, H, dtype=torch.float64)
+    for k in range(digits):
+        x[:, k] = base ** k / s
+        for i, u in enumerate((U0, U1)):
+            v13[0, I + i, k] = s * (u // base ** k % base)
+    x[:, 20] = 32 / s
+    v13[0, :2, 20] = s
+    v2[0, :, 0], v2[0, :, 1] = s, -s
+    assert torch.equal(x, x.to(torch.bfloat16).double())
+    if fmt == "int4":
+        blobs = []
+        for v in (v13, v2):
+            scale = torch.full((1, v.shape[1], v.shape[2] // 32), s, dtype=torch.bfloat16)
+            blob = torch.empty(chord.chord_packed_weight_bytes(1, v.shape[1], v.shape[2]), dtype=torch.uint8, device=DEV)
+            chord.chord_pack_weights((v / s + 8).to(torch.uint8).to(DEV), scale.to(DEV), blob)
+            blobs.append(blob)
+    else:
+        blobs = [mx_blob(v13), mx_blob(v2)]
+    ids, w = torch.zeros((T, 1), dtype=torch.int32), torch.ones(T, 1)
+    out = run(x.to(torch.bfloat16), ids, w, 1, I, *blobs, fmt)
+    ref = torch.full((T, H), 32 * s * (U0 - U1), dtype=torch.float64)
+    check(out, ref, ref * 2.0 ** -22 + 2 * s * 2.0 ** 29 * 2.0 ** -24)
+
+
+@gpu
+@pytest.mark.parametrize("fmt", ["int4", "mxfp4"])
+def test_few_results_differ_from_the_exact_sum_rounded(fmt):
+    """A relative error r in front of the last rounding changes r / 2^-7.5 of the results (the mean
+    step of bf16).  Chopping additions leave out half a unit of FP32 at most, of a partial
+    sum that is half of the final one on average: chains of 32 (gate and up, 1024 columns in two
+    sums) and 48 instructions (down, 512 columns in two sums, three parts), (2 * 32 + 48) / 2 * 2^-24 =
+    3.3e-6, 0.6 of 1000 results; a single chain of 7168 columns 3 of 1000."""
+    need_gpu()
+    T, E, topk, H, I = 16, 4, 4, 7168, 1984
+    g = torch.Generator().manual_seed(77)
+    v13, p13 = make_weights(fmt, E, 2 * I, H, g)
+    v2, p2 = make_weights(fmt, E, H, I, g)
+    ids, w = routing(T, E, topk, g)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16)
+    out = run(x, ids, w, E, I, p13(), p2(), fmt)
+    ref, tol = reference(x, ids, w, v13, v2)
+    check(out, ref, tol)
+    assert (out.cpu() != ref.to(torch.bfloat16)).double().mean() <= 1e-3

@@ -15,9 +15,11 @@
 // inside a tile is whatever puts a lane's own 32 columns into its slots, the same for A
 // and B.  An expert with more than eight tokens is taken in several passes.
 //   gate_up: an item is 64 gate rows and their 64 up rows of one expert, so a lane
-//     ends with a gate sum and its up sum; h is written as two bf16 numbers (value
-//     and remainder, 16 significant bits together).  Few items: a cluster of CTAs
-//     splits K and joins the sums through distributed shared memory in rank order.
+//     ends with a gate sum and its up sum.  h keeps its FP32 number as three bf16 parts of
+//     eight bits each, so the tensor cores multiply all of it (with two parts,
+//     16 bits, 2.4 of 1000 outputs were another bf16 number than the exact sum's for that
+//     reason alone; 16 tokens TP8 88.5 us for 87.7, 32 with MXFP4 170 for 159).  Few items: a cluster
+//     of CTAs splits K and joins the sums through distributed shared memory in rank order.
 //   down: several CTAs share 128 output rows for all experts: each takes a slice of
 //     the (pass, K stage) list, and the last one to finish adds the FP32 sums in
 //     slice order, so there is no combine pass and no order that changes a result.  The
@@ -40,7 +42,16 @@ namespace {
 constexpr int kConsumers = 4;                      // warps, 32 weight rows each
 constexpr int kThreads = (kConsumers + 1) * 32;    // and the producer warp
 constexpr int kPassTokens = 8;                     // tokens of one pass over an expert (MMA N)
-constexpr int kZeroBytes = 1024;                   // covers a token's row of a stage
+constexpr int kZeroBytes = 256;                    // covers a token's 128-column unit
+// The matrix instructions' FP32 additions chop, so a long chain of them on one accumulator ends
+// up a little too small, every time.  Chains are kept to 48 instructions and their sums added in
+// FP32 with rounding: kChainCols columns of gate_up's K (two chains of 32), kDownChainCols of the
+// down projection's (two of up to 48, see Spread).  With the 7168 columns of 16 tokens TP8 in one
+// chain, 3.3 of 1000 outputs were another bf16 number than the exact sum's, now 0.5 (FP32
+// products and sums in PyTorch: 0.25), for 0.5 us of gate_up's 54; with I = 1984 in one chain of the
+// down projection 2.1, now below 1.
+constexpr int kChainCols = 1024;
+constexpr int kDownChainCols = 512;
 constexpr size_t kSmemMax = 96 * 1024;             // dynamic; a ring never takes more than a third of an SM
 
 struct FewArgs {
@@ -50,7 +61,7 @@ struct FewArgs {
     int T, topk, E, H, I;
     const uint8_t* w13;
     const uint8_t* w2;
-    uint16_t* h;         // [2][T * topk, Ip]: bf16 values, then bf16 remainders; a row per (expert, token) in use
+    uint16_t* h;         // [3][T * topk, Ip]: an FP32 number as the sum of three bf16 parts; a row per (expert, token) in use
     int Ip;              // I rounded up to whole stages
     uint16_t* out;
     int* err;
@@ -223,7 +234,8 @@ struct Stage {
     static constexpr int kUpWeights = kScale + (MX ? 4096 : 1024);
     static constexpr int kDownWeights = kScale + 1024;
     static constexpr int kUpRow = kCols * 2 + 16;             // activations of a token, gate_up
-    static constexpr int kDownRow = kCols * 4 + 64;           // value and remainder, down
+    static constexpr int kDownPart = kCols * 2 + 64;          // one of the three parts of an activation row, down
+    static constexpr int kDownRow = 3 * kDownPart;
     // a stage with room for the activations of `tokens`, 128-byte aligned
     static __host__ __device__ int up_bytes(int tokens) { return (kUpWeights + tokens * kUpRow + 127) / 128 * 128; }
     static __host__ __device__ int down_bytes(int tokens) { return (kDownWeights + tokens * kDownRow + 127) / 128 * 128; }
@@ -391,12 +403,16 @@ struct LaneRows {
     uint32_t soff, sd_row, sd_tile;
 };
 
+struct NoMore {
+    __device__ uint4 operator()(int, int) const { return uint4{}; }
+};
+
 // One 128-column unit of a stage: 32 rows of this warp times eight columns.  b(j): this
-// lane's piece j of its column's activations; REST: a second operand for the same
-// columns (b(4 + j)).
-template <bool MX, bool FAST, bool REST, typename LoadB>
+// lane's piece j of its column's activations; MORE: `extra` more operands for the same
+// columns, more(j, e).
+template <bool MX, bool FAST, bool MORE, typename LoadB, typename LoadMore>
 __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32_t code_xor, uint32_t scale_add, bool on, int c,
-                                         float (&acc)[2][2][4], LoadB&& b) {
+                                         float (&acc)[2][2][4], LoadB&& b, int extra, LoadMore&& more) {
     uint4 q[2][2];
     Scale s[2][2];
     const uint32_t codes = st + (lr.off ^ code_xor);   // (MXFP4: d_tile and d_row are multiples of 1024)
@@ -428,14 +444,20 @@ __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32
         }
 #pragma unroll(MX && kOdd ? 1 : 4)   // rare: kept short, the instruction cache is
         for (int j = 0; j < 4; ++j) {
-            const uint4 v = b(j), r = REST ? b(4 + j) : v;
+            const uint4 v = b(j);
+            uint32_t x[2][2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                uint32_t x0[4], x1[4];
-                dequant8<MX, FAST, kOdd>(word(q[i][0], j), s[i][0], x0);
-                dequant8<MX, FAST, kOdd>(word(q[i][1], j), s[i][1], x1);
-                mma16816<kWhole>(acc[i], x0, x1, v);
-                if constexpr (REST) mma16816<kWhole>(acc[i], x0, x1, r);
+                dequant8<MX, FAST, kOdd>(word(q[i][0], j), s[i][0], x[i][0]);
+                dequant8<MX, FAST, kOdd>(word(q[i][1], j), s[i][1], x[i][1]);
+                mma16816<kWhole>(acc[i], x[i][0], x[i][1], v);
+            }
+            if constexpr (MORE) {
+                for (int e = 0; e < extra; ++e) {
+                    const uint4 r = more(j, e);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) mma16816<kWhole>(acc[i], x[i][0], x[i][1], r);
+                }
             }
         }
     };
@@ -475,12 +497,18 @@ __device__ __forceinline__ void store_h(const FewArgs& a, const Route& rt, int s
         for (int k = 0; k < a.topk; ++k)
             if (s_ids[t * a.topk + k] == e) wt += s_w[t * a.topk + k];
         const float h = wt * silu_times(i ? s.y : s.x, i ? s.w : s.z);
-        // bf16 value and remainder; no remainder for infinities and NaN
-        const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-        const float rest = h - __bfloat162float(hi);
+        // Three bf16 parts, each what is left cut to eight bits, so that a finite number has
+        // finite parts and their sum is h; infinities and NaN have the first one only.
+        const int64_t plane = (int64_t)a.T * a.topk * a.Ip;
         uint16_t* to = a.h + (int64_t)(rt.first[slot] + j) * a.Ip + h_pos<MX>(col);
-        to[0] = __bfloat16_as_ushort(hi);
-        to[(int64_t)a.T * a.topk * a.Ip] = __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(rest) ? rest : 0.0f));
+        float rest = h;
+#pragma unroll
+        for (int k = 0; k < 3; ++k, to += plane) {
+            const __nv_bfloat16 part = __float2bfloat16_rz(rest);
+            *to = __bfloat16_as_ushort(part);
+            rest -= __bfloat162float(part);
+            if (!isfinite(rest)) rest = 0.0f;
+        }
     }
 }
 
@@ -587,26 +615,36 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
             lr.sd_row = 2048 + quad[1] * 4 - quad[0] * 4;
         }
         float acc[2][2][4] = {};
-        for (int ks = ks0; ks < ks1; ++ks, r.next(a.depth)) {
-            if (ok) ok = tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err);
-            if (!ok) break;
-            const uint32_t st = rg.base + r.slot * a.stage_bytes;
-            const uint32_t xs = st + S::kUpWeights + g * S::kUpRow + c * 64;
+        float4 sum[2] = {};   // of finished chains
+        for (int ks = ks0; ks < ks1 && ok;) {
+            for (const int end = min(ks + kChainCols / S::kCols, ks1); ks < end; ++ks, r.next(a.depth)) {
+                ok = tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err);
+                if (!ok) break;
+                const uint32_t st = rg.base + r.slot * a.stage_bytes;
+                const uint32_t xs = st + S::kUpWeights + g * S::kUpRow + c * 64;
 #pragma unroll
-            for (int u = 0; u < S::kUnits; ++u) {
-                const bool on = ks * S::kCols + u * 128 + c * 32 < a.H;
-                const uint32_t xb = g < n && on ? xs + u * 256 : rg.zero;
-                unit_mma<MX, FAST, false>(st, lr, u * 64, u * kMxScaleBlock, on, c, acc,
-                                          [&](int j) { return b_order<MX>(lds128(xb + j * 16)); });
+                for (int u = 0; u < S::kUnits; ++u) {
+                    const bool on = ks * S::kCols + u * 128 + c * 32 < a.H;
+                    const uint32_t xb = g < n && on ? xs + u * 256 : rg.zero;
+                    unit_mma<MX, FAST, false>(st, lr, u * 64, u * kMxScaleBlock, on, c, acc,
+                                              [&](int j) { return b_order<MX>(lds128(xb + j * 16)); }, 0, NoMore{});
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&rg.empty[r.slot]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&rg.empty[r.slot]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float4 v = both<!MX && FAST>(acc[i]);
+                sum[i].x += v.x, sum[i].y += v.y, sum[i].z += v.z, sum[i].w += v.w;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[i][k >> 2][k & 3] = 0.0f;
+            }
         }
         const int col0 = m * 64 + 16 * warp + p;
         if (a.cluster == 1) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (ok) store_h<MX>(a, rt, slot, s_ids, s_w, col0 + 8 * i, c, both<!MX && FAST>(acc[i]));
+                if (ok) store_h<MX>(a, rt, slot, s_ids, s_w, col0 + 8 * i, c, sum[i]);
             continue;
         }
         // join the cluster's K ranges: tile q = 2 warp + i belongs to CTA q mod cluster, which
@@ -618,7 +656,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
 #pragma unroll
         for (uint32_t i = 0; i < 2; ++i) {
             const uint32_t q = (uint32_t)warp * 2 + i;
-            st_cluster(smem_u32(buf + ((q / a.cluster) * a.cluster + rank) * 32 + lane), q % a.cluster, both<!MX && FAST>(acc[i]));
+            st_cluster(smem_u32(buf + ((q / a.cluster) * a.cluster + rank) * 32 + lane), q % a.cluster, sum[i]);
         }
         __syncwarp();
         cluster_sync_all();
@@ -674,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 4) few_gate_up_kernel(const FewArgs 
 template <bool MX>
 __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt, const Ring& rg, int tile, int v0, int v1, int kst) {
     using S = Stage<MX>;
-    constexpr int kPieces = S::kCols / 8;   // 16-byte pieces of a value row; as many of the remainder row
+    constexpr int kPieces = S::kCols / 8;   // 16-byte pieces of a part of a row
     const int lane = threadIdx.x & 31;
     struct At {
         int sl, ks;
@@ -706,15 +744,20 @@ __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt,
         }
     };
     const int64_t plane = (int64_t)a.T * a.topk * a.Ip;
-    const int64_t second = MX ? plane : plane - kPieces * 8;   // INT4: lanes 16 .. 31 take the remainder row
+    const int64_t second = MX ? plane : plane - kPieces * 8;   // INT4: lanes 16 .. 31 take the second part
     auto activations = [&](const At& at, int slot) {
         const int n = __popc(rt.tokens[at.sl]);
         uint32_t hs = smem_u32(rg.ptr + slot * a.stage_bytes + S::kDownWeights) + lane * 16;
         const uint16_t* src = a.h + (int64_t)rt.first[at.sl] * a.Ip + at.ks * S::kCols + lane * 8;
-        if (!MX && lane >= kPieces) src += second;
+        if (!MX && lane >= kPieces) src += second, hs += S::kDownPart - kPieces * 16;
         for (int j = 0; j < n; ++j, hs += S::kDownRow, src += a.Ip) {
             cp_async16(hs, src);
-            if constexpr (MX) cp_async16(hs + kPieces * 16, src + second);
+            if constexpr (MX) {
+                cp_async16(hs + S::kDownPart, src + second);
+                cp_async16(hs + 2 * S::kDownPart, src + 2 * second);
+            } else {
+                if (lane < kPieces) cp_async16(hs + 2 * S::kDownPart, src + 2 * plane);
+            }
         }
         cp_async_arrive_noinc(&rg.full[slot]);
     };
@@ -737,17 +780,52 @@ __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt,
     drain_ring(a, rg, r, issued);
 }
 
-// A pass's sums (column j: its j-th token) into the sums by token (lane (g, c), tile nt:
-// tokens 8 nt + 2c and + 1).  half: columns 4 .. 7 hold the remainders' products.
+// Where the three parts of a pass's activations go among the eight columns.
+//   kOne: up to two tokens, one instruction: token j's parts in columns 4 j, 4 j + 1, 4 j + 2
+//   kTwo: up to four, two instructions: first parts in columns 0 .. 3, second ones in 4 .. 7;
+//     third ones in 0 .. 3
+//   kThree: a column a token, an instruction a part
+// The enumerator is the number of instructions after the first.
+enum Spread { kOne = 0, kTwo = 1, kThree = 2 };
+
+// A pass's sums into the sums by token (lane (g, c), tile nt: tokens 8 nt + 2c and + 1).
 template <int NT, bool SIXTEENTH>
-__device__ __forceinline__ void add_pass(float (&sum)[2][NT][4], float (&chains)[2][2][4], uint32_t tokens, bool half, int c) {
+__device__ __forceinline__ void add_pass(float (&sum)[2][NT][4], float (&chains)[2][2][4], uint32_t tokens, Spread spread, int c) {
     float p[2][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         p[i >> 2][i & 3] = fmaf(chains[i >> 2][0][i & 3], SIXTEENTH ? 16.0f : 1.0f, chains[i >> 2][1][i & 3]);
         chains[i >> 2][0][i & 3] = chains[i >> 2][1][i & 3] = 0.0f;
     }
-    if (half) {
+    auto add = [&](int ta, int tb, const float (&va)[4], const float (&vb)[4]) {   // tokens and their sums by (tile, row half)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (NT > 1 && (ta >> 3) != nt && (tb >> 3) != nt) continue;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int t = 8 * nt + 2 * c + k;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (t == ta) sum[i >> 1][nt][(i & 1) * 2 + k] += va[i];
+                    if (t == tb) sum[i >> 1][nt][(i & 1) * 2 + k] += vb[i];
+                }
+            }
+        }
+    };
+    if (spread == kOne) {   // lanes c = 0, 1: the first token's parts, 2, 3: the second one's
+        float va[4], vb[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v = p[i >> 1][(i & 1) * 2] + p[i >> 1][(i & 1) * 2 + 1];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            va[i] = __shfl_sync(0xffffffffu, v, 0, 4);
+            vb[i] = __shfl_sync(0xffffffffu, v, 2, 4);
+        }
+        const int ta = __ffs(tokens) - 1, tb = __ffs(tokens & (tokens - 1)) - 1;
+        add(ta, tb, va, vb);
+        return;
+    }
+    if (spread == kTwo) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] += __shfl_xor_sync(0xffffffffu, p[i >> 2][i & 3], 2);
     }
@@ -756,23 +834,13 @@ __device__ __forceinline__ void add_pass(float (&sum)[2][NT][4], float (&chains)
         tokens &= tokens - 1;
         const int tb = __ffs(tokens) - 1;   // -1: no such column
         tokens &= tokens - 1;
-        float v[2][4];
+        float va[4], vb[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i >> 2][i & 3] = __shfl_sync(0xffffffffu, p[i >> 2][i & 3], jj, 4);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && (ta >> 3) != nt && (tb >> 3) != nt) continue;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int t = 8 * nt + 2 * c + k;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {   // (tile, row half)
-                    if (t == ta) sum[i >> 1][nt][(i & 1) * 2 + k] += v[i >> 1][(i & 1) * 2];
-                    if (t == tb) sum[i >> 1][nt][(i & 1) * 2 + k] += v[i >> 1][(i & 1) * 2 + 1];
-                }
-            }
+        for (int i = 0; i < 4; ++i) {
+            va[i] = __shfl_sync(0xffffffffu, p[i >> 1][(i & 1) * 2], jj, 4);
+            vb[i] = __shfl_sync(0xffffffffu, p[i >> 1][(i & 1) * 2 + 1], jj, 4);
         }
+        add(ta, tb, va, vb);
     }
 }
 
@@ -789,15 +857,15 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
     tc5::Ring r;
     int sl = v0 / kst, ks = v0 - sl * kst;
     float pass[2][2][4] = {};
-    for (int left = v1 - v0; left > 0; ++sl, ks = 0) {
+    for (int left = v1 - v0; left > 0;) {
         const uint32_t tokens = rt.tokens[sl];
         const int n = __popc(tokens);
-        // up to four tokens: their values in columns 0 .. 3, their remainders in 4 .. 7, one
-        // instruction for both; more: two instructions
-        const bool half = n <= 4;
-        const int j = half ? g & 3 : g;
-        const uint32_t h0 = j < n ? S::kDownWeights + (uint32_t)j * S::kDownRow + c * 16 + (half && g >= 4 ? S::kCols * 2 : 0) : 0u;
-        const int end = min(kst, ks + left);
+        const Spread spread = n <= 2 ? kOne : n <= 4 ? kTwo : kThree;
+        const int j = spread == kOne ? g >> 2 : spread == kTwo ? g & 3 : g;            // this lane's token of the pass
+        const int part = spread == kOne ? g & 3 : spread == kTwo ? g >> 2 : 0;
+        const uint32_t h0 = j < n && part < 3 ? S::kDownWeights + (uint32_t)j * S::kDownRow + c * 16 + part * S::kDownPart : 0u;
+        const uint32_t h1 = j < n && part < 1 ? h0 + S::kDownPart * (spread == kTwo ? 2 : 1) : 0u;   // of the instructions after
+        const int end = min(min(kst, ks + left), ks + (spread == kOne ? 2 : 1) * kDownChainCols / S::kCols);
         left -= end - ks;
         for (; ks < end; ++ks, r.next(a.depth)) {
             if (!tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err)) return;
@@ -806,17 +874,24 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
             for (int u = 0; u < S::kUnits; ++u) {
                 const bool on = ks * S::kCols + u * 128 + c * 32 < a.I;
                 const uint32_t hb = h0 && on ? st + h0 + u * 256 : rg.zero;
-                if (half)
+                if (spread == kOne) {
                     unit_mma<MX, FAST, false>(st, lr, u * 64, u * kMxScaleBlock, on, c, pass,
-                                              [&](int j) { return lds128(hb + j * 64); });
-                else
+                                              [&](int j) { return lds128(hb + j * 64); }, 0, NoMore{});
+                } else {
+                    const uint32_t more = h1 && on ? st + h1 + u * 256 : rg.zero, step = h1 && on ? S::kDownPart : 0;
                     unit_mma<MX, FAST, true>(st, lr, u * 64, u * kMxScaleBlock, on, c, pass,
-                                             [&](int j) { return lds128(hb + (j & 3) * 64 + (j >> 2) * S::kCols * 2); });
+                                             [&](int j) { return lds128(hb + j * 64); }, spread,
+                                             [&](int j, int e) { return lds128(more + j * 64 + e * step); });
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&rg.empty[r.slot]);
         }
-        add_pass<NT, !MX && FAST>(sum, pass, tokens, half, c);
+        add_pass<NT, !MX && FAST>(sum, pass, tokens, spread, c);
+        if (ks == kst) {
+            ++sl;
+            ks = 0;
+        }
     }
 }
 
@@ -1059,13 +1134,13 @@ cudaError_t launch_few(const FewArgs& a, bool mx, cudaStream_t st) {
     return mx ? launch_few_nt<true, 4>(a, st) : launch_few_nt<false, 4>(a, st);
 }
 
-// Workspace: h (value and remainder), the down kernel's slices and its counters.
+// Workspace: h (three parts), the down kernel's slices and its counters.
 struct FewWs {
     size_t part, joined, total;
 };
 FewWs few_ws(int T, int topk, int H, int I) {
     FewWs w;
-    w.part = (size_t)T * (size_t)topk * (((size_t)I + 255) / 256 * 256) * 4;
+    w.part = (size_t)T * (size_t)topk * (((size_t)I + 255) / 256 * 256) * 6;
     const size_t tiles = ((size_t)H + 127) / 128, nt = T <= 8 ? 1 : (T <= 16 ? 2 : 4);
     w.joined = w.part + tiles * (size_t)down_slices(H, INT32_MAX) * kConsumers * 2 * nt * 512;
     w.total = w.joined + (tiles * 4 + 255) / 256 * 256;

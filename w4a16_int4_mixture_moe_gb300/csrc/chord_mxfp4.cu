@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(256) mx_index_kernel(const RowSource s, int64_
 template <bool F32, bool VEC>
 __global__ void __launch_bounds__(256) mx_quantize_shared_kernel(const RowSource s, int64_t a_rows, int64_t G, int64_t N, int K,
                                                                  int run, uint8_t* __restrict__ packed,
-                                                                 const int32_t* __restrict__ index) {
+                                                                 const int32_t* index) {
     pdl_trigger();
     constexpr int kRows = 2;
     const int64_t ntp = *s.ntp;   // older than the index kernel, as the rows and sorted_ids are
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(256) mx_quantize_shared_kernel(const RowSource
                 const int64_t p = (row0 + i) * s.divisor + first + lane;
                 int64_t pos = -1;
                 if (row0 + i < a_rows && first + lane < s.divisor && p < s.id_limit) {
-                    pos = index[p];
+                    pos = __ldcg(index + p);   // not as a read-only value: that might be fetched ahead of the wait
                     if (pos < 0 || pos >= ntp || __ldg(s.sorted_ids + pos) != (int32_t)p) pos = -1;
                 }
                 on[i] = __ballot_sync(0xffffffffu, pos >= 0);

@@ -560,7 +560,8 @@ chord_status chord_mxfp4_dequantize(const void *packed, size_t packed_bytes, int
 
 /* Block size for the grouped product: the rows an expert rarely exceeds
  * (tok_e + 3 sqrt(tok_e) + 1, tok_e = T * topk / E_global) in as few equal blocks
- * of at most 208 rows as hold tok_e + 2 sqrt(tok_e) + 1 of them, rounded up to 16. */
+ * of at most 208 rows as hold tok_e + 2 sqrt(tok_e) + 1 of them, rounded up to 16.
+ * Always returns a valid block_m. */
 int chord_mxfp4_select_block_m(int T, int topk, int E_local, int E_global);
 
 /* Grouped product, the indexed contract of chord_w4a16_moe_gemm with both

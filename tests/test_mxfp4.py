@@ -122,6 +122,13 @@ def test_sizes_past_64_bits_are_refused():
                                         64, 32, 8, p, 0, None, None) == 3
 
 
+@pytest.mark.parametrize("T,topk,E_local,E_global", [(-1, 8, 8, 8), (-2 ** 31, 1, 1, 1), (5, -3, 0, 0), (2 ** 31 - 1, 2 ** 31 - 1, 1, 1),
+                                                     (64, 8, 48, 0), (64, 8, 48, -5)])
+def test_select_block_m_is_valid_for_any_arguments(T, topk, E_local, E_global):
+    bm = chord.chord_mxfp4_select_block_m(T, topk, E_local, E_global)
+    assert bm % 16 == 0 and 16 <= bm <= 208
+
+
 def test_select_block_m():
     for T, topk, E in [(1, 1, 8), (1, 8, 384), (64, 8, 48), (1024, 8, 48), (4096, 8, 48), (100000, 8, 8), (0, 8, 8)]:
         bm = chord.chord_mxfp4_select_block_m(T, topk, E, E)

@@ -658,7 +658,7 @@ extern "C" {
 
 int chord_mxfp4_select_block_m(int T, int topk, int E_local, int E_global) {
     const int eg = E_global > 0 ? E_global : (E_local > 0 ? E_local : 1);
-    const double tok_e = (double)T * (double)(topk > 0 ? topk : 1) / (double)eg;
+    const double tok_e = (double)(T > 0 ? T : 0) * (double)(topk > 0 ? topk : 1) / (double)eg;
     // rows that an expert rarely exceeds (mean + 3 sd of a Poisson count), in
     // as few equal blocks as the kernel's largest allows
     const double need = tok_e + 3.0 * sqrt(tok_e) + 1.0;

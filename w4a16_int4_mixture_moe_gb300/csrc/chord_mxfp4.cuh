@@ -76,11 +76,4 @@ __device__ __forceinline__ float mx_scale_f32(uint32_t b) {
     return __uint_as_float(b == 255u ? 0x7FC00000u : (b == 0u ? 0x00400000u : b << 23));
 }
 
-// The value of an E2M1 code without its scale.
-__device__ __forceinline__ float e2m1_f32(uint32_t c) {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const float mag = e == 0u ? 0.5f * (float)m : (float)(1u << (e - 1u)) * (1.0f + 0.5f * (float)m);
-    return (c & 8u) ? -mag : mag;
-}
-
 }  // namespace chord

@@ -253,9 +253,9 @@ def test_activation_is_kept_in_fp32(T, fmt):
 def test_few_results_differ_from_the_exact_sum_rounded(fmt):
     """A relative error r in front of the last rounding changes r / 2^-7.5 of the results (the mean
     step of bf16).  Chopping additions leave out half a unit of FP32 at most, of a partial
-    sum that is half of the final one on average: chains of 32 (gate and up, 1024 columns in two
-    sums) and 48 instructions (down, 512 columns in two sums, three parts), (2 * 32 + 48) / 2 * 2^-24 =
-    3.3e-6, 0.6 of 1000 results; a single chain of 7168 columns 3 of 1000."""
+    sum that is half of the final one on average: chains of 32 instructions (gate and up, 1024
+    columns in two sums) and of 48 (down), (2 * 32 + 48) / 2 * 2^-24 = 3.3e-6, 0.6 of 1000
+    results; a single chain of 7168 columns 3 of 1000."""
     need_gpu()
     T, E, topk, H, I = 16, 4, 4, 7168, 1984
     g = torch.Generator().manual_seed(77)

@@ -18,7 +18,7 @@
 //     ends with a gate sum and its up sum.  h keeps its FP32 number as three bf16 parts of
 //     eight bits each, so the tensor cores multiply all of it (with two parts,
 //     16 bits, 2.4 of 1000 outputs were another bf16 number than the exact sum's for that
-//     reason alone; 16 tokens TP8 88.5 us for 87.7, 32 with MXFP4 170 for 159).  Few items: a cluster
+//     reason alone; 16 tokens TP8 88.3 us for 87.7, 32 with MXFP4 168 for 159).  Few items: a cluster
 //     of CTAs splits K and joins the sums through distributed shared memory in rank order.
 //   down: several CTAs share 128 output rows for all experts: each takes a slice of
 //     the (pass, K stage) list, and the last one to finish adds the FP32 sums in
@@ -45,13 +45,11 @@ constexpr int kPassTokens = 8;                     // tokens of one pass over an
 constexpr int kZeroBytes = 256;                    // covers a token's 128-column unit
 // The matrix instructions' FP32 additions chop, so a long chain of them on one accumulator ends
 // up a little too small, every time.  Chains are kept to 48 instructions and their sums added in
-// FP32 with rounding: kChainCols columns of gate_up's K (two chains of 32), kDownChainCols of the
-// down projection's (two of up to 48, see Spread).  With the 7168 columns of 16 tokens TP8 in one
-// chain, 3.3 of 1000 outputs were another bf16 number than the exact sum's, now 0.5 (FP32
-// products and sums in PyTorch: 0.25), for 0.5 us of gate_up's 54; with I = 1984 in one chain of the
-// down projection 2.1, now below 1.
+// FP32 with rounding: kChainCols columns of gate_up's K (two chains of 32), down_chain_cols of the
+// down projection's.  With the 7168 columns of 16 tokens TP8 in one chain, 3.3 of 1000 outputs were
+// another bf16 number than the exact sum's, now 0.5 (FP32 products and sums in PyTorch: 0.25),
+// for 0.5 us of gate_up's 54; with I = 1984 in one chain of the down projection 2.1, now below 1.
 constexpr int kChainCols = 1024;
-constexpr int kDownChainCols = 512;
 constexpr size_t kSmemMax = 96 * 1024;             // dynamic; a ring never takes more than a third of an SM
 
 struct FewArgs {
@@ -408,8 +406,8 @@ struct NoMore {
 };
 
 // One 128-column unit of a stage: 32 rows of this warp times eight columns.  b(j): this
-// lane's piece j of its column's activations; MORE: `extra` more operands for the same
-// columns, more(j, e).
+// lane's piece j of its column's activations; MORE: `extra` (one or two) more operands for the
+// same columns, more(j, e).
 template <bool MX, bool FAST, bool MORE, typename LoadB, typename LoadMore>
 __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32_t code_xor, uint32_t scale_add, bool on, int c,
                                          float (&acc)[2][2][4], LoadB&& b, int extra, LoadMore&& more) {
@@ -445,6 +443,12 @@ __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32
 #pragma unroll(MX && kOdd ? 1 : 4)   // rare: kept short, the instruction cache is
         for (int j = 0; j < 4; ++j) {
             const uint4 v = b(j);
+            uint4 r0, r1;   // loaded ahead of the dequantisation (one operand after the other: 8 experts of
+                            // 4096 x 3584, 16 tokens 71.6 us, 69.5 so)
+            if constexpr (MORE) {
+                r0 = more(j, 0);
+                r1 = more(j, extra - 1);
+            }
             uint32_t x[2][2][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -453,10 +457,11 @@ __device__ __forceinline__ void unit_mma(uint32_t st, const LaneRows& lr, uint32
                 mma16816<kWhole>(acc[i], x[i][0], x[i][1], v);
             }
             if constexpr (MORE) {
-                for (int e = 0; e < extra; ++e) {
-                    const uint4 r = more(j, e);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) mma16816<kWhole>(acc[i], x[i][0], x[i][1], r);
+                for (int i = 0; i < 2; ++i) mma16816<kWhole>(acc[i], x[i][0], x[i][1], r0);
+                if (extra > 1) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) mma16816<kWhole>(acc[i], x[i][0], x[i][1], r1);
                 }
             }
         }
@@ -787,6 +792,8 @@ __device__ __forceinline__ void down_producer(const FewArgs& a, const Route& rt,
 //   kThree: a column a token, an instruction a part
 // The enumerator is the number of instructions after the first.
 enum Spread { kOne = 0, kTwo = 1, kThree = 2 };
+// Columns of a chain: 48 instructions on each of its two sums.
+__device__ __forceinline__ int down_chain_cols(Spread s) { return s == kOne ? 1536 : s == kTwo ? 768 : 512; }
 
 // A pass's sums into the sums by token (lane (g, c), tile nt: tokens 8 nt + 2c and + 1).
 template <int NT, bool SIXTEENTH>
@@ -865,7 +872,7 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
         const int part = spread == kOne ? g & 3 : spread == kTwo ? g >> 2 : 0;
         const uint32_t h0 = j < n && part < 3 ? S::kDownWeights + (uint32_t)j * S::kDownRow + c * 16 + part * S::kDownPart : 0u;
         const uint32_t h1 = j < n && part < 1 ? h0 + S::kDownPart * (spread == kTwo ? 2 : 1) : 0u;   // of the instructions after
-        const int end = min(min(kst, ks + left), ks + (spread == kOne ? 2 : 1) * kDownChainCols / S::kCols);
+        const int end = min(min(kst, ks + left), ks + down_chain_cols(spread) / S::kCols);
         left -= end - ks;
         for (; ks < end; ++ks, r.next(a.depth)) {
             if (!tc5::wait(&rg.full[r.slot], r.phase, rg.abort_flag, a.err)) return;

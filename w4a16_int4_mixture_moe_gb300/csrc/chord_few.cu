@@ -679,7 +679,7 @@ __device__ __forceinline__ void up_consumer(const FewArgs& a, const Route& rt, c
 
 // One token on 8 experts of 2 x 256 x 7168 is latency: 3 us to the first weights' copies, 2 to
 // their arrival, then 16.5 MB.  More tokens: the weights' stream, with instruction issue
-// close behind (8 tokens, 57 experts: 117 MB at 5.0 TB/s; 16 tokens INT4 issue 2.3 of 4
+// close behind (8 tokens, 57 experts: 117 MB at 5.0 TB/s; 16 tokens INT4 issue 2.1 of 4
 // instructions a cycle; MXFP4 codes take 17 operations for eight against 9).
 template <bool MX>
 __global__ void __launch_bounds__(kThreads, 4) few_gate_up_kernel(const FewArgs a) {
@@ -851,7 +851,7 @@ __device__ __forceinline__ void add_pass(float (&sum)[2][NT][4], float (&chains)
     }
 }
 
-template <bool MX, int NT, bool FAST>
+template <bool MX, int NT, bool ONE, bool FAST>
 __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt, const Ring& rg, int v0, int v1, int kst,
                                               float (&sum)[2][NT][4]) {
     using S = Stage<MX>;
@@ -867,7 +867,7 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
     for (int left = v1 - v0; left > 0;) {
         const uint32_t tokens = rt.tokens[sl];
         const int n = __popc(tokens);
-        const Spread spread = n <= 2 ? kOne : n <= 4 ? kTwo : kThree;
+        const Spread spread = ONE || n <= 2 ? kOne : n <= 4 ? kTwo : kThree;
         const int j = spread == kOne ? g >> 2 : spread == kTwo ? g & 3 : g;            // this lane's token of the pass
         const int part = spread == kOne ? g & 3 : spread == kTwo ? g >> 2 : 0;
         const uint32_t h0 = j < n && part < 3 ? S::kDownWeights + (uint32_t)j * S::kDownRow + c * 16 + part * S::kDownPart : 0u;
@@ -881,7 +881,7 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
             for (int u = 0; u < S::kUnits; ++u) {
                 const bool on = ks * S::kCols + u * 128 + c * 32 < a.I;
                 const uint32_t hb = h0 && on ? st + h0 + u * 256 : rg.zero;
-                if (spread == kOne) {
+                if (ONE || spread == kOne) {
                     unit_mma<MX, FAST, false>(st, lr, u * 64, u * kMxScaleBlock, on, c, pass,
                                               [&](int j) { return lds128(hb + j * 64); }, 0, NoMore{});
                 } else {
@@ -894,7 +894,7 @@ __device__ __forceinline__ void down_consumer(const FewArgs& a, const Route& rt,
             __syncwarp();
             if (lane == 0) mbar_arrive(&rg.empty[r.slot]);
         }
-        add_pass<NT, !MX && FAST>(sum, pass, tokens, spread, c);
+        add_pass<NT, !MX && FAST>(sum, pass, tokens, ONE ? kOne : spread, c);
         if (ks == kst) {
             ++sl;
             ks = 0;
@@ -920,9 +920,11 @@ __host__ __device__ __forceinline__ size_t down_part_bytes(int nt, int cluster) 
 // CTAs fit beside gate_up's.  (Both halves in one cooperative launch, the ring filled
 // ahead of a grid barrier, measured the same: 8 tokens 58.6 us against 58.5, 16 tokens 93
 // against 89.)
+// ONE: no pass has more than two tokens, so the code for more of them is not there (one token
+// TP8 with its weights in L2 18.7 us, with it 19.9).
 // CLUSTERED: four CTAs per SM.  Else three, so up to 128 registers a thread: with 96 the eight
-// tokens of MXFP4 TP8 took 59.9 us instead of 54.1.
-template <bool MX, int NT, bool CLUSTERED>
+// tokens of MXFP4 TP8 (59 experts) take 65.3 us instead of 64.6.
+template <bool MX, int NT, bool ONE, bool CLUSTERED>
 __global__ void __launch_bounds__(kThreads, CLUSTERED ? 4 : 3) few_down_kernel(const FewArgs a) {
     using S = Stage<MX>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -947,9 +949,9 @@ __global__ void __launch_bounds__(kThreads, CLUSTERED ? 4 : 3) few_down_kernel(c
     if (warp == kConsumers)
         down_producer<MX>(a, rt, rg, tile, v0, v1, kst);
     else if (MX || (sh.flags & 8))
-        down_consumer<MX, NT, true>(a, rt, rg, v0, v1, kst, acc);
+        down_consumer<MX, NT, ONE, true>(a, rt, rg, v0, v1, kst, acc);
     else
-        down_consumer<MX, NT, false>(a, rt, rg, v0, v1, kst, acc);
+        down_consumer<MX, NT, ONE, false>(a, rt, rg, v0, v1, kst, acc);
     __syncwarp();
     constexpr int kTiles = kConsumers * 2 * NT;      // (16 rows, 8 tokens) tiles of a CTA, q = (2 warp + i) NT + nt
     constexpr int kPer = kTiles * 32;                // float4 of a CTA: [tile][lane]
@@ -1086,17 +1088,18 @@ cudaError_t launch(Kern kern, const FewArgs& a, unsigned groups, size_t smem, bo
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <bool MX, int NT>
+template <bool MX, int NT, bool ONE>
 cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     using S = Stage<MX>;
     const int sms = device_info().sm_count;
     const size_t route = route_bytes(a.E, a.T * a.topk, a.slot_cap);
     // gate_up: three CTAs per SM while the items of an even routing then run in one wave
-    // (they spread evenly: the layer for 16 tokens TP8, 436 items, 84 us against 92 with four per
-    // SM), else four (32 tokens EP8, 768 items: 99 us against 111).  Where they
+    // (they spread evenly: the layer for 16 tokens TP8, 436 items, 88 us against 92.5 with four per
+    // SM), else four (32 tokens EP8, 22 experts of 32 items each: 138 us against 143).  Where they
     // would leave half of the GPU idle, a cluster shares each item's K range, three stages or
-    // more a CTA (4 tokens, 16 experts of 2 x 1024 x 1024, eight stages: in twos 21.6 us, in
-    // fours 24.7).
+    // more a CTA (4 tokens, top-2 of 16 experts of 2 x 1024 x 1024, eight stages: in twos 17.2 us, in
+    // fours 18.5).  Every pair counts as local: on an expert-parallel share fewer items come than
+    // are planned for, and clusters are smaller than they might be.
     const int mt = (a.I + 63) / 64, stages = (a.H + S::kCols - 1) / S::kCols;
     const int64_t items = (int64_t)a.slot_cap * mt;
     const double pairs = (double)a.T * a.topk, hit = a.E * (1.0 - pow(1.0 - 1.0 / a.E, pairs));   // experts with a token
@@ -1120,7 +1123,7 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
     const int slices = down_slices(a.H, list);
     a.stage_bytes = S::down_bytes(tokens);
     // in clusters of up to eight where the ring then leaves room for four CTAs per SM (16
-    // tokens of a layer of 8 experts, 256 x 128: 17.5 us, joined by the last CTA 19.6)
+    // tokens of a layer of 8 experts, 256 x 128: 12.5 us, joined by the last CTA 14.4)
     a.cluster = slices < 8 ? slices : 8;
     a.depth = ring_depth(third - route, a.stage_bytes, (list + a.cluster - 1) / a.cluster);
     smem = (size_t)a.depth * a.stage_bytes + route + down_part_bytes(NT, a.cluster);
@@ -1131,14 +1134,15 @@ cudaError_t launch_few_nt(FewArgs a, cudaStream_t st) {
         smem = (size_t)a.depth * a.stage_bytes + route;
     }
     const unsigned groups = (unsigned)tiles;
-    return clustered ? launch(few_down_kernel<MX, NT, true>, a, groups, smem, true, pdl_enabled(), st)
-                     : launch(few_down_kernel<MX, NT, false>, a, groups, smem, false, pdl_enabled(), st);
+    return clustered ? launch(few_down_kernel<MX, NT, ONE, true>, a, groups, smem, true, pdl_enabled(), st)
+                     : launch(few_down_kernel<MX, NT, ONE, false>, a, groups, smem, false, pdl_enabled(), st);
 }
 
 cudaError_t launch_few(const FewArgs& a, bool mx, cudaStream_t st) {
-    if (a.T <= 8) return mx ? launch_few_nt<true, 1>(a, st) : launch_few_nt<false, 1>(a, st);
-    if (a.T <= 16) return mx ? launch_few_nt<true, 2>(a, st) : launch_few_nt<false, 2>(a, st);
-    return mx ? launch_few_nt<true, 4>(a, st) : launch_few_nt<false, 4>(a, st);
+    if (a.T <= 2) return mx ? launch_few_nt<true, 1, true>(a, st) : launch_few_nt<false, 1, true>(a, st);
+    if (a.T <= 8) return mx ? launch_few_nt<true, 1, false>(a, st) : launch_few_nt<false, 1, false>(a, st);
+    if (a.T <= 16) return mx ? launch_few_nt<true, 2, false>(a, st) : launch_few_nt<false, 2, false>(a, st);
+    return mx ? launch_few_nt<true, 4, false>(a, st) : launch_few_nt<false, 4, false>(a, st);
 }
 
 // Workspace: h (three parts), the down kernel's slices and its counters.

@@ -613,9 +613,12 @@ size_t chord_moe_few_workspace_bytes(int T, int topk, int E, int H, int I);
  *   workspace   >= chord_moe_few_workspace_bytes(T, topk, E, H, I), 16-byte aligned;
  *               calls that overlap on the GPU need one each
  * The result does not depend on the order in which blocks run.  An expert with
- * more than eight tokens is read once for every eight, so for few experts with
- * many tokens each (32 tokens over 8 experts of 4096 x 1024: 67 us against 54)
- * chord_moe_layer is the faster call. */
+ * more than eight tokens is read once for every eight.  When to call it (INT4,
+ * against chord_moe_layer_cached on the same weights and routing, GB300): for up
+ * to 8 tokens it was the faster call in every layer measured, 1.02 to 1.7 times;
+ * for 9 to 16 tokens where H >= 4096, 1.04 to 1.25 times; beyond that, and above 8
+ * tokens for H = 2048, chord_moe_layer_cached is as fast or faster (32 tokens over 64
+ * experts of 2048 x 1408: 81 us against 115). */
 chord_status chord_moe_layer_few(const void *x, const int32_t *topk_ids, const float *topk_w, int T,
                                  int topk, int E, int H, int I, int weights, const void *packed_w13,
                                  size_t w13_bytes, const void *packed_w2, size_t w2_bytes,

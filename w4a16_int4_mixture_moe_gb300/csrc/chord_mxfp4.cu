@@ -5,8 +5,8 @@
 //   e    = floor(log2 a) - 2, clamped to [-127, 127]   (a = 0: e = -127)
 //   code = the E2M1 number nearest to v * 2^-e (ties to the even code), at most 6
 // stored as (codes, b = e + 127).  2 is the largest exponent of E2M1, so the
-// block's largest element lands in [4, 8) and at most a third of that range
-// saturates at 6 (the OCP Microscaling specification's conversion).  v * 2^-e is exact in
+// block's largest element lands in [4, 8); what is above 6 saturates, off by less than
+// 2 units, a quarter of it (the OCP Microscaling specification's conversion).  v * 2^-e is exact in
 // FP32 (a power of two), so the only rounding is the code's.  A block that
 // holds an infinity or NaN gets the NaN scale: it stays visible downstream.
 #include <cuda_bf16.h>

@@ -103,7 +103,7 @@ def test_clusters_that_take_a_second_item(fmt, layout, H):
 
 @gpu
 @pytest.mark.parametrize("fmt", ["int4", "mxfp4"])
-@pytest.mark.parametrize("T", [3, 8, 9, 16, 24])
+@pytest.mark.parametrize("T", [1, 2, 3, 8, 9, 16, 24])
 @pytest.mark.parametrize("H,I", [(256, 128), (640, 320)])
 def test_lists_joined_by_the_last_cta(T, H, I, fmt):
     """Pass lists long enough for slices that are no cluster: sums through the workspace."""

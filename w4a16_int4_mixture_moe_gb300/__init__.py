@@ -362,7 +362,9 @@ def _dtype(t, what: str) -> int:
 
 
 # The library sees an address and sizes: a tensor of another type, shape or layout, or of
-# host memory, would be misread without a word, so it is refused here.  Each returns the address.
+# host memory, would be misread without a word, so it is refused here.  _dense and _ints return the
+# address.  A small call is bound by its host time, so the checks are few and in line where they
+# are one condition.
 
 def _refuse(what, name, t, expected):
     where = "" if t.is_cuda else ", not in device memory"
@@ -385,11 +387,11 @@ def _ints(what, name, t, at_least=1):
     _refuse(what, name, t, f"a dense int32 array of {at_least} or more in device memory")
 
 
-def _blob(what, name, t):
-    """Packed bytes or scratch."""
-    if t.is_contiguous() and t.is_cuda:
-        return t.data_ptr()
-    _refuse(what, name, t, "dense bytes in device memory")
+def _refuse_blob(what, **blobs):
+    """The first of these packed matrices or workspaces that is not dense device memory."""
+    for name, t in blobs.items():
+        if not (t.is_contiguous() and t.is_cuda):
+            _refuse(what, name, t, "dense bytes in device memory")
 
 
 def chord_mxfp4_bytes(G: int, N: int, K: int) -> int:
@@ -402,12 +404,15 @@ def chord_mxfp4_rows_bytes(capacity: int, block_m: int, K: int) -> int:
 
 def chord_mxfp4_quantize(src, packed, stream=None):
     """src bf16 or float32 [G, N, K] (unit stride along K, any row and matrix stride), packed uint8 output."""
-    what = "chord_mxfp4_quantize"
     shape, strides = src.shape, src.stride()
     if len(shape) != 3 or (strides[2] != 1 and shape[2] > 1) or not src.is_cuda:
-        _refuse(what, "src", src, "3-dimensional with unit stride along K in device memory")
-    _check(load().chord_mxfp4_quantize(src.data_ptr(), _dtype(src, what), strides[1], strides[0], *shape,
-                                       _blob(what, "packed", packed), packed.nbytes, _s(stream)), what)
+        _refuse("chord_mxfp4_quantize", "src", src, "3-dimensional with unit stride along K in device memory")
+    if not (packed.is_contiguous() and packed.is_cuda):
+        _refuse_blob("chord_mxfp4_quantize", packed=packed)
+    st = (_lib or load()).chord_mxfp4_quantize(src.data_ptr(), _dtype(src, "chord_mxfp4_quantize"), strides[1], strides[0],
+                                               *shape, packed.data_ptr(), packed.nbytes, _s(stream))
+    if st:
+        raise ChordError(st, "chord_mxfp4_quantize")
 
 
 def chord_mxfp4_quantize_rows(A, a_row_divisor: int, sorted_ids, num_tokens_padded, block_m: int, num_pairs: int,
@@ -417,20 +422,29 @@ def chord_mxfp4_quantize_rows(A, a_row_divisor: int, sorted_ids, num_tokens_padd
     shape, strides = A.shape, A.stride()
     if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1) or not A.is_cuda:
         _refuse(what, "A", A, "2-dimensional with unit stride along K in device memory")
-    _check(load().chord_mxfp4_quantize_rows(A.data_ptr(), _dtype(A, what), shape[0], strides[0], a_row_divisor, shape[1],
-                                            _ints(what, "sorted_ids", sorted_ids, 0),
-                                            _ints(what, "num_tokens_padded", num_tokens_padded), sorted_ids.numel(),
-                                            block_m, num_pairs, _blob(what, "packed", packed), packed.nbytes, _s(stream)),
-           what)
+    if not (packed.is_contiguous() and packed.is_cuda):
+        _refuse_blob(what, packed=packed)
+    code = _dtype(A, what)
+    st = (_lib or load()).chord_mxfp4_quantize_rows(
+        A.data_ptr(), code, shape[0], strides[0], a_row_divisor, shape[1], _ints(what, "sorted_ids", sorted_ids, 0),
+        _ints(what, "num_tokens_padded", num_tokens_padded), sorted_ids.numel(), block_m, num_pairs, packed.data_ptr(),
+        packed.nbytes, _s(stream))
+    if st:
+        raise ChordError(st, what)
 
 
 def chord_mxfp4_dequantize(packed, out, stream=None):
     """out bf16 or float32 [G, N, K] dense: the values of the packed matrix."""
-    what = "chord_mxfp4_dequantize"
     G, N, K = out.shape
-    code, op = _dtype(out, what), _dense(what, "out", out, None, G, N, K)
-    _check(load().chord_mxfp4_dequantize(_blob(what, "packed", packed), packed.nbytes, G, N, K, op, code, _s(stream)),
-           what)
+    code = _dtype(out, "chord_mxfp4_dequantize")
+    if not (out.is_contiguous() and out.is_cuda):
+        _refuse("chord_mxfp4_dequantize", "out", out, f"dense {(G, N, K)} in device memory")
+    if not (packed.is_contiguous() and packed.is_cuda):
+        _refuse_blob("chord_mxfp4_dequantize", packed=packed)
+    st = (_lib or load()).chord_mxfp4_dequantize(packed.data_ptr(), packed.nbytes, G, N, K, out.data_ptr(), code,
+                                                 _s(stream))
+    if st:
+        raise ChordError(st, "chord_mxfp4_dequantize")
 
 
 def chord_mxfp4_select_block_m(T: int, topk: int, E_local: int, E_global: int) -> int:
@@ -442,20 +456,26 @@ def chord_mxfp4_moe_gemm(Aq, packed, E: int, N: int, K: int, sorted_ids, expert_
     """C bf16 or float32 [num_pairs, N] dense (its dtype selects the output type)."""
     what = "chord_mxfp4_moe_gemm"
     code, cp = _dtype(C, what), _dense(what, "C", C, None, num_pairs, N)
+    if not (Aq.is_contiguous() and Aq.is_cuda and packed.is_contiguous() and packed.is_cuda):
+        _refuse_blob(what, Aq=Aq, packed=packed)
     capacity = sorted_ids.numel()
-    _check(load().chord_mxfp4_moe_gemm(_blob(what, "Aq", Aq), Aq.nbytes, _blob(what, "packed", packed), packed.nbytes,
-                                       E, N, K, _ints(what, "sorted_ids", sorted_ids, 0),
-                                       _ints(what, "expert_ids", expert_ids, capacity // block_m if block_m > 0 else 0),
-                                       _ints(what, "num_tokens_padded", num_tokens_padded), capacity, block_m, num_pairs,
-                                       cp, code, _o(opts), _s(stream)), what)
+    st = (_lib or load()).chord_mxfp4_moe_gemm(
+        Aq.data_ptr(), Aq.nbytes, packed.data_ptr(), packed.nbytes, E, N, K, _ints(what, "sorted_ids", sorted_ids, 0),
+        _ints(what, "expert_ids", expert_ids, capacity // block_m if block_m > 0 else 0),
+        _ints(what, "num_tokens_padded", num_tokens_padded), capacity, block_m, num_pairs, cp, code, _o(opts), _s(stream))
+    if st:
+        raise ChordError(st, what)
 
 
 def chord_mxfp4_gemm(Aq, M: int, packed, N: int, K: int, C, opts=None, stream=None):
     """C bf16 or float32 [M, N] dense (its dtype selects the output type)."""
-    what = "chord_mxfp4_gemm"
-    code, cp = _dtype(C, what), _dense(what, "C", C, None, M, N)
-    _check(load().chord_mxfp4_gemm(_blob(what, "Aq", Aq), Aq.nbytes, M, _blob(what, "packed", packed), packed.nbytes,
-                                   N, K, cp, code, _o(opts), _s(stream)), what)
+    code, cp = _dtype(C, "chord_mxfp4_gemm"), _dense("chord_mxfp4_gemm", "C", C, None, M, N)
+    if not (Aq.is_contiguous() and Aq.is_cuda and packed.is_contiguous() and packed.is_cuda):
+        _refuse_blob("chord_mxfp4_gemm", Aq=Aq, packed=packed)
+    st = (_lib or load()).chord_mxfp4_gemm(Aq.data_ptr(), Aq.nbytes, M, packed.data_ptr(), packed.nbytes, N, K, cp, code,
+                                           None if opts is None else _o(opts), _s(stream))
+    if st:
+        raise ChordError(st, "chord_mxfp4_gemm")
 
 
 def chord_moe_few_workspace_bytes(T: int, topk: int, E: int, H: int, I: int) -> int:
@@ -469,13 +489,16 @@ def chord_moe_layer_few(x, topk_ids, topk_w, E: int, I: int, packed_w13, packed_
     types = _dtypes or _types()
     T, H = x.shape
     topk = topk_ids.shape[1]
-    _check(load().chord_moe_layer_few(_dense(what, "x", x, types["bf16"], T, H),
-                                      _dense(what, "topk_ids", topk_ids, types["int32"], T, topk),
-                                      _dense(what, "topk_w", topk_w, types["f32"], T, topk), T, topk, E, H, I, weights,
-                                      _blob(what, "packed_w13", packed_w13), packed_w13.nbytes,
-                                      _blob(what, "packed_w2", packed_w2), packed_w2.nbytes,
-                                      _blob(what, "workspace", workspace), workspace.nbytes,
-                                      _dense(what, "out", out, types["bf16"], T, H), _o(opts), _s(stream)), what)
+    if not (packed_w13.is_contiguous() and packed_w13.is_cuda and packed_w2.is_contiguous() and packed_w2.is_cuda
+            and workspace.is_contiguous() and workspace.is_cuda):
+        _refuse_blob(what, packed_w13=packed_w13, packed_w2=packed_w2, workspace=workspace)
+    st = (_lib or load()).chord_moe_layer_few(
+        _dense(what, "x", x, types["bf16"], T, H), _dense(what, "topk_ids", topk_ids, types["int32"], T, topk),
+        _dense(what, "topk_w", topk_w, types["f32"], T, topk), T, topk, E, H, I, weights, packed_w13.data_ptr(),
+        packed_w13.nbytes, packed_w2.data_ptr(), packed_w2.nbytes, workspace.data_ptr(), workspace.nbytes,
+        _dense(what, "out", out, types["bf16"], T, H), None if opts is None else _o(opts), _s(stream))
+    if st:
+        raise ChordError(st, what)
 
 
 def chord_selftest_wait_timeout(stream=None):

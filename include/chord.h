@@ -67,6 +67,7 @@ typedef enum chord_status {
 #define CHORD_DEV_TIMEOUT 4      /* a pipeline wait exceeded its bound */
 #define CHORD_DEV_BAD_CODE 5     /* pack: a code above 15 */
 #define CHORD_DEV_BAD_PADDED 6   /* num_tokens_padded above capacity or not a multiple of block_m */
+#define CHORD_DEV_BAD_ADAPTER 7  /* adapter_ids entry outside [-1, adapters) */
 
 /* GEMM kernel family, picked from rows per expert (the article's two
  * regimes, section "Indexed kernels"): both take the block's tokens as the
@@ -624,6 +625,99 @@ chord_status chord_moe_layer_few(const void *x, const int32_t *topk_ids, const f
                                  size_t w13_bytes, const void *packed_w2, size_t w2_bytes,
                                  void *workspace, size_t workspace_bytes, void *out,
                                  const chord_opts *opts, void *stream);
+
+/* ------------------------------------------------------------------ router */
+
+/* Three bf16 numbers that add up to each of the n FP32 numbers of W: parts is bf16
+ * [3, n], eight significant bits each, cut off towards zero (exact for magnitudes
+ * from 2^-110; an infinity or NaN is in the first part alone).  For a router kept in
+ * FP32, split once at load time. */
+chord_status chord_router_split_weights(const float *W, int64_t n, void *parts, void *stream);
+
+/* Router logits:
+ *   logits[t, e] = sum_k x[t, k] * W[e, k],   FP32 sums, FP32 [T, E] dense
+ *   x      device bf16 [T, H], x_stride elements between rows (a multiple of 8)
+ *   W      device bf16 [parts, E, H] dense: parts = 1 for a bf16 router, 3 for the
+ *          parts of an FP32 one (chord_router_split_weights), whose sum is the weight
+ * E <= 1024, H % 8 == 0.  Products are exact; the result does not depend on timing. */
+chord_status chord_router_logits(const void *x, int64_t x_stride, int T, const void *W, int parts, int E, int H,
+                                 float *logits, const chord_opts *opts, void *stream);
+
+typedef enum chord_score {
+    CHORD_SCORE_SOFTMAX = 0,   /* over all experts of the token */
+    CHORD_SCORE_SIGMOID = 1    /* of each expert by itself */
+} chord_score;
+
+/* How chord_moe_route chooses. */
+typedef struct chord_route {
+    int32_t score;         /* chord_score */
+    int32_t groups;        /* 1: every expert may be chosen; otherwise the E experts are that many
+                              equal groups of consecutive experts (at most 32) */
+    int32_t topk_groups;   /* groups that a token may choose from, 1..groups */
+    int32_t group_best;    /* a group's value: its best expert's (1), or the sum of its two best (2) */
+    int32_t renormalize;   /* nonzero: the weights of a token's chosen experts sum to 1 before scale */
+    float scale;           /* factor of every weight */
+    int32_t first;         /* experts [first, first + E_local) live on this GPU ... */
+    int32_t E_local;       /* ... and are ids 0 .. E_local - 1; the others become -1 */
+} chord_route;
+
+/* The choice of experts, in the form that chord_moe_align and the layer calls take:
+ *   logits   device [T, E], CHORD_DTYPE_BF16 or CHORD_DTYPE_F32, row_stride elements apart
+ *   bias     device float [E] or NULL, added to the scores for the choice only
+ *   topk_ids device int32 [T, topk], local id or -1;  topk_w device float [T, topk]
+ * With s = score(logits), the value of an expert is s + bias (without a bias its logit,
+ * which orders the experts as s does); groups take part by their value, the topk
+ * experts with the largest values in the chosen groups are the result, largest
+ * first.  Values are compared as binary64 has them, whatever the precision the kernel begins
+ * with; of equal ones the lower index is first, among groups too.  The weight is
+ * s (not the value), for renormalize divided by the sum of the chosen s (a quotient of
+ * exponentials: it stays defined where every chosen s is below the smallest FP32 number),
+ * times scale, also for an expert on another GPU.
+ * An expert is not available to a token when its logit is -inf or NaN, or its bias is: it
+ * is never chosen (the softmax leaves out -inf and NaN logits; +inf counts as the
+ * largest FP32 number).  A group without an available expert is never chosen; the
+ * value of a group with one is that one's.  Slots that no expert is left for get id -1 and weight 0.
+ * E <= 1024, topk <= 32, topk <= topk_groups * E / groups. */
+chord_status chord_moe_route(const void *logits, int logits_dtype, int64_t row_stride, int T, int E,
+                             const float *bias, int topk, const chord_route *how, int32_t *topk_ids,
+                             float *topk_w, void *stream);
+
+/* ---------------------------------------------------------------- adapters */
+
+/* Scratch bytes of chord_adapter_add; 0 on bad arguments. */
+size_t chord_adapter_workspace_bytes(int64_t T, int topk, int adapters, int E, int rank, int parts);
+
+/* Low-rank adapters of many requests beside a projection that they share (the frozen
+ * 4-bit weights' product in base):
+ *   y[p, n] = base[p, n] + scale[a] * sum_j B[a, e, n, j] * v[p, part(n) * rank + j]
+ *   v[p, i] = sum_k A[a, e, i, k] * x[p / a_row_divisor, k]
+ * for every pair p = t * topk + k of the T * topk, with a = adapter_ids[t] and e =
+ * topk_ids[p] (topk_ids NULL: E = 1, one projection for all; e = 0).  FP32 sums, v kept in
+ * FP32, the result rounded once to y's type.
+ *   x            device bf16 [x_rows, K], x_stride elements apart; a_row_divisor as in
+ *                chord_w4a16_moe_gemm (topk for gate_up, 1 for down)
+ *   adapter_ids  device int32 [T], -1: the token has no adapter, its rows of y are base's;
+ *                an id outside [-1, adapters) is taken for -1 and sets CHORD_DEV_BAD_ADAPTER
+ *   topk_ids     device int32 [T, topk]; a pair outside [0, E) is on another GPU: its row
+ *                of y is not written
+ *   A            device bf16 [adapters, E, parts * rank, K] dense
+ *   B            device bf16 [adapters, E, N, rank] dense.  parts > 1: the N columns are that
+ *                many equal ranges with their own A (gate_up: gate columns, up columns), x read once
+ *   scale        device float [adapters], NULL: 1
+ *   base, y      device [T * topk, N], bf16 or FP32 (y_dtype) both, base_stride and y_stride
+ *                elements apart; base == y (and equal strides) adds in place, otherwise they
+ *                must not overlap
+ *   workspace    >= chord_adapter_workspace_bytes(...), 16-byte aligned; calls that overlap on the
+ *                GPU need one each
+ * rank % 8 == 0 and at most 128 (a smaller rank is padded with zeros), parts <= 4, K % 8 == 0,
+ * N % (8 * parts) == 0, rows 16-byte aligned, adapters * E <= 65536.  A B that is an infinity may
+ * give NaN where the exact sum is infinite. */
+chord_status chord_adapter_add(const void *x, int64_t x_rows, int64_t x_stride, int a_row_divisor,
+                               const int32_t *adapter_ids, const int32_t *topk_ids, int T, int topk,
+                               int adapters, int E, const void *A, const void *B, const float *scale, int rank,
+                               int parts, int N, int K, const void *base, int64_t base_stride, void *y,
+                               int64_t y_stride, int y_dtype, void *workspace, size_t workspace_bytes,
+                               const chord_opts *opts, void *stream);
 
 /* ------------------------------------------------------------------ errors */
 

@@ -26,6 +26,8 @@ __all__ = [
     "chord_grouped_masked_workspace_bytes", "chord_grouped_masked_gemm",
     "chord_mxfp4_bytes", "chord_mxfp4_rows_bytes", "chord_mxfp4_quantize", "chord_mxfp4_quantize_rows",
     "chord_mxfp4_dequantize", "chord_mxfp4_select_block_m", "chord_mxfp4_moe_gemm", "chord_mxfp4_gemm",
+    "chord_router_split_weights", "chord_router_logits", "chord_moe_route", "ChordRoute", "SCORE_SOFTMAX", "SCORE_SIGMOID",
+    "chord_adapter_workspace_bytes", "chord_adapter_add",
     "chord_moe_few_workspace_bytes", "chord_moe_layer_few", "WEIGHTS_INT4", "WEIGHTS_MXFP4", "FEW_MAX_TOKENS",
     "KERNEL_AUTO", "KERNEL_TCGEN05", "KERNEL_WARP_MMA", "LAYOUT_WARP_MMA", "LAYOUT_TCGEN05",
     "DTYPE_BF16", "DTYPE_F32",
@@ -38,6 +40,7 @@ DTYPE_BF16, DTYPE_F32 = 0, 1
 LAYOUT_MXFP4 = 4
 WEIGHTS_INT4, WEIGHTS_MXFP4 = 0, 1
 FEW_MAX_TOKENS = 32
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 STATUS = {0: "CHORD_OK", 1: "CHORD_ERR_INVALID_ARG", 2: "CHORD_ERR_UNSUPPORTED", 3: "CHORD_ERR_LAYOUT_MISMATCH",
           4: "CHORD_ERR_BUFFER_TOO_SMALL", 5: "CHORD_ERR_CUDA", 6: "CHORD_ERR_DEVICE_VALIDATION",
           7: "CHORD_ERR_TIMEOUT"}
@@ -53,6 +56,12 @@ class ChordOpts(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("validate", ctypes.c_int32), ("split_k", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("epilogue", ctypes.c_int32), ("mixed", ctypes.c_int32),
                 ("fuse_combine", ctypes.c_int32), ("tc_pairs", ctypes.c_int32)]
+
+
+class ChordRoute(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("first", ctypes.c_int32), ("E_local", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -108,6 +117,12 @@ _SIGS = {
     "chord_moe_few_workspace_bytes": (_sz, [_int, _int, _int, _int, _int]),
     "chord_moe_layer_few": (_int, [_vp, _vp, _vp, _int, _int, _int, _int, _int, _int, _vp, _sz, _vp, _sz, _vp, _sz,
                                    _vp, _OPTS, _vp]),
+    "chord_router_split_weights": (_int, [_vp, _i64, _vp, _vp]),
+    "chord_router_logits": (_int, [_vp, _i64, _int, _vp, _int, _int, _int, _vp, _OPTS, _vp]),
+    "chord_moe_route": (_int, [_vp, _int, _i64, _int, _int, _vp, _int, ctypes.POINTER(ChordRoute), _vp, _vp, _vp]),
+    "chord_adapter_workspace_bytes": (_sz, [_i64, _int, _int, _int, _int, _int]),
+    "chord_adapter_add": (_int, [_vp, _i64, _i64, _int, _vp, _vp, _int, _int, _int, _int, _vp, _vp, _vp, _int, _int,
+                                 _int, _int, _vp, _i64, _vp, _i64, _int, _vp, _sz, _OPTS, _vp]),
 }
 
 
@@ -497,6 +512,107 @@ def chord_moe_layer_few(x, topk_ids, topk_w, E: int, I: int, packed_w13, packed_
         _dense(what, "topk_w", topk_w, types["f32"], T, topk), T, topk, E, H, I, weights, packed_w13.data_ptr(),
         packed_w13.nbytes, packed_w2.data_ptr(), packed_w2.nbytes, workspace.data_ptr(), workspace.nbytes,
         _dense(what, "out", out, types["bf16"], T, H), None if opts is None else _o(opts), _s(stream))
+    if st:
+        raise ChordError(st, what)
+
+
+def _rows(what, name, t, dtypes):
+    """A matrix with unit stride along its rows, of one of these types, in device memory."""
+    strides = t.stride()
+    if t.dtype not in dtypes or len(strides) != 2 or (strides[1] != 1 and t.shape[1] > 1) or not t.is_cuda:
+        _refuse(what, name, t, f"{' or '.join(map(str, dtypes))}, 2-dimensional with unit stride along its rows in device memory")
+    return t.data_ptr()
+
+
+def _same_device(what, first, *others):
+    """Every tensor is where the first one is, and that is the current device (the stream's)."""
+    import torch
+    dev = first.get_device()
+    if any(t is not None and t.get_device() != dev for t in others) or (dev >= 0 and dev != torch.cuda.current_device()):
+        raise ChordError(1, f"{what}: the tensors must be on the current device")
+
+
+def chord_router_split_weights(W, parts, stream=None):
+    """W float32 of any shape, parts bf16 [3, *W.shape] whose sum is W; both dense."""
+    what = "chord_router_split_weights"
+    types = _dtypes or _types()
+    if parts.shape != (3, *W.shape):
+        _refuse(what, "parts", parts, f"bf16 {(3, *W.shape)}")
+    wp, pp = _dense(what, "W", W, types["f32"], *W.shape), _dense(what, "parts", parts, types["bf16"], *parts.shape)
+    _same_device(what, W, parts)
+    _check(load().chord_router_split_weights(wp, W.numel(), pp, _s(stream)), what)
+
+
+def chord_router_logits(x, W, logits, opts=None, stream=None):
+    """x bf16 [T, H] (any row stride), W bf16 [E, H] or the parts [3, E, H] of an fp32 one, logits float32 [T, E]."""
+    what = "chord_router_logits"
+    types = _dtypes or _types()
+    bf16, shape = types["bf16"], W.shape
+    xp = _rows(what, "x", x, (bf16,))
+    T, H = x.shape
+    if len(shape) not in (2, 3) or shape[-1] != H:
+        _refuse(what, "W", W, f"bf16 [E, {H}] or [3, E, {H}]")
+    E, wp = shape[-2], _dense(what, "W", W, bf16, *shape)
+    out = _dense(what, "logits", logits, types["f32"], T, E)
+    _same_device(what, x, W, logits)
+    st = (_lib or load()).chord_router_logits(xp, x.stride(0), T, wp, shape[0] if len(shape) == 3 else 1, E, H, out,
+                                              None if opts is None else _o(opts), _s(stream))
+    if st:
+        raise ChordError(st, what)
+
+
+def chord_moe_route(logits, topk_ids, topk_w, score: int = SCORE_SOFTMAX, bias=None, groups: int = 1, topk_groups: int = 1,
+                    group_best: int = 1, renormalize: bool = True, scale: float = 1.0, first: int = 0, E_local=None,
+                    stream=None):
+    """logits bf16 or float32 [T, E] (any row stride), topk_ids int32 and topk_w float32 [T, topk] outputs, bias float32 [E]."""
+    what = "chord_moe_route"
+    types = _dtypes or _types()
+    f32, bf16 = types["f32"], types["bf16"]
+    lp = _rows(what, "logits", logits, (bf16, f32))
+    (T, E), topk = logits.shape, topk_ids.shape[-1]
+    ip, wp = _dense(what, "topk_ids", topk_ids, types["int32"], T, topk), _dense(what, "topk_w", topk_w, f32, T, topk)
+    bp = None if bias is None else _dense(what, "bias", bias, f32, E)
+    _same_device(what, logits, topk_ids, topk_w, bias)
+    how = ChordRoute(score, groups, topk_groups, group_best, renormalize, scale, first, E - first if E_local is None else E_local)
+    st = (_lib or load()).chord_moe_route(lp, types[logits.dtype], logits.stride(0), T, E, bp, topk, ctypes.byref(how), ip, wp,
+                                          _s(stream))
+    if st:
+        raise ChordError(st, what)
+
+
+def chord_adapter_workspace_bytes(T: int, topk: int, adapters: int, E: int, rank: int, parts: int = 1) -> int:
+    return load().chord_adapter_workspace_bytes(T, topk, adapters, E, rank, parts)
+
+
+def chord_adapter_add(x, a_row_divisor: int, adapter_ids, topk_ids, A, B, scale, base, y, workspace, opts=None, stream=None):
+    """x bf16 [x_rows, K]; adapter_ids int32 [T]; topk_ids int32 [T, topk], or None for one projection; A bf16 [adapters,
+    (E,) parts * rank, K]; B bf16 [adapters, (E,) N, rank]; scale float32 [adapters] or None; base and y [T * topk, N],
+    both bf16 or both float32 (base may be y).  Rows of x, base and y may be any (aligned) stride apart."""
+    what = "chord_adapter_add"
+    types = _dtypes or _types()
+    bf16, f32, i32 = types["bf16"], types["f32"], types["int32"]
+    xp, bp, yp = _rows(what, "x", x, (bf16,)), _rows(what, "base", base, (bf16, f32)), _rows(what, "y", y, (base.dtype,))
+    (x_rows, K), (P, N) = x.shape, y.shape
+    T = adapter_ids.numel()
+    topk = 1 if topk_ids is None else topk_ids.shape[-1]
+    if B.dim() != (3 if topk_ids is None else 4) or B.shape[-2] != N:
+        _refuse(what, "B", B, f"bf16 [adapters, {'' if topk_ids is None else 'E, '}{N}, rank]")
+    S, E, rank = B.shape[0], 1 if topk_ids is None else B.shape[1], B.shape[-1]
+    if A.dim() != B.dim() or A.shape[:-2] != B.shape[:-2] or A.shape[-1] != K or rank == 0 or A.shape[-2] % rank:
+        _refuse(what, "A", A, f"bf16 {(*B.shape[:-2], 'parts * rank', K)}")
+    if P != T * topk or base.shape != y.shape:
+        _refuse(what, "base" if P == T * topk else "y", base if P == T * topk else y, f"[{T * topk}, {N}]")
+    ip = None if topk_ids is None else _dense(what, "topk_ids", topk_ids, i32, T, topk)
+    ap = _dense(what, "adapter_ids", adapter_ids, i32, T)
+    Ap, Bp = _dense(what, "A", A, bf16, *A.shape), _dense(what, "B", B, bf16, *B.shape)
+    sp = None if scale is None else _dense(what, "scale", scale, f32, S)
+    if not (workspace.is_contiguous() and workspace.is_cuda):
+        _refuse_blob(what, workspace=workspace)
+    _same_device(what, x, adapter_ids, topk_ids, A, B, scale, base, y, workspace)
+    st = (_lib or load()).chord_adapter_add(
+        xp, x_rows, x.stride(0), a_row_divisor, ap, ip, T, topk, S, E, Ap, Bp, sp, rank, A.shape[-2] // rank, N, K, bp,
+        base.stride(0), yp, y.stride(0), types[y.dtype], workspace.data_ptr(), workspace.nbytes, None if opts is None else _o(opts),
+        _s(stream))
     if st:
         raise ChordError(st, what)
 

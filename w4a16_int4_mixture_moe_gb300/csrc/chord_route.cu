@@ -5,6 +5,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "chord_common.cuh"
 #include "chord_internal.h"
 
@@ -47,45 +49,36 @@ __device__ __forceinline__ V warp_sum(V v) {
 
 // The weights of one token's choice: lane k < topk holds choice k (expert e, its logit l; e < 0: none).
 //   softmax: exp(l - m) / sum over all, renormalised exp(l - c) / sum over the chosen
-//   sigmoid: 1 / (1 + exp(-l))
-// Renormalised, both numerators are scaled by exp(-c) with c the largest chosen logit (sigmoid: at
-// most 0), which the quotient does not change and which keeps far negative logits from all
-// becoming 0.
+//   sigmoid: 1 / (1 + exp(-l)), in terms of q = exp(-|l|): 1 / (1 + q) or q / (1 + q)
+// Renormalised, the numerators are scaled by exp(-c) with c the largest chosen logit (sigmoid: only
+// if that is negative), which the quotient does not change and which keeps far negative logits
+// from all becoming 0.
 __device__ __forceinline__ void write_choice(const RouteArgs& a, int64_t t, int lane, int e, float l, float m, float total) {
-    const bool have = lane < a.topk && e >= 0;
-    float s = 0.0f;
-    if (a.renorm) {
-        float c = warp_max(have ? l : -FLT_MAX);
-        if (a.score == CHORD_SCORE_SIGMOID) {
-            c = fminf(c, 0.0f);
-            s = l > 0.0f ? 1.0f / (1.0f + expf(-l)) : expf(l - c) / (1.0f + expf(l));
-        } else {
-            s = expf(l - c);
-        }
-        if (!have) s = 0.0f;
-        const float sum = warp_sum(s);
-        s = have ? s / sum : 0.0f;
-    } else if (have) {
-        s = a.score == CHORD_SCORE_SIGMOID ? 1.0f / (1.0f + expf(-l)) : expf(l - m) / total;
+    const bool have = e >= 0;   // no lane from topk on has one
+    const bool sigmoid = a.score == CHORD_SCORE_SIGMOID;
+    const bool far = a.renorm && !__any_sync(kAll, have && sigmoid && l >= 0.0f);   // warp-uniform
+    float c = sigmoid ? 0.0f : m;
+    if (far) c = warp_max(have ? l : -FLT_MAX);
+    const float q = expf(sigmoid ? -fabsf(l) : l - c);
+    float s = q;
+    if (sigmoid) {
+        if (far) s = expf(l - c);
+        s = (l > 0.0f ? 1.0f : s) / (1.0f + q);
     }
+    if (!have) s = 0.0f;
+    const float sum = a.renorm ? warp_sum(s) : sigmoid ? 1.0f : total;
     if (lane < a.topk) {
         const int id = have && e >= a.first && e - a.first < a.local ? e - a.first : -1;
         a.ids[t * a.topk + lane] = id;
-        a.w[t * a.topk + lane] = s * a.scale;
+        a.w[t * a.topk + lane] = (have ? s / sum : 0.0f) * a.scale;
     }
 }
 
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
-    extern __shared__ double route_smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
-    if (t >= a.T) return;
-    double* z = route_smem + (size_t)warp * (a.E + 32);
+// The choice by the definition, every value in binary64, one expert after the other: lane k gets
+// the k-th (-1: none).  z: E + 32 doubles of the warp's own.
+__device__ __noinline__ int choose_in_64_bits(const RouteArgs& a, int64_t t, int lane, float mx, double* z) {
     double* gz = z + a.E;
     const double ninf = -INFINITY;
-    float mx = -INFINITY;
-    for (int e = lane; e < a.E; e += 32) mx = fmaxf(mx, logit_at(a, t, e));
-    mx = warp_max(mx);
     double total = 0;
     if (a.score == CHORD_SCORE_SOFTMAX) {
         for (int e = lane; e < a.E; e += 32) {
@@ -161,7 +154,256 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
         if (lane == k) mine = at;
         __syncwarp();
     }
-    write_choice(a, t, lane, mine, mine >= 0 ? logit_at(a, t, mine) : 0.0f, mx, (float)total);
+    return mine;
+}
+
+
+// A number's place among unsigned integers, in the order of the numbers (-inf is not 0: 0 is below all).
+__device__ __forceinline__ uint32_t key_of(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);   // -0 and +0 are the same number
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+// e^x and 1 / x in one approximate instruction each (relative error below 2^-22 and 2^-23; e^x next to
+// that |x| 2^-24 from its argument).
+__device__ __forceinline__ float fast_exp(float x) {
+    float r;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm volatile("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// One token per warp; lane l holds experts l, l + 32, ...
+//   1. Values in FP32, each off by at most slack * (1 + |value|).
+//   2. The topk-th largest of the 32 lanes' largest values bounds the topk-th largest value from
+//      below: what is not below it (by twice the slack) are the candidates, about ten for a
+//      top-8 of 384.  One per lane, each counts those before it.
+//   3. Where two candidates' values are too close for FP32 to tell (some of a thousand tokens of a
+//      sigmoid router of 384 experts), the candidates' are computed in binary64; where two groups' are, or
+//      the softmax's sum is needed for that, or more than 32 candidates are left, the whole
+//      token is done by choose_in_64_bits.
+// Slack: a sigmoid of the fast functions is off by s (1 - s) (2^-22 + |l| 2^-24) + 2^-23, below 3e-7, of the
+// accurate ones by three half ulps; a softmax by its sum's E / 32 + 5 half ulps and those of the exponents, below 4e-6.
+constexpr float kSlackFast = 1e-6f, kSlackAccurate = 5e-7f, kSlackSoftmax = 4e-6f;
+
+// Shared memory of a warp, in doubles: the list (16), its candidates (64) and their values in
+// binary64 (32); or the groups' rows; or all values in binary64 and the groups' (E + 32).
+__host__ __device__ inline int own_doubles(int E) { return (E > 80 ? E + 33 : 113) & ~1; }
+
+template <int VPL, bool F32>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
+    using In = typename std::conditional<F32, float, __nv_bfloat16>::type;
+    extern __shared__ double route_smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    if (t >= a.T) return;
+    double* own = route_smem + (size_t)warp * own_doubles(a.E);
+    const bool by_logit = !a.bias && (a.groups == 1 || a.best == 1);
+    const bool softmax = a.score == CHORD_SCORE_SOFTMAX;
+    const In* row = static_cast<const In*>(a.logits) + t * a.stride + lane;
+    // a logit as the scores use it: +inf counts as the largest number
+    auto logit = [&](int i) { return fminf((float)row[32 * i], FLT_MAX); };
+    float z[VPL], bias[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const bool in = lane + 32 * i < a.E;
+        z[i] = in ? (float)row[32 * i] : -INFINITY;
+        bias[i] = in && a.bias ? a.bias[lane + 32 * i] : 0.0f;
+    }
+    float mx = 0.0f, total = 1.0f;
+    if (softmax) {
+        mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) mx = fmaxf(mx, z[i]);   // leaves out NaN
+        mx = fminf(warp_max(mx), FLT_MAX);
+        if (!(by_logit && a.renorm)) {
+            total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) total += z[i] > -INFINITY ? expf(fminf(z[i], FLT_MAX) - mx) : 0.0f;
+            total = warp_sum(total);
+        }
+    }
+    const float slack = softmax ? kSlackSoftmax : a.groups > 1 ? kSlackAccurate : kSlackFast;
+    if (by_logit) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) z[i] = z[i] > -INFINITY ? fminf(z[i], FLT_MAX) : -INFINITY;
+    } else if (softmax) {
+        const float inv = 1.0f / total;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const bool open = z[i] > -INFINITY && bias[i] > -INFINITY;
+            z[i] = open ? expf(fminf(z[i], FLT_MAX) - mx) * inv + bias[i] : -INFINITY;
+        }
+    } else if (a.groups > 1) {
+        // accurate here already: few pairs of groups are then too close
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const bool open = z[i] > -INFINITY && bias[i] > -INFINITY;
+            z[i] = open ? 1.0f / (1.0f + expf(-z[i])) + bias[i] : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const bool open = z[i] > -INFINITY && bias[i] > -INFINITY;
+            z[i] = open ? fast_rcp(1.0f + fast_exp(-z[i])) + bias[i] : -INFINITY;
+        }
+    }
+    bool fine = true;
+    if (a.groups > 1) {
+        float* rows = reinterpret_cast<float*>(own);
+        const int size = a.E / a.groups;
+        const uint32_t inv = (1u << 20) / (uint32_t)size + 1u;   // e * inv >> 20 = e / size for e < 1024
+        int lpg = 32;                                            // lanes that share a group
+        while (lpg * a.groups > 32) lpg >>= 1;
+        // groups lie lpg words further apart, so that lanes read different banks
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int e = lane + 32 * i;
+            if (e < a.E) rows[e + lpg * (int)((uint32_t)e * inv >> 20)] = z[i];
+        }
+        __syncwarp();
+        const int g = lane / lpg;
+        float b1 = -INFINITY, b2 = -INFINITY;
+        if (g < a.groups) {
+            const float* mine = rows + g * (size + lpg);
+#pragma unroll 4
+            for (int i = lane % lpg; i < size; i += lpg) {
+                const float v = mine[i];
+                b2 = fmaxf(b2, fminf(b1, v));
+                b1 = fmaxf(b1, v);
+            }
+        }
+        for (int o = 1; o < lpg; o <<= 1) {
+            const float o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+            b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
+            b1 = fmaxf(b1, o1);
+        }
+        float gv = __shfl_sync(kAll, a.best == 2 && b2 > -INFINITY ? b1 + b2 : b1, (lane * lpg) & 31);
+        if (lane >= a.groups) gv = -INFINITY;
+        int rank = 0;
+        for (int k = 0; k < a.groups; ++k) {
+            const float v = __shfl_sync(kAll, gv, k);
+            rank += v > gv || (v == gv && k < lane);
+        }
+        if (lane >= a.groups) rank = 32;
+        const unsigned kept = __ballot_sync(kAll, rank < a.topk_groups);
+        if (!by_logit && a.topk_groups < a.groups) {
+            // the last group that is kept and the first that is not: two values each, each off by the slack
+            const unsigned last = __ballot_sync(kAll, rank == a.topk_groups - 1), next = __ballot_sync(kAll, rank == a.topk_groups);
+            const float v = __shfl_sync(kAll, gv, __ffs(last) - 1), w = __shfl_sync(kAll, gv, __ffs(next) - 1);
+            fine = !(w > -INFINITY) || (v < INFINITY && v - w > slack * (4.0f + fabsf(v) + fabsf(w)));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const bool in = kept >> ((uint32_t)(lane + 32 * i) * inv >> 20 & 31u) & 1u;
+            z[i] = in ? z[i] : -INFINITY;
+            if (!a.bias && !by_logit && z[i] > -INFINITY) z[i] = logit(i);
+        }
+    }
+    // from here on the logit orders the experts wherever there is no bias
+    const bool exact_order = !a.bias;
+    float top = z[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) top = fmaxf(top, z[i]);
+    uint32_t key = key_of(top), bound = 0;
+    for (int k = 0; k < a.topk;) {
+        bound = __reduce_max_sync(kAll, key);
+        if (bound == 0) break;   // fewer than topk lanes
+        k += __popc(__ballot_sync(kAll, key == bound));
+        if (key == bound) key = 0;
+    }
+    // bound back to a number; 0: fewer than topk lanes hold anything
+    float least = bound == 0 ? -INFINITY : __uint_as_float(bound ^ ((bound & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+    if (!exact_order) {
+        if (!(least < INFINITY)) fine = false;   // biases of +inf: least becomes NaN, the list empty
+        least -= 2.0f * slack * (1.0f + fabsf(least));
+    }
+    least = fmaxf(least, -FLT_MAX);   // -inf is never chosen (the lowest number is)
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) mask |= z[i] >= least ? 1u << i : 0u;
+    const int n = (int)__reduce_add_sync(kAll, (unsigned)__popc(mask));
+    fine = fine && n <= 32;
+    int mine = -1;
+    if (fine) {
+        int* list = reinterpret_cast<int*>(own);
+        float2* cand = reinterpret_cast<float2*>(own + 16);
+        int at = 0;
+        for (unsigned left; (left = __ballot_sync(kAll, mask != 0)) != 0;) {
+            if (mask) {
+                list[at + __popc(left & ((1u << lane) - 1u))] = lane + 32 * (__ffs(mask) - 1);
+                mask &= mask - 1;
+            }
+            at += __popc(left);
+        }
+        __syncwarp();
+        int e = INT32_MAX;
+        float l = 0.0f, b = 0.0f, v = -INFINITY;
+        if (lane < n) {
+            e = list[lane];
+            l = fminf((float)row[e - lane], FLT_MAX);
+            v = l;
+            if (a.bias) {
+                b = a.bias[e];
+                v = (softmax ? expf(l - mx) / total : fast_rcp(1.0f + fast_exp(-l))) + b;
+            }
+            cand[lane] = make_float2(v, __int_as_float(e));
+        }
+        __syncwarp();
+        int rank = 0, close = -1;   // itself
+        const float tol = 2.0f * (softmax ? kSlackSoftmax : kSlackFast) * (1.0f + fabsf(v));
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float2 c = cand[k];
+            rank += c.x > v || (c.x == v && __float_as_int(c.y) < e);
+            close += !(fabsf(c.x - v) > tol);
+        }
+        if (!exact_order && __any_sync(kAll, lane < n && rank < a.topk && close > 0)) {
+            // Equal inputs are equal values in any precision, and in the right order already.
+            double* values = own + 16 + 64;
+            float2* inputs = reinterpret_cast<float2*>(values);
+            if (lane < n) inputs[lane] = make_float2(l, b);
+            __syncwarp();
+            for (int k = 0; k < n; ++k) {
+                const float2 c = inputs[k];
+                close -= k != lane && c.x == l && c.y == b;
+            }
+            __syncwarp();
+            if (!__any_sync(kAll, lane < n && rank < a.topk && close > 0)) {
+            } else if (softmax) {
+                fine = false;   // the sum over all experts is needed in binary64 too
+            } else {
+                // the candidates are certain, their order is not
+                const double d = 1.0 / (1.0 + exp(-(double)l)) + (double)b;
+                if (lane < n) values[lane] = d;
+                __syncwarp();
+                rank = 0;
+                for (int k = 0; k < n; ++k) rank += values[k] > d || (values[k] == d && list[k] < e);
+            }
+        }
+        __syncwarp();
+        if (lane < n && rank < a.topk) list[rank] = e;
+        __syncwarp();
+        mine = lane < min(n, a.topk) ? list[lane] : -1;
+    }
+    __syncwarp();
+    if (!fine) mine = choose_in_64_bits(a, t, lane, mx, own);
+    write_choice(a, t, lane, mine, mine >= 0 ? fminf((float)row[mine - lane], FLT_MAX) : 0.0f, mx, total);
+}
+
+template <bool F32>
+auto route_kernel_for(int E) {
+    return E <= 64    ? route_kernel<2, F32>
+           : E <= 128 ? route_kernel<4, F32>
+           : E <= 256 ? route_kernel<8, F32>
+           : E <= 384 ? route_kernel<12, F32>
+           : E <= 512 ? route_kernel<16, F32>
+                      : route_kernel<32, F32>;
 }
 
 }  // namespace
@@ -186,10 +428,9 @@ chord_status chord_moe_route(const void* logits, int logits_dtype, int64_t row_s
     if (T == 0) return CHORD_OK;
     RouteArgs a{logits, logits_dtype == CHORD_DTYPE_F32, row_stride, T, E, topk, bias, how->score, how->groups,
                 how->topk_groups, how->group_best, how->renormalize != 0, how->scale, how->first, how->E_local, topk_ids, topk_w};
-    const size_t smem = (size_t)kRouteWarps * (E + 32) * 8;
-    if (ensure_smem_limit(reinterpret_cast<const void*>(route_kernel), kRouteWarps * (1024 + 32) * 8) != cudaSuccess)
-        return CHORD_ERR_CUDA;
-    route_kernel<<<(unsigned)ceil_div64(T, kRouteWarps), kRouteWarps * 32, smem, static_cast<cudaStream_t>(stream)>>>(a);
+    const size_t smem = (size_t)kRouteWarps * own_doubles(E) * 8;   // at most 36 KB
+    void (*kern)(RouteArgs) = logits_dtype == CHORD_DTYPE_F32 ? route_kernel_for<true>(E) : route_kernel_for<false>(E);
+    kern<<<(unsigned)ceil_div64(T, kRouteWarps), kRouteWarps * 32, smem, static_cast<cudaStream_t>(stream)>>>(a);
     return cudaGetLastError() == cudaSuccess ? CHORD_OK : CHORD_ERR_CUDA;
 }
 

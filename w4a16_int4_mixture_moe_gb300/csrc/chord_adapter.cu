@@ -1,6 +1,21 @@
 // Low-rank adapters of many requests beside a projection that they share:
-//   y[p] = base[p] + scale[a] * B[a, e] (A[a, e] x[p / div])
-// in two steps, v = A x (FP32, in the workspace) and y = base + scale * B v.
+//   v[p] = A[a, e] x[p / div],   y[p] = base[p] + scale[a] * B[a, e] v[p]
+// A slot is an adapter of an expert, a * E + e; the pairs of one slot are taken together, in blocks of
+// up to 16 rows a matrix-instruction tile, so a slot's weights are read once a block.
+//   plan   (more than kFewPairs pairs) the blocks: a counting sort of the pairs by slot.  With few
+//          pairs every CTA of the two kernels finds the blocks itself, which costs less than a launch.
+//   down   v, a block's rows times the slot's A.  An item is (block, up to 64 rows of A, K slice); the eight
+//          warps of a CTA take every eighth 32 columns of the slice straight from global memory into the
+//          fragments of warp-level matrix instructions (the k order inside a step is whatever puts a
+//          lane's own 16 bytes into its slots, the same for both operands) and add their sums up
+//          through shared memory.  K slices are partial sums in the workspace, so that few blocks
+//          fill the GPU.
+//   up     y, an item is (block, columns).  The slices of v are added in order, scaled and split into three
+//          bf16 parts of eight bits each, so the tensor cores multiply all of an FP32 v.  The
+//          columns of a 32-column tile are dealt so that a lane ends with eight neighbouring ones:
+//          base and y move in 16-byte pieces.
+// Both are bound by bytes: x and A below, base and y (and B) above; tcgen05 would add nothing but the
+// staging in shared memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -11,81 +26,546 @@
 namespace chord {
 namespace {
 
+constexpr int kFewPairs = 256;
+constexpr int kFewRows = 16, kManyRows = 64;   // rows of a block
+constexpr int kThreads = 256, kWarps = 8;
+constexpr int kMaxSplit = 16;
+constexpr int kTargetCtas = 304;
+constexpr int kNone = -2;                      // slot of a pair that is not touched; -1: its row of y is base's
+
 struct AdapterArgs {
     const __nv_bfloat16* x;
     int64_t x_stride;
     int div;
     const int32_t* adapter_ids;   // [T]
     const int32_t* topk_ids;      // [T, topk], null: one projection
-    int64_t P;
-    int topk, S, E;
-    const __nv_bfloat16* A;       // [S, E, parts * rank, K]
+    int P, topk, S, E;
+    const __nv_bfloat16* A;       // [S, E, R, K]
     const __nv_bfloat16* B;       // [S, E, N, rank]
     const float* scale;           // [S], null: 1
-    int rank, parts, N, K;
+    int rank, parts, R, N, K;     // R = parts * rank
     const void* base;
     void* y;
-    int f32;
     int64_t base_stride, y_stride;
-    float* v;                     // [P, parts * rank]
+    int copy;                     // rows without an adapter are copied from base
+    int splits;                   // K slices
+    float* v;                     // [splits, P, R]
+    // the plan, for more than kFewPairs pairs
+    int32_t* nblocks;
+    int32_t* block_slot;
+    int32_t* rows;                // [blocks, kManyRows], -1: none
     int* err;
 };
 
-// Slot of pair p: adapter * E + expert; -1: no adapter, the row is base's; -2: the pair's expert is on another GPU.
-__device__ __forceinline__ int64_t slot_of(const AdapterArgs& g, int64_t p, bool report) {
-    int64_t e = 0;
+__device__ __forceinline__ int slot_of(const AdapterArgs& g, int p, bool report) {
+    int e = 0;
     if (g.topk_ids) {
         e = g.topk_ids[p];
-        if (e < 0 || e >= g.E) return -2;
+        if (e < 0 || e >= g.E) return kNone;
     }
-    int k;
-    const int a = g.adapter_ids[divmod_idx(p, g.topk, k)];
+    const int a = g.adapter_ids[g.topk == 1 ? p : p / g.topk];
     if (a < 0 || a >= g.S) {
         if (a != -1 && report) set_error(g.err, CHORD_DEV_BAD_ADAPTER);
-        return -1;
+        return g.copy ? -1 : kNone;
     }
-    return (int64_t)a * g.E + e;
+    return a * g.E + e;
 }
 
-__global__ void __launch_bounds__(256) adapter_down_kernel(const AdapterArgs g) {
-    const int lane = threadIdx.x & 31, R = g.rank * g.parts;
-    const int64_t n = g.P * R;
-    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += (int64_t)gridDim.x * 8) {
-        int j, q;
-        const int64_t p = divmod_idx(i, R, j), s = slot_of(g, p, lane == 0);
-        if (s < 0) continue;
-        const __nv_bfloat16* w = g.A + (s * R + j) * g.K;
-        const __nv_bfloat16* x = g.x + divmod_idx(p, g.div, q) * g.x_stride;
-        float sum = 0.0f;
-        for (int k = lane; k < g.K; k += 32) sum = fmaf(__bfloat162float(x[k]), __bfloat162float(w[k]), sum);
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) g.v[i] = sum;
+// ---- blocks of few pairs ------------------------------------------------------
+struct FewBlocks {
+    int slot[kFewPairs];     // of each pair
+    int leader[kFewPairs];   // first pair of each block
+    int rank[kFewPairs];     // pairs of the same slot before each
+    int counts[kWarps];
+    int n;
+};
+
+// Every thread of the CTA; thread p is pair p.
+__device__ __forceinline__ void find_blocks(const AdapterArgs& g, FewBlocks& f, bool report) {
+    const int p = threadIdx.x;
+    const int s = p < g.P ? slot_of(g, p, report) : kNone;
+    f.slot[p] = s;
+    __syncthreads();
+    int rank = 0;
+    for (int q = 0; q < p; ++q) rank += f.slot[q] == s;
+    const bool lead = s != kNone && rank % kFewRows == 0;
+    const unsigned m = __ballot_sync(0xffffffffu, lead);
+    f.rank[p] = rank;
+    if ((p & 31) == 0) f.counts[p >> 5] = __popc(m);
+    __syncthreads();
+    int before = __popc(m & ((1u << (p & 31)) - 1u)), n = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < (p >> 5)) before += f.counts[w];
+        n += f.counts[w];
+    }
+    if (lead) f.leader[before] = p;
+    if (p == 0) f.n = n;
+    __syncthreads();
+}
+
+// The rows of block b (MB entries, -1: none) and its slot, by every thread of the CTA.
+template <bool FEW, int MB>
+__device__ __forceinline__ int block_rows(const AdapterArgs& g, const FewBlocks* f, int b, int32_t* rows) {
+    __syncthreads();
+    int slot;
+    if constexpr (FEW) {
+        const int p = threadIdx.x, lead = f->leader[b];
+        slot = f->slot[lead];
+        if (p < MB) rows[p] = -1;
+        __syncthreads();
+        const int at = f->rank[p] - f->rank[lead];
+        if (f->slot[p] == slot && at >= 0 && at < MB) rows[at] = p;
+    } else {
+        slot = g.block_slot[b];
+        if (threadIdx.x < MB) rows[threadIdx.x] = g.rows[(int64_t)b * MB + threadIdx.x];
+    }
+    __syncthreads();
+    return slot;
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ---- v = A x --------------------------------------------------------------------
+// MT tiles of 16 rows, NT tiles of eight rows of A.  Chains of matrix instructions end after kChain steps of
+// 32 columns, their additions chop.
+constexpr int kChain = 24;
+
+template <int MT, int NT, bool FEW>
+__global__ void __launch_bounds__(kThreads) adapter_down_kernel(const AdapterArgs g) {
+    constexpr int MB = MT * 16, NB = NT * 8;
+    extern __shared__ __align__(16) float red[];   // [kWarps][MB][NB]
+    __shared__ int32_t rows[MB];
+    __shared__ FewBlocks few[1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
+    pdl_trigger();
+    pdl_wait();
+    int n;
+    if constexpr (FEW) {
+        find_blocks(g, few[0], blockIdx.x == 0);
+        n = few[0].n;
+    } else {
+        n = *g.nblocks;
+    }
+    const int chunks = (g.R + NB - 1) / NB, per = chunks * g.splits, steps = (g.K + 31) / 32;
+    for (int64_t i = blockIdx.x; i < (int64_t)n * per; i += gridDim.x) {
+        int q;
+        const int b = (int)divmod_idx(i, per, q);
+        const int r0 = q / g.splits * NB, split = q % g.splits;
+        const int slot = block_rows<FEW, MB>(g, few, b, rows);
+        if (slot < 0) continue;
+        const int k_first = (int)((int64_t)split * steps / g.splits), k_last = (int)((int64_t)(split + 1) * steps / g.splits);
+        const __nv_bfloat16* xr[2 * MT];
+#pragma unroll
+        for (int j = 0; j < 2 * MT; ++j) {
+            const int p = rows[j * 8 + gr];
+            xr[j] = p < 0 ? nullptr : g.x + (int64_t)(g.div == 1 ? p : p / g.div) * g.x_stride + 8 * c;
+        }
+        const __nv_bfloat16* ar[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int r = r0 + j * 8 + gr;
+            ar[j] = r < g.R ? g.A + ((int64_t)slot * g.R + r) * g.K + 8 * c : nullptr;
+        }
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        float* mine = red + (warp * MB + gr) * NB + 2 * c;
+        int ks = k_first + warp;
+        for (bool more = false; !more || ks < k_last; more = true) {
+            float acc[MT][NT][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) acc[m][t][u] = 0.0f;
+            for (int chain_end = min(k_last, ks + kChain * kWarps); ks < chain_end; ks += kWarps) {
+                const int k = ks * 32;
+                const bool in = k + 8 * c < g.K;
+                uint4 xa[2 * MT], wb[NT];
+#pragma unroll
+                for (int j = 0; j < 2 * MT; ++j) xa[j] = in && xr[j] ? *reinterpret_cast<const uint4*>(xr[j] + k) : zero;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) wb[j] = in && ar[j] ? *reinterpret_cast<const uint4*>(ar[j] + k) : zero;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        mma(acc[m][t], xa[2 * m].x, xa[2 * m + 1].x, xa[2 * m].y, xa[2 * m + 1].y, wb[t].x, wb[t].y);
+                        mma(acc[m][t], xa[2 * m].z, xa[2 * m + 1].z, xa[2 * m].w, xa[2 * m + 1].w, wb[t].z, wb[t].w);
+                    }
+            }
+            // the warp's own place; a further chain is added to what it holds
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float2* to = reinterpret_cast<float2*>(mine + (m * 16 + h * 8) * NB + t * 8);
+                        float2 o = make_float2(acc[m][t][2 * h], acc[m][t][2 * h + 1]);
+                        if (more) o.x += to->x, o.y += to->y;
+                        *to = o;
+                    }
+        }
+        __syncthreads();
+        for (int u = threadIdx.x; u < MB * NB; u += kThreads) {
+            const int p = rows[u / NB], r = r0 + u % NB;
+            if (p < 0 || r >= g.R) continue;
+            float s = red[u];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) s += red[w * MB * NB + u];
+            g.v[((int64_t)split * g.P + p) * g.R + r] = s;
+        }
     }
 }
 
-__global__ void __launch_bounds__(256) adapter_up_kernel(const AdapterArgs g) {
-    const int64_t n = g.P * g.N;
-    const int R = g.rank * g.parts;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        int c;
-        const int64_t p = divmod_idx(i, g.N, c), s = slot_of(g, p, false);
-        const int64_t from = p * g.base_stride + c, to = p * g.y_stride + c;
-        if (s == -2 || (s == -1 && g.base == g.y)) continue;
-        float sum = 0.0f;
-        if (s >= 0) {
-            const __nv_bfloat16* b = g.B + (s * g.N + c) * g.rank;
-            const float* v = g.v + p * R + c / (g.N / g.parts) * g.rank;
-            for (int k = 0; k < g.rank; ++k) sum = fmaf(v[k], __bfloat162float(b[k]), sum);
-            if (g.scale) sum *= g.scale[s / g.E];
+// ---- y = base + scale * B v --------------------------------------------------------
+// Eight neighbouring numbers of base's or y's type.
+template <bool F32>
+struct Eight;
+template <>
+struct Eight<true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const void* p, int64_t i) {
+        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        a = q[0];
+        b = q[1];
+    }
+    __device__ __forceinline__ void store(void* p, int64_t i) const {
+        float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+        q[0] = a;
+        q[1] = b;
+    }
+    __device__ __forceinline__ void add(const float (&d)[8]) {
+        a.x += d[0], a.y += d[1], a.z += d[2], a.w += d[3];
+        b.x += d[4], b.y += d[5], b.z += d[6], b.w += d[7];
+    }
+};
+template <>
+struct Eight<false> {
+    uint4 a;
+    __device__ __forceinline__ void load(const void* p, int64_t i) {
+        a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
+    }
+    __device__ __forceinline__ void store(void* p, int64_t i) const {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = a;
+    }
+    __device__ __forceinline__ static uint32_t pair(uint32_t o, float d0, float d1) {
+        const float2 f = __bfloat1622float2(u32_as_bf2(o));
+        return bf2_as_u32(__floats2bfloat162_rn(f.x + d0, f.y + d1));
+    }
+    __device__ __forceinline__ void add(const float (&d)[8]) {
+        a.x = pair(a.x, d[0], d[1]), a.y = pair(a.y, d[2], d[3]);
+        a.z = pair(a.z, d[4], d[5]), a.w = pair(a.w, d[6], d[7]);
+    }
+};
+
+// Three bf16 numbers of eight significant bits each whose sum is v; an infinity or NaN is the first alone.
+__device__ __forceinline__ void split3(float v, __nv_bfloat16 (&h)[3]) {
+    const bool finite = fabsf(v) <= 3.4028235e38f;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        h[i] = finite ? __float2bfloat16_rz(v) : __float2bfloat16_rn(i ? 0.0f : v);
+        v = finite ? v - __bfloat162float(h[i]) : 0.0f;
+    }
+}
+
+// MT tiles of 16 rows; a plan's block of 64 rows is several items.
+template <int MT, bool F32, bool FEW>
+__global__ void __launch_bounds__(kThreads) adapter_up_kernel(const AdapterArgs g, int cols) {
+    constexpr int MB = FEW ? kFewRows : kManyRows, MR = MT * 16, SUB = MB / MR;
+    extern __shared__ __align__(16) uint32_t frag[];   // [MT][k steps][3][32][4]
+    __shared__ int32_t rows[MB];
+    __shared__ FewBlocks few[1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
+    if constexpr (!FEW) pdl_wait();
+    int n;
+    if constexpr (FEW) {
+        find_blocks(g, few[0], false);   // the ids are older than the kernel before
+        n = few[0].n;
+        pdl_wait();
+    } else {
+        n = *g.nblocks;
+    }
+    const int Np = g.N / g.parts, tiles = (Np + 31) / 32;          // 32-column tiles of a part
+    const int ksp = (g.rank + 15) / 16, ks = ksp * g.parts;        // 16-wide steps of a part, of all
+    const int groups = (tiles * g.parts + cols - 1) / cols;        // items of a block: `cols` tiles each
+    for (int64_t i = blockIdx.x; i < (int64_t)n * SUB * groups; i += gridDim.x) {
+        int q;
+        const int bs = (int)divmod_idx(i, groups, q);
+        const int slot = block_rows<FEW, MB>(g, few, bs / SUB, rows);
+        const int32_t* mine = rows + bs % SUB * MR;
+        if (mine[0] < 0) continue;   // rows of a block are a prefix
+        if (slot >= 0) {
+            const float scale = g.scale ? g.scale[slot / g.E] : 1.0f;
+            const int quads = g.rank / 4;
+            for (int u = threadIdx.x; u < MR * ks * 4; u += kThreads) {
+                const int row = u % MR, k4 = u / MR, part = k4 / (ksp * 4), kq = k4 % (ksp * 4);
+                const int p = mine[row];
+                float4 f = make_float4(0, 0, 0, 0);
+                if (p >= 0 && kq < quads) {
+                    const float* from = g.v + (int64_t)p * g.R + part * g.rank + kq * 4;
+                    f = *reinterpret_cast<const float4*>(from);
+                    for (int s = 1; s < g.splits; ++s) {
+                        const float4 o = *reinterpret_cast<const float4*>(from + (int64_t)s * g.P * g.R);
+                        f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+                    }
+                }
+                __nv_bfloat16 h[4][3];
+                split3(f.x * scale, h[0]);
+                split3(f.y * scale, h[1]);
+                split3(f.z * scale, h[2]);
+                split3(f.w * scale, h[3]);
+                uint32_t* to = frag + (((row / 16 * ks + k4 / 4) * 3) * 32 + (row % 8) * 4 + k4 % 4) * 4 + row % 16 / 8;
+#pragma unroll
+                for (int t = 0; t < 3; ++t) {
+                    to[t * 128] = bf2_as_u32(__halves2bfloat162(h[0][t], h[1][t]));
+                    to[t * 128 + 2] = bf2_as_u32(__halves2bfloat162(h[2][t], h[3][t]));
+                }
+            }
+            __syncthreads();
         }
-        if (g.f32) {
-            const float o = static_cast<const float*>(g.base)[from];
-            static_cast<float*>(g.y)[to] = s >= 0 ? o + sum : o;
-        } else {
-            const __nv_bfloat16 o = static_cast<const __nv_bfloat16*>(g.base)[from];
-            static_cast<__nv_bfloat16*>(g.y)[to] = s >= 0 ? __float2bfloat16_rn(__bfloat162float(o) + sum) : o;
+        int p[2 * MT];
+#pragma unroll
+        for (int j = 0; j < 2 * MT; ++j) p[j] = mine[j * 8 + gr];
+        const int last = min((q + 1) * cols, tiles * g.parts);
+        for (int t = q * cols + warp; t < last; t += kWarps) {
+            const int part = t / tiles, n0 = t % tiles * 32, width = Np - n0, col = part * Np + n0 + 8 * c;
+            const bool in = 8 * c < width;
+            Eight<F32> o[2 * MT];
+#pragma unroll
+            for (int j = 0; j < 2 * MT; ++j)
+                if (in && p[j] >= 0) o[j].load(g.base, p[j] * g.base_stride + col);
+            if (slot >= 0) {
+                float acc[MT][4][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) acc[m][j][u] = 0.0f;
+                // column of lane group gr in tile j: the eight columns of one lane's results are 8 c ... 8 c + 7
+                const int bc = 8 * (gr >> 1) + (gr & 1);
+                const __nv_bfloat16* b = g.B + ((int64_t)slot * g.N + part * Np + n0 + bc) * g.rank + 4 * c;
+                const bool bin = bc < width;
+                for (int s = 0; s < ksp; ++s) {
+                    uint2 w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = bin && 16 * s + 4 * c < g.rank ? *reinterpret_cast<const uint2*>(b + (int64_t)2 * j * g.rank + 16 * s)
+                                                              : make_uint2(0, 0);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int t3 = 2; t3 >= 0; --t3) {
+                            const uint4 a = *reinterpret_cast<const uint4*>(frag + (((m * ks + part * ksp + s) * 3 + t3) * 32 + lane) * 4);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) mma(acc[m][j], a.x, a.y, a.z, a.w, w[j].x, w[j].y);
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < 2 * MT; ++j) {
+                    float d[8];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        d[2 * u] = acc[j / 2][u][j % 2 * 2];
+                        d[2 * u + 1] = acc[j / 2][u][j % 2 * 2 + 1];
+                    }
+                    o[j].add(d);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2 * MT; ++j)
+                if (in && p[j] >= 0) o[j].store(g.y, p[j] * g.y_stride + col);
         }
     }
+}
+
+// ---- the plan ------------------------------------------------------------------------
+// A counting sort of the pairs by slot (index slot + 1, so that rows without an adapter come first).
+// Which of a slot's pairs come first depends on timing; what a row of y becomes does not.
+struct PlanArgs {
+    AdapterArgs g;
+    int nslots;        // S * E + 1
+    int32_t* counts;   // [nslots], then the next free position of each
+};
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive sum over the threads of the CTA; every thread gets the total too.
+__device__ __forceinline__ int block_scan(int v, int& total) {
+    __shared__ int sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int s = sums[lane];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        sums[lane] = s;
+    }
+    __syncthreads();
+    total = sums[31];
+    return x - v + (warp ? sums[warp - 1] : 0);
+}
+
+// Counts to first positions; the blocks' slots, and -1 behind a slot's last row.
+__device__ __forceinline__ void plan_scan(const PlanArgs& a, int32_t* counts) {
+    const int per = (a.nslots + kPlanThreads - 1) / kPlanThreads;
+    const int s0 = threadIdx.x * per, s1 = min(s0 + per, a.nslots);
+    int mine = 0, total;
+    for (int s = s0; s < s1; ++s) mine += (counts[s] + kManyRows - 1) / kManyRows;
+    int b = block_scan(mine, total);
+    for (int s = s0; s < s1; ++s) {
+        const int n = counts[s], first = b;
+        counts[s] = first * kManyRows;
+        for (int k = 0; k < n; k += kManyRows) a.g.block_slot[b++] = s - 1;
+        for (int k = n; k < (b - first) * kManyRows; ++k) a.g.rows[(int64_t)first * kManyRows + k] = -1;
+    }
+    if (threadIdx.x == 0) *a.g.nblocks = total;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanArgs a) {
+    extern __shared__ int32_t counts_s[];
+    pdl_trigger();
+    for (int s = threadIdx.x; s < a.nslots; s += kPlanThreads) counts_s[s] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < a.g.P; p += kPlanThreads) {
+        const int s = slot_of(a.g, p, true);
+        if (s != kNone) atomicAdd(&counts_s[s + 1], 1);
+    }
+    __syncthreads();
+    plan_scan(a, counts_s);
+    __syncthreads();
+    for (int p = threadIdx.x; p < a.g.P; p += kPlanThreads) {
+        const int s = slot_of(a.g, p, false);
+        if (s != kNone) a.g.rows[atomicAdd(&counts_s[s + 1], 1)] = p;
+    }
+}
+
+__global__ void __launch_bounds__(256) adapter_count_kernel(const PlanArgs a) {
+    for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < a.g.P; p += (int64_t)gridDim.x * 256) {
+        const int s = slot_of(a.g, (int)p, true);
+        if (s != kNone) atomicAdd(&a.counts[s + 1], 1);
+    }
+}
+__global__ void __launch_bounds__(kPlanThreads) adapter_scan_kernel(const PlanArgs a) { plan_scan(a, a.counts); }
+__global__ void __launch_bounds__(256) adapter_place_kernel(const PlanArgs a) {
+    for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < a.g.P; p += (int64_t)gridDim.x * 256) {
+        const int s = slot_of(a.g, (int)p, false);
+        if (s != kNone) a.g.rows[atomicAdd(&a.counts[s + 1], 1)] = (int32_t)p;
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------------
+// One CTA plans up to these; beyond, three kernels over the whole GPU.
+constexpr int kPlanPairs = 16384, kPlanSlots = 16384;
+
+struct Layout {
+    int splits;
+    int64_t blocks;   // at most
+    size_t v, nblocks, block_slot, rows, counts, bytes;
+};
+
+// K slices: with fewer items than CTAs that the GPU holds, K is cut until they are as many.  A block holds at
+// least one pair, few blocks more than one in sixteen of a full one.
+Layout layout_of(int64_t P, int64_t slots, int R, int K) {
+    Layout l{};
+    const bool few = P <= kFewPairs;
+    const int64_t mb = few ? kFewRows : kManyRows;
+    l.blocks = P / mb + (P < slots + 1 ? P : slots + 1) + 1;
+    const int64_t items = (few ? (P < slots ? P : slots) : (P + mb - 1) / mb) * ((R + 63) / 64);
+    int64_t s = (kTargetCtas + items - 1) / items;
+    if (s > kMaxSplit) s = kMaxSplit;
+    if (K > 0 && s > (K + 255) / 256) s = (K + 255) / 256;   // a step of 32 columns for each warp
+    l.splits = (int)(s < 1 ? 1 : s);
+    auto take = [&](size_t n) {
+        const size_t at = l.bytes;
+        l.bytes += (n + 255) / 256 * 256;
+        return at;
+    };
+    l.v = take((size_t)l.splits * P * R * 4);
+    if (!few) {
+        l.nblocks = take(4);
+        l.block_slot = take((size_t)l.blocks * 4);
+        l.rows = take((size_t)l.blocks * kManyRows * 4);
+        l.counts = take((size_t)(slots + 1) * 4);
+    }
+    return l;
+}
+
+template <int MT, int NT, bool FEW>
+cudaError_t launch_down_as(const AdapterArgs& g, int64_t blocks, bool pdl, cudaStream_t st) {
+    auto* kern = adapter_down_kernel<MT, NT, FEW>;
+    const size_t smem = (size_t)kWarps * MT * 16 * NT * 8 * 4;
+    int ctas = 0;
+    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
+    if (e != cudaSuccess) return e;
+    const int64_t items = blocks * ((g.R + NT * 8 - 1) / (NT * 8)) * g.splits, most = (int64_t)device_info().sm_count * ctas;
+    return launch_pdl(pdl, kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g);
+}
+
+template <bool FEW>
+cudaError_t launch_down(const AdapterArgs& g, int64_t blocks, bool pdl, cudaStream_t st) {
+    constexpr int MT = FEW ? kFewRows / 16 : kManyRows / 16;
+    if (g.R <= 8) return launch_down_as<MT, 1, FEW>(g, blocks, pdl, st);
+    if (g.R <= 16) return launch_down_as<MT, 2, FEW>(g, blocks, pdl, st);
+    if (g.R <= 32) return launch_down_as<MT, 4, FEW>(g, blocks, pdl, st);
+    return launch_down_as<MT, FEW ? 8 : 4, FEW>(g, blocks, pdl, st);
+}
+
+template <int MT, bool F32, bool FEW>
+cudaError_t launch_up_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
+    auto* kern = adapter_up_kernel<MT, F32, FEW>;
+    const int ks = (g.rank + 15) / 16 * g.parts;
+    const size_t smem = (size_t)MT * ks * 3 * 512;
+    int ctas = 0;
+    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, 2 * 32 * 3 * 512, &ctas);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (int64_t)device_info().sm_count * ctas;
+    const int tiles = (g.N / g.parts + 31) / 32 * g.parts;
+    // four tiles a warp share the fragments of v, fewer where that leaves CTAs idle
+    int cols = 4 * kWarps;
+    const int64_t rows = blocks * (FEW ? 1 : kManyRows / (MT * 16));
+    while (cols > kWarps && rows * ((tiles + cols - 1) / cols) < most) cols /= 2;
+    const int64_t items = rows * ((tiles + cols - 1) / cols);
+    return launch_pdl(pdl_enabled(), kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g, cols);
+}
+
+template <bool FEW>
+cudaError_t launch_up(const AdapterArgs& g, int64_t blocks, bool f32, cudaStream_t st) {
+    constexpr int MT = FEW ? 1 : 2;
+    return f32 ? launch_up_as<MT, true, FEW>(g, blocks, st) : launch_up_as<MT, false, FEW>(g, blocks, st);
+}
+
+cudaError_t launch_plan(const AdapterArgs& g, int64_t slots, int32_t* counts, cudaStream_t st) {
+    PlanArgs a{g, (int)slots + 1, counts};
+    if (g.P <= kPlanPairs && slots < kPlanSlots) {
+        const size_t smem = (size_t)a.nslots * 4;
+        cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(adapter_plan_kernel), (size_t)kPlanSlots * 4);
+        if (e != cudaSuccess) return e;
+        adapter_plan_kernel<<<1, kPlanThreads, smem, st>>>(a);
+        return cudaGetLastError();
+    }
+    cudaError_t e = cudaMemsetAsync(counts, 0, (size_t)a.nslots * 4, st);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = ceil_div64(g.P, 256), most = 8 * (int64_t)device_info().sm_count;
+    const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+    adapter_count_kernel<<<grid, 256, 0, st>>>(a);
+    adapter_scan_kernel<<<1, kPlanThreads, 0, st>>>(a);
+    adapter_place_kernel<<<grid, 256, 0, st>>>(a);
+    return cudaGetLastError();
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -106,7 +586,8 @@ extern "C" {
 size_t chord_adapter_workspace_bytes(int64_t T, int topk, int adapters, int E, int rank, int parts) {
     if (T < 0 || topk <= 0 || adapters <= 0 || E <= 0 || rank <= 0 || parts <= 0 || rank > 128 || parts > 4) return 0;
     if (T > INT32_MAX / topk || adapters > 65536 / E) return 0;
-    return ((size_t)T * topk * rank * parts * 4 + 255) / 256 * 256 + 256;
+    const size_t bytes = layout_of(T * topk, (int64_t)adapters * E, rank * parts, 0).bytes;
+    return bytes ? bytes : 256;
 }
 
 chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, int a_row_divisor, const int32_t* adapter_ids,
@@ -140,14 +621,26 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     if (workspace_bytes < chord_adapter_workspace_bytes(T, topk, adapters, E, rank, parts)) return CHORD_ERR_BUFFER_TOO_SMALL;
     const DeviceInfo& di = device_info();
     if (!di.err) return CHORD_ERR_CUDA;
-    AdapterArgs g{static_cast<const __nv_bfloat16*>(x), x_stride, a_row_divisor, adapter_ids, topk_ids, P, topk, adapters, E,
-                  static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, rank, parts, N, K, base, y,
-                  y_dtype == CHORD_DTYPE_F32, base_stride, y_stride, static_cast<float*>(workspace), di.err};
+    const int64_t slots = (int64_t)adapters * E;
+    const bool few = P <= kFewPairs, f32 = y_dtype == CHORD_DTYPE_F32;
+    const Layout l = layout_of(P, slots, rank * parts, K);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    AdapterArgs g{static_cast<const __nv_bfloat16*>(x), x_stride, a_row_divisor, adapter_ids, topk_ids, (int)P, topk, adapters, E,
+                  static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, rank, parts, rank * parts, N, K,
+                  base, y, base_stride, y_stride, base != y, l.splits, reinterpret_cast<float*>(ws + l.v),
+                  reinterpret_cast<int32_t*>(ws + l.nblocks), reinterpret_cast<int32_t*>(ws + l.block_slot),
+                  reinterpret_cast<int32_t*>(ws + l.rows), di.err};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t down = ceil_div64(P * rank * parts, 8), up = ceil_div64(P * N, 256);
-    adapter_down_kernel<<<(unsigned)(down < 65536 ? down : 65536), 256, 0, st>>>(g);
-    adapter_up_kernel<<<(unsigned)(up < 65536 ? up : 65536), 256, 0, st>>>(g);
-    if (cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;
+    cudaError_t e;
+    if (few) {
+        e = launch_down<true>(g, l.blocks, false, st);
+        if (e == cudaSuccess) e = launch_up<true>(g, l.blocks, f32, st);
+    } else {
+        e = launch_plan(g, slots, reinterpret_cast<int32_t*>(ws + l.counts), st);
+        if (e == cudaSuccess) e = launch_down<false>(g, l.blocks, pdl_enabled(), st);
+        if (e == cudaSuccess) e = launch_up<false>(g, l.blocks, f32, st);
+    }
+    if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;
     if (!opts || !opts->validate) return CHORD_OK;
     int32_t code = 0;
     const chord_status s = chord_get_device_error(stream, &code);

@@ -22,12 +22,13 @@
 
 #include "chord_common.cuh"
 #include "chord_internal.h"
+#include "chord_rows.cuh"
 
 namespace chord {
 namespace {
 
 constexpr int kFewPairs = 256;
-constexpr int kFewRows = 16, kManyRows = 64;   // rows of a block
+constexpr int kFewRows = 16, kManyRows = 128;   // rows of a block
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kMaxSplit = 16;
 constexpr int kTargetCtas = 304;
@@ -135,28 +136,22 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 // 32 columns, their additions chop.
 constexpr int kChain = 24;
 
-template <int MT, int NT, bool FEW>
+template <int NT>
 __global__ void __launch_bounds__(kThreads) adapter_down_kernel(const AdapterArgs g) {
-    constexpr int MB = MT * 16, NB = NT * 8;
+    constexpr int MT = 1, MB = kFewRows, NB = NT * 8;
     extern __shared__ __align__(16) float red[];   // [kWarps][MB][NB]
     __shared__ int32_t rows[MB];
     __shared__ FewBlocks few[1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
     pdl_trigger();
-    pdl_wait();
-    int n;
-    if constexpr (FEW) {
-        find_blocks(g, few[0], blockIdx.x == 0);
-        n = few[0].n;
-    } else {
-        n = *g.nblocks;
-    }
+    find_blocks(g, few[0], blockIdx.x == 0);
+    const int n = few[0].n;
     const int chunks = (g.R + NB - 1) / NB, per = chunks * g.splits, steps = (g.K + 31) / 32;
     for (int64_t i = blockIdx.x; i < (int64_t)n * per; i += gridDim.x) {
         int q;
         const int b = (int)divmod_idx(i, per, q);
         const int r0 = q / g.splits * NB, split = q % g.splits;
-        const int slot = block_rows<FEW, MB>(g, few, b, rows);
+        const int slot = block_rows<true, MB>(g, few, b, rows);
         if (slot < 0) continue;
         const int k_first = (int)((int64_t)split * steps / g.splits), k_last = (int)((int64_t)(split + 1) * steps / g.splits);
         const __nv_bfloat16* xr[2 * MT];
@@ -485,8 +480,8 @@ Layout layout_of(int64_t P, int64_t slots, int R, int K) {
     const bool few = P <= kFewPairs;
     const int64_t mb = few ? kFewRows : kManyRows;
     l.blocks = P / mb + (P < slots + 1 ? P : slots + 1) + 1;
-    const int64_t items = (few ? (P < slots ? P : slots) : (P + mb - 1) / mb) * ((R + 63) / 64);
-    int64_t s = (kTargetCtas + items - 1) / items;
+    const int64_t items = (P < slots ? P : slots) * ((R + 63) / 64);
+    int64_t s = few && items > 0 ? (kTargetCtas + items - 1) / items : 1;
     if (s > kMaxSplit) s = kMaxSplit;
     if (K > 0 && s > (K + 255) / 256) s = (K + 255) / 256;   // a step of 32 columns for each warp
     l.splits = (int)(s < 1 ? 1 : s);
@@ -505,24 +500,37 @@ Layout layout_of(int64_t P, int64_t slots, int R, int K) {
     return l;
 }
 
-template <int MT, int NT, bool FEW>
-cudaError_t launch_down_as(const AdapterArgs& g, int64_t blocks, bool pdl, cudaStream_t st) {
-    auto* kern = adapter_down_kernel<MT, NT, FEW>;
-    const size_t smem = (size_t)kWarps * MT * 16 * NT * 8 * 4;
+template <int NT>
+cudaError_t launch_down_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
+    auto* kern = adapter_down_kernel<NT>;
+    const size_t smem = (size_t)kWarps * kFewRows * NT * 8 * 4;
     int ctas = 0;
     cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
     if (e != cudaSuccess) return e;
     const int64_t items = blocks * ((g.R + NT * 8 - 1) / (NT * 8)) * g.splits, most = (int64_t)device_info().sm_count * ctas;
-    return launch_pdl(pdl, kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g);
+    kern<<<(unsigned)(items < most ? items : most), kThreads, smem, st>>>(g);
+    return cudaGetLastError();
 }
 
-template <bool FEW>
-cudaError_t launch_down(const AdapterArgs& g, int64_t blocks, bool pdl, cudaStream_t st) {
-    constexpr int MT = FEW ? kFewRows / 16 : kManyRows / 16;
-    if (g.R <= 8) return launch_down_as<MT, 1, FEW>(g, blocks, pdl, st);
-    if (g.R <= 16) return launch_down_as<MT, 2, FEW>(g, blocks, pdl, st);
-    if (g.R <= 32) return launch_down_as<MT, 4, FEW>(g, blocks, pdl, st);
-    return launch_down_as<MT, FEW ? 8 : 4, FEW>(g, blocks, pdl, st);
+cudaError_t launch_down(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
+    if (g.R <= 8) return launch_down_as<1>(g, blocks, st);
+    if (g.R <= 16) return launch_down_as<2>(g, blocks, st);
+    if (g.R <= 32) return launch_down_as<4>(g, blocks, st);
+    return launch_down_as<8>(g, blocks, st);
+}
+
+// The plan's blocks, on the tcgen05 kernel that the router's logits use.
+cudaError_t launch_down_many(const AdapterArgs& g, int64_t blocks, int64_t slots, int64_t x_rows, cudaStream_t st) {
+    RowsArgs r{};
+    r.x = g.x, r.x_rows = x_rows, r.x_stride = g.x_stride;
+    r.W = g.A, r.w_rows = slots * g.R, r.K = g.K, r.parts = 1;
+    r.R = g.R, r.nb = kManyRows, r.items = blocks;
+    r.out = g.v, r.nblocks = g.nblocks, r.block_slot = g.block_slot, r.rows = g.rows, r.div = g.div, r.err = g.err;
+    // blocks that hold rows: at least P / 128, of many slots perhaps half
+    int64_t likely = ceil_div64(g.P, kManyRows);
+    if (likely < (g.P < slots ? g.P : slots) / 2) likely = (g.P < slots ? g.P : slots) / 2;
+    r.splits = rows_splits(g.R, r.nb, (g.K + 63) / 64, likely, kTargetCtas);
+    return launch_rows(r, pdl_enabled(), st);
 }
 
 template <int MT, bool F32, bool FEW>
@@ -633,11 +641,11 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (few) {
-        e = launch_down<true>(g, l.blocks, false, st);
+        e = launch_down(g, l.blocks, st);
         if (e == cudaSuccess) e = launch_up<true>(g, l.blocks, f32, st);
     } else {
         e = launch_plan(g, slots, reinterpret_cast<int32_t*>(ws + l.counts), st);
-        if (e == cudaSuccess) e = launch_down<false>(g, l.blocks, pdl_enabled(), st);
+        if (e == cudaSuccess) e = launch_down_many(g, l.blocks, slots, x_rows, st);
         if (e == cudaSuccess) e = launch_up<false>(g, l.blocks, f32, st);
     }
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;

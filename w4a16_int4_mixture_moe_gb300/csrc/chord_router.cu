@@ -5,6 +5,7 @@
 
 #include "chord_common.cuh"
 #include "chord_internal.h"
+#include "chord_rows.cuh"
 
 namespace chord {
 namespace {
@@ -17,6 +18,8 @@ struct LogitArgs {
     int parts, E, H;
     float* out;
 };
+
+constexpr int kFewTokens = 16;
 
 // A warp per logit.
 __global__ void __launch_bounds__(256) logits_kernel(const LogitArgs a) {
@@ -74,16 +77,39 @@ chord_status chord_router_split_weights(const float* W, int64_t n, void* parts, 
 
 chord_status chord_router_logits(const void* x, int64_t x_stride, int T, const void* W, int parts, int E, int H, float* logits,
                                  const chord_opts* opts, void* stream) {
-    (void)opts;
     if (T < 0 || E <= 0 || H <= 0 || x_stride < (T > 1 ? H : 0)) return CHORD_ERR_INVALID_ARG;
     if ((parts != 1 && parts != 3) || E > 1024 || H % 8 || (T > 1 && x_stride % 8)) return CHORD_ERR_UNSUPPORTED;
     if (!W || !aligned16(W)) return CHORD_ERR_INVALID_ARG;
     if (T > 0 && (!x || !aligned16(x) || !logits || (reinterpret_cast<uintptr_t>(logits) & 3))) return CHORD_ERR_INVALID_ARG;
     if (T == 0) return CHORD_OK;
     LogitArgs a{static_cast<const __nv_bfloat16*>(x), x_stride, T, static_cast<const __nv_bfloat16*>(W), parts, E, H, logits};
-    const int64_t blocks = ceil_div64((int64_t)T * E, 8);
-    logits_kernel<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return cudaGetLastError() == cudaSuccess ? CHORD_OK : CHORD_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T <= kFewTokens) {
+        const int64_t blocks = ceil_div64((int64_t)T * E, 8);
+        logits_kernel<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(a);
+        return cudaGetLastError() == cudaSuccess ? CHORD_OK : CHORD_ERR_CUDA;
+    }
+    const DeviceInfo& di = device_info();
+    if (!di.err) return CHORD_ERR_CUDA;
+    RowsArgs r{};
+    r.x = x, r.x_rows = T, r.x_stride = T > 1 ? x_stride : H;
+    r.W = W, r.w_rows = (int64_t)parts * E, r.K = H, r.parts = parts, r.part_rows = E;
+    r.nb = T > 4096 ? 128 : T >= 64 ? 64 : (T + 15) / 16 * 16;
+    const int64_t tiles = ceil_div64(T, r.nb);
+    const int m_tiles = (E + 127) / 128;
+    // three tiles of 128 experts share the tokens' copy; fewer where that leaves SMs idle even with K cut in eight
+    r.groups = tiles * ((m_tiles + 2) / 3) * 8 < di.sm_count ? m_tiles : (m_tiles + 2) / 3;
+    r.R = ((E + r.groups - 1) / r.groups + 7) / 8 * 8;
+    r.items = tiles * r.groups;
+    r.E = E, r.out = logits, r.err = di.err;
+    r.splits = rows_splits(r.R, r.nb, (H + 63) / 64 * parts, r.items, di.sm_count);
+    if (launch_rows(r, pdl_enabled(), st) != cudaSuccess || cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;
+    if (!opts || !opts->validate) return CHORD_OK;
+    int32_t code = 0;
+    const chord_status s = chord_get_device_error(stream, &code);
+    if (s != CHORD_OK) return s;
+    if (code == CHORD_DEV_TIMEOUT) return CHORD_ERR_TIMEOUT;
+    return code ? CHORD_ERR_DEVICE_VALIDATION : CHORD_OK;
 }
 
 }  // extern "C"

@@ -524,12 +524,12 @@ cudaError_t launch_down_many(const AdapterArgs& g, int64_t blocks, int64_t slots
     RowsArgs r{};
     r.x = g.x, r.x_rows = x_rows, r.x_stride = g.x_stride;
     r.W = g.A, r.w_rows = slots * g.R, r.K = g.K, r.parts = 1;
-    r.R = g.R, r.nb = kManyRows, r.items = blocks;
+    r.R = g.R, r.nb = rows_block(g.R), r.block_rows = kManyRows, r.items = blocks * (kManyRows / r.nb);
     r.out = g.v, r.nblocks = g.nblocks, r.block_slot = g.block_slot, r.rows = g.rows, r.div = g.div, r.err = g.err;
     // blocks that hold rows: at least P / 128, of many slots perhaps half
     int64_t likely = ceil_div64(g.P, kManyRows);
     if (likely < (g.P < slots ? g.P : slots) / 2) likely = (g.P < slots ? g.P : slots) / 2;
-    r.splits = rows_splits(g.R, r.nb, (g.K + 63) / 64, likely, kTargetCtas);
+    r.splits = rows_splits(g.R, r.nb, (g.K + 63) / 64, likely * (kManyRows / r.nb), kTargetCtas);
     return launch_rows(r, pdl_enabled(), st);
 }
 

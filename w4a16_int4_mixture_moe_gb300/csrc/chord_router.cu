@@ -94,7 +94,7 @@ chord_status chord_router_logits(const void* x, int64_t x_stride, int T, const v
     RowsArgs r{};
     r.x = x, r.x_rows = T, r.x_stride = T > 1 ? x_stride : H;
     r.W = W, r.w_rows = (int64_t)parts * E, r.K = H, r.parts = parts, r.part_rows = E;
-    r.nb = T > 4096 ? 128 : T >= 64 ? 64 : (T + 15) / 16 * 16;
+    r.nb = T >= 64 ? 64 : (T + 15) / 16 * 16;
     const int64_t tiles = ceil_div64(T, r.nb);
     const int m_tiles = (E + 127) / 128;
     // three tiles of 128 experts share the tokens' copy; fewer where that leaves SMs idle even with K cut in eight

@@ -4,8 +4,11 @@
 // not read).  A CTA computes one K slice of one item; the slices of an item are a cluster and
 // join their sums through distributed shared memory in rank order.  Roles: a producer warp (a
 // stage of 64 columns: one box of the weights for every 128 rows, and either one box of
-// consecutive rows of x or, gathered, four rows a copy, each lane its own), an issuing warp, four warps that read
-// the accumulators.  Bound by the copies into shared memory, about 45 bytes a cycle and SM.
+// consecutive rows of x or, gathered, four rows a copy, each lane its own), an issuing warp, eight warps that
+// read the accumulators.  The matrix instructions' additions chop, so a chain of them is kept to
+// kChain stages (16 instructions); the eight warps add the chains up in registers, one accumulator being read
+// while the other one is filled (K = 7168 in chains of 224: relative error 3.8e-6, of 16: 3e-7, FP32
+// products and sums in PyTorch: 9e-7).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -20,7 +23,8 @@ namespace {
 
 constexpr int kStepCols = 64;           // columns of a stage: 128 bytes, the swizzle's row
 constexpr int kTileRows = 128;
-constexpr int kRowsThreads = 192;
+constexpr int kRowsThreads = 320;
+constexpr int kChain = 4;               // stages
 constexpr int kMaxStages = 12;
 constexpr long long kLandCycles = 4000000;   // about 2 ms
 constexpr size_t kFixed = 1024;         // alignment
@@ -61,17 +65,16 @@ __device__ __forceinline__ void gather4_g2s(uint32_t dst, const void* map, int c
         "l"(map), "r"(col), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
         : "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-template <bool GATHER>
-__global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a, const RowsPlan pl, const __grid_constant__ RowsMaps maps) {
+// G2: groups of 16 accumulator columns that each of the eight warps adds up, half of an item's.
+template <bool GATHER, int G2>
+__global__ void __launch_bounds__(kRowsThreads, G2 <= 4 ? 2 : 1) rows_kernel(const RowsArgs a, const RowsPlan pl, const __grid_constant__ RowsMaps maps) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int flag[1];   // abort
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -82,7 +85,10 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a, co
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        mbar_init(&acc_full, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], 8);
+        }
         flag[0] = 0;
         fence_barrier_init();
     }
@@ -103,18 +109,21 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a, co
     const int32_t* list = nullptr;
     bool live = true;
     if constexpr (GATHER) {
-        live = item < *a.nblocks;
+        int sub;
+        const int64_t block = divmod_idx(item, a.block_rows / a.nb, sub);
+        live = block < *a.nblocks;
         if (live) {
-            const int slot = a.block_slot[item];
+            const int slot = a.block_slot[block];
             live = slot >= 0;
             w0 = slot * a.R;
-            list = a.rows + item * a.nb;
+            list = a.rows + block * a.block_rows + sub * a.nb;
         }
         if (live) {
             // rows of a block are a prefix
             for (int j = lane; j < a.nb; j += 32)
                 if (list[j] >= 0) n = j + 1;
             n = __reduce_max_sync(0xffffffffu, n);
+            live = n > 0;
         }
     } else {
         int g;
@@ -168,59 +177,78 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a, co
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n16 >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
         tc5::Ring ring;
         for (int s = k0; s < k1; ++s) {
-            ok = tc5::wait(&full[ring.slot], ring.phase, aborted, a.err);
+            const uint32_t chain = (uint32_t)(s - k0) / kChain, buf = chain & 1u;
+            const bool first = (s - k0) % kChain == 0;
+            // the second use of an accumulator on: it has been read
+            if (first && chain >= 2) ok = tc5::wait(&acc_empty[buf], ((chain >> 1) & 1u) ^ 1u, aborted, a.err);
+            ok = ok && tc5::wait(&full[ring.slot], ring.phase, aborted, a.err);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc5::fence_after();
-            const uint32_t st = base + (uint32_t)ring.slot * (uint32_t)pl.stage;
+            const uint32_t st = base + (uint32_t)ring.slot * (uint32_t)pl.stage, acc = tmem + buf * (uint32_t)(pl.tiles * a.nb);
             const uint64_t db = tc5::desc_sw128(st + (uint32_t)(pl.tiles * pl.w_rows) * 128u);
             if (tc5::elect()) {
                 for (int m = 0; m < pl.tiles; ++m) {
                     const uint64_t da = tc5::desc_sw128(st + (uint32_t)(m * pl.w_rows) * 128u);
 #pragma unroll
                     for (uint32_t kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + (uint32_t)(m * a.nb), da + 2u * kk, db + 2u * kk, idesc, s > k0 || kk > 0 ? 1u : 0u);
+                        mma_f16(acc + (uint32_t)(m * a.nb), da + 2u * kk, db + 2u * kk, idesc, !first || kk > 0 ? 1u : 0u);
                 }
                 tc5::commit<false, false>(smem_u32(&empty[ring.slot]));
-                if (s + 1 == k1) tc5::commit<false, false>(smem_u32(&acc_full));
+                if (s + 1 == k1 || (s + 1 - k0) % kChain == 0) tc5::commit<false, false>(smem_u32(&acc_full[buf]));
             }
             __syncwarp();
             ring.next(pl.stages);
         }
     }
-    // ---- the sums: every warp waits for the last instruction, four read the accumulators
-    if (live) {
-        ok = ok && tc5::wait(&acc_full, 0, aborted, a.err);
-        ok = __all_sync(0xffffffffu, ok);
-        tc5::fence_after();
+    // ---- the sums: group g of the accumulator's columns is 16 rows of x and one tile of weight rows
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int per = a.nb / 16, groups = pl.tiles * per;
+    float sum[G2][16];
+    if (live && warp >= 2) {
+#pragma unroll
+        for (int i = 0; i < G2; ++i)
+#pragma unroll
+            for (int u = 0; u < 16; ++u) sum[i][u] = 0.0f;
+        const int chains = (k1 - k0 + kChain - 1) / kChain;
+        for (int c = 0; c < chains; ++c) {
+            const int buf = c & 1;
+            ok = tc5::wait(&acc_full[buf], (uint32_t)((c >> 1) & 1), aborted, a.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc5::fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * pl.tiles * a.nb);
+#pragma unroll
+            for (int i = 0; i < G2; ++i) {
+                const int g = 2 * i + half;
+                if (g >= groups || g % per * 16 >= n || g / per * kTileRows + quarter * 32 >= a.R) continue;
+                uint32_t v[16];
+                tc5::ld16(acc + (uint32_t)(g * 16), v);
+                tc5::wait_ld();
+#pragma unroll
+                for (int u = 0; u < 16; ++u) sum[i][u] += __uint_as_float(v[u]);
+            }
+            tc5::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        }
     }
-    float* sums = reinterpret_cast<float*>(smem);   // [n][R], over the ring
-    const int quarter = warp & 3;
     auto put = [&](int j, int r, float v) {   // sum of weight row r and row j, complete
         if constexpr (GATHER)
             a.out[(int64_t)list[j] * a.R + r] = v;
         else if (w0 + r < a.E)
             a.out[(t0 + j) * a.E + w0 + r] = v;
     };
-    if (live && ok && warp >= 2) {
-        for (int m = 0; m < pl.tiles; ++m) {
-            const int r = m * kTileRows + quarter * 32 + lane;
-            if (m * kTileRows + quarter * 32 >= a.R) continue;
-            for (int j0 = 0; j0 < n16; j0 += 16) {
-                uint32_t v[16];
-                tc5::ld16(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(m * a.nb + j0), v);
-                tc5::wait_ld();
-                if (r >= a.R) continue;
-#pragma unroll
-                for (int u = 0; u < 16; ++u) {
-                    if (j0 + u >= n) break;
-                    if (S == 1)
-                        put(j0 + u, r, __uint_as_float(v[u]));
-                    else
-                        sums[(j0 + u) * a.R + r] = __uint_as_float(v[u]);
-                }
-            }
-        }
+    // the sums of rows first(q) .. first(q + 1) are joined by CTA q, its shared memory holds
+    // [slice][row][R] over the ring
+    __shared__ uint32_t goes_to[kTileRows];   // cluster address of row j's sums of this slice
+    auto first = [&](int q) { return n * q / S; };
+    const int cols = (n + S - 1) / S;
+    if (S > 1 && (int)threadIdx.x < n) {
+        const int j = threadIdx.x;
+        int q = j * S / n;
+        while (j >= first(q + 1)) ++q;   // fewer rows than slices: some own none
+        goes_to[j] = tc5::at_cta(base + (uint32_t)((rank * cols + j - first(q)) * a.R * 4), (uint32_t)q);
     }
     tc5::fence_before();
     __syncthreads();
@@ -230,18 +258,36 @@ __global__ void __launch_bounds__(kRowsThreads) rows_kernel(const RowsArgs a, co
         for (const long long c0 = clock64(); clock64() - c0 < kLandCycles;) __nanosleep(1000);
     tc5::fence_after();
     if (warp == 1) tc5::dealloc<false>(tmem, pl.tmem_cols);
-    if (S > 1) {
-        tc5::cluster_sync();   // every slice's sums are written
-        if (live && !aborted[0]) {
-            // this CTA's share of the rows, slices added in rank order
-            const int j0 = n * rank / S, j1 = n * (rank + 1) / S;
-            for (int i = j0 * a.R + (int)threadIdx.x; i < j1 * a.R; i += kRowsThreads) {
-                float v = 0.0f;
-                for (int s = 0; s < S; ++s) v += ld_cluster(tc5::at_cta(base + (uint32_t)i * 4u, (uint32_t)s));
-                put(i / a.R, i % a.R, v);
+    if (S > 1) tc5::cluster_sync();   // nobody's ring is in use any more
+    if (live && !aborted[0] && warp >= 2) {
+#pragma unroll
+        for (int i = 0; i < G2; ++i) {
+            const int g = 2 * i + half, r = g / per * kTileRows + quarter * 32 + lane, j0 = g % per * 16;
+            if (g >= groups || r >= a.R) continue;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const int j = j0 + u;
+                if (j >= n) break;
+                if (S == 1)
+                    put(j, r, sum[i][u]);
+                else
+                    st_cluster(goes_to[j] + (uint32_t)r * 4u, sum[i][u]);
             }
         }
-        tc5::cluster_sync();   // and read
+    }
+    __syncwarp();
+    if (S > 1) {
+        tc5::cluster_sync();
+        if (live && !aborted[0]) {
+            const float* got = reinterpret_cast<const float*>(smem);
+            const int j0 = first(rank), mine = first(rank + 1) - j0, slice = cols * a.R;
+            for (int j = warp; j < mine; j += kRowsThreads / 32)
+                for (int r = lane; r < a.R; r += 32) {
+                    float v = got[j * a.R + r];
+                    for (int s = 1; s < S; ++s) v += got[s * slice + j * a.R + r];   // in rank order
+                    put(j0 + j, r, v);
+                }
+        }
     }
 }
 
@@ -271,10 +317,15 @@ int rows_stage(int R, int nb) { return (R + nb) * 128; }
 
 }  // namespace
 
+int rows_block(int R) {
+    const int tiles = (R + kTileRows - 1) / kTileRows;
+    return tiles == 1 ? 128 : tiles <= 3 ? 64 : 32;
+}
+
 int rows_splits(int R, int nb, int steps, int64_t items, int want) {
     int s = 1;
     while (s < 8 && items * s * 2 <= want && steps / (s * 2) >= 4) s *= 2;
-    return (size_t)R * nb * 4 <= ring_room(rows_stage((R + 7) / 8 * 8, nb)) ? s : 1;
+    return (size_t)R * (nb + 8) * 4 <= ring_room(rows_stage((R + 127) / 128 * 128, nb)) ? s : 1;
 }
 
 cudaError_t launch_rows(const RowsArgs& a, bool pdl, cudaStream_t st) {
@@ -288,17 +339,19 @@ cudaError_t launch_rows(const RowsArgs& a, bool pdl, cudaStream_t st) {
     if (pl.stages > kMaxStages) pl.stages = kMaxStages;
     if (pl.stages < 2) return cudaErrorInvalidConfiguration;
     pl.tmem_cols = 32;
-    while (pl.tmem_cols < (uint32_t)(pl.tiles * a.nb)) pl.tmem_cols *= 2;
-    if (pl.tmem_cols > 512) return cudaErrorInvalidConfiguration;
+    while (pl.tmem_cols < (uint32_t)(2 * pl.tiles * a.nb)) pl.tmem_cols *= 2;
+    const int groups = pl.tiles * a.nb / 16;
+    if (groups > 12) return cudaErrorInvalidConfiguration;
     size_t ring = (size_t)pl.stages * pl.stage;
-    const size_t join = a.splits > 1 ? (size_t)a.R * a.nb * 4 : 0;
+    const size_t join = a.splits > 1 ? (size_t)a.R * (a.nb + 8) * 4 : 0;
     if (join > room) return cudaErrorInvalidConfiguration;
     if (ring + kOverrun < join) ring = join - kOverrun;
     const size_t smem = kFixed + kOverrun + ring;
     RowsMaps maps{};
     if (!rows_map(&maps.w, a.W, a.w_rows, a.K, a.K, pl.w_rows) || !rows_map(&maps.x, a.x, a.x_rows, a.K, a.x_stride, gather ? 1 : a.nb))
         return cudaErrorInvalidValue;
-    void (*kern)(RowsArgs, RowsPlan, RowsMaps) = gather ? rows_kernel<true> : rows_kernel<false>;
+    void (*kern)(RowsArgs, RowsPlan, RowsMaps) = groups <= 8 ? (gather ? rows_kernel<true, 4> : rows_kernel<false, 4>)
+                                                             : (gather ? rows_kernel<true, 6> : rows_kernel<false, 6>);
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmemMost);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -26,11 +26,14 @@ struct RowsArgs {
     // adapters (nblocks not null): item = block of the plan, out [P, R]
     const int32_t* nblocks;
     const int32_t* block_slot;
-    const int32_t* rows;     // [blocks, nb], a prefix; -1: none
+    const int32_t* rows;     // [blocks, block_rows], a prefix; -1: none
+    int block_rows;          // a multiple of nb: an item is nb of a block's rows
     int div;
     int* err;
 };
 
+// Rows of x that an item of R weight rows (at most 512) may hold.
+int rows_block(int R);
 // The largest split of K whose join fits the shared memory, at most `want`; wanted where items are few.
 int rows_splits(int R, int nb, int steps, int64_t items, int want);
 cudaError_t launch_rows(const RowsArgs& a, bool pdl, cudaStream_t st);

@@ -4,12 +4,9 @@
 // up to 16 rows a matrix-instruction tile, so a slot's weights are read once a block.
 //   plan   (more than kFewPairs pairs) the blocks: a counting sort of the pairs by slot.  With few
 //          pairs every CTA of the two kernels finds the blocks itself, which costs less than a launch.
-//   down   v, a block's rows times the slot's A.  An item is (block, up to 64 rows of A, K slice); the eight
-//          warps of a CTA take every eighth 32 columns of the slice straight from global memory into the
-//          fragments of warp-level matrix instructions (the k order inside a step is whatever puts a
-//          lane's own 16 bytes into its slots, the same for both operands) and add their sums up
-//          through shared memory.  K slices are partial sums in the workspace, so that few blocks
-//          fill the GPU.
+//   down   v, a block's rows times the slot's A: thin products (chord_thin.cuh), an item is (up to 64
+//          rows of a block, up to 64 rows of A, K slice).  K slices are partial sums in the workspace, as many as
+//          fill the GPU; both kernels work the number out from the number of blocks.
 //   up     y, an item is (block, columns).  The slices of v are added in order, scaled and split into three
 //          bf16 parts of eight bits each, so the tensor cores multiply all of an FP32 v.  The
 //          columns of a 32-column tile are dealt so that a lane ends with eight neighbouring ones:
@@ -22,16 +19,16 @@
 
 #include "chord_common.cuh"
 #include "chord_internal.h"
-#include "chord_rows.cuh"
+#include "chord_thin.cuh"
 
 namespace chord {
 namespace {
 
 constexpr int kFewPairs = 256;
-constexpr int kFewRows = 16, kManyRows = 128;   // rows of a block
-constexpr int kThreads = 256, kWarps = 8;
+constexpr int kFewRows = 16, kManyRows = 64;   // rows of a block
+constexpr int kThreads = thin::kThreads, kWarps = thin::kWarps;
 constexpr int kMaxSplit = 16;
-constexpr int kTargetCtas = 304;
+constexpr int64_t kSplitRows = 16384;          // K slices times pairs, at most, where there is more than one slice
 constexpr int kNone = -2;                      // slot of a pair that is not touched; -1: its row of y is base's
 
 struct AdapterArgs {
@@ -49,8 +46,9 @@ struct AdapterArgs {
     void* y;
     int64_t base_stride, y_stride;
     int copy;                     // rows without an adapter are copied from base
-    int splits;                   // K slices
-    float* v;                     // [splits, P, R]
+    int units;                    // items of a block and K slice
+    int max_splits, target;       // K slices: as many as make `target` items
+    float* v;                     // [slices, P, R]
     // the plan, for more than kFewPairs pairs
     int32_t* nblocks;
     int32_t* block_slot;
@@ -124,96 +122,55 @@ __device__ __forceinline__ int block_rows(const AdapterArgs& g, const FewBlocks*
     return slot;
 }
 
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// K slices of a call with n blocks.
+__device__ __forceinline__ int slices_of(const AdapterArgs& g, int n) {
+    const int64_t items = (int64_t)n * g.units;
+    return items >= g.target ? 1 : max(1, min(g.max_splits, (int)((g.target + items - 1) / max(items, (int64_t)1))));
 }
 
 // ---- v = A x --------------------------------------------------------------------
-// MT tiles of 16 rows, NT tiles of eight rows of A.  Chains of matrix instructions end after kChain steps of
-// 32 columns, their additions chop.
-constexpr int kChain = 24;
-
-template <int NT>
+template <int MT, int NT, bool FEW>
 __global__ void __launch_bounds__(kThreads) adapter_down_kernel(const AdapterArgs g) {
-    constexpr int MT = 1, MB = kFewRows, NB = NT * 8;
-    extern __shared__ __align__(16) float red[];   // [kWarps][MB][NB]
+    using Warp = thin::Warp<MT, NT>;
+    constexpr int MB = FEW ? kFewRows : kManyRows, MR = Warp::kRows, NB = Warp::kCols, SUB = MB / MR;
+    extern __shared__ __align__(16) float red[];   // [kWarps][MR][NB]
     __shared__ int32_t rows[MB];
     __shared__ FewBlocks few[1];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2;
     pdl_trigger();
-    find_blocks(g, few[0], blockIdx.x == 0);
-    const int n = few[0].n;
-    const int chunks = (g.R + NB - 1) / NB, per = chunks * g.splits, steps = (g.K + 31) / 32;
+    int n;
+    if constexpr (FEW) {
+        find_blocks(g, few[0], blockIdx.x == 0);
+        n = few[0].n;
+    } else {
+        pdl_wait();
+        n = *g.nblocks;
+    }
+    const int splits = slices_of(g, n), chunks = (g.R + NB - 1) / NB, per = SUB * chunks * splits, steps = (g.K + thin::kStep - 1) / thin::kStep;
     for (int64_t i = blockIdx.x; i < (int64_t)n * per; i += gridDim.x) {
         int q;
         const int b = (int)divmod_idx(i, per, q);
-        const int r0 = q / g.splits * NB, split = q % g.splits;
-        const int slot = block_rows<true, MB>(g, few, b, rows);
-        if (slot < 0) continue;
-        const int k_first = (int)((int64_t)split * steps / g.splits), k_last = (int)((int64_t)(split + 1) * steps / g.splits);
-        const __nv_bfloat16* xr[2 * MT];
+        const int split = q % splits, r0 = q / splits % chunks * NB, sub = q / (splits * chunks);
+        const int slot = block_rows<FEW, MB>(g, few, b, rows);
+        const int32_t* mine = rows + sub * MR;
+        if (slot < 0 || mine[0] < 0) continue;   // a block's rows are a prefix
+        Warp w;
+        w.x = reinterpret_cast<const uint4*>(g.x);
+        w.pieces = g.K / 8;
+        w.wstep = (int64_t)g.K;                  // eight rows of K / 8 pieces
+        w.w = reinterpret_cast<const uint4*>(g.A) + ((int64_t)slot * g.R + r0 + gr) * w.pieces;
+        w.wrows = (g.R - r0 - gr + 7) / 8;
 #pragma unroll
         for (int j = 0; j < 2 * MT; ++j) {
-            const int p = rows[j * 8 + gr];
-            xr[j] = p < 0 ? nullptr : g.x + (int64_t)(g.div == 1 ? p : p / g.div) * g.x_stride + 8 * c;
+            const int p = mine[j * 8 + gr];
+            w.xrow[j] = p < 0 ? thin::kNoRow : (uint32_t)((int64_t)(g.div == 1 ? p : p / g.div) * (g.x_stride / 8));
         }
-        const __nv_bfloat16* ar[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int r = r0 + j * 8 + gr;
-            ar[j] = r < g.R ? g.A + ((int64_t)slot * g.R + r) * g.K + 8 * c : nullptr;
-        }
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        float* mine = red + (warp * MB + gr) * NB + 2 * c;
-        int ks = k_first + warp;
-        for (bool more = false; !more || ks < k_last; more = true) {
-            float acc[MT][NT][4];
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) acc[m][t][u] = 0.0f;
-            for (int chain_end = min(k_last, ks + kChain * kWarps); ks < chain_end; ks += kWarps) {
-                const int k = ks * 32;
-                const bool in = k + 8 * c < g.K;
-                uint4 xa[2 * MT], wb[NT];
-#pragma unroll
-                for (int j = 0; j < 2 * MT; ++j) xa[j] = in && xr[j] ? *reinterpret_cast<const uint4*>(xr[j] + k) : zero;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) wb[j] = in && ar[j] ? *reinterpret_cast<const uint4*>(ar[j] + k) : zero;
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        mma(acc[m][t], xa[2 * m].x, xa[2 * m + 1].x, xa[2 * m].y, xa[2 * m + 1].y, wb[t].x, wb[t].y);
-                        mma(acc[m][t], xa[2 * m].z, xa[2 * m + 1].z, xa[2 * m].w, xa[2 * m + 1].w, wb[t].z, wb[t].w);
-                    }
-            }
-            // the warp's own place; a further chain is added to what it holds
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float2* to = reinterpret_cast<float2*>(mine + (m * 16 + h * 8) * NB + t * 8);
-                        float2 o = make_float2(acc[m][t][2 * h], acc[m][t][2 * h + 1]);
-                        if (more) o.x += to->x, o.y += to->y;
-                        *to = o;
-                    }
-        }
+        const int k0 = (int)((int64_t)split * steps / splits), k1 = (int)((int64_t)(split + 1) * steps / splits);
+        w.run(k0 + warp, k1, red + warp * MR * NB, false);
         __syncthreads();
-        for (int u = threadIdx.x; u < MB * NB; u += kThreads) {
-            const int p = rows[u / NB], r = r0 + u % NB;
-            if (p < 0 || r >= g.R) continue;
-            float s = red[u];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) s += red[w * MB * NB + u];
-            g.v[((int64_t)split * g.P + p) * g.R + r] = s;
+        for (int u = threadIdx.x; u < MR * NB; u += kThreads) {
+            const int p = mine[u / NB], r = r0 + u % NB;
+            if (p >= 0 && r < g.R) g.v[((int64_t)split * g.P + p) * g.R + r] = thin::joined(red, MR * NB, u);
         }
     }
 }
@@ -286,6 +243,7 @@ __global__ void __launch_bounds__(kThreads) adapter_up_kernel(const AdapterArgs 
     } else {
         n = *g.nblocks;
     }
+    const int splits = slices_of(g, n);
     const int Np = g.N / g.parts, tiles = (Np + 31) / 32;          // 32-column tiles of a part
     const int ksp = (g.rank + 15) / 16, ks = ksp * g.parts;        // 16-wide steps of a part, of all
     const int groups = (tiles * g.parts + cols - 1) / cols;        // items of a block: `cols` tiles each
@@ -305,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) adapter_up_kernel(const AdapterArgs 
                 if (p >= 0 && kq < quads) {
                     const float* from = g.v + (int64_t)p * g.R + part * g.rank + kq * 4;
                     f = *reinterpret_cast<const float4*>(from);
-                    for (int s = 1; s < g.splits; ++s) {
+                    for (int s = 1; s < splits; ++s) {
                         const float4 o = *reinterpret_cast<const float4*>(from + (int64_t)s * g.P * g.R);
                         f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
                     }
@@ -359,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) adapter_up_kernel(const AdapterArgs 
                         for (int t3 = 2; t3 >= 0; --t3) {
                             const uint4 a = *reinterpret_cast<const uint4*>(frag + (((m * ks + part * ksp + s) * 3 + t3) * 32 + lane) * 4);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) mma(acc[m][j], a.x, a.y, a.z, a.w, w[j].x, w[j].y);
+                            for (int j = 0; j < 4; ++j) thin::mma(acc[m][j], a.x, a.y, a.z, a.w, w[j].x, w[j].y);
                         }
                 }
 #pragma unroll
@@ -468,29 +426,24 @@ __global__ void __launch_bounds__(256) adapter_place_kernel(const PlanArgs a) {
 constexpr int kPlanPairs = 16384, kPlanSlots = 16384;
 
 struct Layout {
-    int splits;
+    int max_splits;
     int64_t blocks;   // at most
     size_t v, nblocks, block_slot, rows, counts, bytes;
 };
 
-// K slices: with fewer items than CTAs that the GPU holds, K is cut until they are as many.  A block holds at
-// least one pair, few blocks more than one in sixteen of a full one.
-Layout layout_of(int64_t P, int64_t slots, int R, int K) {
+Layout layout_of(int64_t P, int64_t slots, int R) {
     Layout l{};
     const bool few = P <= kFewPairs;
     const int64_t mb = few ? kFewRows : kManyRows;
     l.blocks = P / mb + (P < slots + 1 ? P : slots + 1) + 1;
-    const int64_t items = (P < slots ? P : slots) * ((R + 63) / 64);
-    int64_t s = few && items > 0 ? (kTargetCtas + items - 1) / items : 1;
-    if (s > kMaxSplit) s = kMaxSplit;
-    if (K > 0 && s > (K + 255) / 256) s = (K + 255) / 256;   // a step of 32 columns for each warp
-    l.splits = (int)(s < 1 ? 1 : s);
+    const int64_t s = P > 0 ? kSplitRows / P : 1;
+    l.max_splits = (int)(s > kMaxSplit ? kMaxSplit : s < 1 ? 1 : s);
     auto take = [&](size_t n) {
         const size_t at = l.bytes;
         l.bytes += (n + 255) / 256 * 256;
         return at;
     };
-    l.v = take((size_t)l.splits * P * R * 4);
+    l.v = take((size_t)l.max_splits * P * R * 4);
     if (!few) {
         l.nblocks = take(4);
         l.block_slot = take((size_t)l.blocks * 4);
@@ -500,37 +453,35 @@ Layout layout_of(int64_t P, int64_t slots, int R, int K) {
     return l;
 }
 
-template <int NT>
+// Tile of the first half: all of a block's rows and of A's where registers hold a step ahead, 32 rows for 64 of A.
+struct DownTile {
+    int rows, cols;
+};
+DownTile down_tile(int R, bool few) {
+    const int cols = R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64;
+    return {few ? kFewRows : cols == 64 ? 32 : 64, cols};
+}
+
+template <int MT, int NT, bool FEW>
 cudaError_t launch_down_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
-    auto* kern = adapter_down_kernel<NT>;
-    const size_t smem = (size_t)kWarps * kFewRows * NT * 8 * 4;
+    auto* kern = adapter_down_kernel<MT, NT, FEW>;
+    const size_t smem = (size_t)kWarps * MT * 16 * NT * 8 * 4;
     int ctas = 0;
     cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
     if (e != cudaSuccess) return e;
-    const int64_t items = blocks * ((g.R + NT * 8 - 1) / (NT * 8)) * g.splits, most = (int64_t)device_info().sm_count * ctas;
-    kern<<<(unsigned)(items < most ? items : most), kThreads, smem, st>>>(g);
-    return cudaGetLastError();
+    const int64_t items = blocks * g.units * g.max_splits, most = (int64_t)device_info().sm_count * ctas;
+    return launch_pdl(!FEW && pdl_enabled(), kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g);
 }
 
+template <bool FEW>
 cudaError_t launch_down(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
-    if (g.R <= 8) return launch_down_as<1>(g, blocks, st);
-    if (g.R <= 16) return launch_down_as<2>(g, blocks, st);
-    if (g.R <= 32) return launch_down_as<4>(g, blocks, st);
-    return launch_down_as<8>(g, blocks, st);
-}
-
-// The plan's blocks, on the tcgen05 kernel that the router's logits use.
-cudaError_t launch_down_many(const AdapterArgs& g, int64_t blocks, int64_t slots, int64_t x_rows, cudaStream_t st) {
-    RowsArgs r{};
-    r.x = g.x, r.x_rows = x_rows, r.x_stride = g.x_stride;
-    r.W = g.A, r.w_rows = slots * g.R, r.K = g.K, r.parts = 1;
-    r.R = g.R, r.nb = rows_block(g.R), r.block_rows = kManyRows, r.items = blocks * (kManyRows / r.nb);
-    r.out = g.v, r.nblocks = g.nblocks, r.block_slot = g.block_slot, r.rows = g.rows, r.div = g.div, r.err = g.err;
-    // blocks that hold rows: at least P / 128, of many slots perhaps half
-    int64_t likely = ceil_div64(g.P, kManyRows);
-    if (likely < (g.P < slots ? g.P : slots) / 2) likely = (g.P < slots ? g.P : slots) / 2;
-    r.splits = rows_splits(g.R, r.nb, (g.K + 63) / 64, likely * (kManyRows / r.nb), kTargetCtas);
-    return launch_rows(r, pdl_enabled(), st);
+    constexpr int MT = FEW ? 1 : 4;
+    switch (down_tile(g.R, FEW).cols) {
+        case 8: return launch_down_as<MT, 1, FEW>(g, blocks, st);
+        case 16: return launch_down_as<MT, 2, FEW>(g, blocks, st);
+        case 32: return launch_down_as<MT, 4, FEW>(g, blocks, st);
+        default: return launch_down_as<FEW ? 1 : 2, 8, FEW>(g, blocks, st);
+    }
 }
 
 template <int MT, bool F32, bool FEW>
@@ -594,7 +545,7 @@ extern "C" {
 size_t chord_adapter_workspace_bytes(int64_t T, int topk, int adapters, int E, int rank, int parts) {
     if (T < 0 || topk <= 0 || adapters <= 0 || E <= 0 || rank <= 0 || parts <= 0 || rank > 128 || parts > 4) return 0;
     if (T > INT32_MAX / topk || adapters > 65536 / E) return 0;
-    const size_t bytes = layout_of(T * topk, (int64_t)adapters * E, rank * parts, 0).bytes;
+    const size_t bytes = layout_of(T * topk, (int64_t)adapters * E, rank * parts).bytes;
     return bytes ? bytes : 256;
 }
 
@@ -610,6 +561,8 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     const int per = y_dtype == CHORD_DTYPE_F32 ? 4 : 8;
     if (P >= INT32_MAX || adapters > 65536 / E || rank % 8 || rank > 128 || parts > 4 || N % (8 * parts) || K % 8)
         return CHORD_ERR_UNSUPPORTED;
+    if (x_rows > 0 && x_stride > 0 && x_rows > (INT64_MAX >> 2) / x_stride) return CHORD_ERR_INVALID_ARG;
+    if (x_rows * (x_stride / 8) >= INT64_C(0xffffffff)) return CHORD_ERR_UNSUPPORTED;   // 16-byte pieces of x in 32 bits
     if (!topk_ids && E != 1) return CHORD_ERR_INVALID_ARG;
     if (P == 0) return CHORD_OK;
     if ((P - 1) / a_row_divisor >= x_rows) return CHORD_ERR_INVALID_ARG;
@@ -631,21 +584,25 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     if (!di.err) return CHORD_ERR_CUDA;
     const int64_t slots = (int64_t)adapters * E;
     const bool few = P <= kFewPairs, f32 = y_dtype == CHORD_DTYPE_F32;
-    const Layout l = layout_of(P, slots, rank * parts, K);
+    const Layout l = layout_of(P, slots, rank * parts);
+    const DownTile tile = down_tile(rank * parts, few);
+    const int units = (few ? kFewRows : kManyRows) / tile.rows * ((rank * parts + tile.cols - 1) / tile.cols);
+    const int most = (K + thin::kStep * kWarps - 1) / (thin::kStep * kWarps);   // slices with a step for every warp
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     AdapterArgs g{static_cast<const __nv_bfloat16*>(x), x_stride, a_row_divisor, adapter_ids, topk_ids, (int)P, topk, adapters, E,
                   static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, rank, parts, rank * parts, N, K,
-                  base, y, base_stride, y_stride, base != y, l.splits, reinterpret_cast<float*>(ws + l.v),
+                  base, y, base_stride, y_stride, base != y, units, l.max_splits < most ? l.max_splits : most, 2 * di.sm_count,
+                  reinterpret_cast<float*>(ws + l.v),
                   reinterpret_cast<int32_t*>(ws + l.nblocks), reinterpret_cast<int32_t*>(ws + l.block_slot),
                   reinterpret_cast<int32_t*>(ws + l.rows), di.err};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (few) {
-        e = launch_down(g, l.blocks, st);
+        e = launch_down<true>(g, l.blocks, st);
         if (e == cudaSuccess) e = launch_up<true>(g, l.blocks, f32, st);
     } else {
         e = launch_plan(g, slots, reinterpret_cast<int32_t*>(ws + l.counts), st);
-        if (e == cudaSuccess) e = launch_down_many(g, l.blocks, slots, x_rows, st);
+        if (e == cudaSuccess) e = launch_down<false>(g, l.blocks, st);
         if (e == cudaSuccess) e = launch_up<false>(g, l.blocks, f32, st);
     }
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;

@@ -1,11 +1,13 @@
 // Router logits: bf16 activations times the router's weights, FP32 sums and result.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "chord_common.cuh"
 #include "chord_internal.h"
-#include "chord_rows.cuh"
+#include "chord_tcgen05.cuh"
+#include "chord_thin.cuh"
 
 namespace chord {
 namespace {
@@ -19,24 +21,355 @@ struct LogitArgs {
     float* out;
 };
 
-constexpr int kFewTokens = 16;
+// ---- few tokens: thin products ------------------------------------------------------------
+// A CTA takes MT x 16 tokens, NT x 8 experts and a slice of K (of all parts, one behind the other, the
+// smallest numbers first); the slices of a tile are a cluster.  Each CTA adds its warps' sums up and
+// pushes every CTA the share of the tile that it joins, in rank order.
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 
-// A warp per logit.
-__global__ void __launch_bounds__(256) logits_kernel(const LogitArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t n = (int64_t)a.T * a.E;
-    for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += (int64_t)gridDim.x * 8) {
-        int e;
-        const int64_t t = divmod_idx(i, a.E, e);
-        float sum = 0.0f;
-        for (int p = a.parts - 1; p >= 0; --p) {
-            const __nv_bfloat16* w = a.W + ((int64_t)p * a.E + e) * a.H;
-            const __nv_bfloat16* x = a.x + t * a.stride;
-            for (int k = lane; k < a.H; k += 32) sum = fmaf(__bfloat162float(x[k]), __bfloat162float(w[k]), sum);
-        }
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) a.out[i] = sum;
+template <int MT, int NT>
+__global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const LogitArgs a, int splits) {
+    using Warp = thin::Warp<MT, NT>;
+    constexpr int kTile = Warp::kRows * Warp::kCols;
+    extern __shared__ __align__(16) float red[];   // [kWarps][kTile], then the shares [slice][share]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2;
+    pdl_trigger();
+    pdl_wait();
+    const int rank = splits > 1 ? (int)tc5::cluster_rank() : 0;
+    const int etiles = (a.E + Warp::kCols - 1) / Warp::kCols;
+    int et;
+    const int64_t t0 = divmod_idx(blockIdx.x / splits, etiles, et) * Warp::kRows;
+    const int e0 = et * Warp::kCols;
+    Warp w;
+    w.x = reinterpret_cast<const uint4*>(a.x + t0 * a.stride);
+    w.pieces = a.H / 8;
+    w.wstep = a.H;
+    w.wrows = (a.E - e0 - gr + 7) / 8;
+#pragma unroll
+    for (int j = 0; j < 2 * MT; ++j) w.xrow[j] = t0 + j * 8 + gr < a.T ? (uint32_t)((j * 8 + gr) * (a.stride / 8)) : thin::kNoRow;
+    const int steps1 = (a.H + thin::kStep - 1) / thin::kStep;
+    const int64_t steps = (int64_t)steps1 * a.parts;
+    const int k0 = (int)(rank * steps / splits), k1 = (int)((rank + 1) * steps / splits);
+    float* mine = red + warp * kTile;
+    bool more = false;
+    for (int part = k0 / steps1; part * steps1 < k1; ++part) {
+        w.w = reinterpret_cast<const uint4*>(a.W + ((int64_t)(a.parts - 1 - part) * a.E + e0 + gr) * a.H);
+        const int first = max(k0 - part * steps1, 0), last = min(k1 - part * steps1, steps1);
+        w.run(first + warp, last, mine, more);
+        more = true;
     }
+    auto put = [&](int i, float v) {
+        const int64_t t = t0 + i / Warp::kCols;
+        const int e = e0 + i % Warp::kCols;
+        if (t < a.T && e < a.E) a.out[t * a.E + e] = v;
+    };
+    __syncthreads();
+    if (splits == 1) {
+        for (int i = threadIdx.x; i < kTile; i += thin::kThreads) put(i, thin::joined(red, kTile, i));
+        return;
+    }
+    float* shares = red + thin::kWarps * kTile;
+    const int share = kTile / splits;   // a power of two, as splits is
+    tc5::cluster_sync();                // every CTA of the cluster runs
+    for (int i = threadIdx.x; i < kTile; i += thin::kThreads) {
+        const uint32_t to = smem_u32(shares + rank * share + i % share);
+        st_cluster(tc5::at_cta(to, (uint32_t)(i / share)), thin::joined(red, kTile, i));
+    }
+    tc5::cluster_sync();
+    for (int i = threadIdx.x; i < share; i += thin::kThreads) {
+        float v = shares[i];
+        for (int s = 1; s < splits; ++s) v += shares[s * share + i];
+        put(rank * share + i, v);
+    }
+}
+
+template <int MT, int NT>
+cudaError_t launch_thin(const LogitArgs& a, cudaStream_t st) {
+    using Warp = thin::Warp<MT, NT>;
+    auto* kern = logits_thin_kernel<MT, NT>;
+    const size_t smem = (size_t)(thin::kWarps + 1) * Warp::kRows * Warp::kCols * 4;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = ceil_div64(a.T, Warp::kRows) * ((a.E + Warp::kCols - 1) / Warp::kCols);
+    const int64_t steps = ceil_div64(a.H, thin::kStep) * a.parts;
+    // K is cut until every SM has a CTA, as long as each warp keeps two steps
+    int splits = 1;
+    while (splits < 8 && tiles * splits < device_info().sm_count && steps >= 2 * thin::kWarps * 2 * splits) splits *= 2;
+    if (tiles * splits > INT32_MAX) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * splits));
+    cfg.blockDim = dim3(thin::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (splits > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)splits;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl_enabled()) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kern, a, splits);
+}
+
+// ---- many tokens: tcgen05 -------------------------------------------------------------------
+// A pair of CTAs computes 256 tokens times N experts (cta_group::2, M = 256): each CTA copies its 128
+// tokens and half of the experts' rows, so a CTA's copies are 128 + N / 2 rows for 128 x N sums.  Roles
+// in each CTA: a copying warp (stages of 128 columns, two swizzled tiles of 64; both CTAs' bytes
+// are counted on the first one's barrier), in the first CTA an issuing warp, and eight warps that read the
+// accumulators.  The instructions' additions chop, so a chain is 256 columns (16 instructions) and
+// the eight warps add the chains up in registers, one accumulator being read while the other is filled
+// (relative error of a K = 7168 sum: 3.8e-6 in chains of 224, 2.5e-7 so, 9e-7 of PyTorch's FP32).
+// Bound by the copies from L2.
+constexpr int kReaders = 8, kWideThreads = (kReaders + 2) * 32;
+constexpr int kHalfCols = 64, kStageCols = 2 * kHalfCols;
+constexpr int kPairTokens = 256;
+constexpr int kWideTokens = 768;   // from here on
+constexpr int kChainStages = 2;
+constexpr int kMaxWideStages = 6;
+constexpr long long kLandCycles = 4000000;   // about 2 ms
+constexpr size_t kWideSmem = 225 * 1024;     // dynamic, 1 KB of it alignment; the barriers are static
+
+struct WideMaps {
+    CUtensorMap x, w;
+};
+
+struct WidePlan {
+    int groups, N;   // groups of N experts
+    int stages;
+};
+
+__device__ __forceinline__ void box_g2s_pair(uint32_t dst, const void* map, int col, int row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(map), "r"(col), "r"(row), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// G: groups of 16 accumulator columns that each reading warp adds up.
+template <int G>
+__global__ void __launch_bounds__(kWideThreads, 1) logits_wide_kernel(const LogitArgs a, const WidePlan pl, int* err, const __grid_constant__ WideMaps maps) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = smem_u32(smem_raw) + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ uint64_t full[kMaxWideStages], empty[kMaxWideStages], acc_full[2], acc_empty[2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int flag[1];   // abort
+    volatile int* aborted = flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc5::cluster_rank();
+    if (warp == kReaders) tc5::alloc<true>(&tmem_slot, 512);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMaxWideStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&acc_full[s], 1);
+            mbar_init(&acc_empty[s], 2 * kReaders);
+        }
+        flag[0] = 0;
+        fence_barrier_init();
+    }
+    pdl_wait();
+    tc5::fence_before();
+    __syncthreads();
+    tc5::cluster_sync();   // the barriers are initialised before the other CTA's arrivals reach them
+    tc5::fence_after();
+    pdl_trigger();         // not before this CTA has its tensor memory
+    const uint32_t tmem = tmem_slot;
+    int grp;
+    const int64_t t0 = divmod_idx(blockIdx.x >> 1, pl.groups, grp) * kPairTokens + rank * 128;
+    const int e0 = grp * pl.N, N = pl.N;
+    const int steps1 = (a.H + kStageCols - 1) / kStageCols, steps = steps1 * a.parts;
+    const uint32_t w_half = (uint32_t)(N / 2) * 128u, x_half = 128u * 128u, stage = 2u * (x_half + w_half);
+    bool ok = true;
+    if (warp == kReaders) {
+        tc5::Ring ring;
+        int part = 0, k = 0;
+        for (int s = 0; s < steps; ++s) {
+            if (s >= pl.stages) ok = tc5::wait<false, true>(&empty[ring.slot], ring.phase ^ 1u, aborted, err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t st = base + (uint32_t)ring.slot * stage, bar = smem_u32(&full[ring.slot]);
+            // the part with the smallest numbers first
+            const int row = (a.parts - 1 - part) * a.E + e0 + (int)rank * (N / 2), col = k * kStageCols;
+            if (tc5::elect()) {
+                if (!rank) tc5::arrive_expect_tx(bar, 2u * stage);
+                const uint32_t on = tc5::at_cta(bar, 0);
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {
+                    box_g2s_pair(st + h * x_half, &maps.x, col + (int)h * kHalfCols, (int)t0, on);
+                    box_g2s_pair(st + 2u * x_half + h * w_half, &maps.w, col + (int)h * kHalfCols, row, on);
+                }
+            }
+            __syncwarp();
+            ring.next(pl.stages);
+            if (++k == steps1) k = 0, ++part;
+        }
+    } else if (warp == kReaders + 1 && !rank) {
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kPairTokens >> 4) << 24);
+        tc5::Ring ring;
+        for (int s = 0; s < steps; ++s) {
+            const int chain = s / kChainStages, buf = chain & 1;
+            const bool first = s % kChainStages == 0, last = s + 1 == steps || (s + 1) % kChainStages == 0;
+            // the second use of an accumulator on: it has been read
+            if (first && chain >= 2) ok = tc5::wait<false, true>(&acc_empty[buf], ((uint32_t)(chain >> 1) & 1u) ^ 1u, aborted, err);
+            ok = ok && tc5::wait<false, true>(&full[ring.slot], ring.phase, aborted, err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc5::fence_after();
+            const uint32_t st = base + (uint32_t)ring.slot * stage, acc = tmem + (uint32_t)(buf * 256);
+            const uint64_t dx = tc5::desc_sw128(st), dw = tc5::desc_sw128(st + 2u * x_half);
+            if (tc5::elect()) {
+#pragma unroll
+                for (uint32_t kk = 0; kk < 8; ++kk)
+                    mma_pair(acc, dx + (kk / 4) * (x_half >> 4) + 2u * (kk % 4), dw + (uint64_t)(kk / 4) * (w_half >> 4) + 2u * (kk % 4), idesc,
+                             !first || kk > 0 ? 1u : 0u);
+                tc5::commit<true, true>(smem_u32(&empty[ring.slot]));
+                if (last) tc5::commit<true, true>(smem_u32(&acc_full[buf]));
+            }
+            __syncwarp();
+            ring.next(pl.stages);
+        }
+    } else if (warp < kReaders) {
+        const int quarter = warp & 3, half = warp >> 2, groups = N / 16;
+        float sum[G][16];
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int u = 0; u < 16; ++u) sum[i][u] = 0.0f;
+        const int chains = (steps + kChainStages - 1) / kChainStages;
+        for (int c = 0; c < chains; ++c) {
+            const int buf = c & 1;
+            ok = tc5::wait<false, true>(&acc_full[buf], (uint32_t)(c >> 1) & 1u, aborted, err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc5::fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256);
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const int g = 2 * i + half;
+                if (g >= groups) continue;
+                uint32_t v[16];
+                tc5::ld16(acc + (uint32_t)(g * 16), v);
+                tc5::wait_ld();
+#pragma unroll
+                for (int u = 0; u < 16; ++u) sum[i][u] += __uint_as_float(v[u]);
+            }
+            tc5::fence_before();
+            __syncwarp();
+            if (lane == 0) tc5::arrive_relaxed_at(smem_u32(&acc_empty[buf]), 0);
+        }
+        const int64_t t = t0 + quarter * 32 + lane;
+        if (ok && t < a.T) {
+            float* out = a.out + t * a.E;
+            const bool wide = a.E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const int g = 2 * i + half, e = e0 + g * 16;
+                if (g >= groups) continue;
+#pragma unroll
+                for (int u = 0; u < 16; u += 4) {
+                    if (wide && e + u + 3 < a.E) {
+                        *reinterpret_cast<float4*>(out + e + u) = make_float4(sum[i][u], sum[i][u + 1], sum[i][u + 2], sum[i][u + 3]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (e + u + q < a.E) out[e + u + q] = sum[i][u + q];
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+    tc5::fence_before();
+    __syncthreads();
+    // A role that gave up has made the others' last waits return at once: what is still in flight
+    // (copies into this CTA's shared memory, instructions on its tensor memory) gets its time here,
+    // before either is handed to the next CTA.
+    if (aborted[0])
+        for (const long long c0 = clock64(); clock64() - c0 < kLandCycles;) __nanosleep(1000);
+    tc5::cluster_sync();   // the pair's instructions, and arrivals on the other CTA's barriers, are done
+    tc5::fence_after();
+    if (warp == kReaders) tc5::dealloc<true>(tmem, 512);
+}
+
+// K-major boxes of 64 columns with the 128-byte swizzle; what lies outside the matrix reads as 0.
+bool rows_map(CUtensorMap* map, const void* p, int64_t rows, int cols, int64_t stride, int box) {
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        const bool found = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) == cudaSuccess;
+        return reinterpret_cast<Encode>(found && r == cudaDriverEntryPointSuccess ? f : nullptr);
+    }();
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t boxes[2] = {kHalfCols, (cuuint32_t)box}, ones[2] = {1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, boxes, ones,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Groups of experts (N a multiple of 32, at most 256, as cta_group::2 takes it): rounds of pairs times the rows a CTA copies in one.
+WidePlan wide_plan(int64_t T, int E, int pairs) {
+    WidePlan best{};
+    int64_t least = INT64_MAX;
+    for (int g = (E + 255) / 256; g <= (E + 31) / 32; ++g) {
+        const int n = ((E + g - 1) / g + 31) / 32 * 32;
+        const int64_t items = ceil_div64(T, kPairTokens) * g, cost = ceil_div64(items, pairs) * (128 + n / 2);
+        if (cost < least) {
+            least = cost;
+            best.groups = g;
+            best.N = n;
+        }
+    }
+    best.stages = (int)((kWideSmem - 1024) / ((128 + best.N / 2) * 256));
+    if (best.stages > kMaxWideStages) best.stages = kMaxWideStages;
+    return best;
+}
+
+cudaError_t launch_wide(const LogitArgs& a, int* err, cudaStream_t st) {
+    const WidePlan pl = wide_plan(a.T, a.E, device_info().sm_count / 2);
+    const int64_t items = ceil_div64(a.T, kPairTokens) * pl.groups;
+    WideMaps maps{};
+    if (items > INT32_MAX / 2 || !rows_map(&maps.x, a.x, a.T, a.H, a.stride, 128) ||
+        !rows_map(&maps.w, a.W, (int64_t)a.parts * a.E, a.H, a.H, pl.N / 2))
+        return cudaErrorInvalidValue;
+    auto* kern = pl.N <= 128 ? logits_wide_kernel<4> : pl.N <= 192 ? logits_wide_kernel<6> : logits_wide_kernel<8>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kWideSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * 2));
+    cfg.blockDim = dim3(kWideThreads);
+    cfg.dynamicSmemBytes = 1024 + (size_t)pl.stages * (128 + pl.N / 2) * 256;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, pl, err, maps);
 }
 
 // Eight significant bits a part, cut off towards zero: the three parts add up to the number
@@ -84,26 +417,10 @@ chord_status chord_router_logits(const void* x, int64_t x_stride, int T, const v
     if (T == 0) return CHORD_OK;
     LogitArgs a{static_cast<const __nv_bfloat16*>(x), x_stride, T, static_cast<const __nv_bfloat16*>(W), parts, E, H, logits};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (T <= kFewTokens) {
-        const int64_t blocks = ceil_div64((int64_t)T * E, 8);
-        logits_kernel<<<(unsigned)(blocks < 65536 ? blocks : 65536), 256, 0, st>>>(a);
-        return cudaGetLastError() == cudaSuccess ? CHORD_OK : CHORD_ERR_CUDA;
-    }
     const DeviceInfo& di = device_info();
     if (!di.err) return CHORD_ERR_CUDA;
-    RowsArgs r{};
-    r.x = x, r.x_rows = T, r.x_stride = T > 1 ? x_stride : H;
-    r.W = W, r.w_rows = (int64_t)parts * E, r.K = H, r.parts = parts, r.part_rows = E;
-    r.nb = T >= 64 ? 64 : (T + 15) / 16 * 16;
-    const int64_t tiles = ceil_div64(T, r.nb);
-    const int m_tiles = (E + 127) / 128;
-    // three tiles of 128 experts share the tokens' copy; fewer where that leaves SMs idle even with K cut in eight
-    r.groups = tiles * ((m_tiles + 2) / 3) * 8 < di.sm_count ? m_tiles : (m_tiles + 2) / 3;
-    r.R = ((E + r.groups - 1) / r.groups + 7) / 8 * 8;
-    r.items = tiles * r.groups;
-    r.E = E, r.out = logits, r.err = di.err;
-    r.splits = rows_splits(r.R, r.nb, (H + 63) / 64 * parts, r.items, di.sm_count);
-    if (launch_rows(r, pdl_enabled(), st) != cudaSuccess || cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;
+    const cudaError_t e = T <= 16 ? launch_thin<1, 2>(a, st) : T < kWideTokens || H < kStageCols ? launch_thin<2, 4>(a, st) : launch_wide(a, di.err, st);
+    if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;
     if (!opts || !opts->validate) return CHORD_OK;
     int32_t code = 0;
     const chord_status s = chord_get_device_error(stream, &code);

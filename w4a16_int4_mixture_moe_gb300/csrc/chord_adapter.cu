@@ -19,6 +19,7 @@
 
 #include "chord_common.cuh"
 #include "chord_internal.h"
+#include "chord_tcgen05.cuh"
 #include "chord_thin.cuh"
 
 namespace chord {
@@ -52,7 +53,8 @@ struct AdapterArgs {
     // the plan, for more than kFewPairs pairs
     int32_t* nblocks;
     int32_t* block_slot;
-    int32_t* rows;                // [blocks, kManyRows], -1: none
+    int32_t* block_count;         // rows of each block
+    int32_t* rows;                // [blocks, kManyRows]
     int* err;
 };
 
@@ -116,7 +118,7 @@ __device__ __forceinline__ int block_rows(const AdapterArgs& g, const FewBlocks*
         if (f->slot[p] == slot && at >= 0 && at < MB) rows[at] = p;
     } else {
         slot = g.block_slot[b];
-        if (threadIdx.x < MB) rows[threadIdx.x] = g.rows[(int64_t)b * MB + threadIdx.x];
+        if (threadIdx.x < MB) rows[threadIdx.x] = threadIdx.x < g.block_count[b] ? g.rows[(int64_t)b * MB + threadIdx.x] : -1;
     }
     __syncthreads();
     return slot;
@@ -155,18 +157,17 @@ __global__ void __launch_bounds__(kThreads) adapter_down_kernel(const AdapterArg
         const int32_t* mine = rows + sub * MR;
         if (slot < 0 || mine[0] < 0) continue;   // a block's rows are a prefix
         Warp w;
-        w.x = reinterpret_cast<const uint4*>(g.x);
-        w.pieces = g.K / 8;
-        w.wstep = (int64_t)g.K;                  // eight rows of K / 8 pieces
-        w.w = reinterpret_cast<const uint4*>(g.A) + ((int64_t)slot * g.R + r0 + gr) * w.pieces;
-        w.wrows = (g.R - r0 - gr + 7) / 8;
+        const int c = lane & 3;
 #pragma unroll
         for (int j = 0; j < 2 * MT; ++j) {
-            const int p = mine[j * 8 + gr];
-            w.xrow[j] = p < 0 ? thin::kNoRow : (uint32_t)((int64_t)(g.div == 1 ? p : p / g.div) * (g.x_stride / 8));
+            const int p = mine[j * 8 + gr] < 0 ? mine[0] : mine[j * 8 + gr];
+            w.x[j] = reinterpret_cast<const uint4*>(g.x + (int64_t)(g.div == 1 ? p : p / g.div) * g.x_stride) + c;
         }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            w.w[j] = reinterpret_cast<const uint4*>(g.A + ((int64_t)slot * g.R + min(r0 + j * 8 + gr, g.R - 1)) * g.K) + c;
         const int k0 = (int)((int64_t)split * steps / splits), k1 = (int)((int64_t)(split + 1) * steps / splits);
-        w.run(k0 + warp, k1, red + warp * MR * NB, false);
+        w.run(k0 + warp, k1, g.K / 8, red + warp * MR * NB, false);
         __syncthreads();
         for (int u = threadIdx.x; u < MR * NB; u += kThreads) {
             const int p = mine[u / NB], r = r0 + u % NB;
@@ -226,74 +227,97 @@ __device__ __forceinline__ void split3(float v, __nv_bfloat16 (&h)[3]) {
     }
 }
 
-// MT tiles of 16 rows; a plan's block of 64 rows is several items.
+// An item is MT x 16 rows of a block times `cols` tiles of 32 columns of one part; the eight warps take a tile each.
 template <int MT, bool F32, bool FEW>
-__global__ void __launch_bounds__(kThreads) adapter_up_kernel(const AdapterArgs g, int cols) {
+__global__ void __launch_bounds__(kThreads, 2) adapter_up_kernel(const AdapterArgs g, int cols) {
     constexpr int MB = FEW ? kFewRows : kManyRows, MR = MT * 16, SUB = MB / MR;
-    extern __shared__ __align__(16) uint32_t frag[];   // [MT][k steps][3][32][4]
+    extern __shared__ __align__(16) uint4 frag[];   // [MT][k steps of all parts][3][32]
     __shared__ int32_t rows[MB];
-    __shared__ FewBlocks few[1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
-    if constexpr (!FEW) pdl_wait();
+    FewBlocks* few = nullptr;
     int n;
     if constexpr (FEW) {
-        find_blocks(g, few[0], false);   // the ids are older than the kernel before
-        n = few[0].n;
+        __shared__ FewBlocks blocks;
+        few = &blocks;
+        find_blocks(g, blocks, false);   // the ids are older than the kernel before
+        n = blocks.n;
         pdl_wait();
     } else {
+        pdl_wait();
         n = *g.nblocks;
     }
     const int splits = slices_of(g, n);
-    const int Np = g.N / g.parts, tiles = (Np + 31) / 32;          // 32-column tiles of a part
-    const int ksp = (g.rank + 15) / 16, ks = ksp * g.parts;        // 16-wide steps of a part, of all
-    const int groups = (tiles * g.parts + cols - 1) / cols;        // items of a block: `cols` tiles each
-    for (int64_t i = blockIdx.x; i < (int64_t)n * SUB * groups; i += gridDim.x) {
+    const int Np = g.N / g.parts, tiles = (Np + 31) / 32, groups = (tiles + cols - 1) / cols;
+    const int ksp = (g.rank + 15) / 16;          // 16-wide steps of a part
+    const int per = groups * g.parts;            // items of the rows of a block
+    // column of lane group gr in tile j of a matrix instruction: the eight columns of one lane's results are 8 c ... 8 c + 7
+    const int bc = 8 * (gr >> 1) + (gr & 1);
+    for (int64_t i = blockIdx.x; i < (int64_t)n * SUB * per; i += gridDim.x) {
         int q;
-        const int bs = (int)divmod_idx(i, groups, q);
+        const int bs = (int)divmod_idx(i, per, q);
+        const int part = q / groups, t0 = (q - part * groups) * cols;
         const int slot = block_rows<FEW, MB>(g, few, bs / SUB, rows);
         const int32_t* mine = rows + bs % SUB * MR;
         if (mine[0] < 0) continue;   // rows of a block are a prefix
         if (slot >= 0) {
+            // v as the fragments of the instruction's A side: lane (g, c) has rows g and g + 8, of each k
+            // step the four columns 4 c ... (B's side likewise)
             const float scale = g.scale ? g.scale[slot / g.E] : 1.0f;
-            const int quads = g.rank / 4;
-            for (int u = threadIdx.x; u < MR * ks * 4; u += kThreads) {
-                const int row = u % MR, k4 = u / MR, part = k4 / (ksp * 4), kq = k4 % (ksp * 4);
-                const int p = mine[row];
-                float4 f = make_float4(0, 0, 0, 0);
-                if (p >= 0 && kq < quads) {
-                    const float* from = g.v + (int64_t)p * g.R + part * g.rank + kq * 4;
-                    f = *reinterpret_cast<const float4*>(from);
-                    for (int s = 1; s < splits; ++s) {
-                        const float4 o = *reinterpret_cast<const float4*>(from + (int64_t)s * g.P * g.R);
-                        f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+            for (int u = threadIdx.x; u < MT * ksp * 32; u += kThreads) {
+                const int l = u & 31, ms = u >> 5, m = ms / ksp, s = ms - m * ksp, k = 16 * s + 4 * (l & 3);
+                uint32_t r[3][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int p = mine[m * 16 + h * 8 + (l >> 2)];
+                    float4 f = make_float4(0, 0, 0, 0);
+                    if (p >= 0 && k < g.rank) {
+                        const float* from = g.v + (int64_t)p * g.R + part * g.rank + k;
+                        f = *reinterpret_cast<const float4*>(from);
+                        for (int z = 1; z < splits; ++z) {
+                            const float4 o = *reinterpret_cast<const float4*>(from + (int64_t)z * g.P * g.R);
+                            f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+                        }
+                    }
+                    __nv_bfloat16 e[4][3];
+                    split3(f.x * scale, e[0]);
+                    split3(f.y * scale, e[1]);
+                    split3(f.z * scale, e[2]);
+                    split3(f.w * scale, e[3]);
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) {
+                        r[t][h] = bf2_as_u32(__halves2bfloat162(e[0][t], e[1][t]));
+                        r[t][2 + h] = bf2_as_u32(__halves2bfloat162(e[2][t], e[3][t]));
                     }
                 }
-                __nv_bfloat16 h[4][3];
-                split3(f.x * scale, h[0]);
-                split3(f.y * scale, h[1]);
-                split3(f.z * scale, h[2]);
-                split3(f.w * scale, h[3]);
-                uint32_t* to = frag + (((row / 16 * ks + k4 / 4) * 3) * 32 + (row % 8) * 4 + k4 % 4) * 4 + row % 16 / 8;
 #pragma unroll
-                for (int t = 0; t < 3; ++t) {
-                    to[t * 128] = bf2_as_u32(__halves2bfloat162(h[0][t], h[1][t]));
-                    to[t * 128 + 2] = bf2_as_u32(__halves2bfloat162(h[2][t], h[3][t]));
-                }
+                for (int t = 0; t < 3; ++t) frag[(ms * 3 + t) * 32 + l] = make_uint4(r[t][0], r[t][1], r[t][2], r[t][3]);
             }
             __syncthreads();
         }
-        int p[2 * MT];
+        const bool two = MT > 1 && mine[(MT - 1) * 16] >= 0;   // the second 16 rows hold any
+        int64_t from[2 * MT], to[2 * MT];
+        bool live[2 * MT];
 #pragma unroll
-        for (int j = 0; j < 2 * MT; ++j) p[j] = mine[j * 8 + gr];
-        const int last = min((q + 1) * cols, tiles * g.parts);
-        for (int t = q * cols + warp; t < last; t += kWarps) {
-            const int part = t / tiles, n0 = t % tiles * 32, width = Np - n0, col = part * Np + n0 + 8 * c;
-            const bool in = 8 * c < width;
+        for (int j = 0; j < 2 * MT; ++j) {
+            const int p = mine[j * 8 + gr];
+            live[j] = p >= 0;
+            from[j] = p * g.base_stride + part * Np + 8 * c;
+            to[j] = p * g.y_stride + part * Np + 8 * c;
+        }
+        const __nv_bfloat16* b = g.B + ((int64_t)max(slot, 0) * g.N + part * Np + bc) * g.rank + 4 * c;
+        const int end = min(tiles, t0 + cols);
+        for (int t = t0 + warp; t < end; t += kWarps) {
+            const int n0 = t * 32;
+            const bool in = 8 * c < Np - n0;
             Eight<F32> o[2 * MT];
 #pragma unroll
             for (int j = 0; j < 2 * MT; ++j)
-                if (in && p[j] >= 0) o[j].load(g.base, p[j] * g.base_stride + col);
+                if (in && live[j]) o[j].load(g.base, from[j] + n0);
             if (slot >= 0) {
+                const __nv_bfloat16* bt[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bt[j] = b + (int64_t)(n0 + 2 * j) * g.rank;
+                const bool bin = bc < Np - n0;
                 float acc[MT][4][4];
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
@@ -301,24 +325,22 @@ __global__ void __launch_bounds__(kThreads) adapter_up_kernel(const AdapterArgs 
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int u = 0; u < 4; ++u) acc[m][j][u] = 0.0f;
-                // column of lane group gr in tile j: the eight columns of one lane's results are 8 c ... 8 c + 7
-                const int bc = 8 * (gr >> 1) + (gr & 1);
-                const __nv_bfloat16* b = g.B + ((int64_t)slot * g.N + part * Np + n0 + bc) * g.rank + 4 * c;
-                const bool bin = bc < width;
+#pragma unroll 4
                 for (int s = 0; s < ksp; ++s) {
                     uint2 w[4];
+                    const bool kin = bin && 16 * s + 4 * c < g.rank;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        w[j] = bin && 16 * s + 4 * c < g.rank ? *reinterpret_cast<const uint2*>(b + (int64_t)2 * j * g.rank + 16 * s)
-                                                              : make_uint2(0, 0);
+                    for (int j = 0; j < 4; ++j) w[j] = kin ? *reinterpret_cast<const uint2*>(bt[j] + 16 * s) : make_uint2(0, 0);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+                    for (int m = 0; m < MT; ++m) {
+                        if (m > 0 && !two) break;
 #pragma unroll
                         for (int t3 = 2; t3 >= 0; --t3) {
-                            const uint4 a = *reinterpret_cast<const uint4*>(frag + (((m * ks + part * ksp + s) * 3 + t3) * 32 + lane) * 4);
+                            const uint4 a = frag[((m * ksp + s) * 3 + t3) * 32 + lane];
 #pragma unroll
                             for (int j = 0; j < 4; ++j) thin::mma(acc[m][j], a.x, a.y, a.z, a.w, w[j].x, w[j].y);
                         }
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 2 * MT; ++j) {
@@ -333,7 +355,7 @@ __global__ void __launch_bounds__(kThreads) adapter_up_kernel(const AdapterArgs 
             }
 #pragma unroll
             for (int j = 0; j < 2 * MT; ++j)
-                if (in && p[j] >= 0) o[j].store(g.y, p[j] * g.y_stride + col);
+                if (in && live[j]) o[j].store(g.y, to[j] + n0);
         }
     }
 }
@@ -348,6 +370,8 @@ struct PlanArgs {
 };
 
 constexpr int kPlanThreads = 1024;
+// A cluster of kPlanCtas CTAs plans up to these; beyond, three kernels over the GPU.
+constexpr int kPlanCtas = 8, kPlanPerThread = 2, kPlanPairs = kPlanCtas * kPlanPerThread * kPlanThreads, kPlanSlots = 16384;
 
 // Exclusive sum over the threads of the CTA; every thread gets the total too.
 __device__ __forceinline__ int block_scan(int v, int& total) {
@@ -373,7 +397,7 @@ __device__ __forceinline__ int block_scan(int v, int& total) {
     return x - v + (warp ? sums[warp - 1] : 0);
 }
 
-// Counts to first positions; the blocks' slots, and -1 behind a slot's last row.
+// Counts to first positions; the blocks' slots and rows.
 __device__ __forceinline__ void plan_scan(const PlanArgs& a, int32_t* counts) {
     const int per = (a.nslots + kPlanThreads - 1) / kPlanThreads;
     const int s0 = threadIdx.x * per, s1 = min(s0 + per, a.nslots);
@@ -381,54 +405,116 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& a, int32_t* counts) {
     for (int s = s0; s < s1; ++s) mine += (counts[s] + kManyRows - 1) / kManyRows;
     int b = block_scan(mine, total);
     for (int s = s0; s < s1; ++s) {
-        const int n = counts[s], first = b;
-        counts[s] = first * kManyRows;
-        for (int k = 0; k < n; k += kManyRows) a.g.block_slot[b++] = s - 1;
-        for (int k = n; k < (b - first) * kManyRows; ++k) a.g.rows[(int64_t)first * kManyRows + k] = -1;
+        const int n = counts[s];
+        counts[s] = b * kManyRows;
+        for (int k = 0; k < n; k += kManyRows, ++b) {
+            a.g.block_slot[b] = s - 1;
+            a.g.block_count[b] = min(n - k, kManyRows);
+        }
     }
     if (threadIdx.x == 0) *a.g.nblocks = total;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanArgs a) {
+// This pair's place among those of its slot; the lanes of a warp with one slot for all (the tokens of a
+// prompt) make one addition.  A pair of kNone takes no part.
+__device__ __forceinline__ int take_place(int32_t* counts, int slot) {
+    const int lane = threadIdx.x & 31;
+    if (__all_sync(0xffffffffu, slot == __shfl_sync(0xffffffffu, slot, 0))) {
+        if (slot == kNone) return 0;
+        int base = 0;
+        if (lane == 0) base = atomicAdd(&counts[slot + 1], 32);
+        return __shfl_sync(0xffffffffu, base, 0) + lane;
+    }
+    return slot == kNone ? 0 : atomicAdd(&counts[slot + 1], 1);
+}
+
+__device__ __forceinline__ int32_t ld_cluster(uint32_t addr) {
+    int32_t v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, int32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Each CTA counts its share of the pairs; each then takes a share of the slots, adds up the CTAs'
+// counts, and hands every CTA the position of its first pair of each slot.
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanArgs a) {
     extern __shared__ int32_t counts_s[];
+    __shared__ int32_t blocks_before[kPlanCtas];   // blocks of each CTA's slots
     pdl_trigger();
+    const int rank = (int)tc5::cluster_rank();
+    int slot[kPlanPerThread], place[kPlanPerThread];
+#pragma unroll
+    for (int i = 0; i < kPlanPerThread; ++i) {
+        const int p = (i * kPlanCtas + rank) * kPlanThreads + threadIdx.x;
+        slot[i] = p < a.g.P ? slot_of(a.g, p, true) : kNone;
+    }
     for (int s = threadIdx.x; s < a.nslots; s += kPlanThreads) counts_s[s] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < a.g.P; p += kPlanThreads) {
-        const int s = slot_of(a.g, p, true);
-        if (s != kNone) atomicAdd(&counts_s[s + 1], 1);
+#pragma unroll
+    for (int i = 0; i < kPlanPerThread; ++i) place[i] = take_place(counts_s, slot[i]);
+    tc5::cluster_sync();
+    const int share = (a.nslots + kPlanCtas - 1) / kPlanCtas, per = (share + kPlanThreads - 1) / kPlanThreads;
+    const int s0 = min(rank * share + (int)threadIdx.x * per, a.nslots), s1 = min(min(s0 + per, (rank + 1) * share), a.nslots);
+    auto counts_of = [&](int cta, int s) { return tc5::at_cta(smem_u32(counts_s + s), (uint32_t)cta); };
+    int mine = 0, total;
+    for (int s = s0; s < s1; ++s) {
+        int n = 0;
+#pragma unroll
+        for (int z = 0; z < kPlanCtas; ++z) n += ld_cluster(counts_of(z, s));
+        mine += (n + kManyRows - 1) / kManyRows;
     }
-    __syncthreads();
-    plan_scan(a, counts_s);
-    __syncthreads();
-    for (int p = threadIdx.x; p < a.g.P; p += kPlanThreads) {
-        const int s = slot_of(a.g, p, false);
-        if (s != kNone) a.g.rows[atomicAdd(&counts_s[s + 1], 1)] = p;
+    int b = block_scan(mine, total);
+    if (threadIdx.x < kPlanCtas) st_cluster(tc5::at_cta(smem_u32(blocks_before + rank), threadIdx.x), total);
+    tc5::cluster_sync();
+    int all = 0;
+    for (int z = 0; z < kPlanCtas; ++z) {
+        if (z < rank) b += blocks_before[z];
+        all += blocks_before[z];
     }
+    if (rank == 0 && threadIdx.x == 0) *a.g.nblocks = all;
+    for (int s = s0; s < s1; ++s) {
+        int n = 0;
+#pragma unroll
+        for (int z = 0; z < kPlanCtas; ++z) {
+            const uint32_t at = counts_of(z, s);
+            const int here = ld_cluster(at);
+            st_cluster(at, b * kManyRows + n);
+            n += here;
+        }
+        for (int k = 0; k < n; k += kManyRows, ++b) {
+            a.g.block_slot[b] = s - 1;
+            a.g.block_count[b] = min(n - k, kManyRows);
+        }
+    }
+    tc5::cluster_sync();
+#pragma unroll
+    for (int i = 0; i < kPlanPerThread; ++i)
+        if (slot[i] != kNone) a.g.rows[counts_s[slot[i] + 1] + place[i]] = (i * kPlanCtas + rank) * kPlanThreads + threadIdx.x;
 }
 
 __global__ void __launch_bounds__(256) adapter_count_kernel(const PlanArgs a) {
-    for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < a.g.P; p += (int64_t)gridDim.x * 256) {
-        const int s = slot_of(a.g, (int)p, true);
-        if (s != kNone) atomicAdd(&a.counts[s + 1], 1);
+    for (int64_t p0 = (int64_t)blockIdx.x * 256; p0 < a.g.P; p0 += (int64_t)gridDim.x * 256) {
+        const int64_t p = p0 + threadIdx.x;
+        take_place(a.counts, p < a.g.P ? slot_of(a.g, (int)p, true) : kNone);
     }
 }
 __global__ void __launch_bounds__(kPlanThreads) adapter_scan_kernel(const PlanArgs a) { plan_scan(a, a.counts); }
 __global__ void __launch_bounds__(256) adapter_place_kernel(const PlanArgs a) {
-    for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < a.g.P; p += (int64_t)gridDim.x * 256) {
-        const int s = slot_of(a.g, (int)p, false);
-        if (s != kNone) a.g.rows[atomicAdd(&a.counts[s + 1], 1)] = (int32_t)p;
+    for (int64_t p0 = (int64_t)blockIdx.x * 256; p0 < a.g.P; p0 += (int64_t)gridDim.x * 256) {
+        const int64_t p = p0 + threadIdx.x;
+        const int s = p < a.g.P ? slot_of(a.g, (int)p, false) : kNone;
+        const int at = take_place(a.counts, s);
+        if (s != kNone) a.g.rows[at] = (int32_t)p;
     }
 }
 
 // ---- host ---------------------------------------------------------------------------------
-// One CTA plans up to these; beyond, three kernels over the whole GPU.
-constexpr int kPlanPairs = 16384, kPlanSlots = 16384;
-
 struct Layout {
     int max_splits;
     int64_t blocks;   // at most
-    size_t v, nblocks, block_slot, rows, counts, bytes;
+    size_t v, nblocks, block_slot, block_count, rows, counts, bytes;
 };
 
 Layout layout_of(int64_t P, int64_t slots, int R) {
@@ -447,6 +533,7 @@ Layout layout_of(int64_t P, int64_t slots, int R) {
     if (!few) {
         l.nblocks = take(4);
         l.block_slot = take((size_t)l.blocks * 4);
+        l.block_count = take((size_t)l.blocks * 4);
         l.rows = take((size_t)l.blocks * kManyRows * 4);
         l.counts = take((size_t)(slots + 1) * 4);
     }
@@ -487,17 +574,16 @@ cudaError_t launch_down(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
 template <int MT, bool F32, bool FEW>
 cudaError_t launch_up_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
     auto* kern = adapter_up_kernel<MT, F32, FEW>;
-    const int ks = (g.rank + 15) / 16 * g.parts;
-    const size_t smem = (size_t)MT * ks * 3 * 512;
+    const size_t smem = (size_t)MT * ((g.rank + 15) / 16) * 3 * 512;   // at most 24 KB
     int ctas = 0;
-    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, 2 * 32 * 3 * 512, &ctas);
+    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
     if (e != cudaSuccess) return e;
     const int64_t most = (int64_t)device_info().sm_count * ctas;
-    const int tiles = (g.N / g.parts + 31) / 32 * g.parts;
     // four tiles a warp share the fragments of v, fewer where that leaves CTAs idle
+    const int tiles = (g.N / g.parts + 31) / 32;
+    const int64_t rows = blocks * (FEW ? 1 : kManyRows / (MT * 16)) * g.parts;
     int cols = 4 * kWarps;
-    const int64_t rows = blocks * (FEW ? 1 : kManyRows / (MT * 16));
-    while (cols > kWarps && rows * ((tiles + cols - 1) / cols) < most) cols /= 2;
+    while (cols > kWarps && rows * ((tiles + cols - 1) / cols) < 2 * most) cols /= 2;
     const int64_t items = rows * ((tiles + cols - 1) / cols);
     return launch_pdl(pdl_enabled(), kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g, cols);
 }
@@ -514,7 +600,7 @@ cudaError_t launch_plan(const AdapterArgs& g, int64_t slots, int32_t* counts, cu
         const size_t smem = (size_t)a.nslots * 4;
         cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(adapter_plan_kernel), (size_t)kPlanSlots * 4);
         if (e != cudaSuccess) return e;
-        adapter_plan_kernel<<<1, kPlanThreads, smem, st>>>(a);
+        adapter_plan_kernel<<<kPlanCtas, kPlanThreads, smem, st>>>(a);
         return cudaGetLastError();
     }
     cudaError_t e = cudaMemsetAsync(counts, 0, (size_t)a.nslots * 4, st);
@@ -561,8 +647,6 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     const int per = y_dtype == CHORD_DTYPE_F32 ? 4 : 8;
     if (P >= INT32_MAX || adapters > 65536 / E || rank % 8 || rank > 128 || parts > 4 || N % (8 * parts) || K % 8)
         return CHORD_ERR_UNSUPPORTED;
-    if (x_rows > 0 && x_stride > 0 && x_rows > (INT64_MAX >> 2) / x_stride) return CHORD_ERR_INVALID_ARG;
-    if (x_rows * (x_stride / 8) >= INT64_C(0xffffffff)) return CHORD_ERR_UNSUPPORTED;   // 16-byte pieces of x in 32 bits
     if (!topk_ids && E != 1) return CHORD_ERR_INVALID_ARG;
     if (P == 0) return CHORD_OK;
     if ((P - 1) / a_row_divisor >= x_rows) return CHORD_ERR_INVALID_ARG;
@@ -594,7 +678,7 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
                   base, y, base_stride, y_stride, base != y, units, l.max_splits < most ? l.max_splits : most, 2 * di.sm_count,
                   reinterpret_cast<float*>(ws + l.v),
                   reinterpret_cast<int32_t*>(ws + l.nblocks), reinterpret_cast<int32_t*>(ws + l.block_slot),
-                  reinterpret_cast<int32_t*>(ws + l.rows), di.err};
+                  reinterpret_cast<int32_t*>(ws + l.block_count), reinterpret_cast<int32_t*>(ws + l.rows), di.err};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (few) {

@@ -42,22 +42,22 @@ __global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const Logit
     int et;
     const int64_t t0 = divmod_idx(blockIdx.x / splits, etiles, et) * Warp::kRows;
     const int e0 = et * Warp::kCols;
+    const int c = lane & 3, pieces = a.H / 8;
     Warp w;
-    w.x = reinterpret_cast<const uint4*>(a.x + t0 * a.stride);
-    w.pieces = a.H / 8;
-    w.wstep = a.H;
-    w.wrows = (a.E - e0 - gr + 7) / 8;
-#pragma unroll
-    for (int j = 0; j < 2 * MT; ++j) w.xrow[j] = t0 + j * 8 + gr < a.T ? (uint32_t)((j * 8 + gr) * (a.stride / 8)) : thin::kNoRow;
     const int steps1 = (a.H + thin::kStep - 1) / thin::kStep;
     const int64_t steps = (int64_t)steps1 * a.parts;
     const int k0 = (int)(rank * steps / splits), k1 = (int)((rank + 1) * steps / splits);
     float* mine = red + warp * kTile;
     bool more = false;
     for (int part = k0 / steps1; part * steps1 < k1; ++part) {
-        w.w = reinterpret_cast<const uint4*>(a.W + ((int64_t)(a.parts - 1 - part) * a.E + e0 + gr) * a.H);
+#pragma unroll
+        for (int j = 0; j < 2 * MT; ++j)
+            w.x[j] = reinterpret_cast<const uint4*>(a.x + min(t0 + j * 8 + gr, (int64_t)a.T - 1) * a.stride) + c;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            w.w[j] = reinterpret_cast<const uint4*>(a.W + ((int64_t)(a.parts - 1 - part) * a.E + min(e0 + j * 8 + gr, a.E - 1)) * a.H) + c;
         const int first = max(k0 - part * steps1, 0), last = min(k1 - part * steps1, steps1);
-        w.run(first + warp, last, mine, more);
+        w.run(first + warp, last, pieces, mine, more);
         more = true;
     }
     auto put = [&](int i, float v) {

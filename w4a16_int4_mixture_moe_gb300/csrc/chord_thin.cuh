@@ -19,7 +19,6 @@ constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kStep = 32;     // columns
 // The instructions' additions chop: chains end after 24 steps (48 instructions) and are added up in FP32.
 constexpr int kChain = 24;
-constexpr uint32_t kNoRow = 0xffffffffu;
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -28,32 +27,28 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// What one warp multiplies: MT tiles of 16 rows of x, NT tiles of eight weight rows.
+// What one warp multiplies: MT tiles of 16 rows of x, NT tiles of eight weight rows.  Rows that are not
+// there are any others: their sums are not looked at.
 template <int MT, int NT>
 struct Warp {
     static constexpr int kRows = MT * 16, kCols = NT * 8;
-    // Two steps in registers, one on its way while the other is multiplied, where they fit.
-    static constexpr bool kAhead = MT * NT <= 16;
-    const uint4* x;            // of K columns of bf16, in 16-byte pieces
-    const uint4* w;            // first weight row of this lane's, the others wstep pieces apart
-    uint32_t xrow[2 * MT];     // where this lane's rows begin, in pieces; kNoRow: zeros
-    int64_t wstep;
-    int wrows;                 // tiles of eight whose row of this lane exists
-    int pieces;                // of a row: K / 8
+    // Steps in registers, all but one of them on their way: as many as a few rows need to cover the latency.
+    static constexpr int kDepth = MT * NT <= 2 ? 4 : MT * NT <= 4 ? 3 : 2;
+    const uint4* x[2 * MT];    // this lane's rows and piece of a step: row start + c
+    const uint4* w[NT];
     float acc[MT][NT][4];
 
     struct Step {
         uint4 a[2 * MT], b[NT];
     };
 
-    __device__ __forceinline__ void load(Step& s, int step) const {
-        const int lane = threadIdx.x & 31, at = step * 4 + (lane & 3);
-        const bool in = at < pieces;
+    template <bool TAIL>
+    __device__ __forceinline__ void load(Step& s, int at, bool in) const {
         const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int j = 0; j < 2 * MT; ++j) s.a[j] = in && xrow[j] != kNoRow ? x[(uint64_t)xrow[j] + at] : zero;
+        for (int j = 0; j < 2 * MT; ++j) s.a[j] = !TAIL || in ? x[j][at] : zero;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) s.b[j] = in && j < wrows ? w[j * wstep + at] : zero;
+        for (int j = 0; j < NT; ++j) s.b[j] = !TAIL || in ? w[j][at] : zero;
     }
     __device__ __forceinline__ void multiply(const Step& s) {
 #pragma unroll
@@ -64,39 +59,51 @@ struct Warp {
                 mma(acc[m][t], s.a[2 * m].z, s.a[2 * m + 1].z, s.a[2 * m].w, s.a[2 * m + 1].w, s.b[t].z, s.b[t].w);
             }
     }
-    // Steps first, first + 8, ... below last: the sums go to (or, with `more`, are added to) mine, the
-    // warp's [kRows][kCols] floats in shared memory.
-    __device__ __forceinline__ void run(int first, int last, float* mine, bool more) {
+    __device__ __forceinline__ void move(int pieces) {
+#pragma unroll
+        for (int j = 0; j < 2 * MT; ++j) x[j] += pieces;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) w[j] += pieces;
+    }
+    // Steps first, first + 8, ... below last of K = 8 * pieces columns: the sums go to (or, with `more`, are
+    // added to) mine, the warp's [kRows][kCols] floats in shared memory.  Moves x and w.
+    __device__ __forceinline__ void run(int first, int last, int pieces, float* mine, bool more) {
+        constexpr int kNext = kWarps * 4;   // pieces from a step of this warp to its next
         const int lane = threadIdx.x & 31;
         float* to0 = mine + (lane >> 2) * kCols + 2 * (lane & 3);
-        int s = first;
+        const int full = min(last, pieces / 4);                                        // whole steps end here
+        int left = first < full ? (full - first + kWarps - 1) / kWarps : 0;            // whole steps of this warp
+        const int after = first + left * kWarps;                                       // and its step behind them
+        move(first * 4);
         do {
-            const int end = min(last, s + kChain * kWarps);
+            int n = min(left, kChain);
+            left -= n;
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int u = 0; u < 4; ++u) acc[m][t][u] = 0.0f;
-            if constexpr (kAhead) {
-                Step p, q;
-                if (s < end) load(p, s);
-                while (s < end) {
-                    if (s + kWarps < end) load(q, s + kWarps);
-                    multiply(p);
-                    if (s + kWarps >= end) break;
-                    if (s + 2 * kWarps < end) load(p, s + 2 * kWarps);
-                    multiply(q);
-                    s += 2 * kWarps;
-                }
-            } else {
-                for (; s < end; s += kWarps) {
-                    Step p;
-                    load(p, s);
-                    multiply(p);
+            Step s[kDepth];
+#pragma unroll
+            for (int d = 0; d < kDepth - 1; ++d)
+                if (d < n) load<false>(s[d], d * kNext, true);
+            while (n > 0) {
+#pragma unroll
+                for (int d = 0; d < kDepth; ++d) {
+                    if (n > kDepth - 1) load<false>(s[(d + kDepth - 1) % kDepth], (d + kDepth - 1) * kNext, true);
+                    if (n > 0) {
+                        multiply(s[d]);
+                        if (d + 1 == kDepth) move(kDepth * kNext);
+                        else if (n == 1) move((d + 1) * kNext);
+                    }
+                    --n;
                 }
             }
-            s = end;   // the next chain begins there, or this was the last
+            if (left == 0 && after < last) {   // the last columns, not a whole step
+                load<true>(s[0], 0, after * 4 + (lane & 3) < pieces);
+                multiply(s[0]);
+            }
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -109,7 +116,7 @@ struct Warp {
                         *to = o;
                     }
             more = true;
-        } while (s < last);
+        } while (left > 0);
     }
 };
 

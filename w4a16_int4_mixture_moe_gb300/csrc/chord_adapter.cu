@@ -4,8 +4,8 @@
 // up to 16 rows a matrix-instruction tile, so a slot's weights are read once a block.
 //   plan   (more than kFewPairs pairs) the blocks: a counting sort of the pairs by slot.  With few
 //          pairs every CTA of the two kernels finds the blocks itself, which costs less than a launch.
-//   down   v, a block's rows times the slot's A: thin products (chord_thin.cuh), an item is (up to 64
-//          rows of a block, up to 64 rows of A, K slice).  K slices are partial sums in the workspace, as many as
+//   down   v, a block's rows times the slot's A: thin products (chord_thin.cuh), an item is (block, up to
+//          64 rows of A, K slice).  K slices are partial sums in the workspace, as many as
 //          fill the GPU; both kernels work the number out from the number of blocks.
 //   up     y, an item is (block, columns).  The slices of v are added in order, scaled and split into three
 //          bf16 parts of eight bits each, so the tensor cores multiply all of an FP32 v.  The
@@ -131,36 +131,27 @@ __device__ __forceinline__ int slices_of(const AdapterArgs& g, int n) {
 }
 
 // ---- v = A x --------------------------------------------------------------------
-template <int MT, int NT, bool FEW>
-__global__ void __launch_bounds__(kThreads) adapter_down_kernel(const AdapterArgs g) {
-    using Warp = thin::Warp<MT, NT>;
-    constexpr int MB = FEW ? kFewRows : kManyRows, MR = Warp::kRows, NB = Warp::kCols, SUB = MB / MR;
+template <int NT>
+__global__ void __launch_bounds__(kThreads) adapter_down_few_kernel(const AdapterArgs g) {
+    using Warp = thin::Warp<1, NT>;
+    constexpr int MR = Warp::kRows, NB = Warp::kCols;
     extern __shared__ __align__(16) float red[];   // [kWarps][MR][NB]
-    __shared__ int32_t rows[MB];
-    __shared__ FewBlocks few[1];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2;
+    __shared__ int32_t rows[MR];
+    __shared__ FewBlocks few;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
     pdl_trigger();
-    int n;
-    if constexpr (FEW) {
-        find_blocks(g, few[0], blockIdx.x == 0);
-        n = few[0].n;
-    } else {
-        pdl_wait();
-        n = *g.nblocks;
-    }
-    const int splits = slices_of(g, n), chunks = (g.R + NB - 1) / NB, per = SUB * chunks * splits, steps = (g.K + thin::kStep - 1) / thin::kStep;
+    find_blocks(g, few, blockIdx.x == 0);
+    const int n = few.n, splits = slices_of(g, n), chunks = (g.R + NB - 1) / NB, per = chunks * splits;
+    const int steps = (g.K + thin::kStep - 1) / thin::kStep;
     for (int64_t i = blockIdx.x; i < (int64_t)n * per; i += gridDim.x) {
         int q;
-        const int b = (int)divmod_idx(i, per, q);
-        const int split = q % splits, r0 = q / splits % chunks * NB, sub = q / (splits * chunks);
-        const int slot = block_rows<FEW, MB>(g, few, b, rows);
-        const int32_t* mine = rows + sub * MR;
-        if (slot < 0 || mine[0] < 0) continue;   // a block's rows are a prefix
+        const int b = (int)divmod_idx(i, per, q), split = q % splits, r0 = q / splits * NB;
+        const int slot = block_rows<true, MR>(g, &few, b, rows);
+        if (slot < 0) continue;
         Warp w;
-        const int c = lane & 3;
 #pragma unroll
-        for (int j = 0; j < 2 * MT; ++j) {
-            const int p = mine[j * 8 + gr] < 0 ? mine[0] : mine[j * 8 + gr];
+        for (int j = 0; j < 2; ++j) {
+            const int p = rows[j * 8 + gr] < 0 ? rows[0] : rows[j * 8 + gr];
             w.x[j] = reinterpret_cast<const uint4*>(g.x + (int64_t)(g.div == 1 ? p : p / g.div) * g.x_stride) + c;
         }
 #pragma unroll
@@ -170,8 +161,41 @@ __global__ void __launch_bounds__(kThreads) adapter_down_kernel(const AdapterArg
         w.run(k0 + warp, k1, g.K / 8, red + warp * MR * NB, false);
         __syncthreads();
         for (int u = threadIdx.x; u < MR * NB; u += kThreads) {
-            const int p = mine[u / NB], r = r0 + u % NB;
+            const int p = rows[u / NB], r = r0 + u % NB;
             if (p >= 0 && r < g.R) g.v[((int64_t)split * g.P + p) * g.R + r] = thin::joined(red, MR * NB, u);
+        }
+    }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const AdapterArgs g) {
+    using Tile = thin::Staged<NT>;
+    constexpr int NB = Tile::kCols;
+    static_assert(Tile::kRows == kManyRows, "a block of the plan is a tile");
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int32_t rows[kManyRows];
+    pdl_trigger();
+    pdl_wait();
+    const int n = *g.nblocks, splits = slices_of(g, n), chunks = (g.R + NB - 1) / NB, per = chunks * splits;
+    const int steps = (g.K + Tile::kTileCols - 1) / Tile::kTileCols;
+    for (int64_t i = blockIdx.x; i < (int64_t)n * per; i += gridDim.x) {
+        int q;
+        const int b = (int)divmod_idx(i, per, q), split = q % splits, r0 = q / splits * NB;
+        const int slot = block_rows<false, kManyRows>(g, nullptr, b, rows);
+        if (slot < 0) continue;
+        Tile tile;
+        const int row = threadIdx.x >> 3, piece = threadIdx.x & 7;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int p = rows[row + 32 * h], r = row + 32 * h;
+            tile.x[h] = p < 0 ? nullptr : g.x + (int64_t)(g.div == 1 ? p : p / g.div) * g.x_stride + piece * 8;
+            tile.w[h] = r < NB && r0 + r < g.R ? g.A + ((int64_t)slot * g.R + r0 + r) * g.K + piece * 8 : nullptr;
+        }
+        tile.run(smem, (int)((int64_t)split * steps / splits), (int)((int64_t)(split + 1) * steps / splits), g.K, 1, 0);
+        const float* sums = reinterpret_cast<const float*>(smem);
+        for (int u = threadIdx.x; u < kManyRows * NB; u += kThreads) {
+            const int p = rows[u / NB], r = r0 + u % NB;
+            if (p >= 0 && r < g.R) g.v[((int64_t)split * g.P + p) * g.R + r] = sums[u] + sums[kManyRows * NB + u];
         }
     }
 }
@@ -540,19 +564,13 @@ Layout layout_of(int64_t P, int64_t slots, int R) {
     return l;
 }
 
-// Tile of the first half: all of a block's rows and of A's where registers hold a step ahead, 32 rows for 64 of A.
-struct DownTile {
-    int rows, cols;
-};
-DownTile down_tile(int R, bool few) {
-    const int cols = R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64;
-    return {few ? kFewRows : cols == 64 ? 32 : 64, cols};
-}
+// Rows of A that an item of the first half takes.
+int down_cols(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
-template <int MT, int NT, bool FEW>
+template <int NT, bool FEW>
 cudaError_t launch_down_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
-    auto* kern = adapter_down_kernel<MT, NT, FEW>;
-    const size_t smem = (size_t)kWarps * MT * 16 * NT * 8 * 4;
+    void (*kern)(AdapterArgs) = FEW ? adapter_down_few_kernel<NT> : adapter_down_kernel<NT>;
+    const size_t smem = FEW ? (size_t)kWarps * kFewRows * NT * 8 * 4 : thin::Staged<NT>::kBytes;
     int ctas = 0;
     cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
     if (e != cudaSuccess) return e;
@@ -562,12 +580,11 @@ cudaError_t launch_down_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st
 
 template <bool FEW>
 cudaError_t launch_down(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
-    constexpr int MT = FEW ? 1 : 4;
-    switch (down_tile(g.R, FEW).cols) {
-        case 8: return launch_down_as<MT, 1, FEW>(g, blocks, st);
-        case 16: return launch_down_as<MT, 2, FEW>(g, blocks, st);
-        case 32: return launch_down_as<MT, 4, FEW>(g, blocks, st);
-        default: return launch_down_as<FEW ? 1 : 2, 8, FEW>(g, blocks, st);
+    switch (down_cols(g.R)) {
+        case 8: return launch_down_as<1, FEW>(g, blocks, st);
+        case 16: return launch_down_as<2, FEW>(g, blocks, st);
+        case 32: return launch_down_as<4, FEW>(g, blocks, st);
+        default: return launch_down_as<8, FEW>(g, blocks, st);
     }
 }
 
@@ -669,9 +686,8 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     const int64_t slots = (int64_t)adapters * E;
     const bool few = P <= kFewPairs, f32 = y_dtype == CHORD_DTYPE_F32;
     const Layout l = layout_of(P, slots, rank * parts);
-    const DownTile tile = down_tile(rank * parts, few);
-    const int units = (few ? kFewRows : kManyRows) / tile.rows * ((rank * parts + tile.cols - 1) / tile.cols);
-    const int most = (K + thin::kStep * kWarps - 1) / (thin::kStep * kWarps);   // slices with a step for every warp
+    const int cols = down_cols(rank * parts), units = (rank * parts + cols - 1) / cols;
+    const int most = (K + thin::kStep * kWarps - 1) / (thin::kStep * kWarps);   // slices of 256 columns: a step for every warp
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     AdapterArgs g{static_cast<const __nv_bfloat16*>(x), x_stride, a_row_divisor, adapter_ids, topk_ids, (int)P, topk, adapters, E,
                   static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, rank, parts, rank * parts, N, K,

@@ -128,5 +128,118 @@ __device__ __forceinline__ float joined(const float* red, int n, int i) {
     return v;
 }
 
+// ---- the same for many rows, staged in shared memory ----------------------------------------
+// 64 rows of x times NT x 8 weight rows: every thread copies 16-byte pieces of a stage of 64 columns with
+// cp.async, kStages - 1 stages are on their way.  Warp w takes rows 16 (w mod 4) and half of a stage's four k16
+// steps; the halves are joined at the end.  Rows of 128 bytes, piece p of row r at p xor (r mod 8).
+template <int NT>
+struct Staged {
+    static constexpr int kRows = 64, kCols = NT * 8, kTileCols = 64, kStages = 7;
+    static constexpr int kStageBytes = (kRows + kCols) * 128;
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes;          // the ring
+    static constexpr size_t kSums = (size_t)2 * kRows * kCols * 4;          // over it, afterwards: [2][kRows][kCols]
+    static constexpr size_t kBytes = kSmem > kSums ? kSmem : kSums;
+    static constexpr int kChainStages = 24;                                 // two instructions a stage
+
+    // This thread's rows of x (t / 8 and t / 8 + 32) and weight rows, at piece t mod 8; null: not copied,
+    // whatever is multiplied in its place is not looked at.
+    const __nv_bfloat16* x[2];
+    const __nv_bfloat16* w[2];
+    float acc[NT][4], sum[NT][4];
+
+    __device__ __forceinline__ void copy(uint32_t st, int col, int64_t w_offset, int K) const {
+        const int t = threadIdx.x, row = t >> 3, piece = t & 7;
+        const bool in = col + piece * 8 < K;
+        const uint32_t at = st + (uint32_t)row * 128u + (uint32_t)(((piece ^ row) & 7) << 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (x[h]) fill(at + h * 4096u, x[h] + col, in);
+            if (h * 32 < kCols && w[h]) fill(at + kRows * 128u + h * 4096u, w[h] + w_offset + col, in);
+        }
+    }
+    // 16 bytes, or zeros behind the last column.
+    __device__ __forceinline__ static void fill(uint32_t dst, const __nv_bfloat16* src, bool in) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+    }
+    __device__ __forceinline__ static void ldsm(uint32_t (&r)[4], uint32_t addr) {
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr)
+                     : "memory");
+    }
+    __device__ __forceinline__ void multiply(uint32_t st) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int ar = (warp & 3) * 16 + (lane & 15), br = (lane >> 4) * 8 + (lane & 7);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int kk = (warp >> 2) * 2 + q;
+            uint32_t a[4];
+            ldsm(a, st + (uint32_t)ar * 128u + (uint32_t)(((kk * 2 + (lane >> 4)) ^ (ar & 7)) << 4));
+#pragma unroll
+            for (int t = 0; t < NT; t += 2) {
+                uint32_t b[4];
+                // with one tile of weights the second half of the lanes reads its rows again
+                const int r = t * 8 + (NT > 1 ? br : (lane & 7));
+                ldsm(b, st + kRows * 128u + (uint32_t)r * 128u + (uint32_t)(((kk * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+                mma(acc[t], a[0], a[1], a[2], a[3], b[0], b[1]);
+                if (t + 1 < NT) mma(acc[t + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+            }
+        }
+    }
+    __device__ __forceinline__ void end_chain() {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                sum[t][u] += acc[t][u];
+                acc[t][u] = 0.0f;
+            }
+    }
+    // Stages s0 .. s1 - 1 of `parts` weight matrices one behind the other, part_stride elements apart, the last
+    // one first.  Every thread of the CTA; the sums are in smem ([2][kRows][kCols] floats) when it returns.
+    __device__ __forceinline__ void run(uint8_t* smem, int s0, int s1, int K, int parts, int64_t part_stride) {
+        const uint32_t base = smem_u32(smem);
+        const int per = (K + kTileCols - 1) / kTileCols;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[t][u] = sum[t][u] = 0.0f;
+        int next = s0, part = s0 / per, k = s0 - part * per, slot_in = 0, slot_out = 0, chain = 0;
+        auto issue = [&]() {
+            if (next < s1) {
+                copy(base + (uint32_t)(slot_in * kStageBytes), k * kTileCols, (int64_t)(parts - 1 - part) * part_stride, K);
+                if (++k == per) k = 0, ++part;
+                ++next;
+            }
+            cp_async_commit();
+            if (++slot_in == kStages) slot_in = 0;
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) issue();
+        for (int s = s0; s < s1; ++s) {
+            cp_async_wait<kStages - 2>();
+            __syncthreads();   // the stage is there for all, and the one before has been read by all
+            issue();
+            multiply(base + (uint32_t)(slot_out * kStageBytes));
+            if (++slot_out == kStages) slot_out = 0;
+            if (++chain == kChainStages) {
+                chain = 0;
+                end_chain();
+            }
+        }
+        end_chain();
+        cp_async_wait<0>();
+        __syncthreads();
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        float* to = reinterpret_cast<float*>(smem) + ((warp >> 2) * kRows + (warp & 3) * 16 + (lane >> 2)) * kCols + 2 * (lane & 3);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<float2*>(to + h * 8 * kCols + t * 8) = make_float2(sum[t][2 * h], sum[t][2 * h + 1]);
+        __syncthreads();
+    }
+};
+
 }  // namespace thin
 }  // namespace chord

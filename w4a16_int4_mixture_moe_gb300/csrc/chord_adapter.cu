@@ -241,48 +241,42 @@ struct Eight<false> {
     }
 };
 
-// Three bf16 numbers of eight significant bits each whose sum is v; an infinity or NaN is the first alone.
-__device__ __forceinline__ void split3(float v, __nv_bfloat16 (&h)[3]) {
-    const bool finite = fabsf(v) <= 3.4028235e38f;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        h[i] = finite ? __float2bfloat16_rz(v) : __float2bfloat16_rn(i ? 0.0f : v);
-        v = finite ? v - __bfloat162float(h[i]) : 0.0f;
-    }
+// Two FP32 numbers as three pairs of bf16 numbers of eight significant bits each, cut off towards zero, whose sums
+// they are (exactly, down to 2^-110): the upper half of a number is its first part.  An infinity or NaN is the
+// first part alone.
+__device__ __forceinline__ void split3(float v0, float v1, uint32_t& h0, uint32_t& h1, uint32_t& h2) {
+    auto upper = [](float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); };
+    auto rest = [](float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); };
+    h0 = upper(v0, v1);
+    v0 = fabsf(v0) <= 3.4028235e38f ? rest(v0) : 0.0f;
+    v1 = fabsf(v1) <= 3.4028235e38f ? rest(v1) : 0.0f;
+    h1 = upper(v0, v1);
+    h2 = upper(rest(v0), rest(v1));
 }
 
-// An item is MT x 16 rows of a block times `cols` tiles of 32 columns of one part; the eight warps take a tile each.
-template <int MT, bool F32, bool FEW>
-__global__ void __launch_bounds__(kThreads, 2) adapter_up_kernel(const AdapterArgs g, int cols) {
-    constexpr int MB = FEW ? kFewRows : kManyRows, MR = MT * 16, SUB = MB / MR;
+// Few pairs: an item is a block times `cols` tiles of 32 columns of one part, straight from global memory; the
+// eight warps take a tile each.
+template <bool F32>
+__global__ void __launch_bounds__(kThreads, 2) adapter_up_few_kernel(const AdapterArgs g, int cols) {
+    constexpr int MT = 1;
     extern __shared__ __align__(16) uint4 frag[];   // [MT][k steps of all parts][3][32]
-    __shared__ int32_t rows[MB];
+    __shared__ int32_t mine[kFewRows];   // the block's rows
+    __shared__ FewBlocks few;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
-    FewBlocks* few = nullptr;
-    int n;
-    if constexpr (FEW) {
-        __shared__ FewBlocks blocks;
-        few = &blocks;
-        find_blocks(g, blocks, false);   // the ids are older than the kernel before
-        n = blocks.n;
-        pdl_wait();
-    } else {
-        pdl_wait();
-        n = *g.nblocks;
-    }
+    find_blocks(g, few, false);   // the ids are older than the kernel before
+    const int n = few.n;
+    pdl_wait();
     const int splits = slices_of(g, n);
     const int Np = g.N / g.parts, tiles = (Np + 31) / 32, groups = (tiles + cols - 1) / cols;
     const int ksp = (g.rank + 15) / 16;          // 16-wide steps of a part
     const int per = groups * g.parts;            // items of the rows of a block
     // column of lane group gr in tile j of a matrix instruction: the eight columns of one lane's results are 8 c ... 8 c + 7
     const int bc = 8 * (gr >> 1) + (gr & 1);
-    for (int64_t i = blockIdx.x; i < (int64_t)n * SUB * per; i += gridDim.x) {
+    for (int64_t i = blockIdx.x; i < (int64_t)n * per; i += gridDim.x) {
         int q;
-        const int bs = (int)divmod_idx(i, per, q);
+        const int b16 = (int)divmod_idx(i, per, q);
         const int part = q / groups, t0 = (q - part * groups) * cols;
-        const int slot = block_rows<FEW, MB>(g, few, bs / SUB, rows);
-        const int32_t* mine = rows + bs % SUB * MR;
-        if (mine[0] < 0) continue;   // rows of a block are a prefix
+        const int slot = block_rows<true, kFewRows>(g, &few, b16, mine);
         if (slot >= 0) {
             // v as the fragments of the instruction's A side: lane (g, c) has rows g and g + 8, of each k
             // step the four columns 4 c ... (B's side likewise)
@@ -302,23 +296,14 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up_kernel(const AdapterAr
                             f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
                         }
                     }
-                    __nv_bfloat16 e[4][3];
-                    split3(f.x * scale, e[0]);
-                    split3(f.y * scale, e[1]);
-                    split3(f.z * scale, e[2]);
-                    split3(f.w * scale, e[3]);
-#pragma unroll
-                    for (int t = 0; t < 3; ++t) {
-                        r[t][h] = bf2_as_u32(__halves2bfloat162(e[0][t], e[1][t]));
-                        r[t][2 + h] = bf2_as_u32(__halves2bfloat162(e[2][t], e[3][t]));
-                    }
+                    split3(f.x * scale, f.y * scale, r[0][h], r[1][h], r[2][h]);
+                    split3(f.z * scale, f.w * scale, r[0][2 + h], r[1][2 + h], r[2][2 + h]);
                 }
 #pragma unroll
                 for (int t = 0; t < 3; ++t) frag[(ms * 3 + t) * 32 + l] = make_uint4(r[t][0], r[t][1], r[t][2], r[t][3]);
             }
             __syncthreads();
         }
-        const bool two = MT > 1 && mine[(MT - 1) * 16] >= 0;   // the second 16 rows hold any
         int64_t from[2 * MT], to[2 * MT];
         bool live[2 * MT];
 #pragma unroll
@@ -357,7 +342,6 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up_kernel(const AdapterAr
                     for (int j = 0; j < 4; ++j) w[j] = kin ? *reinterpret_cast<const uint2*>(bt[j] + 16 * s) : make_uint2(0, 0);
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
-                        if (m > 0 && !two) break;
 #pragma unroll
                         for (int t3 = 2; t3 >= 0; --t3) {
                             const uint4 a = frag[((m * ksp + s) * 3 + t3) * 32 + lane];
@@ -381,6 +365,164 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up_kernel(const AdapterAr
             for (int j = 0; j < 2 * MT; ++j)
                 if (in && live[j]) o[j].store(g.y, to[j] + n0);
         }
+    }
+}
+
+// Many pairs: the tiles of 64 columns of all blocks of the plan are dealt to the CTAs in equal ranges.  A
+// stage, base's tile and B's, comes by cp.async, kUpStages - 1 of them are on their way.  Warp w has rows 16 (w mod 4) and 32 of the
+// columns; its rows of v stay in registers as fragments of the instruction's A side (KS k steps of 16).
+constexpr int kUpCols = 64, kUpStages = 4;
+
+template <int KS, bool F32>
+struct UpTile {
+    static constexpr int kEsize = F32 ? 4 : 2;
+    static constexpr int kRowPitch = kUpCols * kEsize + 16;                 // padded: neighbouring rows in other banks
+    static constexpr int kBase = kManyRows * kRowPitch;
+    static constexpr int kBPitch = KS * 32 + 16;                            // likewise
+    static constexpr int kBPieces = (kUpCols * KS * 2 + kThreads - 1) / kThreads;   // 16-byte pieces of B a thread copies
+    static constexpr int kStage = kBase + kUpCols * kBPitch;
+    static constexpr size_t kBytes = (size_t)kUpStages * kStage;
+};
+
+template <int KS, bool F32>
+__global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_up_kernel(const AdapterArgs g) {
+    using T = UpTile<KS, F32>;
+    constexpr int kPieces = kUpCols * T::kEsize / 16, kRowsAtOnce = kThreads / kPieces, kPasses = kManyRows / kRowsAtOnce;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int32_t rows[kManyRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
+    pdl_wait();
+    const int n = *g.nblocks, splits = slices_of(g, n);
+    const int Np = g.N / g.parts, tiles = (Np + kUpCols - 1) / kUpCols;
+    const uint32_t base = smem_u32(smem);
+    const int b_pieces = g.rank / 8;
+    // Row i of the 8-column tile t of a matrix instruction is column 8 (i / 2) + 2 t + (i & 1) of 32, so that lane
+    // (g, c) ends with columns 8 c .. 8 c + 7; B is stored in the tiles' order, where neighbouring rows
+    // lie in different banks.  ldmatrix: matrix j of two tiles is k half j & 1 of tile j >> 1.
+    const uint32_t b_at = (uint32_t)(T::kBase + ((warp >> 2) * 32 + (lane >> 4) * 8 + (lane & 7)) * T::kBPitch + ((lane >> 3) & 1) * 16);
+    int b_col[T::kBPieces], b_to[T::kBPieces];
+#pragma unroll
+    for (int h = 0; h < T::kBPieces; ++h) {
+        const int u = threadIdx.x + h * kThreads, col = u / b_pieces, k = u - col * b_pieces;
+        b_col[h] = col < kUpCols ? col : INT32_MAX;
+        b_to[h] = T::kBase + ((col & 32) | (col >> 1 & 3) * 8 | (col >> 3 & 3) * 2 | (col & 1)) * T::kBPitch + k * 16;
+    }
+    const int64_t total = (int64_t)n * g.parts * tiles, end = total * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t at = total * blockIdx.x / gridDim.x; at < end;) {
+        int t0, part;
+        const int b = (int)divmod_idx(divmod_idx(at, tiles, t0), g.parts, part), t1 = (int)min((int64_t)tiles, t0 + (end - at));
+        at += t1 - t0;
+        const int slot = block_rows<false, kManyRows>(g, nullptr, b, rows);
+        // copies of a tile
+        const int piece = threadIdx.x % kPieces, row0 = threadIdx.x / kPieces;
+        const uint8_t* from[kPasses];
+#pragma unroll
+        for (int h = 0; h < kPasses; ++h) {
+            const int p = rows[row0 + h * kRowsAtOnce];
+            from[h] = p < 0 ? nullptr
+                            : static_cast<const uint8_t*>(g.base) + (p * g.base_stride + part * Np) * T::kEsize + piece * 16;
+        }
+        const __nv_bfloat16* bsrc = g.B + ((int64_t)max(slot, 0) * g.N + part * Np) * g.rank;
+        int next = t0, slot_in = 0, slot_out = 0;
+        auto issue = [&]() {
+            if (next < t1) {
+                const uint32_t st = base + (uint32_t)(slot_in * T::kStage);
+                const int n0 = next * kUpCols;
+                if (n0 + piece * (16 / T::kEsize) < Np)
+#pragma unroll
+                    for (int h = 0; h < kPasses; ++h)
+                        if (from[h]) cp_async16(st + (uint32_t)((row0 + h * kRowsAtOnce) * T::kRowPitch + piece * 16), from[h] + (int64_t)n0 * T::kEsize);
+                if (slot >= 0) {
+                    const __nv_bfloat16* src = bsrc + (int64_t)n0 * g.rank + threadIdx.x * 8;
+#pragma unroll
+                    for (int h = 0; h < T::kBPieces; ++h)
+                        if (b_col[h] < Np - n0) cp_async16(st + (uint32_t)b_to[h], src + h * kThreads * 8);
+                }
+                ++next;
+            }
+            cp_async_commit();
+            if (++slot_in == kUpStages) slot_in = 0;
+        };
+        // a rank that ends inside a k step: zeros behind it, in every stage
+        if (g.rank % 16)
+            for (int u = threadIdx.x; u < kUpStages * kUpCols; u += kThreads)
+                *reinterpret_cast<uint4*>(smem + u / kUpCols * T::kStage + T::kBase + u % kUpCols * T::kBPitch + g.rank * 2) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < kUpStages - 1; ++k) issue();
+        // this warp's rows of v: slices added in order, scaled, in three parts
+        const int r0 = (warp & 3) * 16, p0 = rows[r0 + gr], p1 = rows[r0 + gr + 8];
+        const bool busy = rows[r0] >= 0;   // rows of a block are a prefix
+        uint32_t a[KS][3][4];
+        if (slot >= 0 && busy) {
+            const float scale = g.scale ? g.scale[slot / g.E] : 1.0f;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const int k = 16 * s + 2 * c;   // and k + 1, k + 8, k + 9
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int p = h ? p1 : p0;
+                    float4 f = make_float4(0, 0, 0, 0);
+                    if (p >= 0 && k < g.rank) {
+                        const float* v = g.v + (int64_t)p * g.R + part * g.rank + k;
+                        const bool up = k + 8 < g.rank;
+                        for (int z = 0; z < splits; ++z, v += (int64_t)g.P * g.R) {
+                            const float2 l = *reinterpret_cast<const float2*>(v), r = up ? *reinterpret_cast<const float2*>(v + 8) : make_float2(0, 0);
+                            f.x += l.x, f.y += l.y, f.z += r.x, f.w += r.y;
+                        }
+                    }
+                    split3(f.x * scale, f.y * scale, a[s][0][h], a[s][1][h], a[s][2][h]);
+                    split3(f.z * scale, f.w * scale, a[s][0][2 + h], a[s][1][2 + h], a[s][2][2 + h]);
+                }
+            }
+        }
+        const int mycol = (warp >> 2) * 32;
+        for (int t = t0; t < t1; ++t) {
+            cp_async_wait<kUpStages - 2>();
+            __syncthreads();   // the stage is there for all, and the one before has been read by all
+            issue();
+            const uint32_t st = base + (uint32_t)(slot_out * T::kStage);
+            if (++slot_out == kUpStages) slot_out = 0;
+            const int n0 = t * kUpCols + mycol;
+            if (!busy || n0 >= Np) continue;
+            float d[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) d[j][u] = 0.0f;
+            if (slot >= 0) {
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    if (16 * s >= g.rank) break;
+                    uint32_t w[2][4];
+                    thin::ldsm4(w[0], st + b_at + (uint32_t)(s * 32));
+                    thin::ldsm4(w[1], st + b_at + (uint32_t)(16 * T::kBPitch + s * 32));
+                    // instructions on one accumulator are four apart
+#pragma unroll
+                    for (int t3 = 2; t3 >= 0; --t3)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            thin::mma(d[j], a[s][t3][0], a[s][t3][1], a[s][t3][2], a[s][t3][3], w[j >> 1][(j & 1) * 2], w[j >> 1][(j & 1) * 2 + 1]);
+                }
+            }
+            if (n0 + 8 * c < Np) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int p = h ? p1 : p0;
+                    if (p < 0) continue;
+                    float e[8];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        e[2 * u] = d[u][2 * h];
+                        e[2 * u + 1] = d[u][2 * h + 1];
+                    }
+                    Eight<F32> o;
+                    o.load(smem + (st - base) + (r0 + gr + 8 * h) * T::kRowPitch, mycol + 8 * c);
+                    if (slot >= 0) o.add(e);
+                    o.store(g.y, p * g.y_stride + part * Np + n0 + 8 * c);
+                }
+            }
+        }
+        cp_async_wait<0>();   // empty groups
     }
 }
 
@@ -588,27 +730,41 @@ cudaError_t launch_down(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
     }
 }
 
-template <int MT, bool F32, bool FEW>
-cudaError_t launch_up_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
-    auto* kern = adapter_up_kernel<MT, F32, FEW>;
-    const size_t smem = (size_t)MT * ((g.rank + 15) / 16) * 3 * 512;   // at most 24 KB
+template <bool F32>
+cudaError_t launch_up_few(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
+    auto* kern = adapter_up_few_kernel<F32>;
+    const size_t smem = (size_t)((g.rank + 15) / 16) * 3 * 512;   // at most 12 KB
     int ctas = 0;
     cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
     if (e != cudaSuccess) return e;
     const int64_t most = (int64_t)device_info().sm_count * ctas;
     // four tiles a warp share the fragments of v, fewer where that leaves CTAs idle
     const int tiles = (g.N / g.parts + 31) / 32;
-    const int64_t rows = blocks * (FEW ? 1 : kManyRows / (MT * 16)) * g.parts;
     int cols = 4 * kWarps;
-    while (cols > kWarps && rows * ((tiles + cols - 1) / cols) < 2 * most) cols /= 2;
-    const int64_t items = rows * ((tiles + cols - 1) / cols);
+    while (cols > kWarps && blocks * g.parts * ((tiles + cols - 1) / cols) < 2 * most) cols /= 2;
+    const int64_t items = blocks * g.parts * ((tiles + cols - 1) / cols);
     return launch_pdl(pdl_enabled(), kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g, cols);
 }
 
-template <bool FEW>
-cudaError_t launch_up(const AdapterArgs& g, int64_t blocks, bool f32, cudaStream_t st) {
-    constexpr int MT = FEW ? 1 : 2;
-    return f32 ? launch_up_as<MT, true, FEW>(g, blocks, st) : launch_up_as<MT, false, FEW>(g, blocks, st);
+template <int KS, bool F32>
+cudaError_t launch_up_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
+    auto* kern = adapter_up_kernel<KS, F32>;
+    const size_t smem = UpTile<KS, F32>::kBytes;
+    int ctas = 0;
+    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (int64_t)device_info().sm_count * ctas;
+    const int64_t tiles = blocks * g.parts * ((g.N / g.parts + kUpCols - 1) / kUpCols);
+    return launch_pdl(pdl_enabled(), kern, dim3((unsigned)(tiles < most ? tiles : most)), dim3(kThreads), smem, st, g);
+}
+
+template <bool F32>
+cudaError_t launch_up(const AdapterArgs& g, int64_t blocks, bool few, cudaStream_t st) {
+    if (few) return launch_up_few<F32>(g, blocks, st);
+    if (g.rank <= 16) return launch_up_as<1, F32>(g, blocks, st);
+    if (g.rank <= 32) return launch_up_as<2, F32>(g, blocks, st);
+    if (g.rank <= 64) return launch_up_as<4, F32>(g, blocks, st);
+    return launch_up_as<8, F32>(g, blocks, st);
 }
 
 cudaError_t launch_plan(const AdapterArgs& g, int64_t slots, int32_t* counts, cudaStream_t st) {
@@ -699,12 +855,11 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     cudaError_t e;
     if (few) {
         e = launch_down<true>(g, l.blocks, st);
-        if (e == cudaSuccess) e = launch_up<true>(g, l.blocks, f32, st);
-    } else {
+        } else {
         e = launch_plan(g, slots, reinterpret_cast<int32_t*>(ws + l.counts), st);
         if (e == cudaSuccess) e = launch_down<false>(g, l.blocks, st);
-        if (e == cudaSuccess) e = launch_up<false>(g, l.blocks, f32, st);
     }
+    if (e == cudaSuccess) e = f32 ? launch_up<true>(g, l.blocks, few, st) : launch_up<false>(g, l.blocks, few, st);
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;
     if (!opts || !opts->validate) return CHORD_OK;
     int32_t code = 0;

@@ -27,6 +27,14 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Four 8 x 8 matrices of 16-bit numbers, lane l gives the address of row l mod 8 of matrix l / 8.
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // What one warp multiplies: MT tiles of 16 rows of x, NT tiles of eight weight rows.  Rows that are not
 // there are any others: their sums are not looked at.
 template <int MT, int NT>
@@ -161,12 +169,6 @@ struct Staged {
     __device__ __forceinline__ static void fill(uint32_t dst, const __nv_bfloat16* src, bool in) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
     }
-    __device__ __forceinline__ static void ldsm(uint32_t (&r)[4], uint32_t addr) {
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                     : "r"(addr)
-                     : "memory");
-    }
     __device__ __forceinline__ void multiply(uint32_t st) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const int ar = (warp & 3) * 16 + (lane & 15), br = (lane >> 4) * 8 + (lane & 7);
@@ -174,13 +176,13 @@ struct Staged {
         for (int q = 0; q < 2; ++q) {
             const int kk = (warp >> 2) * 2 + q;
             uint32_t a[4];
-            ldsm(a, st + (uint32_t)ar * 128u + (uint32_t)(((kk * 2 + (lane >> 4)) ^ (ar & 7)) << 4));
+            ldsm4(a, st + (uint32_t)ar * 128u + (uint32_t)(((kk * 2 + (lane >> 4)) ^ (ar & 7)) << 4));
 #pragma unroll
             for (int t = 0; t < NT; t += 2) {
                 uint32_t b[4];
                 // with one tile of weights the second half of the lanes reads its rows again
                 const int r = t * 8 + (NT > 1 ? br : (lane & 7));
-                ldsm(b, st + kRows * 128u + (uint32_t)r * 128u + (uint32_t)(((kk * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+                ldsm4(b, st + kRows * 128u + (uint32_t)r * 128u + (uint32_t)(((kk * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
                 mma(acc[t], a[0], a[1], a[2], a[3], b[0], b[1]);
                 if (t + 1 < NT) mma(acc[t + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
             }

@@ -17,6 +17,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "chord_common.cuh"
 #include "chord_internal.h"
 #include "chord_tcgen05.cuh"
@@ -51,10 +53,11 @@ struct AdapterArgs {
     int max_splits, target;       // K slices: as many as make `target` items
     float* v;                     // [slices, P, R]
     // the plan, for more than kFewPairs pairs
-    int32_t* nblocks;
+    int32_t* nblocks;             // [2]: blocks, sixteens
     int32_t* block_slot;
     int32_t* block_count;         // rows of each block
     int32_t* rows;                // [blocks, kManyRows]
+    int32_t* sixteens;            // up to 16 rows of a block that hold any: 4 block + place
     int* err;
 };
 
@@ -290,10 +293,14 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up_few_kernel(const Adapt
                     float4 f = make_float4(0, 0, 0, 0);
                     if (p >= 0 && k < g.rank) {
                         const float* from = g.v + (int64_t)p * g.R + part * g.rank + k;
-                        f = *reinterpret_cast<const float4*>(from);
-                        for (int z = 1; z < splits; ++z) {
-                            const float4 o = *reinterpret_cast<const float4*>(from + (int64_t)z * g.P * g.R);
-                            f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+                        const int64_t slice = (int64_t)g.P * g.R;
+                        for (int z = 0; z < splits; z += 4) {   // four slices' loads in flight, added in order
+                            float4 o[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[i] = *reinterpret_cast<const float4*>(from + min(z + i, splits - 1) * slice);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (z + i < splits) f.x += o[i].x, f.y += o[i].y, f.z += o[i].z, f.w += o[i].w;
                         }
                     }
                     split3(f.x * scale, f.y * scale, r[0][h], r[1][h], r[2][h]);
@@ -368,161 +375,267 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up_few_kernel(const Adapt
     }
 }
 
-// Many pairs: the tiles of 64 columns of all blocks of the plan are dealt to the CTAs in equal ranges.  A
-// stage, base's tile and B's, comes by cp.async, kUpStages - 1 of them are on their way.  Warp w has rows 16 (w mod 4) and 32 of the
-// columns; its rows of v stay in registers as fragments of the instruction's A side (KS k steps of 16).
-constexpr int kUpCols = 64, kUpStages = 4;
+// Many pairs.  A warp has 16 rows of a block, its rows of v in registers as fragments of the instruction's A side (KS k
+// steps of 16), and takes 32 columns at a time, base's pieces of the next tile on their way in registers.
+// Row i of the instruction's 8-column tile j is this one of the 32 columns, so that lane (g, c) ends with whole
+// 16-byte pieces of its rows: bf16 columns 8 c .. 8 c + 7, FP32 columns 4 c .. 4 c + 3 and 16 more.
+template <bool F32>
+__device__ __forceinline__ int column_of(int j, int i) {
+    return F32 ? 16 * (j >> 1) + 4 * (i >> 1) + 2 * (j & 1) + (i & 1) : 8 * (i >> 1) + 2 * j + (i & 1);
+}
+
+constexpr int kUpThreads = 128;
 
 template <int KS, bool F32>
-struct UpTile {
-    static constexpr int kEsize = F32 ? 4 : 2;
-    static constexpr int kRowPitch = kUpCols * kEsize + 16;                 // padded: neighbouring rows in other banks
-    static constexpr int kBase = kManyRows * kRowPitch;
-    static constexpr int kBPitch = KS * 32 + 16;                            // likewise
-    static constexpr int kBPieces = (kUpCols * KS * 2 + kThreads - 1) / kThreads;   // 16-byte pieces of B a thread copies
-    static constexpr int kStage = kBase + kUpCols * kBPitch;
-    static constexpr size_t kBytes = (size_t)kUpStages * kStage;
+struct UpRows {
+    using Out = typename std::conditional<F32, float, __nv_bfloat16>::type;
+    static constexpr int kY = F32 ? 2 : 1, kFirst = F32 ? 4 : 8;   // 16-byte pieces of a row that a lane has; elements of one
+    struct Y {
+        uint4 y[2][kY];
+    };
+    uint32_t a[KS][3][4];
+    const Out* from[2];
+    Out* to[2];
+    bool live[2], adds;
+
+    // Rows p[0] and p[1] of y (-1: not there, reads row `other` and writes nothing) in this part's columns.
+    __device__ __forceinline__ void begin(const AdapterArgs& g, const int (&p)[2], int other, int slot, int part, int Np, int splits) {
+        const int c = threadIdx.x & 3;
+        adds = slot >= 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            live[h] = p[h] >= 0;
+            const int q = live[h] ? p[h] : other;
+            from[h] = static_cast<const Out*>(g.base) + q * g.base_stride + part * Np + kFirst * c;
+            to[h] = static_cast<Out*>(g.y) + q * g.y_stride + part * Np + kFirst * c;
+        }
+        if (!adds) return;
+        // v: slices added in order, scaled, in three parts; of each k step the columns 2 c, 2 c + 1 and 8 more.  All of a
+        // slice's loads are in flight together.
+        const float scale = g.scale ? g.scale[slot / g.E] : 1.0f;
+        float2 f[KS][2][2] = {};
+        const float* v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[h] = g.v + (int64_t)(live[h] ? p[h] : other) * g.R + part * g.rank + 2 * c;
+        for (int z = 0; z < splits; ++z) {
+            float2 o[KS][2][2];
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)   // no branch: what is not there is read elsewhere and left out
+                        o[s][h][u] = *reinterpret_cast<const float2*>(v[h] + (16 * s + 8 * u < g.rank ? 16 * s + 8 * u : 0));
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const bool in = live[h] && 16 * s + 8 * u < g.rank;
+                        f[s][h][u].x += in ? o[s][h][u].x : 0.0f;
+                        f[s][h][u].y += in ? o[s][h][u].y : 0.0f;
+                    }
+            v[0] += (int64_t)g.P * g.R;
+            v[1] += (int64_t)g.P * g.R;
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    split3(f[s][h][u].x * scale, f[s][h][u].y * scale, a[s][0][2 * u + h], a[s][1][2 * u + h], a[s][2][2 * u + h]);
+    }
+    __device__ __forceinline__ void load(Y& x, int n0, int Np) const {
+        const int c = threadIdx.x & 3;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int z = 0; z < kY; ++z)
+                if (n0 + z * 16 + kFirst * c < Np) x.y[h][z] = *reinterpret_cast<const uint4*>(from[h] + n0 + z * 16);
+    }
+    // One k step; instructions on one accumulator are four apart.
+    __device__ __forceinline__ void multiply(float (&d)[4][4], int s, const uint32_t (&w)[4][2]) const {
+#pragma unroll
+        for (int t3 = 2; t3 >= 0; --t3)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) thin::mma(d[j], a[s][t3][0], a[s][t3][1], a[s][t3][2], a[s][t3][3], w[j][0], w[j][1]);
+    }
+    __device__ __forceinline__ void store(const Y& x, const float (&d)[4][4], int n0, int Np) const {
+        const int c = threadIdx.x & 3;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int z = 0; z < kY; ++z) {
+                if (!live[h] || n0 + z * 16 + kFirst * c >= Np) continue;
+                uint4 o = x.y[h][z];
+                if (adds) {
+                    if constexpr (F32) {
+                        o.x = __float_as_uint(__uint_as_float(o.x) + d[2 * z][2 * h]);
+                        o.y = __float_as_uint(__uint_as_float(o.y) + d[2 * z][2 * h + 1]);
+                        o.z = __float_as_uint(__uint_as_float(o.z) + d[2 * z + 1][2 * h]);
+                        o.w = __float_as_uint(__uint_as_float(o.w) + d[2 * z + 1][2 * h + 1]);
+                    } else {
+                        o.x = Eight<false>::pair(o.x, d[0][2 * h], d[0][2 * h + 1]);
+                        o.y = Eight<false>::pair(o.y, d[1][2 * h], d[1][2 * h + 1]);
+                        o.z = Eight<false>::pair(o.z, d[2][2 * h], d[2][2 * h + 1]);
+                        o.w = Eight<false>::pair(o.w, d[3][2 * h], d[3][2 * h + 1]);
+                    }
+                }
+                *reinterpret_cast<uint4*>(to[h] + n0 + z * 16) = o;
+            }
+    }
+};
+
+// Ranks up to 16: the work of all rows, sixteen at a time, is dealt to the warps in equal ranges (blocks hold 1 to 64
+// rows), B's pieces come straight from global memory a tile ahead, nothing is shared and no warp waits for another.
+template <bool F32>
+__global__ void __launch_bounds__(kUpThreads, 4) adapter_up_small_kernel(const AdapterArgs g) {
+    using Rows = UpRows<1, F32>;
+    const int lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
+    pdl_wait();
+    const int splits = slices_of(g, g.nblocks[0]);
+    const int Np = g.N / g.parts, tiles = (Np + 31) / 32;
+    const int64_t total = (int64_t)g.nblocks[1] * g.parts * tiles, warps = (int64_t)gridDim.x * (kUpThreads / 32);
+    const int64_t warp = (int64_t)blockIdx.x * (kUpThreads / 32) + (threadIdx.x >> 5), end = total * (warp + 1) / warps;
+    for (int64_t at = total * warp / warps; at < end;) {
+        int t0, part;
+        const int u = (int)divmod_idx(divmod_idx(at, tiles, t0), g.parts, part), t1 = (int)min((int64_t)tiles, t0 + (end - at));
+        at += t1 - t0;
+        const int where = g.sixteens[u], b = where >> 2, r0 = (where & 3) * 16, count = g.block_count[b], slot = g.block_slot[b];
+        const int32_t* rows = g.rows + (int64_t)b * kManyRows + r0;
+        const int p[2] = {r0 + gr < count ? rows[gr] : -1, r0 + gr + 8 < count ? rows[gr + 8] : -1};
+        struct Tile {
+            typename Rows::Y y;
+            uint32_t w[4][2];
+        } x, y;
+        Rows r;
+        const __nv_bfloat16* bw = g.B + ((int64_t)max(slot, 0) * g.N + part * Np) * g.rank + 2 * c;
+        auto load = [&](Tile& z, int t) {
+            r.load(z.y, t * 32, Np);
+            if (slot < 0) return;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int col = t * 32 + column_of<F32>(j, gr);
+                const __nv_bfloat16* from = bw + (int64_t)col * g.rank;
+                z.w[j][0] = col < Np ? *reinterpret_cast<const uint32_t*>(from) : 0u;
+                z.w[j][1] = col < Np && g.rank > 8 ? *reinterpret_cast<const uint32_t*>(from + 8) : 0u;
+            }
+        };
+        auto finish = [&](Tile& z, int t) {
+            float d[4][4] = {};
+            if (slot >= 0) r.multiply(d, 0, z.w);
+            r.store(z.y, d, t * 32, Np);
+        };
+        r.begin(g, p, rows[0], slot, part, Np, splits);
+        load(x, t0);
+        for (int t = t0; t < t1; t += 2) {
+            if (t + 1 < t1) load(y, t + 1);
+            finish(x, t);
+            if (t + 1 >= t1) break;
+            if (t + 2 < t1) load(x, t + 2);
+            finish(y, t + 1);
+        }
+    }
+}
+
+// Larger ranks: B's bytes and the instructions weigh as much as base and y, so the four warps of a CTA take the rows of a
+// block and share B, 128 columns a stage, that cp.async copies two stages ahead.
+template <int KS>
+struct UpStage {
+    static constexpr int kCols = 128, kStages = 3;
+    static constexpr int kPitch = KS * 32 + 16;                 // padded: neighbouring rows lie in other banks
+    static constexpr int kBytes = kCols * kPitch;
+    static constexpr int kPieces = kCols * KS * 2 / kUpThreads; // 16-byte pieces a thread copies
 };
 
 template <int KS, bool F32>
-__global__ void __launch_bounds__(kThreads, KS <= 4 ? 2 : 1) adapter_up_kernel(const AdapterArgs g) {
-    using T = UpTile<KS, F32>;
-    constexpr int kPieces = kUpCols * T::kEsize / 16, kRowsAtOnce = kThreads / kPieces, kPasses = kManyRows / kRowsAtOnce;
+__global__ void __launch_bounds__(kUpThreads, KS <= 4 ? 3 : 2) adapter_up_kernel(const AdapterArgs g) {
+    using T = UpStage<KS>;
+    using Rows = UpRows<KS, F32>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int32_t rows[kManyRows];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2;
     pdl_wait();
-    const int n = *g.nblocks, splits = slices_of(g, n);
-    const int Np = g.N / g.parts, tiles = (Np + kUpCols - 1) / kUpCols;
+    const int n = g.nblocks[0], splits = slices_of(g, n);
+    const int Np = g.N / g.parts, chunks = (Np + T::kCols - 1) / T::kCols;
     const uint32_t base = smem_u32(smem);
-    const int b_pieces = g.rank / 8;
-    // Row i of the 8-column tile t of a matrix instruction is column 8 (i / 2) + 2 t + (i & 1) of 32, so that lane
-    // (g, c) ends with columns 8 c .. 8 c + 7; B is stored in the tiles' order, where neighbouring rows
-    // lie in different banks.  ldmatrix: matrix j of two tiles is k half j & 1 of tile j >> 1.
-    const uint32_t b_at = (uint32_t)(T::kBase + ((warp >> 2) * 32 + (lane >> 4) * 8 + (lane & 7)) * T::kBPitch + ((lane >> 3) & 1) * 16);
-    int b_col[T::kBPieces], b_to[T::kBPieces];
+    // Columns are stored in the order of the instruction's rows.  ldmatrix: matrix j of two 8-column tiles is k half j & 1
+    // of tile j >> 1.
+    const uint32_t b_at = (uint32_t)(((lane >> 4) * 8 + (lane & 7)) * T::kPitch + ((lane >> 3) & 1) * 16);
+    int b_col[T::kPieces], b_to[T::kPieces];
 #pragma unroll
-    for (int h = 0; h < T::kBPieces; ++h) {
-        const int u = threadIdx.x + h * kThreads, col = u / b_pieces, k = u - col * b_pieces;
-        b_col[h] = col < kUpCols ? col : INT32_MAX;
-        b_to[h] = T::kBase + ((col & 32) | (col >> 1 & 3) * 8 | (col >> 3 & 3) * 2 | (col & 1)) * T::kBPitch + k * 16;
+    for (int h = 0; h < T::kPieces; ++h) {
+        const int u = threadIdx.x + h * kUpThreads, row = u / (g.rank / 8), k = u - row * (g.rank / 8);
+        b_col[h] = row < T::kCols ? row : INT32_MAX;
+        const int w = row & 31;   // column w of 32 is row i of tile j
+        const int j = F32 ? (w >> 4) * 2 + (w >> 1 & 1) : w >> 1 & 3, i = F32 ? (w >> 2 & 3) * 2 + (w & 1) : (w >> 3) * 2 + (w & 1);
+        b_to[h] = ((row & ~31) + j * 8 + i) * T::kPitch + k * 16;
     }
-    const int64_t total = (int64_t)n * g.parts * tiles, end = total * (blockIdx.x + 1) / gridDim.x;
+    const int64_t total = (int64_t)n * g.parts * chunks, end = total * (blockIdx.x + 1) / gridDim.x;
     for (int64_t at = total * blockIdx.x / gridDim.x; at < end;) {
-        int t0, part;
-        const int b = (int)divmod_idx(divmod_idx(at, tiles, t0), g.parts, part), t1 = (int)min((int64_t)tiles, t0 + (end - at));
-        at += t1 - t0;
+        int c0, part;
+        const int b = (int)divmod_idx(divmod_idx(at, chunks, c0), g.parts, part), c1 = (int)min((int64_t)chunks, c0 + (end - at));
+        at += c1 - c0;
         const int slot = block_rows<false, kManyRows>(g, nullptr, b, rows);
-        // copies of a tile
-        const int piece = threadIdx.x % kPieces, row0 = threadIdx.x / kPieces;
-        const uint8_t* from[kPasses];
-#pragma unroll
-        for (int h = 0; h < kPasses; ++h) {
-            const int p = rows[row0 + h * kRowsAtOnce];
-            from[h] = p < 0 ? nullptr
-                            : static_cast<const uint8_t*>(g.base) + (p * g.base_stride + part * Np) * T::kEsize + piece * 16;
-        }
-        const __nv_bfloat16* bsrc = g.B + ((int64_t)max(slot, 0) * g.N + part * Np) * g.rank;
-        int next = t0, slot_in = 0, slot_out = 0;
+        const __nv_bfloat16* src = g.B + ((int64_t)max(slot, 0) * g.N + part * Np) * g.rank + threadIdx.x * 8;
+        int next = c0, slot_in = 0, slot_out = 0;
         auto issue = [&]() {
-            if (next < t1) {
-                const uint32_t st = base + (uint32_t)(slot_in * T::kStage);
-                const int n0 = next * kUpCols;
-                if (n0 + piece * (16 / T::kEsize) < Np)
+            if (next < c1 && slot >= 0) {
+                const int n0 = next * T::kCols;
+                const uint32_t st = base + (uint32_t)(slot_in * T::kBytes);
 #pragma unroll
-                    for (int h = 0; h < kPasses; ++h)
-                        if (from[h]) cp_async16(st + (uint32_t)((row0 + h * kRowsAtOnce) * T::kRowPitch + piece * 16), from[h] + (int64_t)n0 * T::kEsize);
-                if (slot >= 0) {
-                    const __nv_bfloat16* src = bsrc + (int64_t)n0 * g.rank + threadIdx.x * 8;
-#pragma unroll
-                    for (int h = 0; h < T::kBPieces; ++h)
-                        if (b_col[h] < Np - n0) cp_async16(st + (uint32_t)b_to[h], src + h * kThreads * 8);
-                }
-                ++next;
+                for (int h = 0; h < T::kPieces; ++h)
+                    if (b_col[h] < Np - n0) cp_async16(st + (uint32_t)b_to[h], src + (int64_t)n0 * g.rank + h * kUpThreads * 8);
             }
+            ++next;
             cp_async_commit();
-            if (++slot_in == kUpStages) slot_in = 0;
+            if (++slot_in == T::kStages) slot_in = 0;
         };
         // a rank that ends inside a k step: zeros behind it, in every stage
         if (g.rank % 16)
-            for (int u = threadIdx.x; u < kUpStages * kUpCols; u += kThreads)
-                *reinterpret_cast<uint4*>(smem + u / kUpCols * T::kStage + T::kBase + u % kUpCols * T::kBPitch + g.rank * 2) = make_uint4(0, 0, 0, 0);
+            for (int u = threadIdx.x; u < T::kStages * T::kCols; u += kUpThreads)
+                *reinterpret_cast<uint4*>(smem + u * T::kPitch + g.rank * 2) = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int k = 0; k < kUpStages - 1; ++k) issue();
-        // this warp's rows of v: slices added in order, scaled, in three parts
-        const int r0 = (warp & 3) * 16, p0 = rows[r0 + gr], p1 = rows[r0 + gr + 8];
+        for (int k = 0; k < T::kStages - 1; ++k) issue();
+        const int r0 = warp * 16, p[2] = {rows[r0 + gr], rows[r0 + gr + 8]};
         const bool busy = rows[r0] >= 0;   // rows of a block are a prefix
-        uint32_t a[KS][3][4];
-        if (slot >= 0 && busy) {
-            const float scale = g.scale ? g.scale[slot / g.E] : 1.0f;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const int k = 16 * s + 2 * c;   // and k + 1, k + 8, k + 9
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int p = h ? p1 : p0;
-                    float4 f = make_float4(0, 0, 0, 0);
-                    if (p >= 0 && k < g.rank) {
-                        const float* v = g.v + (int64_t)p * g.R + part * g.rank + k;
-                        const bool up = k + 8 < g.rank;
-                        for (int z = 0; z < splits; ++z, v += (int64_t)g.P * g.R) {
-                            const float2 l = *reinterpret_cast<const float2*>(v), r = up ? *reinterpret_cast<const float2*>(v + 8) : make_float2(0, 0);
-                            f.x += l.x, f.y += l.y, f.z += r.x, f.w += r.y;
-                        }
-                    }
-                    split3(f.x * scale, f.y * scale, a[s][0][h], a[s][1][h], a[s][2][h]);
-                    split3(f.z * scale, f.w * scale, a[s][0][2 + h], a[s][1][2 + h], a[s][2][2 + h]);
-                }
-            }
+        Rows r;
+        typename Rows::Y y[2];
+        if (busy) {
+            r.begin(g, p, rows[r0], slot, part, Np, splits);
+            r.load(y[0], c0 * T::kCols, Np);
         }
-        const int mycol = (warp >> 2) * 32;
-        for (int t = t0; t < t1; ++t) {
-            cp_async_wait<kUpStages - 2>();
+        for (int ch = c0; ch < c1; ++ch) {
+            cp_async_wait<T::kStages - 2>();
             __syncthreads();   // the stage is there for all, and the one before has been read by all
             issue();
-            const uint32_t st = base + (uint32_t)(slot_out * T::kStage);
-            if (++slot_out == kUpStages) slot_out = 0;
-            const int n0 = t * kUpCols + mycol;
-            if (!busy || n0 >= Np) continue;
-            float d[4][4];
+            const uint32_t st = base + (uint32_t)(slot_out * T::kBytes) + b_at;
+            if (++slot_out == T::kStages) slot_out = 0;
+            if (!busy) continue;
+            const int end_col = min(Np, (ch + 1) * T::kCols);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int q = 0; q < T::kCols / 32; ++q) {
+                const int n0 = ch * T::kCols + q * 32;
+                if (n0 >= end_col) break;
+                if (n0 + 32 < Np && (ch + 1 < c1 || q + 1 < T::kCols / 32)) r.load(y[(q + 1) & 1], n0 + 32, Np);
+                float d[4][4] = {};
+                if (slot >= 0) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) d[j][u] = 0.0f;
-            if (slot >= 0) {
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    if (16 * s >= g.rank) break;
-                    uint32_t w[2][4];
-                    thin::ldsm4(w[0], st + b_at + (uint32_t)(s * 32));
-                    thin::ldsm4(w[1], st + b_at + (uint32_t)(16 * T::kBPitch + s * 32));
-                    // instructions on one accumulator are four apart
-#pragma unroll
-                    for (int t3 = 2; t3 >= 0; --t3)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            thin::mma(d[j], a[s][t3][0], a[s][t3][1], a[s][t3][2], a[s][t3][3], w[j >> 1][(j & 1) * 2], w[j >> 1][(j & 1) * 2 + 1]);
-                }
-            }
-            if (n0 + 8 * c < Np) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int p = h ? p1 : p0;
-                    if (p < 0) continue;
-                    float e[8];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        e[2 * u] = d[u][2 * h];
-                        e[2 * u + 1] = d[u][2 * h + 1];
+                    for (int s = 0; s < KS; ++s) {
+                        if (16 * s >= g.rank) break;
+                        uint32_t w[2][4];
+                        thin::ldsm4(w[0], st + (uint32_t)(q * 32 * T::kPitch + s * 32));
+                        thin::ldsm4(w[1], st + (uint32_t)((q * 32 + 16) * T::kPitch + s * 32));
+                        const uint32_t v[4][2] = {{w[0][0], w[0][1]}, {w[0][2], w[0][3]}, {w[1][0], w[1][1]}, {w[1][2], w[1][3]}};
+                        r.multiply(d, s, v);
                     }
-                    Eight<F32> o;
-                    o.load(smem + (st - base) + (r0 + gr + 8 * h) * T::kRowPitch, mycol + 8 * c);
-                    if (slot >= 0) o.add(e);
-                    o.store(g.y, p * g.y_stride + part * Np + n0 + 8 * c);
                 }
+                r.store(y[q & 1], d, n0, Np);
             }
         }
-        cp_async_wait<0>();   // empty groups
+        cp_async_wait<0>();
     }
 }
 
@@ -563,22 +676,40 @@ __device__ __forceinline__ int block_scan(int v, int& total) {
     return x - v + (warp ? sums[warp - 1] : 0);
 }
 
-// Counts to first positions; the blocks' slots and rows.
+// The n pairs of a slot: blocks from b on, sixteens from u on.
+__device__ __forceinline__ void lay_out(const AdapterArgs& g, int slot, int n, int& b, int& u) {
+    for (int k = 0; k < n; k += kManyRows, ++b) {
+        const int here = min(n - k, kManyRows);
+        g.block_slot[b] = slot;
+        g.block_count[b] = here;
+        for (int j = 0; j < here; j += 16) g.sixteens[u++] = 4 * b + j / 16;
+    }
+}
+__device__ __forceinline__ int blocks_for(int n) { return (n + kManyRows - 1) / kManyRows; }
+// n / 64 full blocks of four sixteens and the rest's
+__device__ __forceinline__ int sixteens_for(int n) { return (n + 15) / 16; }
+
+// Counts to first positions; the blocks and sixteens.
 __device__ __forceinline__ void plan_scan(const PlanArgs& a, int32_t* counts) {
     const int per = (a.nslots + kPlanThreads - 1) / kPlanThreads;
     const int s0 = threadIdx.x * per, s1 = min(s0 + per, a.nslots);
-    int mine = 0, total;
-    for (int s = s0; s < s1; ++s) mine += (counts[s] + kManyRows - 1) / kManyRows;
-    int b = block_scan(mine, total);
+    int blocks = 0, sixteens = 0, total_b, total_u;
+    for (int s = s0; s < s1; ++s) {
+        blocks += blocks_for(counts[s]);
+        sixteens += sixteens_for(counts[s]);
+    }
+    int b = block_scan(blocks, total_b);
+    __syncthreads();
+    int u = block_scan(sixteens, total_u);
     for (int s = s0; s < s1; ++s) {
         const int n = counts[s];
         counts[s] = b * kManyRows;
-        for (int k = 0; k < n; k += kManyRows, ++b) {
-            a.g.block_slot[b] = s - 1;
-            a.g.block_count[b] = min(n - k, kManyRows);
-        }
+        lay_out(a.g, s - 1, n, b, u);
     }
-    if (threadIdx.x == 0) *a.g.nblocks = total;
+    if (threadIdx.x == 0) {
+        a.g.nblocks[0] = total_b;
+        a.g.nblocks[1] = total_u;
+    }
 }
 
 // This pair's place among those of its slot; the lanes of a warp with one slot for all (the tokens of a
@@ -607,7 +738,7 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, int32_t v) {
 // counts, and hands every CTA the position of its first pair of each slot.
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanArgs a) {
     extern __shared__ int32_t counts_s[];
-    __shared__ int32_t blocks_before[kPlanCtas];   // blocks of each CTA's slots
+    __shared__ int32_t before[kPlanCtas];   // blocks of each CTA's slots, and sixteens in the upper half (below 2^15 both)
     pdl_trigger();
     const int rank = (int)tc5::cluster_rank();
     int slot[kPlanPerThread], place[kPlanPerThread];
@@ -629,17 +760,21 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         int n = 0;
 #pragma unroll
         for (int z = 0; z < kPlanCtas; ++z) n += ld_cluster(counts_of(z, s));
-        mine += (n + kManyRows - 1) / kManyRows;
+        mine += blocks_for(n) + (sixteens_for(n) << 16);
     }
-    int b = block_scan(mine, total);
-    if (threadIdx.x < kPlanCtas) st_cluster(tc5::at_cta(smem_u32(blocks_before + rank), threadIdx.x), total);
+    int first = block_scan(mine, total);
+    if (threadIdx.x < kPlanCtas) st_cluster(tc5::at_cta(smem_u32(before + rank), threadIdx.x), total);
     tc5::cluster_sync();
     int all = 0;
     for (int z = 0; z < kPlanCtas; ++z) {
-        if (z < rank) b += blocks_before[z];
-        all += blocks_before[z];
+        if (z < rank) first += before[z];
+        all += before[z];
     }
-    if (rank == 0 && threadIdx.x == 0) *a.g.nblocks = all;
+    if (rank == 0 && threadIdx.x == 0) {
+        a.g.nblocks[0] = all & 0xffff;
+        a.g.nblocks[1] = all >> 16;
+    }
+    int b = first & 0xffff, u = first >> 16;
     for (int s = s0; s < s1; ++s) {
         int n = 0;
 #pragma unroll
@@ -649,10 +784,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             st_cluster(at, b * kManyRows + n);
             n += here;
         }
-        for (int k = 0; k < n; k += kManyRows, ++b) {
-            a.g.block_slot[b] = s - 1;
-            a.g.block_count[b] = min(n - k, kManyRows);
-        }
+        lay_out(a.g, s - 1, n, b, u);
     }
     tc5::cluster_sync();
 #pragma unroll
@@ -680,7 +812,7 @@ __global__ void __launch_bounds__(256) adapter_place_kernel(const PlanArgs a) {
 struct Layout {
     int max_splits;
     int64_t blocks;   // at most
-    size_t v, nblocks, block_slot, block_count, rows, counts, bytes;
+    size_t v, nblocks, block_slot, block_count, rows, sixteens, counts, bytes;
 };
 
 Layout layout_of(int64_t P, int64_t slots, int R) {
@@ -697,10 +829,11 @@ Layout layout_of(int64_t P, int64_t slots, int R) {
     };
     l.v = take((size_t)l.max_splits * P * R * 4);
     if (!few) {
-        l.nblocks = take(4);
+        l.nblocks = take(8);
         l.block_slot = take((size_t)l.blocks * 4);
         l.block_count = take((size_t)l.blocks * 4);
         l.rows = take((size_t)l.blocks * kManyRows * 4);
+        l.sixteens = take((size_t)(l.blocks + P / 16) * 4);
         l.counts = take((size_t)(slots + 1) * 4);
     }
     return l;
@@ -746,25 +879,20 @@ cudaError_t launch_up_few(const AdapterArgs& g, int64_t blocks, cudaStream_t st)
     return launch_pdl(pdl_enabled(), kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g, cols);
 }
 
-template <int KS, bool F32>
-cudaError_t launch_up_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
-    auto* kern = adapter_up_kernel<KS, F32>;
-    const size_t smem = UpTile<KS, F32>::kBytes;
+cudaError_t launch_up_as(void (*kern)(AdapterArgs), const AdapterArgs& g, size_t smem, cudaStream_t st) {
     int ctas = 0;
-    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
+    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kUpThreads, smem, smem, &ctas);
     if (e != cudaSuccess) return e;
-    const int64_t most = (int64_t)device_info().sm_count * ctas;
-    const int64_t tiles = blocks * g.parts * ((g.N / g.parts + kUpCols - 1) / kUpCols);
-    return launch_pdl(pdl_enabled(), kern, dim3((unsigned)(tiles < most ? tiles : most)), dim3(kThreads), smem, st, g);
+    return launch_pdl(pdl_enabled(), kern, dim3((unsigned)(device_info().sm_count * ctas)), dim3(kUpThreads), smem, st, g);
 }
 
 template <bool F32>
 cudaError_t launch_up(const AdapterArgs& g, int64_t blocks, bool few, cudaStream_t st) {
     if (few) return launch_up_few<F32>(g, blocks, st);
-    if (g.rank <= 16) return launch_up_as<1, F32>(g, blocks, st);
-    if (g.rank <= 32) return launch_up_as<2, F32>(g, blocks, st);
-    if (g.rank <= 64) return launch_up_as<4, F32>(g, blocks, st);
-    return launch_up_as<8, F32>(g, blocks, st);
+    if (g.rank <= 16) return launch_up_as(adapter_up_small_kernel<F32>, g, 0, st);
+    if (g.rank <= 32) return launch_up_as(adapter_up_kernel<2, F32>, g, UpStage<2>::kStages * UpStage<2>::kBytes, st);
+    if (g.rank <= 64) return launch_up_as(adapter_up_kernel<4, F32>, g, UpStage<4>::kStages * UpStage<4>::kBytes, st);
+    return launch_up_as(adapter_up_kernel<8, F32>, g, UpStage<8>::kStages * UpStage<8>::kBytes, st);
 }
 
 cudaError_t launch_plan(const AdapterArgs& g, int64_t slots, int32_t* counts, cudaStream_t st) {
@@ -850,7 +978,8 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
                   base, y, base_stride, y_stride, base != y, units, l.max_splits < most ? l.max_splits : most, 2 * di.sm_count,
                   reinterpret_cast<float*>(ws + l.v),
                   reinterpret_cast<int32_t*>(ws + l.nblocks), reinterpret_cast<int32_t*>(ws + l.block_slot),
-                  reinterpret_cast<int32_t*>(ws + l.block_count), reinterpret_cast<int32_t*>(ws + l.rows), di.err};
+                  reinterpret_cast<int32_t*>(ws + l.block_count), reinterpret_cast<int32_t*>(ws + l.rows),
+                  reinterpret_cast<int32_t*>(ws + l.sixteens), di.err};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (few) {

@@ -516,19 +516,35 @@ def chord_moe_layer_few(x, topk_ids, topk_w, E: int, I: int, packed_w13, packed_
         raise ChordError(st, what)
 
 
+# The router and adapter calls are made for single tokens, where the host's time is the call's: one condition passes
+# what a program usually hands over, and only where it fails do the checks one by one say what is wrong, or that
+# nothing is (a row of stride 1, say).
+
+_device = None
+
+
+def _current_device():
+    """Index of the current device; where there is none a number that no tensor's device has."""
+    global _device
+    if _device is None:
+        import torch
+        if not torch.cuda.is_available():
+            return -2
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _device()
+
+
 def _rows(what, name, t, dtypes):
     """A matrix with unit stride along its rows, of one of these types, in device memory."""
     strides = t.stride()
     if t.dtype not in dtypes or len(strides) != 2 or (strides[1] != 1 and t.shape[1] > 1) or not t.is_cuda:
         _refuse(what, name, t, f"{' or '.join(map(str, dtypes))}, 2-dimensional with unit stride along its rows in device memory")
-    return t.data_ptr()
 
 
-def _same_device(what, first, *others):
-    """Every tensor is where the first one is, and that is the current device (the stream's)."""
-    import torch
-    dev = first.get_device()
-    if any(t is not None and t.get_device() != dev for t in others) or (dev >= 0 and dev != torch.cuda.current_device()):
+def _same_device(what, *tensors):
+    """Every tensor is on the current device, the stream's."""
+    dev = {t.get_device() for t in tensors if t is not None}
+    if len(dev) != 1 or (dev != {-1} and dev != {_current_device()}):
         raise ChordError(1, f"{what}: the tensors must be on the current device")
 
 
@@ -543,78 +559,139 @@ def chord_router_split_weights(W, parts, stream=None):
     _check(load().chord_router_split_weights(wp, W.numel(), pp, _s(stream)), what)
 
 
-def chord_router_logits(x, W, logits, opts=None, stream=None):
-    """x bf16 [T, H] (any row stride), W bf16 [E, H] or the parts [3, E, H] of an fp32 one, logits float32 [T, E]."""
+def _check_logits(x, W, logits, types):
     what = "chord_router_logits"
-    types = _dtypes or _types()
-    bf16, shape = types["bf16"], W.shape
-    xp = _rows(what, "x", x, (bf16,))
-    T, H = x.shape
+    _rows(what, "x", x, (types["bf16"],))
+    shape, (T, H) = W.shape, x.shape
     if len(shape) not in (2, 3) or shape[-1] != H:
         _refuse(what, "W", W, f"bf16 [E, {H}] or [3, E, {H}]")
-    E, wp = shape[-2], _dense(what, "W", W, bf16, *shape)
-    out = _dense(what, "logits", logits, types["f32"], T, E)
+    _dense(what, "W", W, types["bf16"], *shape)
+    _dense(what, "logits", logits, types["f32"], T, shape[-2])
     _same_device(what, x, W, logits)
-    st = (_lib or load()).chord_router_logits(xp, x.stride(0), T, wp, shape[0] if len(shape) == 3 else 1, E, H, out,
-                                              None if opts is None else _o(opts), _s(stream))
+
+
+def chord_router_logits(x, W, logits, opts=None, stream=None):
+    """x bf16 [T, H] (any row stride), W bf16 [E, H] or the parts [3, E, H] of an fp32 one, logits float32 [T, E]."""
+    types = _dtypes or _types()
+    bf16, xs, shape, dev = types["bf16"], x.shape, W.shape, _current_device()
+    if not (x.dtype is bf16 and W.dtype is bf16 and logits.dtype is types["f32"] and len(xs) == 2 and x.stride(1) == 1
+            and 2 <= len(shape) <= 3 and shape[-1] == xs[1] and logits.shape == (xs[0], shape[-2]) and W.is_contiguous()
+            and logits.is_contiguous() and x.get_device() == W.get_device() == logits.get_device() == dev):
+        _check_logits(x, W, logits, types)
+        xs = x.shape
+    st = (_lib or load()).chord_router_logits(x.data_ptr(), x.stride(0), xs[0], W.data_ptr(), shape[0] if len(shape) == 3 else 1,
+                                              shape[-2], xs[1], logits.data_ptr(), None if opts is None else _o(opts), _s(stream))
     if st:
-        raise ChordError(st, what)
+        raise ChordError(st, "chord_router_logits")
+
+
+_routes = {}
+
+
+def _route(*fields):
+    """The library's struct of these options, made once for each combination."""
+    how = _routes.get(fields)
+    if how is None:
+        if len(_routes) >= 256:
+            _routes.clear()
+        how = _routes[fields] = ChordRoute(*fields)
+    return how
+
+
+def _check_route(logits, topk_ids, topk_w, bias, types):
+    what, f32 = "chord_moe_route", types["f32"]
+    _rows(what, "logits", logits, (types["bf16"], f32))
+    (T, E), topk = logits.shape, topk_ids.shape[-1]
+    _dense(what, "topk_ids", topk_ids, types["int32"], T, topk)
+    _dense(what, "topk_w", topk_w, f32, T, topk)
+    if bias is not None:
+        _dense(what, "bias", bias, f32, E)
+    _same_device(what, logits, topk_ids, topk_w, bias)
 
 
 def chord_moe_route(logits, topk_ids, topk_w, score: int = SCORE_SOFTMAX, bias=None, groups: int = 1, topk_groups: int = 1,
                     group_best: int = 1, renormalize: bool = True, scale: float = 1.0, first: int = 0, E_local=None,
                     stream=None):
     """logits bf16 or float32 [T, E] (any row stride), topk_ids int32 and topk_w float32 [T, topk] outputs, bias float32 [E]."""
-    what = "chord_moe_route"
     types = _dtypes or _types()
-    f32, bf16 = types["f32"], types["bf16"]
-    lp = _rows(what, "logits", logits, (bf16, f32))
-    (T, E), topk = logits.shape, topk_ids.shape[-1]
-    ip, wp = _dense(what, "topk_ids", topk_ids, types["int32"], T, topk), _dense(what, "topk_w", topk_w, f32, T, topk)
-    bp = None if bias is None else _dense(what, "bias", bias, f32, E)
-    _same_device(what, logits, topk_ids, topk_w, bias)
-    how = ChordRoute(score, groups, topk_groups, group_best, renormalize, scale, first, E - first if E_local is None else E_local)
-    st = (_lib or load()).chord_moe_route(lp, types[logits.dtype], logits.stride(0), T, E, bp, topk, ctypes.byref(how), ip, wp,
-                                          _s(stream))
+    f32, ls, ks, dev = types["f32"], logits.shape, topk_ids.shape, _current_device()
+    code = types.get(logits.dtype)
+    if not (code is not None and topk_ids.dtype is types["int32"] and topk_w.dtype is f32 and len(ls) == 2 and logits.stride(1) == 1
+            and len(ks) == 2 and ks[0] == ls[0] and topk_w.shape == ks and topk_ids.is_contiguous() and topk_w.is_contiguous()
+            and (bias is None or (bias.dtype is f32 and bias.shape == ls[1:] and bias.is_contiguous() and bias.get_device() == dev))
+            and logits.get_device() == topk_ids.get_device() == topk_w.get_device() == dev):
+        _check_route(logits, topk_ids, topk_w, bias, types)
+    how = _route(score, groups, topk_groups, group_best, renormalize, scale, first, ls[1] - first if E_local is None else E_local)
+    st = (_lib or load()).chord_moe_route(logits.data_ptr(), code, logits.stride(0), ls[0], ls[1], None if bias is None else bias.data_ptr(),
+                                          ks[-1], ctypes.byref(how), topk_ids.data_ptr(), topk_w.data_ptr(), _s(stream))
     if st:
-        raise ChordError(st, what)
+        raise ChordError(st, "chord_moe_route")
 
 
 def chord_adapter_workspace_bytes(T: int, topk: int, adapters: int, E: int, rank: int, parts: int = 1) -> int:
     return load().chord_adapter_workspace_bytes(T, topk, adapters, E, rank, parts)
 
 
-def chord_adapter_add(x, a_row_divisor: int, adapter_ids, topk_ids, A, B, scale, base, y, workspace, opts=None, stream=None):
-    """x bf16 [x_rows, K]; adapter_ids int32 [T]; topk_ids int32 [T, topk], or None for one projection; A bf16 [adapters,
-    (E,) parts * rank, K]; B bf16 [adapters, (E,) N, rank]; scale float32 [adapters] or None; base and y [T * topk, N],
-    both bf16 or both float32 (base may be y).  Rows of x, base and y may be any (aligned) stride apart."""
+def _check_adapter(x, adapter_ids, topk_ids, A, B, scale, base, y, workspace, types):
     what = "chord_adapter_add"
-    types = _dtypes or _types()
     bf16, f32, i32 = types["bf16"], types["f32"], types["int32"]
-    xp, bp, yp = _rows(what, "x", x, (bf16,)), _rows(what, "base", base, (bf16, f32)), _rows(what, "y", y, (base.dtype,))
-    (x_rows, K), (P, N) = x.shape, y.shape
-    T = adapter_ids.numel()
-    topk = 1 if topk_ids is None else topk_ids.shape[-1]
+    _rows(what, "x", x, (bf16,))
+    _rows(what, "base", base, (bf16, f32))
+    _rows(what, "y", y, (base.dtype,))
+    K, (P, N) = x.shape[1], y.shape
+    T, topk = adapter_ids.numel(), 1 if topk_ids is None else topk_ids.shape[-1]
     if B.dim() != (3 if topk_ids is None else 4) or B.shape[-2] != N:
         _refuse(what, "B", B, f"bf16 [adapters, {'' if topk_ids is None else 'E, '}{N}, rank]")
-    S, E, rank = B.shape[0], 1 if topk_ids is None else B.shape[1], B.shape[-1]
+    rank = B.shape[-1]
     if A.dim() != B.dim() or A.shape[:-2] != B.shape[:-2] or A.shape[-1] != K or rank == 0 or A.shape[-2] % rank:
         _refuse(what, "A", A, f"bf16 {(*B.shape[:-2], 'parts * rank', K)}")
     if P != T * topk or base.shape != y.shape:
         _refuse(what, "base" if P == T * topk else "y", base if P == T * topk else y, f"[{T * topk}, {N}]")
-    ip = None if topk_ids is None else _dense(what, "topk_ids", topk_ids, i32, T, topk)
-    ap = _dense(what, "adapter_ids", adapter_ids, i32, T)
-    Ap, Bp = _dense(what, "A", A, bf16, *A.shape), _dense(what, "B", B, bf16, *B.shape)
-    sp = None if scale is None else _dense(what, "scale", scale, f32, S)
+    if topk_ids is not None:
+        _dense(what, "topk_ids", topk_ids, i32, T, topk)
+    _dense(what, "adapter_ids", adapter_ids, i32, T)
+    _dense(what, "A", A, bf16, *A.shape)
+    _dense(what, "B", B, bf16, *B.shape)
+    if scale is not None:
+        _dense(what, "scale", scale, f32, B.shape[0])
     if not (workspace.is_contiguous() and workspace.is_cuda):
         _refuse_blob(what, workspace=workspace)
     _same_device(what, x, adapter_ids, topk_ids, A, B, scale, base, y, workspace)
+
+
+def chord_adapter_add(x, a_row_divisor: int, adapter_ids, topk_ids, A, B, scale, base, y, workspace, opts=None, stream=None):
+    """x bf16 [x_rows, K]; adapter_ids int32 [T]; topk_ids int32 [T, topk], or None for one projection; A bf16 [adapters,
+    (E,) parts * rank, K]; B bf16 [adapters, (E,) N, rank]; scale float32 [adapters] or None; base and y [T * topk, N],
+    both bf16 or both float32 (base may be y).  Rows of x, base and y may be any (aligned) stride apart."""
+    types = _dtypes or _types()
+    bf16, i32, dt, dev = types["bf16"], types["int32"], y.dtype, _current_device()
+    xs, ys, As, Bs, code = x.shape, y.shape, A.shape, B.shape, types.get(dt)
+    T = adapter_ids.numel()
+    if topk_ids is None:
+        topk, lead = 1, 1
+        good = len(As) == 3
+    else:
+        ids = topk_ids.shape
+        topk, lead = ids[-1], 2
+        good = (len(As) == 4 and len(ids) == 2 and ids[0] == T and topk_ids.dtype is i32 and topk_ids.is_contiguous()
+                and topk_ids.get_device() == dev)
+    if not (good and code is not None and x.dtype is A.dtype is B.dtype is bf16 and base.dtype is dt and adapter_ids.dtype is i32
+            and len(xs) == len(ys) == 2 and x.stride(1) == base.stride(1) == y.stride(1) == 1 and base.shape == ys
+            and ys[0] == T * topk and As[:lead] == Bs[:lead] and len(Bs) == lead + 2 and Bs[-2] == ys[1] and As[-1] == xs[1]
+            and Bs[-1] and As[-2] % Bs[-1] == 0 and A.is_contiguous() and B.is_contiguous() and adapter_ids.is_contiguous()
+            and workspace.is_contiguous() and x.get_device() == A.get_device() == B.get_device() == base.get_device()
+            == y.get_device() == adapter_ids.get_device() == workspace.get_device() == dev
+            and (scale is None or (scale.dtype is types["f32"] and scale.shape == Bs[:1] and scale.is_contiguous()
+                                   and scale.get_device() == dev))):
+        _check_adapter(x, adapter_ids, topk_ids, A, B, scale, base, y, workspace, types)
+    rank = Bs[-1]
     st = (_lib or load()).chord_adapter_add(
-        xp, x_rows, x.stride(0), a_row_divisor, ap, ip, T, topk, S, E, Ap, Bp, sp, rank, A.shape[-2] // rank, N, K, bp,
-        base.stride(0), yp, y.stride(0), types[y.dtype], workspace.data_ptr(), workspace.nbytes, None if opts is None else _o(opts),
-        _s(stream))
+        x.data_ptr(), xs[0], x.stride(0), a_row_divisor, adapter_ids.data_ptr(), None if topk_ids is None else topk_ids.data_ptr(), T,
+        topk, Bs[0], 1 if topk_ids is None else Bs[1], A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr(), rank,
+        As[-2] // rank, ys[1], xs[1], base.data_ptr(), base.stride(0), y.data_ptr(), y.stride(0), code, workspace.data_ptr(),
+        workspace.nbytes, None if opts is None else _o(opts), _s(stream))
     if st:
-        raise ChordError(st, what)
+        raise ChordError(st, "chord_adapter_add")
 
 
 def chord_selftest_wait_timeout(stream=None):

@@ -21,62 +21,25 @@ struct LogitArgs {
     float* out;
 };
 
-// ---- few tokens: thin products ------------------------------------------------------------
-// A CTA takes MT x 16 tokens, NT x 8 experts and a slice of K (of all parts, one behind the other, the
-// smallest numbers first); the slices of a tile are a cluster.  Each CTA adds its warps' sums up and
-// pushes every CTA the share of the tile that it joins, in rank order.
+// ---- few tokens: thin products (chord_thin.cuh) -------------------------------------------
+// A CTA takes a tile of tokens and experts and a slice of K (of all parts, one behind the other, the smallest
+// numbers first); the slices of a tile are a cluster.  Each CTA pushes every one the share of
+// its sums that that one adds up, in rank order.
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-template <int MT, int NT>
-__global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const LogitArgs a, int splits) {
-    using Warp = thin::Warp<MT, NT>;
-    constexpr int kTile = Warp::kRows * Warp::kCols;
-    extern __shared__ __align__(16) float red[];   // [kWarps][kTile], then the shares [slice][share]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2;
-    pdl_trigger();
-    pdl_wait();
-    const int rank = splits > 1 ? (int)tc5::cluster_rank() : 0;
-    const int etiles = (a.E + Warp::kCols - 1) / Warp::kCols;
-    int et;
-    const int64_t t0 = divmod_idx(blockIdx.x / splits, etiles, et) * Warp::kRows;
-    const int e0 = et * Warp::kCols;
-    const int c = lane & 3, pieces = a.H / 8;
-    Warp w;
-    const int steps1 = (a.H + thin::kStep - 1) / thin::kStep;
-    const int64_t steps = (int64_t)steps1 * a.parts;
-    const int k0 = (int)(rank * steps / splits), k1 = (int)((rank + 1) * steps / splits);
-    float* mine = red + warp * kTile;
-    bool more = false;
-    for (int part = k0 / steps1; part * steps1 < k1; ++part) {
-#pragma unroll
-        for (int j = 0; j < 2 * MT; ++j)
-            w.x[j] = reinterpret_cast<const uint4*>(a.x + min(t0 + j * 8 + gr, (int64_t)a.T - 1) * a.stride) + c;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            w.w[j] = reinterpret_cast<const uint4*>(a.W + ((int64_t)(a.parts - 1 - part) * a.E + min(e0 + j * 8 + gr, a.E - 1)) * a.H) + c;
-        const int first = max(k0 - part * steps1, 0), last = min(k1 - part * steps1, steps1);
-        w.run(first + warp, last, pieces, mine, more);
-        more = true;
-    }
-    auto put = [&](int i, float v) {
-        const int64_t t = t0 + i / Warp::kCols;
-        const int e = e0 + i % Warp::kCols;
-        if (t < a.T && e < a.E) a.out[t * a.E + e] = v;
-    };
-    __syncthreads();
+// Sum i of kCount, put(i, sum) for each; `mine(i)` is this CTA's, `shares` kCount floats that nobody uses.
+template <int kCount, typename Mine, typename Put>
+__device__ __forceinline__ void join_slices(int splits, float* shares, Mine mine, Put put) {
     if (splits == 1) {
-        for (int i = threadIdx.x; i < kTile; i += thin::kThreads) put(i, thin::joined(red, kTile, i));
+        for (int i = threadIdx.x; i < kCount; i += thin::kThreads) put(i, mine(i));
         return;
     }
-    float* shares = red + thin::kWarps * kTile;
-    const int share = kTile / splits;   // a power of two, as splits is
-    tc5::cluster_sync();                // every CTA of the cluster runs
-    for (int i = threadIdx.x; i < kTile; i += thin::kThreads) {
-        const uint32_t to = smem_u32(shares + rank * share + i % share);
-        st_cluster(tc5::at_cta(to, (uint32_t)(i / share)), thin::joined(red, kTile, i));
-    }
+    const int rank = (int)tc5::cluster_rank(), share = kCount / splits;   // a power of two, as splits is
+    tc5::cluster_sync();                                                  // every CTA of the cluster runs
+    for (int i = threadIdx.x; i < kCount; i += thin::kThreads)
+        st_cluster(tc5::at_cta(smem_u32(shares + rank * share + i % share), (uint32_t)(i / share)), mine(i));
     tc5::cluster_sync();
     for (int i = threadIdx.x; i < share; i += thin::kThreads) {
         float v = shares[i];
@@ -85,18 +48,77 @@ __global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const Logit
     }
 }
 
-template <int MT, int NT>
-cudaError_t launch_thin(const LogitArgs& a, cudaStream_t st) {
-    using Warp = thin::Warp<MT, NT>;
-    auto* kern = logits_thin_kernel<MT, NT>;
-    const size_t smem = (size_t)(thin::kWarps + 1) * Warp::kRows * Warp::kCols * 4;
+// Up to 16 tokens, NT x 8 experts.
+template <int NT>
+__global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const LogitArgs a, int splits) {
+    using Warp = thin::Warp<1, NT>;
+    constexpr int kTile = Warp::kRows * Warp::kCols;
+    extern __shared__ __align__(16) float red[];   // [kWarps][kTile], then the shares
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
+    pdl_trigger();
+    pdl_wait();
+    const int rank = splits > 1 ? (int)tc5::cluster_rank() : 0, e0 = (int)(blockIdx.x / splits) * Warp::kCols;
+    const int steps1 = (a.H + thin::kStep - 1) / thin::kStep;
+    const int64_t steps = (int64_t)steps1 * a.parts;
+    const int k0 = (int)(rank * steps / splits), k1 = (int)((rank + 1) * steps / splits);
+    float* mine = red + warp * kTile;
+    Warp w;
+    bool more = false;
+    for (int part = k0 / steps1; part * steps1 < k1; ++part) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) w.x[j] = reinterpret_cast<const uint4*>(a.x + min(j * 8 + gr, a.T - 1) * a.stride) + c;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            w.w[j] = reinterpret_cast<const uint4*>(a.W + ((int64_t)(a.parts - 1 - part) * a.E + min(e0 + j * 8 + gr, a.E - 1)) * a.H) + c;
+        w.run(max(k0 - part * steps1, 0) + warp, min(k1 - part * steps1, steps1), a.H / 8, mine, more);
+        more = true;
+    }
+    __syncthreads();
+    join_slices<kTile>(
+        splits, red + thin::kWarps * kTile, [&](int i) { return thin::joined(red, kTile, i); },
+        [&](int i, float v) {
+            const int t = i / Warp::kCols, e = e0 + i % Warp::kCols;
+            if (t < a.T && e < a.E) a.out[(int64_t)t * a.E + e] = v;
+        });
+}
+
+// 64 tokens, 32 experts.
+using LogitTile = thin::Staged<4>;
+constexpr int kLogitTile = LogitTile::kRows * LogitTile::kCols;
+
+__global__ void __launch_bounds__(thin::kThreads, 2) logits_staged_kernel(const LogitArgs a, int splits) {
+    extern __shared__ __align__(128) uint8_t smem[];   // the tile's ring, then the shares
+    pdl_trigger();
+    pdl_wait();
+    const int rank = splits > 1 ? (int)tc5::cluster_rank() : 0;
+    int et;
+    const int64_t t0 = divmod_idx(blockIdx.x / splits, (a.E + LogitTile::kCols - 1) / LogitTile::kCols, et) * LogitTile::kRows;
+    const int e0 = et * LogitTile::kCols, row = threadIdx.x >> 3, piece = threadIdx.x & 7;
+    LogitTile tile;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t t = t0 + row + 32 * h;
+        tile.x[h] = t < a.T ? a.x + t * a.stride + piece * 8 : nullptr;
+        tile.w[h] = h == 0 && e0 + row < a.E ? a.W + (int64_t)(e0 + row) * a.H + piece * 8 : nullptr;
+    }
+    const int64_t steps = (int64_t)((a.H + LogitTile::kTileCols - 1) / LogitTile::kTileCols) * a.parts;
+    tile.run(smem, (int)(rank * steps / splits), (int)((rank + 1) * steps / splits), a.H, a.parts, (int64_t)a.E * a.H);
+    const float* sums = reinterpret_cast<const float*>(smem);
+    join_slices<kLogitTile>(
+        splits, reinterpret_cast<float*>(smem + LogitTile::kBytes), [&](int i) { return sums[i] + sums[kLogitTile + i]; },
+        [&](int i, float v) {
+            const int64_t t = t0 + i / LogitTile::kCols;
+            const int e = e0 + i % LogitTile::kCols;
+            if (t < a.T && e < a.E) a.out[t * a.E + e] = v;
+        });
+}
+
+// tiles x slices CTAs; K is cut until every SM has a CTA, as long as a slice keeps `least` steps.
+cudaError_t launch_tiles(void (*kern)(LogitArgs, int), const LogitArgs& a, int64_t tiles, int64_t steps, int least, size_t smem, cudaStream_t st) {
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = ceil_div64(a.T, Warp::kRows) * ((a.E + Warp::kCols - 1) / Warp::kCols);
-    const int64_t steps = ceil_div64(a.H, thin::kStep) * a.parts;
-    // K is cut until every SM has a CTA, as long as each warp keeps two steps
     int splits = 1;
-    while (splits < 8 && tiles * splits < device_info().sm_count && steps >= 2 * thin::kWarps * 2 * splits) splits *= 2;
+    while (splits < 8 && tiles * splits < device_info().sm_count && steps >= (int64_t)least * 2 * splits) splits *= 2;
     if (tiles * splits > INT32_MAX) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * splits));
@@ -121,6 +143,21 @@ cudaError_t launch_thin(const LogitArgs& a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, a, splits);
 }
 
+cudaError_t launch_thin(const LogitArgs& a, cudaStream_t st) {
+    using Warp = thin::Warp<1, 2>;
+    const size_t smem = (size_t)(thin::kWarps + 1) * Warp::kRows * Warp::kCols * 4;
+    // a slice keeps two steps for each warp
+    return launch_tiles(logits_thin_kernel<2>, a, (a.E + Warp::kCols - 1) / Warp::kCols, ceil_div64(a.H, thin::kStep) * a.parts, 2 * thin::kWarps,
+                        smem, st);
+}
+
+int64_t staged_tiles(const LogitArgs& a) { return ceil_div64(a.T, LogitTile::kRows) * ((a.E + LogitTile::kCols - 1) / LogitTile::kCols); }
+
+cudaError_t launch_staged(const LogitArgs& a, cudaStream_t st) {
+    const size_t smem = LogitTile::kBytes + (size_t)kLogitTile * 4;
+    return launch_tiles(logits_staged_kernel, a, staged_tiles(a), ceil_div64(a.H, LogitTile::kTileCols) * a.parts, 4, smem, st);
+}
+
 // ---- many tokens: tcgen05 -------------------------------------------------------------------
 // A pair of CTAs computes 256 tokens times N experts (cta_group::2, M = 256): each CTA copies its 128
 // tokens and half of the experts' rows, so a CTA's copies are 128 + N / 2 rows for 128 x N sums.  Roles
@@ -133,7 +170,10 @@ cudaError_t launch_thin(const LogitArgs& a, cudaStream_t st) {
 constexpr int kReaders = 8, kWideThreads = (kReaders + 2) * 32;
 constexpr int kHalfCols = 64, kStageCols = 2 * kHalfCols;
 constexpr int kPairTokens = 256;
-constexpr int kWideTokens = 768;   // from here on
+// The staged tiles copy 96 rows of K columns for 64 x 32 sums, the wide ones 128 + N / 2 for 128 x N; a step of 128 columns
+// takes the wide kernel 0.3 us at least.  Staged and wide, us (E, H, tiles): 384, 7168: 48 tiles 18.3, 24.6; 96 26.6,
+// 24.6; 192 41, 25.  161, 2088: 48 12.3, 16.4; 96 16.4, 16.4; 192 20.5, 16.4.  64, 4096: 64 14.8, 18.4; 128 20.8, 19.5.
+constexpr int64_t kStagedTiles = 90;
 constexpr int kChainStages = 2;
 constexpr int kMaxWideStages = 6;
 constexpr long long kLandCycles = 4000000;   // about 2 ms
@@ -419,7 +459,9 @@ chord_status chord_router_logits(const void* x, int64_t x_stride, int T, const v
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const DeviceInfo& di = device_info();
     if (!di.err) return CHORD_ERR_CUDA;
-    const cudaError_t e = T <= 16 ? launch_thin<1, 2>(a, st) : T < kWideTokens || H < kStageCols ? launch_thin<2, 4>(a, st) : launch_wide(a, di.err, st);
+    const cudaError_t e = T <= 16                                                   ? launch_thin(a, st)
+                          : staged_tiles(a) <= kStagedTiles || H < kStageCols ? launch_staged(a, st)
+                                                                                    : launch_wide(a, di.err, st);
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;
     if (!opts || !opts->validate) return CHORD_OK;
     int32_t code = 0;

@@ -147,7 +147,7 @@ struct Staged {
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes;          // the ring
     static constexpr size_t kSums = (size_t)2 * kRows * kCols * 4;          // over it, afterwards: [2][kRows][kCols]
     static constexpr size_t kBytes = kSmem > kSums ? kSmem : kSums;
-    static constexpr int kChainStages = 24;                                 // two instructions a stage
+    static constexpr int kChainStages = 8;                                  // two instructions a stage
 
     // This thread's rows of x (t / 8 and t / 8 + 32) and weight rows, at piece t mod 8; null: not copied,
     // whatever is multiplied in its place is not looked at.

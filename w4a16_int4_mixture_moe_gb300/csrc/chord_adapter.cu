@@ -77,7 +77,7 @@ __device__ __forceinline__ int slot_of(const AdapterArgs& g, int p, bool report)
 
 // ---- blocks of few pairs ------------------------------------------------------
 struct FewBlocks {
-    int slot[kFewPairs];     // of each pair
+    alignas(16) int slot[kFewPairs];   // of each pair
     int leader[kFewPairs];   // first pair of each block
     int rank[kFewPairs];     // pairs of the same slot before each
     int counts[kWarps];
@@ -90,8 +90,15 @@ __device__ __forceinline__ void find_blocks(const AdapterArgs& g, FewBlocks& f, 
     const int s = p < g.P ? slot_of(g, p, report) : kNone;
     f.slot[p] = s;
     __syncthreads();
-    int rank = 0;
-    for (int q = 0; q < p; ++q) rank += f.slot[q] == s;
+    int rank = 0;   // pairs of the same slot before this one
+    if (s != kNone) {
+        const int4* four = reinterpret_cast<const int4*>(f.slot);
+        for (int q = 0; q < p / 4; ++q) {
+            const int4 o = four[q];
+            rank += (o.x == s) + (o.y == s) + (o.z == s) + (o.w == s);
+        }
+        for (int q = p & ~3; q < p; ++q) rank += f.slot[q] == s;
+    }
     const bool lead = s != kNone && rank % kFewRows == 0;
     const unsigned m = __ballot_sync(0xffffffffu, lead);
     f.rank[p] = rank;
@@ -134,42 +141,6 @@ __device__ __forceinline__ int slices_of(const AdapterArgs& g, int n) {
 }
 
 // ---- v = A x --------------------------------------------------------------------
-template <int NT>
-__global__ void __launch_bounds__(kThreads) adapter_down_few_kernel(const AdapterArgs g) {
-    using Warp = thin::Warp<1, NT>;
-    constexpr int MR = Warp::kRows, NB = Warp::kCols;
-    extern __shared__ __align__(16) float red[];   // [kWarps][MR][NB]
-    __shared__ int32_t rows[MR];
-    __shared__ FewBlocks few;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
-    pdl_trigger();
-    find_blocks(g, few, blockIdx.x == 0);
-    const int n = few.n, splits = slices_of(g, n), chunks = (g.R + NB - 1) / NB, per = chunks * splits;
-    const int steps = (g.K + thin::kStep - 1) / thin::kStep;
-    for (int64_t i = blockIdx.x; i < (int64_t)n * per; i += gridDim.x) {
-        int q;
-        const int b = (int)divmod_idx(i, per, q), split = q % splits, r0 = q / splits * NB;
-        const int slot = block_rows<true, MR>(g, &few, b, rows);
-        if (slot < 0) continue;
-        Warp w;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int p = rows[j * 8 + gr] < 0 ? rows[0] : rows[j * 8 + gr];
-            w.x[j] = reinterpret_cast<const uint4*>(g.x + (int64_t)(g.div == 1 ? p : p / g.div) * g.x_stride) + c;
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-            w.w[j] = reinterpret_cast<const uint4*>(g.A + ((int64_t)slot * g.R + min(r0 + j * 8 + gr, g.R - 1)) * g.K) + c;
-        const int k0 = (int)((int64_t)split * steps / splits), k1 = (int)((int64_t)(split + 1) * steps / splits);
-        w.run(k0 + warp, k1, g.K / 8, red + warp * MR * NB, false);
-        __syncthreads();
-        for (int u = threadIdx.x; u < MR * NB; u += kThreads) {
-            const int p = rows[u / NB], r = r0 + u % NB;
-            if (p >= 0 && r < g.R) g.v[((int64_t)split * g.P + p) * g.R + r] = thin::joined(red, MR * NB, u);
-        }
-    }
-}
-
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const AdapterArgs g) {
     using Tile = thin::Staged<NT>;
@@ -257,90 +228,122 @@ __device__ __forceinline__ void split3(float v0, float v1, uint32_t& h0, uint32_
     h2 = upper(rest(v0), rest(v1));
 }
 
-// Few pairs: an item is a block times `cols` tiles of 32 columns of one part, straight from global memory; the
-// eight warps take a tile each.
-template <bool F32>
-__global__ void __launch_bounds__(kThreads, 2) adapter_up_few_kernel(const AdapterArgs g, int cols) {
-    constexpr int MT = 1;
-    extern __shared__ __align__(16) uint4 frag[];   // [MT][k steps of all parts][3][32]
-    __shared__ int32_t mine[kFewRows];   // the block's rows
+// ---- few pairs: one launch ---------------------------------------------------------------
+// A cluster of CTAs takes an item (block, part, group of columns): each CTA a slice of K for v (chord_thin.cuh), all
+// slices read by each through distributed shared memory and added in rank order, then each its share of
+// the columns.  Where there are few blocks, several clusters compute the same v for columns of their own: A
+// comes from L2 then, and one launch is what a call of one token costs.  Clusters are of eight CTAs while all
+// blocks find one at once, of four beyond.
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+// The two halves of tc5::cluster_sync.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+template <int kFewCtas, int NT, bool F32>
+__global__ void __launch_bounds__(kThreads, 2) adapter_few_kernel(const AdapterArgs g) {
+    using Warp = thin::Warp<1, NT>;
+    constexpr int NB = Warp::kCols;
+    extern __shared__ __align__(16) float red[];             // [kWarps][16][NB], then v [16][rank] and its fragments
+    __shared__ int32_t rows[kFewRows];
     __shared__ FewBlocks few;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
-    find_blocks(g, few, false);   // the ids are older than the kernel before
-    const int n = few.n;
+    float* v = red + kWarps * kFewRows * NB;
+    uint4* frag = reinterpret_cast<uint4*>(v + kFewRows * g.rank);   // [k steps][3][32]
+    pdl_trigger();
     pdl_wait();
-    const int splits = slices_of(g, n);
-    const int Np = g.N / g.parts, tiles = (Np + 31) / 32, groups = (tiles + cols - 1) / cols;
-    const int ksp = (g.rank + 15) / 16;          // 16-wide steps of a part
-    const int per = groups * g.parts;            // items of the rows of a block
+    const int cta = (int)tc5::cluster_rank();
+    find_blocks(g, few, blockIdx.x == 0);
+    const int n = few.n, steps = (g.K + thin::kStep - 1) / thin::kStep, k0 = steps * cta / kFewCtas, k1 = steps * (cta + 1) / kFewCtas;
+    const int Np = g.N / g.parts, tiles = (Np + 31) / 32, ksp = (g.rank + 15) / 16;
+    const int clusters = (int)gridDim.x / kFewCtas, cluster = (int)blockIdx.x / kFewCtas;
+    // groups of columns: clusters that would have nothing take some, as long as every CTA has a tile
+    const int groups = max(1, min(clusters / max(n * g.parts, 1), tiles / kFewCtas));
     // column of lane group gr in tile j of a matrix instruction: the eight columns of one lane's results are 8 c ... 8 c + 7
     const int bc = 8 * (gr >> 1) + (gr & 1);
-    for (int64_t i = blockIdx.x; i < (int64_t)n * per; i += gridDim.x) {
-        int q;
-        const int b16 = (int)divmod_idx(i, per, q);
-        const int part = q / groups, t0 = (q - part * groups) * cols;
-        const int slot = block_rows<true, kFewRows>(g, &few, b16, mine);
+    bool reading = false;
+    for (int i = cluster; i < n * g.parts * groups; i += clusters) {
+        const int b = i / (g.parts * groups), q = i - b * g.parts * groups, part = q / groups, group = q - part * groups;
+        const int slot = block_rows<true, kFewRows>(g, &few, b, rows);
+        const int share = group * kFewCtas + cta, shares = groups * kFewCtas;
+        const int t0 = (int)((int64_t)tiles * share / shares), t1 = (int)((int64_t)tiles * (share + 1) / shares);
+        const __nv_bfloat16* B = g.B + ((int64_t)max(slot, 0) * g.N + part * Np) * g.rank;
         if (slot >= 0) {
+            // B on its way to L2 while v is computed
+            for (int64_t u = (int64_t)t0 * 32 * g.rank + threadIdx.x * 64, e = (int64_t)min(t1 * 32, Np) * g.rank; u < e; u += kThreads * 64)
+                prefetch(B + u);
+            if (reading) cluster_wait();   // the slices of the item before have been read
+            for (int r0 = 0; r0 < g.rank; r0 += NB) {
+                Warp w;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int p = rows[j * 8 + gr] < 0 ? rows[0] : rows[j * 8 + gr];
+                    w.x[j] = reinterpret_cast<const uint4*>(g.x + (int64_t)(g.div == 1 ? p : p / g.div) * g.x_stride) + c;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    w.w[j] = reinterpret_cast<const uint4*>(g.A + ((int64_t)slot * g.R + part * g.rank + min(r0 + j * 8 + gr, g.rank - 1)) * g.K) + c;
+                w.run(k0 + warp, k1, g.K / 8, red + warp * kFewRows * NB, false);
+                __syncthreads();
+                for (int u = threadIdx.x; u < kFewRows * NB; u += kThreads)
+                    if (r0 + u % NB < g.rank) v[u / NB * g.rank + r0 + u % NB] = thin::joined(red, kFewRows * NB, u);
+                __syncthreads();
+            }
+            tc5::cluster_sync();
             // v as the fragments of the instruction's A side: lane (g, c) has rows g and g + 8, of each k
             // step the four columns 4 c ... (B's side likewise)
             const float scale = g.scale ? g.scale[slot / g.E] : 1.0f;
-            for (int u = threadIdx.x; u < MT * ksp * 32; u += kThreads) {
-                const int l = u & 31, ms = u >> 5, m = ms / ksp, s = ms - m * ksp, k = 16 * s + 4 * (l & 3);
+            for (int u = threadIdx.x; u < ksp * 32; u += kThreads) {
+                const int l = u & 31, s = u >> 5, k = 16 * s + 4 * (l & 3);
                 uint32_t r[3][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int p = mine[m * 16 + h * 8 + (l >> 2)];
                     float4 f = make_float4(0, 0, 0, 0);
-                    if (p >= 0 && k < g.rank) {
-                        const float* from = g.v + (int64_t)p * g.R + part * g.rank + k;
-                        const int64_t slice = (int64_t)g.P * g.R;
-                        for (int z = 0; z < splits; z += 4) {   // four slices' loads in flight, added in order
-                            float4 o[4];
+                    if (rows[h * 8 + (l >> 2)] >= 0 && k < g.rank) {
+                        const uint32_t at = smem_u32(v + (h * 8 + (l >> 2)) * g.rank + k);
+                        float4 o[kFewCtas];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) o[i] = *reinterpret_cast<const float4*>(from + min(z + i, splits - 1) * slice);
+                        for (int z = 0; z < kFewCtas; ++z) o[z] = ld_cluster4(tc5::at_cta(at, (uint32_t)z));
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (z + i < splits) f.x += o[i].x, f.y += o[i].y, f.z += o[i].z, f.w += o[i].w;
-                        }
+                        for (int z = 0; z < kFewCtas; ++z) f.x += o[z].x, f.y += o[z].y, f.z += o[z].z, f.w += o[z].w;
                     }
                     split3(f.x * scale, f.y * scale, r[0][h], r[1][h], r[2][h]);
                     split3(f.z * scale, f.w * scale, r[0][2 + h], r[1][2 + h], r[2][2 + h]);
                 }
 #pragma unroll
-                for (int t = 0; t < 3; ++t) frag[(ms * 3 + t) * 32 + l] = make_uint4(r[t][0], r[t][1], r[t][2], r[t][3]);
+                for (int t = 0; t < 3; ++t) frag[(s * 3 + t) * 32 + l] = make_uint4(r[t][0], r[t][1], r[t][2], r[t][3]);
             }
             __syncthreads();
+            cluster_arrive();   // waited for where v is written next, or the kernel ends
+            reading = true;
         }
-        int64_t from[2 * MT], to[2 * MT];
-        bool live[2 * MT];
+        int64_t from[2], to[2];
+        bool live[2];
 #pragma unroll
-        for (int j = 0; j < 2 * MT; ++j) {
-            const int p = mine[j * 8 + gr];
+        for (int j = 0; j < 2; ++j) {
+            const int p = rows[j * 8 + gr];
             live[j] = p >= 0;
             from[j] = p * g.base_stride + part * Np + 8 * c;
             to[j] = p * g.y_stride + part * Np + 8 * c;
         }
-        const __nv_bfloat16* b = g.B + ((int64_t)max(slot, 0) * g.N + part * Np + bc) * g.rank + 4 * c;
-        const int end = min(tiles, t0 + cols);
-        for (int t = t0 + warp; t < end; t += kWarps) {
+        for (int t = t0 + warp; t < t1; t += kWarps) {
             const int n0 = t * 32;
             const bool in = 8 * c < Np - n0;
-            Eight<F32> o[2 * MT];
+            Eight<F32> o[2];
 #pragma unroll
-            for (int j = 0; j < 2 * MT; ++j)
+            for (int j = 0; j < 2; ++j)
                 if (in && live[j]) o[j].load(g.base, from[j] + n0);
             if (slot >= 0) {
                 const __nv_bfloat16* bt[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) bt[j] = b + (int64_t)(n0 + 2 * j) * g.rank;
+                for (int j = 0; j < 4; ++j) bt[j] = B + (int64_t)(n0 + bc + 2 * j) * g.rank + 4 * c;
                 const bool bin = bc < Np - n0;
-                float acc[MT][4][4];
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) acc[m][j][u] = 0.0f;
+                float d[4][4] = {};
 #pragma unroll 4
                 for (int s = 0; s < ksp; ++s) {
                     uint2 w[4];
@@ -348,31 +351,29 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_up_few_kernel(const Adapt
 #pragma unroll
                     for (int j = 0; j < 4; ++j) w[j] = kin ? *reinterpret_cast<const uint2*>(bt[j] + 16 * s) : make_uint2(0, 0);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
+                    for (int t3 = 2; t3 >= 0; --t3) {
+                        const uint4 a = frag[(s * 3 + t3) * 32 + lane];
 #pragma unroll
-                        for (int t3 = 2; t3 >= 0; --t3) {
-                            const uint4 a = frag[((m * ksp + s) * 3 + t3) * 32 + lane];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) thin::mma(acc[m][j], a.x, a.y, a.z, a.w, w[j].x, w[j].y);
-                        }
+                        for (int j = 0; j < 4; ++j) thin::mma(d[j], a.x, a.y, a.z, a.w, w[j].x, w[j].y);
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 2 * MT; ++j) {
-                    float d[8];
+                for (int j = 0; j < 2; ++j) {
+                    float e[8];
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        d[2 * u] = acc[j / 2][u][j % 2 * 2];
-                        d[2 * u + 1] = acc[j / 2][u][j % 2 * 2 + 1];
+                        e[2 * u] = d[u][j * 2];
+                        e[2 * u + 1] = d[u][j * 2 + 1];
                     }
-                    o[j].add(d);
+                    o[j].add(e);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 2 * MT; ++j)
+            for (int j = 0; j < 2; ++j)
                 if (in && live[j]) o[j].store(g.y, to[j] + n0);
         }
     }
+    if (reading) cluster_wait();   // nobody reads this CTA's v any more
 }
 
 // Many pairs.  A warp has 16 rows of a block, its rows of v in registers as fragments of the instruction's A side (KS k
@@ -817,7 +818,7 @@ struct Layout {
 
 Layout layout_of(int64_t P, int64_t slots, int R) {
     Layout l{};
-    const bool few = P <= kFewPairs;
+    const bool few = P <= kFewPairs;   // needs no workspace
     const int64_t mb = few ? kFewRows : kManyRows;
     l.blocks = P / mb + (P < slots + 1 ? P : slots + 1) + 1;
     const int64_t s = P > 0 ? kSplitRows / P : 1;
@@ -827,8 +828,8 @@ Layout layout_of(int64_t P, int64_t slots, int R) {
         l.bytes += (n + 255) / 256 * 256;
         return at;
     };
-    l.v = take((size_t)l.max_splits * P * R * 4);
     if (!few) {
+        l.v = take((size_t)l.max_splits * P * R * 4);
         l.nblocks = take(8);
         l.block_slot = take((size_t)l.blocks * 4);
         l.block_count = take((size_t)l.blocks * 4);
@@ -842,53 +843,75 @@ Layout layout_of(int64_t P, int64_t slots, int R) {
 // Rows of A that an item of the first half takes.
 int down_cols(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
-template <int NT, bool FEW>
+template <int NT>
 cudaError_t launch_down_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
-    void (*kern)(AdapterArgs) = FEW ? adapter_down_few_kernel<NT> : adapter_down_kernel<NT>;
-    const size_t smem = FEW ? (size_t)kWarps * kFewRows * NT * 8 * 4 : thin::Staged<NT>::kBytes;
+    auto* kern = adapter_down_kernel<NT>;
+    const size_t smem = thin::Staged<NT>::kBytes;
     int ctas = 0;
     cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
     if (e != cudaSuccess) return e;
     const int64_t items = blocks * g.units * g.max_splits, most = (int64_t)device_info().sm_count * ctas;
-    return launch_pdl(!FEW && pdl_enabled(), kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g);
+    return launch_pdl(pdl_for(g.P), kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g);
 }
 
-template <bool FEW>
 cudaError_t launch_down(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
     switch (down_cols(g.R)) {
-        case 8: return launch_down_as<1, FEW>(g, blocks, st);
-        case 16: return launch_down_as<2, FEW>(g, blocks, st);
-        case 32: return launch_down_as<4, FEW>(g, blocks, st);
-        default: return launch_down_as<8, FEW>(g, blocks, st);
+        case 8: return launch_down_as<1>(g, blocks, st);
+        case 16: return launch_down_as<2>(g, blocks, st);
+        case 32: return launch_down_as<4>(g, blocks, st);
+        default: return launch_down_as<8>(g, blocks, st);
+    }
+}
+
+template <int CTAS, int NT, bool F32>
+cudaError_t launch_few_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
+    auto* kern = adapter_few_kernel<CTAS, NT, F32>;
+    const size_t smem = ((size_t)kWarps * kFewRows * NT * 8 + (size_t)kFewRows * g.rank) * 4 + (size_t)((g.rank + 15) / 16) * 3 * 512;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), 64 * 1024);   // at most 52 KB
+    if (e != cudaSuccess) return e;
+    // clusters for the blocks' parts, or to share the columns of few; two CTAs to an SM
+    const int tiles = (g.N / g.parts + 31) / 32, most = 2 * device_info().sm_count / CTAS;
+    const int64_t want = blocks * g.parts * ((tiles + CTAS - 1) / CTAS);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((want < most ? want : most) * CTAS));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CTAS;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, g);
+}
+
+template <int CTAS, bool F32>
+cudaError_t launch_few_of(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
+    switch (down_cols(g.rank)) {
+        case 8: return launch_few_as<CTAS, 1, F32>(g, blocks, st);
+        case 16: return launch_few_as<CTAS, 2, F32>(g, blocks, st);
+        case 32: return launch_few_as<CTAS, 4, F32>(g, blocks, st);
+        default: return launch_few_as<CTAS, 8, F32>(g, blocks, st);
     }
 }
 
 template <bool F32>
-cudaError_t launch_up_few(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
-    auto* kern = adapter_up_few_kernel<F32>;
-    const size_t smem = (size_t)((g.rank + 15) / 16) * 3 * 512;   // at most 12 KB
-    int ctas = 0;
-    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
-    if (e != cudaSuccess) return e;
-    const int64_t most = (int64_t)device_info().sm_count * ctas;
-    // four tiles a warp share the fragments of v, fewer where that leaves CTAs idle
-    const int tiles = (g.N / g.parts + 31) / 32;
-    int cols = 4 * kWarps;
-    while (cols > kWarps && blocks * g.parts * ((tiles + cols - 1) / cols) < 2 * most) cols /= 2;
-    const int64_t items = blocks * g.parts * ((tiles + cols - 1) / cols);
-    return launch_pdl(pdl_enabled(), kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g, cols);
+cudaError_t launch_few(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
+    return blocks * g.parts * 8 <= 2 * device_info().sm_count ? launch_few_of<8, F32>(g, blocks, st) : launch_few_of<4, F32>(g, blocks, st);
 }
 
 cudaError_t launch_up_as(void (*kern)(AdapterArgs), const AdapterArgs& g, size_t smem, cudaStream_t st) {
     int ctas = 0;
     cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kUpThreads, smem, smem, &ctas);
     if (e != cudaSuccess) return e;
-    return launch_pdl(pdl_enabled(), kern, dim3((unsigned)(device_info().sm_count * ctas)), dim3(kUpThreads), smem, st, g);
+    return launch_pdl(pdl_for(g.P), kern, dim3((unsigned)(device_info().sm_count * ctas)), dim3(kUpThreads), smem, st, g);
 }
 
 template <bool F32>
-cudaError_t launch_up(const AdapterArgs& g, int64_t blocks, bool few, cudaStream_t st) {
-    if (few) return launch_up_few<F32>(g, blocks, st);
+cudaError_t launch_up(const AdapterArgs& g, cudaStream_t st) {
     if (g.rank <= 16) return launch_up_as(adapter_up_small_kernel<F32>, g, 0, st);
     if (g.rank <= 32) return launch_up_as(adapter_up_kernel<2, F32>, g, UpStage<2>::kStages * UpStage<2>::kBytes, st);
     if (g.rank <= 64) return launch_up_as(adapter_up_kernel<4, F32>, g, UpStage<4>::kStages * UpStage<4>::kBytes, st);
@@ -983,12 +1006,12 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (few) {
-        e = launch_down<true>(g, l.blocks, st);
-        } else {
+        e = f32 ? launch_few<true>(g, l.blocks, st) : launch_few<false>(g, l.blocks, st);
+    } else {
         e = launch_plan(g, slots, reinterpret_cast<int32_t*>(ws + l.counts), st);
-        if (e == cudaSuccess) e = launch_down<false>(g, l.blocks, st);
+        if (e == cudaSuccess) e = launch_down(g, l.blocks, st);
+        if (e == cudaSuccess) e = f32 ? launch_up<true>(g, st) : launch_up<false>(g, st);
     }
-    if (e == cudaSuccess) e = f32 ? launch_up<true>(g, l.blocks, few, st) : launch_up<false>(g, l.blocks, few, st);
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;
     if (!opts || !opts->validate) return CHORD_OK;
     int32_t code = 0;

@@ -190,9 +190,9 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // accurate ones by three half ulps; a softmax by its sum's E / 32 + 5 half ulps and those of the exponents, below 4e-6.
 constexpr float kSlackFast = 1e-6f, kSlackAccurate = 5e-7f, kSlackSoftmax = 4e-6f;
 
-// Shared memory of a warp, in doubles: the list (16), its candidates (64) and their values in
+// Shared memory of a warp, in doubles: the list (16), its candidates (16), their inputs or values in
 // binary64 (32); or the groups' rows; or all values in binary64 and the groups' (E + 32).
-__host__ __device__ inline int own_doubles(int E) { return (E > 80 ? E + 33 : 113) & ~1; }
+__host__ __device__ inline int own_doubles(int E) { return (E > 32 ? E + 33 : 65) & ~1; }
 
 template <int VPL, bool F32>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     int mine = -1;
     if (fine) {
         int* list = reinterpret_cast<int*>(own);
-        float2* cand = reinterpret_cast<float2*>(own + 16);
+        float* cand = reinterpret_cast<float*>(own + 16);
         int at = 0;
         for (unsigned left; (left = __ballot_sync(kAll, mask != 0)) != 0;) {
             if (mask) {
@@ -352,33 +352,38 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
                 b = a.bias[e];
                 v = (softmax ? expf(l - mx) / total : fast_rcp(1.0f + fast_exp(-l))) + b;
             }
-            cand[lane] = make_float2(v, __int_as_float(e));
+            cand[lane] = v;
         }
         __syncwarp();
-        int rank = 0, close = -1;   // itself
-        const float tol = 2.0f * (softmax ? kSlackSoftmax : kSlackFast) * (1.0f + fabsf(v));
+        // Those before this one, and those that FP32 cannot tell from it (without a bias: that are equal), itself among them.
+        int rank = 0, close = 0;
+        const float tol = exact_order ? 0.0f : 2.0f * (softmax ? kSlackSoftmax : kSlackFast) * (1.0f + fabsf(v));
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
-            const float2 c = cand[k];
-            rank += c.x > v || (c.x == v && __float_as_int(c.y) < e);
-            close += !(fabsf(c.x - v) > tol);
+            const float c = cand[k];
+            rank += c > v;
+            close += !(fabsf(c - v) > tol);
         }
-        if (!exact_order && __any_sync(kAll, lane < n && rank < a.topk && close > 0)) {
-            // Equal inputs are equal values in any precision, and in the right order already.
-            double* values = own + 16 + 64;
-            float2* inputs = reinterpret_cast<float2*>(values);
+        if (__any_sync(kAll, lane < n && rank < a.topk && close > 1)) {
+            // Equal inputs are equal values in any precision: the lower index is first.
+            float2* inputs = reinterpret_cast<float2*>(own + 16 + 16);
             if (lane < n) inputs[lane] = make_float2(l, b);
             __syncwarp();
+            int before = 0;
             for (int k = 0; k < n; ++k) {
                 const float2 c = inputs[k];
-                close -= k != lane && c.x == l && c.y == b;
+                const bool same = c.x == l && c.y == b;
+                close -= same;
+                before += same && list[k] < e;
             }
             __syncwarp();
+            rank += before;
             if (!__any_sync(kAll, lane < n && rank < a.topk && close > 0)) {
             } else if (softmax) {
                 fine = false;   // the sum over all experts is needed in binary64 too
             } else {
                 // the candidates are certain, their order is not
+                double* values = own + 16 + 16;
                 const double d = 1.0 / (1.0 + exp(-(double)l)) + (double)b;
                 if (lane < n) values[lane] = d;
                 __syncwarp();

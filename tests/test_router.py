@@ -354,6 +354,30 @@ def test_strides_and_many_rows():
 
 
 @gpu
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("T", [7295, 7296, 12345])
+def test_many_tokens(T, score, with_bias):
+    """More tokens than the GPU has warps for: two at a time, an odd one left over; ties, close values, empty
+    rows and rows with many candidates next to one another."""
+    need_gpu()
+    g = gen(T + score)
+    E, topk = 40, 5
+    l = torch.randn((T, E), generator=g) * 2
+    l[::7] = l[::7].to(torch.bfloat16).float()
+    l[5::50] = torch.randint(0, 3, l[5::50].shape, generator=g).float()
+    l[9::100] = 1.5
+    l[13::100] = NINF
+    l[14::100, 3:] = NINF
+    l[15::200] = torch.full((E,), 1.25) + torch.randint(0, 4, l[15::200].shape, generator=g) * 2.0 ** -23
+    bias = torch.randn(E, generator=g) * 0.1 if with_bias else None
+    if with_bias:
+        bias[:8] = 0.0
+    check(l, topk, bias, score=score)
+    check(l.to(torch.bfloat16), topk, bias, score=score, groups=8, topk_groups=3, group_best=2, renormalize=False)
+
+
+@gpu
 def test_route_in_a_graph_and_on_another_stream():
     need_gpu()
     g = gen(4)

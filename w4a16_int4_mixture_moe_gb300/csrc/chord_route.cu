@@ -183,8 +183,8 @@ __device__ __forceinline__ float fast_rcp(float x) {
 //      below: what is not below it (by twice the slack) are the candidates, about ten for a
 //      top-8 of 384.  One per lane, each counts those before it.
 //   3. Where two candidates' values are too close for FP32 to tell (some of a thousand tokens of a
-//      sigmoid router of 384 experts), the candidates' are computed in binary64; where two groups' are, or
-//      the softmax's sum is needed for that, or more than 32 candidates are left, the whole
+//      sigmoid router of 384 experts), the candidates' are computed in binary64; where two groups' are, those
+//      of the groups in question; where the softmax's sum is needed for that, or more than 32 candidates are left, the whole
 //      token is done by choose_in_64_bits.
 // Slack: a sigmoid of the fast functions is off by s (1 - s) (2^-22 + |l| 2^-24) + 2^-23, below 3e-7, of the
 // accurate ones by three half ulps; a softmax by its sum's E / 32 + 5 half ulps and those of the exponents, below 4e-6.
@@ -193,6 +193,54 @@ constexpr float kSlackFast = 1e-6f, kSlackAccurate = 5e-7f, kSlackSoftmax = 4e-6
 // Shared memory of a warp, in doubles: the list (16), its candidates (16), their inputs or values in
 // binary64 (32); or the groups' rows; or all values in binary64 and the groups' (E + 32).
 __host__ __device__ inline int own_doubles(int E) { return (E > 32 ? E + 33 : 65) & ~1; }
+
+// A value in binary64 (-inf: not available); total: the softmax's sum.
+__device__ __forceinline__ double value_in_64_bits(const RouteArgs& a, float l, float b, float mx, double total) {
+    if (!(l > -INFINITY && b > -INFINITY)) return -INFINITY;
+    return (a.score == CHORD_SCORE_SOFTMAX ? exp((double)l - (double)mx) / total : 1.0 / (1.0 + exp(-(double)l))) + (double)b;
+}
+
+// The groups that take part, where FP32 does not decide: lane g has group g's value in FP32, those above `above` are
+// in, those below `below` out, the ones between are ordered by their values in binary64, the lower index first of equal
+// ones.  z: E doubles of the warp's own; lpg lanes (a power of two) share a group.
+__device__ __noinline__ unsigned groups_in_64_bits(const RouteArgs& a, int64_t t, int lane, float value, float above, float below, float mx, int lpg,
+                                                   double* z) {
+    const int size = a.E / a.groups;
+    const bool in = lane < a.groups && value > above, open = lane < a.groups && !in && value > -INFINITY && !(value < below);
+    const unsigned sure = __ballot_sync(kAll, in), asked = __ballot_sync(kAll, open);
+    double total = 0;
+    if (a.score == CHORD_SCORE_SOFTMAX) {
+        for (int e = lane; e < a.E; e += 32) {
+            const float l = logit_at(a, t, e);
+            if (l > -INFINITY) total += exp((double)l - (double)mx);
+        }
+        total = warp_sum(total);
+    }
+    for (int e = lane; e < a.E; e += 32)
+        if (asked >> (e / size) & 1u) z[e] = value_in_64_bits(a, logit_at(a, t, e), a.bias ? a.bias[e] : 0.0f, mx, total);
+    __syncwarp();
+    double b1 = -INFINITY, b2 = -INFINITY;
+    const int g = lane / lpg;
+    if (g < a.groups && asked >> g & 1u)
+        for (int i = lane % lpg; i < size; i += lpg) {
+            const double v = z[g * size + i];
+            b2 = fmax(b2, fmin(b1, v));
+            b1 = fmax(b1, v);
+        }
+    for (int o = 1; o < lpg; o <<= 1) {
+        const double o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+        b2 = fmax(fmax(b2, o2), fmin(b1, o1));
+        b1 = fmax(b1, o1);
+    }
+    double mine = __shfl_sync(kAll, a.best == 2 && b2 > -INFINITY ? b1 + b2 : b1, (lane * lpg) & 31);
+    int rank = __popc(sure);
+    for (int k = 0; k < a.groups; ++k) {
+        const double v = __shfl_sync(kAll, mine, k);
+        rank += (asked >> k & 1u) && (v > mine || (v == mine && k < lane));
+    }
+    __syncwarp();
+    return sure | __ballot_sync(kAll, open && rank < a.topk_groups);
+}
 
 template <int VPL, bool F32>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
@@ -290,12 +338,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
             rank += v > gv || (v == gv && k < lane);
         }
         if (lane >= a.groups) rank = 32;
-        const unsigned kept = __ballot_sync(kAll, rank < a.topk_groups);
+        unsigned kept = __ballot_sync(kAll, rank < a.topk_groups);
         if (!by_logit && a.topk_groups < a.groups) {
             // the last group that is kept and the first that is not: two values each, each off by the slack
             const unsigned last = __ballot_sync(kAll, rank == a.topk_groups - 1), next = __ballot_sync(kAll, rank == a.topk_groups);
             const float v = __shfl_sync(kAll, gv, __ffs(last) - 1), w = __shfl_sync(kAll, gv, __ffs(next) - 1);
-            fine = !(w > -INFINITY) || (v < INFINITY && v - w > slack * (4.0f + fabsf(v) + fabsf(w)));
+            const float apart = slack * (4.0f + fabsf(v) + fabsf(w));
+            __syncwarp();
+            if (w > -INFINITY && !(v < INFINITY && v - w > apart)) kept = groups_in_64_bits(a, t, lane, gv, v + apart, w - apart, mx, lpg, own);
         }
         __syncwarp();
 #pragma unroll

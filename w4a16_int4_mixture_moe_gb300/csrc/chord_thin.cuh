@@ -137,17 +137,18 @@ __device__ __forceinline__ float joined(const float* red, int n, int i) {
 }
 
 // ---- the same for many rows, staged in shared memory ----------------------------------------
-// 64 rows of x times NT x 8 weight rows: every thread copies 16-byte pieces of a stage of 64 columns with
-// cp.async, kStages - 1 stages are on their way.  Warp w takes rows 16 (w mod 4) and half of a stage's four k16
-// steps; the halves are joined at the end.  Rows of 128 bytes, piece p of row r at p xor (r mod 8).
+// 64 rows of x times NT x 8 weight rows: every thread copies 16-byte pieces of a stage of 128 columns, two tiles of 64,
+// with cp.async, kStages - 1 stages are on their way.  Warp w takes rows 16 (w mod 4) of tile w / 4; the tiles' sums
+// are joined at the end.  A tile's rows are 128 bytes, piece p of row r at p xor (r mod 8).  (Stages of 64
+// columns meet twice as often: 48 tokens of 384 experts in FP32 14.6 us for 13.9.)
 template <int NT>
 struct Staged {
-    static constexpr int kRows = 64, kCols = NT * 8, kTileCols = 64, kStages = 7;
-    static constexpr int kStageBytes = (kRows + kCols) * 128;
+    static constexpr int kRows = 64, kCols = NT * 8, kTileCols = 128, kHalf = (kRows + kCols) * 128;
+    static constexpr int kStageBytes = 2 * kHalf, kStages = NT <= 2 ? 5 : NT <= 4 ? 4 : 3;
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes;          // the ring
     static constexpr size_t kSums = (size_t)2 * kRows * kCols * 4;          // over it, afterwards: [2][kRows][kCols]
     static constexpr size_t kBytes = kSmem > kSums ? kSmem : kSums;
-    static constexpr int kChainStages = 8;                                  // two instructions a stage
+    static constexpr int kChainStages = 4;                                  // four instructions a stage
 
     // This thread's rows of x (t / 8 and t / 8 + 32) and weight rows, at piece t mod 8; null: not copied,
     // whatever is multiplied in its place is not looked at.
@@ -157,12 +158,17 @@ struct Staged {
 
     __device__ __forceinline__ void copy(uint32_t st, int col, int64_t w_offset, int K) const {
         const int t = threadIdx.x, row = t >> 3, piece = t & 7;
-        const bool in = col + piece * 8 < K;
         const uint32_t at = st + (uint32_t)row * 128u + (uint32_t)(((piece ^ row) & 7) << 4);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (x[h]) fill(at + h * 4096u, x[h] + col, in);
-            if (h * 32 < kCols && w[h]) fill(at + kRows * 128u + h * 4096u, w[h] + w_offset + col, in);
+        for (int half = 0; half < 2; ++half) {
+            const int k = col + half * 64;
+            const bool in = k + piece * 8 < K;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t to = at + (uint32_t)(half * kHalf + h * 4096);
+                if (x[h]) fill(to, in ? x[h] + k : x[h], in);
+                if (h * 32 < kCols && w[h]) fill(to + kRows * 128u, in ? w[h] + w_offset + k : w[h], in);
+            }
         }
     }
     // 16 bytes, or zeros behind the last column.
@@ -172,9 +178,9 @@ struct Staged {
     __device__ __forceinline__ void multiply(uint32_t st) {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         const int ar = (warp & 3) * 16 + (lane & 15), br = (lane >> 4) * 8 + (lane & 7);
+        st += (uint32_t)((warp >> 2) * kHalf);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int kk = (warp >> 2) * 2 + q;
+        for (int kk = 0; kk < 4; ++kk) {
             uint32_t a[4];
             ldsm4(a, st + (uint32_t)ar * 128u + (uint32_t)(((kk * 2 + (lane >> 4)) ^ (ar & 7)) << 4));
 #pragma unroll

@@ -142,7 +142,7 @@ __device__ __forceinline__ int slices_of(const AdapterArgs& g, int n) {
 
 // ---- v = A x --------------------------------------------------------------------
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 2) adapter_down_kernel(const AdapterArgs g) {
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) adapter_down_kernel(const AdapterArgs g) {
     using Tile = thin::Staged<NT>;
     constexpr int NB = Tile::kCols;
     static_assert(Tile::kRows == kManyRows, "a block of the plan is a tile");

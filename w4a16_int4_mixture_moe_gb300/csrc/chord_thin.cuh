@@ -144,7 +144,7 @@ __device__ __forceinline__ float joined(const float* red, int n, int i) {
 template <int NT>
 struct Staged {
     static constexpr int kRows = 64, kCols = NT * 8, kTileCols = 128, kHalf = (kRows + kCols) * 128;
-    static constexpr int kStageBytes = 2 * kHalf, kStages = NT <= 2 ? 5 : NT <= 4 ? 4 : 3;
+    static constexpr int kStageBytes = 2 * kHalf, kStages = NT == 4 ? 4 : 3;
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes;          // the ring
     static constexpr size_t kSums = (size_t)2 * kRows * kCols * 4;          // over it, afterwards: [2][kRows][kCols]
     static constexpr size_t kBytes = kSmem > kSums ? kSmem : kSums;

@@ -710,8 +710,9 @@ size_t chord_adapter_workspace_bytes(int64_t T, int topk, int adapters, int E, i
  *   workspace    >= chord_adapter_workspace_bytes(...), 16-byte aligned; calls that overlap on the
  *                GPU need one each
  * rank % 8 == 0 and at most 128 (a smaller rank is padded with zeros), parts <= 4, K % 8 == 0,
- * N % (8 * parts) == 0, rows 16-byte aligned, adapters * E <= 65536.  A B that is an infinity may
- * give NaN where the exact sum is infinite. */
+ * N % (8 * parts) == 0, rows 16-byte aligned, adapters * E <= 65536, T * topk < 2^30.  A B that is
+ * an infinity may give NaN where the exact sum is infinite.  The result does not depend on timing.  Up
+ * to 256 pairs are one launch. */
 chord_status chord_adapter_add(const void *x, int64_t x_rows, int64_t x_stride, int a_row_divisor,
                                const int32_t *adapter_ids, const int32_t *topk_ids, int T, int topk,
                                int adapters, int E, const void *A, const void *B, const float *scale, int rank,

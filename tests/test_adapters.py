@@ -155,6 +155,22 @@ def test_one_adapter_no_adapter_and_all_different(T):
         check(c, exact=True)
 
 
+#        T, topk, S, E, rank, parts, K, N, div, dense: more pairs than one cluster plans, ranks and parts of every kernel
+LARGE = [(20000, 1, 3, 1, 16, 1, 64, 40, 1, True), (5000, 4, 2, 7, 8, 2, 40, 48, 4, False), (400, 1, 9, 1, 128, 4, 136, 416, 1, True),
+         (300, 2, 2, 3, 104, 1, 520, 264, 2, False), (300, 1, 2, 1, 48, 2, 328, 336, 1, True), (260, 1, 200, 1, 24, 1, 72, 136, 1, True),
+         (257, 1, 1, 1, 8, 1, 8, 8, 1, True), (1000, 3, 4, 5, 16, 4, 96, 1056, 3, False)]
+
+
+@gpu
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("shape", LARGE)
+def test_many_pairs(shape, out):
+    need_gpu()
+    T, topk, S, E, rank, parts, K, N, div, dense = shape
+    check(make(T, topk, S, E, rank, parts, K, N, div, out, seed=7 + T, dense=dense, integer=True), exact=True)
+    check(make(T, topk, S, E, rank, parts, K, N, div, out, seed=8 + T, dense=dense))
+
+
 @gpu
 def test_every_pair_elsewhere():
     need_gpu()

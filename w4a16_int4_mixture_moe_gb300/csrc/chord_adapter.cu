@@ -32,6 +32,7 @@ constexpr int kFewRows = 16, kManyRows = 64;   // rows of a block
 constexpr int kThreads = thin::kThreads, kWarps = thin::kWarps;
 constexpr int kMaxSplit = 16;
 constexpr int64_t kSplitRows = 16384;          // K slices times pairs, at most, where there is more than one slice
+constexpr int kMaxPairs = 1 << 30;             // positions in the plan, padded, stay below 2^31
 constexpr int kNone = -2;                      // slot of a pair that is not touched; -1: its row of y is base's
 
 struct AdapterArgs {
@@ -954,7 +955,7 @@ extern "C" {
 
 size_t chord_adapter_workspace_bytes(int64_t T, int topk, int adapters, int E, int rank, int parts) {
     if (T < 0 || topk <= 0 || adapters <= 0 || E <= 0 || rank <= 0 || parts <= 0 || rank > 128 || parts > 4) return 0;
-    if (T > INT32_MAX / topk || adapters > 65536 / E) return 0;
+    if (T > (kMaxPairs - 1) / topk || adapters > 65536 / E) return 0;
     const size_t bytes = layout_of(T * topk, (int64_t)adapters * E, rank * parts).bytes;
     return bytes ? bytes : 256;
 }
@@ -969,7 +970,7 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
         return CHORD_ERR_INVALID_ARG;
     const int64_t P = (int64_t)T * topk;
     const int per = y_dtype == CHORD_DTYPE_F32 ? 4 : 8;
-    if (P >= INT32_MAX || adapters > 65536 / E || rank % 8 || rank > 128 || parts > 4 || N % (8 * parts) || K % 8)
+    if (P >= kMaxPairs || adapters > 65536 / E || rank % 8 || rank > 128 || parts > 4 || N % (8 * parts) || K % 8)
         return CHORD_ERR_UNSUPPORTED;
     if (!topk_ids && E != 1) return CHORD_ERR_INVALID_ARG;
     if (P == 0) return CHORD_OK;

@@ -115,15 +115,17 @@ __global__ void __launch_bounds__(thin::kThreads, 2) logits_staged_kernel(const 
         });
 }
 
-// tiles x slices CTAs; K is cut until every SM has a CTA, as long as a slice keeps `least` steps.  Sixteen slices are
-// more than a cluster may have everywhere, which the kernel has to be allowed once on each device (48 tokens of 384
-// experts in FP32: eight slices 13.9 us, sixteen 10.9).
+// tiles x slices CTAs: as many slices as leave two CTAs to an SM, of `least` steps at least.  Sixteen, more than a
+// cluster may have everywhere, need the kernel to be allowed that once on each device, and pay only where their
+// clusters find SMs of their own (384 experts in FP32, 48 tokens: eight slices 13.9 us, sixteen 10.9; 64 experts, 512
+// tokens: eight 6.8, sixteen 8.6).
 template <void (*KERN)(LogitArgs, int)>
 cudaError_t launch_tiles(const LogitArgs& a, int64_t tiles, int64_t steps, int least, size_t smem, cudaStream_t st) {
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(KERN), smem);
     if (e != cudaSuccess) return e;
     int splits = 1;
-    while (splits < 16 && tiles * splits < device_info().sm_count && steps >= (int64_t)least * 2 * splits) splits *= 2;
+    const int64_t sms = device_info().sm_count;
+    while (splits < 16 && tiles * splits * 2 <= (splits < 8 ? 2 * sms : sms + sms / 3) && steps >= (int64_t)least * 2 * splits) splits *= 2;
     if (splits > 8) {
         static std::atomic<uint64_t> allowed{0};   // a bit for each device
         int dev = 0;
@@ -186,9 +188,9 @@ cudaError_t launch_staged(const LogitArgs& a, cudaStream_t st) {
 constexpr int kReaders = 8, kWideThreads = (kReaders + 2) * 32;
 constexpr int kHalfCols = 64, kStageCols = 2 * kHalfCols;
 constexpr int kPairTokens = 256;
-// The staged tiles copy 96 rows of K columns for 64 x 32 sums, the wide ones 128 + N / 2 for 128 x N; a step of 128 columns
-// takes the wide kernel 0.3 us at least.  Staged and wide, us (E, H, tiles): 384, 7168: 48 tiles 18.3, 24.6; 96 26.6,
-// 24.6; 192 41, 25.  161, 2088: 48 12.3, 16.4; 96 16.4, 16.4; 192 20.5, 16.4.  64, 4096: 64 14.8, 18.4; 128 20.8, 19.5.
+// The staged tiles copy 96 rows of K columns for 64 x 32 sums, the wide ones 128 + N / 2 for 128 x N, where a step of 128
+// columns takes 0.25 us at least.  Staged and wide, us in a graph (E, H: tiles): 384, 7168: 72 13.1, 19.6; 96 21.0,
+// 19.6; 192 34, 20.  161, 2088: 72 8.7, 10.2; 96 12.3, 10.2.  64, 4096: 64 9.5, 12.4; 94 14.3, 13.0.
 constexpr int64_t kStagedTiles = 90;
 constexpr int kChainStages = 2;
 constexpr int kMaxWideStages = 6;
@@ -334,25 +336,23 @@ __global__ void __launch_bounds__(kWideThreads, 1) logits_wide_kernel(const Logi
             __syncwarp();
             if (lane == 0) tc5::arrive_relaxed_at(smem_u32(&acc_empty[buf]), 0);
         }
-        const int64_t t = t0 + quarter * 32 + lane;
-        if (ok && t < a.T) {
-            float* out = a.out + t * a.E;
-            const bool wide = a.E % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
+        // Through the warp's part of the ring, which nobody uses any more, so that 16 lanes write 64 bytes of a row.
+        float* stg = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw))) + warp * (32 * 17);
 #pragma unroll
-            for (int i = 0; i < G; ++i) {
-                const int g = 2 * i + half, e = e0 + g * 16;
-                if (g >= groups) continue;
+        for (int i = 0; i < G; ++i) {
+            const int g = 2 * i + half;
+            if (!ok || g >= groups) continue;
 #pragma unroll
-                for (int u = 0; u < 16; u += 4) {
-                    if (wide && e + u + 3 < a.E) {
-                        *reinterpret_cast<float4*>(out + e + u) = make_float4(sum[i][u], sum[i][u + 1], sum[i][u + 2], sum[i][u + 3]);
-                    } else {
+            for (int u = 0; u < 16; ++u) stg[lane * 17 + u] = sum[i][u];
+            __syncwarp();
+            const int e = e0 + g * 16 + (lane & 15);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (e + u + q < a.E) out[e + u + q] = sum[i][u + q];
-                    }
-                }
+            for (int k = 0; k < 16; ++k) {
+                const int r = 2 * k + (lane >> 4);
+                const int64_t t = t0 + quarter * 32 + r;
+                if (t < a.T && e < a.E) a.out[t * a.E + e] = stg[r * 17 + (lane & 15)];
             }
+            __syncwarp();
         }
         __syncwarp();
     }

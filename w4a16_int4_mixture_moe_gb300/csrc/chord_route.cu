@@ -74,32 +74,32 @@ __device__ __forceinline__ void write_choice(const RouteArgs& a, int64_t t, int 
     }
 }
 
+// The softmax's sum in binary64.
+__device__ __noinline__ double total_in_64_bits(const RouteArgs& a, int64_t t, int lane, float mx) {
+    double total = 0;
+    for (int e = lane; e < a.E; e += 32) {
+        const float l = logit_at(a, t, e);
+        if (l > -INFINITY) total += exp((double)l - (double)mx);
+    }
+    return warp_sum(total);
+}
+
+// A value in binary64 (-inf: not available); total: the softmax's sum.
+__device__ __forceinline__ double value_in_64_bits(const RouteArgs& a, float l, float b, float mx, double total) {
+    if (!(l > -INFINITY && b > -INFINITY)) return -INFINITY;
+    return (a.score == CHORD_SCORE_SOFTMAX ? exp((double)l - (double)mx) / total : 1.0 / (1.0 + exp(-(double)l))) + (double)b;
+}
+
 // The choice by the definition, every value in binary64, one expert after the other: lane k gets
 // the k-th (-1: none).  z: E + 32 doubles of the warp's own.
 __device__ __noinline__ int choose_in_64_bits(const RouteArgs& a, int64_t t, int lane, float mx, double* z) {
     double* gz = z + a.E;
     const double ninf = -INFINITY;
-    double total = 0;
-    if (a.score == CHORD_SCORE_SOFTMAX) {
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = logit_at(a, t, e);
-            if (l > -INFINITY) total += exp((double)l - (double)mx);
-        }
-        total = warp_sum(total);
-    }
+    const double total = a.score == CHORD_SCORE_SOFTMAX ? total_in_64_bits(a, t, lane, mx) : 0.0;
     const bool by_logit = !a.bias && (a.groups == 1 || a.best == 1);
     for (int e = lane; e < a.E; e += 32) {
-        const float l = logit_at(a, t, e), b = a.bias ? a.bias[e] : 0.0f;
-        double v = ninf;
-        if (l > -INFINITY && b > -INFINITY) {
-            if (by_logit)
-                v = l;
-            else if (a.score == CHORD_SCORE_SOFTMAX)
-                v = exp((double)l - (double)mx) / total + (double)b;
-            else
-                v = 1.0 / (1.0 + exp(-(double)l)) + (double)b;
-        }
-        z[e] = v;
+        const float l = logit_at(a, t, e);
+        z[e] = by_logit ? (l > -INFINITY ? (double)l : ninf) : value_in_64_bits(a, l, a.bias ? a.bias[e] : 0.0f, mx, total);
     }
     __syncwarp();
     if (a.groups > 1) {
@@ -164,6 +164,10 @@ __device__ __forceinline__ uint32_t key_of(float v) {
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
+__device__ __forceinline__ float number_of(uint32_t key) {
+    return __uint_as_float(key ^ ((key & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+}
+
 // e^x and 1 / x in one approximate instruction each (relative error below 2^-22 and 2^-23; e^x next to
 // that |x| 2^-24 from its argument).
 __device__ __forceinline__ float fast_exp(float x) {
@@ -178,27 +182,24 @@ __device__ __forceinline__ float fast_rcp(float x) {
 }
 
 // One token per warp; lane l holds experts l, l + 32, ...
-//   1. Values in FP32, each off by at most slack * (1 + |value|).
+//   1. Values in FP32, each off by a known slack.
 //   2. The topk-th largest of the 32 lanes' largest values bounds the topk-th largest value from
 //      below: what is not below it (by twice the slack) are the candidates, about ten for a
 //      top-8 of 384.  One per lane, each counts those before it.
 //   3. Where two candidates' values are too close for FP32 to tell (some of a thousand tokens of a
 //      sigmoid router of 384 experts), the candidates' are computed in binary64; where two groups' are, those
-//      of the groups in question; where the softmax's sum is needed for that, or more than 32 candidates are left, the whole
-//      token is done by choose_in_64_bits.
-// Slack: a sigmoid of the fast functions is off by s (1 - s) (2^-22 + |l| 2^-24) + 2^-23, below 3e-7, of the
-// accurate ones by three half ulps; a softmax by its sum's E / 32 + 5 half ulps and those of the exponents, below 4e-6.
-constexpr float kSlackFast = 1e-6f, kSlackAccurate = 5e-7f, kSlackSoftmax = 4e-6f;
+//      of the groups in question.
+//   4. More than 32 candidates: one after the other by reductions over the warp; where two of these are too close,
+//      or values are infinite, the whole token is done by choose_in_64_bits.
+// A value in FP32 is off by at most slack + kRounding |value|.  A sigmoid of the fast functions is off by s (1 - s)
+// (2^-22 + |l| 2^-24) + 2^-23, below 3e-7, of the accurate ones by s (1 - s) 2^-22 + s 2^-23, below 1.8e-7.  A softmax's score e / total, of E <= 1024
+// experts: the sum by 37 half ulps for its additions, 2 ulps for the function and 7 half ulps for the exponents' rounding
+// (their mean weighted by the scores is below ln E), each exponential by 2 ulps and 0.37 half ulps; all below 4e-6 / total.
+constexpr float kSlackFast = 1e-6f, kSlackAccurate = 2.5e-7f, kSlackSoftmax = 4e-6f, kRounding = 1.2e-7f;
 
 // Shared memory of a warp, in doubles: the list (16), its candidates (16), their inputs or values in
 // binary64 (32); or the groups' rows; or all values in binary64 and the groups' (E + 32).
 __host__ __device__ inline int own_doubles(int E) { return (E > 32 ? E + 33 : 65) & ~1; }
-
-// A value in binary64 (-inf: not available); total: the softmax's sum.
-__device__ __forceinline__ double value_in_64_bits(const RouteArgs& a, float l, float b, float mx, double total) {
-    if (!(l > -INFINITY && b > -INFINITY)) return -INFINITY;
-    return (a.score == CHORD_SCORE_SOFTMAX ? exp((double)l - (double)mx) / total : 1.0 / (1.0 + exp(-(double)l))) + (double)b;
-}
 
 // The groups that take part, where FP32 does not decide: lane g has group g's value in FP32, those above `above` are
 // in, those below `below` out, the ones between are ordered by their values in binary64, the lower index first of equal
@@ -208,14 +209,7 @@ __device__ __noinline__ unsigned groups_in_64_bits(const RouteArgs& a, int64_t t
     const int size = a.E / a.groups;
     const bool in = lane < a.groups && value > above, open = lane < a.groups && !in && value > -INFINITY && !(value < below);
     const unsigned sure = __ballot_sync(kAll, in), asked = __ballot_sync(kAll, open);
-    double total = 0;
-    if (a.score == CHORD_SCORE_SOFTMAX) {
-        for (int e = lane; e < a.E; e += 32) {
-            const float l = logit_at(a, t, e);
-            if (l > -INFINITY) total += exp((double)l - (double)mx);
-        }
-        total = warp_sum(total);
-    }
+    const double total = a.score == CHORD_SCORE_SOFTMAX ? total_in_64_bits(a, t, lane, mx) : 0.0;
     for (int e = lane; e < a.E; e += 32)
         if (asked >> (e / size) & 1u) z[e] = value_in_64_bits(a, logit_at(a, t, e), a.bias ? a.bias[e] : 0.0f, mx, total);
     __syncwarp();
@@ -242,8 +236,48 @@ __device__ __noinline__ unsigned groups_in_64_bits(const RouteArgs& a, int64_t t
     return sure | __ballot_sync(kAll, open && rank < a.topk_groups);
 }
 
+// The places of the n <= 32 candidates, a lane each, by their values in binary64.
+__device__ __noinline__ int rank_in_64_bits(const RouteArgs& a, int64_t t, int lane, float mx, int n, double* own) {
+    const int* list = reinterpret_cast<const int*>(own);
+    double* values = own + 16 + 16;
+    const double total = a.score == CHORD_SCORE_SOFTMAX ? total_in_64_bits(a, t, lane, mx) : 0.0;
+    const int e = list[min(lane, n - 1)];
+    const double d = value_in_64_bits(a, logit_at(a, t, e), a.bias[e], mx, total);   // without a bias nothing is in doubt
+    if (lane < n) values[lane] = d;
+    __syncwarp();
+    int rank = 0;
+    for (int k = 0; k < n; ++k) rank += values[k] > d || (values[k] == d && list[k] < e);
+    return rank;
+}
+
+// More candidates than lanes (many equal logits, a top-k that comes near to 32): the largest of all values, topk times
+// and once more, since it has to be told from the last one chosen; -2 in every lane
+// where FP32 does not tell.
+__device__ __noinline__ int choose_one_by_one(const RouteArgs& a, int lane, float* z, bool exact_order, float slack) {
+    int mine = -1;
+    float before = INFINITY;
+    for (int k = 0; k <= a.topk; ++k) {
+        float best = -INFINITY;
+        int at = lane;
+        for (int e = lane; e < a.E; e += 32)
+            if (z[e] > best) {
+                best = z[e];
+                at = e;
+            }
+        const uint32_t mine_key = key_of(best), key = __reduce_max_sync(kAll, mine_key);
+        const float v = number_of(key);
+        if (!(v > -INFINITY)) break;
+        if (!exact_order && k > 0 && !(before - v > 2.0f * slack + kRounding * (fabsf(v) + fabsf(before)))) return -2;
+        before = v;
+        const int e = (int)__reduce_min_sync(kAll, mine_key == key ? (unsigned)at : 0xffffffffu);
+        if (lane == k && k < a.topk) mine = e;
+        if (e == at) z[e] = -INFINITY;   // this lane's own
+    }
+    return mine;
+}
+
 template <int VPL, bool F32>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, VPL > 16 ? 4 : 8) route_kernel(const RouteArgs a) {
     using In = typename std::conditional<F32, float, __nv_bfloat16>::type;
     extern __shared__ double route_smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -275,7 +309,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
             total = warp_sum(total);
         }
     }
-    const float slack = softmax ? kSlackSoftmax : a.groups > 1 ? kSlackAccurate : kSlackFast;
+    const float slack = softmax ? kSlackSoftmax / total : a.groups > 1 ? kSlackAccurate : kSlackFast;
+    auto off_by = [&](float v) { return slack + kRounding * fabsf(v); };
     if (by_logit) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) z[i] = z[i] > -INFINITY ? fminf(z[i], FLT_MAX) : -INFINITY;
@@ -330,7 +365,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
             b2 = fmaxf(fmaxf(b2, o2), fminf(b1, o1));
             b1 = fmaxf(b1, o1);
         }
-        float gv = __shfl_sync(kAll, a.best == 2 && b2 > -INFINITY ? b1 + b2 : b1, (lane * lpg) & 31);
+        const bool pair = a.best == 2 && b2 > -INFINITY;
+        float gv = __shfl_sync(kAll, pair ? b1 + b2 : b1, (lane * lpg) & 31);
+        const float size_of = warp_max(b1 > -INFINITY ? (pair ? fabsf(b1) + fabsf(b2) : fabsf(b1)) : 0.0f);
         if (lane >= a.groups) gv = -INFINITY;
         int rank = 0;
         for (int k = 0; k < a.groups; ++k) {
@@ -343,7 +380,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
             // the last group that is kept and the first that is not: two values each, each off by the slack
             const unsigned last = __ballot_sync(kAll, rank == a.topk_groups - 1), next = __ballot_sync(kAll, rank == a.topk_groups);
             const float v = __shfl_sync(kAll, gv, __ffs(last) - 1), w = __shfl_sync(kAll, gv, __ffs(next) - 1);
-            const float apart = slack * (4.0f + fabsf(v) + fabsf(w));
+            const float apart = 4.0f * slack + 4.0f * kRounding * size_of;   // of two groups, two values each and their sum
             __syncwarp();
             if (w > -INFINITY && !(v < INFINITY && v - w > apart)) kept = groups_in_64_bits(a, t, lane, gv, v + apart, w - apart, mx, lpg, own);
         }
@@ -368,19 +405,25 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
         if (key == bound) key = 0;
     }
     // bound back to a number; 0: fewer than topk lanes hold anything
-    float least = bound == 0 ? -INFINITY : __uint_as_float(bound ^ ((bound & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+    float least = bound == 0 ? -INFINITY : number_of(bound);
     if (!exact_order) {
         if (!(least < INFINITY)) fine = false;   // biases of +inf: least becomes NaN, the list empty
-        least -= 2.0f * slack * (1.0f + fabsf(least));
+        least -= 2.0f * off_by(least);
     }
     least = fmaxf(least, -FLT_MAX);   // -inf is never chosen (the lowest number is)
     uint32_t mask = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) mask |= z[i] >= least ? 1u << i : 0u;
     const int n = (int)__reduce_add_sync(kAll, (unsigned)__popc(mask));
-    fine = fine && n <= 32;
     int mine = -1;
-    if (fine) {
+    if (fine && n > 32) {
+        float* rows = reinterpret_cast<float*>(own);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (lane + 32 * i < a.E) rows[lane + 32 * i] = z[i];
+        mine = choose_one_by_one(a, lane, rows, exact_order, slack);
+        fine = mine != -2;
+    } else if (fine) {
         int* list = reinterpret_cast<int*>(own);
         float* cand = reinterpret_cast<float*>(own + 16);
         int at = 0;
@@ -400,14 +443,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
             v = l;
             if (a.bias) {
                 b = a.bias[e];
-                v = (softmax ? expf(l - mx) / total : fast_rcp(1.0f + fast_exp(-l))) + b;
+                v = (softmax ? expf(l - mx) / total : 1.0f / (1.0f + expf(-l))) + b;   // accurate: fewer are too close then
             }
             cand[lane] = v;
         }
         __syncwarp();
         // Those before this one, and those that FP32 cannot tell from it (without a bias: that are equal), itself among them.
         int rank = 0, close = 0;
-        const float tol = exact_order ? 0.0f : 2.0f * (softmax ? kSlackSoftmax : kSlackFast) * (1.0f + fabsf(v));
+        const float tol = exact_order ? 0.0f : 2.0f * ((softmax ? slack : kSlackAccurate) + kRounding * fabsf(v));
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
             const float c = cand[k];
@@ -428,17 +471,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
             }
             __syncwarp();
             rank += before;
-            if (!__any_sync(kAll, lane < n && rank < a.topk && close > 0)) {
-            } else if (softmax) {
-                fine = false;   // the sum over all experts is needed in binary64 too
-            } else {
+            if (__any_sync(kAll, lane < n && rank < a.topk && close > 0)) {
                 // the candidates are certain, their order is not
-                double* values = own + 16 + 16;
-                const double d = 1.0 / (1.0 + exp(-(double)l)) + (double)b;
-                if (lane < n) values[lane] = d;
-                __syncwarp();
-                rank = 0;
-                for (int k = 0; k < n; ++k) rank += values[k] > d || (values[k] == d && list[k] < e);
+                rank = rank_in_64_bits(a, t, lane, mx, n, own);
             }
         }
         __syncwarp();

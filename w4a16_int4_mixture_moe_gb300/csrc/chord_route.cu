@@ -189,8 +189,8 @@ __device__ __forceinline__ float fast_rcp(float x) {
 //   3. Where two candidates' values are too close for FP32 to tell (some of a thousand tokens of a
 //      sigmoid router of 384 experts), the candidates' are computed in binary64; where two groups' are, those
 //      of the groups in question.
-//   4. More than 32 candidates: one after the other by reductions over the warp; where two of these are too close,
-//      or values are infinite, the whole token is done by choose_in_64_bits.
+//   4. More than 32 candidates: choose_one_by_one.  Where that is still in doubt, or values are infinite, the whole
+//      token is done by choose_in_64_bits.
 // A value in FP32 is off by at most slack + kRounding |value|.  A sigmoid of the fast functions is off by s (1 - s)
 // (2^-22 + |l| 2^-24) + 2^-23, below 3e-7, of the accurate ones by s (1 - s) 2^-22 + s 2^-23, below 1.8e-7.  A softmax's score e / total, of E <= 1024
 // experts: the sum by 37 half ulps for its additions, 2 ulps for the function and 7 half ulps for the exponents' rounding
@@ -198,7 +198,7 @@ __device__ __forceinline__ float fast_rcp(float x) {
 constexpr float kSlackFast = 1e-6f, kSlackAccurate = 2.5e-7f, kSlackSoftmax = 4e-6f, kRounding = 1.2e-7f;
 
 // Shared memory of a warp, in doubles: the list (16), its candidates (16), their inputs or values in
-// binary64 (32); or the groups' rows; or all values in binary64 and the groups' (E + 32).
+// binary64 (32); or the list and all values (E / 2); or the groups' rows; or all values in binary64 and the groups' (E + 32).
 __host__ __device__ inline int own_doubles(int E) { return (E > 32 ? E + 33 : 65) & ~1; }
 
 // The groups that take part, where FP32 does not decide: lane g has group g's value in FP32, those above `above` are
@@ -250,13 +250,16 @@ __device__ __noinline__ int rank_in_64_bits(const RouteArgs& a, int64_t t, int l
     return rank;
 }
 
-// More candidates than lanes (many equal logits, a top-k that comes near to 32): the largest of all values, topk times
-// and once more, since it has to be told from the last one chosen; -2 in every lane
-// where FP32 does not tell.
-__device__ __noinline__ int choose_one_by_one(const RouteArgs& a, int lane, float* z, bool exact_order, float slack) {
-    int mine = -1;
-    float before = INFINITY;
-    for (int k = 0; k <= a.topk; ++k) {
+// More candidates than lanes (many equal logits, a top-k that comes near to 32): the largest of all values z, one after
+// the other, until one is certainly below the topk-th; where FP32 does not tell the order of those before it, that is
+// found in binary64.  -2 in every lane: still in doubt after 32.  z lies behind the list in the warp's own memory.
+__device__ __noinline__ int choose_one_by_one(const RouteArgs& a, int64_t t, int lane, float mx, bool exact_order, float slack, double* own) {
+    int* list = reinterpret_cast<int*>(own);
+    float* z = reinterpret_cast<float*>(own + 16);
+    bool sure = true;
+    float before = INFINITY, bound = -INFINITY;
+    int n = 0;
+    for (;; ++n) {
         float best = -INFINITY;
         int at = lane;
         for (int e = lane; e < a.E; e += 32)
@@ -267,13 +270,23 @@ __device__ __noinline__ int choose_one_by_one(const RouteArgs& a, int lane, floa
         const uint32_t mine_key = key_of(best), key = __reduce_max_sync(kAll, mine_key);
         const float v = number_of(key);
         if (!(v > -INFINITY)) break;
-        if (!exact_order && k > 0 && !(before - v > 2.0f * slack + kRounding * (fabsf(v) + fabsf(before)))) return -2;
+        if (n >= a.topk && (exact_order || bound - v > 2.0f * slack + kRounding * (fabsf(v) + fabsf(bound)))) break;
+        if (n == 32) return -2;
+        if (!exact_order && n > 0 && !(before - v > 2.0f * slack + kRounding * (fabsf(v) + fabsf(before)))) sure = false;
         before = v;
+        if (n < a.topk) bound = v;
         const int e = (int)__reduce_min_sync(kAll, mine_key == key ? (unsigned)at : 0xffffffffu);
-        if (lane == k && k < a.topk) mine = e;
+        if (lane == 0) list[n] = e;
         if (e == at) z[e] = -INFINITY;   // this lane's own
     }
-    return mine;
+    __syncwarp();
+    if (!sure) {
+        const int e = list[min(lane, n - 1)], rank = rank_in_64_bits(a, t, lane, mx, n, own);
+        __syncwarp();
+        if (lane < n && rank < a.topk) list[rank] = e;
+        __syncwarp();
+    }
+    return lane < min(n, a.topk) ? list[lane] : -1;
 }
 
 template <int VPL, bool F32>
@@ -417,11 +430,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL > 16 ? 4 : 8) route_kern
     const int n = (int)__reduce_add_sync(kAll, (unsigned)__popc(mask));
     int mine = -1;
     if (fine && n > 32) {
-        float* rows = reinterpret_cast<float*>(own);
+        float* rows = reinterpret_cast<float*>(own + 16);
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
             if (lane + 32 * i < a.E) rows[lane + 32 * i] = z[i];
-        mine = choose_one_by_one(a, lane, rows, exact_order, slack);
+        mine = choose_one_by_one(a, t, lane, mx, exact_order, slack, own);
         fine = mine != -2;
     } else if (fine) {
         int* list = reinterpret_cast<int*>(own);

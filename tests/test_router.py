@@ -295,6 +295,25 @@ def test_values_that_fp32_cannot_tell_apart(score):
 
 @gpu
 @pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("E,topk", [(384, 8), (384, 31), (384, 32), (512, 16), (1024, 30), (33, 32), (40, 32)])
+@pytest.mark.parametrize("same", [2, 3, 8, 40])
+def test_near_ties_in_clusters(score, E, topk, same):
+    """Clusters of `same` experts whose values agree to an FP32 rounding, well apart from one another, in any places of
+    the choice and across its end."""
+    need_gpu()
+    g = gen(E + topk * 5 + same)
+    for scale in (1.0, 0.01):
+        l = torch.randn((1, E), generator=g)
+        s = torch.sigmoid(l.double()) if score == SIGMOID else torch.softmax(l.double(), dim=1)
+        target = torch.empty(E, dtype=torch.float64)
+        target[torch.randperm(E, generator=g)] = (torch.arange(E) // same).double() * scale
+        bias = (target - s[0]).float()
+        check(l, topk, bias, score=score)
+        check(l.repeat(5, 1), topk, bias, score=score, renormalize=False)
+
+
+@gpu
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
 @pytest.mark.parametrize("with_bias", [False, True])
 @pytest.mark.parametrize("groups,topk_groups", [(1, 1), (8, 3)])
 def test_masked_experts_and_empty_rows(score, with_bias, groups, topk_groups):

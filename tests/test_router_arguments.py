@@ -65,6 +65,14 @@ def test_adapter_tensors():
         chord.chord_adapter_add(*args[:3], None, *args[4:])      # experts' adapters without their ids
 
 
+def test_adapter_tensors_of_other_dimensions():
+    args = adapter_args()
+    for at, bad, name in ((0, dev(64), "x"), (3, dev(6, dtype=torch.int32), "topk_ids"), (3, dev(dtype=torch.int32), "topk_ids"),
+                          (3, dev(1, 3, 2, dtype=torch.int32), "topk_ids"), (4, dev(64), "A"), (5, dev(16), "B"), (7, dev(32), "base"),
+                          (7, dev(1, 6, 32), "base"), (8, dev(32), "y"), (8, dev(), "y")):
+        refused(chord.chord_adapter_add, args, at, bad, name)
+
+
 def test_workspace_bytes():
     f = chord.chord_adapter_workspace_bytes
     assert f(1, 1, 1, 1, 8, 1) > 0 and f(0, 1, 1, 1, 8, 1) > 0

@@ -638,8 +638,10 @@ def _check_adapter(x, adapter_ids, topk_ids, A, B, scale, base, y, workspace, ty
     _rows(what, "x", x, (bf16,))
     _rows(what, "base", base, (bf16, f32))
     _rows(what, "y", y, (base.dtype,))
+    if topk_ids is not None and topk_ids.dim() != 2:
+        _refuse(what, "topk_ids", topk_ids, "int32 [T, topk]")
     K, (P, N) = x.shape[1], y.shape
-    T, topk = adapter_ids.numel(), 1 if topk_ids is None else topk_ids.shape[-1]
+    T, topk = adapter_ids.numel(), 1 if topk_ids is None else topk_ids.shape[1]
     if B.dim() != (3 if topk_ids is None else 4) or B.shape[-2] != N:
         _refuse(what, "B", B, f"bf16 [adapters, {'' if topk_ids is None else 'E, '}{N}, rank]")
     rank = B.shape[-1]
@@ -665,31 +667,40 @@ def chord_adapter_add(x, a_row_divisor: int, adapter_ids, topk_ids, A, B, scale,
     both bf16 or both float32 (base may be y).  Rows of x, base and y may be any (aligned) stride apart."""
     types = _dtypes or _types()
     bf16, i32, dt, dev = types["bf16"], types["int32"], y.dtype, _current_device()
-    xs, ys, As, Bs, code = x.shape, y.shape, A.shape, B.shape, types.get(dt)
-    T = adapter_ids.numel()
+    T, code = adapter_ids.numel(), types.get(dt)
+    good = x.dim() == y.dim() == base.dim() == 2
     if topk_ids is None:
-        topk, lead = 1, 1
-        good = len(As) == 3
+        topk = E = 1
+        ids = None
+        if good := good and A.dim() == B.dim() == 3:
+            adapters, R, AK = A.shape
+            lead, N, rank = B.shape
+            good = lead == adapters
     else:
-        ids = topk_ids.shape
-        topk, lead = ids[-1], 2
-        good = (len(As) == 4 and len(ids) == 2 and ids[0] == T and topk_ids.dtype is i32 and topk_ids.is_contiguous()
-                and topk_ids.get_device() == dev)
-    if not (good and code is not None and x.dtype is A.dtype is B.dtype is bf16 and base.dtype is dt and adapter_ids.dtype is i32
-            and len(xs) == len(ys) == 2 and x.stride(1) == base.stride(1) == y.stride(1) == 1 and base.shape == ys
-            and ys[0] == T * topk and As[:lead] == Bs[:lead] and len(Bs) == lead + 2 and Bs[-2] == ys[1] and As[-1] == xs[1]
-            and Bs[-1] and As[-2] % Bs[-1] == 0 and A.is_contiguous() and B.is_contiguous() and adapter_ids.is_contiguous()
-            and workspace.is_contiguous() and x.get_device() == A.get_device() == B.get_device() == base.get_device()
-            == y.get_device() == adapter_ids.get_device() == workspace.get_device() == dev
-            and (scale is None or (scale.dtype is types["f32"] and scale.shape == Bs[:1] and scale.is_contiguous()
+        ids, topk = topk_ids.data_ptr(), 0
+        if good := (good and A.dim() == B.dim() == 4 and topk_ids.dim() == 2 and topk_ids.dtype is i32 and topk_ids.is_contiguous()
+                    and topk_ids.get_device() == dev):
+            tokens, topk = topk_ids.shape
+            adapters, E, R, AK = A.shape
+            lead, also, N, rank = B.shape
+            good = tokens == T and lead == adapters and also == E
+    if good:
+        (x_rows, K), (x_stride, one), (y_stride, one_y), (base_stride, one_base) = x.shape, x.stride(), y.stride(), base.stride()
+    if not (good and AK == K and one == one_y == one_base == 1 and rank and R % rank == 0 and y.shape == (T * topk, N) == base.shape
+            and x.dtype is A.dtype is B.dtype is bf16 and base.dtype is dt and code is not None and adapter_ids.dtype is i32
+            and A.is_contiguous() and B.is_contiguous() and adapter_ids.is_contiguous() and workspace.is_contiguous()
+            and x.get_device() == A.get_device() == B.get_device() == base.get_device() == y.get_device()
+            == adapter_ids.get_device() == workspace.get_device() == dev
+            and (scale is None or (scale.dtype is types["f32"] and scale.shape == (adapters,) and scale.is_contiguous()
                                    and scale.get_device() == dev))):
         _check_adapter(x, adapter_ids, topk_ids, A, B, scale, base, y, workspace, types)
-    rank = Bs[-1]
+        (x_rows, K), N, rank, R = x.shape, y.shape[1], B.shape[-1], A.shape[-2]
+        adapters, E, topk = B.shape[0], *((1, 1) if topk_ids is None else (B.shape[1], topk_ids.shape[1]))
+        x_stride, y_stride, base_stride = x.stride(0), y.stride(0), base.stride(0)
     st = (_lib or load()).chord_adapter_add(
-        x.data_ptr(), xs[0], x.stride(0), a_row_divisor, adapter_ids.data_ptr(), None if topk_ids is None else topk_ids.data_ptr(), T,
-        topk, Bs[0], 1 if topk_ids is None else Bs[1], A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr(), rank,
-        As[-2] // rank, ys[1], xs[1], base.data_ptr(), base.stride(0), y.data_ptr(), y.stride(0), code, workspace.data_ptr(),
-        workspace.nbytes, None if opts is None else _o(opts), _s(stream))
+        x.data_ptr(), x_rows, x_stride, a_row_divisor, adapter_ids.data_ptr(), ids, T, topk, adapters, E, A.data_ptr(), B.data_ptr(),
+        None if scale is None else scale.data_ptr(), rank, R // rank, N, K, base.data_ptr(), base_stride, y.data_ptr(), y_stride, code,
+        workspace.data_ptr(), workspace.nbytes, None if opts is None else _o(opts), _s(stream))
     if st:
         raise ChordError(st, "chord_adapter_add")
 

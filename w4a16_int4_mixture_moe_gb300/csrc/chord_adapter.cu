@@ -1,18 +1,22 @@
 // Low-rank adapters of many requests beside a projection that they share:
 //   v[p] = A[a, e] x[p / div],   y[p] = base[p] + scale[a] * B[a, e] v[p]
-// A slot is an adapter of an expert, a * E + e; the pairs of one slot are taken together, in blocks of
-// up to 16 rows a matrix-instruction tile, so a slot's weights are read once a block.
-//   plan   (more than kFewPairs pairs) the blocks: a counting sort of the pairs by slot.  With few
-//          pairs every CTA of the two kernels finds the blocks itself, which costs less than a launch.
-//   down   v, a block's rows times the slot's A: thin products (chord_thin.cuh), an item is (block, up to
-//          64 rows of A, K slice).  K slices are partial sums in the workspace, as many as
-//          fill the GPU; both kernels work the number out from the number of blocks.
-//   up     y, an item is (block, columns).  The slices of v are added in order, scaled and split into three
-//          bf16 parts of eight bits each, so the tensor cores multiply all of an FP32 v.  The
-//          columns of a 32-column tile are dealt so that a lane ends with eight neighbouring ones:
-//          base and y move in 16-byte pieces.
-// Both are bound by bytes: x and A below, base and y (and B) above; tcgen05 would add nothing but the
-// staging in shared memory.
+// A slot is an adapter of an expert, a * E + e; the pairs of one slot are taken together, in blocks, so a slot's
+// weights are read once a block.
+// Up to kFewPairs pairs: one launch (adapter_few_kernel), in which every CTA finds the blocks, of 16 rows, itself.  Bound by
+//   latency (one token of 7168 columns, 4096 outputs, rank 16: 6.4 us in a graph).
+// More pairs: three launches.
+//   plan   blocks of 64 rows by a counting sort of the pairs by slot: 5.5 to 8.5 us for 8192 pairs.
+//   down   v, a block's rows times the slot's A, staged products (chord_thin.cuh); an item is (block, up to 64 rows of A,
+//          K slice).  K slices are partial sums in the workspace, as many as fill the GPU.  Bound by the copies to shared
+//          memory, x's and A's (3584 pairs of 7168 columns, rank 64: 21 us, 2.4 TB/s of x; 7168 pairs of 2048, rank 16: 12).
+//   up     y = base + scale B v.  The slices of v are added in order, scaled and split into three bf16 parts of eight bits
+//          each, so the tensor cores multiply all of an FP32 v.  A tile's columns are dealt so that a lane ends with whole
+//          16-byte pieces of its rows of base and y.  Ranks up to 16 are bound by base's and y's bytes (8192 pairs of 7168
+//          FP32 columns, rank 16: 100 us, 4.7 TB/s; a copy in the same pattern 84), larger ones by latency between
+//          instructions at 12 warps an SM, which is what v's fragments leave room for (4096 rows of 4096 columns,
+//          rank 64: 29 us, tensor pipe 41 % busy).
+// Warp-level instructions: a block's rows are gathered, which TMA does at 46 ns for four rows, and a rank of 8 to 128 leaves
+// tcgen05 nothing to gain from.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -27,6 +31,8 @@
 namespace chord {
 namespace {
 
+// One launch up to these.  One and three launches, us in a graph, rank 16: 256 pairs of 8 adapters 11.5, 16.4; of 16 adapters
+// of 8 experts (111 blocks, two rounds of clusters) 28.7, 22.9, but 128 pairs 15.3, 19.4, and the blocks are not known before the launch.
 constexpr int kFewPairs = 256;
 constexpr int kFewRows = 16, kManyRows = 64;   // rows of a block
 constexpr int kThreads = thin::kThreads, kWarps = thin::kWarps;
@@ -79,8 +85,8 @@ __device__ __forceinline__ int slot_of(const AdapterArgs& g, int p, bool report)
 // ---- blocks of few pairs ------------------------------------------------------
 struct FewBlocks {
     alignas(16) int slot[kFewPairs];   // of each pair
-    int leader[kFewPairs];   // first pair of each block
-    int rank[kFewPairs];     // pairs of the same slot before each
+    int leader[kFewPairs];             // first pair of each block
+    int rank[kFewPairs];               // pairs of the same slot before each
     int counts[kWarps];
     int n;
 };
@@ -234,7 +240,8 @@ __device__ __forceinline__ void split3(float v0, float v1, uint32_t& h0, uint32_
 // slices read by each through distributed shared memory and added in rank order, then each its share of
 // the columns.  Where there are few blocks, several clusters compute the same v for columns of their own: A
 // comes from L2 then, and one launch is what a call of one token costs.  Clusters are of eight CTAs while all
-// blocks find one at once, of four beyond.
+// blocks find one at once, of four beyond (eight and four: one token of rank 16 6.3, 7.2, of rank 64 13.3, 17.2; 64 pairs of 128 slots
+// 17.8, 14.8).
 
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
     float4 v;
@@ -491,7 +498,8 @@ struct UpRows {
 };
 
 // Ranks up to 16: the work of all rows, sixteen at a time, is dealt to the warps in equal ranges (blocks hold 1 to 64
-// rows), B's pieces come straight from global memory a tile ahead, nothing is shared and no warp waits for another.
+// rows), B's pieces come straight from global memory a tile ahead, nothing is shared and no warp waits for another.  (8192
+// pairs of rank 16, whole calls, with this kernel and with the next: FP32 126, 149; bf16 the same.)
 template <bool F32>
 __global__ void __launch_bounds__(kUpThreads, 4) adapter_up_small_kernel(const AdapterArgs g) {
     using Rows = UpRows<1, F32>;
@@ -651,7 +659,8 @@ struct PlanArgs {
 };
 
 constexpr int kPlanThreads = 1024;
-// A cluster of kPlanCtas CTAs plans up to these; beyond, three kernels over the GPU.
+// A cluster of kPlanCtas CTAs plans up to these, as many as its threads hold; beyond, three kernels over the GPU (a call of 512
+// pairs 12.3 us with the one, 18.5 with the three; of 16384 19.5, 27.4).
 constexpr int kPlanCtas = 8, kPlanPerThread = 2, kPlanPairs = kPlanCtas * kPlanPerThread * kPlanThreads, kPlanSlots = 16384;
 
 // Exclusive sum over the threads of the CTA; every thread gets the total too.

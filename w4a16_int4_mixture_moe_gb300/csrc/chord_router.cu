@@ -50,7 +50,7 @@ __device__ __forceinline__ void join_slices(int splits, float* shares, Mine mine
     }
 }
 
-// Up to 16 tokens, NT x 8 experts.
+// Up to 16 tokens, NT x 8 experts (16 tokens of 7168 columns, 384 experts: 4.2 us in a graph, staged as below 6.9).
 template <int NT>
 __global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const LogitArgs a, int splits) {
     using Warp = thin::Warp<1, NT>;
@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const Logit
         });
 }
 
-// 64 tokens, 32 experts.
+// 64 tokens, 32 experts.  Bound by its copies to shared memory and their latency (48 tokens of 7168 columns, 384 experts in
+// three parts: 10.9 us in a graph, 16.5 MB of weights).
 using LogitTile = thin::Staged<4>;
 constexpr int kLogitTile = LogitTile::kRows * LogitTile::kCols;
 
@@ -184,7 +185,7 @@ cudaError_t launch_staged(const LogitArgs& a, cudaStream_t st) {
 // accumulators.  The instructions' additions chop, so a chain is 256 columns (16 instructions) and
 // the eight warps add the chains up in registers, one accumulator being read while the other is filled
 // (relative error of a K = 7168 sum: 3.8e-6 in chains of 224, 2.5e-7 so, 9e-7 of PyTorch's FP32).
-// Bound by the copies from L2.
+// 8192 tokens of 7168 columns, 384 experts: 36 us in a graph, 1.25 PFLOP/s, the tensor pipe 71 % busy in the CTAs that run.
 constexpr int kReaders = 8, kWideThreads = (kReaders + 2) * 32;
 constexpr int kHalfCols = 64, kStageCols = 2 * kHalfCols;
 constexpr int kPairTokens = 256;

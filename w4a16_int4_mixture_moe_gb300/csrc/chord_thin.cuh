@@ -1,10 +1,12 @@
-// Thin products on the warp-level tensor cores: up to 64 rows of x times up to 64 rows of weights over a long
-// K, for the router's logits and the first half of an adapter.  There is little to compute and every
-// byte is used once or a few times, so nothing is staged: a lane loads 16 bytes of its rows
-// straight into the fragments of m16n8k16 instructions.  Lane (g, c) takes columns 8c .. 8c + 7 of a
-// 32-column step; the instruction's k order is whatever puts them into its slots, the same for
+// Thin products on the warp-level tensor cores: some rows of x times some rows of weights over a long K, for the
+// router's logits and the first half of an adapter.
+// Up to 16 rows (Warp): there is little to compute and every byte is used once or a few times, so nothing is staged: a
+// lane loads 16 bytes of its rows straight into the fragments of m16n8k16 instructions.  Lane (g, c) takes columns
+// 8c .. 8c + 7 of a 32-column step; the instruction's k order is whatever puts them into its slots, the same for
 // both operands.  The warps of a CTA take every eighth step, so a CTA reads 512 neighbouring bytes of a row, and
-// add their sums up through shared memory.
+// add their sums up through shared memory.  Bound by latency: one row of 7168 columns times 384 rows 3.9 us in a graph,
+// 1.4 TB/s of weights.
+// Up to 64 rows (Staged): below.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -57,10 +57,10 @@ struct AdapterArgs {
     int64_t base_stride, y_stride;
     int copy;                     // rows without an adapter are copied from base
     int units;                    // items of a block and K slice
-    int max_splits, target;       // K slices: as many as make `target` items
+    int max_splits, resident;     // K slices at most; CTAs of the first half that run at once
     float* v;                     // [slices, P, R]
     // the plan, for more than kFewPairs pairs
-    int32_t* nblocks;             // [2]: blocks, sixteens
+    int32_t* nblocks;             // [4]: blocks, sixteens, blocks without an adapter (the first ones), K slices
     int32_t* block_slot;
     int32_t* block_count;         // rows of each block
     int32_t* rows;                // [blocks, kManyRows]
@@ -141,12 +141,6 @@ __device__ __forceinline__ int block_rows(const AdapterArgs& g, const FewBlocks*
     return slot;
 }
 
-// K slices of a call with n blocks.
-__device__ __forceinline__ int slices_of(const AdapterArgs& g, int n) {
-    const int64_t items = (int64_t)n * g.units;
-    return items >= g.target ? 1 : max(1, min(g.max_splits, (int)((g.target + items - 1) / max(items, (int64_t)1))));
-}
-
 // ---- v = A x --------------------------------------------------------------------
 template <int NT>
 __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) adapter_down_kernel(const AdapterArgs g) {
@@ -157,13 +151,12 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) adapter_down_kernel
     __shared__ int32_t rows[kManyRows];
     pdl_trigger();
     pdl_wait();
-    const int n = *g.nblocks, splits = slices_of(g, n), chunks = (g.R + NB - 1) / NB, per = chunks * splits;
+    const int first = g.nblocks[2], n = g.nblocks[0] - first, splits = g.nblocks[3], chunks = (g.R + NB - 1) / NB, per = chunks * splits;
     const int steps = (g.K + Tile::kTileCols - 1) / Tile::kTileCols;
     for (int64_t i = blockIdx.x; i < (int64_t)n * per; i += gridDim.x) {
         int q;
-        const int b = (int)divmod_idx(i, per, q), split = q % splits, r0 = q / splits * NB;
+        const int b = first + (int)divmod_idx(i, per, q), split = q % splits, r0 = q / splits * NB;
         const int slot = block_rows<false, kManyRows>(g, nullptr, b, rows);
-        if (slot < 0) continue;
         Tile tile;
         const int row = threadIdx.x >> 3, piece = threadIdx.x & 7;
 #pragma unroll
@@ -505,7 +498,7 @@ __global__ void __launch_bounds__(kUpThreads, 4) adapter_up_small_kernel(const A
     using Rows = UpRows<1, F32>;
     const int lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
     pdl_wait();
-    const int splits = slices_of(g, g.nblocks[0]);
+    const int splits = g.nblocks[3];
     const int Np = g.N / g.parts, tiles = (Np + 31) / 32;
     const int64_t total = (int64_t)g.nblocks[1] * g.parts * tiles, warps = (int64_t)gridDim.x * (kUpThreads / 32);
     const int64_t warp = (int64_t)blockIdx.x * (kUpThreads / 32) + (threadIdx.x >> 5), end = total * (warp + 1) / warps;
@@ -568,7 +561,7 @@ __global__ void __launch_bounds__(kUpThreads, KS <= 4 ? 3 : 2) adapter_up_kernel
     __shared__ int32_t rows[kManyRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2;
     pdl_wait();
-    const int n = g.nblocks[0], splits = slices_of(g, n);
+    const int n = g.nblocks[0], splits = g.nblocks[3];
     const int Np = g.N / g.parts, chunks = (Np + T::kCols - 1) / T::kCols;
     const uint32_t base = smem_u32(smem);
     // Columns are stored in the order of the instruction's rows.  ldmatrix: matrix j of two 8-column tiles is k half j & 1
@@ -700,10 +693,23 @@ __device__ __forceinline__ int blocks_for(int n) { return (n + kManyRows - 1) / 
 // n / 64 full blocks of four sixteens and the rest's
 __device__ __forceinline__ int sixteens_for(int n) { return (n + 15) / 16; }
 
+// K slices of the first half for so many blocks, by a whole warp: the fewest rounds of CTAs times what a round takes, its
+// stages and about four more to fill the ring and to add the sums up.  (As many slices as
+// make an item for every CTA, whatever is left for a second round: 4096 rows of 8 adapters, K 4096, rank 128, 76 us for 70; 4096 pairs
+// of 64 experts, K 7168, rank 16, 103 for 95.)
+__device__ __forceinline__ int slices_for(const AdapterArgs& g, int blocks) {
+    const int s = (threadIdx.x & 31) + 1, steps = (g.K + thin::Staged<8>::kTileCols - 1) / thin::Staged<8>::kTileCols;
+    if (g.max_splits == 1) return 1;   // more than one only where all of this fits 32 bits
+    const int rounds = (blocks * g.units * s + g.resident - 1) / g.resident;
+    const unsigned cost = s <= g.max_splits ? (unsigned)(rounds * ((steps + s - 1) / s + 4)) : 0xffffffffu, least = __reduce_min_sync(0xffffffffu, cost);
+    return __ffs(__ballot_sync(0xffffffffu, cost == least));
+}
+
 // Counts to first positions; the blocks and sixteens.
 __device__ __forceinline__ void plan_scan(const PlanArgs& a, int32_t* counts) {
     const int per = (a.nslots + kPlanThreads - 1) / kPlanThreads;
     const int s0 = threadIdx.x * per, s1 = min(s0 + per, a.nslots);
+    const int none = blocks_for(counts[0]);   // read by all before anyone's positions overwrite it
     int blocks = 0, sixteens = 0, total_b, total_u;
     for (int s = s0; s < s1; ++s) {
         blocks += blocks_for(counts[s]);
@@ -717,9 +723,14 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& a, int32_t* counts) {
         counts[s] = b * kManyRows;
         lay_out(a.g, s - 1, n, b, u);
     }
-    if (threadIdx.x == 0) {
-        a.g.nblocks[0] = total_b;
-        a.g.nblocks[1] = total_u;
+    if (threadIdx.x < 32) {
+        const int splits = slices_for(a.g, total_b - none);
+        if (threadIdx.x == 0) {
+            a.g.nblocks[0] = total_b;
+            a.g.nblocks[1] = total_u;
+            a.g.nblocks[2] = none;
+            a.g.nblocks[3] = splits;
+        }
     }
 }
 
@@ -750,6 +761,7 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, int32_t v) {
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads) adapter_plan_kernel(const PlanArgs a) {
     extern __shared__ int32_t counts_s[];
     __shared__ int32_t before[kPlanCtas];   // blocks of each CTA's slots, and sixteens in the upper half (below 2^15 both)
+    __shared__ int32_t none;                // blocks of rows without an adapter, in the first CTA
     pdl_trigger();
     const int rank = (int)tc5::cluster_rank();
     int slot[kPlanPerThread], place[kPlanPerThread];
@@ -772,6 +784,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 #pragma unroll
         for (int z = 0; z < kPlanCtas; ++z) n += ld_cluster(counts_of(z, s));
         mine += blocks_for(n) + (sixteens_for(n) << 16);
+        if (s == 0) none = blocks_for(n);
     }
     int first = block_scan(mine, total);
     if (threadIdx.x < kPlanCtas) st_cluster(tc5::at_cta(smem_u32(before + rank), threadIdx.x), total);
@@ -781,9 +794,14 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         if (z < rank) first += before[z];
         all += before[z];
     }
-    if (rank == 0 && threadIdx.x == 0) {
-        a.g.nblocks[0] = all & 0xffff;
-        a.g.nblocks[1] = all >> 16;
+    if (rank == 0 && threadIdx.x >= kPlanThreads - 32) {   // the last slots' warp has the least to lay out
+        const int splits = slices_for(a.g, (all & 0xffff) - none);
+        if (threadIdx.x == kPlanThreads - 1) {
+            a.g.nblocks[0] = all & 0xffff;
+            a.g.nblocks[1] = all >> 16;
+            a.g.nblocks[2] = none;
+            a.g.nblocks[3] = splits;
+        }
     }
     int b = first & 0xffff, u = first >> 16;
     for (int s = s0; s < s1; ++s) {
@@ -840,7 +858,7 @@ Layout layout_of(int64_t P, int64_t slots, int R) {
     };
     if (!few) {
         l.v = take((size_t)l.max_splits * P * R * 4);
-        l.nblocks = take(8);
+        l.nblocks = take(16);
         l.block_slot = take((size_t)l.blocks * 4);
         l.block_count = take((size_t)l.blocks * 4);
         l.rows = take((size_t)l.blocks * kManyRows * 4);
@@ -853,24 +871,25 @@ Layout layout_of(int64_t P, int64_t slots, int R) {
 // Rows of A that an item of the first half takes.
 int down_cols(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
-template <int NT>
-cudaError_t launch_down_as(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
-    auto* kern = adapter_down_kernel<NT>;
-    const size_t smem = thin::Staged<NT>::kBytes;
-    int ctas = 0;
-    cudaError_t e = kernel_ctas_per_sm(reinterpret_cast<const void*>(kern), kThreads, smem, smem, &ctas);
-    if (e != cudaSuccess) return e;
-    const int64_t items = blocks * g.units * g.max_splits, most = (int64_t)device_info().sm_count * ctas;
-    return launch_pdl(pdl_for(g.P), kern, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, st, g);
+struct DownKernel {
+    void (*kern)(AdapterArgs);
+    size_t smem;
+    int ctas;   // to an SM
+};
+
+cudaError_t down_kernel(int R, DownKernel& k) {
+    switch (down_cols(R)) {
+        case 8: k = {adapter_down_kernel<1>, thin::Staged<1>::kBytes, 0}; break;
+        case 16: k = {adapter_down_kernel<2>, thin::Staged<2>::kBytes, 0}; break;
+        case 32: k = {adapter_down_kernel<4>, thin::Staged<4>::kBytes, 0}; break;
+        default: k = {adapter_down_kernel<8>, thin::Staged<8>::kBytes, 0}; break;
+    }
+    return kernel_ctas_per_sm(reinterpret_cast<const void*>(k.kern), kThreads, k.smem, k.smem, &k.ctas);
 }
 
-cudaError_t launch_down(const AdapterArgs& g, int64_t blocks, cudaStream_t st) {
-    switch (down_cols(g.R)) {
-        case 8: return launch_down_as<1>(g, blocks, st);
-        case 16: return launch_down_as<2>(g, blocks, st);
-        case 32: return launch_down_as<4>(g, blocks, st);
-        default: return launch_down_as<8>(g, blocks, st);
-    }
+cudaError_t launch_down(const AdapterArgs& g, const DownKernel& k, int64_t blocks, cudaStream_t st) {
+    const int64_t items = blocks * g.units * g.max_splits;
+    return launch_pdl(pdl_for(g.P), k.kern, dim3((unsigned)(items < g.resident ? items : g.resident)), dim3(kThreads), k.smem, st, g);
 }
 
 template <int CTAS, int NT, bool F32>
@@ -1008,7 +1027,7 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     AdapterArgs g{static_cast<const __nv_bfloat16*>(x), x_stride, a_row_divisor, adapter_ids, topk_ids, (int)P, topk, adapters, E,
                   static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, rank, parts, rank * parts, N, K,
-                  base, y, base_stride, y_stride, base != y, units, l.max_splits < most ? l.max_splits : most, 2 * di.sm_count,
+                  base, y, base_stride, y_stride, base != y, units, l.max_splits < most ? l.max_splits : most, 0,
                   reinterpret_cast<float*>(ws + l.v),
                   reinterpret_cast<int32_t*>(ws + l.nblocks), reinterpret_cast<int32_t*>(ws + l.block_slot),
                   reinterpret_cast<int32_t*>(ws + l.block_count), reinterpret_cast<int32_t*>(ws + l.rows),
@@ -1018,8 +1037,11 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     if (few) {
         e = f32 ? launch_few<true>(g, l.blocks, st) : launch_few<false>(g, l.blocks, st);
     } else {
-        e = launch_plan(g, slots, reinterpret_cast<int32_t*>(ws + l.counts), st);
-        if (e == cudaSuccess) e = launch_down(g, l.blocks, st);
+        DownKernel down;
+        e = down_kernel(g.R, down);
+        g.resident = di.sm_count * down.ctas;
+        if (e == cudaSuccess) e = launch_plan(g, slots, reinterpret_cast<int32_t*>(ws + l.counts), st);
+        if (e == cudaSuccess) e = launch_down(g, down, l.blocks, st);
         if (e == cudaSuccess) e = f32 ? launch_up<true>(g, st) : launch_up<false>(g, st);
     }
     if (e != cudaSuccess || cudaGetLastError() != cudaSuccess) return CHORD_ERR_CUDA;

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) adapter_down_kernel
         const float* sums = reinterpret_cast<const float*>(smem);
         for (int u = threadIdx.x; u < kManyRows * NB; u += kThreads) {
             const int p = rows[u / NB], r = r0 + u % NB;
-            if (p >= 0 && r < g.R) g.v[((int64_t)split * g.P + p) * g.R + r] = sums[u] + sums[kManyRows * NB + u];
+            if (p >= 0 && r < g.R) g.v[((int64_t)split * g.P + p) * g.R + r] = Tile::joined(sums, u);
         }
     }
 }

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(thin::kThreads, 2) logits_staged_kernel(const 
     tile.run(smem, (int)(rank * steps / splits), (int)((rank + 1) * steps / splits), a.H, a.parts, (int64_t)a.E * a.H);
     const float* sums = reinterpret_cast<const float*>(smem);
     join_slices<kLogitTile>(
-        splits, reinterpret_cast<float*>(smem + LogitTile::kBytes), [&](int i) { return sums[i] + sums[kLogitTile + i]; },
+        splits, reinterpret_cast<float*>(smem + LogitTile::kBytes), [&](int i) { return LogitTile::joined(sums, i); },
         [&](int i, float v) {
             const int64_t t = t0 + i / LogitTile::kCols;
             const int e = e0 + i % LogitTile::kCols;

@@ -140,23 +140,25 @@ __device__ __forceinline__ float joined(const float* red, int n, int i) {
 
 // ---- the same for many rows, staged in shared memory ----------------------------------------
 // 64 rows of x times NT x 8 weight rows: every thread copies 16-byte pieces of a stage of 128 columns, two tiles of 64,
-// with cp.async, kStages - 1 stages are on their way.  Warp w takes rows 16 (w mod 4) of tile w / 4; the tiles' sums
-// are joined at the end.  A tile's rows are 128 bytes, piece p of row r at p xor (r mod 8).  (Stages of 64
+// with cp.async, kStages - 1 stages are on their way.  A warp takes 32 rows, 32 weight rows (or all) and a share of a
+// stage's columns, a half or a quarter, so that a fragment read from shared memory serves two or four instructions; the
+// shares' sums are joined at the end.  A tile's rows are 128 bytes, piece p of row r at p xor (r mod 8).  (Stages of 64
 // columns meet twice as often: 48 tokens of 384 experts in FP32 14.6 us for 13.9.)
 template <int NT>
 struct Staged {
     static constexpr int kRows = 64, kCols = NT * 8, kTileCols = 128, kHalf = (kRows + kCols) * 128;
     static constexpr int kStageBytes = 2 * kHalf, kStages = NT == 4 ? 4 : 3;
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes;          // the ring
-    static constexpr size_t kSums = (size_t)2 * kRows * kCols * 4;          // over it, afterwards: [2][kRows][kCols]
+    static constexpr int kTiles = NT < 4 ? NT : 4, kShares = NT == 8 ? 2 : 4, kSteps = 8 / kShares;   // of a warp: weight tiles; a stage's k steps
+    static constexpr size_t kSums = (size_t)kShares * kRows * kCols * 4;    // over it, afterwards: [kShares][kRows][kCols]
     static constexpr size_t kBytes = kSmem > kSums ? kSmem : kSums;
-    static constexpr int kChainStages = 4;                                  // four instructions a stage
+    static constexpr int kChainStages = 16 / kSteps;                        // chains of sixteen instructions
 
     // This thread's rows of x (t / 8 and t / 8 + 32) and weight rows, at piece t mod 8; null: not copied,
     // whatever is multiplied in its place is not looked at.
     const __nv_bfloat16* x[2];
     const __nv_bfloat16* w[2];
-    float acc[NT][4], sum[NT][4];
+    float acc[2][kTiles][4], sum[2][kTiles][4];
 
     __device__ __forceinline__ void copy(uint32_t st, int col, int64_t w_offset, int K) const {
         const int t = threadIdx.x, row = t >> 3, piece = t & 7;
@@ -177,43 +179,63 @@ struct Staged {
     __device__ __forceinline__ static void fill(uint32_t dst, const __nv_bfloat16* src, bool in) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
     }
+    // This warp's first row, weight row and k step of a stage.
+    __device__ __forceinline__ static int first_row() { return (threadIdx.x >> 5 & 1) * 32; }
+    __device__ __forceinline__ static int first_col() { return NT == 8 ? (threadIdx.x >> 6 & 1) * 32 : 0; }
+    __device__ __forceinline__ static int share() { return NT == 8 ? threadIdx.x >> 7 : threadIdx.x >> 6; }
     __device__ __forceinline__ void multiply(uint32_t st) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        const int ar = (warp & 3) * 16 + (lane & 15), br = (lane >> 4) * 8 + (lane & 7);
-        st += (uint32_t)((warp >> 2) * kHalf);
+        const int lane = threadIdx.x & 31, ar = first_row() + (lane & 15), br = first_col() + (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            uint32_t a[4];
-            ldsm4(a, st + (uint32_t)ar * 128u + (uint32_t)(((kk * 2 + (lane >> 4)) ^ (ar & 7)) << 4));
+        for (int s = 0; s < kSteps; ++s) {
+            const int step = share() * kSteps + s, kk = step & 3;
+            const uint32_t from = st + (uint32_t)((step >> 2) * kHalf);
+            uint32_t a[2][4];
 #pragma unroll
-            for (int t = 0; t < NT; t += 2) {
+            for (int m = 0; m < 2; ++m)
+                ldsm4(a[m], from + (uint32_t)(ar + m * 16) * 128u + (uint32_t)(((kk * 2 + (lane >> 4)) ^ (ar & 7)) << 4));
+#pragma unroll
+            for (int t = 0; t < kTiles; t += 2) {
                 uint32_t b[4];
                 // with one tile of weights the second half of the lanes reads its rows again
                 const int r = t * 8 + (NT > 1 ? br : (lane & 7));
-                ldsm4(b, st + kRows * 128u + (uint32_t)r * 128u + (uint32_t)(((kk * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
-                mma(acc[t], a[0], a[1], a[2], a[3], b[0], b[1]);
-                if (t + 1 < NT) mma(acc[t + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+                ldsm4(b, from + kRows * 128u + (uint32_t)r * 128u + (uint32_t)(((kk * 2 + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    mma(acc[m][t], a[m][0], a[m][1], a[m][2], a[m][3], b[0], b[1]);
+                    if (t + 1 < kTiles) mma(acc[m][t + 1], a[m][0], a[m][1], a[m][2], a[m][3], b[2], b[3]);
+                }
             }
         }
     }
     __device__ __forceinline__ void end_chain() {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                sum[t][u] += acc[t][u];
-                acc[t][u] = 0.0f;
-            }
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    sum[m][t][u] += acc[m][t][u];
+                    acc[m][t][u] = 0.0f;
+                }
+    }
+    // Sum i of the tile, of its shares in order; sums: what run left.
+    __device__ __forceinline__ static float joined(const float* sums, int i) {
+        float v = sums[i];
+#pragma unroll
+        for (int z = 1; z < kShares; ++z) v += sums[z * kRows * kCols + i];
+        return v;
     }
     // Stages s0 .. s1 - 1 of `parts` weight matrices one behind the other, part_stride elements apart, the last
-    // one first.  Every thread of the CTA; the sums are in smem ([2][kRows][kCols] floats) when it returns.
+    // one first.  Every thread of the CTA; the sums are in smem ([kShares][kRows][kCols] floats) when it returns.
     __device__ __forceinline__ void run(uint8_t* smem, int s0, int s1, int K, int parts, int64_t part_stride) {
         const uint32_t base = smem_u32(smem);
         const int per = (K + kTileCols - 1) / kTileCols;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) acc[t][u] = sum[t][u] = 0.0f;
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) acc[m][t][u] = sum[m][t][u] = 0.0f;
         int next = s0, part = s0 / per, k = s0 - part * per, slot_in = 0, slot_out = 0, chain = 0;
         auto issue = [&]() {
             if (next < s1) {
@@ -240,13 +262,15 @@ struct Staged {
         end_chain();
         cp_async_wait<0>();
         __syncthreads();
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        float* to = reinterpret_cast<float*>(smem) + ((warp >> 2) * kRows + (warp & 3) * 16 + (lane >> 2)) * kCols + 2 * (lane & 3);
+        const int lane = threadIdx.x & 31;
+        float* to = reinterpret_cast<float*>(smem) + (share() * kRows + first_row() + (lane >> 2)) * kCols + first_col() + 2 * (lane & 3);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<float2*>(to + h * 8 * kCols + t * 8) = make_float2(sum[t][2 * h], sum[t][2 * h + 1]);
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<float2*>(to + (m * 16 + h * 8) * kCols + t * 8) = make_float2(sum[m][t][2 * h], sum[m][t][2 * h + 1]);
         __syncthreads();
     }
 };

@@ -57,7 +57,8 @@ struct AdapterArgs {
     int64_t base_stride, y_stride;
     int copy;                     // rows without an adapter are copied from base
     int units;                    // items of a block and K slice
-    int max_splits, resident;     // K slices at most; CTAs of the first half that run at once
+    int cluster;                  // CTAs that share an item of the first half, each a part of its K slice
+    int max_splits, resident;     // K slices at most; clusters of the first half that run at once
     float* v;                     // [slices, P, R]
     // the plan, for more than kFewPairs pairs
     int32_t* nblocks;             // [4]: blocks, sixteens, blocks without an adapter (the first ones), K slices
@@ -147,13 +148,14 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) adapter_down_kernel
     using Tile = thin::Staged<NT>;
     constexpr int NB = Tile::kCols;
     static_assert(Tile::kRows == kManyRows, "a block of the plan is a tile");
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem[];   // the tile's ring, then the cluster's shares
     __shared__ int32_t rows[kManyRows];
     pdl_trigger();
     pdl_wait();
+    const int rank = g.cluster > 1 ? (int)tc5::cluster_rank() : 0;
     const int first = g.nblocks[2], n = g.nblocks[0] - first, splits = g.nblocks[3], chunks = (g.R + NB - 1) / NB, per = chunks * splits;
     const int steps = (g.K + Tile::kTileCols - 1) / Tile::kTileCols;
-    for (int64_t i = blockIdx.x; i < (int64_t)n * per; i += gridDim.x) {
+    for (int64_t i = blockIdx.x / g.cluster; i < (int64_t)n * per; i += gridDim.x / g.cluster) {
         int q;
         const int b = first + (int)divmod_idx(i, per, q), split = q % splits, r0 = q / splits * NB;
         const int slot = block_rows<false, kManyRows>(g, nullptr, b, rows);
@@ -165,12 +167,15 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 3 : 2) adapter_down_kernel
             tile.x[h] = p < 0 ? nullptr : g.x + (int64_t)(g.div == 1 ? p : p / g.div) * g.x_stride + piece * 8;
             tile.w[h] = r < NB && r0 + r < g.R ? g.A + ((int64_t)slot * g.R + r0 + r) * g.K + piece * 8 : nullptr;
         }
-        tile.run(smem, (int)((int64_t)split * steps / splits), (int)((int64_t)(split + 1) * steps / splits), g.K, 1, 0);
+        const int cut = splits * g.cluster, at = split * g.cluster + rank;
+        tile.run(smem, (int)((int64_t)at * steps / cut), (int)((int64_t)(at + 1) * steps / cut), g.K, 1, 0);
         const float* sums = reinterpret_cast<const float*>(smem);
-        for (int u = threadIdx.x; u < kManyRows * NB; u += kThreads) {
-            const int p = rows[u / NB], r = r0 + u % NB;
-            if (p >= 0 && r < g.R) g.v[((int64_t)split * g.P + p) * g.R + r] = Tile::joined(sums, u);
-        }
+        thin::join_slices<kManyRows * NB>(
+            g.cluster, reinterpret_cast<float*>(smem + Tile::kBytes), [&](int u) { return Tile::joined(sums, u); },
+            [&](int u, float v) {
+                const int p = rows[u / NB], r = r0 + u % NB;
+                if (p >= 0 && r < g.R) g.v[((int64_t)split * g.P + p) * g.R + r] = v;
+            });
     }
 }
 
@@ -693,15 +698,15 @@ __device__ __forceinline__ int blocks_for(int n) { return (n + kManyRows - 1) / 
 // n / 64 full blocks of four sixteens and the rest's
 __device__ __forceinline__ int sixteens_for(int n) { return (n + 15) / 16; }
 
-// K slices of the first half for so many blocks, by a whole warp: the fewest rounds of CTAs times what a round takes, its
-// stages and about four more to fill the ring and to add the sums up.  (As many slices as
+// K slices of the first half for so many blocks, by a whole warp: the fewest rounds of clusters times what a round takes, its
+// stages and about five more to fill the ring and to add the sums up, and one for a slice, which the second half reads.  (As many slices as
 // make an item for every CTA, whatever is left for a second round: 4096 rows of 8 adapters, K 4096, rank 128, 76 us for 70; 4096 pairs
 // of 64 experts, K 7168, rank 16, 103 for 95.)
 __device__ __forceinline__ int slices_for(const AdapterArgs& g, int blocks) {
     const int s = (threadIdx.x & 31) + 1, steps = (g.K + thin::Staged<8>::kTileCols - 1) / thin::Staged<8>::kTileCols;
     if (g.max_splits == 1) return 1;   // more than one only where all of this fits 32 bits
-    const int rounds = (blocks * g.units * s + g.resident - 1) / g.resident;
-    const unsigned cost = s <= g.max_splits ? (unsigned)(rounds * ((steps + s - 1) / s + 4)) : 0xffffffffu, least = __reduce_min_sync(0xffffffffu, cost);
+    const int rounds = (blocks * g.units * s + g.resident - 1) / g.resident, cut = s * g.cluster;
+    const unsigned cost = s <= g.max_splits ? (unsigned)(rounds * ((steps + cut - 1) / cut + 5) + s) : 0xffffffffu, least = __reduce_min_sync(0xffffffffu, cost);
     return __ffs(__ballot_sync(0xffffffffu, cost == least));
 }
 
@@ -877,19 +882,40 @@ struct DownKernel {
     int ctas;   // to an SM
 };
 
+template <int NT>
+DownKernel down_kernel_as() {
+    return {adapter_down_kernel<NT>, thin::Staged<NT>::kBytes + kManyRows * NT * 8 * 4, 0};
+}
+
 cudaError_t down_kernel(int R, DownKernel& k) {
-    switch (down_cols(R)) {
-        case 8: k = {adapter_down_kernel<1>, thin::Staged<1>::kBytes, 0}; break;
-        case 16: k = {adapter_down_kernel<2>, thin::Staged<2>::kBytes, 0}; break;
-        case 32: k = {adapter_down_kernel<4>, thin::Staged<4>::kBytes, 0}; break;
-        default: k = {adapter_down_kernel<8>, thin::Staged<8>::kBytes, 0}; break;
-    }
+    const int cols = down_cols(R);
+    k = cols == 8 ? down_kernel_as<1>() : cols == 16 ? down_kernel_as<2>() : cols == 32 ? down_kernel_as<4>() : down_kernel_as<8>();
     return kernel_ctas_per_sm(reinterpret_cast<const void*>(k.kern), kThreads, k.smem, k.smem, &k.ctas);
 }
 
 cudaError_t launch_down(const AdapterArgs& g, const DownKernel& k, int64_t blocks, cudaStream_t st) {
     const int64_t items = blocks * g.units * g.max_splits;
-    return launch_pdl(pdl_for(g.P), k.kern, dim3((unsigned)(items < g.resident ? items : g.resident)), dim3(kThreads), k.smem, st, g);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((items < g.resident ? items : g.resident) * g.cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = k.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (g.cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)g.cluster;
+        attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (pdl_for(g.P)) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, k.kern, g);
 }
 
 template <int CTAS, int NT, bool F32>
@@ -1027,7 +1053,7 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     AdapterArgs g{static_cast<const __nv_bfloat16*>(x), x_stride, a_row_divisor, adapter_ids, topk_ids, (int)P, topk, adapters, E,
                   static_cast<const __nv_bfloat16*>(A), static_cast<const __nv_bfloat16*>(B), scale, rank, parts, rank * parts, N, K,
-                  base, y, base_stride, y_stride, base != y, units, l.max_splits < most ? l.max_splits : most, 0,
+                  base, y, base_stride, y_stride, base != y, units, 1, 1, 0,
                   reinterpret_cast<float*>(ws + l.v),
                   reinterpret_cast<int32_t*>(ws + l.nblocks), reinterpret_cast<int32_t*>(ws + l.block_slot),
                   reinterpret_cast<int32_t*>(ws + l.block_count), reinterpret_cast<int32_t*>(ws + l.rows),
@@ -1039,7 +1065,14 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
     } else {
         DownKernel down;
         e = down_kernel(g.R, down);
-        g.resident = di.sm_count * down.ctas;
+        // Few blocks: clusters join their sums before the second half reads them, which it does once for each of its CTAs.  As large
+        // as all blocks find a place at once, by the most there can be (without and with clusters: 512 rows of rank 16 18.3 and
+        // 15.4 us, 2048 rows of rank 64 41.0, 35.7; 4096 pairs of 512 slots 95, 128).
+        const int splits = l.max_splits < most ? l.max_splits : most, resident = di.sm_count * down.ctas;
+        g.cluster = 1;
+        while (g.cluster < 4 && 2 * g.cluster <= splits && l.blocks * units * 2 * g.cluster <= resident) g.cluster *= 2;
+        g.max_splits = splits / g.cluster;
+        g.resident = resident / g.cluster;
         if (e == cudaSuccess) e = launch_plan(g, slots, reinterpret_cast<int32_t*>(ws + l.counts), st);
         if (e == cudaSuccess) e = launch_down(g, down, l.blocks, st);
         if (e == cudaSuccess) e = f32 ? launch_up<true>(g, st) : launch_up<false>(g, st);

@@ -25,31 +25,7 @@ struct LogitArgs {
 
 // ---- few tokens: thin products (chord_thin.cuh) -------------------------------------------
 // A CTA takes a tile of tokens and experts and a slice of K (of all parts, one behind the other, the smallest
-// numbers first); the slices of a tile are a cluster.  Each CTA pushes every one the share of
-// its sums that that one adds up, in rank order.
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-// Sum i of kCount, put(i, sum) for each; `mine(i)` is this CTA's, `shares` kCount floats that nobody uses.
-template <int kCount, typename Mine, typename Put>
-__device__ __forceinline__ void join_slices(int splits, float* shares, Mine mine, Put put) {
-    if (splits == 1) {
-        for (int i = threadIdx.x; i < kCount; i += thin::kThreads) put(i, mine(i));
-        return;
-    }
-    const int rank = (int)tc5::cluster_rank(), share = kCount / splits;   // a power of two, as splits is
-    tc5::cluster_sync();                                                  // every CTA of the cluster runs
-    for (int i = threadIdx.x; i < kCount; i += thin::kThreads)
-        st_cluster(tc5::at_cta(smem_u32(shares + rank * share + i % share), (uint32_t)(i / share)), mine(i));
-    tc5::cluster_sync();
-    for (int i = threadIdx.x; i < share; i += thin::kThreads) {
-        float v = shares[i];
-        for (int s = 1; s < splits; ++s) v += shares[s * share + i];
-        put(rank * share + i, v);
-    }
-}
-
+// numbers first); the slices of a tile are a cluster.
 // Up to 16 tokens, NT x 8 experts (16 tokens of 7168 columns, 384 experts: 4.2 us in a graph, staged as below 6.9).
 template <int NT>
 __global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const LogitArgs a, int splits) {
@@ -76,7 +52,7 @@ __global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const Logit
         more = true;
     }
     __syncthreads();
-    join_slices<kTile>(
+    thin::join_slices<kTile>(
         splits, red + thin::kWarps * kTile, [&](int i) { return thin::joined(red, kTile, i); },
         [&](int i, float v) {
             const int t = i / Warp::kCols, e = e0 + i % Warp::kCols;
@@ -107,7 +83,7 @@ __global__ void __launch_bounds__(thin::kThreads, 2) logits_staged_kernel(const 
     const int64_t steps = (int64_t)((a.H + LogitTile::kTileCols - 1) / LogitTile::kTileCols) * a.parts;
     tile.run(smem, (int)(rank * steps / splits), (int)((rank + 1) * steps / splits), a.H, a.parts, (int64_t)a.E * a.H);
     const float* sums = reinterpret_cast<const float*>(smem);
-    join_slices<kLogitTile>(
+    thin::join_slices<kLogitTile>(
         splits, reinterpret_cast<float*>(smem + LogitTile::kBytes), [&](int i) { return LogitTile::joined(sums, i); },
         [&](int i, float v) {
             const int64_t t = t0 + i / LogitTile::kCols;

@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "chord_common.cuh"
+#include "chord_tcgen05.cuh"
 
 namespace chord {
 namespace thin {
@@ -136,6 +137,32 @@ __device__ __forceinline__ float joined(const float* red, int n, int i) {
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) v += red[w * n + i];
     return v;
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// Sum i of kCount over the CTAs of a cluster (splits, a power of two), put(i, sum) for each by one of them: every CTA
+// pushes each one the share of its sums that that one adds up, in rank order.  `mine(i)` is this CTA's sum, `shares` kCount
+// floats that no earlier call's reads are left on.
+template <int kCount, typename Mine, typename Put>
+__device__ __forceinline__ void join_slices(int splits, float* shares, Mine mine, Put put) {
+    static_assert((kCount & (kCount - 1)) == 0, "shares are powers of two");
+    if (splits == 1) {
+        for (int i = threadIdx.x; i < kCount; i += kThreads) put(i, mine(i));
+        return;
+    }
+    const int rank = (int)tc5::cluster_rank(), share = kCount / splits, bits = __ffs(share) - 1;   // a power of two, as splits is
+    tc5::cluster_sync();                                                                           // every CTA of the cluster runs
+    for (int i = threadIdx.x; i < kCount; i += kThreads)
+        st_cluster(tc5::at_cta(smem_u32(shares + rank * share + (i & (share - 1))), (uint32_t)(i >> bits)), mine(i));
+    tc5::cluster_sync();
+    for (int i = threadIdx.x; i < share; i += kThreads) {
+        float v = shares[i];
+        for (int s = 1; s < splits; ++s) v += shares[s * share + i];
+        put(rank * share + i, v);
+    }
 }
 
 // ---- the same for many rows, staged in shared memory ----------------------------------------

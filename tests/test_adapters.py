@@ -171,6 +171,23 @@ def test_many_pairs(shape, out):
     check(make(T, topk, S, E, rank, parts, K, N, div, out, seed=8 + T, dense=dense))
 
 
+#        the same: long K, so that clusters of four, of two and none share an item, with one slice and with several
+LONG = [(300, 1, 1, 1, 16, 1, 7176, 64, 1, True), (700, 1, 4, 1, 64, 1, 4104, 40, 1, True), (4096, 1, 8, 1, 128, 1, 1288, 72, 1, True),
+        (3000, 1, 8, 1, 64, 1, 1032, 48, 1, True), (1024, 8, 4, 48, 16, 1, 1000, 64, 1, False), (512, 8, 2, 200, 8, 2, 776, 64, 8, False),
+        (300, 1, 300, 1, 32, 1, 2056, 48, 1, True), (600, 1, 2, 1, 24, 2, 264, 48, 1, True), (257, 1, 2, 1, 96, 4, 3080, 64, 1, True)]
+
+
+@gpu
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("shape", LONG)
+def test_many_pairs_of_long_rows(shape, out):
+    need_gpu()
+    T, topk, S, E, rank, parts, K, N, div, dense = shape
+    check(make(T, topk, S, E, rank, parts, K, N, div, out, seed=9 + T, dense=dense, integer=True), exact=True)
+    check(make(T, topk, S, E, rank, parts, K, N, div, out, seed=10 + T, dense=dense))
+    check(make(T, topk, S, E, rank, parts, K, N, div, out, seed=11 + T, dense=dense, none=0.9))
+
+
 @gpu
 def test_every_pair_elsewhere():
     need_gpu()

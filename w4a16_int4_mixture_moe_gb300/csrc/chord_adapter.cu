@@ -7,14 +7,15 @@
 // More pairs: three launches.
 //   plan   blocks of 64 rows by a counting sort of the pairs by slot: 5.5 to 8.5 us for 8192 pairs.
 //   down   v, a block's rows times the slot's A, staged products (chord_thin.cuh); an item is (block, up to 64 rows of A,
-//          K slice).  K slices are partial sums in the workspace, as many as fill the GPU.  Bound by the copies to shared
-//          memory, x's and A's (3584 pairs of 7168 columns, rank 64: 21 us, 2.4 TB/s of x; 7168 pairs of 2048, rank 16: 12).
+//          K slice).  A cluster takes an item while there are few blocks; beyond, K slices are partial sums in the
+//          workspace, as many as fill the GPU.  Bound by the copies to shared memory, x's and A's (3584 pairs of 7168
+//          columns, rank 64: 22 us, 2.3 TB/s of x; 7168 pairs of 2048, rank 16: 12).
 //   up     y = base + scale B v.  The slices of v are added in order, scaled and split into three bf16 parts of eight bits
 //          each, so the tensor cores multiply all of an FP32 v.  A tile's columns are dealt so that a lane ends with whole
 //          16-byte pieces of its rows of base and y.  Ranks up to 16 are bound by base's and y's bytes (8192 pairs of 7168
 //          FP32 columns, rank 16: 100 us, 4.7 TB/s; a copy in the same pattern 84), larger ones by latency between
 //          instructions at 12 warps an SM, which is what v's fragments leave room for (4096 rows of 4096 columns,
-//          rank 64: 29 us, tensor pipe 41 % busy).
+//          rank 64: 26 us, tensor pipe 48 % busy).
 // Warp-level instructions: a block's rows are gathered, which TMA does at 46 ns for four rows, and a rank of 8 to 128 leaves
 // tcgen05 nothing to gain from.
 #include <cuda_bf16.h>

@@ -684,7 +684,8 @@ chord_status chord_moe_route(const void *logits, int logits_dtype, int64_t row_s
 
 /* ---------------------------------------------------------------- adapters */
 
-/* Scratch bytes of chord_adapter_add; 0 on bad arguments. */
+/* Scratch bytes of chord_adapter_add; 0 on bad arguments.  They never fall as an argument grows: the
+ * workspace of the largest batch serves every smaller one. */
 size_t chord_adapter_workspace_bytes(int64_t T, int topk, int adapters, int E, int rank, int parts);
 
 /* Low-rank adapters of many requests beside a projection that they share (the frozen

@@ -152,3 +152,16 @@ def test_adapter_sizes(lib):
     a = list(args)
     a[at["T"]] = 0
     assert call(*a) == 0
+
+
+def test_workspace_never_shrinks_with_more_tokens():
+    """Scratch for the largest batch is enough for every smaller one."""
+    f = chord.chord_adapter_workspace_bytes
+    for topk, S, E, rank, parts in ((8, 4, 48, 16, 2), (1, 8, 1, 64, 1), (3, 200, 1, 8, 1), (2, 1, 300, 128, 4)):
+        # every number of tokens up to 3000, and both sides of every step of 16384 / pairs
+        counts = {*range(3000), *(p // topk + d for k in range(1, 17) for p in (16384 // k, 32768 * k) for d in (-1, 0, 1, 2))}
+        prev = 0
+        for T in sorted(counts):
+            now = f(T, topk, S, E, rank, parts)
+            assert now >= prev, (T, topk)
+            prev = now

@@ -863,7 +863,10 @@ Layout layout_of(int64_t P, int64_t slots, int R) {
         return at;
     };
     if (!few) {
-        l.v = take((size_t)l.max_splits * P * R * 4);
+        // Room for what a smaller call may take too, whose slices are more (16384 / P of them, at most 16): the largest
+        // batch's workspace is enough for every other.
+        const int64_t rows = kMaxSplit * P < kSplitRows ? kMaxSplit * P : kSplitRows;
+        l.v = take((size_t)(rows > P ? rows : P) * R * 4);
         l.nblocks = take(16);
         l.block_slot = take((size_t)l.blocks * 4);
         l.block_count = take((size_t)l.blocks * 4);

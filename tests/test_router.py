@@ -446,3 +446,40 @@ def test_router_to_align():
     at = torch.nonzero(order < T * topk).reshape(-1)
     assert torch.equal(flat[pairs.long()], blocks[torch.div(at, bm, rounding_mode="floor")])
     assert math.isclose(float(w.sum(1).mean()), 2.5, rel_tol=1e-5)
+
+
+@gpu
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_groups_of_biases_whose_sum_leaves_fp32(score, renorm):
+    """Experts switched off by the lowest (or raised by the largest) number: the sum of a group's two best is beyond FP32 and
+    still a number, above a group without an available expert and in order with the other groups' sums."""
+    need_gpu()
+    g = gen(31)
+    low = -3.4028234663852886e38
+    for size, groups in ((8, 4), (16, 8), (2, 32), (5, 3)):
+        E = size * groups
+        l = torch.randn((6, E), generator=g)
+        l[3] = 1.0
+        l[4, ::2] = NINF
+        for tg in (1, 2):
+            topk = min(4, tg * size)
+            for kind in range(5):
+                b = torch.full((groups, size), low)
+                if kind == 0:                       # only the second group has anybody
+                    b[:] = NINF
+                    b[1] = low
+                elif kind == 1:                     # sums of -2, -1.5 (the last group) and -1.75 of the largest number
+                    b[-1, ::2] = low * 0.5
+                    b[groups // 2, 1::2] = low * 0.75
+                elif kind == 2:                     # one expert of the first group against two of the last
+                    b[0, 1:] = NINF
+                elif kind == 3:                     # the same above zero
+                    b[:] = -low
+                    b[0] = -low * 0.75
+                    b[1] = NINF
+                else:                               # the first two groups have nobody, the others one expert or several
+                    b[:2] = NINF
+                    b[2, :-1] = NINF if groups > 3 else low
+                check(l, topk, b.reshape(-1), score=score, groups=groups, topk_groups=tg, group_best=2, renormalize=renorm)
+                check(l.to(torch.bfloat16), topk, b.reshape(-1), score=score, groups=groups, topk_groups=tg, group_best=1, renormalize=renorm)

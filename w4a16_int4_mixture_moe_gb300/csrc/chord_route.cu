@@ -381,7 +381,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL > 16 ? 4 : 8) route_kern
             b1 = fmaxf(b1, o1);
         }
         const bool pair = a.best == 2 && b2 > -INFINITY;
-        float gv = __shfl_sync(kAll, pair ? b1 + b2 : b1, (lane * lpg) & 31);
+        // A sum below FP32's range is still a number, not a group without experts; which of such sums is larger is
+        // found in binary64 below, since size_of is infinite then.
+        float gv = __shfl_sync(kAll, pair ? fmaxf(b1 + b2, -FLT_MAX) : b1, (lane * lpg) & 31);
         const float size_of = warp_max(b1 > -INFINITY ? (pair ? fabsf(b1) + fabsf(b2) : fabsf(b1)) : 0.0f);
         if (lane >= a.groups) gv = -INFINITY;
         int rank = 0;

@@ -629,9 +629,9 @@ chord_status chord_moe_layer_few(const void *x, const int32_t *topk_ids, const f
 /* ------------------------------------------------------------------ router */
 
 /* Three bf16 numbers that add up to each of the n FP32 numbers of W: parts is bf16
- * [3, n], eight significant bits each, cut off towards zero (exact for magnitudes
- * from 2^-110; an infinity or NaN is in the first part alone).  For a router kept in
- * FP32, split once at load time. */
+ * [3, n], at most eight significant bits each (exact for magnitudes from 2^-110).  All three have
+ * the number's sign, and of a number from 2^-110 on none is 0; an infinity or NaN is in the first part
+ * alone.  For a router kept in FP32, split once at load time. */
 chord_status chord_router_split_weights(const float *W, int64_t n, void *parts, void *stream);
 
 /* Router logits:
@@ -639,7 +639,9 @@ chord_status chord_router_split_weights(const float *W, int64_t n, void *parts, 
  *   x      device bf16 [T, H], x_stride elements between rows (a multiple of 8)
  *   W      device bf16 [parts, E, H] dense: parts = 1 for a bf16 router, 3 for the
  *          parts of an FP32 one (chord_router_split_weights), whose sum is the weight
- * E <= 1024, H % 8 == 0.  Products are exact; the result does not depend on timing. */
+ * E <= 1024, H % 8 == 0.  Products are exact; the result does not depend on timing.  An infinite x gives
+ * the infinity or NaN that the sum has, with parts = 3 too; there an infinite W times an infinite x is a
+ * NaN, and so is an infinite x times a W below 2^-110. */
 chord_status chord_router_logits(const void *x, int64_t x_stride, int T, const void *W, int parts, int E, int H,
                                  float *logits, const chord_opts *opts, void *stream);
 

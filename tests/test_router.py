@@ -483,3 +483,54 @@ def test_groups_of_biases_whose_sum_leaves_fp32(score, renorm):
                     b[2, :-1] = NINF if groups > 3 else low
                 check(l, topk, b.reshape(-1), score=score, groups=groups, topk_groups=tg, group_best=2, renormalize=renorm)
                 check(l.to(torch.bfloat16), topk, b.reshape(-1), score=score, groups=groups, topk_groups=tg, group_best=1, renormalize=renorm)
+
+
+def split(W):
+    parts = torch.empty((3, *W.shape), dtype=torch.bfloat16, device=DEV)
+    chord.chord_router_split_weights(W.to(DEV), parts)
+    return parts
+
+
+@gpu
+def test_split_weights_of_few_bits():
+    """Every number from 2^-110 on ends in three parts that are not 0, of its sign, whose sum it is: however few bits it has."""
+    need_gpu()
+    g = gen(14)
+    n = 4000
+    for bits in (1, 2, 7, 8, 9, 15, 16, 17, 24):
+        m = torch.randint(2 ** (bits - 1), 2 ** bits, (n,), generator=g).double()
+        e = torch.randint(-110, 127, (n,), generator=g).double()
+        e[:4] = torch.tensor([-110.0, -110.0, 127.0, 0.0], dtype=torch.float64)
+        w = (m * torch.exp2(e - (bits - 1)) * (torch.randint(0, 2, (n,), generator=g) * 2 - 1)).float()
+        assert w.abs().min() >= 2.0 ** -110 and w.abs().max() < float("inf")
+        p = split(w).cpu().double()
+        assert torch.equal(p.sum(0), w.double())
+        assert (p * w.double().sign() > 0).all()
+    assert (split(torch.tensor([0.0, -0.0])) == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("T,E", [(1, 40), (3, 40), (70, 40), (3000, 40), (1300, 161)])
+def test_infinite_activations_with_fp32_weights(T, E):
+    """The logit is the infinity or NaN of the sum, as with bf16 weights, in every kernel; other rows are untouched."""
+    need_gpu()
+    g = gen(T + E)
+    H = 264
+    x = torch.randint(-3, 4, (T, H), generator=g).to(torch.bfloat16)
+    W = torch.randint(-3, 4, (E, H), generator=g).float()           # 0 among them: infinity times 0 is NaN
+    W[1::2] += 0.375
+    W[3 % E], W[4] = W[3 % E] * (1 + 2.0 ** -22), W[4] * (1 + 2.0 ** -12)
+    inf = float("inf")
+    for k, t in enumerate((0, 1, 65, 130, 200, 255, 257, T - 1)):
+        if 0 <= t < T:
+            x[t, 3 + 31 * k] = inf if k % 2 else -inf
+    if T > 2:
+        x[2, 7], x[2, 9] = inf, -inf
+    ref = x.double() @ W.double().t()
+    got = run_logits(x.to(DEV), split(W)).cpu().double()
+    bad = ~ref.isfinite()
+    assert bad.any(1).sum() >= min(T, 2) and torch.equal(got[bad].isnan(), ref[bad].isnan())
+    both = bad & ~ref.isnan()
+    assert both.any() and torch.equal(got[both], ref[both])
+    mag = x.double().abs() @ W.double().abs().t()
+    assert ((got - ref).abs()[~bad] <= 128 * 2.0 ** -22 * 1.02 * mag[~bad]).all()

@@ -406,18 +406,27 @@ cudaError_t launch_wide(const LogitArgs& a, int* err, cudaStream_t st) {
 }
 
 // Eight significant bits a part, cut off towards zero: the three parts add up to the number
-// exactly (down to 2^-110, where the last part's bits end), and none overflows.  An infinity
-// or NaN is the first part alone.
+// exactly (down to 2^-110, where the last part's bits end), and none overflows.  Of a number of fewer
+// bits the last part that is not 0 is dealt out over the ones behind it (1 is 1/2 + 1/4 + 1/4): no part of a
+// number is 0 then, so that an infinite activation times the parts is an infinity and not a NaN.  An
+// infinity or NaN is the first part alone.
 __global__ void __launch_bounds__(256) split_kernel(const float* __restrict__ w, int64_t n, __nv_bfloat16* __restrict__ parts) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        float v = w[i];
+        const float v = w[i];
         const bool finite = fabsf(v) <= 3.4028235e38f;
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-            const __nv_bfloat16 h = finite ? __float2bfloat16_rz(v) : __float2bfloat16_rn(p ? 0.0f : v);
-            parts[p * n + i] = h;
-            v = finite ? v - __bfloat162float(h) : 0.0f;
+        float p0 = v, p1 = 0.0f, p2 = 0.0f;
+        if (finite) {
+            p0 = __bfloat162float(__float2bfloat16_rz(v));
+            p1 = __bfloat162float(__float2bfloat16_rz(v - p0));
+            p2 = v - p0 - p1;
+            if (p2 == 0.0f && fabsf(v) >= 0x1p-110f) {   // halves and quarters are exact
+                if (p1 == 0.0f) p0 = 0.5f * v, p1 = 0.5f * v;
+                p1 = p2 = 0.5f * p1;
+            }
         }
+        parts[i] = __float2bfloat16_rn(p0);
+        parts[n + i] = __float2bfloat16_rn(p1);
+        parts[2 * n + i] = __float2bfloat16_rz(p2);
     }
 }
 

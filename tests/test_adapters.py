@@ -396,3 +396,19 @@ def test_layer_from_router_to_combine_with_adapters():
     ref = (C2.double().reshape(T, topk, H) * w.double().unsqueeze(2)).sum(1)
     mag = (C2.double().reshape(T, topk, H) * w.double().unsqueeze(2)).abs().sum(1)
     assert ((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -21 * mag).all()
+
+
+@gpu
+@pytest.mark.parametrize("T", [20, 200, 6000])
+def test_invalid_ids_of_tokens_whose_pairs_are_elsewhere(T):
+    """An adapter id out of range is reported wherever the token's experts live (one launch, one plan, three kernels' plan)."""
+    need_gpu()
+    c = make(T, 4, 3, 5, 16, 1, 64, 64, 1, F32, seed=T, integer=True, foreign=0.3)
+    c["ids"][7] = -1
+    ref, _, written = reference(c)
+    for value in (3, -2, 2 ** 31 - 1, -2 ** 31):
+        d = on_gpu(c)
+        d["a"][7] = value
+        y = add(d, torch.zeros_like(d["base"]))
+        assert chord.chord_get_device_error() == 7
+        assert torch.equal(y.cpu()[written], ref[written].float()) and (y.cpu()[~written] == 0).all()

@@ -71,16 +71,12 @@ struct AdapterArgs {
 };
 
 __device__ __forceinline__ int slot_of(const AdapterArgs& g, int p, bool report) {
-    int e = 0;
-    if (g.topk_ids) {
-        e = g.topk_ids[p];
-        if (e < 0 || e >= g.E) return kNone;
-    }
-    const int a = g.adapter_ids[g.topk == 1 ? p : p / g.topk];
-    if (a < 0 || a >= g.S) {
-        if (a != -1 && report) set_error(g.err, CHORD_DEV_BAD_ADAPTER);
-        return g.copy ? -1 : kNone;
-    }
+    // The adapter is looked at first, so that a bad one is reported wherever the pair's expert lives.
+    const int a = g.adapter_ids[g.topk == 1 ? p : p / g.topk], e = g.topk_ids ? g.topk_ids[p] : 0;
+    const bool none = a < 0 || a >= g.S;
+    if (none && a != -1 && report) set_error(g.err, CHORD_DEV_BAD_ADAPTER);
+    if (e < 0 || e >= g.E) return kNone;
+    if (none) return g.copy ? -1 : kNone;
     return a * g.E + e;
 }
 

@@ -708,8 +708,9 @@ size_t chord_adapter_workspace_bytes(int64_t T, int topk, int adapters, int E, i
  *                many equal ranges with their own A (gate_up: gate columns, up columns), x read once
  *   scale        device float [adapters], NULL: 1
  *   base, y      device [T * topk, N], bf16 or FP32 (y_dtype) both, base_stride and y_stride
- *                elements apart; base == y (and equal strides) adds in place, otherwise they
- *                must not overlap
+ *                elements apart; base == y (and equal strides) adds in place.  Otherwise y's rows must not
+ *                overlap base's, and never x's.  They may be columns of one buffer, as many bytes
+ *                apart; rows of different distances must not lie between one another
  *   workspace    >= chord_adapter_workspace_bytes(...), 16-byte aligned; calls that overlap on the
  *                GPU need one each
  * rank % 8 == 0 and at most 128 (a smaller rank is padded with zeros), parts <= 4, K % 8 == 0,

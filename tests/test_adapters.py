@@ -412,3 +412,25 @@ def test_invalid_ids_of_tokens_whose_pairs_are_elsewhere(T):
         y = add(d, torch.zeros_like(d["base"]))
         assert chord.chord_get_device_error() == 7
         assert torch.equal(y.cpu()[written], ref[written].float()) and (y.cpu()[~written] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("T", [4, 300])
+def test_column_ranges_of_one_buffer(T, out):
+    """x, base and y side by side in the rows of one buffer: none overlaps another."""
+    need_gpu()
+    c = make(T, 2, 3, 4, 16, 1, 96, 128, 1, out, seed=T + 1, integer=True)
+    d = on_gpu(c)
+    ref, _, written = reference(c)
+    row = torch.full((2 * T, 128 + 128 + (96 if out == BF else 48) + 16), 3.0, dtype=out, device=DEV)
+    for y0, b0 in ((0, 128), (128, 0)):
+        base, y = row[:, b0:b0 + 128], row[:, y0:y0 + 128]
+        base.copy_(d["base"])
+        y.fill_(5.0)
+        x = row.view(BF)[:, 256 * (1 if out == BF else 2):][:, :96]
+        x.copy_(c["x"].to(DEV))
+        d["x"] = x
+        add(d, y, base=base)
+        assert torch.equal(y.cpu()[written], ref.float().to(out)[written]) and (y.cpu()[~written] == 5).all()
+        assert torch.equal(base.cpu(), c["base"]) and torch.equal(x.cpu(), c["x"]) and (row[:, -16:] == 3).all()

@@ -165,3 +165,26 @@ def test_workspace_never_shrinks_with_more_tokens():
             now = f(T, topk, S, E, rank, parts)
             assert now >= prev, (T, topk)
             prev = now
+
+
+def test_overlap_is_of_rows_not_of_their_range(lib):
+    """y and base, or y and x, may be column ranges of one buffer; not with a byte in common.  The scratch is too small in
+    every call, which is found after the overlap: nothing is launched."""
+    n = chord.chord_adapter_workspace_bytes(3, 2, 4, 5, 16, 1)
+
+    def call(x, xs, base, bs, y, ys, dtype=0):
+        return lib.chord_adapter_add(x, 6, xs, 1, P * 9, P * 10, 3, 2, 4, 5, P * 11, P * 12, None, 16, 1, 32, 64, base, bs, y, ys, dtype, P * 13, n - 1,
+                                     None, None)
+
+    far = P * 20
+    # 6 rows of x are 64 bf16, of base and y 32 bf16; a buffer of 128 bf16 a row
+    for y, st in ((P + 64, 4), (P + 128, 4), (P + 192, 4), (P + 48, 1), (P + 16, 1), (P - 16, 1), (P - 64, 4), (P + 256 * 6, 4), (P + 256 * 3 + 64, 4),
+                  (P + 256 * 3 + 48, 1), (P + 256 * 5 - 16, 1), (P + 256 * 5 + 64, 4), (P - 256 * 2 + 128, 4), (P - 256 * 2 + 208, 1)):
+        assert call(far, 64, P, 128, y, 128) == st, y - P
+    for y, st in ((P, 1), (P + 64, 1), (P + 128, 4), (P + 192, 4), (P + 208, 1), (P - 64, 4), (P - 48, 1), (P + 256 * 2 + 112, 1), (P + 256 * 2 + 128, 4)):
+        assert call(P, 128, far, 32, y, 128) == st, y - P
+    # another row distance: the ranges decide; FP32 rows in the buffer of bf16 ones
+    assert call(far, 64, P, 128, P + 64, 136) == 1 and call(far, 64, P, 128, P + 256 * 6, 136) == 4
+    assert call(P, 128, far, 32, P + 128, 64, dtype=1) == 4 and call(P, 128, far, 32, P + 112, 64, dtype=1) == 1
+    # rows of base that lie closer than y's are wide
+    assert call(far, 64, P, 32, P + 32, 32) == 1 and call(far, 64, P, 32, P, 32) == 4

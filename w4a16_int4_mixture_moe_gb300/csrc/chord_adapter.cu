@@ -994,10 +994,21 @@ cudaError_t launch_plan(const AdapterArgs& g, int64_t slots, int32_t* counts, cu
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// The bytes from a to a + na and from b to b + nb have one in common.
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+// n rows of `width` bytes, `pitch` apart (at least a width).
+struct Rows2D {
+    const void* at;
+    int64_t n, pitch, width;
+};
+
+// The rows have a byte in common.  Rows of the same distance may lie between one another, columns of one buffer; of
+// different distances, the ranges from first to last byte decide.
+bool overlap(const Rows2D& a, const Rows2D& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    if (x >= y + (uintptr_t)((b.n - 1) * b.pitch + b.width) || y >= x + (uintptr_t)((a.n - 1) * a.pitch + a.width)) return false;
+    if (a.n > 1 && b.n > 1 && a.pitch != b.pitch) return true;
+    // a single row meets the other ones as any of their distance would
+    const int64_t pitch = a.n > 1 ? a.pitch : b.pitch, d = (int64_t)(y - x) % pitch, off = d < 0 ? d + pitch : d;   // of b's rows behind a's
+    return off < a.width || off + b.width > pitch;
 }
 
 }  // namespace
@@ -1038,10 +1049,9 @@ chord_status chord_adapter_add(const void* x, int64_t x_rows, int64_t x_stride, 
         !aligned16(y) || !workspace || !aligned16(workspace))
         return CHORD_ERR_INVALID_ARG;
     const int64_t esize = 16 / per;
-    const int64_t y_bytes = ((P - 1) * y_stride + N) * esize, base_bytes = ((P - 1) * base_stride + N) * esize;
-    const int64_t x_bytes = ((P - 1) / a_row_divisor * x_stride + K) * 2;
-    if (overlap(y, y_bytes, x, x_bytes) || (base == y ? base_stride != y_stride : overlap(y, y_bytes, base, base_bytes)))
-        return CHORD_ERR_INVALID_ARG;
+    const Rows2D xs{x, (P - 1) / a_row_divisor + 1, x_stride * 2, (int64_t)K * 2}, bases{base, P, base_stride * esize, N * esize},
+        ys{y, P, y_stride * esize, N * esize};
+    if (overlap(ys, xs) || (base == y ? base_stride != y_stride : overlap(ys, bases))) return CHORD_ERR_INVALID_ARG;
     if (workspace_bytes < chord_adapter_workspace_bytes(T, topk, adapters, E, rank, parts)) return CHORD_ERR_BUFFER_TOO_SMALL;
     const DeviceInfo& di = device_info();
     if (!di.err) return CHORD_ERR_CUDA;

@@ -188,3 +188,9 @@ def test_overlap_is_of_rows_not_of_their_range(lib):
     assert call(P, 128, far, 32, P + 128, 64, dtype=1) == 4 and call(P, 128, far, 32, P + 112, 64, dtype=1) == 1
     # rows of base that lie closer than y's are wide
     assert call(far, 64, P, 32, P + 32, 32) == 1 and call(far, 64, P, 32, P, 32) == 4
+
+
+def test_route_outputs_without_dimensions():
+    args = [dev(4, 16, dtype=F32), dev(4, 2, dtype=I32), dev(4, 2, dtype=F32)]
+    refused(chord.chord_moe_route, args, 1, dev(dtype=I32), "topk_ids")
+    refused(chord.chord_moe_route, args, 2, dev(dtype=F32), "topk_w")

@@ -601,7 +601,7 @@ def _route(*fields):
 def _check_route(logits, topk_ids, topk_w, bias, types):
     what, f32 = "chord_moe_route", types["f32"]
     _rows(what, "logits", logits, (types["bf16"], f32))
-    (T, E), topk = logits.shape, topk_ids.shape[-1]
+    (T, E), topk = logits.shape, topk_ids.shape[-1] if topk_ids.dim() else 1
     _dense(what, "topk_ids", topk_ids, types["int32"], T, topk)
     _dense(what, "topk_w", topk_w, f32, T, topk)
     if bias is not None:

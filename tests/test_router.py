@@ -534,3 +534,39 @@ def test_infinite_activations_with_fp32_weights(T, E):
     assert both.any() and torch.equal(got[both], ref[both])
     mag = x.double().abs() @ W.double().abs().t()
     assert ((got - ref).abs()[~bad] <= 128 * 2.0 ** -22 * 1.02 * mag[~bad]).all()
+
+
+#        T, E, H of the pairs of CTAs: groups of 32, 160, 192, 224 and 256 experts, fewer experts than a box has rows, a ring
+#        that wraps, a last pair of CTAs with tokens for one of the two only and for a part of one
+WIDE = [(8192, 3, 136), (5888, 7, 264), (3000, 40, 392), (8192, 384, 264), (16384, 160, 264), (16290, 187, 136), (16384, 200, 136),
+        (16290, 224, 520), (16384, 256, 264), (16221, 250, 648), (19456, 1024, 136)]
+
+
+@gpu
+@pytest.mark.parametrize("T,E,H", WIDE)
+@pytest.mark.parametrize("parts", [1, 3])
+def test_logits_of_many_tokens(T, E, H, parts):
+    """Strided rows: integers exactly, real numbers within the bound, infinities and NaN in their own rows only."""
+    need_gpu()
+    g = torch.Generator(device=DEV).manual_seed(T + E + H)
+    big = torch.randint(-3, 4, (T, H + 136), generator=g, device=DEV).to(torch.bfloat16)
+    x = big[:, 8:8 + H]
+    W = torch.randint(-3, 4, (E, H), generator=g, device=DEV).float()
+    Wd = W.to(torch.bfloat16) if parts == 1 else split(W)
+    ref = x.double() @ W.double().t()
+    assert torch.equal(run_logits(x, Wd), ref.float())
+    rows = [0, 127, 128, 200, 255, 256, T - 1]       # of both CTAs of a pair
+    inf, nan = float("inf"), float("nan")
+    big[rows, 20] = torch.tensor([inf, nan, nan, inf, -inf, nan, inf], dtype=torch.bfloat16, device=DEV)
+    pos = W.abs() + 1
+    got = run_logits(x, pos.to(torch.bfloat16) if parts == 1 else split(pos))
+    keep = torch.ones(T, dtype=torch.bool, device=DEV)
+    keep[rows] = False
+    assert torch.equal(got[keep], (x[keep].double() @ pos.double().t()).float())
+    assert (got[[0, 200, T - 1]] == inf).all() and (got[255] == -inf).all() and got[[127, 128, 256]].isnan().all()
+    big.copy_(torch.randn(big.shape, generator=g, device=DEV))
+    W = torch.randn((E, H), generator=g, device=DEV) * H ** -0.5
+    W = W.to(torch.bfloat16).float() if parts == 1 else W
+    got = run_logits(x, W.to(torch.bfloat16) if parts == 1 else split(W)).double()
+    mag = x.double().abs() @ W.double().abs().t()
+    assert ((got - x.double() @ W.double().t()).abs() <= 128 * 2.0 ** -22 * mag * (1.02 if parts == 3 else 1.0)).all()

@@ -90,17 +90,14 @@ __device__ __forceinline__ double value_in_64_bits(const RouteArgs& a, float l, 
     return (a.score == CHORD_SCORE_SOFTMAX ? exp((double)l - (double)mx) / total : 1.0 / (1.0 + exp(-(double)l))) + (double)b;
 }
 
-// The choice by the definition, every value in binary64, one expert after the other: lane k gets
-// the k-th (-1: none).  z: E + 32 doubles of the warp's own.
+// The choice with a bias by the definition, every value in binary64, one expert after the other: lane k gets
+// the k-th (-1: none).  z: E + 32 doubles of the warp's own.  (Without a bias the logits order the experts, and
+// nothing is in doubt.)
 __device__ __noinline__ int choose_in_64_bits(const RouteArgs& a, int64_t t, int lane, float mx, double* z) {
     double* gz = z + a.E;
     const double ninf = -INFINITY;
     const double total = a.score == CHORD_SCORE_SOFTMAX ? total_in_64_bits(a, t, lane, mx) : 0.0;
-    const bool by_logit = !a.bias && (a.groups == 1 || a.best == 1);
-    for (int e = lane; e < a.E; e += 32) {
-        const float l = logit_at(a, t, e);
-        z[e] = by_logit ? (l > -INFINITY ? (double)l : ninf) : value_in_64_bits(a, l, a.bias ? a.bias[e] : 0.0f, mx, total);
-    }
+    for (int e = lane; e < a.E; e += 32) z[e] = value_in_64_bits(a, logit_at(a, t, e), a.bias[e], mx, total);
     __syncwarp();
     if (a.groups > 1) {
         const int size = a.E / a.groups;
@@ -129,9 +126,6 @@ __device__ __noinline__ int choose_in_64_bits(const RouteArgs& a, int64_t t, int
             if (!(kept >> (e / size) & 1u)) z[e] = ninf;
         __syncwarp();
     }
-    if (!a.bias && !by_logit)
-        for (int e = lane; e < a.E; e += 32)
-            if (z[e] > ninf) z[e] = logit_at(a, t, e);
     int mine = -1;
     for (int k = 0; k < a.topk; ++k) {
         double best = ninf;
@@ -156,7 +150,6 @@ __device__ __noinline__ int choose_in_64_bits(const RouteArgs& a, int64_t t, int
     }
     return mine;
 }
-
 
 // A number's place among unsigned integers, in the order of the numbers (-inf is not 0: 0 is below all).
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -191,7 +184,7 @@ __device__ __forceinline__ float fast_rcp(float x) {
 //   3. Where two candidates' values are too close for FP32 to tell (some of a thousand tokens of a
 //      sigmoid router of 384 experts), the candidates' are computed in binary64; where two groups' are, those
 //      of the groups in question.
-//   4. More than 32 candidates: choose_one_by_one.  Where that is still in doubt, or values are infinite, the whole
+//   4. More than 32 candidates: choose_one_by_one.  Where that is still in doubt, or biases are +inf, the whole
 //      token is done by choose_in_64_bits.
 // A value in FP32 is off by at most slack + kRounding |value|.  A sigmoid of the fast functions is off by s (1 - s)
 // (2^-22 + |l| 2^-24) + 2^-23, below 3e-7, of the accurate ones by s (1 - s) 2^-22 + s 2^-23, below 1.8e-7.  A softmax's score e / total, of E <= 1024

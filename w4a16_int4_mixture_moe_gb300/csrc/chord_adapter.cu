@@ -250,7 +250,7 @@ __device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch
 
 template <int kFewCtas, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, 2) adapter_few_kernel(const AdapterArgs g) {
-    using Warp = thin::Warp<1, NT>;
+    using Warp = thin::Warp<NT>;
     constexpr int NB = Warp::kCols;
     extern __shared__ __align__(16) float red[];             // [kWarps][16][NB], then v [16][rank] and its fragments
     __shared__ int32_t rows[kFewRows];

@@ -26,10 +26,11 @@ struct LogitArgs {
 // ---- few tokens: thin products (chord_thin.cuh) -------------------------------------------
 // A CTA takes a tile of tokens and experts and a slice of K (of all parts, one behind the other, the smallest
 // numbers first); the slices of a tile are a cluster.
-// Up to 16 tokens, NT x 8 experts (16 tokens of 7168 columns, 384 experts: 4.2 us in a graph, staged as below 6.9).
-template <int NT>
+// Up to 16 tokens, 16 experts (16 tokens of 7168 columns, 384 experts: 4.2 us in a graph, staged as below 6.9).
+using ThinWarp = thin::Warp<2>;
+
 __global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const LogitArgs a, int splits) {
-    using Warp = thin::Warp<1, NT>;
+    using Warp = ThinWarp;
     constexpr int kTile = Warp::kRows * Warp::kCols;
     extern __shared__ __align__(16) float red[];   // [kWarps][kTile], then the shares
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gr = lane >> 2, c = lane & 3;
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(thin::kThreads) logits_thin_kernel(const Logit
 #pragma unroll
         for (int j = 0; j < 2; ++j) w.x[j] = reinterpret_cast<const uint4*>(a.x + min(j * 8 + gr, a.T - 1) * a.stride) + c;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < Warp::kCols / 8; ++j)
             w.w[j] = reinterpret_cast<const uint4*>(a.W + ((int64_t)(a.parts - 1 - part) * a.E + min(e0 + j * 8 + gr, a.E - 1)) * a.H) + c;
         w.run(max(k0 - part * steps1, 0) + warp, min(k1 - part * steps1, steps1), a.H / 8, mine, more);
         more = true;
@@ -139,10 +140,10 @@ cudaError_t launch_tiles(const LogitArgs& a, int64_t tiles, int64_t steps, int l
 }
 
 cudaError_t launch_thin(const LogitArgs& a, cudaStream_t st) {
-    using Warp = thin::Warp<1, 2>;
+    using Warp = ThinWarp;
     const size_t smem = (size_t)(thin::kWarps + 1) * Warp::kRows * Warp::kCols * 4;
     // a slice keeps two steps for each warp
-    return launch_tiles<logits_thin_kernel<2>>(a, (a.E + Warp::kCols - 1) / Warp::kCols, ceil_div64(a.H, thin::kStep) * a.parts, 2 * thin::kWarps,
+    return launch_tiles<logits_thin_kernel>(a, (a.E + Warp::kCols - 1) / Warp::kCols, ceil_div64(a.H, thin::kStep) * a.parts, 2 * thin::kWarps,
                         smem, st);
 }
 

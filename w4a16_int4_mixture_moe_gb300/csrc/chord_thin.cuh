@@ -38,41 +38,39 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
                  : "memory");
 }
 
-// What one warp multiplies: MT tiles of 16 rows of x, NT tiles of eight weight rows.  Rows that are not
+// What one warp multiplies: 16 rows of x, NT tiles of eight weight rows.  Rows that are not
 // there are any others: their sums are not looked at.
-template <int MT, int NT>
+template <int NT>
 struct Warp {
-    static constexpr int kRows = MT * 16, kCols = NT * 8;
+    static constexpr int kRows = 16, kCols = NT * 8;
     // Steps in registers, all but one of them on their way: as many as a few rows need to cover the latency.
-    static constexpr int kDepth = MT * NT <= 2 ? 4 : MT * NT <= 4 ? 3 : 2;
-    const uint4* x[2 * MT];    // this lane's rows and piece of a step: row start + c
+    static constexpr int kDepth = NT <= 2 ? 4 : NT <= 4 ? 3 : 2;
+    const uint4* x[2];    // this lane's rows and piece of a step: row start + c
     const uint4* w[NT];
-    float acc[MT][NT][4];
+    float acc[NT][4];
 
     struct Step {
-        uint4 a[2 * MT], b[NT];
+        uint4 a[2], b[NT];
     };
 
     template <bool TAIL>
     __device__ __forceinline__ void load(Step& s, int at, bool in) const {
         const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int j = 0; j < 2 * MT; ++j) s.a[j] = !TAIL || in ? x[j][at] : zero;
+        for (int j = 0; j < 2; ++j) s.a[j] = !TAIL || in ? x[j][at] : zero;
 #pragma unroll
         for (int j = 0; j < NT; ++j) s.b[j] = !TAIL || in ? w[j][at] : zero;
     }
     __device__ __forceinline__ void multiply(const Step& s) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                mma(acc[m][t], s.a[2 * m].x, s.a[2 * m + 1].x, s.a[2 * m].y, s.a[2 * m + 1].y, s.b[t].x, s.b[t].y);
-                mma(acc[m][t], s.a[2 * m].z, s.a[2 * m + 1].z, s.a[2 * m].w, s.a[2 * m + 1].w, s.b[t].z, s.b[t].w);
-            }
+        for (int t = 0; t < NT; ++t) {
+            mma(acc[t], s.a[0].x, s.a[1].x, s.a[0].y, s.a[1].y, s.b[t].x, s.b[t].y);
+            mma(acc[t], s.a[0].z, s.a[1].z, s.a[0].w, s.a[1].w, s.b[t].z, s.b[t].w);
+        }
     }
     __device__ __forceinline__ void move(int pieces) {
 #pragma unroll
-        for (int j = 0; j < 2 * MT; ++j) x[j] += pieces;
+        for (int j = 0; j < 2; ++j) x[j] += pieces;
 #pragma unroll
         for (int j = 0; j < NT; ++j) w[j] += pieces;
     }
@@ -90,11 +88,9 @@ struct Warp {
             int n = min(left, kChain);
             left -= n;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) acc[m][t][u] = 0.0f;
+                for (int u = 0; u < 4; ++u) acc[t][u] = 0.0f;
             Step s[kDepth];
 #pragma unroll
             for (int d = 0; d < kDepth - 1; ++d)
@@ -116,16 +112,14 @@ struct Warp {
                 multiply(s[0]);
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float2* to = reinterpret_cast<float2*>(to0 + (m * 16 + h * 8) * kCols + t * 8);
-                        float2 o = make_float2(acc[m][t][2 * h], acc[m][t][2 * h + 1]);
-                        if (more) o.x += to->x, o.y += to->y;
-                        *to = o;
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    float2* to = reinterpret_cast<float2*>(to0 + h * 8 * kCols + t * 8);
+                    float2 o = make_float2(acc[t][2 * h], acc[t][2 * h + 1]);
+                    if (more) o.x += to->x, o.y += to->y;
+                    *to = o;
+                }
             more = true;
         } while (left > 0);
     }

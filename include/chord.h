@@ -667,8 +667,8 @@ typedef struct chord_route {
  *   logits   device [T, E], CHORD_DTYPE_BF16 or CHORD_DTYPE_F32, row_stride elements apart
  *   bias     device float [E] or NULL, added to the scores for the choice only
  *   topk_ids device int32 [T, topk], local id or -1;  topk_w device float [T, topk]
- * With s = score(logits), the value of an expert is s + bias (without a bias its logit,
- * which orders the experts as s does); groups take part by their value, the topk
+ * With s = score(logits), the value of an expert is s + bias (without a bias its logit, which
+ * orders the experts as s does; a group's sum is of s); groups take part by their value, the topk
  * experts with the largest values in the chosen groups are the result, largest
  * first.  Values are compared as binary64 has them, whatever the precision the kernel begins
  * with; of equal ones the lower index is first, among groups too.  The weight is

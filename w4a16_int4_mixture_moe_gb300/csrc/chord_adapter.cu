@@ -3,7 +3,9 @@
 // A slot is an adapter of an expert, a * E + e; the pairs of one slot are taken together, in blocks, so a slot's
 // weights are read once a block.
 // Up to kFewPairs pairs: one launch (adapter_few_kernel), in which every CTA finds the blocks, of 16 rows, itself.  Bound by
-//   latency (one token of 7168 columns, 4096 outputs, rank 16: 6.4 us in a graph).
+//   latency (one token of 7168 columns, 4096 outputs, rank 16: 6.2 us in a graph; rank 32 8.3), above rank 32 also by the
+//   registers: two CTAs to an SM leave 128 a thread, and what the first half holds for 64 rows of A spills 404 to 476 bytes (28 to 168
+//   for 8 to 32 rows; rank 64 13.3 us, rank 128, which takes A in two passes, 21.3).
 // More pairs: three launches.
 //   plan   blocks of 64 rows by a counting sort of the pairs by slot: 5.5 to 8.5 us for 8192 pairs.
 //   down   v, a block's rows times the slot's A, staged products (chord_thin.cuh); an item is (block, up to 64 rows of A,

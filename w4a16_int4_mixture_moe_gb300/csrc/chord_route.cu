@@ -175,8 +175,9 @@ __device__ __forceinline__ float fast_rcp(float x) {
 }
 
 // One token per warp; lane l holds experts l, l + 32, ...  Bound by instructions: 16384 tokens of 384 experts, sigmoid, a
-// bias, top-8, 18.4 us in a graph (1.4 TB/s of logits, 2.7 of 4 instructions a cycle issued).  Eight CTAs to an SM:
-// 8192 tokens of 512 experts top-16 15.8 us, without the bound, at 88 registers, 17.5.
+// bias, top-8, 18.4 us in a graph (1.4 TB/s of logits, 2.7 of 4 instructions a cycle issued).  Eight CTAs to an SM
+// (64 registers; 8 bytes a thread spilled at 8 values a lane, 44 to 64 at 12 and 16): 8192 tokens of 512 experts top-16 15.8 us,
+// without the bound, at 88 registers, 17.5.
 //   1. Values in FP32, each off by a known slack.
 //   2. The topk-th largest of the 32 lanes' largest values bounds the topk-th largest value from
 //      below: what is not below it (by twice the slack) are the candidates, about ten for a

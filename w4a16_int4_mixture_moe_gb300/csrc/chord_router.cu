@@ -167,8 +167,12 @@ constexpr int kReaders = 8, kWideThreads = (kReaders + 2) * 32;
 constexpr int kHalfCols = 64, kStageCols = 2 * kHalfCols;
 constexpr int kPairTokens = 256;
 // The staged tiles copy 96 rows of K columns for 64 x 32 sums, the wide ones 128 + N / 2 for 128 x N, where a step of 128
-// columns takes 0.25 us at least.  Staged and wide, us in a graph (E, H: tiles): 384, 7168: 72 13.1, 19.6; 96 21.0,
-// 19.6; 192 34, 20.  161, 2088: 72 8.7, 10.2; 96 12.3, 10.2.  64, 4096: 64 9.5, 12.4; 94 14.3, 13.0.
+// columns takes 0.25 us at least.  Staged and wide, us in a graph (E, H: tiles):
+//   bf16  384, 7168: 72 12.3, 19.6; 96 19.6, 19.6; 192 31.9, 20.1.  161, 2088: 72 8.6, 10.3; 96 11.5, 10.2.  64, 4096: 64 9.3,
+//         12.8; 94 13.5, 13.1.
+//   FP32  384, 7168: 72 26.5, 52.0; 96 46.7, 52.2; 144 47.0, 52.2; 192 86.4, 52.6.  161, 2088: 72 14.1, 23.5; 96 22.7, 23.5; 192 37.5,
+//         23.9.  64, 4096: 64 17.3, 31.2; 94 29.3, 31.4.
+// One rule for both types: from 91 to about 150 tiles an FP32 router loses up to a tenth by it.
 constexpr int64_t kStagedTiles = 90;
 constexpr int kChainStages = 2;
 constexpr int kMaxWideStages = 6;

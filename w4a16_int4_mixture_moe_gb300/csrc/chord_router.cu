@@ -215,6 +215,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) logits_wide_kernel(const Logi
     volatile int* aborted = flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc5::cluster_rank();
+    // All of an SM's tensor memory, before the wait: no CTA of an earlier kernel that still has to allocate its own can be on
+    // the SM, since 181 KB at least of shared memory here leave less than 47 KB, and the kernels that use tensor memory take more.
     if (warp == kReaders) tc5::alloc<true>(&tmem_slot, 512);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxWideStages; ++s) {
